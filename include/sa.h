@@ -361,6 +361,116 @@ SA_API sa_status sa_fused_decode_noalloc(const sa_index_args *ia, const sa_attn_
                                          int32_t K, int32_t *idx_out, void *out,
                                          uint32_t *device_status, sa_stream_t stream);
 
+/* ---------------------------------------------------------------- paged cache
+ *
+ * Keys and values of raw positions in pages: page i of the cache holds P
+ * consecutive positions of one sequence for every KV head,
+ *   K, V: [n_pages, H_kv, P, D] bf16,
+ * and position p of sequence b lives in page page_table[b, p / P], slot p % P.
+ * Query head h reads KV head h / (H / H_kv).  Sequences may name the same page
+ * (a shared prefix).  A page that covers positions nobody has written yet may
+ * hold anything there, NaN included: such positions are never used.
+ *
+ * For every call below, a token whose q_seq lies outside [0, B), or whose
+ * q_pos is negative or at or past max_pages * P, is skipped (what it would
+ * write stays as it was) and flagged; a page id outside [0, n_pages) counts as
+ * a page without positions and is flagged (SA_ERR_DEVICE_DATA from
+ * sa_check_device_status).  The page table and the positions are read on the
+ * device at each call, so a captured call follows their contents at replay. */
+typedef struct {
+  int32_t B, T;         /* sequences (>= 1), tokens of the call (>= 0) */
+  int32_t H, H_kv, D;   /* query heads, KV heads (H_kv divides H, H / H_kv <= 128), head dim 64 or 128 */
+  int32_t P;            /* positions per page: 16, 32, 64 or 128 */
+  int32_t n_pages;      /* pages in the cache (>= 1; n_pages * H_kv * P < 2^31 - 256) */
+  int32_t max_pages;    /* page table entries per sequence (>= 1; max_pages * P <= 2^30) */
+  const int32_t *q_seq; /* [T] sequence id of each token */
+  const int32_t *q_pos; /* [T] absolute position of each token */
+  const int32_t *page_table; /* [B, max_pages], rows table_stride entries apart */
+  int64_t table_stride; /* 0 for max_pages, else at least max_pages */
+  void *K, *V;          /* [n_pages, H_kv, P, D] bf16, 16-byte aligned */
+  float scale;          /* factor on q . k (e.g. D^-0.5) */
+} sa_paged_args;
+
+/* Bytes of workspace the paged calls need: sa_paged_append and sa_page_scores
+ * (256), sa_block_attn and sa_fused_block_attn with these K and local,
+ * sa_prefix_attn with these shared_pages (pass 0 for what is not used).
+ * Returns 0 when the arguments are invalid.  Initialise the workspace with
+ * sa_workspace_init; graphs that may run at once need one each. */
+SA_API size_t sa_paged_workspace_size(const sa_paged_args *pa, int32_t K, int32_t local, int32_t shared_pages);
+
+/* Appends new keys and values to the pages, rotary embedding applied on the
+ * way ("DeepSeek-V4.1-Flash-NVFP4 inference/model.py", Attention._window_kv:
+ * apply_rotary_emb, then the cache write).  For token t at position p of
+ * sequence b, page i = page_table[b, p / P], slot s = p % P, every KV head h:
+ *   K[i, h, s] = bf16( R(p) k[t, h] ),   V[i, h, s] = v[t, h]
+ * with R(p) the rotation of the last rope->dim values at position p (rope NULL
+ * or dim 0: none; dim a multiple of 16, at most D).  rope_halves 0 pairs
+ * adjacent values (2i, 2i + 1), nonzero pairs value i with value i + dim / 2
+ * ("DeepSeek-V3.2-Exp inference/model.py", apply_rotary_emb with interleaved
+ * false).  With q ([T, H, D]) the rotated queries go to q_out ([T, H, D]
+ * dense; q_out == q is allowed when q is dense).  k, v and q rows of
+ * consecutive tokens are *_stride elements apart (0: dense; else a multiple of
+ * 8 of at least the row), heads dense, e.g. slices of one projection's output.
+ *
+ * With k_mean ([n_pages, H_kv, D] bf16), every page whose last position is
+ * among the tokens gets the mean of its P key rows as stored (summed in fp32,
+ * rounded once): the keys sa_page_scores reads.  The positions of one call are
+ * distinct within a sequence, in any order; a position given twice leaves
+ * either token's values.  Angles are taken as exact multiples of the frequency
+ * modulo a turn (64-bit fixed point), so far positions lose nothing. */
+SA_API sa_status sa_paged_append(const sa_paged_args *pa, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                 const sa_rope_args *rope, int32_t rope_halves, void *k_mean, void *ws,
+                                 size_t ws_bytes, sa_stream_t stream);
+
+/* The cheap score of pages.  For token t, KV head h and every complete page
+ * j < n_vis(t) = (q_pos[t] + 1) / P of its sequence:
+ *   scores[t, h, j] = scale * sum_g q[t, h * G + g] . k_mean[page_table[b, j], h]    (G = H / H_kv)
+ * and -inf for n_vis(t) <= j < max_pages (and for a page id out of range).
+ * q: [T, H, D] bf16 dense, rotated; k_mean as sa_paged_append keeps it;
+ * scores: [T, H_kv, ld] fp32, columns 0 .. max_pages - 1 of every row written,
+ * ld >= max_pages.  The queries' sum and the products are held in fp32.  Rows
+ * of T * H_kv scores are what sa_topk selects from (r = P, one row per token
+ * and KV head); sa_fused_block_attn does so.  K and V of pa are not read and
+ * may be NULL. */
+SA_API sa_status sa_page_scores(const sa_paged_args *pa, const void *q, const void *k_mean, float *scores, int64_t ld,
+                                void *ws, size_t ws_bytes, sa_stream_t stream);
+
+/* Attention over selected pages.  Token t at position p attends, for KV head
+ * h, the positions of the pages idx[t, h, 0 .. K) and the `local` newest pages
+ * of its sequence, never past p itself: with f = p / P + 1 - local (at least 0)
+ * the first local page, the keys are the positions f * P .. p and, for each
+ * entry 0 <= j < f, those of j * P .. j * P + P - 1 up to p.  An entry of -1,
+ * or one in [f, p / P] (a page already local), adds nothing; any other entry
+ * is skipped and flagged.  An entry given twice counts twice (the keys are
+ * concatenated, as in sa_sparse_attn).
+ *   out[t, h'] = sum_j softmax(scale q[t, h'] . K_j) V_j,  0 for a row without keys.
+ * q, out: [T, H, D] bf16 dense; idx: [T, H_kv, K] int32 (NULL when K is 0);
+ * K >= 0, local >= 0.  The logits, the softmax statistics and the output sums
+ * are fp32; the weights enter their product as bf16. */
+SA_API sa_status sa_block_attn(const sa_paged_args *pa, const void *q, const int32_t *idx, int32_t K, int32_t local,
+                               void *out, void *ws, size_t ws_bytes, sa_stream_t stream);
+
+/* Page scores, the exact top-k of every (token, KV head) row over its complete
+ * pages before the local ones (ties to the lower page), and attention over the
+ * picks and the local pages, in one call without host synchronisation.
+ * idx_out: [T, H_kv, K] int32, ascending, -1 at the end, or NULL.  local >= 1. */
+SA_API sa_status sa_fused_block_attn(const sa_paged_args *pa, const void *q, const void *k_mean, int32_t K,
+                                     int32_t local, int32_t *idx_out, void *out, void *ws, size_t ws_bytes,
+                                     sa_stream_t stream);
+
+/* Attention over whole sequences whose first shared_pages pages are the same:
+ * token t attends every position 0 .. q_pos[t] of its sequence.  The shared
+ * pages are the first shared_pages entries of page_table row 0 for every
+ * token, and are read once for the whole batch (a matrix product of all
+ * tokens' heads with each shared key); the positions from shared_pages * P on
+ * come from each sequence's own row.  Every position of the shared pages has
+ * been written.  A token inside the shared pages (q_pos[t] < shared_pages * P)
+ * is skipped and flagged.  shared_pages 0 is plain attention over the paged
+ * cache.  q, out and precision as for sa_block_attn. */
+SA_API sa_status sa_prefix_attn(const sa_paged_args *pa, const void *q, int32_t shared_pages, void *out, void *ws,
+                                size_t ws_bytes, sa_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the workspace's sticky device
  * status: SA_OK, SA_ERR_DEVICE_DATA (out-of-range device data was skipped)
  * or SA_ERR_TIMEOUT. */

@@ -10,13 +10,23 @@ from .binding import (  # noqa: F401
     AttnArgs,
     DeviceProblem,
     IndexArgs,
+    PagedArgs,
+    RopeArgs,
     SAError,
     SA_BF16,
     SA_FP8_E4M3,
+    new_paged_workspace,
     new_workspace,
+    paged_args,
+    sa_block_attn,
     sa_check_device_status,
+    sa_fused_block_attn,
     sa_fused_decode,
     sa_indexer_scores,
+    sa_page_scores,
+    sa_paged_append,
+    sa_paged_workspace_size,
+    sa_prefix_attn,
     sa_sparse_attn,
     sa_topk,
     sa_workspace_init,

@@ -66,12 +66,23 @@ class RopeArgs(ctypes.Structure):
     ]
 
 
+class PagedArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("P", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("q_seq", ctypes.c_void_p), ("q_pos", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("scale", ctypes.c_float),
+    ]
+
+
 EXPORTED = ("sa_workspace_size", "sa_workspace_init", "sa_indexer_scores", "sa_topk",
             "sa_candidate_blocks", "sa_candidate_words", "sa_topk_candidates", "sa_rotate_quant",
             "sa_compress_prefill", "sa_compress_decode", "sa_index_key_publish",
             "sa_sparse_attn", "sa_fused_decode", "sa_fused_decode_staged",
             "sa_fused_decode_launch_count", "sa_check_device_status", "sa_status_string",
-            "sa_last_error_detail", "sa_fused_decode_noalloc", "sa_noalloc_scratch_bytes", "sa_set_wait_budget")
+            "sa_last_error_detail", "sa_fused_decode_noalloc", "sa_noalloc_scratch_bytes", "sa_set_wait_budget",
+            "sa_paged_workspace_size", "sa_paged_append", "sa_page_scores", "sa_block_attn", "sa_fused_block_attn",
+            "sa_prefix_attn")
 
 _LIB = None
 
@@ -111,6 +122,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.sa_fused_decode_noalloc.restype = i32
     lib.sa_noalloc_scratch_bytes.argtypes = []
     lib.sa_noalloc_scratch_bytes.restype = sz
+    PA = ctypes.POINTER(PagedArgs)
+    lib.sa_paged_workspace_size.argtypes = [PA, i32, i32, i32]
+    lib.sa_paged_workspace_size.restype = sz
+    lib.sa_paged_append.argtypes = [PA, vp, i64, vp, i64, vp, i64, vp, ctypes.POINTER(RopeArgs), i32, vp, vp, sz, vp]
+    lib.sa_page_scores.argtypes = [PA, vp, vp, vp, i64, vp, sz, vp]
+    lib.sa_block_attn.argtypes = [PA, vp, vp, i32, i32, vp, vp, sz, vp]
+    lib.sa_fused_block_attn.argtypes = [PA, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+    lib.sa_prefix_attn.argtypes = [PA, vp, i32, vp, vp, sz, vp]
     lib.sa_check_device_status.argtypes = [vp, vp]
     lib.sa_set_wait_budget.argtypes = [i64]
     lib.sa_set_wait_budget.restype = i32
@@ -120,7 +139,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     for name in ("sa_workspace_init", "sa_indexer_scores", "sa_topk", "sa_candidate_blocks",
                  "sa_topk_candidates", "sa_rotate_quant", "sa_compress_prefill", "sa_compress_decode",
                  "sa_index_key_publish", "sa_sparse_attn",
-                 "sa_fused_decode", "sa_fused_decode_staged", "sa_check_device_status"):
+                 "sa_fused_decode", "sa_fused_decode_staged", "sa_check_device_status", "sa_paged_append",
+                 "sa_page_scores", "sa_block_attn", "sa_fused_block_attn", "sa_prefix_attn"):
         getattr(lib, name).restype = i32
     if path == LIB:
         _LIB = lib
@@ -274,6 +294,59 @@ def sa_noalloc_scratch_bytes() -> int:
     return int(load().sa_noalloc_scratch_bytes())
 
 
+def sa_paged_workspace_size(pa: PagedArgs, K: int = 0, local: int = 0, shared_pages: int = 0) -> int:
+    return int(load().sa_paged_workspace_size(ctypes.byref(pa), K, local, shared_pages))
+
+
+def _token_stride(name: str, x) -> int:
+    """Elements between consecutive tokens of [T, heads, D] rows (0: dense, or a
+    raw pointer); the heads of a token have to be dense."""
+    if not isinstance(x, torch.Tensor):
+        return 0
+    if x.dim() != 3 or x.stride(2) != 1 or (x.size(1) > 1 and x.stride(1) != x.size(2)):
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} must be [T, heads, D] with dense heads")
+    return x.stride(0) if x.size(0) > 1 else 0
+
+
+def sa_paged_append(pa: PagedArgs, k, v, ws, q=None, q_out=None, rope: Optional[RopeArgs] = None,
+                    halves: bool = False, k_mean=None, stream=None) -> None:
+    """New keys and values into their pages with the rotary embedding applied;
+    ``q`` is rotated into ``q_out`` alongside, and ``k_mean`` gets the mean key of
+    every page that fills.  k, v and q may be slices of a fused projection
+    (their token strides are passed on)."""
+    p, n = _ws(ws)
+    _check(load().sa_paged_append(ctypes.byref(pa), _p(k), _token_stride("k", k), _p(v), _token_stride("v", v), _p(q),
+                                  _token_stride("q", q), _p(q_out), ctypes.byref(rope) if rope is not None else None,
+                                  int(halves), _p(k_mean), p, n, _s(stream)))
+
+
+def sa_page_scores(pa: PagedArgs, q, k_mean, scores, ws, stream=None, ld=None) -> None:
+    """Score of every complete page for every token and KV head ([T, H_kv, ld] fp32)."""
+    if ld is None:
+        ld = scores.stride(-2) if isinstance(scores, torch.Tensor) and scores.dim() == 3 else pa.max_pages
+    p, n = _ws(ws)
+    _check(load().sa_page_scores(ctypes.byref(pa), _p(q), _p(k_mean), _p(scores), int(ld), p, n, _s(stream)))
+
+
+def sa_block_attn(pa: PagedArgs, q, idx, K: int, local: int, out, ws, stream=None) -> None:
+    """Attention over the pages of ``idx`` ([T, H_kv, K] int32) and the ``local`` newest pages."""
+    p, n = _ws(ws)
+    _check(load().sa_block_attn(ctypes.byref(pa), _p(q), _p(idx), K, local, _p(out), p, n, _s(stream)))
+
+
+def sa_fused_block_attn(pa: PagedArgs, q, k_mean, K: int, local: int, idx_out, out, ws, stream=None) -> None:
+    """Page scores, exact top-k and attention over the picks and the local pages."""
+    p, n = _ws(ws)
+    _check(load().sa_fused_block_attn(ctypes.byref(pa), _p(q), _p(k_mean), K, local, _p(idx_out), _p(out), p, n,
+                                      _s(stream)))
+
+
+def sa_prefix_attn(pa: PagedArgs, q, shared_pages: int, out, ws, stream=None) -> None:
+    """Attention over whole sequences whose first ``shared_pages`` pages are the same."""
+    p, n = _ws(ws)
+    _check(load().sa_prefix_attn(ctypes.byref(pa), _p(q), shared_pages, _p(out), p, n, _s(stream)))
+
+
 def sa_check_device_status(ws, stream=None) -> int:
     """Synchronise, read and clear the sticky device status; returns the sa status."""
     return int(load().sa_check_device_status(_p(ws), _s(stream)))
@@ -346,6 +419,28 @@ def upload(w, device="cuda", K: Optional[int] = None, pad: Optional[dict] = None
 
 def new_workspace(dp: DeviceProblem, device="cuda", stream=None) -> torch.Tensor:
     n = sa_workspace_size(dp.ia, dp.aa, dp.K)
+    if n == 0:
+        raise SAError(SA_ERR_INVALID_ARG, "workspace size query rejected the arguments")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    sa_workspace_init(ws, stream)
+    return ws
+
+
+def paged_args(q_seq, q_pos, page_table, H: int, H_kv: int, D: int, P: int, n_pages: int, K, V,
+               scale: float) -> PagedArgs:
+    """Argument struct of the paged calls from device tensors (which the caller
+    keeps alive): q_seq and q_pos [T] int32, page_table [B, max_pages] int32
+    (rows may be strided), K and V [n_pages, H_kv, P, D] bf16."""
+    if page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise SAError(SA_ERR_INVALID_ARG, "page_table must be [B, max_pages] with dense rows")
+    B, max_pages = page_table.shape
+    return PagedArgs(B, q_seq.numel(), H, H_kv, D, P, n_pages, max_pages, _p(q_seq), _p(q_pos), _p(page_table),
+                     page_table.stride(0) if B > 1 else 0, _p(K), _p(V), float(scale))
+
+
+def new_paged_workspace(pa: PagedArgs, K: int = 0, local: int = 0, shared_pages: int = 0, device="cuda",
+                        stream=None) -> torch.Tensor:
+    n = sa_paged_workspace_size(pa, K, local, shared_pages)
     if n == 0:
         raise SAError(SA_ERR_INVALID_ARG, "workspace size query rejected the arguments")
     ws = torch.empty(n, dtype=torch.uint8, device=device)

@@ -94,35 +94,28 @@ index_key_kernel(const uint16_t *__restrict__ kproj, int n, const int32_t *__res
 
 }  // namespace
 
+double rope_frequency(const sa_rope_args &rope, int i) {
+  double f = 1.0 / std::pow(rope.base, static_cast<double>(2 * i) / rope.dim);
+  if (rope.original_seq_len > 0) {
+    auto corrected = [&](double turns) {
+      return rope.dim * std::log(rope.original_seq_len / (turns * 2.0 * kPi)) / (2.0 * std::log(rope.base));
+    };
+    const double low = std::max(std::floor(corrected(rope.beta_fast)), 0.0);
+    const double high = std::min(std::ceil(corrected(rope.beta_slow)), static_cast<double>(rope.dim - 1));
+    const double ramp = std::min(std::max((i - low) / std::max(high - low, 1e-3), 0.0), 1.0);
+    f = f / rope.factor * ramp + f * (1.0 - ramp);
+  }
+  return f;
+}
+
 cudaError_t launch_index_key_publish(const void *kproj, int n, const int32_t *seq, const int32_t *grp, int r,
                                      const float *weight, float eps, const sa_rope_args &rope, uint8_t *k_I,
                                      float *k_scale, int B, int N_rows, int64_t k_seq_stride, uint32_t *status,
                                      cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
   const int64_t kseq_rows = k_seq_stride ? k_seq_stride / kKeyDim : N_rows;
-  // f_i = base^(-2i / dim); with original_seq_len > 0 (YaRN) the pairs below
-  // the corrected dimension of beta_fast keep it, those above that of
-  // beta_slow are divided by factor, and a linear ramp fades between (the
-  // corrected dimension: the one whose wavelength completes `turns` rotations
-  // over the training context)
   RopeFreqs fr{};
-  const int pairs = rope.dim / 2;
-  double low = 0.0, high = 0.0;
-  if (rope.original_seq_len > 0) {
-    auto corrected = [&](double turns) {
-      return rope.dim * std::log(rope.original_seq_len / (turns * 2.0 * kPi)) / (2.0 * std::log(rope.base));
-    };
-    low = std::max(std::floor(corrected(rope.beta_fast)), 0.0);
-    high = std::min(std::ceil(corrected(rope.beta_slow)), static_cast<double>(rope.dim - 1));
-  }
-  for (int i = 0; i < pairs; ++i) {
-    double f = 1.0 / std::pow(rope.base, static_cast<double>(2 * i) / rope.dim);
-    if (rope.original_seq_len > 0) {
-      const double ramp = std::min(std::max((i - low) / std::max(high - low, 1e-3), 0.0), 1.0);
-      f = f / rope.factor * ramp + f * (1.0 - ramp);
-    }
-    fr.f[i] = f;
-  }
+  for (int i = 0; i < rope.dim / 2; ++i) fr.f[i] = rope_frequency(rope, i);
   return launch_ex(false, index_key_kernel, dim3((n + kKeyWarps - 1) / kKeyWarps), dim3(32 * kKeyWarps), 0, stream, 1,
                    static_cast<const uint16_t *>(kproj), n, seq, grp, r, weight, eps, rope.dim, fr, k_I, k_scale, B,
                    N_rows, kseq_rows, status);

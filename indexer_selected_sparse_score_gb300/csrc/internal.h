@@ -106,6 +106,32 @@ size_t attn_umma_scratch(const sa_index_args &ia, const sa_attn_args &aa, int K)
 cudaError_t launch_sparse_mqa_umma(const sa_index_args &ia, const sa_attn_args &aa, const int32_t *idx, int K,
                                    void *out, void *scratch, bool inputs_ready, uint32_t *status, cudaStream_t stream);
 
+// Rotation frequency of pair i of `rope` (radians per position): base^(-2i /
+// dim); with original_seq_len > 0 (YaRN) the pairs below the corrected
+// dimension of beta_fast keep it, those above that of beta_slow are divided by
+// factor, and a linear ramp fades between (the corrected dimension: the one
+// whose wavelength completes `turns` rotations over the training context).
+double rope_frequency(const sa_rope_args &rope, int i);
+
+// Paged cache (sa_paged_args).  `status` is the workspace's status word.
+cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t k_stride, const void *v,
+                                int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                const sa_rope_args *rope, bool halves, void *k_mean, uint32_t *status,
+                                cudaStream_t stream);
+// With row_seq and row_pos ([T, H_kv]) it also writes the top-k's token arrays:
+// per row the token's sequence and a position whose visible count at ratio P is
+// the number of pages before the `local` newest.
+cudaError_t launch_page_scores(const sa_paged_args &pa, const void *q, const void *k_mean, float *scores, int64_t ld,
+                               int local, int32_t *row_seq, int32_t *row_pos, uint32_t *status, cudaStream_t stream);
+// Attention over selected pages (idx, K, local) and over whole sequences with
+// a shared prefix; scratch holds the split partials.
+cudaError_t launch_block_attn(const sa_paged_args &pa, const void *q, const int32_t *idx, int K, int local, void *out,
+                              void *scratch, uint32_t *status, cudaStream_t stream);
+cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int shared_pages, void *out, void *scratch,
+                               uint32_t *status, cudaStream_t stream);
+size_t block_attn_scratch(const sa_paged_args &pa, int K, int local);
+size_t prefix_attn_scratch(const sa_paged_args &pa, int shared_pages);
+
 // Kernel launches of one fused call (index score, top-k, attention, combine).
 int fused_launch_count(const sa_index_args &ia, const sa_attn_args &aa, int K,
                        const SplitPlan &plan);

@@ -1,0 +1,226 @@
+// New keys and values into the pages of a paged cache, rotary embedding on the
+// way ("DeepSeek-V4.1-Flash-NVFP4 inference/model.py", Attention._window_kv:
+// apply_rotary_emb of the new kv, then the cache write), the queries rotated
+// alongside, and the mean key of every page that fills.
+//
+// Rotation: pair i turns by p f_i.  The frequency is held as a 64-bit fraction
+// of a turn, F = f / (2 pi) 2^64, so p F modulo 2^64 is the angle modulo a turn
+// by one integer product (the wrap-around is the reduction), exact to p 2^-53
+// of F for any 31-bit position; its upper 32 bits go to fp32 as half turns
+// (error below 2^-24 of a half turn) and to sincospif.  A reduction in double
+// would be limited by the part's FP64 rate (two operations a clock per SM).
+//
+// Traffic: every row is read once and written once (2 T (H + 2 H_kv) D values),
+// bound by HBM for a prefill and by latency for a decode step.  One CTA per
+// token: half of it tables the D / 2 rotations in shared memory while every
+// thread already holds its first rows' loads, then 32-byte units (two 16-byte
+// chunks, the two halves of their pairs) stream through registers.
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "paged.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 64;
+
+struct Turns {
+  uint64_t f[kMaxPairs];  // turns per position, times 2^64
+};
+
+struct AppendParams {
+  PagedView pv;
+  const uint16_t *k, *v, *q;
+  int64_t k_stride, v_stride, q_stride;
+  uint16_t *K, *V, *q_out;
+  int q_heads;   // H, or 0 without queries
+  int D, dim;
+  int halves;
+  uint32_t *status;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Four adjacent pairs of one chunk.
+__device__ __forceinline__ uint4 rotate_adjacent(uint4 x, const float2 *cs) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 c = cs[i];
+    const float a = lo_f(w[i]), b = hi_f(w[i]);
+    w[i] = pack_bf16(a * c.x - b * c.y, a * c.y + b * c.x);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight pairs (x[e], y[e]) of two chunks half the rotated span apart.
+__device__ __forceinline__ void rotate_halves(uint4 &x, uint4 &y, const float2 *cs) {
+  uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
+    const float a0 = lo_f(u[i]), a1 = hi_f(u[i]), b0 = lo_f(w[i]), b1 = hi_f(w[i]);
+    u[i] = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
+    w[i] = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
+  }
+  x = make_uint4(u[0], u[1], u[2], u[3]);
+  y = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(kThreads)
+paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
+  __shared__ float2 cs[kMaxPairs];
+  pdl_trigger();
+  const int t = blockIdx.x;
+  int b, pos;
+  if (!load_paged_token(p.pv, t, p.status, threadIdx.x == 0, b, pos)) return;  // the whole CTA alike
+  const int page = load_page(p.pv, b, pos >> p.pv.logP, p.status, threadIdx.x == 0);
+  const int slot = pos & (p.pv.P - 1);
+  const int upr = p.D >> 4;                 // 32-byte units per row
+  const int kept = (p.D - p.dim) >> 4;      // units before the rotated span
+  const int span = p.dim >> 3;              // chunks of the rotated span
+  const int units = (p.q_heads + 2 * p.pv.H_kv) * upr;
+  bool tabled = false;
+  for (int u0 = threadIdx.x; u0 - static_cast<int>(threadIdx.x) < units; u0 += 4 * kThreads) {
+    uint4 x[4], y[4];
+    int row[4], c0[4], c1[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int u = u0 + e * kThreads;
+      row[e] = u < units ? u / upr : -1;
+      const int i = u % upr, j = i - kept;
+      const bool half = p.halves && j >= 0;
+      c0[e] = half ? (p.D >> 3) - span + j : 2 * i;
+      c1[e] = half ? c0[e] + (span >> 1) : 2 * i + 1;
+      if (row[e] < 0) continue;
+      const int h = row[e] - p.q_heads;
+      const uint16_t *src = h < 0             ? p.q + t * p.q_stride + static_cast<int64_t>(row[e]) * p.D
+                            : h < p.pv.H_kv ? p.k + t * p.k_stride + static_cast<int64_t>(h) * p.D
+                                            : p.v + t * p.v_stride + static_cast<int64_t>(h - p.pv.H_kv) * p.D;
+      x[e] = *reinterpret_cast<const uint4 *>(src + 8 * c0[e]);
+      y[e] = *reinterpret_cast<const uint4 *>(src + 8 * c1[e]);
+    }
+    if (!tabled) {
+      if (threadIdx.x < p.dim / 2) {
+        const uint64_t ph = static_cast<uint64_t>(pos) * turns.f[threadIdx.x] + (uint64_t{1} << 31);
+        float sn, c;
+        sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &sn, &c);
+        cs[threadIdx.x] = make_float2(c, sn);
+      }
+      __syncthreads();
+      tabled = true;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (row[e] < 0) continue;
+      const int h = row[e] - p.q_heads;
+      uint16_t *dst;
+      if (h < 0) {
+        dst = p.q_out + (static_cast<int64_t>(t) * p.pv.H + row[e]) * p.D;
+      } else {
+        if (page < 0) continue;
+        const int hk = h < p.pv.H_kv ? h : h - p.pv.H_kv;
+        dst = (h < p.pv.H_kv ? p.K : p.V) +
+              ((static_cast<int64_t>(page) * p.pv.H_kv + hk) * p.pv.P + slot) * p.D;
+      }
+      const int first = (p.D >> 3) - span;  // first rotated chunk
+      if (h < p.pv.H_kv && c0[e] >= first) {
+        if (p.halves) {
+          rotate_halves(x[e], y[e], cs + 8 * (c0[e] - first));
+        } else {
+          x[e] = rotate_adjacent(x[e], cs + 4 * (c0[e] - first));
+          y[e] = rotate_adjacent(y[e], cs + 4 * (c1[e] - first));
+        }
+      }
+      *reinterpret_cast<uint4 *>(dst + 8 * c0[e]) = x[e];
+      *reinterpret_cast<uint4 *>(dst + 8 * c1[e]) = y[e];
+    }
+  }
+}
+
+// Mean of the key rows of every page whose last position is among the tokens.
+// CTA (x, h): tokens x * per .. + per - 1, KV head h.  It runs after the append
+// has written every row, so a page may fill from tokens in any order.
+__global__ void __launch_bounds__(kThreads)
+page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int D, int per) {
+  __shared__ float part[kThreads / 8 * 64];
+  pdl_wait();
+  const int h = blockIdx.y, cpr = D >> 3;          // 16-byte chunks per row
+  const int c = threadIdx.x % cpr, r0 = threadIdx.x / cpr, rows = kThreads / cpr;
+  const int t0 = blockIdx.x * per, t1 = min(t0 + per, pv.T);
+  for (int t = t0; t < t1; ++t) {
+    int b, pos;
+    if (!load_paged_token(pv, t, nullptr, false, b, pos) || ((pos + 1) & (pv.P - 1))) continue;
+    const int page = load_page(pv, b, pos >> pv.logP, nullptr, false);
+    if (page < 0) continue;
+    const int64_t tile = static_cast<int64_t>(page) * pv.H_kv + h;
+    float s[8] = {};
+    for (int r = r0; r < pv.P; r += rows) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(K + (tile * pv.P + r) * D + 8 * c);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[2 * i] += lo_f(w[i]);
+        s[2 * i + 1] += hi_f(w[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[r0 * D + 8 * c + i] = s[i];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float m = 0.f;
+      for (int r = 0; r < rows; ++r) m += part[r * D + threadIdx.x];
+      const __nv_bfloat16 o = __float2bfloat16_rn(m / static_cast<float>(pv.P));
+      k_mean[tile * D + threadIdx.x] = *reinterpret_cast<const uint16_t *>(&o);
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t k_stride, const void *v,
+                                int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                const sa_rope_args *rope, bool halves, void *k_mean, uint32_t *status,
+                                cudaStream_t stream) {
+  if (pa.T == 0) return cudaSuccess;
+  AppendParams p;
+  p.pv = paged_view(pa);
+  p.k = static_cast<const uint16_t *>(k);
+  p.v = static_cast<const uint16_t *>(v);
+  p.q = static_cast<const uint16_t *>(q);
+  p.k_stride = k_stride ? k_stride : static_cast<int64_t>(pa.H_kv) * pa.D;
+  p.v_stride = v_stride ? v_stride : static_cast<int64_t>(pa.H_kv) * pa.D;
+  p.q_stride = q_stride ? q_stride : static_cast<int64_t>(pa.H) * pa.D;
+  p.K = static_cast<uint16_t *>(pa.K);
+  p.V = static_cast<uint16_t *>(pa.V);
+  p.q_out = static_cast<uint16_t *>(q_out);
+  p.q_heads = q ? pa.H : 0;
+  p.D = pa.D;
+  p.dim = rope ? rope->dim : 0;
+  p.halves = halves ? 1 : 0;
+  p.status = status;
+  Turns turns{};
+  for (int i = 0; i < p.dim / 2; ++i) {
+    const double f = rope_frequency(*rope, i) / (2.0 * 3.14159265358979323846);
+    turns.f[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
+  }
+  cudaError_t e = launch_ex(false, paged_append_kernel, dim3(pa.T), dim3(kThreads), 0, stream, 1, p, turns);
+  if (e != cudaSuccess || !k_mean) return e;
+  // one CTA per token and head while they are few; more tokens per CTA once
+  // the grid would exceed eight CTAs per SM (most tokens end no page)
+  const int64_t most = static_cast<int64_t>(sm_count()) * 8;
+  const int per = static_cast<int>(std::max<int64_t>(1, static_cast<int64_t>(pa.T) * pa.H_kv / most));
+  return launch_ex(true, page_mean_kernel, dim3((pa.T + per - 1) / per, pa.H_kv), dim3(kThreads), 0, stream, 1, p.pv,
+                   static_cast<const uint16_t *>(pa.K), static_cast<uint16_t *>(k_mean), pa.D, per);
+}
+
+}  // namespace sa

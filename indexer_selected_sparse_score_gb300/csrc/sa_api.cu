@@ -480,9 +480,9 @@ sa_status sa_check_device_status(void *ws, sa_stream_t stream) {
   e = cudaMemset(ws, 0, sizeof(flags));
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemset (status word)");
   if (flags & sa::kFlagTimeout) return fail(SA_ERR_TIMEOUT, "a bounded device wait gave up (flags 0x%x)", flags);
-  return fail(SA_ERR_DEVICE_DATA, "device data out of range was skipped (flags 0x%x:%s%s%s)", flags,
+  return fail(SA_ERR_DEVICE_DATA, "device data out of range was skipped (flags 0x%x:%s%s%s%s)", flags,
               (flags & sa::kFlagBadSeq) ? " q_seq" : "", (flags & sa::kFlagBadPos) ? " q_pos" : "",
-              (flags & sa::kFlagBadIndex) ? " idx" : "");
+              (flags & sa::kFlagBadIndex) ? " idx" : "", (flags & sa::kFlagBadPage) ? " page_table" : "");
 }
 
 const char *sa_status_string(sa_status s) {

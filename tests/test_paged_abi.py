@@ -1,0 +1,178 @@
+"""Argument checks of the paged-cache calls (no GPU needed): a bad argument
+returns its error before anything is enqueued."""
+import ctypes
+
+import pytest
+
+from indexer_selected_sparse_score_gb300 import binding, build
+
+INV, UNS, WS = binding.SA_ERR_INVALID_ARG, binding.SA_ERR_UNSUPPORTED, binding.SA_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load()
+
+
+def _pa(**kw):
+    base = dict(B=2, T=3, H=16, H_kv=2, D=128, P=64, n_pages=10, max_pages=5, q_seq=16, q_pos=16, page_table=16,
+                table_stride=0, K=256, V=256, scale=0.088)
+    base.update(kw)
+    return binding.PagedArgs(*[base[f] for f, _ in binding.PagedArgs._fields_])
+
+
+def _ref(pa):
+    return ctypes.byref(pa) if pa is not None else None
+
+
+SHAPES = [
+    (None, INV),
+    (dict(B=0), INV), (dict(T=-1), INV), (dict(H=0), INV), (dict(H_kv=0), INV), (dict(H=15), INV),
+    (dict(n_pages=0), INV), (dict(max_pages=0), INV),
+    (dict(D=96), UNS), (dict(D=512), UNS), (dict(P=48), UNS), (dict(P=8), UNS), (dict(P=256), UNS),
+    (dict(H=258, H_kv=2), UNS),                       # 129 heads per KV head
+    (dict(n_pages=1 << 24, H_kv=2), UNS),             # 2^31 cache rows
+    (dict(max_pages=(1 << 24) + 1), UNS),             # positions past 2^30
+    (dict(T=1 << 27), UNS),
+    (dict(table_stride=4), INV), (dict(table_stride=-5), INV),
+    (dict(q_seq=None), INV), (dict(q_pos=None), INV), (dict(page_table=None), INV),
+    (dict(q_seq=18), INV), (dict(page_table=17), INV),
+]
+CACHE = [(dict(K=None), INV), (dict(V=None), INV), (dict(K=264), INV), (dict(V=257), INV)]
+
+
+def _append(lib, pa, **kw):
+    a = dict(k=256, ks=0, v=256, vs=0, q=None, qs=0, qo=None, rope=None, halves=0, mean=None, ws=256, nb=256)
+    a.update(kw)
+    return lib.sa_paged_append(_ref(pa), a["k"], a["ks"], a["v"], a["vs"], a["q"], a["qs"], a["qo"],
+                               ctypes.byref(a["rope"]) if a["rope"] is not None else None, a["halves"], a["mean"],
+                               a["ws"], a["nb"], None)
+
+
+def _scores(lib, pa, **kw):
+    a = dict(q=256, mean=256, scores=256, ld=5, ws=256, nb=256)
+    a.update(kw)
+    return lib.sa_page_scores(_ref(pa), a["q"], a["mean"], a["scores"], a["ld"], a["ws"], a["nb"], None)
+
+
+def _block(lib, pa, **kw):
+    a = dict(q=256, idx=256, K=4, local=1, out=256, ws=256, nb=1 << 30)
+    a.update(kw)
+    return lib.sa_block_attn(_ref(pa), a["q"], a["idx"], a["K"], a["local"], a["out"], a["ws"], a["nb"], None)
+
+
+def _fused(lib, pa, **kw):
+    a = dict(q=256, mean=256, K=4, local=1, idx=None, out=256, ws=256, nb=1 << 30)
+    a.update(kw)
+    return lib.sa_fused_block_attn(_ref(pa), a["q"], a["mean"], a["K"], a["local"], a["idx"], a["out"], a["ws"],
+                                   a["nb"], None)
+
+
+def _prefix(lib, pa, **kw):
+    a = dict(q=256, shared=2, out=256, ws=256, nb=1 << 30)
+    a.update(kw)
+    return lib.sa_prefix_attn(_ref(pa), a["q"], a["shared"], a["out"], a["ws"], a["nb"], None)
+
+
+@pytest.mark.parametrize("kw,status", SHAPES)
+def test_shapes_are_checked_by_every_call(lib, kw, status):
+    pa = None if kw is None else _pa(**kw)
+    for call in (_append, _scores, _block, _fused, _prefix):
+        assert call(lib, pa) == status, call.__name__
+        assert lib.sa_last_error_detail()
+    assert lib.sa_paged_workspace_size(_ref(pa), 4, 1, 2) == 0
+
+
+@pytest.mark.parametrize("kw,status", CACHE)
+def test_cache_pointers_are_checked(lib, kw, status):
+    for call in (_append, _block, _fused, _prefix):
+        assert call(lib, _pa(**kw)) == status, call.__name__
+
+
+def _rope(**kw):
+    base = dict(dim=64, base=10000.0, factor=1.0, original_seq_len=0, beta_fast=32.0, beta_slow=1.0)
+    base.update(kw)
+    return binding.RopeArgs(*[base[f] for f, _ in binding.RopeArgs._fields_])
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=None), INV), (dict(v=None), INV), (dict(k=264), INV), (dict(mean=8), INV),
+    (dict(q=256), INV), (dict(qo=256), INV),                        # q and q_out go together
+    (dict(q=256, qo=256, qs=16 * 128 + 8), INV),                    # in place needs dense queries
+    (dict(ks=2 * 128 - 8), INV), (dict(vs=2 * 128 + 4), INV), (dict(q=256, qo=512, qs=128), INV), (dict(ks=-8), INV),
+    (dict(rope=_rope(dim=72)), INV), (dict(rope=_rope(dim=144)), INV), (dict(rope=_rope(dim=-16)), INV),
+    (dict(rope=_rope(base=1.0)), INV), (dict(rope=_rope(base=float("nan"))), INV), (dict(rope=_rope(factor=0.0)), INV),
+    (dict(rope=_rope(original_seq_len=4096, beta_slow=0.0)), INV),
+    (dict(ws=None), WS), (dict(nb=255), WS), (dict(ws=264), INV),
+])
+def test_append_rejects_bad_arguments(lib, kw, status):
+    assert _append(lib, _pa(), **kw) == status
+    assert lib.sa_last_error_detail()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INV), (dict(mean=None), INV), (dict(scores=None), INV), (dict(scores=258), INV), (dict(ld=4), INV),
+    (dict(q=264), INV), (dict(ws=None), WS), (dict(nb=128), WS),
+])
+def test_scores_reject_bad_arguments(lib, kw, status):
+    assert _scores(lib, _pa(), **kw) == status
+
+
+@pytest.mark.parametrize("call", [_block, _fused])
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INV), (dict(out=None), INV), (dict(out=264), INV), (dict(K=-1), INV), (dict(local=-1), INV),
+    (dict(idx=258), INV), (dict(ws=None), WS), (dict(nb=128), WS),
+])
+def test_block_attention_rejects_bad_arguments(lib, call, kw, status):
+    assert call(lib, _pa(), **kw) == status
+
+
+def test_block_attention_needs_a_list_and_the_fused_call_a_local_page(lib):
+    assert _block(lib, _pa(), idx=None) == INV
+    assert _fused(lib, _pa(), local=0) == INV
+    assert _fused(lib, _pa(), mean=None) == INV
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INV), (dict(out=None), INV), (dict(shared=-1), INV), (dict(shared=6), INV), (dict(ws=None), WS),
+    (dict(nb=128), WS),
+])
+def test_prefix_attention_rejects_bad_arguments(lib, kw, status):
+    assert _prefix(lib, _pa(), **kw) == status
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf")])
+def test_scale_must_be_finite(lib, scale):
+    for call in (_scores, _block, _fused, _prefix):
+        assert call(lib, _pa(scale=scale)) == INV
+
+
+def test_no_tokens_enqueue_nothing(lib):
+    pa = _pa(T=0, q_seq=None, q_pos=None, page_table=None, K=None, V=None)
+    assert _append(lib, pa, k=None, v=None) == binding.SA_OK
+    assert _scores(lib, pa, q=None, mean=None, scores=None) == binding.SA_OK
+    assert _block(lib, pa, q=None, idx=None, out=None) == binding.SA_OK
+    assert _prefix(lib, pa, q=None, out=None) == binding.SA_OK
+
+
+def test_workspace_grows_with_what_it_holds(lib):
+    n = lib.sa_paged_workspace_size(_ref(_pa()), 0, 1, 0)
+    assert n >= 256 and n % 256 == 0
+    assert lib.sa_paged_workspace_size(_ref(_pa()), 4, 1, 0) > n
+    assert lib.sa_paged_workspace_size(_ref(_pa()), -1, 1, 0) == 0
+    assert lib.sa_paged_workspace_size(_ref(_pa()), 0, -1, 0) == 0
+    assert lib.sa_paged_workspace_size(_ref(_pa()), 0, 0, 6) == 0
+
+
+def test_strides_of_python_tensors():
+    import torch
+    x = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    assert binding._token_stride("k", x) == 256
+    assert binding._token_stride("k", torch.zeros(4, 6, 128)[:, 1:3]) == 768
+    with pytest.raises(binding.SAError):
+        binding._token_stride("k", torch.zeros(4, 2, 256)[..., ::2])
+    with pytest.raises(binding.SAError):
+        binding._token_stride("k", torch.zeros(2, 4, 128).transpose(0, 1))
+    with pytest.raises(binding.SAError):
+        binding.paged_args(x, x, torch.zeros(5, 2, dtype=torch.int32).T, 16, 2, 128, 64, 10, x, x, 1.0)
