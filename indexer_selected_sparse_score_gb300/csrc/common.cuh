@@ -14,7 +14,6 @@ enum : uint32_t {
   kFlagBadPos = 2u,     // q_pos[t] < 0 or n_vis(t) > N_c
   kFlagBadIndex = 4u,   // an index outside [-1, n_vis(t))
   kFlagTimeout = 8u,    // a bounded wait gave up
-  kFlagBadPage = 16u,   // a page id outside [0, n_pages)
 };
 
 __device__ __forceinline__ void raise_flag(uint32_t *status, uint32_t f) {

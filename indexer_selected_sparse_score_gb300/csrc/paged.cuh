@@ -6,6 +6,9 @@
 
 namespace sa {
 
+// Sticky status flag of the paged calls, beside those of common.cuh.
+constexpr uint32_t kFlagBadPage = 16u;  // a page id outside [0, n_pages)
+
 struct PagedView {
   int B, T, H, H_kv, P, logP, n_pages, max_pages;
   int64_t table_stride;

@@ -101,17 +101,7 @@ cudaError_t launch(const sa_paged_args &pa, PagedAttnParams &p, const void *q, v
 
 }  // namespace
 
-size_t block_attn_scratch(const sa_paged_args &, int, int) { return 0; }
 size_t prefix_attn_scratch(const sa_paged_args &, int) { return 0; }
-
-cudaError_t launch_block_attn(const sa_paged_args &pa, const void *q, const int32_t *idx, int K, int local, void *out,
-                              void *, uint32_t *status, cudaStream_t stream) {
-  PagedAttnParams p{};
-  p.idx = idx;
-  p.n_list = K;
-  p.local = local;
-  return launch(pa, p, q, out, status, stream);
-}
 
 cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int shared_pages, void *out, void *,
                                uint32_t *status, cudaStream_t stream) {

@@ -1,0 +1,765 @@
+// Attention of single tokens over lists of pages, on the 5th-generation tensor
+// cores: the selected and local pages of sa_block_attn, and the pages past the
+// shared ones of sa_prefix_attn.
+//
+// A unit is one token's group of query heads over one KV head (64 heads at
+// most): few rows against many keys.  So the products are taken transposed,
+// the keys in the 128 lanes of the accumulator and the heads in its columns,
+// and no row of the tensor core is spent on padding:
+//   S^T = K Q^T     M = 128 keys, N = heads (16, 32 or 64), K = D
+//   P^T             one thread per key: p = 2^(c s - m_ref[h]), bf16, to shared
+//                   memory with the heads contiguous (the MN-major B operand)
+//   O^T += V^T P^T  M = D, N = heads, K = 128 keys
+// The pages land by TMA in the 128-byte swizzle, which is K-major for the
+// first product and MN-major for the second, so K and V are copied once and
+// never rearranged.  The reference maximum m_ref is the first tile's and is
+// raised only when a logit passes it by 2^8 (one vote per tile); sums of p stay
+// in registers per key and head and are reduced once per unit.  Weights are
+// rounded to bf16 for the second product (2^-9 of each at most, against an
+// output that is itself rounded to bf16); logits, sums and O are fp32.
+//
+// Work: the tiles of all units (128 keys each) form one list, cut evenly over
+// one CTA per SM (a decode step reads each page once, so HBM is the bound and
+// every SM must stream to the end).  A unit that falls into several CTAs
+// leaves its parts (m_ref, sum, O) in scratch for a merge kernel.  Entries that
+// name no page are dropped before tiles are formed; positions past the token's
+// own are masked, and the V rows they hold are zeroed in shared memory, since
+// 0 x NaN would reach the sum.
+//
+// Warps: 0-3 softmax and output; 4 issues S^T, 5 issues O^T; 6 resolves the
+// lists and issues the copies, publishing one record per tile.  Every wait is
+// bounded; on expiry the kernel flags the status word, drains its copies and
+// products and returns.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "paged_list.h"
+#include "paged_umma.cuh"
+
+namespace sa {
+namespace {
+
+using namespace umma;
+
+constexpr int kTile = 128;      // keys per tile
+constexpr int kThreads = 224;
+constexpr int kWarpS = 4, kWarpO = 5, kWarpLoad = 6;
+constexpr int kRecs = 8;        // tile records; the loader runs fewer tiles ahead
+// The reference a weight is taken against lies kHead above the maximum that
+// set it (log2 units), and is raised once a logit passes that maximum by kLazy:
+// unnormalised sums of weights up to 2^(kLazy - kHead) times any bf16 values
+// stay finite, and weights down to 2^-106 of the largest are kept.
+constexpr float kLazy = 8.f, kHead = 20.f;
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kMasked = 8, kDirect = 16 };
+
+struct Record {
+  int flags;
+  int row;       // first output row of the unit (t * H + head)
+  int heads;     // heads of the unit
+  int slot;      // part slot of the piece
+  uint32_t cnt[2];  // byte g: keys present among keys 16 g .. 16 g + 15
+};
+
+template <int N, int kDim>
+struct ListSmem {
+  static constexpr int kStages = kDim == 128 ? 3 : 6;
+  static constexpr uint32_t kBlock = kTile * 128;          // one 64-dim block of a tile
+  static constexpr uint32_t kKv = kBlock * (kDim / 64);
+  static constexpr size_t k = 0;
+  static constexpr size_t v = k + kStages * kKv;
+  static constexpr size_t p = v + kStages * kKv;           // [128 keys][64 heads] bf16
+  static constexpr size_t q = p + 16384;                   // [D / 64][N][128 B]
+  static constexpr size_t recs = q + N * kDim * 2;
+  static constexpr size_t red = recs + kRecs * sizeof(Record);   // [4][N]
+  static constexpr size_t fac = red;                       // [N], over the reduction's first row (see below)
+  static constexpr size_t mref = red + 4 * N * 4;          // [N]
+  static constexpr size_t queue = mref + N * 4;             // [48] page entries waiting for a tile
+  static constexpr size_t bars = (queue + 48 * 4 + 7) & ~size_t(7);
+  static constexpr int kBars = 4 * kStages + 2 + 4 + 2 + 2 + kRecs + 2;
+  static constexpr size_t misc = bars + kBars * 8;
+  static constexpr size_t total = misc + 64;
+  static_assert(total + 1024 <= 232448, "shared memory budget");
+  // O^T at dim 64 reads a second block past V's last slot (lanes nobody reads)
+  static_assert(v + kStages * kKv + kBlock <= total, "V overread stays in bounds");
+};
+
+__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <int N, int kDim>
+__global__ void __launch_bounds__(kThreads, 1)
+page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap, const ListParams p) {
+  using L = ListSmem<N, kDim>;
+  constexpr int kSt = L::kStages, kB = kDim / 64;
+  constexpr uint32_t kColO = 2 * N;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *ks = smem + L::k, *vs = smem + L::v, *ps = smem + L::p, *qs = smem + L::q;
+  Record *recs = reinterpret_cast<Record *>(smem + L::recs);
+  float *red_s = reinterpret_cast<float *>(smem + L::red);
+  float *mref_s = reinterpret_cast<float *>(smem + L::mref);
+  // fac[h] overwrites red[0][h], which only the thread that writes it has read;
+  // between a read of fac and the next write of red lie a vote of the four
+  // warps or (raise, then end of the unit, in one tile) the product that waits
+  // for all four
+  float *fac_s = reinterpret_cast<float *>(smem + L::fac);
+  int *queue = reinterpret_cast<int *>(smem + L::queue);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
+  uint64_t *kfull = bars, *kempty = kfull + kSt, *vfull = kempty + kSt, *vempty = vfull + kSt;
+  uint64_t *qfull = vempty + kSt, *qempty = qfull + 1, *sfull = qempty + 1, *sempty = sfull + 2;
+  uint64_t *pfull = sempty + 2, *pempty = pfull + 1, *ofull = pempty + 1, *oempty = ofull + 1;
+  uint64_t *rfull = oempty + 1, *done = rfull + kRecs;
+  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
+  volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 8);
+  long long *start_s = reinterpret_cast<long long *>(smem + L::misc + 16);  // total tiles, offset of the first token
+  int *start_t = reinterpret_cast<int *>(smem + L::misc + 32);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = gridDim.x, c = blockIdx.x;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < kSt; ++i) {
+      mbar_init(&kfull[i], 1);
+      mbar_init(&kempty[i], 1);
+      mbar_init(&vfull[i], 1);
+      mbar_init(&vempty[i], 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sempty[i], 4);
+      mbar_init(&done[i], 1);
+    }
+    mbar_init(pfull, 4);
+    mbar_init(pempty, 1);
+    mbar_init(ofull, 1);
+    mbar_init(oempty, 4);
+    for (int i = 0; i < kRecs; ++i) mbar_init(&rfull[i], 1);
+    *abort_s = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpS) {
+    tmem_alloc(tmem_base_s, 256);
+    tmem_relinquish();
+  }
+  // tiles of token t's units in whole-sequence mode (0 for a token to skip)
+  const int spt = kTile >> p.pv.logP;  // pages per tile
+  const int upt = p.pv.H_kv * p.gb;    // units per token
+  auto count_of = [&](int t, bool report) -> int {
+    int b, pos;
+    if (!load_paged_token(p.pv, t, p.status, report, b, pos)) return 0;
+    const int n = (pos >> p.pv.logP) + 1 - p.first_page;
+    if (n <= 0) {
+      if (report) raise_flag(p.status, kFlagBadPos);
+      return 0;
+    }
+    return (n + spt - 1) / spt;
+  };
+  if (p.whole) {
+    // Sequence lengths are known to the device only: every CTA sums the tiles
+    // of all tokens (a contiguous share per thread, one scan) and finds the
+    // token its first tile falls into.
+    long long *sums = reinterpret_cast<long long *>(ks);
+    const int per = (p.pv.T + kThreads - 1) / kThreads;
+    const int ta = min(tid * per, p.pv.T), tb = min(ta + per, p.pv.T);
+    long long own = 0;
+    for (int t = ta; t < tb; ++t) own += count_of(t, c == 0);
+    sums[tid] = own;
+    if (tid == 0) *start_t = p.pv.T;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int i = 0; i < kThreads; ++i) {
+      if (i < tid) before += sums[i];
+      total += sums[i];
+    }
+    const long long x0 = total * upt * c / G;
+    if (tid == 0) start_s[0] = total * upt;
+    if (before * upt <= x0 && x0 < (before + own) * upt) {
+      int t = ta;
+      for (; t < tb; ++t) {
+        const int n = count_of(t, false);
+        if (x0 < (before + n) * upt) break;
+        before += n;
+      }
+      *start_t = t;
+      start_s[1] = before * upt;
+    }
+  } else if (tid == 0) {
+    start_s[0] = static_cast<long long>(p.pv.T) * upt * p.tpu;
+  }
+  fence_proxy_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_s;
+  const long long tot = start_s[0];
+  const long long x_begin = tot * c / G, x_end = tot * (c + 1) / G;
+  auto fail = [&]() {
+    raise_flag(p.status, kFlagTimeout);
+    *abort_s = 1;
+  };
+
+  if (warp == kWarpLoad) {
+    // ------------------------------------------------------------------ loader
+    if (lane == 0) {
+      prefetch_tmap(&qmap);
+      prefetch_tmap(&kmap);
+      prefetch_tmap(&vmap);
+    }
+    int n = 0, qn = 0;
+    bool ok = true;
+    int cut_unit = -1, cut_last = 0;
+    long long base;
+    int t, sub;
+    if (p.whole) {
+      t = *start_t;
+      base = start_s[1];
+      sub = 0;
+      if (x_begin < x_end) {  // units of the token before the first tile
+        const int cnt = count_of(t, false);
+        sub = static_cast<int>((x_begin - base) / cnt);
+        base += static_cast<long long>(sub) * cnt;
+      }
+    } else {
+      const long long u = p.tpu ? x_begin / p.tpu : 0;
+      t = static_cast<int>(u / upt);
+      sub = static_cast<int>(u % upt);
+      base = u * p.tpu;
+    }
+    const uint32_t rows_total = static_cast<uint32_t>(p.pv.n_pages) * p.pv.H_kv * p.pv.P;
+    long long x = x_begin;
+    while (ok && x < x_end) {
+      const int cnt = p.whole ? count_of(t, false) : p.tpu;
+      if (cnt == 0) {
+        ++t;
+        continue;
+      }
+      const int u = t * upt + sub;
+      const int a = static_cast<int>(x - base);
+      const int e = static_cast<int>(min(static_cast<long long>(cnt), x_end - base));
+      const bool starts = a == 0, ends = e == cnt;
+      int b = 0, pos = 0;
+      const bool tok = load_paged_token(p.pv, t, p.status, lane == 0 && sub == 0 && starts && !p.whole, b, pos);
+      if (tok) {
+        const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64;
+        const int last = pos >> p.pv.logP;
+        const int f = p.whole ? p.first_page : max(last + 1 - p.local, 0);
+        const int nlist = p.whole ? 0 : p.K;
+        const int r1 = min(e * spt, nlist + last + 1 - f);
+        int r = a * spt, qh = 0, qe = 0;  // raw entries, queue head and end
+        // the CTA of tile y is floor(((y + 1) G - 1) / tot)
+        const int c_last = static_cast<int>(((base + cnt) * G - 1) / tot);
+        if (starts && !ends) {
+          cut_unit = u;
+          cut_last = c_last;
+        }
+        if (p.keep && starts && lane == 0) p.info[u] = make_int2(c, c_last);
+        // page entry i of the list (page id, bit 30 set for the token's own
+        // page, whose later positions are masked), -1 when it names no page
+        auto resolve = [&](int i) -> int {
+          int j;
+          if (i < nlist) {
+            j = p.idx[(static_cast<int64_t>(t) * p.pv.H_kv + hk) * p.K + i];
+            if (j < 0 || j >= f) {
+              if (j < -1 || j > last) raise_flag(p.status, kFlagBadIndex);
+              return -1;
+            }
+          } else {
+            j = f + i - nlist;
+          }
+          const int page = load_page(p.pv, b, j, p.status, true);
+          return page < 0 ? -1 : page | (j == last ? 1 << 30 : 0);
+        };
+        bool first = true, more = true;
+        while (more) {
+          while (qe - qh <= spt && r < r1) {  // enough for this tile and to know whether another follows
+            const int rest = qe - qh;
+            const int keep = lane < rest ? queue[qh + lane] : 0;
+            const int ent = r + lane < r1 ? resolve(r + lane) : -1;
+            const uint32_t m = __ballot_sync(0xffffffffu, ent >= 0);
+            __syncwarp();
+            if (lane < rest) queue[lane] = keep;
+            if (ent >= 0) queue[rest + __popc(m & ((1u << lane) - 1))] = ent;
+            __syncwarp();
+            qh = 0;
+            qe = rest + __popc(m);
+            r += 32;
+          }
+          const int take = min(spt, qe - qh);
+          more = qe - qh > take;
+          const int s = n % kSt;
+          if (!mbar_wait_warp(&kempty[s], ((n / kSt) & 1) ^ 1) || *abort_s) {
+            ok = false;
+            break;
+          }
+          // slot of this lane's copy: boxes of P rows x 64 dims
+          const int q = lane / kB, kb = lane % kB;
+          const int ent = q < take ? queue[qh + q] : -1;
+          // an empty slot reads past the tensor's end: the copy fills zeros
+          const uint32_t y = ent >= 0 ? ((static_cast<uint32_t>(ent) & 0x3FFFFFFFu) * p.pv.H_kv + hk) * p.pv.P
+                                      : rows_total;
+          if (lane == 0) {
+            uint32_t cn[2] = {0, 0};
+            int masked = 0;
+            for (int g = 0; g < 8; ++g) {
+              const int qq = (16 * g) >> p.pv.logP;
+              int have = 0;
+              if (qq < take) {
+                have = 16;
+                if (queue[qh + qq] >> 30) {
+                  have = min(max(pos + 1 - last * p.pv.P - (16 * g - qq * p.pv.P), 0), 16);
+                  masked |= have < 16;
+                }
+              }
+              cn[g >> 2] |= static_cast<uint32_t>(have) << (8 * (g & 3));
+            }
+            Record &rec = recs[n % kRecs];
+            rec.flags = (first ? kFirst : 0) | (more ? 0 : kLast) | (masked ? kMasked : 0) |
+                        (!p.keep && starts && ends ? kDirect : 0);
+            rec.row = t * p.pv.H + h0;
+            rec.heads = min(64, (hk + 1) * p.group - h0);
+            rec.slot = p.keep ? u + c : 2 * c + (starts ? 1 : 0);
+            rec.cnt[0] = cn[0];
+            rec.cnt[1] = cn[1];
+            mbar_arrive(&rfull[n % kRecs]);
+            mbar_expect_tx(&kfull[s], L::kKv);
+          }
+          __syncwarp();
+          const bool mine = q < spt;
+          const uint32_t dst = kb * L::kBlock + q * p.pv.P * 128;
+          if (mine) tma_load_2d(ks + s * L::kKv + dst, &kmap, &kfull[s], 64 * kb, static_cast<int>(y));
+          if (first) {
+            // the queries, once the previous unit's last product has read its own
+            bool got = true;
+            if (lane == 0) {
+              got = mbar_wait(qempty, (qn & 1) ^ 1);
+              if (got) {
+                mbar_expect_tx(qfull, N * kDim * 2);
+                for (int i = 0; i < kB; ++i)
+                  tma_load_2d(qs + i * N * 128, &qmap, qfull, 64 * i, t * p.pv.H + h0);
+              }
+            }
+            if (!__shfl_sync(0xffffffffu, got, 0)) ok = false;
+            else ++qn;
+          }
+          if (!mbar_wait_warp(&vempty[s], ((n / kSt) & 1) ^ 1)) ok = false;
+          if (ok) {
+            if (lane == 0) mbar_expect_tx(&vfull[s], L::kKv);
+            __syncwarp();
+            if (mine) tma_load_2d(vs + s * L::kKv + dst, &vmap, &vfull[s], 64 * kb, static_cast<int>(y));
+          }
+          ++n;
+          if (!ok) break;
+          qh += take;
+          first = false;
+        }
+      }
+      x = base + e;
+      if (ends) {
+        base += cnt;
+        if (++sub == upt) {
+          sub = 0;
+          ++t;
+        }
+      }
+    }
+    if (lane == 0) {
+      if (!ok) fail();
+      if (!p.keep) p.cut[c] = make_int2(cut_unit, cut_last);
+      if (ok) {
+        recs[n % kRecs].flags = kEnd;
+        mbar_arrive(&rfull[n % kRecs]);
+      }
+      // drain: every copy issued lands before the CTA exits (the last tile's V
+      // copy may not have been issued when a wait gave up)
+      for (int i = max(0, n - kSt); i < n; ++i) {
+        mbar_wait(&kfull[i % kSt], (i / kSt) & 1);
+        if (ok || i < n - 1) mbar_wait(&vfull[i % kSt], (i / kSt) & 1);
+      }
+      if (qn > 0) mbar_wait(qfull, (qn - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kWarpS) {
+    // ---------------------------------------------------------- S^T = K Q^T
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = idesc_bf16(128, N);
+    bool ok = true;
+    int qn = 0;
+    for (int n = 0;; ++n) {
+      ok = mbar_wait_warp(&rfull[n % kRecs], (n / kRecs) & 1);
+      if (!ok) break;
+      const int flags = recs[n % kRecs].flags;
+      if (flags & kEnd) break;
+      const int s = n % kSt, bf = n & 1;
+      if (flags & kFirst) ok = mbar_wait_warp(qfull, (qn++) & 1);
+      ok = ok && mbar_wait_warp(&kfull[s], (n / kSt) & 1) && mbar_wait_warp(&sempty[bf], ((n >> 1) & 1) ^ 1);
+      if (!ok || *abort_s) break;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t da = desc_sw128_kmajor(smem_u32(ks + s * L::kKv)), db = desc_sw128_kmajor(smem_u32(qs));
+#pragma unroll
+        for (int kk = 0; kk < kDim / 16; ++kk) {
+          const uint64_t ao = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+          const uint64_t bo = ((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4;
+          mma_f16(tmem + N * bf, da + ao, db + bo, idesc, kk > 0);
+        }
+        mma_commit(&sfull[bf]);
+        mma_commit(&kempty[s]);
+        if (flags & kLast) mma_commit(qempty);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) fail();
+    if (leader) {
+      mma_commit(&done[0]);
+      if (!mbar_wait(&done[0], 0)) raise_flag(p.status, kFlagTimeout);
+    }
+    __syncwarp();
+  } else if (warp == kWarpO) {
+    // ------------------------------------------------------- O^T += V^T P^T
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = idesc_bf16(128, N) | (1u << 15) | (1u << 16);  // MN-major A and B
+    bool ok = true;
+    int pieces = 0;
+    for (int n = 0;; ++n) {
+      ok = mbar_wait_warp(&rfull[n % kRecs], (n / kRecs) & 1);
+      if (!ok) break;
+      const int flags = recs[n % kRecs].flags;
+      if (flags & kEnd) break;
+      const int s = n % kSt;
+      if (flags & kFirst) ok = mbar_wait_warp(oempty, (pieces++ & 1) ^ 1);
+      ok = ok && mbar_wait_warp(&vfull[s], (n / kSt) & 1) && mbar_wait_warp(pfull, n & 1);
+      if (!ok || *abort_s) break;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t da = desc_mn(smem_u32(vs + s * L::kKv), L::kBlock), db = desc_mn(smem_u32(ps), 16384);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk) {
+          const uint64_t o = (kk * 2048) >> 4;
+          mma_f16(tmem + kColO, da + o, db + o, idesc, !((flags & kFirst) && kk == 0));
+        }
+        mma_commit(&vempty[s]);
+        mma_commit(pempty);
+        if (flags & kLast) mma_commit(ofull);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) fail();
+    if (leader) {
+      mma_commit(&done[1]);
+      if (!mbar_wait(&done[1], 0)) raise_flag(p.status, kFlagTimeout);
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------------- softmax
+    const int key = tid;
+    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    const float cs = p.qk_scale;
+    float l[N];
+#pragma unroll
+    for (int h = 0; h < N; ++h) l[h] = 0.f;
+    int pieces = 0;
+    for (int n = 0;; ++n) {
+      bool ok = mbar_wait_warp(&rfull[n % kRecs], (n / kRecs) & 1);
+      Record rec{};
+      if (ok) rec = recs[n % kRecs];
+      const bool end = (rec.flags & kEnd) != 0;
+      const int bf = n & 1, s = n % kSt;
+      const bool first = (rec.flags & kFirst) != 0;
+      ok = ok && (end || mbar_wait_warp(&sfull[bf], (n >> 1) & 1));
+      uint32_t sv[N];
+      const uint32_t word = key < 64 ? rec.cnt[0] : rec.cnt[1];
+      const bool present = static_cast<uint32_t>(key & 15) < ((word >> (8 * ((key >> 4) & 3))) & 0xFFu);
+      bool over = first;
+      if (ok && !end) {
+        tc_fence_after();
+        const uint32_t ta = tmem + lanes + N * bf;
+        if constexpr (N == 16) {
+          tmem_load(ta, sv);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N / 32; ++i) tmem_load(ta + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * i));
+        }
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[bf]);
+        if (!first && present) {
+#pragma unroll
+          for (int h = 0; h < N; ++h) over |= fmaf(__uint_as_float(sv[h]), cs, -mref_s[h]) > kLazy - kHead;
+        }
+      }
+      if (!ok && lane == 0) fail();
+      // one vote per tile; only when it passes, a second one tells a raise of
+      // the reference from the end or a failure (all four warps leave together)
+      const bool leave = !ok || end || *abort_s;
+      if (barrier_any(2, 128, over || leave)) {
+        if (barrier_any(3, 128, leave)) break;
+        float x[N];
+#pragma unroll
+        for (int h = 0; h < N; ++h) x[h] = present ? __uint_as_float(sv[h]) * cs : -INFINITY;
+        if constexpr (N == 64) {
+          float(&lo)[32] = *reinterpret_cast<float(*)[32]>(x);
+          float(&hi)[32] = *reinterpret_cast<float(*)[32]>(x + 32);
+          red_s[N * warp + lane] = reduce_scatter<true>(lo, lane);
+          red_s[N * warp + 32 + lane] = reduce_scatter<true>(hi, lane);
+        } else {
+          const float m = reduce_scatter<true>(x, lane);
+          if (lane < N) red_s[N * warp + lane] = m;
+        }
+        group_sync();
+        if (tid < N) {
+          const float mo = first ? -INFINITY : mref_s[tid];
+          const float mt = fmaxf(fmaxf(red_s[tid], red_s[N + tid]), fmaxf(red_s[2 * N + tid], red_s[3 * N + tid]));
+          const float mn = fmaxf(mo, mt + kHead);
+          fac_s[tid] = (mo == -INFINITY || mn == -INFINITY) ? 1.f : exp2f(mo - mn);
+          mref_s[tid] = mn;
+        }
+        group_sync();
+        if (!first) {
+          // O^T holds the products up to tile n - 1; scale its columns
+          bool done_o = mbar_wait_warp(pempty, (n & 1) ^ 1);
+          if (!done_o && lane == 0) fail();
+          tc_fence_after();
+          if (done_o && warp < kDim / 32) {
+#pragma unroll
+            for (int i = 0; i < N / 16; ++i) {
+              uint32_t o[16];
+              tmem_load(tmem + lanes + kColO + 16 * i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * fac_s[16 * i + q]);
+              tmem_store(tmem + lanes + kColO + 16 * i, o);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+#pragma unroll
+          for (int h = 0; h < N; ++h) l[h] *= fac_s[h];
+        }
+      }
+      // P^T buffer free: the previous tile's product is done
+      if (!mbar_wait_warp(pempty, (n & 1) ^ 1) && lane == 0) fail();
+#pragma unroll
+      for (int ch = 0; ch < N / 8; ++ch) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int h = 8 * ch + 2 * q;
+          const float2 m2 = *reinterpret_cast<const float2 *>(&mref_s[h]);
+          const float pa = present ? exp2_hw(fmaf(__uint_as_float(sv[h]), cs, -m2.x)) : 0.f;
+          const float pb = present ? exp2_hw(fmaf(__uint_as_float(sv[h + 1]), cs, -m2.y)) : 0.f;
+          l[h] += pa;
+          l[h + 1] += pb;
+          w[q] = pack_bf16x2(pa, pb);
+        }
+        *reinterpret_cast<uint4 *>(ps + sw128_offset(key, 16u * ch)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (rec.flags & kMasked) {
+        // positions past the token's own may hold anything: their V rows
+        // become zeros before the product reads them
+        if (!mbar_wait_warp(&vfull[s], (n / kSt) & 1) && lane == 0) fail();
+        if (!present) {
+#pragma unroll
+          for (int i = 0; i < kB; ++i)
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+              *reinterpret_cast<uint4 *>(vs + s * L::kKv + i * L::kBlock + key * 128 + 16 * ch) =
+                  make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull);
+      if (rec.flags & kLast) {
+        if (!mbar_wait_warp(ofull, pieces & 1) && lane == 0) fail();
+        ++pieces;
+        tc_fence_after();
+        if constexpr (N == 64) {
+          float(&lo)[32] = *reinterpret_cast<float(*)[32]>(l);
+          float(&hi)[32] = *reinterpret_cast<float(*)[32]>(l + 32);
+          red_s[N * warp + lane] = reduce_scatter<false>(lo, lane);
+          red_s[N * warp + 32 + lane] = reduce_scatter<false>(hi, lane);
+        } else {
+          const float v = reduce_scatter<false>(l, lane);
+          if (lane < N) red_s[N * warp + lane] = v;
+        }
+#pragma unroll
+        for (int h = 0; h < N; ++h) l[h] = 0.f;
+        group_sync();
+        if (tid < N) {
+          const float sum = (red_s[tid] + red_s[N + tid]) + (red_s[2 * N + tid] + red_s[3 * N + tid]);
+          fac_s[tid] = sum > 0.f ? 1.f / sum : 0.f;
+          if (!(rec.flags & kDirect))
+            p.ml[static_cast<int64_t>(rec.slot) * N + tid] = make_float2(mref_s[tid], sum);
+        }
+        group_sync();
+        if (warp < kDim / 32) {
+          const int d = 32 * warp + lane;
+#pragma unroll
+          for (int i = 0; i < N / 16; ++i) {
+            uint32_t o[16];
+            tmem_load(tmem + lanes + kColO + 16 * i, o);
+            tmem_ld_wait();
+            if (rec.flags & kDirect) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                if (16 * i + q < rec.heads)
+                  p.out[(static_cast<int64_t>(rec.row) + 16 * i + q) * kDim + d] =
+                      __float2bfloat16_rn(__uint_as_float(o[q]) * fac_s[16 * i + q]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                if (16 * i + q < rec.heads)
+                  p.part[(static_cast<int64_t>(rec.slot) * N + 16 * i + q) * kDim + d] = __uint_as_float(o[q]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(oempty);
+      }
+    }
+  }
+  // parts of a whole-sequence call are merged by a kernel that also needs the
+  // one before this: completing after it makes the chain transitive
+  if (p.keep) pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpS) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// Merges the parts of the unit that CTA c's range cuts: o = sum 2^(m_i - M) o_i
+// / sum 2^(m_i - M) l_i.  One warp per head, parts in order.
+template <int N, int kDim>
+__global__ void __launch_bounds__(256)
+merge_cut_kernel(const ListParams p) {
+  pdl_wait();
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int2 cut = p.cut[c];
+  if (cut.x < 0) return;
+  const int upt = p.pv.H_kv * p.gb, t = cut.x / upt, sub = cut.x % upt;
+  const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64, heads = min(64, (hk + 1) * p.group - h0);
+  constexpr int V = kDim / 32;  // values per lane
+  for (int i = blockIdx.y * 8 + warp; i < heads; i += 8 * gridDim.y) {
+    float M = -INFINITY;
+    for (int k = c; k <= cut.y; ++k) M = fmaxf(M, p.ml[static_cast<int64_t>(k == c ? 2 * c + 1 : 2 * k) * N + i].x);
+    float acc[V] = {}, l = 0.f;
+    for (int k = c; k <= cut.y; ++k) {
+      const int64_t at = static_cast<int64_t>(k == c ? 2 * c + 1 : 2 * k) * N + i;
+      const float2 ml = p.ml[at];
+      const float a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      l += a * ml.y;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(a, p.part[at * kDim + V * lane + e], acc[e]);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      p.out[(static_cast<int64_t>(t) * p.pv.H + h0 + i) * kDim + V * lane + e] = __float2bfloat16_rn(acc[e] * inv);
+  }
+}
+
+template <int N, int kDim>
+cudaError_t launch_list(const sa_paged_args &pa, const void *q, ListParams &p, int grid, bool pdl,
+                        cudaStream_t stream) {
+  using L = ListSmem<N, kDim>;
+  CUtensorMap qmap, kmap, vmap;
+  const uint64_t rows = static_cast<uint64_t>(pa.n_pages) * pa.H_kv * pa.P;
+  if (!encode_rows(&qmap, q, static_cast<uint64_t>(pa.T) * pa.H, kDim, N) ||
+      !encode_rows(&kmap, pa.K, rows, kDim, pa.P) || !encode_rows(&vmap, pa.V, rows, kDim, pa.P))
+    return cudaErrorInvalidValue;
+  auto kern = page_list_kernel<N, kDim>;
+  const size_t smem = L::total + 1024;
+  static bool attr_done[64] = {};
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, attr_done);
+  if (e != cudaSuccess) return e;
+  e = launch_ex(pdl, kern, dim3(grid), dim3(kThreads), smem, stream, 1, qmap, kmap, vmap, p);
+  if (e != cudaSuccess || p.keep) return e;
+  return launch_ex(true, merge_cut_kernel<N, kDim>, dim3(grid, N / 16), dim3(256), 0, stream, 1, p);
+}
+
+template <int kDim>
+cudaError_t launch_dim(const sa_paged_args &pa, const void *q, ListParams &p, int grid, bool pdl, cudaStream_t stream) {
+  switch (list_cols(pa)) {
+    case 16: return launch_list<16, kDim>(pa, q, p, grid, pdl, stream);
+    case 32: return launch_list<32, kDim>(pa, q, p, grid, pdl, stream);
+    default: return launch_list<64, kDim>(pa, q, p, grid, pdl, stream);
+  }
+}
+
+size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+bool encode_rows(CUtensorMap *m, const void *base, uint64_t rows, int dim, uint32_t box_rows) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(dim), rows};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(dim) * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int list_cols(const sa_paged_args &pa) {
+  const int g = pa.H / pa.H_kv;
+  return g <= 16 ? 16 : g <= 32 ? 32 : 64;
+}
+
+size_t list_scratch(const sa_paged_args &pa, bool keep) {
+  const int g = pa.H / pa.H_kv;
+  const size_t units = static_cast<size_t>(pa.T) * pa.H_kv * ((g + 63) / 64);
+  const size_t slots = keep ? units + kMaxCtas : 2 * kMaxCtas;
+  return round_up(slots * list_cols(pa) * pa.D * sizeof(float)) + round_up(slots * list_cols(pa) * sizeof(float2)) +
+         round_up((keep ? units : kMaxCtas) * sizeof(int2));
+}
+
+cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams &p, void *out, void *scratch,
+                             uint32_t *status, bool pdl, cudaStream_t stream) {
+  p.pv = paged_view(pa);
+  p.group = pa.H / pa.H_kv;
+  p.gb = (p.group + 63) / 64;
+  p.qk_scale = pa.scale * kLog2e;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.status = status;
+  const size_t units = static_cast<size_t>(pa.T) * pa.H_kv * p.gb;
+  const size_t slots = p.keep ? units + kMaxCtas : 2 * kMaxCtas;
+  char *w = static_cast<char *>(scratch);
+  p.part = reinterpret_cast<float *>(w);
+  w += round_up(slots * list_cols(pa) * pa.D * sizeof(float));
+  p.ml = reinterpret_cast<float2 *>(w);
+  w += round_up(slots * list_cols(pa) * sizeof(float2));
+  p.info = p.cut = reinterpret_cast<int2 *>(w);
+  int grid = std::min(sm_count(), kMaxCtas);
+  if (!p.whole) {
+    const int spt = kTile / pa.P;
+    const int64_t entries = static_cast<int64_t>(p.K) + std::min(p.local, pa.max_pages);
+    p.tpu = static_cast<int>(std::max<int64_t>(1, (entries + spt - 1) / spt));
+    grid = static_cast<int>(std::min<int64_t>(grid, static_cast<int64_t>(units) * p.tpu));
+  }
+  return pa.D == 128 ? launch_dim<128>(pa, q, p, grid, pdl, stream) : launch_dim<64>(pa, q, p, grid, pdl, stream);
+}
+
+size_t block_attn_scratch(const sa_paged_args &pa, int, int) { return list_scratch(pa, false); }
+
+cudaError_t launch_block_attn(const sa_paged_args &pa, const void *q, const int32_t *idx, int K, int local, void *out,
+                              void *scratch, uint32_t *status, cudaStream_t stream) {
+  if (pa.T == 0) return cudaSuccess;
+  ListParams p{};
+  p.idx = idx;
+  p.K = K;
+  p.local = local;
+  return launch_page_list(pa, q, p, out, scratch, status, false, stream);
+}
+
+}  // namespace sa

@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "paged.cuh"
 
 namespace {
 
