@@ -118,7 +118,10 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   int *start_t = reinterpret_cast<int *>(smem + L::misc + 32);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = gridDim.x, c = blockIdx.x;
+  const int c = blockIdx.x;
+  // CTAs that share the tiles out: no more than there are tiles, so that every
+  // CTA between a unit's first and last holds a piece of it
+  auto shares = [&](long long tiles) { return static_cast<int>(min(static_cast<long long>(gridDim.x), max(tiles, 1ll))); };
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < kSt; ++i) {
@@ -176,7 +179,8 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       if (i < tid) before += sums[i];
       total += sums[i];
     }
-    const long long x0 = total * upt * c / G;
+    const int g = shares(total * upt);
+    const long long x0 = total * upt * min(c, g) / g;
     if (tid == 0) start_s[0] = total * upt;
     if (before * upt <= x0 && x0 < (before + own) * upt) {
       int t = ta;
@@ -197,7 +201,8 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
   const long long tot = start_s[0];
-  const long long x_begin = tot * c / G, x_end = tot * (c + 1) / G;
+  const int G = shares(tot);
+  const long long x_begin = tot * min(c, G) / G, x_end = tot * min(c + 1, G) / G;
   auto fail = [&]() {
     raise_flag(p.status, kFlagTimeout);
     *abort_s = 1;

@@ -1,0 +1,551 @@
+// Attention of a batch whose sequences share their first pages, on the 5th-
+// generation tensor cores.
+//
+// The shared keys are met by every query row of the batch (T tokens x G heads
+// per KV head), so that part is two dense products with a softmax between them
+// and bound by the tensor pipe once there are a few hundred rows (4 D flops a
+// row and key against 4 D / rows bytes); with few rows it streams the shared
+// pages once and HBM is the bound.  The rows sit in the accumulator's lanes:
+//   S = Q K^T   M = 128 rows, N = 128 keys, K = D; a thread owns a row, so the
+//               running maximum and sum need no exchange between threads
+//   P           bf16, written over S in tensor memory (the A operand of P V)
+//   O += P V    M = 128 rows, N = D, K = 128 keys, V read MN-major as it landed
+// A CTA holds two row tiles (A, B: 256 rows) against the same K and V tiles,
+// each with its own softmax warpgroup and its own issuing warp, so one tile's
+// products run while the other's weights are computed.  One pass per tile: the
+// weights are taken against a reference set by the piece's first tile and kept
+// in registers until a vote has shown that no logit passes it by 2^8; then they
+// are stored (else S, still in tensor memory, is read again against the raised
+// reference and O is rescaled).  Weights are rounded to bf16 for the product,
+// logits, statistics and O are fp32.
+//
+// Work: (KV head, 256 rows) items x key tiles form one list cut evenly over one
+// CTA per SM.  Every piece leaves (reference, sum) and O per row in scratch.
+// The positions past the shared pages, each sequence's own, are a page-list
+// call (paged_attn_list.cu) that starts as SMs fall free, and a last kernel
+// merges a row's pieces of both.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "paged_list.h"
+#include "paged_umma.cuh"
+
+namespace sa {
+namespace {
+
+using namespace umma;
+
+constexpr int kTile = 128;      // keys per tile, rows per row tile
+constexpr int kRows = 256;      // rows per item
+constexpr int kThreads = 384;
+constexpr int kWarpMma = 8;     // and 9: the issuers of row tiles A and B
+constexpr int kWarpLoad = 10;   // (warp 11 only joins the block barriers)
+constexpr int kSlots = 5;       // ring of K and V tiles: K(0), V(0), K(1), ...
+constexpr int kMasks = 8;
+constexpr float kLazy = 8.f, kHead = 20.f;  // as in paged_attn_list.cu
+
+struct PrefixParams {
+  PagedView pv;
+  int pages;                  // shared pages
+  int group;
+  int64_t rows;               // T * group
+  int npairs, nkt;            // items per KV head, key tiles per item
+  const uint16_t *q;
+  float *part;                // [piece][kRows][D]
+  float2 *ml;                 // [piece][kRows]
+  float qk_scale;
+  uint32_t *status;
+};
+
+template <int kDim>
+struct PrefixSmem {
+  static constexpr uint32_t kBlock = kTile * 128;
+  static constexpr uint32_t kKv = kBlock * (kDim / 64);
+  static constexpr size_t q = 0;                           // [row tile][D / 64][128 rows][128 B]
+  static constexpr size_t kv = q + 2 * kKv;
+  static constexpr size_t masks = kv + kSlots * kKv;       // [kMasks] u32: bit g = keys 16 g .. + 15 exist
+  static constexpr size_t bars = masks + kMasks * 4;
+  static constexpr int kBars = 2 * kSlots + 8 + kMasks + 2;
+  static constexpr size_t misc = bars + kBars * 8;
+  static constexpr size_t total = misc + 16;
+  static_assert(total + 1024 <= 232448, "shared memory budget");
+};
+
+// Walk over a CTA's tiles: item, key tile within it, and whether the tile is the
+// first or last of this CTA's piece of the item.
+struct Walk {
+  int64_t left;  // tiles after this one
+  int item, kt, nkt;
+  bool first;
+  __device__ Walk(int64_t x0, int64_t x1, int nkt_) : left(x1 - x0 - 1), nkt(nkt_), first(true) {
+    item = static_cast<int>(x0 / nkt);
+    kt = static_cast<int>(x0 - static_cast<int64_t>(item) * nkt);
+  }
+  __device__ bool on() const { return left >= 0; }
+  __device__ bool last() const { return left == 0 || kt + 1 == nkt; }
+  __device__ void next() {
+    --left;
+    first = ++kt == nkt;
+    if (first) {
+      kt = 0;
+      ++item;
+    }
+  }
+};
+
+// The CTA whose range of the tile list [tot c / G, tot (c + 1) / G) holds tile y.
+__host__ __device__ inline int cta_of(int64_t y, int64_t tot, int G) { return static_cast<int>(((y + 1) * G - 1) / tot); }
+
+template <int kDim>
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+              const PrefixParams p) {
+  using L = PrefixSmem<kDim>;
+  constexpr int kB = kDim / 64;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *qs = smem + L::q, *kvs = smem + L::kv;
+  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::masks);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
+  uint64_t *full = bars, *empty = full + kSlots;
+  uint64_t *qfull = empty + kSlots, *sfull = qfull + 2, *pfull = sfull + 2, *ofull = pfull + 2;
+  uint64_t *mfull = ofull + 2, *done = mfull + kMasks;
+  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
+  volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 8);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = gridDim.x, c = blockIdx.x;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 4);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+      mbar_init(&ofull[i], 1);
+      mbar_init(&done[i], 1);
+    }
+    for (int i = 0; i < kMasks; ++i) mbar_init(&mfull[i], 1);
+    *abort_s = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(tmem_base_s, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_s;
+  const int64_t tot = static_cast<int64_t>(p.pv.H_kv) * p.npairs * p.nkt;
+  const int64_t x0 = tot * c / G, x1 = tot * (c + 1) / G;
+  auto fail = [&]() {
+    raise_flag(p.status, kFlagTimeout);
+    *abort_s = 1;
+  };
+
+  if (warp == kWarpLoad) {
+    // ------------------------------------------------------------------ loader
+    if (lane == 0) {
+      prefetch_tmap(&kmap);
+      prefetch_tmap(&vmap);
+    }
+    const int spt = kTile >> p.pv.logP;
+    const uint32_t rows_total = static_cast<uint32_t>(p.pv.n_pages) * p.pv.H_kv * p.pv.P;
+    const int q = lane / kB, kb = lane % kB;  // this lane's copy: page slot q of the tile, 64-dim block kb
+    auto page_of = [&](int kt) -> int {
+      const int j = kt * spt + q;
+      return q < spt && j < p.pages ? load_page(p.pv, 0, j, p.status, true) : -1;
+    };
+    bool ok = true;
+    int n = 0, issued = 0;
+    Walk at(x0, x1, p.nkt);
+    int next = at.on() ? page_of(at.kt) : -1;
+    for (; at.on() && ok; at.next(), ++n) {
+      const int page = next;
+      if (at.left > 0) next = page_of(at.kt + 1 == p.nkt ? 0 : at.kt + 1);
+      const int hk = at.item / p.npairs;
+      // a slot without a page reads past the tensor's end: the copy fills zeros
+      const uint32_t y = page >= 0 ? (static_cast<uint32_t>(page) * p.pv.H_kv + hk) * p.pv.P : rows_total;
+      // mask: P / 16 bits per page slot
+      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0 && kb == 0);
+      uint32_t mask = 0;
+      for (int g = 0; g < 8; ++g) mask |= ((have >> (((16 * g) >> p.pv.logP) * kB)) & 1u) << g;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int m = 2 * n + kv, s = m % kSlots;
+        if (!mbar_wait_warp(&empty[s], ((m / kSlots) & 1) ^ 1) || *abort_s) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          if (kv == 0) {
+            masks[n % kMasks] = mask;
+            mbar_arrive(&mfull[n % kMasks]);
+          }
+          mbar_expect_tx(&full[s], L::kKv);
+        }
+        __syncwarp();
+        ++issued;
+        if (q < spt)
+          tma_load_2d(kvs + s * L::kKv + kb * L::kBlock + q * p.pv.P * 128, kv ? &vmap : &kmap, &full[s], 64 * kb,
+                      static_cast<int>(y));
+      }
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      if (!ok) fail();
+      // every copy lands before the CTA exits
+      for (int m = max(0, issued - kSlots); m < issued; ++m) mbar_wait(&full[m % kSlots], (m / kSlots) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // ------------------------------------------------- issuer of one row tile
+    const int w = warp - kWarpMma;
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_s = idesc_bf16(128, kTile);
+    constexpr uint32_t idesc_o = idesc_bf16(128, kDim) | (1u << 16);  // V is MN-major
+    const uint32_t ts = tmem + 128 * w, to = tmem + 256 + 128 * w;
+    bool ok = true;
+    int qn = 0, n = 0, ln = 0;  // pieces, tiles of the ring, tiles of this row tile
+    bool live = false;
+    for (Walk at(x0, x1, p.nkt); at.on(); at.next(), ++n) {
+      const bool first = at.first, last = at.last();
+      // a row tile without rows only frees the ring
+      if (first) live = static_cast<int64_t>(at.item % p.npairs) * kRows + 128 * w < p.rows;
+      const int mk = 2 * n, mv = 2 * n + 1;
+      if (live && first) ok = mbar_wait_warp(&qfull[w], (qn++) & 1);
+      ok = ok && mbar_wait_warp(&full[mk % kSlots], (mk / kSlots) & 1);
+      if (!ok || *abort_s) break;
+      if (!live) {
+        if (leader) mbar_arrive(&empty[mk % kSlots]);
+        ok = mbar_wait_warp(&full[mv % kSlots], (mv / kSlots) & 1);
+        if (!ok) break;
+        if (leader) mbar_arrive(&empty[mv % kSlots]);
+        __syncwarp();
+        continue;
+      }
+      tc_fence_after();
+      if (leader) {
+        const uint64_t da = desc_sw128_kmajor(smem_u32(qs + w * L::kKv));
+        const uint64_t db = desc_sw128_kmajor(smem_u32(kvs + (mk % kSlots) * L::kKv));
+#pragma unroll
+        for (int kk = 0; kk < kDim / 16; ++kk) {
+          const uint64_t o = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+          mma_f16(ts, da + o, db + o, idesc_s, kk > 0);
+        }
+        mma_commit(&sfull[w]);
+        mma_commit(&empty[mk % kSlots]);
+      }
+      __syncwarp();
+      ok = mbar_wait_warp(&full[mv % kSlots], (mv / kSlots) & 1) && mbar_wait_warp(&pfull[w], ln & 1);
+      if (!ok || *abort_s) break;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t db = desc_mn(smem_u32(kvs + (mv % kSlots) * L::kKv), L::kBlock);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_f16_tmem_a(to, ts + 8 * kk, db + ((kk * 2048) >> 4), idesc_o, !(first && kk == 0));
+        mma_commit(&empty[mv % kSlots]);
+        if (last) mma_commit(&ofull[w]);
+      }
+      __syncwarp();
+      ++ln;
+    }
+    if (!ok && lane == 0) fail();
+    if (leader) {
+      mma_commit(&done[w]);
+      if (!mbar_wait(&done[w], 0)) raise_flag(p.status, kFlagTimeout);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------ softmax of one row tile
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
+    const float cs = p.qk_scale;
+    const float2 cs2 = make_float2(cs, cs);
+    uint8_t *qt = qs + w * L::kKv;
+    float ref = -INFINITY, l = 0.f;
+    int n = 0, ln = 0, pieces = 0;
+    bool ok = true;
+    int64_t r = 0;
+    for (Walk at(x0, x1, p.nkt); at.on(); at.next(), ++n) {
+      const bool first = at.first, last = at.last();
+      if (first) r = static_cast<int64_t>(at.item % p.npairs) * kRows + 128 * w + row;
+      if (r - row >= p.rows) continue;
+      if (first) {
+        // this thread's query row, into the K-major swizzled layout (every
+        // product of the piece before has been read out)
+        const int hk = at.item / p.npairs;
+        const bool in = r < p.rows;
+        const int64_t t = r / p.group;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + (t * p.pv.H + static_cast<int64_t>(hk) * p.group + (r - t * p.group)) * kDim);
+        uint4 v[kDim / 8];
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) v[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i)
+          *reinterpret_cast<uint4 *>(qt + (i >> 3) * L::kBlock + sw128_offset(row, 16u * (i & 7))) = v[i];
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[w]);
+        l = 0.f;
+      }
+      ok = mbar_wait_warp(&mfull[n % kMasks], (n / kMasks) & 1) && mbar_wait_warp(&sfull[w], ln & 1);
+      if (!ok || *abort_s) break;
+      const uint32_t mask = masks[n % kMasks];
+      tc_fence_after();
+      // the row's largest scaled logit of the tile
+      auto tile_max = [&]() -> float {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t s[32];
+          tmem_load(ts + 32 * i, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if ((mask >> (2 * i + (e >> 4))) & 1u) m = fmaxf(m, __uint_as_float(s[e]) * cs);
+        }
+        return m;
+      };
+      // (finite even when the tile has no key: the next tile then raises it)
+      if (first) ref = fmaxf(tile_max() + kHead, -1e30f);
+      uint32_t pk[64];
+      float2 sum;
+      while (true) {
+        sum = make_float2(0.f, 0.f);
+        float top = -INFINITY;
+        const float2 nref2 = make_float2(-ref, -ref);
+        uint32_t s[2][32];
+        tmem_load(ts, s[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          tmem_ld_wait();
+          if (i < 3) tmem_load(ts + 32 * (i + 1), s[(i + 1) & 1]);
+          uint32_t(&c)[32] = s[i & 1];
+          if (mask != 0xFFu) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((mask >> (2 * i + (e >> 4))) & 1u)) c[e] = cs > 0.f ? 0xFF800000u : 0x7F800000u;  // cs s = -inf
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 v =
+                fma2(make_float2(__uint_as_float(c[2 * e]), __uint_as_float(c[2 * e + 1])), cs2, nref2);
+            top = max3(top, v.x, v.y);
+            const float2 w2 = make_float2(exp2_hw(v.x), exp2_hw(v.y));
+            sum = add2(sum, w2);
+            pk[16 * i + e] = pack_bf16x2(w2.x, w2.y);
+          }
+        }
+        if (!__any_sync(0xffffffffu, top > kLazy - kHead)) break;
+        // a logit passes its row's reference by the lazy margin: raise it, scale
+        // O (which holds the products up to the tile before) and the sum, and
+        // take the weights again
+        float fac = 1.f;
+        const float m = tile_max();
+        if (m + kHead > ref) {
+          fac = exp2f(ref - (m + kHead));
+          ref = m + kHead;
+        }
+        l *= fac;
+        if (!first) {
+#pragma unroll 1
+          for (int i = 0; i < kDim / 32; ++i) {
+            uint32_t o[32];
+            tmem_load(to + 32 * i, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
+            tmem_store(to + 32 * i, o);
+            tmem_store(to + 32 * i + 16, o + 16);
+          }
+          tmem_wait_st();
+        }
+      }
+      l += sum.x + sum.y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_store(ts + 16 * i, pk + 16 * i);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[w]);
+      ++ln;
+      if (last) {
+        ok = mbar_wait_warp(&ofull[w], pieces & 1);
+        if (!ok) break;
+        ++pieces;
+        tc_fence_after();
+        const int64_t to_row = static_cast<int64_t>(at.item + c) * kRows + 128 * w + row;
+        if (r < p.rows) p.ml[to_row] = make_float2(ref, l);
+#pragma unroll 1
+        for (int i = 0; i < kDim / 32; ++i) {
+          uint32_t o[32];
+          tmem_load(to + 32 * i, o);
+          tmem_ld_wait();
+          if (r < p.rows) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4 *>(p.part + to_row * kDim + 32 * i + 4 * e) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        tc_fence_before();
+      }
+    }
+    if (!ok && lane == 0) fail();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Output rows: the pieces of the shared part (of the row's item) and of the
+// token's own pages, o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  One warp
+// per row; the pieces in order.
+template <int kDim>
+__global__ void __launch_bounds__(256)
+merge_rows_kernel(const PrefixParams p, const ListParams own, int cols, int grid_shared) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (id >= static_cast<int64_t>(p.pv.T) * p.pv.H) return;
+  const int t = static_cast<int>(id / p.pv.H), h = static_cast<int>(id % p.pv.H);
+  int b, pos;
+  if (!load_paged_token(p.pv, t, nullptr, false, b, pos) || pos < p.pages * p.pv.P) return;
+  const int hk = h / p.group, g = h % p.group;
+  const int64_t r = static_cast<int64_t>(t) * p.group + g;
+  const int64_t tot = static_cast<int64_t>(p.pv.H_kv) * p.npairs * p.nkt;
+  const int64_t item = static_cast<int64_t>(hk) * p.npairs + r / kRows;
+  const int a0 = cta_of(item * p.nkt, tot, grid_shared), a1 = cta_of((item + 1) * p.nkt - 1, tot, grid_shared);
+  const int64_t u = (static_cast<int64_t>(t) * p.pv.H_kv + hk) * own.gb + g / 64;
+  const int2 rng = own.info[u];
+  const int na = a1 - a0 + 1, total = na + rng.y - rng.x + 1;
+  constexpr int V = kDim / 32;
+  float M = -INFINITY;
+  auto locate = [&](int k, const float2 *&ml, const float *&o) {
+    if (k < na) {
+      const int64_t at = (item + a0 + k) * kRows + r % kRows;
+      ml = p.ml + at;
+      o = p.part + at * kDim;
+    } else {
+      const int64_t at = (u + rng.x + (k - na)) * cols + g % 64;
+      ml = own.ml + at;
+      o = own.part + at * kDim;
+    }
+  };
+  for (int k = lane; k < total; k += 32) {
+    const float2 *ml;
+    const float *o;
+    locate(k, ml, o);
+    M = fmaxf(M, ml->x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[V] = {}, l = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < total; ++k) {
+    const float2 *mlp;
+    const float *o;
+    locate(k, mlp, o);
+    const float2 ml = *mlp;
+    const float a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    l = fmaf(a, ml.y, l);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = fmaf(a, o[V * lane + e], acc[e]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) own.out[id * kDim + V * lane + e] = __float2bfloat16_rn(acc[e] * inv);
+}
+
+size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+struct Shape {
+  int64_t rows, items;
+  int npairs, nkt, spt;
+  size_t slots;
+};
+Shape shape_of(const sa_paged_args &pa, int pages) {
+  Shape s{};
+  s.spt = kTile / pa.P;
+  s.rows = static_cast<int64_t>(pa.T) * (pa.H / pa.H_kv);
+  s.npairs = static_cast<int>((s.rows + kRows - 1) / kRows);
+  s.nkt = (pages + s.spt - 1) / s.spt;
+  s.items = static_cast<int64_t>(pa.H_kv) * s.npairs;
+  s.slots = static_cast<size_t>(s.items) + kMaxCtas;
+  return s;
+}
+
+template <int kDim>
+cudaError_t launch_shared(const sa_paged_args &pa, const PrefixParams &p, int grid, cudaStream_t stream) {
+  CUtensorMap kmap, vmap;
+  const uint64_t rows = static_cast<uint64_t>(pa.n_pages) * pa.H_kv * pa.P;
+  if (!encode_rows(&kmap, pa.K, rows, kDim, pa.P) || !encode_rows(&vmap, pa.V, rows, kDim, pa.P))
+    return cudaErrorInvalidValue;
+  auto kern = prefix_kernel<kDim>;
+  const size_t smem = PrefixSmem<kDim>::total + 1024;
+  static bool attr_done[64] = {};
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, attr_done);
+  if (e != cudaSuccess) return e;
+  return launch_ex(false, kern, dim3(grid), dim3(kThreads), smem, stream, 1, kmap, vmap, p);
+}
+
+}  // namespace
+
+size_t prefix_attn_scratch(const sa_paged_args &pa, int shared_pages) {
+  if (shared_pages == 0) return list_scratch(pa, false);
+  const Shape s = shape_of(pa, shared_pages);
+  return list_scratch(pa, true) + round_up(s.slots * kRows * pa.D * sizeof(float)) +
+         round_up(s.slots * kRows * sizeof(float2));
+}
+
+cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int shared_pages, void *out, void *scratch,
+                               uint32_t *status, cudaStream_t stream) {
+  if (pa.T == 0) return cudaSuccess;
+  ListParams own{};
+  own.whole = 1;
+  own.first_page = shared_pages;
+  if (shared_pages == 0) return launch_page_list(pa, q, own, out, scratch, status, false, stream);
+  own.keep = 1;
+  const Shape s = shape_of(pa, shared_pages);
+  PrefixParams p{};
+  p.pv = paged_view(pa);
+  p.pages = shared_pages;
+  p.group = pa.H / pa.H_kv;
+  p.rows = s.rows;
+  p.npairs = s.npairs;
+  p.nkt = s.nkt;
+  p.q = static_cast<const uint16_t *>(q);
+  char *w = static_cast<char *>(scratch) + list_scratch(pa, true);
+  p.part = reinterpret_cast<float *>(w);
+  p.ml = reinterpret_cast<float2 *>(w + round_up(s.slots * kRows * pa.D * sizeof(float)));
+  // masked keys become infinite logits of the sign that the scale turns to
+  // -inf, so a scale of 0 is taken as one too small to tell
+  p.qk_scale = pa.scale == 0.f ? 1e-37f : pa.scale * kLog2e;
+  p.status = status;
+  const int grid = static_cast<int>(std::min<int64_t>(std::min(sm_count(), kMaxCtas), s.items * s.nkt));
+  cudaError_t e = pa.D == 128 ? launch_shared<128>(pa, p, grid, stream) : launch_shared<64>(pa, p, grid, stream);
+  if (e != cudaSuccess) return e;
+  e = launch_page_list(pa, q, own, out, scratch, status, true, stream);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(pa.T) * pa.H;
+  const dim3 blocks(static_cast<unsigned>((rows + 7) / 8));
+  return pa.D == 128
+             ? launch_ex(true, merge_rows_kernel<128>, blocks, dim3(256), 0, stream, 1, p, own, list_cols(pa), grid)
+             : launch_ex(true, merge_rows_kernel<64>, blocks, dim3(256), 0, stream, 1, p, own, list_cols(pa), grid);
+}
+
+}  // namespace sa
