@@ -7,8 +7,9 @@
 // the keys in the 128 lanes of the accumulator and the heads in its columns,
 // and no row of the tensor core is spent on padding:
 //   S^T = K Q^T     M = 128 keys, N = heads (16, 32 or 64), K = D
-//   P^T             one thread per key: p = 2^(c s - m_ref[h]), bf16, to shared
-//                   memory with the heads contiguous (the MN-major B operand)
+//   P^T             two threads per key, each half of the heads: p = 2^(c s -
+//                   m_ref[h]), bf16, to shared memory with the heads contiguous
+//                   (the MN-major B operand)
 //   O^T += V^T P^T  M = D, N = heads, K = 128 keys
 // The pages land by TMA in the 128-byte swizzle, which is K-major for the
 // first product and MN-major for the second, so K and V are copied once and
@@ -26,8 +27,9 @@
 // own are masked, and the V rows they hold are zeroed in shared memory, since
 // 0 x NaN would reach the sum.
 //
-// Warps: 0-3 softmax and output; 4 issues S^T, 5 issues O^T; 6 resolves the
-// lists and issues the copies, publishing one record per tile.  Every wait is
+// Warps: 0-7 softmax and output; 8 issues S^T, 9 issues O^T; 10 and 11 resolve
+// the lists and issue the copies of K and V, warp 10 publishing one record per
+// tile.  Every wait is
 // bounded; on expiry the kernel flags the status word, drains its copies and
 // products and returns.
 #include <cudaTypedefs.h>
@@ -45,9 +47,10 @@ namespace {
 using namespace umma;
 
 constexpr int kTile = 128;      // keys per tile
-constexpr int kThreads = 224;
-constexpr int kWarpS = 4, kWarpO = 5, kWarpLoad = 6;
-constexpr int kRecs = 8;        // tile records; the loader runs fewer tiles ahead
+constexpr int kThreads = 384;
+constexpr int kSoftmax = 256;   // threads of the softmax warps, 0-7
+constexpr int kWarpS = 8, kWarpO = 9, kWarpK = 10;  // and 11
+constexpr int kQueue = 40;      // page entries a loader holds: under a tile's and one batch of 32
 // The reference a weight is taken against lies kHead above the maximum that
 // set it (log2 units), and is raised once a logit passes that maximum by kLazy:
 // unnormalised sums of weights up to 2^(kLazy - kHead) times any bf16 values
@@ -56,9 +59,8 @@ constexpr float kLazy = 8.f, kHead = 20.f;
 enum : int { kFirst = 1, kLast = 2, kEnd = 4, kMasked = 8, kDirect = 16 };
 
 struct Record {
-  int flags;
+  int flags;     // bits 0-7; the unit's heads from bit 8
   int row;       // first output row of the unit (t * H + head)
-  int heads;     // heads of the unit
   int slot;      // part slot of the piece
   uint32_t cnt[2];  // byte g: keys present among keys 16 g .. 16 g + 15
 };
@@ -66,6 +68,13 @@ struct Record {
 template <int N, int kDim>
 struct ListSmem {
   static constexpr int kStages = kDim == 128 ? 3 : 6;
+  // P^T buffers: with up to 32 heads a second one takes the upper half of the
+  // 128-byte rows
+  static constexpr int kPBufs = N <= 32 ? 2 : 1;
+  // Tile records.  Record n + kStages + 5 is written once S(n + 5) is done,
+  // for which the weights of tile n + 2 were written and so, with two P^T
+  // buffers at most, O(n) issued: every reader is past record n.
+  static constexpr int kRecs = kStages + 5;
   static constexpr uint32_t kBlock = kTile * 128;          // one 64-dim block of a tile
   static constexpr uint32_t kKv = kBlock * (kDim / 64);
   static constexpr size_t k = 0;
@@ -73,27 +82,28 @@ struct ListSmem {
   static constexpr size_t p = v + kStages * kKv;           // [128 keys][64 heads] bf16
   static constexpr size_t q = p + 16384;                   // [D / 64][N][128 B]
   static constexpr size_t recs = q + N * kDim * 2;
-  static constexpr size_t red = recs + kRecs * sizeof(Record);   // [4][N]
+  static constexpr size_t red = (recs + kRecs * sizeof(Record) + 15) & ~size_t(15);   // [4][N]
   static constexpr size_t fac = red;                       // [N], over the reduction's first row (see below)
   static constexpr size_t mref = red + 4 * N * 4;          // [N]
-  static constexpr size_t queue = mref + N * 4;             // [48] page entries waiting for a tile
-  static constexpr size_t bars = (queue + 48 * 4 + 7) & ~size_t(7);
-  static constexpr int kBars = 4 * kStages + 2 + 4 + 2 + 2 + kRecs + 2;
+  static constexpr size_t queue = mref + N * 4;            // [2][kQueue] page entries waiting for a tile
+  static constexpr size_t bars = (queue + 2 * kQueue * 4 + 7) & ~size_t(7);
+  static constexpr int kBars = 4 * kStages + 2 + 4 + 2 * kPBufs + 2 + kRecs + 2;
   static constexpr size_t misc = bars + kBars * 8;
-  static constexpr size_t total = misc + 64;
+  static constexpr size_t total = misc + 32;
   static_assert(total + 1024 <= 232448, "shared memory budget");
+  static_assert(red % 16 == 0 && mref % 16 == 0 && queue % 4 == 0 && bars % 8 == 0 && misc % 8 == 0, "alignment");
   // O^T at dim 64 reads a second block past V's last slot (lanes nobody reads)
   static_assert(v + kStages * kKv + kBlock <= total, "V overread stays in bounds");
 };
 
-__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
 
 template <int N, int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
 page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const ListParams p) {
   using L = ListSmem<N, kDim>;
-  constexpr int kSt = L::kStages, kB = kDim / 64;
+  constexpr int kSt = L::kStages, kB = kDim / 64, kPb = L::kPBufs, kRecs = L::kRecs;
   constexpr uint32_t kColO = 2 * N;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -102,20 +112,18 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   float *red_s = reinterpret_cast<float *>(smem + L::red);
   float *mref_s = reinterpret_cast<float *>(smem + L::mref);
   // fac[h] overwrites red[0][h], which only the thread that writes it has read;
-  // between a read of fac and the next write of red lie a vote of the four
-  // warps or (raise, then end of the unit, in one tile) the product that waits
-  // for all four
+  // a vote or a barrier of the softmax warps lies between a read of fac and the
+  // next write of red
   float *fac_s = reinterpret_cast<float *>(smem + L::fac);
-  int *queue = reinterpret_cast<int *>(smem + L::queue);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
   uint64_t *kfull = bars, *kempty = kfull + kSt, *vfull = kempty + kSt, *vempty = vfull + kSt;
   uint64_t *qfull = vempty + kSt, *qempty = qfull + 1, *sfull = qempty + 1, *sempty = sfull + 2;
-  uint64_t *pfull = sempty + 2, *pempty = pfull + 1, *ofull = pempty + 1, *oempty = ofull + 1;
+  uint64_t *pfull = sempty + 2, *pempty = pfull + kPb, *ofull = pempty + kPb, *oempty = ofull + 1;
   uint64_t *rfull = oempty + 1, *done = rfull + kRecs;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
-  volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 8);
+  volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 4);
+  int *start_t = reinterpret_cast<int *>(smem + L::misc + 8);
   long long *start_s = reinterpret_cast<long long *>(smem + L::misc + 16);  // total tiles, offset of the first token
-  int *start_t = reinterpret_cast<int *>(smem + L::misc + 32);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
@@ -134,13 +142,15 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     mbar_init(qempty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&sempty[i], 4);
+      mbar_init(&sempty[i], kSoftmax / 32);
       mbar_init(&done[i], 1);
     }
-    mbar_init(pfull, 4);
-    mbar_init(pempty, 1);
+    for (int i = 0; i < kPb; ++i) {
+      mbar_init(&pfull[i], kSoftmax / 32);
+      mbar_init(&pempty[i], 1);
+    }
     mbar_init(ofull, 1);
-    mbar_init(oempty, 4);
+    mbar_init(oempty, kSoftmax / 32);
     for (int i = 0; i < kRecs; ++i) mbar_init(&rfull[i], 1);
     *abort_s = 0;
     fence_barrier_init();
@@ -208,12 +218,18 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     *abort_s = 1;
   };
 
-  if (warp == kWarpLoad) {
-    // ------------------------------------------------------------------ loader
+  if (warp >= kWarpK) {
+    // ----------------------------------------------------------------- loaders
+    // One warp copies K (and the queries, and publishes the records), one V;
+    // both walk the same lists.
+    const bool is_k = warp == kWarpK;
+    int *queue = reinterpret_cast<int *>(smem + L::queue) + (is_k ? 0 : kQueue);
+    uint64_t *full = is_k ? kfull : vfull, *empty = is_k ? kempty : vempty;
+    const CUtensorMap *map = is_k ? &kmap : &vmap;
+    uint8_t *ring = is_k ? ks : vs;
     if (lane == 0) {
-      prefetch_tmap(&qmap);
-      prefetch_tmap(&kmap);
-      prefetch_tmap(&vmap);
+      prefetch_tmap(map);
+      if (is_k) prefetch_tmap(&qmap);
     }
     int n = 0, qn = 0;
     bool ok = true;
@@ -236,6 +252,8 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       base = u * p.tpu;
     }
     const uint32_t rows_total = static_cast<uint32_t>(p.pv.n_pages) * p.pv.H_kv * p.pv.P;
+    const int slot = lane / kB, kb = lane % kB;  // this lane's copy: page slot, 64-dim block
+    const uint32_t dst = kb * L::kBlock + slot * p.pv.P * 128;
     long long x = x_begin;
     while (ok && x < x_end) {
       const int cnt = p.whole ? count_of(t, false) : p.tpu;
@@ -248,10 +266,11 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       const int e = static_cast<int>(min(static_cast<long long>(cnt), x_end - base));
       const bool starts = a == 0, ends = e == cnt;
       int b = 0, pos = 0;
-      const bool tok = load_paged_token(p.pv, t, p.status, lane == 0 && sub == 0 && starts && !p.whole, b, pos);
+      const bool tok = load_paged_token(p.pv, t, p.status, is_k && lane == 0 && sub == 0 && starts && !p.whole, b, pos);
       if (tok) {
         const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64;
         const int last = pos >> p.pv.logP;
+        const int own = pos + 1 - last * p.pv.P;  // positions of the token's own page that it sees
         const int f = p.whole ? p.first_page : max(last + 1 - p.local, 0);
         const int nlist = p.whole ? 0 : p.K;
         const int r1 = min(e * spt, nlist + last + 1 - f);
@@ -262,29 +281,32 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           cut_unit = u;
           cut_last = c_last;
         }
-        if (p.keep && starts && lane == 0) p.info[u] = make_int2(c, c_last);
+        if (p.keep && starts && is_k && lane == 0) p.info[u] = make_int2(c, c_last);
         // page entry i of the list (page id, bit 30 set for the token's own
         // page, whose later positions are masked), -1 when it names no page
         auto resolve = [&](int i) -> int {
+          if (i >= r1) return -1;
           int j;
           if (i < nlist) {
             j = p.idx[(static_cast<int64_t>(t) * p.pv.H_kv + hk) * p.K + i];
             if (j < 0 || j >= f) {
-              if (j < -1 || j > last) raise_flag(p.status, kFlagBadIndex);
+              if (is_k && (j < -1 || j > last)) raise_flag(p.status, kFlagBadIndex);
               return -1;
             }
           } else {
             j = f + i - nlist;
           }
-          const int page = load_page(p.pv, b, j, p.status, true);
+          const int page = load_page(p.pv, b, j, p.status, is_k);
           return page < 0 ? -1 : page | (j == last ? 1 << 30 : 0);
         };
         bool first = true, more = true;
+        int ahead = resolve(r + lane);  // the next batch, resolved while earlier tiles are copied
         while (more) {
           while (qe - qh <= spt && r < r1) {  // enough for this tile and to know whether another follows
-            const int rest = qe - qh;
+            const int rest = qe - qh, ent = ahead;
+            r += 32;
+            ahead = resolve(r + lane);
             const int keep = lane < rest ? queue[qh + lane] : 0;
-            const int ent = r + lane < r1 ? resolve(r + lane) : -1;
             const uint32_t m = __ballot_sync(0xffffffffu, ent >= 0);
             __syncwarp();
             if (lane < rest) queue[lane] = keep;
@@ -292,73 +314,60 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             __syncwarp();
             qh = 0;
             qe = rest + __popc(m);
-            r += 32;
           }
           const int take = min(spt, qe - qh);
           more = qe - qh > take;
+          const int ent = slot < take ? queue[qh + slot] : -1;
           const int s = n % kSt;
-          if (!mbar_wait_warp(&kempty[s], ((n / kSt) & 1) ^ 1) || *abort_s) {
+          uint32_t cn0 = 0, cn1 = 0;
+          bool masked = false;
+          if (is_k) {
+            // keys present among each 16: lane g's own granule, its page slot
+            // held by the lanes of that slot
+            const int g = lane & 7, sg = (16 * g) >> p.pv.logP;
+            const int eg = __shfl_sync(0xffffffffu, ent, sg * kB);
+            int have = eg >= 0 ? 16 : 0;
+            if (eg >= 0 && (eg >> 30)) have = min(max(own - (16 * g - (sg << p.pv.logP)), 0), 16);
+            masked = __any_sync(0xffffffffu, eg >= 0 && have < 16);
+            const uint32_t byte = lane < 8 ? static_cast<uint32_t>(have) << (8 * (g & 3)) : 0u;
+            cn0 = __reduce_or_sync(0xffffffffu, g < 4 ? byte : 0u);
+            cn1 = __reduce_or_sync(0xffffffffu, g < 4 ? 0u : byte);
+          }
+          if (!mbar_wait_warp(&empty[s], ((n / kSt) & 1) ^ 1) || *abort_s) {
             ok = false;
             break;
           }
-          // slot of this lane's copy: boxes of P rows x 64 dims
-          const int q = lane / kB, kb = lane % kB;
-          const int ent = q < take ? queue[qh + q] : -1;
-          // an empty slot reads past the tensor's end: the copy fills zeros
+          if (lane == 0) mbar_expect_tx(&full[s], L::kKv);
+          __syncwarp();
+          // a slot without a page reads past the tensor's end: the copy fills zeros
           const uint32_t y = ent >= 0 ? ((static_cast<uint32_t>(ent) & 0x3FFFFFFFu) * p.pv.H_kv + hk) * p.pv.P
                                       : rows_total;
-          if (lane == 0) {
-            uint32_t cn[2] = {0, 0};
-            int masked = 0;
-            for (int g = 0; g < 8; ++g) {
-              const int qq = (16 * g) >> p.pv.logP;
-              int have = 0;
-              if (qq < take) {
-                have = 16;
-                if (queue[qh + qq] >> 30) {
-                  have = min(max(pos + 1 - last * p.pv.P - (16 * g - qq * p.pv.P), 0), 16);
-                  masked |= have < 16;
-                }
-              }
-              cn[g >> 2] |= static_cast<uint32_t>(have) << (8 * (g & 3));
-            }
+          if (slot < spt) tma_load_2d(ring + s * L::kKv + dst, map, &full[s], 64 * kb, static_cast<int>(y));
+          if (is_k && lane == 0) {
             Record &rec = recs[n % kRecs];
             rec.flags = (first ? kFirst : 0) | (more ? 0 : kLast) | (masked ? kMasked : 0) |
-                        (!p.keep && starts && ends ? kDirect : 0);
+                        (!p.keep && starts && ends ? kDirect : 0) | min(64, (hk + 1) * p.group - h0) << 8;
             rec.row = t * p.pv.H + h0;
-            rec.heads = min(64, (hk + 1) * p.group - h0);
             rec.slot = p.keep ? u + c : 2 * c + (starts ? 1 : 0);
-            rec.cnt[0] = cn[0];
-            rec.cnt[1] = cn[1];
+            rec.cnt[0] = cn0;
+            rec.cnt[1] = cn1;
             mbar_arrive(&rfull[n % kRecs]);
-            mbar_expect_tx(&kfull[s], L::kKv);
           }
-          __syncwarp();
-          const bool mine = q < spt;
-          const uint32_t dst = kb * L::kBlock + q * p.pv.P * 128;
-          if (mine) tma_load_2d(ks + s * L::kKv + dst, &kmap, &kfull[s], 64 * kb, static_cast<int>(y));
-          if (first) {
+          ++n;
+          if (is_k && first) {
             // the queries, once the previous unit's last product has read its own
-            bool got = true;
             if (lane == 0) {
-              got = mbar_wait(qempty, (qn & 1) ^ 1);
-              if (got) {
+              ok = mbar_wait(qempty, (qn & 1) ^ 1);
+              if (ok) {
                 mbar_expect_tx(qfull, N * kDim * 2);
                 for (int i = 0; i < kB; ++i)
                   tma_load_2d(qs + i * N * 128, &qmap, qfull, 64 * i, t * p.pv.H + h0);
               }
             }
-            if (!__shfl_sync(0xffffffffu, got, 0)) ok = false;
-            else ++qn;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            ++qn;
           }
-          if (!mbar_wait_warp(&vempty[s], ((n / kSt) & 1) ^ 1)) ok = false;
-          if (ok) {
-            if (lane == 0) mbar_expect_tx(&vfull[s], L::kKv);
-            __syncwarp();
-            if (mine) tma_load_2d(vs + s * L::kKv + dst, &vmap, &vfull[s], 64 * kb, static_cast<int>(y));
-          }
-          ++n;
-          if (!ok) break;
           qh += take;
           first = false;
         }
@@ -374,17 +383,15 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     }
     if (lane == 0) {
       if (!ok) fail();
-      if (!p.keep) p.cut[c] = make_int2(cut_unit, cut_last);
-      if (ok) {
-        recs[n % kRecs].flags = kEnd;
-        mbar_arrive(&rfull[n % kRecs]);
+      if (is_k) {
+        if (!p.keep) p.cut[c] = make_int2(cut_unit, cut_last);
+        if (ok) {
+          recs[n % kRecs].flags = kEnd;
+          mbar_arrive(&rfull[n % kRecs]);
+        }
       }
-      // drain: every copy issued lands before the CTA exits (the last tile's V
-      // copy may not have been issued when a wait gave up)
-      for (int i = max(0, n - kSt); i < n; ++i) {
-        mbar_wait(&kfull[i % kSt], (i / kSt) & 1);
-        if (ok || i < n - 1) mbar_wait(&vfull[i % kSt], (i / kSt) & 1);
-      }
+      // drain: every copy issued lands before the CTA exits
+      for (int i = max(0, n - kSt); i < n; ++i) mbar_wait(&full[i % kSt], (i / kSt) & 1);
       if (qn > 0) mbar_wait(qfull, (qn - 1) & 1);
     }
     __syncwarp();
@@ -435,20 +442,20 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       if (!ok) break;
       const int flags = recs[n % kRecs].flags;
       if (flags & kEnd) break;
-      const int s = n % kSt;
+      const int s = n % kSt, pb = n % kPb;
       if (flags & kFirst) ok = mbar_wait_warp(oempty, (pieces++ & 1) ^ 1);
-      ok = ok && mbar_wait_warp(&vfull[s], (n / kSt) & 1) && mbar_wait_warp(pfull, n & 1);
+      ok = ok && mbar_wait_warp(&vfull[s], (n / kSt) & 1) && mbar_wait_warp(&pfull[pb], (n / kPb) & 1);
       if (!ok || *abort_s) break;
       tc_fence_after();
       if (leader) {
-        const uint64_t da = desc_mn(smem_u32(vs + s * L::kKv), L::kBlock), db = desc_mn(smem_u32(ps), 16384);
+        const uint64_t da = desc_mn(smem_u32(vs + s * L::kKv), L::kBlock), db = desc_mn(smem_u32(ps) + 64 * pb, 16384);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk) {
           const uint64_t o = (kk * 2048) >> 4;
           mma_f16(tmem + kColO, da + o, db + o, idesc, !((flags & kFirst) && kk == 0));
         }
         mma_commit(&vempty[s]);
-        mma_commit(pempty);
+        mma_commit(&pempty[pb]);
         if (flags & kLast) mma_commit(ofull);
       }
       __syncwarp();
@@ -461,12 +468,18 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     __syncwarp();
   } else {
     // ----------------------------------------------------------------- softmax
-    const int key = tid;
-    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    // Thread: one key of the tile (the accumulator lane) and half of the heads.
+    // The logits' arguments are formed once, tested against the reference, and
+    // only then raised to weights.
+    constexpr int NH = N / 2;
+    const int quarter = warp & 3, key = tid & 127, hb = warp >= 4 ? NH : 0;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const float cs = p.qk_scale;
-    float l[N];
+    const float2 cs2 = make_float2(cs, cs);
+    float *red_w = red_s + N * quarter + hb;
+    float l[NH];
 #pragma unroll
-    for (int h = 0; h < N; ++h) l[h] = 0.f;
+    for (int h = 0; h < NH; ++h) l[h] = 0.f;
     int pieces = 0;
     for (int n = 0;; ++n) {
       bool ok = mbar_wait_warp(&rfull[n % kRecs], (n / kRecs) & 1);
@@ -475,126 +488,126 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       const bool end = (rec.flags & kEnd) != 0;
       const int bf = n & 1, s = n % kSt;
       const bool first = (rec.flags & kFirst) != 0;
-      ok = ok && (end || mbar_wait_warp(&sfull[bf], (n >> 1) & 1));
-      uint32_t sv[N];
       const uint32_t word = key < 64 ? rec.cnt[0] : rec.cnt[1];
       const bool present = static_cast<uint32_t>(key & 15) < ((word >> (8 * ((key >> 4) & 3))) & 0xFFu);
+      ok = ok && (end || mbar_wait_warp(&sfull[bf], (n >> 1) & 1));
+      float v[NH];  // logits, then c s - m_ref
       bool over = first;
       if (ok && !end) {
         tc_fence_after();
-        const uint32_t ta = tmem + lanes + N * bf;
-        if constexpr (N == 16) {
-          tmem_load(ta, sv);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N / 32; ++i) tmem_load(ta + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * i));
-        }
+        tmem_load(tmem + lanes + N * bf + hb, reinterpret_cast<uint32_t(&)[NH]>(v));
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[bf]);
-        if (!first && present) {
+        if (!first) {
+          float top = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < N; ++h) over |= fmaf(__uint_as_float(sv[h]), cs, -mref_s[h]) > kLazy - kHead;
+          for (int h = 0; h < NH; h += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(mref_s + hb + h);
+            float2 *w = reinterpret_cast<float2 *>(v + h);
+            w[0] = fma2(w[0], cs2, make_float2(-m.x, -m.y));
+            w[1] = fma2(w[1], cs2, make_float2(-m.z, -m.w));
+            top = max3(max3(top, w[0].x, w[0].y), w[1].x, w[1].y);
+          }
+          over = present && top > kLazy - kHead;
         }
       }
       if (!ok && lane == 0) fail();
       // one vote per tile; only when it passes, a second one tells a raise of
-      // the reference from the end or a failure (all four warps leave together)
+      // the reference from the end or a failure (all warps leave together)
       const bool leave = !ok || end || *abort_s;
-      if (barrier_any(2, 128, over || leave)) {
-        if (barrier_any(3, 128, leave)) break;
-        float x[N];
+      if (barrier_any(2, kSoftmax, over || leave)) {
+        if (barrier_any(3, kSoftmax, leave)) break;
+        // the tile's maximum per head, over the keys that exist (for a tile
+        // after the first: of c s - m_ref)
+        float x[NH];
 #pragma unroll
-        for (int h = 0; h < N; ++h) x[h] = present ? __uint_as_float(sv[h]) * cs : -INFINITY;
-        if constexpr (N == 64) {
-          float(&lo)[32] = *reinterpret_cast<float(*)[32]>(x);
-          float(&hi)[32] = *reinterpret_cast<float(*)[32]>(x + 32);
-          red_s[N * warp + lane] = reduce_scatter<true>(lo, lane);
-          red_s[N * warp + 32 + lane] = reduce_scatter<true>(hi, lane);
-        } else {
-          const float m = reduce_scatter<true>(x, lane);
-          if (lane < N) red_s[N * warp + lane] = m;
-        }
+        for (int h = 0; h < NH; ++h) x[h] = present ? (first ? v[h] * cs : v[h]) : -INFINITY;
+        const float top = reduce_scatter<true>(x, lane);
+        if (lane < NH) red_w[lane] = top;
         group_sync();
         if (tid < N) {
-          const float mo = first ? -INFINITY : mref_s[tid];
+          const float mo = first ? 0.f : mref_s[tid];
           const float mt = fmaxf(fmaxf(red_s[tid], red_s[N + tid]), fmaxf(red_s[2 * N + tid], red_s[3 * N + tid]));
-          const float mn = fmaxf(mo, mt + kHead);
-          fac_s[tid] = (mo == -INFINITY || mn == -INFINITY) ? 1.f : exp2f(mo - mn);
-          mref_s[tid] = mn;
+          // the new reference relative to the old one, which only rises
+          const float up = first ? mt + kHead : fmaxf(mt + kHead, 0.f);
+          fac_s[tid] = up;
+          mref_s[tid] = mo + up;
         }
         group_sync();
+#pragma unroll
+        for (int h = 0; h < NH; ++h) v[h] = (first ? v[h] * cs : v[h]) - fac_s[hb + h];
         if (!first) {
           // O^T holds the products up to tile n - 1; scale its columns
-          bool done_o = mbar_wait_warp(pempty, (n & 1) ^ 1);
+          const bool done_o = mbar_wait_warp(&pempty[(n - 1) % kPb], ((n - 1) / kPb) & 1);
           if (!done_o && lane == 0) fail();
           tc_fence_after();
-          if (done_o && warp < kDim / 32) {
-#pragma unroll
-            for (int i = 0; i < N / 16; ++i) {
-              uint32_t o[16];
-              tmem_load(tmem + lanes + kColO + 16 * i, o);
+          if (done_o && quarter < kDim / 32) {
+#pragma unroll 1
+            for (int i = 0; i < NH; i += 8) {
+              uint32_t o[8];
+              tmem_load(tmem + lanes + kColO + hb + i, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * fac_s[16 * i + q]);
-              tmem_store(tmem + lanes + kColO + 16 * i, o);
+              for (int q = 0; q < 8; ++q)
+                o[q] = __float_as_uint(__uint_as_float(o[q]) * exp2f(-fac_s[hb + i + q]));
+              tmem_store8(tmem + lanes + kColO + hb + i, o);
             }
             tmem_wait_st();
           }
           tc_fence_before();
 #pragma unroll
-          for (int h = 0; h < N; ++h) l[h] *= fac_s[h];
+          for (int h = 0; h < NH; ++h) l[h] *= exp2f(-fac_s[hb + h]);
         }
       }
-      // P^T buffer free: the previous tile's product is done
-      if (!mbar_wait_warp(pempty, (n & 1) ^ 1) && lane == 0) fail();
+      // P^T buffer free: the product that read it last is done
+      const int pb = n % kPb;
+      if (!mbar_wait_warp(&pempty[pb], ((n / kPb) & 1) ^ 1) && lane == 0) fail();
+      if (!__all_sync(0xffffffffu, present)) {
 #pragma unroll
-      for (int ch = 0; ch < N / 8; ++ch) {
+        for (int h = 0; h < NH; ++h) v[h] = present ? v[h] : -INFINITY;
+      }
+#pragma unroll
+      for (int ch = 0; ch < NH / 8; ++ch) {
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int h = 8 * ch + 2 * q;
-          const float2 m2 = *reinterpret_cast<const float2 *>(&mref_s[h]);
-          const float pa = present ? exp2_hw(fmaf(__uint_as_float(sv[h]), cs, -m2.x)) : 0.f;
-          const float pb = present ? exp2_hw(fmaf(__uint_as_float(sv[h + 1]), cs, -m2.y)) : 0.f;
-          l[h] += pa;
-          l[h + 1] += pb;
-          w[q] = pack_bf16x2(pa, pb);
+          const float2 e2 = make_float2(exp2_hw(v[h]), exp2_hw(v[h + 1]));
+          float2 *l2 = reinterpret_cast<float2 *>(l + h);
+          *l2 = add2(*l2, e2);
+          w[q] = pack_bf16x2(e2.x, e2.y);
         }
-        *reinterpret_cast<uint4 *>(ps + sw128_offset(key, 16u * ch)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(ps + sw128_offset(key, 64u * pb + 2u * hb + 16u * ch)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
       }
       if (rec.flags & kMasked) {
         // positions past the token's own may hold anything: their V rows
-        // become zeros before the product reads them
+        // become zeros before the product reads them (each half of the heads'
+        // threads half of the row)
         if (!mbar_wait_warp(&vfull[s], (n / kSt) & 1) && lane == 0) fail();
         if (!present) {
+          constexpr int kChunks = kDim / 16;  // 16-byte chunks of half a row
 #pragma unroll
-          for (int i = 0; i < kB; ++i)
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-              *reinterpret_cast<uint4 *>(vs + s * L::kKv + i * L::kBlock + key * 128 + 16 * ch) =
-                  make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < kChunks; ++i) {
+            const int ch = (hb ? kChunks : 0) + i;
+            *reinterpret_cast<uint4 *>(vs + s * L::kKv + (ch >> 3) * L::kBlock + key * 128 + 16 * (ch & 7)) =
+                make_uint4(0, 0, 0, 0);
+          }
         }
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pfull);
+      if (lane == 0) mbar_arrive(&pfull[pb]);
       if (rec.flags & kLast) {
-        if (!mbar_wait_warp(ofull, pieces & 1) && lane == 0) fail();
-        ++pieces;
-        tc_fence_after();
-        if constexpr (N == 64) {
-          float(&lo)[32] = *reinterpret_cast<float(*)[32]>(l);
-          float(&hi)[32] = *reinterpret_cast<float(*)[32]>(l + 32);
-          red_s[N * warp + lane] = reduce_scatter<false>(lo, lane);
-          red_s[N * warp + 32 + lane] = reduce_scatter<false>(hi, lane);
-        } else {
-          const float v = reduce_scatter<false>(l, lane);
-          if (lane < N) red_s[N * warp + lane] = v;
-        }
+        // sums over the keys while the last product runs (the barrier: a raise
+        // in this tile still reads fac, which lies over the reduction's rows)
+        const float sum_w = reduce_scatter<false>(l, lane);
+        group_sync();
+        if (lane < NH) red_w[lane] = sum_w;
 #pragma unroll
-        for (int h = 0; h < N; ++h) l[h] = 0.f;
+        for (int h = 0; h < NH; ++h) l[h] = 0.f;
         group_sync();
         if (tid < N) {
           const float sum = (red_s[tid] + red_s[N + tid]) + (red_s[2 * N + tid] + red_s[3 * N + tid]);
@@ -603,24 +616,27 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             p.ml[static_cast<int64_t>(rec.slot) * N + tid] = make_float2(mref_s[tid], sum);
         }
         group_sync();
-        if (warp < kDim / 32) {
-          const int d = 32 * warp + lane;
-#pragma unroll
-          for (int i = 0; i < N / 16; ++i) {
-            uint32_t o[16];
-            tmem_load(tmem + lanes + kColO + 16 * i, o);
+        if (!mbar_wait_warp(ofull, pieces & 1) && lane == 0) fail();
+        ++pieces;
+        tc_fence_after();
+        if (quarter < kDim / 32) {
+          const int d = 32 * quarter + lane, heads = (rec.flags >> 8) - hb;
+          __nv_bfloat16 *out = p.out + (static_cast<int64_t>(rec.row) + hb) * kDim + d;
+          float *part = p.part + (static_cast<int64_t>(rec.slot) * N + hb) * kDim + d;
+#pragma unroll 1
+          for (int i = 0; i < NH && i < heads; i += 8) {
+            uint32_t o[8];
+            tmem_load(tmem + lanes + kColO + hb + i, o);
             tmem_ld_wait();
             if (rec.flags & kDirect) {
 #pragma unroll
-              for (int q = 0; q < 16; ++q)
-                if (16 * i + q < rec.heads)
-                  p.out[(static_cast<int64_t>(rec.row) + 16 * i + q) * kDim + d] =
-                      __float2bfloat16_rn(__uint_as_float(o[q]) * fac_s[16 * i + q]);
+              for (int q = 0; q < 8; ++q)
+                if (i + q < heads)
+                  out[(i + q) * kDim] = __float2bfloat16_rn(__uint_as_float(o[q]) * fac_s[hb + i + q]);
             } else {
 #pragma unroll
-              for (int q = 0; q < 16; ++q)
-                if (16 * i + q < rec.heads)
-                  p.part[(static_cast<int64_t>(rec.slot) * N + 16 * i + q) * kDim + d] = __uint_as_float(o[q]);
+              for (int q = 0; q < 8; ++q)
+                if (i + q < heads) part[(i + q) * kDim] = __uint_as_float(o[q]);
             }
           }
         }
@@ -653,23 +669,35 @@ merge_cut_kernel(const ListParams p) {
   const int upt = p.pv.H_kv * p.gb, t = cut.x / upt, sub = cut.x % upt;
   const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64, heads = min(64, (hk + 1) * p.group - h0);
   constexpr int V = kDim / 32;  // values per lane
-  for (int i = blockIdx.y * 8 + warp; i < heads; i += 8 * gridDim.y) {
-    float M = -INFINITY;
-    for (int k = c; k <= cut.y; ++k) M = fmaxf(M, p.ml[static_cast<int64_t>(k == c ? 2 * c + 1 : 2 * k) * N + i].x);
-    float acc[V] = {}, l = 0.f;
-    for (int k = c; k <= cut.y; ++k) {
-      const int64_t at = static_cast<int64_t>(k == c ? 2 * c + 1 : 2 * k) * N + i;
-      const float2 ml = p.ml[at];
-      const float a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      l += a * ml.y;
+  const int i = blockIdx.y * 8 + warp;
+  if (i >= heads) return;
+  auto slot_of = [&](int k) { return static_cast<int64_t>(k == c ? 2 * c + 1 : 2 * k) * N + i; };
+  float M = -INFINITY;
+  for (int k = c + lane; k <= cut.y; k += 32) M = fmaxf(M, p.ml[slot_of(k)].x);
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(a, p.part[at * kDim + V * lane + e], acc[e]);
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[V] = {}, l = 0.f;
+  for (int k0 = c; k0 <= cut.y; k0 += 32) {
+    float a = 0.f, la = 0.f;  // this lane's part: weight, weighted sum
+    if (k0 + lane <= cut.y) {
+      const float2 ml = p.ml[slot_of(k0 + lane)];
+      a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      la = a * ml.y;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int n = min(32, cut.y + 1 - k0);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float w = __shfl_sync(0xffffffffu, a, k);
+      l += __shfl_sync(0xffffffffu, la, k);
+      const float *o = p.part + slot_of(k0 + k) * kDim + V * lane;
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      p.out[(static_cast<int64_t>(t) * p.pv.H + h0 + i) * kDim + V * lane + e] = __float2bfloat16_rn(acc[e] * inv);
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[e], acc[e]);
+    }
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    p.out[(static_cast<int64_t>(t) * p.pv.H + h0 + i) * kDim + V * lane + e] = __float2bfloat16_rn(acc[e] * inv);
 }
 
 template <int N, int kDim>
@@ -688,7 +716,7 @@ cudaError_t launch_list(const sa_paged_args &pa, const void *q, ListParams &p, i
   if (e != cudaSuccess) return e;
   e = launch_ex(pdl, kern, dim3(grid), dim3(kThreads), smem, stream, 1, qmap, kmap, vmap, p);
   if (e != cudaSuccess || p.keep) return e;
-  return launch_ex(true, merge_cut_kernel<N, kDim>, dim3(grid, N / 16), dim3(256), 0, stream, 1, p);
+  return launch_ex(true, merge_cut_kernel<N, kDim>, dim3(grid, N / 8), dim3(256), 0, stream, 1, p);
 }
 
 template <int kDim>

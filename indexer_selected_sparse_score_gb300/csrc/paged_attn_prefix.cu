@@ -455,16 +455,26 @@ merge_rows_kernel(const PrefixParams p, const ListParams own, int cols, int grid
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[V] = {}, l = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < total; ++k) {
-    const float2 *mlp;
-    const float *o;
-    locate(k, mlp, o);
-    const float2 ml = *mlp;
-    const float a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-    l = fmaf(a, ml.y, l);
+  for (int k0 = 0; k0 < total; k0 += 32) {
+    float a = 0.f, la = 0.f;  // this lane's piece: weight, weighted sum
+    const float *mine = nullptr;
+    if (k0 + lane < total) {
+      const float2 *ml;
+      locate(k0 + lane, ml, mine);
+      const float2 v = *ml;
+      a = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
+      la = a * v.y;
+    }
+    const int n = min(32, total - k0);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float w = __shfl_sync(0xffffffffu, a, k);
+      l += __shfl_sync(0xffffffffu, la, k);
+      const float *o =
+          reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k));
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = fmaf(a, o[V * lane + e], acc[e]);
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[V * lane + e], acc[e]);
+    }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll

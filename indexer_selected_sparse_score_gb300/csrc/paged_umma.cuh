@@ -11,6 +11,12 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 // 32 lanes x N consecutive 32-bit columns (the 32x32b shape): thread i of the
 // warp accesses lane (warp's lane quarter + i).
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -31,6 +37,11 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t *r /* 8 */) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t *r /* 16 */) {
   asm volatile(
@@ -102,10 +113,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
-// Reduces N (16 or 32) values per lane over the warp.  N = 32: the result for
-// value l lands in lane l.  N = 16: in lanes l and l + 16.  Halving rounds, in
-// the round of offset o each lane keeps the half of its remaining values picked
-// by bit o of its lane number.
+// Reduces N (8, 16 or 32) values per lane over the warp; the result for value v
+// lands in the lanes with lane % N = v.  Halving rounds: in the round of offset
+// o each lane keeps the half of its remaining values picked by bit o of its
+// lane number.
 template <bool kMax, int N>
 __device__ __forceinline__ float reduce_scatter(float (&v)[N], int lane) {
 #pragma unroll
@@ -119,8 +130,9 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[N], int lane) {
       v[i] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
-  if (N == 16) {
-    const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
     v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
   }
   return v[0];
