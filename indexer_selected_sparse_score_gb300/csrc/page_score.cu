@@ -1,45 +1,382 @@
 // The cheap score of the pages of a paged cache: scale times the product of
 // the summed queries of a KV head's group with the mean key of every complete
-// page.  One warp per (token, KV head, page).
+// page.
+//
+// The score is an fp32 number, so the summed query enters the tensor cores as
+// three bf16 pieces (q = hi + mid + lo to 2^-24 of it) against the bf16 means:
+// products exact, sums fp32.  Two kernels.  With few tokens per sequence (a
+// decode step) every mean key is met by one token: a stream of 2 D-byte rows
+// bound by HBM; there a warp-level product takes 16 pages' rows straight from
+// registers against the three pieces as columns (on the CUDA cores the unpacking
+// and reducing of every row had cost more issue slots than the stream leaves).
+// With many tokens per sequence (a prefill chunk) it is a product of 128 tokens
+// with 128 pages at a time (tcgen05), bound by reading the queries and writing
+// the scores.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "internal.h"
 #include "paged.cuh"
+#include "paged_umma.cuh"
 
 namespace sa {
 namespace {
 
-constexpr int kThreads = 256;
+using namespace umma;
 
-__global__ void __launch_bounds__(kThreads)
-page_score_kernel(const PagedView pv, const uint16_t *q, const uint16_t *k_mean, float *scores, int64_t ld, int D,
-                  float scale, int local, int32_t *row_seq, int32_t *row_pos, uint32_t *status) {
-  const int t = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31;
-  const int j = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (j >= pv.max_pages) return;
-  int b, pos;
-  const bool ok = load_paged_token(pv, t, status, threadIdx.x == 0 && blockIdx.x == 0, b, pos);
-  if (row_seq && j == 0 && lane == 0) {
-    const int f = ok ? max((pos >> pv.logP) + 1 - local, 0) : 0;
-    row_seq[t * pv.H_kv + h] = ok ? b : -1;
-    row_pos[t * pv.H_kv + h] = max(f * pv.P - 1, 0);
+struct ScoreParams {
+  PagedView pv;
+  const uint16_t *q, *k_mean;
+  float *scores;
+  int64_t ld;
+  float scale;
+  int local;
+  int32_t *row_seq, *row_pos;  // [T, H_kv] or NULL: the top-k's token arrays
+  uint32_t *status;
+};
+
+__device__ __forceinline__ void add_bf16x8(float (&a)[8], uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[2 * i] += __uint_as_float(w[i] << 16);
+    a[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
   }
+}
+
+// Sum of the G queries of (token t, KV head h) over 8 dims from chunk c.
+template <int kDim>
+__device__ __forceinline__ void sum_queries(const ScoreParams &p, int64_t t, int h, int G, int c, float (&a)[8]) {
+  const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (t * p.pv.H + static_cast<int64_t>(h) * G) * kDim) + c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = 0.f;
+#pragma unroll 16
+  for (int g = 0; g < G; ++g) add_bf16x8(a, src[g * (kDim / 8)]);
+}
+
+__device__ __forceinline__ void write_row_token(const ScoreParams &p, int64_t row, bool ok, int b, int pos) {
+  const int f = ok ? max((pos >> p.pv.logP) + 1 - p.local, 0) : 0;
+  p.row_seq[row] = ok ? b : -1;
+  p.row_pos[row] = max(f * p.pv.P - 1, 0);
+}
+
+// ------------------------------------------------------- one token at a time
+
+constexpr int kThreads = 256;
+constexpr int kHeads = 8;     // KV heads of a CTA
+constexpr int kMaxChunk = 256;
+
+// D += A B, 16 x 8 x 16, bf16 inputs.
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// CTA (x, t, z): pages x * chunk .. of token t for KV heads 8 z .. 8 z + 7.  A
+// warp's item is 16 pages of one head: A rows are the pages, B columns 0-2 the
+// query's pieces.  The order of the dims within a product is free, so lane 4 g
+// + i holds 16-byte chunks i, i + 4, .. of rows g and g + 8 as they lie in
+// memory, two k-steps a chunk.
+template <int kDim>
+__global__ void __launch_bounds__(kThreads)
+score_token_kernel(const ScoreParams p, int chunk) {
+  constexpr int kChunks = kDim / 8, kLoads = kChunks / 4;  // of a row; a lane's loads of it
+  __shared__ __align__(16) uint16_t qs[kHeads][3][kDim];
+  __shared__ float tile[kHeads * kMaxChunk];
+  __shared__ int page_s[kMaxChunk];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t = blockIdx.y, h0 = blockIdx.z * kHeads, nh = min(kHeads, p.pv.H_kv - h0), G = p.pv.H / p.pv.H_kv;
+  const int j0 = blockIdx.x * chunk, nj = min(chunk, p.pv.max_pages - j0);
+  const bool report = tid == 0 && blockIdx.x == 0 && blockIdx.z == 0;
+  int b, pos;
+  const bool ok = load_paged_token(p.pv, t, p.status, report, b, pos);
+  if (p.row_seq && blockIdx.x == 0 && tid < nh) write_row_token(p, static_cast<int64_t>(t) * p.pv.H_kv + h0 + tid, ok, b, pos);
   if (!ok) return;
-  const int G = pv.H / pv.H_kv;
-  float s = -INFINITY;
-  if (j < (pos + 1) >> pv.logP) {
-    const int page = load_page(pv, b, j, status, lane == 0);
-    if (page >= 0) {
-      s = 0.f;
-      for (int d = lane; d < D; d += 32) {
-        float qs = 0.f;
-        for (int g = 0; g < G; ++g)
-          qs += bf16_bits_to_float(q[(static_cast<int64_t>(t) * pv.H + h * G + g) * D + d]);
-        s = fmaf(qs, bf16_bits_to_float(k_mean[(static_cast<int64_t>(page) * pv.H_kv + h) * D + d]), s);
+  const int vis = min(max(((pos + 1) >> p.pv.logP) - j0, 0), nj);
+  for (int j = tid; j < vis; j += kThreads) page_s[j] = load_page(p.pv, b, j0 + j, p.status, blockIdx.z == 0);
+  if (vis > 0 && tid < nh * kChunks) {
+    float a[8];
+    const int h = tid / kChunks, c = tid % kChunks;
+    sum_queries<kDim>(p, t, h0 + h, G, c, a);
+#pragma unroll
+    for (int piece = 0; piece < 3; ++piece) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+        a[2 * e] -= __uint_as_float(w[e] << 16);
+        a[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
       }
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s *= scale;
+      *reinterpret_cast<uint4 *>(&qs[h][piece][8 * c]) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  if (lane == 0) scores[(static_cast<int64_t>(t) * pv.H_kv + h) * ld + j] = s;
+  __syncthreads();
+  const int g = lane >> 2, ti = lane & 3;
+  const int items = ((vis + 15) >> 4) * nh;
+  for (int it = warp; it < items; it += kThreads / 32) {
+    const int jt = it / nh, h = it - jt * nh;
+    uint4 x[2][kLoads];
+    bool bad[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int j = 16 * jt + g + 8 * r;
+      const int page = j < vis ? page_s[j] : -1;
+      bad[r] = page < 0;
+      const uint4 *src =
+          reinterpret_cast<const uint4 *>(p.k_mean + (static_cast<int64_t>(max(page, 0)) * p.pv.H_kv + h0 + h) * kDim);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) x[r][i] = bad[r] ? make_uint4(0, 0, 0, 0) : src[ti + 4 * i];
+    }
+    float d[4] = {};
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (g < 3) y = *reinterpret_cast<const uint4 *>(&qs[h][g][8 * (ti + 4 * i)]);
+      mma_16816(d, x[0][i].x, x[1][i].x, x[0][i].y, x[1][i].y, y.x, y.y);
+      mma_16816(d, x[0][i].z, x[1][i].z, x[0][i].w, x[1][i].w, y.z, y.w);
+    }
+    // columns 0 and 1 sit in lane 4 g, column 2 in lane 4 g + 1
+    const float e0 = __shfl_down_sync(0xffffffffu, d[0], 1), e1 = __shfl_down_sync(0xffffffffu, d[2], 1);
+    if (ti == 0) {
+      const float s0 = (d[0] + (d[1] + e0)) * p.scale, s1 = (d[2] + (d[3] + e1)) * p.scale;
+      float *row = tile + h * chunk + 16 * jt + g;
+      if (16 * jt + g < vis) row[0] = bad[0] ? -INFINITY : s0;
+      if (16 * jt + g + 8 < vis) row[8] = bad[1] ? -INFINITY : s1;
+    }
+  }
+  __syncthreads();
+  for (int h = warp; h < nh; h += kThreads / 32) {
+    float *row = p.scores + (static_cast<int64_t>(t) * p.pv.H_kv + h0 + h) * p.ld + j0;
+    for (int j = lane; j < nj; j += 32) row[j] = j < vis ? tile[h * chunk + j] : -INFINITY;
+  }
+}
+
+// ------------------------------------------------------ 128 tokens at a time
+
+constexpr int kTile = 128;  // tokens, and pages, of a product
+constexpr int kTileThreads = 512;
+constexpr int kPieces = 3;  // bf16 pieces of a summed query
+
+template <int kDim>
+struct ScoreSmem {
+  static constexpr uint32_t kBlock = kTile * 128;          // one 64-dim block of 128 rows
+  static constexpr uint32_t kRows = kBlock * (kDim / 64);
+  static constexpr size_t q = 0;                           // [piece][D / 64][128 tokens][128 B]
+  static constexpr size_t k = kPieces * kRows;             // [2][D / 64][128 pages][128 B]
+  static constexpr size_t pages = k + 2 * kRows;           // [2][128] page ids of a block
+  static constexpr size_t tok = pages + 2 * kTile * 4;     // [128] int2: sequence (-1: skip), visible pages
+  static constexpr size_t bars = tok + kTile * 8;
+  static constexpr size_t misc = bars + 4 * 8;
+  static constexpr size_t total = misc + 32;
+  static_assert(total + 1024 <= 232448, "shared memory budget");
+};
+
+// CTA (x, h): tokens 128 x .. 128 x + 127, KV head h, every page.  Per
+// sequence among the tokens: blocks of 128 pages, two in flight, the next
+// block's product running and the one after being gathered while the current
+// one's scores are written.
+template <int kDim>
+__global__ void __launch_bounds__(kTileThreads, 1)
+score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p) {
+  using L = ScoreSmem<kDim>;
+  constexpr int kB = kDim / 64, kChunks = kDim / 8;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *qs = smem + L::q, *ks = smem + L::k;
+  int *page_s = reinterpret_cast<int *>(smem + L::pages);
+  int2 *tok_s = reinterpret_cast<int2 *>(smem + L::tok);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bars), *ready = full + 2;
+  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
+  int *seq_s = reinterpret_cast<int *>(smem + L::misc + 8);  // sequence and page bound of the pass
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t0 = blockIdx.x * kTile, nt = min(kTile, p.pv.T - t0), h = blockIdx.y, G = p.pv.H / p.pv.H_kv;
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 1);
+    fence_barrier_init();
+    prefetch_tmap(&kmap);
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_base_s, 256);
+    tmem_relinquish();
+  }
+  if (tid < kTile) {
+    int b = -1, pos = -1;
+    bool ok = false;
+    if (tid < nt) {
+      ok = load_paged_token(p.pv, t0 + tid, p.status, h == 0, b, pos);
+      if (p.row_seq) write_row_token(p, static_cast<int64_t>(t0 + tid) * p.pv.H_kv + h, ok, b, pos);
+    }
+    tok_s[tid] = make_int2(ok ? b : -1, ok ? (pos + 1) >> p.pv.logP : 0);
+  }
+  // summed queries, split into bf16 pieces (round to nearest: each piece takes
+  // at least 8 bits of what is left)
+  for (int i = tid; i < kTile * kChunks; i += kTileThreads) {
+    const int r = i / kChunks, ch = i % kChunks;
+    float a[8] = {};
+    if (r < nt) sum_queries<kDim>(p, t0 + r, h, G, ch, a);
+    const uint32_t off = (ch >> 3) * L::kBlock + sw128_offset(r, 16u * (ch & 7));
+#pragma unroll
+    for (int piece = 0; piece < kPieces; ++piece) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+        a[2 * e] -= __uint_as_float(w[e] << 16);
+        a[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint4 *>(qs + piece * L::kRows + off) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  fence_proxy_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_s;
+  const int row = 32 * (warp & 3) + lane;          // this thread's token
+  const int2 mine = tok_s[row];
+  const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  float *out = p.scores + (static_cast<int64_t>(t0 + row) * p.pv.H_kv + h) * p.ld;
+  const bool vec = (p.ld & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scores) & 15) == 0;
+  const int nblk = (p.pv.max_pages + kTile - 1) / kTile;
+  int n = 0;  // blocks issued so far (of all passes)
+  int prev = -1;  // sequences are taken in rising order
+  while (true) {
+    if (warp == 0) {
+      // the next sequence among the tokens and the most pages any of them sees
+      int next = INT32_MAX;
+      for (int i = lane; i < kTile; i += 32) {
+        const int b = tok_s[i].x;
+        if (b > prev) next = min(next, b);
+      }
+      next = __reduce_min_sync(0xffffffffu, next);
+      int most = 0;
+      for (int i = lane; i < kTile; i += 32)
+        if (tok_s[i].x == next) most = max(most, tok_s[i].y);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) {
+        seq_s[0] = next;
+        seq_s[1] = most;
+      }
+    }
+    __syncthreads();
+    const int b = seq_s[0], seen = seq_s[1], used = (seen + kTile - 1) / kTile;
+    if (b == INT32_MAX) break;
+    __syncthreads();  // everyone has read the pass before the next one is written
+    prev = b;
+    // block i of the pass (block n + i of all) into buffer (n + i) & 1: mean
+    // keys by gather, four pages a copy; pages that do not exist or lie past
+    // the tokens' sight read row 0 and are masked when written
+    auto gather = [&](int i) {
+      const int bf = (n + i) & 1;
+      int rows[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = i * kTile + 4 * lane + e;
+        const int page = j < seen ? load_page(p.pv, b, j, p.status, h == 0) : -1;
+        page_s[bf * kTile + 4 * lane + e] = page;
+        rows[e] = page >= 0 ? page * p.pv.H_kv + h : 0;
+      }
+      if (lane == 0) mbar_expect_tx(&full[bf], L::kRows);
+      __syncwarp();
+#pragma unroll
+      for (int kb = 0; kb < kB; ++kb)
+        gather_rows4(ks + bf * L::kRows + kb * L::kBlock + lane * 512, &kmap, &full[bf], 64 * kb, rows[0], rows[1],
+                     rows[2], rows[3]);
+    };
+    auto multiply = [&](int i) {
+      const int u = n + i, bf = u & 1;
+      if (!mbar_wait_warp(&full[bf], (u >> 1) & 1)) {
+        if (lane == 0) raise_flag(p.status, kFlagTimeout);
+        return;
+      }
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t db = desc_sw128_kmajor(smem_u32(ks + bf * L::kRows));
+#pragma unroll
+        for (int piece = 0; piece < kPieces; ++piece) {
+          const uint64_t da = desc_sw128_kmajor(smem_u32(qs + piece * L::kRows));
+#pragma unroll
+          for (int kk = 0; kk < kDim / 16; ++kk) {
+            const uint64_t o = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+            mma_f16(tmem + kTile * bf, da + o, db + o, idesc_bf16(128, kTile), piece + kk > 0);
+          }
+        }
+        mma_commit(&ready[bf]);
+      }
+      __syncwarp();
+    };
+    if (warp == 0 && used > 0) {
+      gather(0);
+      multiply(0);
+      if (used > 1) gather(1);
+    }
+    for (int i = 0; i < nblk; ++i) {
+      const int u = n + i, bf = u & 1;
+      const bool live = i < used;
+      float v[32];
+      const int c0 = 32 * (warp >> 2), j0 = i * kTile + c0;
+      if (live) {
+        // the other accumulator was read out before the last barrier
+        if (warp == 0 && i + 1 < used) multiply(i + 1);
+        if (!mbar_wait_warp(&ready[bf], (u >> 1) & 1) && lane == 0) raise_flag(p.status, kFlagTimeout);
+        tc_fence_after();
+        tmem_load(tmem + lanes + kTile * bf + c0, reinterpret_cast<uint32_t(&)[32]>(v));
+        tmem_ld_wait();
+        tc_fence_before();
+        const bool all = j0 + 32 <= mine.y;
+        const int pg = page_s[bf * kTile + c0 + lane];
+        const uint32_t exist = __ballot_sync(0xffffffffu, pg >= 0);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          v[e] *= p.scale;
+          if (!all || exist != 0xffffffffu)
+            v[e] = j0 + e < mine.y && ((exist >> e) & 1u) ? v[e] : -INFINITY;
+        }
+        __syncthreads();  // buffer bf (keys, page ids, accumulator) is free
+        tc_fence_after();
+        if (warp == 0 && i + 2 < used) gather(i + 2);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = -INFINITY;
+      }
+      if (mine.x == b) {
+        if (vec && j0 + 32 <= p.pv.max_pages) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(out + j0 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (j0 + e < p.pv.max_pages) out[j0 + e] = v[e];
+        }
+      }
+      __syncwarp();
+    }
+    n += used;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+template <int kDim>
+cudaError_t launch_tile(const sa_paged_args &pa, const ScoreParams &p, cudaStream_t stream) {
+  CUtensorMap kmap;
+  if (!encode_rows(&kmap, p.k_mean, static_cast<uint64_t>(pa.n_pages) * pa.H_kv, kDim, 1)) return cudaErrorInvalidValue;
+  auto kern = score_tile_kernel<kDim>;
+  const size_t smem = ScoreSmem<kDim>::total + 1024;
+  static bool attr_done[64] = {};
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, attr_done);
+  if (e != cudaSuccess) return e;
+  return launch_ex(false, kern, dim3((pa.T + kTile - 1) / kTile, pa.H_kv), dim3(kTileThreads), smem, stream, 1, kmap, p);
 }
 
 }  // namespace
@@ -47,10 +384,27 @@ page_score_kernel(const PagedView pv, const uint16_t *q, const uint16_t *k_mean,
 cudaError_t launch_page_scores(const sa_paged_args &pa, const void *q, const void *k_mean, float *scores, int64_t ld,
                                int local, int32_t *row_seq, int32_t *row_pos, uint32_t *status, cudaStream_t stream) {
   if (pa.T == 0) return cudaSuccess;
-  const int per = kThreads / 32;
-  return launch_ex(false, page_score_kernel, dim3((pa.max_pages + per - 1) / per, pa.T, pa.H_kv), dim3(kThreads), 0,
-                   stream, 1, paged_view(pa), static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k_mean),
-                   scores, ld, pa.D, pa.scale, local, row_seq, row_pos, status);
+  const ScoreParams p{paged_view(pa),
+                      static_cast<const uint16_t *>(q),
+                      static_cast<const uint16_t *>(k_mean),
+                      scores,
+                      ld,
+                      pa.scale,
+                      local,
+                      row_seq,
+                      row_pos,
+                      status};
+  // a product pays once a tile of 128 tokens holds few sequences
+  if (pa.T >= 16 * static_cast<int64_t>(pa.B) || pa.T > 65535)
+    return pa.D == 128 ? launch_tile<128>(pa, p, stream) : launch_tile<64>(pa, p, stream);
+  // pages per CTA: the most that still give every SM two CTAs
+  int chunk = kMaxChunk;
+  const int groups = (pa.H_kv + kHeads - 1) / kHeads;
+  while (chunk > 16 && static_cast<int64_t>((pa.max_pages + chunk - 1) / chunk) * pa.T * groups < 2 * sm_count()) chunk /= 2;
+  const dim3 grid((pa.max_pages + chunk - 1) / chunk, pa.T, groups);
+  return pa.D == 128
+             ? launch_ex(false, score_token_kernel<128>, grid, dim3(kThreads), 0, stream, 1, p, chunk)
+             : launch_ex(false, score_token_kernel<64>, grid, dim3(kThreads), 0, stream, 1, p, chunk);
 }
 
 }  // namespace sa

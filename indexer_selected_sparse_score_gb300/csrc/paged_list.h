@@ -26,8 +26,6 @@ struct ListParams {
   uint32_t *status;
 };
 
-// 2-D tensor map over `rows` rows of `dim` bf16, boxes of 64 values x box_rows rows, 128-byte swizzle.
-bool encode_rows(CUtensorMap *m, const void *base, uint64_t rows, int dim, uint32_t box_rows);
 // Columns (padded heads) of a unit: 16, 32 or 64.
 int list_cols(const sa_paged_args &pa);
 size_t list_scratch(const sa_paged_args &pa, bool keep);
