@@ -130,7 +130,7 @@ cudaError_t launch_block_attn(const sa_paged_args &pa, const void *q, const int3
 cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int shared_pages, void *out, void *scratch,
                                uint32_t *status, cudaStream_t stream);
 // 2-D tensor map over `rows` rows of `dim` bf16, boxes of 64 values x box_rows
-// rows (1 for gathered loads), 128-byte swizzle.
+// rows, 128-byte swizzle.
 bool encode_rows(CUtensorMap *m, const void *base, uint64_t rows, int dim, uint32_t box_rows);
 size_t block_attn_scratch(const sa_paged_args &pa, int K, int local);
 size_t prefix_attn_scratch(const sa_paged_args &pa, int shared_pages);

@@ -12,8 +12,6 @@
 // With many tokens per sequence (a prefill chunk) it is a product of 128 tokens
 // with 128 pages at a time (tcgen05), bound by reading the queries and writing
 // the scores.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 
 #include "internal.h"
@@ -64,8 +62,8 @@ __device__ __forceinline__ void write_row_token(const ScoreParams &p, int64_t ro
 // ------------------------------------------------------- one token at a time
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 8;     // KV heads of a CTA
-constexpr int kMaxChunk = 256;
+constexpr int kHeads = 8;       // KV heads of a CTA
+constexpr int kPass = 16;       // 16-page tiles of one pass over the shared memory
 
 // D += A B, 16 x 8 x 16, bf16 inputs.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -77,82 +75,143 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// CTA (x, t, z): pages x * chunk .. of token t for KV heads 8 z .. 8 z + 7.  A
-// warp's item is 16 pages of one head: A rows are the pages, B columns 0-2 the
-// query's pieces.  The order of the dims within a product is free, so lane 4 g
-// + i holds 16-byte chunks i, i + 4, .. of rows g and g + 8 as they lie in
-// memory, two k-steps a chunk.
+// The 16-page tiles that the tokens see form one list, cut evenly over the CTAs
+// of x (four to an SM, all at once: tokens differ in length, and a second wave
+// would start its chain of dependent loads when the first has ended); z takes 8
+// KV heads.  A warp's item is a tile of one head: A rows are the pages, B
+// columns 0-2 the query's pieces.  The order of the dims within a product is
+// free, so lane 4 g + i holds 16-byte chunks i, i + 4, .. of rows g and g + 8
+// as they lie in memory, two k-steps a chunk.
 template <int kDim>
-__global__ void __launch_bounds__(kThreads)
-score_token_kernel(const ScoreParams p, int chunk) {
+__global__ void __launch_bounds__(kThreads, 4)
+score_token_kernel(const ScoreParams p) {
   constexpr int kChunks = kDim / 8, kLoads = kChunks / 4;  // of a row; a lane's loads of it
   __shared__ __align__(16) uint16_t qs[kHeads][3][kDim];
-  __shared__ float tile[kHeads * kMaxChunk];
-  __shared__ int page_s[kMaxChunk];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.y, h0 = blockIdx.z * kHeads, nh = min(kHeads, p.pv.H_kv - h0), G = p.pv.H / p.pv.H_kv;
-  const int j0 = blockIdx.x * chunk, nj = min(chunk, p.pv.max_pages - j0);
-  const bool report = tid == 0 && blockIdx.x == 0 && blockIdx.z == 0;
-  int b, pos;
-  const bool ok = load_paged_token(p.pv, t, p.status, report, b, pos);
-  if (p.row_seq && blockIdx.x == 0 && tid < nh) write_row_token(p, static_cast<int64_t>(t) * p.pv.H_kv + h0 + tid, ok, b, pos);
-  if (!ok) return;
-  const int vis = min(max(((pos + 1) >> p.pv.logP) - j0, 0), nj);
-  for (int j = tid; j < vis; j += kThreads) page_s[j] = load_page(p.pv, b, j0 + j, p.status, blockIdx.z == 0);
-  if (vis > 0 && tid < nh * kChunks) {
-    float a[8];
-    const int h = tid / kChunks, c = tid % kChunks;
-    sum_queries<kDim>(p, t, h0 + h, G, c, a);
-#pragma unroll
-    for (int piece = 0; piece < 3; ++piece) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
-        a[2 * e] -= __uint_as_float(w[e] << 16);
-        a[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+  __shared__ float tile[kHeads][16 * kPass];
+  __shared__ int page_s[16 * kPass];
+  __shared__ long long warp_s[kThreads / 32], start_off;
+  __shared__ int start_t;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  const int h0 = blockIdx.z * kHeads, nh = min(kHeads, p.pv.H_kv - h0), G = p.pv.H / p.pv.H_kv;
+  // complete pages a token sees (-1 for a token to skip)
+  auto seen = [&](int t, bool report, int &b) -> int {
+    int pos;
+    const bool ok = load_paged_token(p.pv, t, p.status, report, b, pos);
+    if (report && p.row_seq)
+      for (int h = 0; h < p.pv.H_kv; ++h) write_row_token(p, static_cast<int64_t>(t) * p.pv.H_kv + h, ok, b, pos);
+    return ok ? (pos + 1) >> p.pv.logP : -1;
+  };
+  const int per = (p.pv.T + kThreads - 1) / kThreads;
+  const int ta = min(tid * per, p.pv.T), tb = min(ta + per, p.pv.T);
+  long long own = 0, total;
+  int b;
+  for (int t = ta; t < tb; ++t) own += (seen(t, c == 0 && blockIdx.z == 0, b) + 15) >> 4;
+  long long before = block_prefix(own, warp_s, total);
+  const int cta = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1ll)));
+  const long long x0 = total * min(c, cta) / cta, x1 = total * min(c + 1, cta) / cta;
+  if (before <= x0 && x0 < before + own) {
+    for (int t = ta; t < tb; ++t) {
+      const int n = (seen(t, false, b) + 15) >> 4;
+      if (x0 < before + n) {
+        start_t = t;
+        start_off = before;
+        break;
       }
-      *reinterpret_cast<uint4 *>(&qs[h][piece][8 * c]) = make_uint4(w[0], w[1], w[2], w[3]);
+      before += n;
+    }
+  }
+  // columns past the pages a token sees
+  for (int t = c; t < p.pv.T; t += gridDim.x) {
+    const int vis = seen(t, false, b);
+    if (vis < 0) continue;
+    for (int h = warp; h < nh; h += kThreads / 32) {
+      float *row = p.scores + (static_cast<int64_t>(t) * p.pv.H_kv + h0 + h) * p.ld;
+      for (int j = vis + lane; j < p.pv.max_pages; j += 32) row[j] = -INFINITY;
     }
   }
   __syncthreads();
   const int g = lane >> 2, ti = lane & 3;
-  const int items = ((vis + 15) >> 4) * nh;
-  for (int it = warp; it < items; it += kThreads / 32) {
-    const int jt = it / nh, h = it - jt * nh;
-    uint4 x[2][kLoads];
-    bool bad[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int j = 16 * jt + g + 8 * r;
-      const int page = j < vis ? page_s[j] : -1;
-      bad[r] = page < 0;
-      const uint4 *src =
-          reinterpret_cast<const uint4 *>(p.k_mean + (static_cast<int64_t>(max(page, 0)) * p.pv.H_kv + h0 + h) * kDim);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) x[r][i] = bad[r] ? make_uint4(0, 0, 0, 0) : src[ti + 4 * i];
+  long long x = x0, base = start_off;
+  int t = start_t, summed = -1;
+  while (x < x1) {
+    const int vis = seen(t, false, b);
+    const int n = (vis + 15) >> 4;
+    if (n <= 0) {
+      ++t;
+      continue;
     }
-    float d[4] = {};
+    // tiles [a, e) of token t
+    const int a = static_cast<int>(x - base);
+    const int e = static_cast<int>(min(min(static_cast<long long>(n), x1 - base), static_cast<long long>(a) + kPass));
+    const int j0 = 16 * a, nj = min(16 * e, vis) - j0;
+    if (tid < nj) page_s[tid] = load_page(p.pv, b, j0 + tid, p.status, blockIdx.z == 0);
+    if (summed != t && tid < nh * kChunks) {
+      float s[8];
+      const int h = tid / kChunks, ch = tid % kChunks;
+      sum_queries<kDim>(p, t, h0 + h, G, ch, s);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      uint4 y = make_uint4(0, 0, 0, 0);
-      if (g < 3) y = *reinterpret_cast<const uint4 *>(&qs[h][g][8 * (ti + 4 * i)]);
-      mma_16816(d, x[0][i].x, x[1][i].x, x[0][i].y, x[1][i].y, y.x, y.y);
-      mma_16816(d, x[0][i].z, x[1][i].z, x[0][i].w, x[1][i].w, y.z, y.w);
+      for (int piece = 0; piece < 3; ++piece) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
+          s[2 * i] -= __uint_as_float(w[i] << 16);
+          s[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint4 *>(&qs[h][piece][8 * ch]) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    // columns 0 and 1 sit in lane 4 g, column 2 in lane 4 g + 1
-    const float e0 = __shfl_down_sync(0xffffffffu, d[0], 1), e1 = __shfl_down_sync(0xffffffffu, d[2], 1);
-    if (ti == 0) {
-      const float s0 = (d[0] + (d[1] + e0)) * p.scale, s1 = (d[2] + (d[3] + e1)) * p.scale;
-      float *row = tile + h * chunk + 16 * jt + g;
-      if (16 * jt + g < vis) row[0] = bad[0] ? -INFINITY : s0;
-      if (16 * jt + g + 8 < vis) row[8] = bad[1] ? -INFINITY : s1;
+    summed = t;
+    __syncthreads();
+    const int items = (e - a) * nh;
+    constexpr int kAtOnce = 2;  // items whose rows a warp has in flight
+    for (int it0 = warp * kAtOnce; it0 < items; it0 += kThreads / 32 * kAtOnce) {
+      uint4 v[kAtOnce][2][kLoads];
+      bool bad[kAtOnce][2];
+#pragma unroll
+      for (int m = 0; m < kAtOnce; ++m) {
+        const int it = it0 + m, jt = it / nh, h = it - jt * nh;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int j = 16 * jt + g + 8 * r;
+          const int page = it < items && j < nj ? page_s[j] : -1;
+          bad[m][r] = page < 0;
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              p.k_mean + (static_cast<int64_t>(max(page, 0)) * p.pv.H_kv + h0 + h) * kDim);
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) v[m][r][i] = bad[m][r] ? make_uint4(0, 0, 0, 0) : src[ti + 4 * i];
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < kAtOnce; ++m) {
+        const int it = it0 + m, jt = it / nh, h = it - jt * nh;
+        float d[4] = {};
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          uint4 y = make_uint4(0, 0, 0, 0);
+          if (g < 3 && it < items) y = *reinterpret_cast<const uint4 *>(&qs[h][g][8 * (ti + 4 * i)]);
+          mma_16816(d, v[m][0][i].x, v[m][1][i].x, v[m][0][i].y, v[m][1][i].y, y.x, y.y);
+          mma_16816(d, v[m][0][i].z, v[m][1][i].z, v[m][0][i].w, v[m][1][i].w, y.z, y.w);
+        }
+        // columns 0 and 1 sit in lane 4 g, column 2 in lane 4 g + 1
+        const float e0 = __shfl_down_sync(0xffffffffu, d[0], 1), e1 = __shfl_down_sync(0xffffffffu, d[2], 1);
+        if (ti == 0 && it < items) {
+          tile[h][16 * jt + g] = bad[m][0] ? -INFINITY : (d[0] + (d[1] + e0)) * p.scale;
+          tile[h][16 * jt + g + 8] = bad[m][1] ? -INFINITY : (d[2] + (d[3] + e1)) * p.scale;
+        }
+      }
     }
-  }
-  __syncthreads();
-  for (int h = warp; h < nh; h += kThreads / 32) {
-    float *row = p.scores + (static_cast<int64_t>(t) * p.pv.H_kv + h0 + h) * p.ld + j0;
-    for (int j = lane; j < nj; j += 32) row[j] = j < vis ? tile[h * chunk + j] : -INFINITY;
+    __syncthreads();
+    for (int h = warp; h < nh; h += kThreads / 32) {
+      float *row = p.scores + (static_cast<int64_t>(t) * p.pv.H_kv + h0 + h) * p.ld + j0;
+      for (int j = lane; j < nj; j += 32) row[j] = tile[h][j];
+    }
+    __syncthreads();  // the next pass writes tile and page_s
+    x = base + e;
+    if (e == n) {
+      base += n;
+      ++t;
+    }
   }
 }
 
@@ -168,10 +227,11 @@ struct ScoreSmem {
   static constexpr uint32_t kRows = kBlock * (kDim / 64);
   static constexpr size_t q = 0;                           // [piece][D / 64][128 tokens][128 B]
   static constexpr size_t k = kPieces * kRows;             // [2][D / 64][128 pages][128 B]
-  static constexpr size_t pages = k + 2 * kRows;           // [2][128] page ids of a block
+  static constexpr size_t stage = k + 2 * kRows;           // [16 warps][32][16] f32
+  static constexpr size_t pages = stage + 16 * 2048;           // [2][128] page ids of a block
   static constexpr size_t tok = pages + 2 * kTile * 4;     // [128] int2: sequence (-1: skip), visible pages
   static constexpr size_t bars = tok + kTile * 8;
-  static constexpr size_t misc = bars + 4 * 8;
+  static constexpr size_t misc = bars + 2 * 8;
   static constexpr size_t total = misc + 32;
   static_assert(total + 1024 <= 232448, "shared memory budget");
 };
@@ -182,23 +242,22 @@ struct ScoreSmem {
 // one's scores are written.
 template <int kDim>
 __global__ void __launch_bounds__(kTileThreads, 1)
-score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p) {
+score_tile_kernel(const ScoreParams p) {
   using L = ScoreSmem<kDim>;
-  constexpr int kB = kDim / 64, kChunks = kDim / 8;
+  constexpr int kChunks = kDim / 8;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *qs = smem + L::q, *ks = smem + L::k;
   int *page_s = reinterpret_cast<int *>(smem + L::pages);
   int2 *tok_s = reinterpret_cast<int2 *>(smem + L::tok);
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bars), *ready = full + 2;
+  uint64_t *ready = reinterpret_cast<uint64_t *>(smem + L::bars);
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
   int *seq_s = reinterpret_cast<int *>(smem + L::misc + 8);  // sequence and page bound of the pass
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = blockIdx.x * kTile, nt = min(kTile, p.pv.T - t0), h = blockIdx.y, G = p.pv.H / p.pv.H_kv;
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ready[i], 1);
     fence_barrier_init();
-    prefetch_tmap(&kmap);
   }
   if (warp == 0) {
     tmem_alloc(tmem_base_s, 256);
@@ -213,25 +272,6 @@ score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p)
     }
     tok_s[tid] = make_int2(ok ? b : -1, ok ? (pos + 1) >> p.pv.logP : 0);
   }
-  // summed queries, split into bf16 pieces (round to nearest: each piece takes
-  // at least 8 bits of what is left)
-  for (int i = tid; i < kTile * kChunks; i += kTileThreads) {
-    const int r = i / kChunks, ch = i % kChunks;
-    float a[8] = {};
-    if (r < nt) sum_queries<kDim>(p, t0 + r, h, G, ch, a);
-    const uint32_t off = (ch >> 3) * L::kBlock + sw128_offset(r, 16u * (ch & 7));
-#pragma unroll
-    for (int piece = 0; piece < kPieces; ++piece) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
-        a[2 * e] -= __uint_as_float(w[e] << 16);
-        a[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
-      }
-      *reinterpret_cast<uint4 *>(qs + piece * L::kRows + off) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
@@ -241,9 +281,34 @@ score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p)
   const int2 mine = tok_s[row];
   const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
   float *out = p.scores + (static_cast<int64_t>(t0 + row) * p.pv.H_kv + h) * p.ld;
+  float4 *stage = reinterpret_cast<float4 *>(smem + L::stage + warp * 2048);
   const bool vec = (p.ld & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scores) & 15) == 0;
   const int nblk = (p.pv.max_pages + kTile - 1) / kTile;
   int n = 0;  // blocks issued so far (of all passes)
+  // the summed queries, split into bf16 pieces (round to nearest: each piece
+  // takes at least 8 bits of what is left), while the first mean keys come in
+  auto sum_all = [&]() {
+    for (int i = tid; i < kTile * kChunks; i += kTileThreads) {
+      const int r = i / kChunks, ch = i % kChunks;
+      float a[8] = {};
+      if (r < nt) sum_queries<kDim>(p, t0 + r, h, G, ch, a);
+      const uint32_t off = (ch >> 3) * L::kBlock + sw128_offset(r, 16u * (ch & 7));
+#pragma unroll
+      for (int piece = 0; piece < kPieces; ++piece) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+          a[2 * e] -= __uint_as_float(w[e] << 16);
+          a[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint4 *>(qs + piece * L::kRows + off) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    fence_proxy_async();
+    __syncthreads();
+  };
+  bool summed = false;
   int prev = -1;  // sequences are taken in rising order
   while (true) {
     if (warp == 0) {
@@ -268,32 +333,30 @@ score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p)
     if (b == INT32_MAX) break;
     __syncthreads();  // everyone has read the pass before the next one is written
     prev = b;
-    // block i of the pass (block n + i of all) into buffer (n + i) & 1: mean
-    // keys by gather, four pages a copy; pages that do not exist or lie past
-    // the tokens' sight read row 0 and are masked when written
+    // block i of the pass (block n + i of all) into buffer (n + i) & 1; pages
+    // that do not exist or lie past the tokens' sight read row 0 and are masked
+    // when written
+    // Row r of the block is copied by threads 4 r .. 4 r + 3, 16 bytes at a
+    // time into the swizzle (gathered TMA loads take 70 ns each to issue).
     auto gather = [&](int i) {
-      const int bf = (n + i) & 1;
-      int rows[4];
+      const int bf = (n + i) & 1, r = tid >> 2, j = i * kTile + r;
+      const int page = j < seen ? load_page(p.pv, b, j, p.status, h == 0) : -1;
+      if ((tid & 3) == 0) page_s[bf * kTile + r] = page;
+      const uint16_t *src = p.k_mean + (static_cast<int64_t>(max(page, 0)) * p.pv.H_kv + h) * kDim;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = i * kTile + 4 * lane + e;
-        const int page = j < seen ? load_page(p.pv, b, j, p.status, h == 0) : -1;
-        page_s[bf * kTile + 4 * lane + e] = page;
-        rows[e] = page >= 0 ? page * p.pv.H_kv + h : 0;
+      for (int e = 0; e < kChunks / 4; ++e) {
+        const int ch = (tid & 3) + 4 * e;
+        cp_async16_plain(ks + bf * L::kRows + (ch >> 3) * L::kBlock + sw128_offset(r, 16u * (ch & 7)), src + 8 * ch);
       }
-      if (lane == 0) mbar_expect_tx(&full[bf], L::kRows);
-      __syncwarp();
-#pragma unroll
-      for (int kb = 0; kb < kB; ++kb)
-        gather_rows4(ks + bf * L::kRows + kb * L::kBlock + lane * 512, &kmap, &full[bf], 64 * kb, rows[0], rows[1],
-                     rows[2], rows[3]);
+    };
+    // The copies of every thread have landed and are visible to the tensor core.
+    auto landed = [&]() {
+      cp_async_wait_all();
+      fence_proxy_async();
+      __syncthreads();
     };
     auto multiply = [&](int i) {
-      const int u = n + i, bf = u & 1;
-      if (!mbar_wait_warp(&full[bf], (u >> 1) & 1)) {
-        if (lane == 0) raise_flag(p.status, kFlagTimeout);
-        return;
-      }
+      const int bf = (n + i) & 1;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t db = desc_sw128_kmajor(smem_u32(ks + bf * L::kRows));
@@ -310,9 +373,14 @@ score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p)
       }
       __syncwarp();
     };
-    if (warp == 0 && used > 0) {
-      gather(0);
-      multiply(0);
+    if (used > 0) gather(0);
+    if (!summed) {
+      sum_all();
+      summed = true;
+    }
+    if (used > 0) {
+      landed();
+      if (warp == 0) multiply(0);
       if (used > 1) gather(1);
     }
     for (int i = 0; i < nblk; ++i) {
@@ -321,8 +389,6 @@ score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p)
       float v[32];
       const int c0 = 32 * (warp >> 2), j0 = i * kTile + c0;
       if (live) {
-        // the other accumulator was read out before the last barrier
-        if (warp == 0 && i + 1 < used) multiply(i + 1);
         if (!mbar_wait_warp(&ready[bf], (u >> 1) & 1) && lane == 0) raise_flag(p.status, kFlagTimeout);
         tc_fence_after();
         tmem_load(tmem + lanes + kTile * bf + c0, reinterpret_cast<uint32_t(&)[32]>(v));
@@ -337,23 +403,39 @@ score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p)
           if (!all || exist != 0xffffffffu)
             v[e] = j0 + e < mine.y && ((exist >> e) & 1u) ? v[e] : -INFINITY;
         }
-        __syncthreads();  // buffer bf (keys, page ids, accumulator) is free
-        tc_fence_after();
-        if (warp == 0 && i + 2 < used) gather(i + 2);
+        landed();  // block i + 1 is in; buffer bf (keys, page ids, accumulator) is free
+        if (warp == 0 && i + 1 < used) multiply(i + 1);
+        if (i + 2 < used) gather(i + 2);
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = -INFINITY;
       }
-      if (mine.x == b) {
-        if (vec && j0 + 32 <= p.pv.max_pages) {
+      // 32 rows x 32 columns of the warp, transposed through shared memory 16
+      // columns at a time so that a store covers 64 contiguous bytes of each of
+      // eight rows
+      if (vec && j0 + 32 <= p.pv.max_pages) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(out + j0 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        } else {
+        for (int half = 0; half < 2; ++half) {
+          __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (j0 + e < p.pv.max_pages) out[j0 + e] = v[e];
+          for (int e = 0; e < 4; ++e)
+            stage[4 * lane + (e ^ ((lane >> 1) & 3))] =
+                make_float4(v[16 * half + 4 * e], v[16 * half + 4 * e + 1], v[16 * half + 4 * e + 2], v[16 * half + 4 * e + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 8 * e + (lane >> 2), ch = lane & 3;
+            const float4 x = stage[4 * r + (ch ^ ((r >> 1) & 3))];
+            const int row_r = 32 * (warp & 3) + r;
+            if (tok_s[row_r].x == b)
+              *reinterpret_cast<float4 *>(p.scores + (static_cast<int64_t>(t0 + row_r) * p.pv.H_kv + h) * p.ld + j0 +
+                                          16 * half + 4 * ch) = x;
+          }
         }
+      } else if (mine.x == b) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (j0 + e < p.pv.max_pages) out[j0 + e] = v[e];
       }
       __syncwarp();
     }
@@ -369,14 +451,12 @@ score_tile_kernel(const __grid_constant__ CUtensorMap kmap, const ScoreParams p)
 
 template <int kDim>
 cudaError_t launch_tile(const sa_paged_args &pa, const ScoreParams &p, cudaStream_t stream) {
-  CUtensorMap kmap;
-  if (!encode_rows(&kmap, p.k_mean, static_cast<uint64_t>(pa.n_pages) * pa.H_kv, kDim, 1)) return cudaErrorInvalidValue;
   auto kern = score_tile_kernel<kDim>;
   const size_t smem = ScoreSmem<kDim>::total + 1024;
   static bool attr_done[64] = {};
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_ex(false, kern, dim3((pa.T + kTile - 1) / kTile, pa.H_kv), dim3(kTileThreads), smem, stream, 1, kmap, p);
+  return launch_ex(false, kern, dim3((pa.T + kTile - 1) / kTile, pa.H_kv), dim3(kTileThreads), smem, stream, 1, p);
 }
 
 }  // namespace
@@ -395,16 +475,13 @@ cudaError_t launch_page_scores(const sa_paged_args &pa, const void *q, const voi
                       row_pos,
                       status};
   // a product pays once a tile of 128 tokens holds few sequences
-  if (pa.T >= 16 * static_cast<int64_t>(pa.B) || pa.T > 65535)
+  if (pa.T >= 16 * static_cast<int64_t>(pa.B))
     return pa.D == 128 ? launch_tile<128>(pa, p, stream) : launch_tile<64>(pa, p, stream);
-  // pages per CTA: the most that still give every SM two CTAs
-  int chunk = kMaxChunk;
   const int groups = (pa.H_kv + kHeads - 1) / kHeads;
-  while (chunk > 16 && static_cast<int64_t>((pa.max_pages + chunk - 1) / chunk) * pa.T * groups < 2 * sm_count()) chunk /= 2;
-  const dim3 grid((pa.max_pages + chunk - 1) / chunk, pa.T, groups);
-  return pa.D == 128
-             ? launch_ex(false, score_token_kernel<128>, grid, dim3(kThreads), 0, stream, 1, p, chunk)
-             : launch_ex(false, score_token_kernel<64>, grid, dim3(kThreads), 0, stream, 1, p, chunk);
+  const int64_t most = static_cast<int64_t>(pa.T) * ((pa.max_pages + 15) / 16);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, std::max(4 * sm_count() / groups, 1))), 1, groups);
+  return pa.D == 128 ? launch_ex(false, score_token_kernel<128>, grid, dim3(kThreads), 0, stream, 1, p)
+                     : launch_ex(false, score_token_kernel<64>, grid, dim3(kThreads), 0, stream, 1, p);
 }
 
 }  // namespace sa

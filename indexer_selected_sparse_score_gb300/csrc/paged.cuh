@@ -49,4 +49,25 @@ __device__ __forceinline__ int load_page(const PagedView &v, int b, int j, uint3
   return -1;
 }
 
+// Sum of `v` over the threads before this one, and over the block (`warp_s`:
+// one slot per warp).  Every thread of the block calls it.
+__device__ __forceinline__ long long block_prefix(long long v, long long *warp_s, long long &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x + 31) >> 5;
+  long long s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += up;
+  }
+  if (lane == 31) warp_s[warp] = s;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += warp_s[w];
+    total += warp_s[w];
+  }
+  return before + s - v;
+}
+
 }  // namespace sa

@@ -12,9 +12,9 @@
 //
 // Traffic: every row is read once and written once (2 T (H + 2 H_kv) D values),
 // bound by HBM for a prefill and by latency for a decode step.  One CTA per
-// token: half of it tables the D / 2 rotations in shared memory while every
-// thread already holds its first rows' loads, then 32-byte units (two 16-byte
-// chunks, the two halves of their pairs) stream through registers.
+// token: every thread issues its rows' loads, then a part of the block finds
+// the token's page and tables the rotations in shared memory, and 32-byte units
+// (two 16-byte chunks, the two halves of their pairs) leave through registers.
 #include <algorithm>
 #include <cmath>
 
@@ -75,105 +75,130 @@ __device__ __forceinline__ void rotate_halves(uint4 &x, uint4 &y, const float2 *
   y = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
   __shared__ float2 cs[kMaxPairs];
   pdl_trigger();
   const int t = blockIdx.x;
-  int b, pos;
-  if (!load_paged_token(p.pv, t, p.status, threadIdx.x == 0, b, pos)) return;  // the whole CTA alike
-  const int page = load_page(p.pv, b, pos >> p.pv.logP, p.status, threadIdx.x == 0);
-  const int slot = pos & (p.pv.P - 1);
   const int upr = p.D >> 4;                 // 32-byte units per row
   const int kept = (p.D - p.dim) >> 4;      // units before the rotated span
   const int span = p.dim >> 3;              // chunks of the rotated span
+  const int first = (p.D >> 3) - span;      // first rotated chunk
   const int units = (p.q_heads + 2 * p.pv.H_kv) * upr;
+  // chunks of unit u within its row: two neighbours, or the two halves of
+  // eight pairs
+  auto chunks = [&](int u, int &c0, int &c1) {
+    const int i = u % upr, j = i - kept;
+    const bool half = p.halves && j >= 0;
+    c0 = half ? first + j : 2 * i;
+    c1 = half ? c0 + (span >> 1) : 2 * i + 1;
+  };
+  constexpr int kUnits = 3;  // units a thread has in flight (2.5 at 64 + 2 x 8 heads of dim 128)
+  bool ok = false;
+  int page = -1, slot = 0;
   bool tabled = false;
-  for (int u0 = threadIdx.x; u0 - static_cast<int>(threadIdx.x) < units; u0 += 4 * kThreads) {
-    uint4 x[4], y[4];
-    int row[4], c0[4], c1[4];
+  for (int base = 0; base < units; base += kUnits * kThreads) {
+    // the rows' loads need no more than t: they go out before the token's
+    // position and page are known
+    uint4 x[kUnits], y[kUnits];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int u = u0 + e * kThreads;
-      row[e] = u < units ? u / upr : -1;
-      const int i = u % upr, j = i - kept;
-      const bool half = p.halves && j >= 0;
-      c0[e] = half ? (p.D >> 3) - span + j : 2 * i;
-      c1[e] = half ? c0[e] + (span >> 1) : 2 * i + 1;
-      if (row[e] < 0) continue;
-      const int h = row[e] - p.q_heads;
-      const uint16_t *src = h < 0             ? p.q + t * p.q_stride + static_cast<int64_t>(row[e]) * p.D
+    for (int e = 0; e < kUnits; ++e) {
+      const int u = base + e * kThreads + threadIdx.x;
+      if (u >= units) continue;
+      int c0, c1;
+      chunks(u, c0, c1);
+      const int row = u / upr, h = row - p.q_heads;
+      const uint16_t *src = h < 0           ? p.q + t * p.q_stride + static_cast<int64_t>(row) * p.D
                             : h < p.pv.H_kv ? p.k + t * p.k_stride + static_cast<int64_t>(h) * p.D
                                             : p.v + t * p.v_stride + static_cast<int64_t>(h - p.pv.H_kv) * p.D;
-      x[e] = *reinterpret_cast<const uint4 *>(src + 8 * c0[e]);
-      y[e] = *reinterpret_cast<const uint4 *>(src + 8 * c1[e]);
+      x[e] = *reinterpret_cast<const uint4 *>(src + 8 * c0);
+      y[e] = *reinterpret_cast<const uint4 *>(src + 8 * c1);
     }
     if (!tabled) {
-      if (threadIdx.x < p.dim / 2) {
-        const uint64_t ph = static_cast<uint64_t>(pos) * turns.f[threadIdx.x] + (uint64_t{1} << 31);
-        float sn, c;
-        sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &sn, &c);
-        cs[threadIdx.x] = make_float2(c, sn);
+      int b, pos;
+      ok = load_paged_token(p.pv, t, p.status, threadIdx.x == 0, b, pos);
+      if (ok) {
+        page = load_page(p.pv, b, pos >> p.pv.logP, p.status, threadIdx.x == 0);
+        slot = pos & (p.pv.P - 1);
+        if (threadIdx.x < p.dim / 2) {
+          const uint64_t ph = static_cast<uint64_t>(pos) * turns.f[threadIdx.x] + (uint64_t{1} << 31);
+          float sn, c;
+          sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &sn, &c);
+          cs[threadIdx.x] = make_float2(c, sn);
+        }
       }
       __syncthreads();
       tabled = true;
     }
+    if (!ok) return;  // the whole CTA alike
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (row[e] < 0) continue;
-      const int h = row[e] - p.q_heads;
+    for (int e = 0; e < kUnits; ++e) {
+      const int u = base + e * kThreads + threadIdx.x;
+      if (u >= units) continue;
+      int c0, c1;
+      chunks(u, c0, c1);
+      const int row = u / upr, h = row - p.q_heads;
       uint16_t *dst;
       if (h < 0) {
-        dst = p.q_out + (static_cast<int64_t>(t) * p.pv.H + row[e]) * p.D;
+        dst = p.q_out + (static_cast<int64_t>(t) * p.pv.H + row) * p.D;
       } else {
         if (page < 0) continue;
         const int hk = h < p.pv.H_kv ? h : h - p.pv.H_kv;
         dst = (h < p.pv.H_kv ? p.K : p.V) +
               ((static_cast<int64_t>(page) * p.pv.H_kv + hk) * p.pv.P + slot) * p.D;
       }
-      const int first = (p.D >> 3) - span;  // first rotated chunk
-      if (h < p.pv.H_kv && c0[e] >= first) {
+      if (h < p.pv.H_kv && c0 >= first) {
         if (p.halves) {
-          rotate_halves(x[e], y[e], cs + 8 * (c0[e] - first));
+          rotate_halves(x[e], y[e], cs + 8 * (c0 - first));
         } else {
-          x[e] = rotate_adjacent(x[e], cs + 4 * (c0[e] - first));
-          y[e] = rotate_adjacent(y[e], cs + 4 * (c1[e] - first));
+          x[e] = rotate_adjacent(x[e], cs + 4 * (c0 - first));
+          y[e] = rotate_adjacent(y[e], cs + 4 * (c1 - first));
         }
       }
-      *reinterpret_cast<uint4 *>(dst + 8 * c0[e]) = x[e];
-      *reinterpret_cast<uint4 *>(dst + 8 * c1[e]) = y[e];
+      *reinterpret_cast<uint4 *>(dst + 8 * c0) = x[e];
+      *reinterpret_cast<uint4 *>(dst + 8 * c1) = y[e];
     }
   }
 }
 
 // Mean of the key rows of every page whose last position is among the tokens.
-// CTA (x, h): tokens x * per .. + per - 1, KV head h.  It runs after the append
-// has written every row, so a page may fill from tokens in any order.
+// CTA (x, h): tokens x * per .. + per - 1 (at most kThreads), KV head h.  It
+// runs after the append has written every row, so a page may fill from tokens
+// in any order; which pages those are is found before the wait.
 __global__ void __launch_bounds__(kThreads)
 page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int D, int per) {
   __shared__ float part[kThreads / 8 * 64];
+  __shared__ int pages[kThreads], n_s;
+  if (threadIdx.x == 0) n_s = 0;
+  __syncthreads();
+  const int own = blockIdx.x * per + threadIdx.x;
+  if (threadIdx.x < per && own < pv.T) {
+    int b, pos;
+    if (load_paged_token(pv, own, nullptr, false, b, pos) && ((pos + 1) & (pv.P - 1)) == 0) {
+      const int page = load_page(pv, b, pos >> pv.logP, nullptr, false);
+      if (page >= 0) pages[atomicAdd(&n_s, 1)] = page;
+    }
+  }
+  __syncthreads();
   pdl_wait();
   const int h = blockIdx.y, cpr = D >> 3;          // 16-byte chunks per row
   const int c = threadIdx.x % cpr, r0 = threadIdx.x / cpr, rows = kThreads / cpr;
-  const int t0 = blockIdx.x * per, t1 = min(t0 + per, pv.T);
-  for (int t = t0; t < t1; ++t) {
-    int b, pos;
-    if (!load_paged_token(pv, t, nullptr, false, b, pos) || ((pos + 1) & (pv.P - 1))) continue;
-    const int page = load_page(pv, b, pos >> pv.logP, nullptr, false);
-    if (page < 0) continue;
-    const int64_t tile = static_cast<int64_t>(page) * pv.H_kv + h;
+  for (int i = 0; i < n_s; ++i) {
+    const int64_t tile = static_cast<int64_t>(pages[i]) * pv.H_kv + h;
     float s[8] = {};
+    const uint4 *src = reinterpret_cast<const uint4 *>(K + tile * pv.P * D) + c;
+#pragma unroll 8
     for (int r = r0; r < pv.P; r += rows) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(K + (tile * pv.P + r) * D + 8 * c);
+      const uint4 x = src[r * cpr];
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[2 * i] += lo_f(w[i]);
-        s[2 * i + 1] += hi_f(w[i]);
+      for (int e = 0; e < 4; ++e) {
+        s[2 * e] += lo_f(w[e]);
+        s[2 * e + 1] += hi_f(w[e]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[r0 * D + 8 * c + i] = s[i];
+    for (int e = 0; e < 8; ++e) part[r0 * D + 8 * c + e] = s[e];
     __syncthreads();
     if (threadIdx.x < D) {
       float m = 0.f;
@@ -218,7 +243,8 @@ cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t 
   // one CTA per token and head while they are few; more tokens per CTA once
   // the grid would exceed eight CTAs per SM (most tokens end no page)
   const int64_t most = static_cast<int64_t>(sm_count()) * 8;
-  const int per = static_cast<int>(std::max<int64_t>(1, static_cast<int64_t>(pa.T) * pa.H_kv / most));
+  const int per = static_cast<int>(
+      std::min<int64_t>(std::max<int64_t>(1, static_cast<int64_t>(pa.T) * pa.H_kv / most), kThreads));
   return launch_ex(true, page_mean_kernel, dim3((pa.T + per - 1) / per, pa.H_kv), dim3(kThreads), 0, stream, 1, p.pv,
                    static_cast<const uint16_t *>(pa.K), static_cast<uint16_t *>(k_mean), pa.D, per);
 }

@@ -62,15 +62,9 @@ __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
-// Gathered load of four rows (128 bytes each from column x) of a tensor map with
-// a one-row box.
-__device__ __forceinline__ void gather_rows4(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y0, int y1,
-                                             int y2, int y3) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
-      : "memory");
+// 16-byte global -> shared copy through L2 (cp_async_wait_all waits for it).
+__device__ __forceinline__ void cp_async16_plain(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 // MN-major 128-byte-swizzled operand: rows = K (8-row atoms 1024 B apart), 64 M
