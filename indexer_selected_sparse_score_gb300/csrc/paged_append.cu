@@ -24,7 +24,8 @@
 namespace sa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 320;     // append: two units a thread at 64 + 2 x 8 heads of dim 128
+constexpr int kMeanThreads = 256;
 constexpr int kMaxPairs = 64;
 
 struct Turns {
@@ -75,7 +76,7 @@ __device__ __forceinline__ void rotate_halves(uint4 &x, uint4 &y, const float2 *
   y = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 5)
 paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
   __shared__ float2 cs[kMaxPairs];
   pdl_trigger();
@@ -93,7 +94,9 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
     c0 = half ? first + j : 2 * i;
     c1 = half ? c0 + (span >> 1) : 2 * i + 1;
   };
-  constexpr int kUnits = 3;  // units a thread has in flight (2.5 at 64 + 2 x 8 heads of dim 128)
+  // units a thread has in flight (3 of 256 threads and 1 of 640 measured 2 and
+  // 12 % slower on a prefill)
+  constexpr int kUnits = 2;
   bool ok = false;
   int page = -1, slot = 0;
   bool tabled = false;
@@ -162,13 +165,15 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
 }
 
 // Mean of the key rows of every page whose last position is among the tokens.
-// CTA (x, h): tokens x * per .. + per - 1 (at most kThreads), KV head h.  It
-// runs after the append has written every row, so a page may fill from tokens
-// in any order; which pages those are is found before the wait.
-__global__ void __launch_bounds__(kThreads)
-page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int D, int per) {
-  __shared__ float part[kThreads / 8 * 64];
-  __shared__ int pages[kThreads], n_s;
+// CTA x: tokens x * per .. + per - 1 (at most kMeanThreads); a warp takes a
+// (page, KV head).  It runs after the append has written every row, so a page
+// may fill from tokens in any order; which pages those are is found before the
+// wait.
+template <int kDim>
+__global__ void __launch_bounds__(kMeanThreads)
+page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int per) {
+  constexpr int kLanes = kDim / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a load
+  __shared__ int pages[kMeanThreads], n_s;
   if (threadIdx.x == 0) n_s = 0;
   __syncthreads();
   const int own = blockIdx.x * per + threadIdx.x;
@@ -181,15 +186,15 @@ page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int D,
   }
   __syncthreads();
   pdl_wait();
-  const int h = blockIdx.y, cpr = D >> 3;          // 16-byte chunks per row
-  const int c = threadIdx.x % cpr, r0 = threadIdx.x / cpr, rows = kThreads / cpr;
-  for (int i = 0; i < n_s; ++i) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes;
+  for (int it = warp; it < n_s * pv.H_kv; it += kMeanThreads / 32) {
+    const int i = it / pv.H_kv, h = it - i * pv.H_kv;
     const int64_t tile = static_cast<int64_t>(pages[i]) * pv.H_kv + h;
+    const uint4 *src = reinterpret_cast<const uint4 *>(K + tile * pv.P * kDim) + lane;
     float s[8] = {};
-    const uint4 *src = reinterpret_cast<const uint4 *>(K + tile * pv.P * D) + c;
 #pragma unroll 8
-    for (int r = r0; r < pv.P; r += rows) {
-      const uint4 x = src[r * cpr];
+    for (int r = 0; r < pv.P; r += kRows) {
+      const uint4 x = src[r * kLanes];
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -198,15 +203,15 @@ page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int D,
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part[r0 * D + 8 * c + e] = s[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float m = 0.f;
-      for (int r = 0; r < rows; ++r) m += part[r * D + threadIdx.x];
-      const __nv_bfloat16 o = __float2bfloat16_rn(m / static_cast<float>(pv.P));
-      k_mean[tile * D + threadIdx.x] = *reinterpret_cast<const uint16_t *>(&o);
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) s[e] += __shfl_xor_sync(0xffffffffu, s[e], o);
+    if (lane < kLanes) {
+      const float f = 1.f / static_cast<float>(pv.P);  // exact: P is a power of two
+      *reinterpret_cast<uint4 *>(k_mean + tile * kDim + 8 * c) =
+          make_uint4(pack_bf16(s[0] * f, s[1] * f), pack_bf16(s[2] * f, s[3] * f), pack_bf16(s[4] * f, s[5] * f),
+                     pack_bf16(s[6] * f, s[7] * f));
     }
-    __syncthreads();
   }
 }
 
@@ -240,13 +245,14 @@ cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t 
   }
   cudaError_t e = launch_ex(false, paged_append_kernel, dim3(pa.T), dim3(kThreads), 0, stream, 1, p, turns);
   if (e != cudaSuccess || !k_mean) return e;
-  // one CTA per token and head while they are few; more tokens per CTA once
-  // the grid would exceed eight CTAs per SM (most tokens end no page)
-  const int64_t most = static_cast<int64_t>(sm_count()) * 8;
-  const int per = static_cast<int>(
-      std::min<int64_t>(std::max<int64_t>(1, static_cast<int64_t>(pa.T) * pa.H_kv / most), kThreads));
-  return launch_ex(true, page_mean_kernel, dim3((pa.T + per - 1) / per, pa.H_kv), dim3(kThreads), 0, stream, 1, p.pv,
-                   static_cast<const uint16_t *>(pa.K), static_cast<uint16_t *>(k_mean), pa.D, per);
+  // one CTA per token while they are few, two CTAs per SM for more (most
+  // tokens end no page)
+  const int per = std::min(std::max(1, pa.T / (2 * sm_count())), kMeanThreads);
+  const dim3 grid((pa.T + per - 1) / per);
+  return pa.D == 128 ? launch_ex(true, page_mean_kernel<128>, grid, dim3(kMeanThreads), 0, stream, 1, p.pv,
+                                 static_cast<const uint16_t *>(pa.K), static_cast<uint16_t *>(k_mean), per)
+                     : launch_ex(true, page_mean_kernel<64>, grid, dim3(kMeanThreads), 0, stream, 1, p.pv,
+                                 static_cast<const uint16_t *>(pa.K), static_cast<uint16_t *>(k_mean), per);
 }
 
 }  // namespace sa

@@ -11,12 +11,10 @@
 //   P           bf16, written over S in tensor memory (the A operand of P V)
 //   O += P V    M = 128 rows, N = D, K = 128 keys, V read MN-major as it landed
 // A CTA holds two row tiles (A, B: 256 rows) against the same K and V tiles,
-// each with its own softmax warpgroup and its own issuing warp, so one tile's
-// products run while the other's weights are computed.  One pass per tile: the
-// weights are taken against a reference set by the piece's first tile and kept
-// in registers until a vote has shown that no logit passes it by 2^8; then they
-// are stored (else S, still in tensor memory, is read again against the raised
-// reference and O is rescaled).  Weights are rounded to bf16 for the product,
+// each with its own softmax warpgroup and its own issuing warp; the issuers take
+// turns, so one tile's products run while the other's weights are computed.  A row's logits are taken
+// relative to a reference set by the piece's first tile; only when a vote of the
+// warp finds one that passes it by 2^8 is it raised and O rescaled.  Weights are rounded to bf16 for the product,
 // logits, statistics and O are fp32.
 //
 // Work: (KV head, 256 rows) items x key tiles form one list cut evenly over one
@@ -45,6 +43,10 @@ constexpr int kWarpMma = 8;     // and 9: the issuers of row tiles A and B
 constexpr int kWarpLoad = 10;   // (warp 11 only joins the block barriers)
 constexpr int kSlots = 5;       // ring of K and V tiles: K(0), V(0), K(1), ...
 constexpr int kMasks = 8;
+// Registers per thread: built for 168 (384 threads); the two softmax warpgroups
+// raise their limit and the third lowers its own, 2 * 208 + 88 <= 3 * 168.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "register split exceeds the launch allocation");
 constexpr float kLazy = 8.f, kHead = 20.f;  // as in paged_attn_list.cu
 
 struct PrefixParams {
@@ -68,7 +70,7 @@ struct PrefixSmem {
   static constexpr size_t kv = q + 2 * kKv;
   static constexpr size_t masks = kv + kSlots * kKv;       // [kMasks] u32: bit g = keys 16 g .. + 15 exist
   static constexpr size_t bars = masks + kMasks * 4;
-  static constexpr int kBars = 2 * kSlots + 8 + kMasks + 2;
+  static constexpr int kBars = 2 * kSlots + 10 + kMasks + 4;
   static constexpr size_t misc = bars + kBars * 8;
   static constexpr size_t total = misc + 16;
   static_assert(total + 1024 <= 232448, "shared memory budget");
@@ -111,8 +113,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::masks);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
   uint64_t *full = bars, *empty = full + kSlots;
-  uint64_t *qfull = empty + kSlots, *sfull = qfull + 2, *pfull = sfull + 2, *ofull = pfull + 2;
-  uint64_t *mfull = ofull + 2, *done = mfull + kMasks;
+  uint64_t *qfull = empty + kSlots, *sfull = qfull + 2, *pfull = sfull + 2, *ofull = pfull + 4;  // pfull: [tile][half]
+  uint64_t *mfull = ofull + 2, *turn = mfull + kMasks, *done = turn + 2;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 8);
 
@@ -127,8 +129,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[2 * i], 4);
+      mbar_init(&pfull[2 * i + 1], 4);
       mbar_init(&ofull[i], 1);
+      mbar_init(&turn[i], 1);
       mbar_init(&done[i], 1);
     }
     for (int i = 0; i < kMasks; ++i) mbar_init(&mfull[i], 1);
@@ -150,6 +154,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     *abort_s = 1;
   };
 
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kWarpLoad) {
     // ------------------------------------------------------------------ loader
     if (lane == 0) {
@@ -207,54 +212,82 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     __syncwarp();
   } else if (warp == kWarpMma || warp == kWarpMma + 1) {
     // ------------------------------------------------- issuer of one row tile
+    // The two issuers take turns: O_A(n), S_A(n + 1), then O_B(n), S_B(n + 1),
+    // so that the softmax of one row tile runs while the products of the other
+    // do.  (Without turns the tensor core took both tiles' products together and
+    // idled while both softmaxes ran; with one issuer for both, its waits lay
+    // between the products.)  A turn is waited for last, when the inputs are in.
     const int w = warp - kWarpMma;
     const bool leader = elect_one();
     constexpr uint32_t idesc_s = idesc_bf16(128, kTile);
     constexpr uint32_t idesc_o = idesc_bf16(128, kDim) | (1u << 16);  // V is MN-major
     const uint32_t ts = tmem + 128 * w, to = tmem + 256 + 128 * w;
-    bool ok = true;
-    int qn = 0, n = 0, ln = 0;  // pieces, tiles of the ring, tiles of this row tile
-    bool live = false;
-    for (Walk at(x0, x1, p.nkt); at.on(); at.next(), ++n) {
-      const bool first = at.first, last = at.last();
-      // a row tile without rows only frees the ring
-      if (first) live = static_cast<int64_t>(at.item % p.npairs) * kRows + 128 * w < p.rows;
-      const int mk = 2 * n, mv = 2 * n + 1;
-      if (live && first) ok = mbar_wait_warp(&qfull[w], (qn++) & 1);
-      ok = ok && mbar_wait_warp(&full[mk % kSlots], (mk / kSlots) & 1);
-      if (!ok || *abort_s) break;
-      if (!live) {
-        if (leader) mbar_arrive(&empty[mk % kSlots]);
-        ok = mbar_wait_warp(&full[mv % kSlots], (mv / kSlots) & 1);
-        if (!ok) break;
-        if (leader) mbar_arrive(&empty[mv % kSlots]);
-        __syncwarp();
-        continue;
-      }
-      tc_fence_after();
+    const uint64_t dq = desc_sw128_kmajor(smem_u32(qs + w * L::kKv));
+    bool ok = true, two = false, live = false;  // row tile B, this row tile has rows
+    int n = 0, qn = 0, ln = 0, turns = 0;
+    auto take_turn = [&]() -> bool {
+      if (!two) return true;
+      const int k = turns++;
+      return w == 0 ? k == 0 || mbar_wait_warp(&turn[1], (k - 1) & 1) : mbar_wait_warp(&turn[0], k & 1);
+    };
+    auto issue_s = [&](int slot) {
       if (leader) {
-        const uint64_t da = desc_sw128_kmajor(smem_u32(qs + w * L::kKv));
-        const uint64_t db = desc_sw128_kmajor(smem_u32(kvs + (mk % kSlots) * L::kKv));
+        const uint64_t db = desc_sw128_kmajor(smem_u32(kvs + slot * L::kKv));
 #pragma unroll
         for (int kk = 0; kk < kDim / 16; ++kk) {
           const uint64_t o = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
-          mma_f16(ts, da + o, db + o, idesc_s, kk > 0);
+          mma_f16(ts, dq + o, db + o, idesc_s, kk > 0);
         }
         mma_commit(&sfull[w]);
-        mma_commit(&empty[mk % kSlots]);
+        mma_commit(&empty[slot]);
       }
-      __syncwarp();
-      ok = mbar_wait_warp(&full[mv % kSlots], (mv / kSlots) & 1) && mbar_wait_warp(&pfull[w], ln & 1);
+    };
+    for (Walk at(x0, x1, p.nkt); at.on(); at.next(), ++n) {
+      const bool first = at.first, last = at.last();
+      const int m = 2 * n, v = m + 1, k = m + 2;
+      if (first) {
+        two = static_cast<int64_t>(at.item % p.npairs) * kRows + 128 < p.rows;
+        live = w == 0 || two;
+      }
+      if (!live) {  // only frees the ring
+        ok = mbar_wait_warp(&full[m % kSlots], (m / kSlots) & 1);
+        if (ok && leader) mbar_arrive(&empty[m % kSlots]);
+        ok = ok && mbar_wait_warp(&full[v % kSlots], (v / kSlots) & 1);
+        if (!ok) break;
+        if (leader) mbar_arrive(&empty[v % kSlots]);
+        __syncwarp();
+        continue;
+      }
+      if (first) {
+        ok = mbar_wait_warp(&full[m % kSlots], (m / kSlots) & 1) && mbar_wait_warp(&qfull[w], (qn++) & 1) && take_turn();
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(m % kSlots);
+        if (leader && two) mbar_arrive(&turn[w]);
+        __syncwarp();
+      }
+      ok = mbar_wait_warp(&full[v % kSlots], (v / kSlots) & 1) &&
+           (last || mbar_wait_warp(&full[k % kSlots], (k / kSlots) & 1)) && mbar_wait_warp(&pfull[2 * w], ln & 1) &&
+           take_turn();
       if (!ok || *abort_s) break;
       tc_fence_after();
+      const uint64_t dv = desc_mn(smem_u32(kvs + (v % kSlots) * L::kKv), L::kBlock);
       if (leader) {
-        const uint64_t db = desc_mn(smem_u32(kvs + (mv % kSlots) * L::kKv), L::kBlock);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_tmem_a(to, ts + 8 * kk, db + ((kk * 2048) >> 4), idesc_o, !(first && kk == 0));
-        mma_commit(&empty[mv % kSlots]);
-        if (last) mma_commit(&ofull[w]);
+        for (int kk = 0; kk < 4; ++kk)  // keys 0-63
+          mma_f16_tmem_a(to, ts + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, !(first && kk == 0));
       }
+      ok = mbar_wait_warp(&pfull[2 * w + 1], ln & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk) mma_f16_tmem_a(to, ts + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, 1);
+        mma_commit(last ? &ofull[w] : &empty[v % kSlots]);
+        if (last) mma_commit(&empty[v % kSlots]);
+      }
+      if (!last) issue_s(k % kSlots);
+      if (leader && two) mbar_arrive(&turn[w]);
       __syncwarp();
       ++ln;
     }
@@ -266,13 +299,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------ softmax of one row tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int w = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
     const float cs = p.qk_scale;
     const float2 cs2 = make_float2(cs, cs);
     uint8_t *qt = qs + w * L::kKv;
-    float ref = -INFINITY, l = 0.f;
+    float ref = 0.f, l = 0.f;
     int n = 0, ln = 0, pieces = 0;
     bool ok = true;
     int64_t r = 0;
@@ -303,82 +337,76 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (!ok || *abort_s) break;
       const uint32_t mask = masks[n % kMasks];
       tc_fence_after();
-      // the row's largest scaled logit of the tile
-      auto tile_max = [&]() -> float {
-        float m = -INFINITY;
+      // the row's logits, relative to its reference
+      float v[128];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t s[32];
-          tmem_load(ts + 32 * i, s);
-          tmem_ld_wait();
+      for (int i = 0; i < 4; ++i) tmem_load(ts + 32 * i, reinterpret_cast<uint32_t(&)[32]>(v[32 * i]));
+      tmem_ld_wait();
+      if (mask != 0xFFu) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if ((mask >> (2 * i + (e >> 4))) & 1u) m = fmaxf(m, __uint_as_float(s[e]) * cs);
-        }
-        return m;
-      };
-      // (finite even when the tile has no key: the next tile then raises it)
-      if (first) ref = fmaxf(tile_max() + kHead, -1e30f);
-      uint32_t pk[64];
-      float2 sum;
-      while (true) {
-        sum = make_float2(0.f, 0.f);
-        float top = -INFINITY;
+        for (int e = 0; e < 128; ++e)
+          if (!((mask >> (e >> 4)) & 1u)) v[e] = cs > 0.f ? -INFINITY : INFINITY;  // cs v = -inf
+      }
+      if (first) ref = 0.f;
+      float2 *v2 = reinterpret_cast<float2 *>(v);
+      float top = -INFINITY;
+      {
         const float2 nref2 = make_float2(-ref, -ref);
-        uint32_t s[2][32];
-        tmem_load(ts, s[0]);
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          tmem_ld_wait();
-          if (i < 3) tmem_load(ts + 32 * (i + 1), s[(i + 1) & 1]);
-          uint32_t(&c)[32] = s[i & 1];
-          if (mask != 0xFFu) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((mask >> (2 * i + (e >> 4))) & 1u)) c[e] = cs > 0.f ? 0xFF800000u : 0x7F800000u;  // cs s = -inf
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 v =
-                fma2(make_float2(__uint_as_float(c[2 * e]), __uint_as_float(c[2 * e + 1])), cs2, nref2);
-            top = max3(top, v.x, v.y);
-            const float2 w2 = make_float2(exp2_hw(v.x), exp2_hw(v.y));
-            sum = add2(sum, w2);
-            pk[16 * i + e] = pack_bf16x2(w2.x, w2.y);
-          }
+        for (int e = 0; e < 64; ++e) {
+          v2[e] = fma2(v2[e], cs2, nref2);
+          t4[e & 3] = max3(t4[e & 3], v2[e].x, v2[e].y);
         }
-        if (!__any_sync(0xffffffffu, top > kLazy - kHead)) break;
-        // a logit passes its row's reference by the lazy margin: raise it, scale
-        // O (which holds the products up to the tile before) and the sum, and
-        // take the weights again
-        float fac = 1.f;
-        const float m = tile_max();
-        if (m + kHead > ref) {
-          fac = exp2f(ref - (m + kHead));
-          ref = m + kHead;
-        }
-        l *= fac;
+        top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+      }
+      if (__any_sync(0xffffffffu, first || top > kLazy - kHead)) {
+        // the piece's first tile, or a logit passes its row's reference by the
+        // lazy margin: raise it; the sum and O (which holds the products up to
+        // the tile before) shrink in step.  (Finite even when the tile has no
+        // key: the next tile then raises it.)
+        const float up = first ? fmaxf(top + kHead, -1e30f) : fmaxf(top + kHead, 0.f);
+        const float2 nup2 = make_float2(-up, -up);
+        ref += up;
+#pragma unroll
+        for (int e = 0; e < 64; ++e) v2[e] = add2(v2[e], nup2);
         if (!first) {
+          const float fac = exp2f(-up);
+          l *= fac;
 #pragma unroll 1
-          for (int i = 0; i < kDim / 32; ++i) {
-            uint32_t o[32];
-            tmem_load(to + 32 * i, o);
+          for (int i = 0; i < kDim / 16; ++i) {
+            uint32_t o[16];
+            tmem_load(to + 16 * i, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
-            tmem_store(to + 32 * i, o);
-            tmem_store(to + 32 * i + 16, o + 16);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
+            tmem_store(to + 16 * i, o);
           }
           tmem_wait_st();
         }
       }
-      l += sum.x + sum.y;
+      // weights, half a tile at a time: the product over the first 64 keys
+      // starts while the second half's are computed
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_store(ts + 16 * i, pk + 16 * i);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[w]);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float2 x = v2[32 * half + e];
+          const float2 w2 = make_float2(exp2_hw(x.x), exp2_hw(x.y));
+          sum[e & 1] = add2(sum[e & 1], w2);
+          pk[e] = pack_bf16x2(w2.x, w2.y);
+        }
+        tmem_store(ts + 32 * half, pk);
+        tmem_store(ts + 32 * half + 16, pk + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[2 * w + half]);
+      }
+      const float2 sum2 = add2(sum[0], sum[1]);
+      l += sum2.x + sum2.y;
       ++ln;
       if (last) {
         ok = mbar_wait_warp(&ofull[w], pieces & 1);
@@ -506,6 +534,16 @@ cudaError_t launch_shared(const sa_paged_args &pa, const PrefixParams &p, int gr
   if (!encode_rows(&kmap, pa.K, rows, kDim, pa.P) || !encode_rows(&vmap, pa.V, rows, kDim, pa.P))
     return cudaErrorInvalidValue;
   auto kern = prefix_kernel<kDim>;
+  // the register split assumes kLaunchRegs registers per thread at launch;
+  // anything else could leave a raise waiting forever
+  static int regs = -1;
+  if (regs < 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void *>(kern));
+    if (e != cudaSuccess) return e;
+    regs = fa.numRegs;
+  }
+  if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   const size_t smem = PrefixSmem<kDim>::total + 1024;
   static bool attr_done[64] = {};
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, attr_done);
