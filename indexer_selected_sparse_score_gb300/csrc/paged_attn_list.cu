@@ -19,17 +19,18 @@
 // rounded to bf16 for the second product (2^-9 of each at most, against an
 // output that is itself rounded to bf16); logits, sums and O are fp32.
 //
-// Work: the tiles of all units (128 keys each) form one list, cut evenly over
-// one CTA per SM (a decode step reads each page once, so HBM is the bound and
-// every SM must stream to the end).  A unit that falls into several CTAs
+// Work: the tiles of all units (128 keys each) form one list, cut evenly into
+// parts: one for each CTA, one CTA per SM (a decode step reads each page once,
+// so HBM is the bound and every SM must stream to the end); beside the product
+// with the shared pages, whose CTAs leave their SMs at different times, four
+// per SM that CTAs claim.  A unit that falls into several CTAs
 // leaves its parts (m_ref, sum, O) in scratch for a merge kernel.  Entries that
 // name no page are dropped before tiles are formed; positions past the token's
 // own are masked, and the V rows they hold are zeroed in shared memory, since
 // 0 x NaN would reach the sum.
 //
-// Warps: 0-7 softmax and output; 8 issues S^T, 9 issues O^T; 10 and 11 resolve
-// the lists and issue the copies of K and V, warp 10 publishing one record per
-// tile.  Every wait is
+// Warps: 0-7 softmax and output; 8 issues S^T, 9 issues O^T; 10 resolves the
+// lists, copies K and publishes one record per tile; 11 copies V.  Every wait is
 // bounded; on expiry the kernel flags the status word, drains its copies and
 // products and returns.
 #include <cudaTypedefs.h>
@@ -49,8 +50,8 @@ using namespace umma;
 constexpr int kTile = 128;      // keys per tile
 constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;   // threads of the softmax warps, 0-7
-constexpr int kWarpS = 8, kWarpO = 9, kWarpK = 10;  // and 11
-constexpr int kQueue = 40;      // page entries a loader holds: under a tile's and one batch of 32
+constexpr int kWarpS = 8, kWarpO = 9, kWarpK = 10, kWarpV = 11;
+constexpr int kQueue = 40;      // page entries the loader holds: under a tile's and one batch of 32
 // The reference a weight is taken against lies kHead above the maximum that
 // set it (log2 units), and is raised once a logit passes that maximum by kLazy:
 // unnormalised sums of weights up to 2^(kLazy - kHead) times any bf16 values
@@ -63,6 +64,7 @@ struct Record {
   int row;       // first output row of the unit (t * H + head)
   int slot;      // part slot of the piece
   uint32_t cnt[2];  // byte g: keys present among keys 16 g .. 16 g + 15
+  uint32_t y[8];    // cache row of each page slot (past the end: an empty slot)
 };
 
 template <int N, int kDim>
@@ -73,7 +75,8 @@ struct ListSmem {
   static constexpr int kPBufs = N <= 32 ? 2 : 1;
   // Tile records.  Record n + kStages + 5 is written once S(n + 5) is done,
   // for which the weights of tile n + 2 were written and so, with two P^T
-  // buffers at most, O(n) issued: every reader is past record n.
+  // buffers at most, O(n) issued: every reader (V's loader among them) is past
+  // record n.
   static constexpr int kRecs = kStages + 5;
   static constexpr uint32_t kBlock = kTile * 128;          // one 64-dim block of a tile
   static constexpr uint32_t kKv = kBlock * (kDim / 64);
@@ -85,12 +88,12 @@ struct ListSmem {
   static constexpr size_t red = (recs + kRecs * sizeof(Record) + 15) & ~size_t(15);   // [4][N]
   static constexpr size_t fac = red;                       // [N], over the reduction's first row (see below)
   static constexpr size_t mref = red + 4 * N * 4;          // [N]
-  static constexpr size_t queue = mref + N * 4;            // [2][kQueue] page entries waiting for a tile
-  static constexpr size_t bars = (queue + 2 * kQueue * 4 + 7) & ~size_t(7);
+  static constexpr size_t queue = mref + N * 4;            // [kQueue] page entries waiting for a tile
+  static constexpr size_t bars = (queue + kQueue * 4 + 7) & ~size_t(7);
   static constexpr int kBars = 4 * kStages + 2 + 4 + 2 * kPBufs + 2 + kRecs + 2;
   static constexpr size_t misc = bars + kBars * 8;
-  static constexpr size_t total = misc + 32;
-  static_assert(total + 1024 <= 232448, "shared memory budget");
+  static constexpr size_t total = misc + 16;
+  static_assert(total <= 232448, "shared memory budget");
   static_assert(red % 16 == 0 && mref % 16 == 0 && queue % 4 == 0 && bars % 8 == 0 && misc % 8 == 0, "alignment");
   // O^T at dim 64 reads a second block past V's last slot (lanes nobody reads)
   static_assert(v + kStages * kKv + kBlock <= total, "V overread stays in bounds");
@@ -105,8 +108,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   using L = ListSmem<N, kDim>;
   constexpr int kSt = L::kStages, kB = kDim / 64, kPb = L::kPBufs, kRecs = L::kRecs;
   constexpr uint32_t kColO = 2 * N;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];  // (its alignment is checked below)
   uint8_t *ks = smem + L::k, *vs = smem + L::v, *ps = smem + L::p, *qs = smem + L::q;
   Record *recs = reinterpret_cast<Record *>(smem + L::recs);
   float *red_s = reinterpret_cast<float *>(smem + L::red);
@@ -122,14 +124,12 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   uint64_t *rfull = oempty + 1, *done = rfull + kRecs;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 4);
-  int *start_t = reinterpret_cast<int *>(smem + L::misc + 8);
-  long long *start_s = reinterpret_cast<long long *>(smem + L::misc + 16);  // total tiles, offset of the first token
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = blockIdx.x;
-  // CTAs that share the tiles out: no more than there are tiles, so that every
-  // CTA between a unit's first and last holds a piece of it
-  auto shares = [&](long long tiles) { return static_cast<int>(min(static_cast<long long>(gridDim.x), max(tiles, 1ll))); };
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
+    if (tid == 0) raise_flag(p.status, kFlagTimeout);
+    return;
+  }
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < kSt; ++i) {
@@ -172,226 +172,255 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     }
     return (n + spt - 1) / spt;
   };
+  long long tot = static_cast<long long>(p.pv.T) * upt * p.tpu;
   if (p.whole) {
-    // Sequence lengths are known to the device only: every CTA sums the tiles
-    // of all tokens (a contiguous share per thread, one scan) and finds the
-    // token its first tile falls into.
-    long long *sums = reinterpret_cast<long long *>(ks);
-    const int per = (p.pv.T + kThreads - 1) / kThreads;
-    const int ta = min(tid * per, p.pv.T), tb = min(ta + per, p.pv.T);
+    // sequence lengths are known to the device only: every CTA sums the tiles
+    // of all tokens (shared memory of the ring as scratch)
     long long own = 0;
-    for (int t = ta; t < tb; ++t) own += count_of(t, c == 0);
-    sums[tid] = own;
-    if (tid == 0) *start_t = p.pv.T;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int i = 0; i < kThreads; ++i) {
-      if (i < tid) before += sums[i];
-      total += sums[i];
-    }
-    const int g = shares(total * upt);
-    const long long x0 = total * upt * min(c, g) / g;
-    if (tid == 0) start_s[0] = total * upt;
-    if (before * upt <= x0 && x0 < (before + own) * upt) {
-      int t = ta;
-      for (; t < tb; ++t) {
-        const int n = count_of(t, false);
-        if (x0 < (before + n) * upt) break;
-        before += n;
-      }
-      *start_t = t;
-      start_s[1] = before * upt;
-    }
-  } else if (tid == 0) {
-    start_s[0] = static_cast<long long>(p.pv.T) * upt * p.tpu;
+    for (int t = tid; t < p.pv.T; t += kThreads) own += count_of(t, blockIdx.x == 0);
+    block_prefix(own, reinterpret_cast<long long *>(ks), tot);
+    tot *= upt;
   }
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
-  const long long tot = start_s[0];
-  const int G = shares(tot);
-  const long long x_begin = tot * min(c, G) / G, x_end = tot * min(c + 1, G) / G;
+  // parts the tiles are cut into: no more than there are tiles, so that every
+  // part between a unit's first and last holds a piece of it
+  const int G = static_cast<int>(min(static_cast<long long>(p.parts), max(tot, 1ll)));
   auto fail = [&]() {
     raise_flag(p.status, kFlagTimeout);
     *abort_s = 1;
   };
 
-  if (warp >= kWarpK) {
-    // ----------------------------------------------------------------- loaders
-    // One warp copies K (and the queries, and publishes the records), one V;
-    // both walk the same lists.
-    const bool is_k = warp == kWarpK;
-    int *queue = reinterpret_cast<int *>(smem + L::queue) + (is_k ? 0 : kQueue);
-    uint64_t *full = is_k ? kfull : vfull, *empty = is_k ? kempty : vempty;
-    const CUtensorMap *map = is_k ? &kmap : &vmap;
-    uint8_t *ring = is_k ? ks : vs;
+  if (warp == kWarpV) {
+    // ------------------------------------------------------------ loader of V
+    // follows the records
+    const int slot = lane / kB, kb = lane % kB;  // this lane's copy: page slot, 64-dim block
+    const uint32_t dst = kb * L::kBlock + slot * p.pv.P * 128;
+    if (lane == 0) prefetch_tmap(&vmap);
+    bool ok = true;
+    int n = 0;
+    for (;; ++n) {
+      ok = mbar_wait_warp(&rfull[n % kRecs], (n / kRecs) & 1);
+      if (!ok) break;
+      const Record &rec = recs[n % kRecs];
+      if (rec.flags & kEnd) break;
+      const uint32_t y = rec.y[min(slot, 7)];
+      const int s = n % kSt;
+      ok = mbar_wait_warp(&vempty[s], ((n / kSt) & 1) ^ 1);
+      if (!ok || *abort_s) break;
+      if (lane == 0) mbar_expect_tx(&vfull[s], L::kKv);
+      __syncwarp();
+      if (slot < spt) tma_load_2d(vs + s * L::kKv + dst, &vmap, &vfull[s], 64 * kb, static_cast<int>(y));
+    }
     if (lane == 0) {
-      prefetch_tmap(map);
-      if (is_k) prefetch_tmap(&qmap);
+      if (!ok) fail();
+      // drain: every copy issued lands before the CTA exits
+      for (int i = max(0, n - kSt); i < n; ++i) mbar_wait(&vfull[i % kSt], (i / kSt) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kWarpK) {
+    // ---------------------------------------------- loader of K, Q; the lists
+    int *queue = reinterpret_cast<int *>(smem + L::queue);
+    if (lane == 0) {
+      prefetch_tmap(&kmap);
+      prefetch_tmap(&qmap);
     }
     int n = 0, qn = 0;
     bool ok = true;
-    int cut_unit = -1, cut_last = 0;
-    long long base;
-    int t, sub;
-    if (p.whole) {
-      t = *start_t;
-      base = start_s[1];
-      sub = 0;
-      if (x_begin < x_end) {  // units of the token before the first tile
-        const int cnt = count_of(t, false);
-        sub = static_cast<int>((x_begin - base) / cnt);
-        base += static_cast<long long>(sub) * cnt;
-      }
-    } else {
-      const long long u = p.tpu ? x_begin / p.tpu : 0;
-      t = static_cast<int>(u / upt);
-      sub = static_cast<int>(u % upt);
-      base = u * p.tpu;
-    }
     const uint32_t rows_total = static_cast<uint32_t>(p.pv.n_pages) * p.pv.H_kv * p.pv.P;
-    const int slot = lane / kB, kb = lane % kB;  // this lane's copy: page slot, 64-dim block
+    const int slot = lane / kB, kb = lane % kB;
     const uint32_t dst = kb * L::kBlock + slot * p.pv.P * 128;
-    long long x = x_begin;
-    while (ok && x < x_end) {
-      const int cnt = p.whole ? count_of(t, false) : p.tpu;
-      if (cnt == 0) {
-        ++t;
-        continue;
-      }
-      const int u = t * upt + sub;
-      const int a = static_cast<int>(x - base);
-      const int e = static_cast<int>(min(static_cast<long long>(cnt), x_end - base));
-      const bool starts = a == 0, ends = e == cnt;
-      int b = 0, pos = 0;
-      const bool tok = load_paged_token(p.pv, t, p.status, is_k && lane == 0 && sub == 0 && starts && !p.whole, b, pos);
-      if (tok) {
-        const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64;
-        const int last = pos >> p.pv.logP;
-        const int own = pos + 1 - last * p.pv.P;  // positions of the token's own page that it sees
-        const int f = p.whole ? p.first_page : max(last + 1 - p.local, 0);
-        const int nlist = p.whole ? 0 : p.K;
-        const int r1 = min(e * spt, nlist + last + 1 - f);
-        int r = a * spt, qh = 0, qe = 0;  // raw entries, queue head and end
-        // the CTA of tile y is floor(((y + 1) G - 1) / tot)
-        const int c_last = static_cast<int>(((base + cnt) * G - 1) / tot);
-        if (starts && !ends) {
-          cut_unit = u;
-          cut_last = c_last;
+    int t = 0, sub = 0, cnt = p.tpu;  // token, unit of the token, tiles of the unit
+    long long base = 0;               // tiles before the unit
+    // whole sequences: moves on to the token that holds tile x (x is not before
+    // the current token's), 32 tokens at a time
+    auto seek = [&](long long x) {
+      base -= static_cast<long long>(sub) * cnt;
+      sub = 0;
+      for (;;) {
+        const int own = t + lane < p.pv.T ? count_of(t + lane, false) : 0;
+        int sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += up;
         }
-        if (p.keep && starts && is_k && lane == 0) p.info[u] = make_int2(c, c_last);
-        // page entry i of the list (page id, bit 30 set for the token's own
-        // page, whose later positions are masked), -1 when it names no page
-        auto resolve = [&](int i) -> int {
-          if (i >= r1) return -1;
-          int j;
-          if (i < nlist) {
-            j = p.idx[(static_cast<int64_t>(t) * p.pv.H_kv + hk) * p.K + i];
-            if (j < 0 || j >= f) {
-              if (is_k && (j < -1 || j > last)) raise_flag(p.status, kFlagBadIndex);
-              return -1;
+        const uint32_t m = __ballot_sync(0xffffffffu, x < base + static_cast<long long>(sum) * upt);
+        const int at = m ? __ffs(m) - 1 : 31;
+        const int incl = __shfl_sync(0xffffffffu, sum, at), mine = __shfl_sync(0xffffffffu, own, at);
+        if (m) {
+          t += at;
+          base += static_cast<long long>(incl - mine) * upt;
+          cnt = mine;
+          return;
+        }
+        base += static_cast<long long>(incl) * upt;
+        t += 32;
+      }
+    };
+    int c = blockIdx.x;  // the part being worked on
+    while (ok) {
+      if (p.counter) {
+        // parts are claimed: CTAs start when the kernel before leaves their SM
+        if (lane == 0) c = static_cast<int>(atomicAdd(p.counter, 1u));
+        c = __shfl_sync(0xffffffffu, c, 0);
+      }
+      const long long x_begin = tot * min(c, G) / G, x_end = tot * min(c + 1, G) / G;
+      int cut_unit = -1, cut_last = 0;
+      long long x = x_begin;
+      if (x < x_end) {
+        if (p.whole) {
+          seek(x);
+          sub = static_cast<int>((x - base) / cnt);
+          base += static_cast<long long>(sub) * cnt;
+        } else {
+          const long long u = x / p.tpu;
+          t = static_cast<int>(u / upt);
+          sub = static_cast<int>(u % upt);
+          base = u * p.tpu;
+        }
+      }
+      while (ok && x < x_end) {
+        const int u = t * upt + sub;
+        const int a = static_cast<int>(x - base);
+        const int e = static_cast<int>(min(static_cast<long long>(cnt), x_end - base));
+        const bool starts = a == 0, ends = e == cnt;
+        int b = 0, pos = 0;
+        const bool tok = load_paged_token(p.pv, t, p.status, lane == 0 && sub == 0 && starts && !p.whole, b, pos);
+        if (tok) {
+          const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64;
+          const int last = pos >> p.pv.logP;
+          const int own = pos + 1 - last * p.pv.P;  // positions of the token's own page that it sees
+          const int f = p.whole ? p.first_page : max(last + 1 - p.local, 0);
+          const int nlist = p.whole ? 0 : p.K;
+          const int r1 = min(e * spt, nlist + last + 1 - f);
+          int r = a * spt, qh = 0, qe = 0;  // raw entries, queue head and end
+          // the part of tile y is floor(((y + 1) G - 1) / tot)
+          const int c_last = static_cast<int>(((base + cnt) * G - 1) / tot);
+          if (starts && !ends) {
+            cut_unit = u;
+            cut_last = c_last;
+          }
+          if (p.keep && starts && lane == 0) p.info[u] = make_int2(c, c_last);
+          // page entry i of the list (page id, bit 30 set for the token's own
+          // page, whose later positions are masked), -1 when it names no page
+          auto resolve = [&](int i) -> int {
+            if (i >= r1) return -1;
+            int j;
+            if (i < nlist) {
+              j = p.idx[(static_cast<int64_t>(t) * p.pv.H_kv + hk) * p.K + i];
+              if (j < 0 || j >= f) {
+                if (j < -1 || j > last) raise_flag(p.status, kFlagBadIndex);
+                return -1;
+              }
+            } else {
+              j = f + i - nlist;
             }
-          } else {
-            j = f + i - nlist;
-          }
-          const int page = load_page(p.pv, b, j, p.status, is_k);
-          return page < 0 ? -1 : page | (j == last ? 1 << 30 : 0);
-        };
-        bool first = true, more = true;
-        int ahead = resolve(r + lane);  // the next batch, resolved while earlier tiles are copied
-        while (more) {
-          while (qe - qh <= spt && r < r1) {  // enough for this tile and to know whether another follows
-            const int rest = qe - qh, ent = ahead;
-            r += 32;
-            ahead = resolve(r + lane);
-            const int keep = lane < rest ? queue[qh + lane] : 0;
-            const uint32_t m = __ballot_sync(0xffffffffu, ent >= 0);
-            __syncwarp();
-            if (lane < rest) queue[lane] = keep;
-            if (ent >= 0) queue[rest + __popc(m & ((1u << lane) - 1))] = ent;
-            __syncwarp();
-            qh = 0;
-            qe = rest + __popc(m);
-          }
-          const int take = min(spt, qe - qh);
-          more = qe - qh > take;
-          const int ent = slot < take ? queue[qh + slot] : -1;
-          const int s = n % kSt;
-          uint32_t cn0 = 0, cn1 = 0;
-          bool masked = false;
-          if (is_k) {
+            const int page = load_page(p.pv, b, j, p.status, true);
+            return page < 0 ? -1 : page | (j == last ? 1 << 30 : 0);
+          };
+          bool first = true, more = true;
+          int ahead = resolve(r + lane);  // the next batch, resolved while earlier tiles are copied
+          while (more) {
+            while (qe - qh <= spt && r < r1) {  // enough for this tile and to know whether another follows
+              const int rest = qe - qh, ent = ahead;
+              r += 32;
+              ahead = resolve(r + lane);
+              const int keep = lane < rest ? queue[qh + lane] : 0;
+              const uint32_t m = __ballot_sync(0xffffffffu, ent >= 0);
+              __syncwarp();
+              if (lane < rest) queue[lane] = keep;
+              if (ent >= 0) queue[rest + __popc(m & ((1u << lane) - 1))] = ent;
+              __syncwarp();
+              qh = 0;
+              qe = rest + __popc(m);
+            }
+            const int take = min(spt, qe - qh);
+            more = qe - qh > take;
+            const int ent = slot < take ? queue[qh + slot] : -1;
+            const int s = n % kSt;
             // keys present among each 16: lane g's own granule, its page slot
             // held by the lanes of that slot
             const int g = lane & 7, sg = (16 * g) >> p.pv.logP;
             const int eg = __shfl_sync(0xffffffffu, ent, sg * kB);
             int have = eg >= 0 ? 16 : 0;
             if (eg >= 0 && (eg >> 30)) have = min(max(own - (16 * g - (sg << p.pv.logP)), 0), 16);
-            masked = __any_sync(0xffffffffu, eg >= 0 && have < 16);
+            const bool masked = __any_sync(0xffffffffu, eg >= 0 && have < 16);
             const uint32_t byte = lane < 8 ? static_cast<uint32_t>(have) << (8 * (g & 3)) : 0u;
-            cn0 = __reduce_or_sync(0xffffffffu, g < 4 ? byte : 0u);
-            cn1 = __reduce_or_sync(0xffffffffu, g < 4 ? 0u : byte);
-          }
-          if (!mbar_wait_warp(&empty[s], ((n / kSt) & 1) ^ 1) || *abort_s) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_expect_tx(&full[s], L::kKv);
-          __syncwarp();
-          // a slot without a page reads past the tensor's end: the copy fills zeros
-          const uint32_t y = ent >= 0 ? ((static_cast<uint32_t>(ent) & 0x3FFFFFFFu) * p.pv.H_kv + hk) * p.pv.P
-                                      : rows_total;
-          if (slot < spt) tma_load_2d(ring + s * L::kKv + dst, map, &full[s], 64 * kb, static_cast<int>(y));
-          if (is_k && lane == 0) {
-            Record &rec = recs[n % kRecs];
-            rec.flags = (first ? kFirst : 0) | (more ? 0 : kLast) | (masked ? kMasked : 0) |
-                        (!p.keep && starts && ends ? kDirect : 0) | min(64, (hk + 1) * p.group - h0) << 8;
-            rec.row = t * p.pv.H + h0;
-            rec.slot = p.keep ? u + c : 2 * c + (starts ? 1 : 0);
-            rec.cnt[0] = cn0;
-            rec.cnt[1] = cn1;
-            mbar_arrive(&rfull[n % kRecs]);
-          }
-          ++n;
-          if (is_k && first) {
-            // the queries, once the previous unit's last product has read its own
-            if (lane == 0) {
-              ok = mbar_wait(qempty, (qn & 1) ^ 1);
-              if (ok) {
-                mbar_expect_tx(qfull, N * kDim * 2);
-                for (int i = 0; i < kB; ++i)
-                  tma_load_2d(qs + i * N * 128, &qmap, qfull, 64 * i, t * p.pv.H + h0);
-              }
+            const uint32_t cn0 = __reduce_or_sync(0xffffffffu, g < 4 ? byte : 0u);
+            const uint32_t cn1 = __reduce_or_sync(0xffffffffu, g < 4 ? 0u : byte);
+            // a slot without a page reads past the tensor's end: the copy fills zeros
+            const uint32_t y = ent >= 0 ? ((static_cast<uint32_t>(ent) & 0x3FFFFFFFu) * p.pv.H_kv + hk) * p.pv.P
+                                        : rows_total;
+            if (!mbar_wait_warp(&kempty[s], ((n / kSt) & 1) ^ 1) || *abort_s) {
+              ok = false;
+              break;
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            ++qn;
+            if (lane == 0) mbar_expect_tx(&kfull[s], L::kKv);
+            __syncwarp();
+            if (slot < spt) tma_load_2d(ks + s * L::kKv + dst, &kmap, &kfull[s], 64 * kb, static_cast<int>(y));
+            Record &rec = recs[n % kRecs];
+            if (slot < 8 && kb == 0) rec.y[slot] = y;
+            if (lane == 0) {
+              rec.flags = (first ? kFirst : 0) | (more ? 0 : kLast) | (masked ? kMasked : 0) |
+                          (!p.keep && starts && ends ? kDirect : 0) | min(64, (hk + 1) * p.group - h0) << 8;
+              rec.row = t * p.pv.H + h0;
+              rec.slot = p.keep ? u + c : 2 * c + (starts ? 1 : 0);
+              rec.cnt[0] = cn0;
+              rec.cnt[1] = cn1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rfull[n % kRecs]);
+            ++n;
+            if (first) {
+              // the queries, once the previous unit's last product has read its own
+              if (lane == 0) {
+                ok = mbar_wait(qempty, (qn & 1) ^ 1);
+                if (ok) {
+                  mbar_expect_tx(qfull, N * kDim * 2);
+                  for (int i = 0; i < kB; ++i)
+                    tma_load_2d(qs + i * N * 128, &qmap, qfull, 64 * i, t * p.pv.H + h0);
+                }
+              }
+              ok = __shfl_sync(0xffffffffu, ok, 0);
+              if (!ok) break;
+              ++qn;
+            }
+            qh += take;
+            first = false;
           }
-          qh += take;
-          first = false;
+        }
+        x = base + e;
+        if (ends && x < x_end) {
+          if (++sub < upt) {
+            base += cnt;
+          } else if (p.whole) {
+            --sub;
+            seek(x);
+          } else {
+            base += cnt;
+            sub = 0;
+            ++t;
+          }
         }
       }
-      x = base + e;
-      if (ends) {
-        base += cnt;
-        if (++sub == upt) {
-          sub = 0;
-          ++t;
-        }
+      if (!p.counter) {
+        if (lane == 0) p.cut[c] = make_int2(cut_unit, cut_last);
+        break;
       }
+      if (c >= G) break;
     }
     if (lane == 0) {
-      if (!ok) fail();
-      if (is_k) {
-        if (!p.keep) p.cut[c] = make_int2(cut_unit, cut_last);
-        if (ok) {
-          recs[n % kRecs].flags = kEnd;
-          mbar_arrive(&rfull[n % kRecs]);
-        }
+      if (ok) {
+        recs[n % kRecs].flags = kEnd;
+        mbar_arrive(&rfull[n % kRecs]);
+      } else {
+        fail();
       }
-      // drain: every copy issued lands before the CTA exits
-      for (int i = max(0, n - kSt); i < n; ++i) mbar_wait(&full[i % kSt], (i / kSt) & 1);
+      for (int i = max(0, n - kSt); i < n; ++i) mbar_wait(&kfull[i % kSt], (i / kSt) & 1);
       if (qn > 0) mbar_wait(qfull, (qn - 1) & 1);
     }
     __syncwarp();
@@ -658,46 +687,31 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 }
 
 // Merges the parts of the unit that CTA c's range cuts: o = sum 2^(m_i - M) o_i
-// / sum 2^(m_i - M) l_i.  One warp per head, parts in order.
-template <int N, int kDim>
+// / sum 2^(m_i - M) l_i.  kSplit warps per head, each every kSplit-th part (8
+// when a unit has many parts: the chain of loads is then what the merge costs).
+template <int N, int kDim, int kSplit>
 __global__ void __launch_bounds__(256)
 merge_cut_kernel(const ListParams p) {
+  __shared__ float acc_s[8][kDim + 1];
   pdl_wait();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int2 cut = p.cut[c];
   if (cut.x < 0) return;
   const int upt = p.pv.H_kv * p.gb, t = cut.x / upt, sub = cut.x % upt;
   const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64, heads = min(64, (hk + 1) * p.group - h0);
-  constexpr int V = kDim / 32;  // values per lane
-  const int i = blockIdx.y * 8 + warp;
-  if (i >= heads) return;
-  auto slot_of = [&](int k) { return static_cast<int64_t>(k == c ? 2 * c + 1 : 2 * k) * N + i; };
-  float M = -INFINITY;
-  for (int k = c + lane; k <= cut.y; k += 32) M = fmaxf(M, p.ml[slot_of(k)].x);
+  const int i = blockIdx.y * (8 / kSplit) + warp / kSplit;
+  if (kSplit == 1 && i >= heads) return;
+  const int row = min(i, N - 1);
+  auto locate = [&](int k, const float2 *&ml, const float *&o) {
+    const int64_t at = static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * N + row;
+    ml = p.ml + at;
+    o = p.part + at * kDim;
+  };
+  float out[kDim / 32];
+  if (!merge_parts<kDim, kSplit>(cut.y - c + 1, warp % kSplit, lane, locate, acc_s, out) || i >= heads) return;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[V] = {}, l = 0.f;
-  for (int k0 = c; k0 <= cut.y; k0 += 32) {
-    float a = 0.f, la = 0.f;  // this lane's part: weight, weighted sum
-    if (k0 + lane <= cut.y) {
-      const float2 ml = p.ml[slot_of(k0 + lane)];
-      a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      la = a * ml.y;
-    }
-    const int n = min(32, cut.y + 1 - k0);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float w = __shfl_sync(0xffffffffu, a, k);
-      l += __shfl_sync(0xffffffffu, la, k);
-      const float *o = p.part + slot_of(k0 + k) * kDim + V * lane;
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[e], acc[e]);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < V; ++e)
-    p.out[(static_cast<int64_t>(t) * p.pv.H + h0 + i) * kDim + V * lane + e] = __float2bfloat16_rn(acc[e] * inv);
+  for (int e = 0; e < kDim / 32; ++e)
+    p.out[(static_cast<int64_t>(t) * p.pv.H + h0 + i) * kDim + kDim / 32 * lane + e] = __float2bfloat16_rn(out[e]);
 }
 
 template <int N, int kDim>
@@ -710,13 +724,16 @@ cudaError_t launch_list(const sa_paged_args &pa, const void *q, ListParams &p, i
       !encode_rows(&kmap, pa.K, rows, kDim, pa.P) || !encode_rows(&vmap, pa.V, rows, kDim, pa.P))
     return cudaErrorInvalidValue;
   auto kern = page_list_kernel<N, kDim>;
-  const size_t smem = L::total + 1024;
+  const size_t smem = L::total;
   static bool attr_done[64] = {};
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, attr_done);
   if (e != cudaSuccess) return e;
   e = launch_ex(pdl, kern, dim3(grid), dim3(kThreads), smem, stream, 1, qmap, kmap, vmap, p);
   if (e != cudaSuccess || p.keep) return e;
-  return launch_ex(true, merge_cut_kernel<N, kDim>, dim3(grid, N / 8), dim3(256), 0, stream, 1, p);
+  const int64_t units = static_cast<int64_t>(pa.T) * pa.H_kv * p.gb;
+  return units * 8 <= grid
+             ? launch_ex(true, merge_cut_kernel<N, kDim, 8>, dim3(grid, N), dim3(256), 0, stream, 1, p)
+             : launch_ex(true, merge_cut_kernel<N, kDim, 1>, dim3(grid, N / 8), dim3(256), 0, stream, 1, p);
 }
 
 template <int kDim>
@@ -752,7 +769,7 @@ int list_cols(const sa_paged_args &pa) {
 size_t list_scratch(const sa_paged_args &pa, bool keep) {
   const int g = pa.H / pa.H_kv;
   const size_t units = static_cast<size_t>(pa.T) * pa.H_kv * ((g + 63) / 64);
-  const size_t slots = keep ? units + kMaxCtas : 2 * kMaxCtas;
+  const size_t slots = keep ? units + kMaxParts : 2 * kMaxCtas;
   return round_up(slots * list_cols(pa) * pa.D * sizeof(float)) + round_up(slots * list_cols(pa) * sizeof(float2)) +
          round_up((keep ? units : kMaxCtas) * sizeof(int2));
 }
@@ -766,7 +783,7 @@ cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams 
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.status = status;
   const size_t units = static_cast<size_t>(pa.T) * pa.H_kv * p.gb;
-  const size_t slots = p.keep ? units + kMaxCtas : 2 * kMaxCtas;
+  const size_t slots = p.keep ? units + kMaxParts : 2 * kMaxCtas;
   char *w = static_cast<char *>(scratch);
   p.part = reinterpret_cast<float *>(w);
   w += round_up(slots * list_cols(pa) * pa.D * sizeof(float));
@@ -780,6 +797,8 @@ cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams 
     p.tpu = static_cast<int>(std::max<int64_t>(1, (entries + spt - 1) / spt));
     grid = static_cast<int>(std::min<int64_t>(grid, static_cast<int64_t>(units) * p.tpu));
   }
+  p.parts = p.keep ? std::min(4 * sm_count(), kMaxParts) : grid;
+  p.counter = p.keep ? status + kCounterWord : nullptr;
   return pa.D == 128 ? launch_dim<128>(pa, q, p, grid, pdl, stream) : launch_dim<64>(pa, q, p, grid, pdl, stream);
 }
 

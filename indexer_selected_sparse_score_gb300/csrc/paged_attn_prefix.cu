@@ -441,28 +441,28 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 }
 
 // Output rows: the pieces of the shared part (of the row's item) and of the
-// token's own pages, o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  One warp
-// per row; the pieces in order.
-template <int kDim>
+// token's own pages.  kSplit warps per row.
+template <int kDim, int kSplit>
 __global__ void __launch_bounds__(256)
 merge_rows_kernel(const PrefixParams p, const ListParams own, int cols, int grid_shared) {
+  __shared__ float acc_s[8][kDim + 1];
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (id >= static_cast<int64_t>(p.pv.T) * p.pv.H) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *own.counter = 0;  // for the next call
+  const int64_t rows = static_cast<int64_t>(p.pv.T) * p.pv.H;
+  const int64_t id = min(static_cast<int64_t>(blockIdx.x) * (8 / kSplit) + warp / kSplit, rows - 1);
+  const bool in = static_cast<int64_t>(blockIdx.x) * (8 / kSplit) + warp / kSplit < rows;
   const int t = static_cast<int>(id / p.pv.H), h = static_cast<int>(id % p.pv.H);
   int b, pos;
-  if (!load_paged_token(p.pv, t, nullptr, false, b, pos) || pos < p.pages * p.pv.P) return;
+  const bool ok = load_paged_token(p.pv, t, nullptr, false, b, pos) && pos >= p.pages * p.pv.P;
   const int hk = h / p.group, g = h % p.group;
   const int64_t r = static_cast<int64_t>(t) * p.group + g;
   const int64_t tot = static_cast<int64_t>(p.pv.H_kv) * p.npairs * p.nkt;
   const int64_t item = static_cast<int64_t>(hk) * p.npairs + r / kRows;
   const int a0 = cta_of(item * p.nkt, tot, grid_shared), a1 = cta_of((item + 1) * p.nkt - 1, tot, grid_shared);
   const int64_t u = (static_cast<int64_t>(t) * p.pv.H_kv + hk) * own.gb + g / 64;
-  const int2 rng = own.info[u];
-  const int na = a1 - a0 + 1, total = na + rng.y - rng.x + 1;
-  constexpr int V = kDim / 32;
-  float M = -INFINITY;
+  const int2 rng = ok ? own.info[u] : make_int2(0, -1);
+  const int na = a1 - a0 + 1, total = ok ? na + rng.y - rng.x + 1 : 0;
   auto locate = [&](int k, const float2 *&ml, const float *&o) {
     if (k < na) {
       const int64_t at = (item + a0 + k) * kRows + r % kRows;
@@ -474,39 +474,10 @@ merge_rows_kernel(const PrefixParams p, const ListParams own, int cols, int grid
       o = own.part + at * kDim;
     }
   };
-  for (int k = lane; k < total; k += 32) {
-    const float2 *ml;
-    const float *o;
-    locate(k, ml, o);
-    M = fmaxf(M, ml->x);
-  }
+  float out[kDim / 32];
+  if (!merge_parts<kDim, kSplit>(total, warp % kSplit, lane, locate, acc_s, out) || !ok || !in) return;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[V] = {}, l = 0.f;
-  for (int k0 = 0; k0 < total; k0 += 32) {
-    float a = 0.f, la = 0.f;  // this lane's piece: weight, weighted sum
-    const float *mine = nullptr;
-    if (k0 + lane < total) {
-      const float2 *ml;
-      locate(k0 + lane, ml, mine);
-      const float2 v = *ml;
-      a = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
-      la = a * v.y;
-    }
-    const int n = min(32, total - k0);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float w = __shfl_sync(0xffffffffu, a, k);
-      l += __shfl_sync(0xffffffffu, la, k);
-      const float *o =
-          reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k));
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[V * lane + e], acc[e]);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < V; ++e) own.out[id * kDim + V * lane + e] = __float2bfloat16_rn(acc[e] * inv);
+  for (int e = 0; e < kDim / 32; ++e) own.out[id * kDim + kDim / 32 * lane + e] = __float2bfloat16_rn(out[e]);
 }
 
 size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -584,16 +555,30 @@ cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int share
   // -inf, so a scale of 0 is taken as one too small to tell
   p.qk_scale = pa.scale == 0.f ? 1e-37f : pa.scale * kLog2e;
   p.status = status;
-  const int grid = static_cast<int>(std::min<int64_t>(std::min(sm_count(), kMaxCtas), s.items * s.nkt));
+  // The page list of the sequences' own pages streams from HBM while the shared
+  // part keeps the tensor cores busy: it gets SMs of its own, by the two parts'
+  // tile counts (the own pages taken as half the table's) at about 2.0 us a tile
+  // of 256 rows and 0.9 us a list tile; what it has left is shared out as the
+  // shared part's CTAs leave.
+  const int sms = std::min(sm_count(), kMaxCtas);
+  const double shared_us = 2.0 * static_cast<double>(s.items) * s.nkt;
+  const double own_us = 0.9 * 0.5 * static_cast<double>(pa.T) * pa.H_kv * ((pa.H / pa.H_kv + 63) / 64) *
+                        ((pa.max_pages - shared_pages + s.spt - 1) / s.spt);
+  const int most = std::max(sms / 2, static_cast<int>(sms * shared_us / (shared_us + own_us) + 0.5));
+  const int grid = static_cast<int>(std::min<int64_t>(most, s.items * s.nkt));
   cudaError_t e = pa.D == 128 ? launch_shared<128>(pa, p, grid, stream) : launch_shared<64>(pa, p, grid, stream);
   if (e != cudaSuccess) return e;
   e = launch_page_list(pa, q, own, out, scratch, status, true, stream);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(pa.T) * pa.H;
-  const dim3 blocks(static_cast<unsigned>((rows + 7) / 8));
-  return pa.D == 128
-             ? launch_ex(true, merge_rows_kernel<128>, blocks, dim3(256), 0, stream, 1, p, own, list_cols(pa), grid)
-             : launch_ex(true, merge_rows_kernel<64>, blocks, dim3(256), 0, stream, 1, p, own, list_cols(pa), grid);
+  const bool many = grid >= 8 * s.items;  // pieces of a row's shared part
+  const dim3 blocks(static_cast<unsigned>(many ? rows : (rows + 7) / 8));
+  const int cols = list_cols(pa);
+  if (pa.D == 128)
+    return many ? launch_ex(true, merge_rows_kernel<128, 8>, blocks, dim3(256), 0, stream, 1, p, own, cols, grid)
+                : launch_ex(true, merge_rows_kernel<128, 1>, blocks, dim3(256), 0, stream, 1, p, own, cols, grid);
+  return many ? launch_ex(true, merge_rows_kernel<64, 8>, blocks, dim3(256), 0, stream, 1, p, own, cols, grid)
+              : launch_ex(true, merge_rows_kernel<64, 1>, blocks, dim3(256), 0, stream, 1, p, own, cols, grid);
 }
 
 }  // namespace sa
