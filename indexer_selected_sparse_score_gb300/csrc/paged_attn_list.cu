@@ -69,47 +69,62 @@ struct Record {
 
 template <int N, int kDim>
 struct ListSmem {
-  static constexpr int kStages = kDim == 128 ? 3 : 6;
-  // P^T buffers: with up to 32 heads a second one takes the upper half of the
-  // 128-byte rows
+  // One ring holds the K and V tiles in turn (K(n) is copy 2 n, V(n) copy 2 n +
+  // 1).  Up to 16 heads two CTAs share an SM, half a ring each: a tile's chain of
+  // waits (logits, weights, product) is then longer than its work, and the other
+  // CTA's tiles fill it.
+  static constexpr int kCtas = N == 16 ? 2 : 1;
+  static constexpr int kSlots = (kDim == 128 ? 6 : 12) / kCtas;
+  // P^T: rows of 64 heads in the 128-byte swizzle, with up to 32 heads a second
+  // buffer in the upper half of the rows; up to 16 heads both buffers in rows
+  // of 32 in the 64-byte swizzle.
   static constexpr int kPBufs = N <= 32 ? 2 : 1;
-  // Tile records.  Record n + kStages + 5 is written once S(n + 5) is done,
+  static constexpr uint32_t kPRow = N == 16 ? 64 : 128;
+  // Tile records.  Record n + kSlots / 2 + 5 is written once S(n + 5) is done,
   // for which the weights of tile n + 2 were written and so, with two P^T
   // buffers at most, O(n) issued: every reader (V's loader among them) is past
   // record n.
-  static constexpr int kRecs = kStages + 5;
+  static constexpr int kRecs = kSlots / 2 + 5;
   static constexpr uint32_t kBlock = kTile * 128;          // one 64-dim block of a tile
   static constexpr uint32_t kKv = kBlock * (kDim / 64);
-  static constexpr size_t k = 0;
-  static constexpr size_t v = k + kStages * kKv;
-  static constexpr size_t p = v + kStages * kKv;           // [128 keys][64 heads] bf16
-  static constexpr size_t q = p + 16384;                   // [D / 64][N][128 B]
+  static constexpr size_t ring = 0;
+  static constexpr size_t p = ring + kSlots * kKv;         // [128 keys][kPRow]
+  static constexpr size_t q = p + kTile * kPRow;           // [D / 64][N][128 B]
   static constexpr size_t recs = q + N * kDim * 2;
   static constexpr size_t red = (recs + kRecs * sizeof(Record) + 15) & ~size_t(15);   // [4][N]
   static constexpr size_t fac = red;                       // [N], over the reduction's first row (see below)
   static constexpr size_t mref = red + 4 * N * 4;          // [N]
   static constexpr size_t queue = mref + N * 4;            // [kQueue] page entries waiting for a tile
   static constexpr size_t bars = (queue + kQueue * 4 + 7) & ~size_t(7);
-  static constexpr int kBars = 4 * kStages + 2 + 4 + 2 * kPBufs + 2 + kRecs + 2;
+  static constexpr int kBars = 2 * kSlots + 2 + 4 + 2 * kPBufs + 2 + kRecs + 2;
   static constexpr size_t misc = bars + kBars * 8;
-  static constexpr size_t total = misc + 16;
-  static_assert(total <= 232448, "shared memory budget");
+  static constexpr size_t used = misc + 16;
+  // O^T at dim 64 reads a second block past a V tile (lanes nobody reads)
+  static constexpr size_t total = kDim == 128 || used > p + kBlock ? used : p + kBlock;
+  static_assert(kCtas * (total + 1024) <= 233472, "shared memory budget");
   static_assert(red % 16 == 0 && mref % 16 == 0 && queue % 4 == 0 && bars % 8 == 0 && misc % 8 == 0, "alignment");
-  // O^T at dim 64 reads a second block past V's last slot (lanes nobody reads)
-  static_assert(v + kStages * kKv + kBlock <= total, "V overread stays in bounds");
+  static constexpr uint32_t kCols = N == 16 ? 64 : N == 32 ? 128 : 256;  // tensor memory: S^T twice, O^T
 };
+
+// Byte of a P^T buffer's row `key` at which head `h` of the buffer begins.
+template <int N>
+__device__ __forceinline__ uint32_t p_offset(int key, int buf, int h) {
+  if (N > 16) return sw128_offset(key, 64u * buf + 2u * h);
+  const uint32_t b = 32u * buf + 2u * h;
+  return static_cast<uint32_t>(key) * 64u + ((((b >> 4) ^ (static_cast<uint32_t>(key) >> 1)) & 3u) << 4) + (b & 15u);
+}
 
 __device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
 
 template <int N, int kDim>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, ListSmem<N, kDim>::kCtas)
 page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const ListParams p) {
   using L = ListSmem<N, kDim>;
-  constexpr int kSt = L::kStages, kB = kDim / 64, kPb = L::kPBufs, kRecs = L::kRecs;
+  constexpr int kSl = L::kSlots, kB = kDim / 64, kPb = L::kPBufs, kRecs = L::kRecs;
   constexpr uint32_t kColO = 2 * N;
   extern __shared__ __align__(1024) uint8_t smem[];  // (its alignment is checked below)
-  uint8_t *ks = smem + L::k, *vs = smem + L::v, *ps = smem + L::p, *qs = smem + L::q;
+  uint8_t *ring = smem + L::ring, *ps = smem + L::p, *qs = smem + L::q;
   Record *recs = reinterpret_cast<Record *>(smem + L::recs);
   float *red_s = reinterpret_cast<float *>(smem + L::red);
   float *mref_s = reinterpret_cast<float *>(smem + L::mref);
@@ -118,12 +133,13 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   // next write of red
   float *fac_s = reinterpret_cast<float *>(smem + L::fac);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
-  uint64_t *kfull = bars, *kempty = kfull + kSt, *vfull = kempty + kSt, *vempty = vfull + kSt;
-  uint64_t *qfull = vempty + kSt, *qempty = qfull + 1, *sfull = qempty + 1, *sempty = sfull + 2;
+  uint64_t *full = bars, *empty = full + kSl;  // per ring slot
+  uint64_t *qfull = empty + kSl, *qempty = qfull + 1, *sfull = qempty + 1, *sempty = sfull + 2;
   uint64_t *pfull = sempty + 2, *pempty = pfull + kPb, *ofull = pempty + kPb, *oempty = ofull + 1;
   uint64_t *rfull = oempty + 1, *done = rfull + kRecs;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 4);
+  int *issued_s = reinterpret_cast<int *>(smem + L::misc + 8);  // tiles whose K and whose V were copied
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
@@ -132,11 +148,9 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   }
   pdl_trigger();
   if (tid == 0) {
-    for (int i = 0; i < kSt; ++i) {
-      mbar_init(&kfull[i], 1);
-      mbar_init(&kempty[i], 1);
-      mbar_init(&vfull[i], 1);
-      mbar_init(&vempty[i], 1);
+    for (int i = 0; i < kSl; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
     mbar_init(qfull, 1);
     mbar_init(qempty, 1);
@@ -156,7 +170,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     fence_barrier_init();
   }
   if (warp == kWarpS) {
-    tmem_alloc(tmem_base_s, 256);
+    tmem_alloc(tmem_base_s, L::kCols);
     tmem_relinquish();
   }
   // tiles of token t's units in whole-sequence mode (0 for a token to skip)
@@ -178,7 +192,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     // of all tokens (shared memory of the ring as scratch)
     long long own = 0;
     for (int t = tid; t < p.pv.T; t += kThreads) own += count_of(t, blockIdx.x == 0);
-    block_prefix(own, reinterpret_cast<long long *>(ks), tot);
+    block_prefix(own, reinterpret_cast<long long *>(ring), tot);
     tot *= upt;
   }
   fence_proxy_async();
@@ -189,6 +203,9 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   // parts the tiles are cut into: no more than there are tiles, so that every
   // part between a unit's first and last holds a piece of it
   const int G = static_cast<int>(min(static_cast<long long>(p.parts), max(tot, 1ll)));
+  // Ring copy m: its slot, and the parity of its phase there.
+  auto slot_of = [](int m) { return m % kSl; };
+  auto phase_of = [](int m) { return static_cast<uint32_t>((m / kSl) & 1); };
   auto fail = [&]() {
     raise_flag(p.status, kFlagTimeout);
     *abort_s = 1;
@@ -208,17 +225,16 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       const Record &rec = recs[n % kRecs];
       if (rec.flags & kEnd) break;
       const uint32_t y = rec.y[min(slot, 7)];
-      const int s = n % kSt;
-      ok = mbar_wait_warp(&vempty[s], ((n / kSt) & 1) ^ 1);
+      const int m = 2 * n + 1, s = slot_of(m);
+      ok = mbar_wait_warp(&empty[s], phase_of(m) ^ 1);
       if (!ok || *abort_s) break;
-      if (lane == 0) mbar_expect_tx(&vfull[s], L::kKv);
+      if (lane == 0) mbar_expect_tx(&full[s], L::kKv);
       __syncwarp();
-      if (slot < spt) tma_load_2d(vs + s * L::kKv + dst, &vmap, &vfull[s], 64 * kb, static_cast<int>(y));
+      if (slot < spt) tma_load_2d(ring + s * L::kKv + dst, &vmap, &full[s], 64 * kb, static_cast<int>(y));
     }
     if (lane == 0) {
       if (!ok) fail();
-      // drain: every copy issued lands before the CTA exits
-      for (int i = max(0, n - kSt); i < n; ++i) mbar_wait(&vfull[i % kSt], (i / kSt) & 1);
+      issued_s[1] = n;
     }
     __syncwarp();
   } else if (warp == kWarpK) {
@@ -341,7 +357,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             const int take = min(spt, qe - qh);
             more = qe - qh > take;
             const int ent = slot < take ? queue[qh + slot] : -1;
-            const int s = n % kSt;
+            const int s = slot_of(2 * n);
             // keys present among each 16: lane g's own granule, its page slot
             // held by the lanes of that slot
             const int g = lane & 7, sg = (16 * g) >> p.pv.logP;
@@ -355,13 +371,13 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             // a slot without a page reads past the tensor's end: the copy fills zeros
             const uint32_t y = ent >= 0 ? ((static_cast<uint32_t>(ent) & 0x3FFFFFFFu) * p.pv.H_kv + hk) * p.pv.P
                                         : rows_total;
-            if (!mbar_wait_warp(&kempty[s], ((n / kSt) & 1) ^ 1) || *abort_s) {
+            if (!mbar_wait_warp(&empty[s], phase_of(2 * n) ^ 1) || *abort_s) {
               ok = false;
               break;
             }
-            if (lane == 0) mbar_expect_tx(&kfull[s], L::kKv);
+            if (lane == 0) mbar_expect_tx(&full[s], L::kKv);
             __syncwarp();
-            if (slot < spt) tma_load_2d(ks + s * L::kKv + dst, &kmap, &kfull[s], 64 * kb, static_cast<int>(y));
+            if (slot < spt) tma_load_2d(ring + s * L::kKv + dst, &kmap, &full[s], 64 * kb, static_cast<int>(y));
             Record &rec = recs[n % kRecs];
             if (slot < 8 && kb == 0) rec.y[slot] = y;
             if (lane == 0) {
@@ -420,7 +436,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       } else {
         fail();
       }
-      for (int i = max(0, n - kSt); i < n; ++i) mbar_wait(&kfull[i % kSt], (i / kSt) & 1);
+      issued_s[0] = n;
       if (qn > 0) mbar_wait(qfull, (qn - 1) & 1);
     }
     __syncwarp();
@@ -435,13 +451,13 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       if (!ok) break;
       const int flags = recs[n % kRecs].flags;
       if (flags & kEnd) break;
-      const int s = n % kSt, bf = n & 1;
+      const int s = slot_of(2 * n), bf = n & 1;
       if (flags & kFirst) ok = mbar_wait_warp(qfull, (qn++) & 1);
-      ok = ok && mbar_wait_warp(&kfull[s], (n / kSt) & 1) && mbar_wait_warp(&sempty[bf], ((n >> 1) & 1) ^ 1);
+      ok = ok && mbar_wait_warp(&full[s], phase_of(2 * n)) && mbar_wait_warp(&sempty[bf], ((n >> 1) & 1) ^ 1);
       if (!ok || *abort_s) break;
       tc_fence_after();
       if (leader) {
-        const uint64_t da = desc_sw128_kmajor(smem_u32(ks + s * L::kKv)), db = desc_sw128_kmajor(smem_u32(qs));
+        const uint64_t da = desc_sw128_kmajor(smem_u32(ring + s * L::kKv)), db = desc_sw128_kmajor(smem_u32(qs));
 #pragma unroll
         for (int kk = 0; kk < kDim / 16; ++kk) {
           const uint64_t ao = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
@@ -449,7 +465,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           mma_f16(tmem + N * bf, da + ao, db + bo, idesc, kk > 0);
         }
         mma_commit(&sfull[bf]);
-        mma_commit(&kempty[s]);
+        mma_commit(&empty[s]);
         if (flags & kLast) mma_commit(qempty);
       }
       __syncwarp();
@@ -471,19 +487,19 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       if (!ok) break;
       const int flags = recs[n % kRecs].flags;
       if (flags & kEnd) break;
-      const int s = n % kSt, pb = n % kPb;
+      const int s = slot_of(2 * n + 1), pb = n % kPb;
       if (flags & kFirst) ok = mbar_wait_warp(oempty, (pieces++ & 1) ^ 1);
-      ok = ok && mbar_wait_warp(&vfull[s], (n / kSt) & 1) && mbar_wait_warp(&pfull[pb], (n / kPb) & 1);
+      ok = ok && mbar_wait_warp(&full[s], phase_of(2 * n + 1)) && mbar_wait_warp(&pfull[pb], (n / kPb) & 1);
       if (!ok || *abort_s) break;
       tc_fence_after();
       if (leader) {
-        const uint64_t da = desc_mn(smem_u32(vs + s * L::kKv), L::kBlock), db = desc_mn(smem_u32(ps) + 64 * pb, 16384);
+        const uint64_t da = desc_mn(smem_u32(ring + s * L::kKv), L::kBlock);
+        const uint64_t db = N == 16 ? desc_mn64(smem_u32(ps) + 32 * pb) : desc_mn(smem_u32(ps) + 64 * pb, 16384);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk) {
-          const uint64_t o = (kk * 2048) >> 4;
-          mma_f16(tmem + kColO, da + o, db + o, idesc, !((flags & kFirst) && kk == 0));
+          mma_f16(tmem + kColO, da + ((kk * 2048) >> 4), db + ((kk * 16 * L::kPRow) >> 4), idesc, !((flags & kFirst) && kk == 0));
         }
-        mma_commit(&vempty[s]);
+        mma_commit(&empty[s]);
         mma_commit(&pempty[pb]);
         if (flags & kLast) mma_commit(ofull);
       }
@@ -515,7 +531,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       Record rec{};
       if (ok) rec = recs[n % kRecs];
       const bool end = (rec.flags & kEnd) != 0;
-      const int bf = n & 1, s = n % kSt;
+      const int bf = n & 1, s = slot_of(2 * n + 1);
       const bool first = (rec.flags & kFirst) != 0;
       const uint32_t word = key < 64 ? rec.cnt[0] : rec.cnt[1];
       const bool present = static_cast<uint32_t>(key & 15) < ((word >> (8 * ((key >> 4) & 3))) & 0xFFu);
@@ -608,20 +624,20 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           *l2 = add2(*l2, e2);
           w[q] = pack_bf16x2(e2.x, e2.y);
         }
-        *reinterpret_cast<uint4 *>(ps + sw128_offset(key, 64u * pb + 2u * hb + 16u * ch)) =
+        *reinterpret_cast<uint4 *>(ps + p_offset<N>(key, pb, hb + 8 * ch)) =
             make_uint4(w[0], w[1], w[2], w[3]);
       }
       if (rec.flags & kMasked) {
         // positions past the token's own may hold anything: their V rows
         // become zeros before the product reads them (each half of the heads'
         // threads half of the row)
-        if (!mbar_wait_warp(&vfull[s], (n / kSt) & 1) && lane == 0) fail();
+        if (!mbar_wait_warp(&full[s], phase_of(2 * n + 1)) && lane == 0) fail();
         if (!present) {
           constexpr int kChunks = kDim / 16;  // 16-byte chunks of half a row
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
             const int ch = (hb ? kChunks : 0) + i;
-            *reinterpret_cast<uint4 *>(vs + s * L::kKv + (ch >> 3) * L::kBlock + key * 128 + 16 * (ch & 7)) =
+            *reinterpret_cast<uint4 *>(ring + s * L::kKv + (ch >> 3) * L::kBlock + key * 128 + 16 * (ch & 7)) =
                 make_uint4(0, 0, 0, 0);
           }
         }
@@ -680,9 +696,17 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   if (p.keep) pdl_wait();
   tc_fence_before();
   __syncthreads();
+  if (tid < kSl) {
+    // every copy lands before the CTA exits: the last one issued into slot tid
+    // (long done unless a wait gave up)
+    int m = 2 * max(issued_s[0], issued_s[1]) + kSl;
+    m -= (m - tid) % kSl;
+    while (m >= 0 && m / 2 >= issued_s[m & 1]) m -= kSl;
+    if (m >= 0) mbar_wait(&full[tid], phase_of(m));
+  }
   if (warp == kWarpS) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, L::kCols);
   }
 }
 
@@ -766,12 +790,15 @@ int list_cols(const sa_paged_args &pa) {
   return g <= 16 ? 16 : g <= 32 ? 32 : 64;
 }
 
+// Most CTAs of a grid (two to an SM with up to 16 heads).
+static int list_ctas(const sa_paged_args &pa) { return list_cols(pa) == 16 ? 512 : 256; }
+
 size_t list_scratch(const sa_paged_args &pa, bool keep) {
   const int g = pa.H / pa.H_kv;
   const size_t units = static_cast<size_t>(pa.T) * pa.H_kv * ((g + 63) / 64);
-  const size_t slots = keep ? units + kMaxParts : 2 * kMaxCtas;
+  const size_t slots = keep ? units + kMaxParts : 2 * list_ctas(pa);
   return round_up(slots * list_cols(pa) * pa.D * sizeof(float)) + round_up(slots * list_cols(pa) * sizeof(float2)) +
-         round_up((keep ? units : kMaxCtas) * sizeof(int2));
+         round_up((keep ? units : list_ctas(pa)) * sizeof(int2));
 }
 
 cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams &p, void *out, void *scratch,
@@ -783,14 +810,14 @@ cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams 
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.status = status;
   const size_t units = static_cast<size_t>(pa.T) * pa.H_kv * p.gb;
-  const size_t slots = p.keep ? units + kMaxParts : 2 * kMaxCtas;
+  const size_t slots = p.keep ? units + kMaxParts : 2 * list_ctas(pa);
   char *w = static_cast<char *>(scratch);
   p.part = reinterpret_cast<float *>(w);
   w += round_up(slots * list_cols(pa) * pa.D * sizeof(float));
   p.ml = reinterpret_cast<float2 *>(w);
   w += round_up(slots * list_cols(pa) * sizeof(float2));
   p.info = p.cut = reinterpret_cast<int2 *>(w);
-  int grid = std::min(sm_count(), kMaxCtas);
+  int grid = std::min(sm_count() * (list_cols(pa) == 16 ? 2 : 1), list_ctas(pa));
   if (!p.whole) {
     const int spt = kTile / pa.P;
     const int64_t entries = static_cast<int64_t>(p.K) + std::min(p.local, pa.max_pages);

@@ -39,6 +39,7 @@ using namespace umma;
 constexpr int kTile = 128;      // keys per tile, rows per row tile
 constexpr int kRows = 256;      // rows per item
 constexpr int kThreads = 384;
+constexpr int kMaxCtas = 256;   // one CTA per SM
 constexpr int kWarpMma = 8;     // and 9: the issuers of row tiles A and B
 constexpr int kWarpLoad = 10;   // (warp 11 only joins the block barriers)
 constexpr int kSlots = 5;       // ring of K and V tiles: K(0), V(0), K(1), ...

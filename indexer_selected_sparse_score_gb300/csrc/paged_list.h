@@ -6,7 +6,6 @@
 
 namespace sa {
 
-constexpr int kMaxCtas = 256;    // most CTAs of a grid that shares tiles out
 constexpr int kMaxParts = 1024;  // most parts of a claimed list
 // Word of the workspace header that counts claimed parts: 0 between calls (the
 // merge that ends a call resets it).

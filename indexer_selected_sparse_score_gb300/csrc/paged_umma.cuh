@@ -79,6 +79,18 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
   return d;
 }
 
+// The same in the 64-byte swizzle: rows of 32 values, 8-row atoms 512 B apart
+// (one block of 32 values).
+__device__ __forceinline__ uint64_t desc_mn64(uint32_t addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(512 >> 4) << 16;
+  d |= static_cast<uint64_t>(512 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(4) << 61;
+  return d;
+}
+
 // 2^x by the hardware approximation (relative error about 2^-22; results
 // below 2^-126 flush to zero).
 __device__ __forceinline__ float exp2_hw(float x) {
