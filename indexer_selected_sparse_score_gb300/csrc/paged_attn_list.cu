@@ -7,9 +7,9 @@
 // the keys in the 128 lanes of the accumulator and the heads in its columns,
 // and no row of the tensor core is spent on padding:
 //   S^T = K Q^T     M = 128 keys, N = heads (16, 32 or 64), K = D
-//   P^T             two threads per key, each half of the heads: p = 2^(c s -
-//                   m_ref[h]), bf16, to shared memory with the heads contiguous
-//                   (the MN-major B operand)
+//   P^T             one thread per key, or two with half of the heads each: p =
+//                   2^(c s - m_ref[h]), bf16, to shared memory with the heads
+//                   contiguous (the MN-major B operand)
 //   O^T += V^T P^T  M = D, N = heads, K = 128 keys
 // The pages land by TMA in the 128-byte swizzle, which is K-major for the
 // first product and MN-major for the second, so K and V are copied once and
@@ -29,8 +29,9 @@
 // own are masked, and the V rows they hold are zeroed in shared memory, since
 // 0 x NaN would reach the sum.
 //
-// Warps: 0-7 softmax and output; 8 issues S^T, 9 issues O^T; 10 resolves the
-// lists, copies K and publishes one record per tile; 11 copies V.  Every wait is
+// Warps: 0-3 or 0-7 softmax and output; the next two issue S^T and O^T; then one
+// resolves the lists, copies K and publishes one record per tile; the last
+// copies V.  Every wait is
 // bounded; on expiry the kernel flags the status word, drains its copies and
 // products and returns.
 #include <cudaTypedefs.h>
@@ -48,9 +49,6 @@ namespace {
 using namespace umma;
 
 constexpr int kTile = 128;      // keys per tile
-constexpr int kThreads = 384;
-constexpr int kSoftmax = 256;   // threads of the softmax warps, 0-7
-constexpr int kWarpS = 8, kWarpO = 9, kWarpK = 10, kWarpV = 11;
 constexpr int kQueue = 40;      // page entries the loader holds: under a tile's and one batch of 32
 // The reference a weight is taken against lies kHead above the maximum that
 // set it (log2 units), and is raised once a logit passes that maximum by kLazy:
@@ -74,6 +72,10 @@ struct ListSmem {
   // waits (logits, weights, product) is then longer than its work, and the other
   // CTA's tiles fill it.
   static constexpr int kCtas = N == 16 ? 2 : 1;
+  // Softmax warps: a thread takes one key and all heads (up to 16) or half of
+  // them; then the two issuers and the two loaders.
+  static constexpr int kSoftmaxWarps = N == 16 ? 4 : 8;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kSlots = (kDim == 128 ? 6 : 12) / kCtas;
   // P^T: rows of 64 heads in the 128-byte swizzle, with up to 32 heads a second
   // buffer in the upper half of the rows; up to 16 heads both buffers in rows
@@ -114,15 +116,21 @@ __device__ __forceinline__ uint32_t p_offset(int key, int buf, int h) {
   return static_cast<uint32_t>(key) * 64u + ((((b >> 4) ^ (static_cast<uint32_t>(key) >> 1)) & 3u) << 4) + (b & 15u);
 }
 
-__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
+// Barrier of the softmax warps.
+template <int kSoftmax>
+__device__ __forceinline__ void group_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory");
+}
 
 template <int N, int kDim>
-__global__ void __launch_bounds__(kThreads, ListSmem<N, kDim>::kCtas)
+__global__ void __launch_bounds__(ListSmem<N, kDim>::kThreads, ListSmem<N, kDim>::kCtas)
 page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const ListParams p) {
   using L = ListSmem<N, kDim>;
   constexpr int kSl = L::kSlots, kB = kDim / 64, kPb = L::kPBufs, kRecs = L::kRecs;
   constexpr uint32_t kColO = 2 * N;
+  constexpr int kSoftmax = 32 * L::kSoftmaxWarps, kThreads = L::kThreads;
+  constexpr int kWarpS = L::kSoftmaxWarps, kWarpO = kWarpS + 1, kWarpK = kWarpS + 2, kWarpV = kWarpS + 3;
   extern __shared__ __align__(1024) uint8_t smem[];  // (its alignment is checked below)
   uint8_t *ring = smem + L::ring, *ps = smem + L::p, *qs = smem + L::q;
   Record *recs = reinterpret_cast<Record *>(smem + L::recs);
@@ -513,10 +521,10 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     __syncwarp();
   } else {
     // ----------------------------------------------------------------- softmax
-    // Thread: one key of the tile (the accumulator lane) and half of the heads.
+    // Thread: one key of the tile (the accumulator lane) and NH of the heads.
     // The logits' arguments are formed once, tested against the reference, and
     // only then raised to weights.
-    constexpr int NH = N / 2;
+    constexpr int NH = 4 * N / L::kSoftmaxWarps;
     const int quarter = warp & 3, key = tid & 127, hb = warp >= 4 ? NH : 0;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const float cs = p.qk_scale;
@@ -571,7 +579,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         for (int h = 0; h < NH; ++h) x[h] = present ? (first ? v[h] * cs : v[h]) : -INFINITY;
         const float top = reduce_scatter<true>(x, lane);
         if (lane < NH) red_w[lane] = top;
-        group_sync();
+        group_sync<kSoftmax>();
         if (tid < N) {
           const float mo = first ? 0.f : mref_s[tid];
           const float mt = fmaxf(fmaxf(red_s[tid], red_s[N + tid]), fmaxf(red_s[2 * N + tid], red_s[3 * N + tid]));
@@ -580,7 +588,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           fac_s[tid] = up;
           mref_s[tid] = mo + up;
         }
-        group_sync();
+        group_sync<kSoftmax>();
 #pragma unroll
         for (int h = 0; h < NH; ++h) v[h] = (first ? v[h] * cs : v[h]) - fac_s[hb + h];
         if (!first) {
@@ -629,11 +637,11 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       }
       if (rec.flags & kMasked) {
         // positions past the token's own may hold anything: their V rows
-        // become zeros before the product reads them (each half of the heads'
-        // threads half of the row)
+        // become zeros before the product reads them (each thread its
+        // share of the row)
         if (!mbar_wait_warp(&full[s], phase_of(2 * n + 1)) && lane == 0) fail();
         if (!present) {
-          constexpr int kChunks = kDim / 16;  // 16-byte chunks of half a row
+          constexpr int kChunks = kDim / 8 * NH / N;  // 16-byte chunks of this thread's share of the row
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
             const int ch = (hb ? kChunks : 0) + i;
@@ -649,18 +657,18 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         // sums over the keys while the last product runs (the barrier: a raise
         // in this tile still reads fac, which lies over the reduction's rows)
         const float sum_w = reduce_scatter<false>(l, lane);
-        group_sync();
+        group_sync<kSoftmax>();
         if (lane < NH) red_w[lane] = sum_w;
 #pragma unroll
         for (int h = 0; h < NH; ++h) l[h] = 0.f;
-        group_sync();
+        group_sync<kSoftmax>();
         if (tid < N) {
           const float sum = (red_s[tid] + red_s[N + tid]) + (red_s[2 * N + tid] + red_s[3 * N + tid]);
           fac_s[tid] = sum > 0.f ? 1.f / sum : 0.f;
           if (!(rec.flags & kDirect))
             p.ml[static_cast<int64_t>(rec.slot) * N + tid] = make_float2(mref_s[tid], sum);
         }
-        group_sync();
+        group_sync<kSoftmax>();
         if (!mbar_wait_warp(ofull, pieces & 1) && lane == 0) fail();
         ++pieces;
         tc_fence_after();
@@ -752,7 +760,7 @@ cudaError_t launch_list(const sa_paged_args &pa, const void *q, ListParams &p, i
   static bool attr_done[64] = {};
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, attr_done);
   if (e != cudaSuccess) return e;
-  e = launch_ex(pdl, kern, dim3(grid), dim3(kThreads), smem, stream, 1, qmap, kmap, vmap, p);
+  e = launch_ex(pdl, kern, dim3(grid), dim3(L::kThreads), smem, stream, 1, qmap, kmap, vmap, p);
   if (e != cudaSuccess || p.keep) return e;
   const int64_t units = static_cast<int64_t>(pa.T) * pa.H_kv * p.gb;
   return units * 8 <= grid
