@@ -22,7 +22,7 @@
 // Work: the tiles of all units (128 keys each) form one list, cut evenly into
 // parts: one for each CTA, one CTA per SM (a decode step reads each page once,
 // so HBM is the bound and every SM must stream to the end); beside the product
-// with the shared pages, whose CTAs leave their SMs at different times, four
+// with the shared pages, whose CTAs leave their SMs at different times, eight
 // per SM that CTAs claim.  A unit that falls into several CTAs
 // leaves its parts (m_ref, sum, O) in scratch for a merge kernel.  Entries that
 // name no page are dropped before tiles are formed; positions past the token's
@@ -67,8 +67,9 @@ struct Record {
 
 template <int N, int kDim>
 struct ListSmem {
-  // One ring holds the K and V tiles in turn (K(n) is copy 2 n, V(n) copy 2 n +
-  // 1).  Up to 16 heads two CTAs share an SM, half a ring each: a tile's chain of
+  // One ring holds the K and V tiles, in the order K(0), K(1), V(0), K(2), V(1),
+  // ..: a V tile is needed a softmax later than its K, and with three slots it
+  // takes the very slot that its K leaves.  Up to 16 heads two CTAs share an SM, half a ring each: a tile's chain of
   // waits (logits, weights, product) is then longer than its work, and the other
   // CTA's tiles fill it.
   static constexpr int kCtas = N == 16 ? 2 : 1;
@@ -147,7 +148,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   uint64_t *rfull = oempty + 1, *done = rfull + kRecs;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 4);
-  int *issued_s = reinterpret_cast<int *>(smem + L::misc + 8);  // tiles whose K and whose V were copied
+  volatile int *issued_s = reinterpret_cast<volatile int *>(smem + L::misc + 8);  // tiles whose K and whose V were copied
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
@@ -175,6 +176,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     mbar_init(oempty, kSoftmax / 32);
     for (int i = 0; i < kRecs; ++i) mbar_init(&rfull[i], 1);
     *abort_s = 0;
+    issued_s[0] = issued_s[1] = 0;
     fence_barrier_init();
   }
   if (warp == kWarpS) {
@@ -211,7 +213,10 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   // parts the tiles are cut into: no more than there are tiles, so that every
   // part between a unit's first and last holds a piece of it
   const int G = static_cast<int>(min(static_cast<long long>(p.parts), max(tot, 1ll)));
-  // Ring copy m: its slot, and the parity of its phase there.
+  // Place of K(n) and V(n) in the ring's order, the slot of place m and the
+  // parity of its phase there.
+  auto place_k = [](int n) { return n == 0 ? 0 : 2 * n - 1; };
+  auto place_v = [](int n) { return 2 * n + 2; };
   auto slot_of = [](int m) { return m % kSl; };
   auto phase_of = [](int m) { return static_cast<uint32_t>((m / kSl) & 1); };
   auto fail = [&]() {
@@ -233,17 +238,15 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       const Record &rec = recs[n % kRecs];
       if (rec.flags & kEnd) break;
       const uint32_t y = rec.y[min(slot, 7)];
-      const int m = 2 * n + 1, s = slot_of(m);
+      const int m = place_v(n), s = slot_of(m);
       ok = mbar_wait_warp(&empty[s], phase_of(m) ^ 1);
       if (!ok || *abort_s) break;
       if (lane == 0) mbar_expect_tx(&full[s], L::kKv);
       __syncwarp();
       if (slot < spt) tma_load_2d(ring + s * L::kKv + dst, &vmap, &full[s], 64 * kb, static_cast<int>(y));
+      if (lane == 0) issued_s[1] = n + 1;
     }
-    if (lane == 0) {
-      if (!ok) fail();
-      issued_s[1] = n;
-    }
+    if (lane == 0 && !ok) fail();
     __syncwarp();
   } else if (warp == kWarpK) {
     // ---------------------------------------------- loader of K, Q; the lists
@@ -365,7 +368,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             const int take = min(spt, qe - qh);
             more = qe - qh > take;
             const int ent = slot < take ? queue[qh + slot] : -1;
-            const int s = slot_of(2 * n);
+            const int m = place_k(n), s = slot_of(m);
             // keys present among each 16: lane g's own granule, its page slot
             // held by the lanes of that slot
             const int g = lane & 7, sg = (16 * g) >> p.pv.logP;
@@ -379,7 +382,16 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             // a slot without a page reads past the tensor's end: the copy fills zeros
             const uint32_t y = ent >= 0 ? ((static_cast<uint32_t>(ent) & 0x3FFFFFFFu) * p.pv.H_kv + hk) * p.pv.P
                                         : rows_total;
-            if (!mbar_wait_warp(&empty[s], phase_of(2 * n) ^ 1) || *abort_s) {
+            // With an odd number of slots the phase before V(n - 3)'s in this
+            // slot is K(n - 3)'s: the parity tells them apart once V(n - 3) has
+            // been issued.
+            bool mine = true;
+            if ((kSl & 1) != 0 && n >= 3) {
+              const long long since = clock64();
+              while (mine && issued_s[1] < n - 2) mine = clock64() - since < kWaitBudgetCycles && !*abort_s;
+              mine = __all_sync(0xffffffffu, mine);
+            }
+            if (!mine || !mbar_wait_warp(&empty[s], phase_of(m) ^ 1) || *abort_s) {
               ok = false;
               break;
             }
@@ -459,9 +471,9 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       if (!ok) break;
       const int flags = recs[n % kRecs].flags;
       if (flags & kEnd) break;
-      const int s = slot_of(2 * n), bf = n & 1;
+      const int m = place_k(n), s = slot_of(m), bf = n & 1;
       if (flags & kFirst) ok = mbar_wait_warp(qfull, (qn++) & 1);
-      ok = ok && mbar_wait_warp(&full[s], phase_of(2 * n)) && mbar_wait_warp(&sempty[bf], ((n >> 1) & 1) ^ 1);
+      ok = ok && mbar_wait_warp(&full[s], phase_of(m)) && mbar_wait_warp(&sempty[bf], ((n >> 1) & 1) ^ 1);
       if (!ok || *abort_s) break;
       tc_fence_after();
       if (leader) {
@@ -495,9 +507,11 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       if (!ok) break;
       const int flags = recs[n % kRecs].flags;
       if (flags & kEnd) break;
-      const int s = slot_of(2 * n + 1), pb = n % kPb;
+      const int m = place_v(n), s = slot_of(m), pb = n % kPb;
       if (flags & kFirst) ok = mbar_wait_warp(oempty, (pieces++ & 1) ^ 1);
-      ok = ok && mbar_wait_warp(&full[s], phase_of(2 * n + 1)) && mbar_wait_warp(&pfull[pb], (n / kPb) & 1);
+      // (the weights first: they say that K(n), perhaps the slot's phase before,
+      // is done with)
+      ok = ok && mbar_wait_warp(&pfull[pb], (n / kPb) & 1) && mbar_wait_warp(&full[s], phase_of(m));
       if (!ok || *abort_s) break;
       tc_fence_after();
       if (leader) {
@@ -539,7 +553,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       Record rec{};
       if (ok) rec = recs[n % kRecs];
       const bool end = (rec.flags & kEnd) != 0;
-      const int bf = n & 1, s = slot_of(2 * n + 1);
+      const int bf = n & 1, s = slot_of(place_v(n));
       const bool first = (rec.flags & kFirst) != 0;
       const uint32_t word = key < 64 ? rec.cnt[0] : rec.cnt[1];
       const bool present = static_cast<uint32_t>(key & 15) < ((word >> (8 * ((key >> 4) & 3))) & 0xFFu);
@@ -639,7 +653,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         // positions past the token's own may hold anything: their V rows
         // become zeros before the product reads them (each thread its
         // share of the row)
-        if (!mbar_wait_warp(&full[s], phase_of(2 * n + 1)) && lane == 0) fail();
+        if (!mbar_wait_warp(&full[s], phase_of(place_v(n))) && lane == 0) fail();
         if (!present) {
           constexpr int kChunks = kDim / 8 * NH / N;  // 16-byte chunks of this thread's share of the row
 #pragma unroll
@@ -707,9 +721,12 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   if (tid < kSl) {
     // every copy lands before the CTA exits: the last one issued into slot tid
     // (long done unless a wait gave up)
-    int m = 2 * max(issued_s[0], issued_s[1]) + kSl;
+    auto issued = [&](int m) {
+      return m == 0 ? issued_s[0] > 0 : (m & 1) ? (m + 1) / 2 < issued_s[0] : (m - 2) / 2 < issued_s[1];
+    };
+    int m = 2 * max(issued_s[0], issued_s[1]) + 2 + kSl;
     m -= (m - tid) % kSl;
-    while (m >= 0 && m / 2 >= issued_s[m & 1]) m -= kSl;
+    while (m >= 0 && !issued(m)) m -= kSl;
     if (m >= 0) mbar_wait(&full[tid], phase_of(m));
   }
   if (warp == kWarpS) {
@@ -832,7 +849,7 @@ cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams 
     p.tpu = static_cast<int>(std::max<int64_t>(1, (entries + spt - 1) / spt));
     grid = static_cast<int>(std::min<int64_t>(grid, static_cast<int64_t>(units) * p.tpu));
   }
-  p.parts = p.keep ? std::min(4 * sm_count(), kMaxParts) : grid;
+  p.parts = p.keep ? std::min(8 * sm_count(), kMaxParts) : grid;
   p.counter = p.keep ? status + kCounterWord : nullptr;
   return pa.D == 128 ? launch_dim<128>(pa, q, p, grid, pdl, stream) : launch_dim<64>(pa, q, p, grid, pdl, stream);
 }

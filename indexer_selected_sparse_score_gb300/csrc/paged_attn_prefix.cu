@@ -316,19 +316,26 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (first) r = static_cast<int64_t>(at.item % p.npairs) * kRows + 128 * w + row;
       if (r - row >= p.rows) continue;
       if (first) {
-        // this thread's query row, into the K-major swizzled layout (every
-        // product of the piece before has been read out)
+        // the warp's 32 query rows, into the K-major swizzled layout (every
+        // product of the piece before has been read out); a load covers whole rows
         const int hk = at.item / p.npairs;
-        const bool in = r < p.rows;
-        const int64_t t = r / p.group;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (t * p.pv.H + static_cast<int64_t>(hk) * p.group + (r - t * p.group)) * kDim);
-        uint4 v[kDim / 8];
+        const int64_t r0 = r - row + 32 * (warp & 3);
+        constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a load
+        uint4 v[32 / kPer];
 #pragma unroll
-        for (int i = 0; i < kDim / 8; ++i) v[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const int64_t rr = r0 + kPer * i + lane / kLanes;
+          const int t = static_cast<int>(rr) / p.group;
+          const int64_t src = static_cast<int64_t>(t) * p.pv.H + static_cast<int64_t>(hk) * p.group + (rr - static_cast<int64_t>(t) * p.group);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (rr < p.rows) v[i] = reinterpret_cast<const uint4 *>(p.q + src * kDim)[lane % kLanes];
+        }
 #pragma unroll
-        for (int i = 0; i < kDim / 8; ++i)
-          *reinterpret_cast<uint4 *>(qt + (i >> 3) * L::kBlock + sw128_offset(row, 16u * (i & 7))) = v[i];
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const int ch = lane % kLanes;
+          *reinterpret_cast<uint4 *>(qt + (ch >> 3) * L::kBlock +
+                                     sw128_offset(32 * (warp & 3) + kPer * i + lane / kLanes, 16u * (ch & 7))) = v[i];
+        }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[w]);
@@ -416,18 +423,32 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         tc_fence_after();
         const int64_t to_row = static_cast<int64_t>(at.item + c) * kRows + 128 * w + row;
         if (r < p.rows) p.ml[to_row] = make_float2(ref, l);
+        // O of the warp's rows, 32 columns at a time through this warp's part of
+        // the query tile (its products are done), so that a store covers 128
+        // contiguous bytes of each of four rows
+        float4 *stage = reinterpret_cast<float4 *>(qt + (warp & 3) * 4096);
+        const int64_t row0 = to_row - lane;
+        const int64_t valid = p.rows - (r - lane);  // rows of this warp
 #pragma unroll 1
         for (int i = 0; i < kDim / 32; ++i) {
           uint32_t o[32];
           tmem_load(to + 32 * i, o);
           tmem_ld_wait();
-          if (r < p.rows) {
+          __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4 *>(p.part + to_row * kDim + 32 * i + 4 * e) =
-                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 8; ++e)
+            stage[8 * lane + (e ^ (lane & 7))] =
+                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                            __uint_as_float(o[4 * e + 3]));
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int rr = 4 * e + (lane >> 3), ch = lane & 7;
+            if (rr < valid)
+              *reinterpret_cast<float4 *>(p.part + (row0 + rr) * kDim + 32 * i + 4 * ch) = stage[8 * rr + (ch ^ (rr & 7))];
           }
         }
+        __syncwarp();
         tc_fence_before();
       }
     }
@@ -558,12 +579,12 @@ cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int share
   p.status = status;
   // The page list of the sequences' own pages streams from HBM while the shared
   // part keeps the tensor cores busy: it gets SMs of its own, by the two parts'
-  // tile counts (the own pages taken as half the table's) at about 2.0 us a tile
-  // of 256 rows and 0.9 us a list tile; what it has left is shared out as the
+  // tile counts (the own pages taken as half the table's) at about 1.7 us a tile
+  // of 256 rows and 0.9 us a list tile (2.2 with many heads); what it has left is shared out as the
   // shared part's CTAs leave.
   const int sms = std::min(sm_count(), kMaxCtas);
-  const double shared_us = 2.0 * static_cast<double>(s.items) * s.nkt;
-  const double own_us = 0.9 * 0.5 * static_cast<double>(pa.T) * pa.H_kv * ((pa.H / pa.H_kv + 63) / 64) *
+  const double shared_us = 1.7 * static_cast<double>(s.items) * s.nkt;
+  const double own_us = (list_cols(pa) == 16 ? 0.9 : 2.2) * 0.5 * static_cast<double>(pa.T) * pa.H_kv * ((pa.H / pa.H_kv + 63) / 64) *
                         ((pa.max_pages - shared_pages + s.spt - 1) / s.spt);
   const int most = std::max(sms / 2, static_cast<int>(sms * shared_us / (shared_us + own_us) + 0.5));
   const int grid = static_cast<int>(std::min<int64_t>(most, s.items * s.nkt));

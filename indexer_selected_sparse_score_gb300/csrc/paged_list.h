@@ -6,7 +6,7 @@
 
 namespace sa {
 
-constexpr int kMaxParts = 1024;  // most parts of a claimed list
+constexpr int kMaxParts = 2048;  // most parts of a claimed list
 // Word of the workspace header that counts claimed parts: 0 between calls (the
 // merge that ends a call resets it).
 constexpr int kCounterWord = 16;
