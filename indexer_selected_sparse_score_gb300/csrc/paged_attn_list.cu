@@ -22,7 +22,7 @@
 // Work: the tiles of all units (128 keys each) form one list, cut evenly into
 // parts: one for each CTA, one CTA per SM (a decode step reads each page once,
 // so HBM is the bound and every SM must stream to the end); beside the product
-// with the shared pages, whose CTAs leave their SMs at different times, eight
+// with the shared pages, whose CTAs leave their SMs at different times, four
 // per SM that CTAs claim.  A unit that falls into several CTAs
 // leaves its parts (m_ref, sum, O) in scratch for a merge kernel.  Entries that
 // name no page are dropped before tiles are formed; positions past the token's
@@ -741,7 +741,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 template <int N, int kDim, int kSplit>
 __global__ void __launch_bounds__(256)
 merge_cut_kernel(const ListParams p) {
-  __shared__ float acc_s[8][kDim + 1];
+  __shared__ float acc_s[8][kDim + 2];
   pdl_wait();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int2 cut = p.cut[c];
@@ -749,18 +749,11 @@ merge_cut_kernel(const ListParams p) {
   const int upt = p.pv.H_kv * p.gb, t = cut.x / upt, sub = cut.x % upt;
   const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64, heads = min(64, (hk + 1) * p.group - h0);
   const int i = blockIdx.y * (8 / kSplit) + warp / kSplit;
-  if (kSplit == 1 && i >= heads) return;
-  const int row = min(i, N - 1);
-  auto locate = [&](int k, const float2 *&ml, const float *&o) {
-    const int64_t at = static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * N + row;
-    ml = p.ml + at;
-    o = p.part + at * kDim;
-  };
-  float out[kDim / 32];
-  if (!merge_parts<kDim, kSplit>(cut.y - c + 1, warp % kSplit, lane, locate, acc_s, out) || i >= heads) return;
-#pragma unroll
-  for (int e = 0; e < kDim / 32; ++e)
-    p.out[(static_cast<int64_t>(t) * p.pv.H + h0 + i) * kDim + kDim / 32 * lane + e] = __float2bfloat16_rn(out[e]);
+  if (i >= heads) return;  // (kSplit 8: the whole block)
+  Merge<kDim> m;
+  m.add(warp % kSplit, kSplit, cut.y - c + 1, lane, p.ml, p.part,
+        [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * N + i; });
+  if (m.template join<kSplit>(acc_s, lane)) m.store(p.out + (static_cast<int64_t>(t) * p.pv.H + h0 + i) * kDim, lane);
 }
 
 template <int N, int kDim>
@@ -849,7 +842,7 @@ cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams 
     p.tpu = static_cast<int>(std::max<int64_t>(1, (entries + spt - 1) / spt));
     grid = static_cast<int>(std::min<int64_t>(grid, static_cast<int64_t>(units) * p.tpu));
   }
-  p.parts = p.keep ? std::min(8 * sm_count(), kMaxParts) : grid;
+  p.parts = p.keep ? std::min(4 * sm_count(), kMaxParts) : grid;
   p.counter = p.keep ? status + kCounterWord : nullptr;
   return pa.D == 128 ? launch_dim<128>(pa, q, p, grid, pdl, stream) : launch_dim<64>(pa, q, p, grid, pdl, stream);
 }

@@ -144,12 +144,33 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     tmem_alloc(tmem_base_s, 512);
     tmem_relinquish();
   }
+  const int64_t tot = static_cast<int64_t>(p.pv.H_kv) * p.npairs * p.nkt;
+  const int64_t x0 = tot * c / G, x1 = tot * (c + 1) / G;
+  // A softmax warp's 32 query rows of an item, into the K-major swizzled layout;
+  // a load covers whole rows.
+  auto load_queries = [&](int item) {
+    constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a load
+    const int hk = item / p.npairs, row0 = 32 * (warp & 3), ch = lane % kLanes;
+    const int64_t r0 = static_cast<int64_t>(item - hk * p.npairs) * kRows + 128 * (warp >> 2) + row0;
+    uint8_t *dst = qs + (warp >> 2) * L::kKv + (ch >> 3) * L::kBlock;
+    uint4 v[32 / kPer];
+#pragma unroll
+    for (int i = 0; i < 32 / kPer; ++i) {
+      const int64_t rr = r0 + kPer * i + lane / kLanes;
+      const int t = static_cast<int>(rr) / p.group;
+      const int64_t src = static_cast<int64_t>(t) * p.pv.H + hk * p.group + (rr - static_cast<int64_t>(t) * p.group);
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (rr < p.rows) v[i] = reinterpret_cast<const uint4 *>(p.q + src * kDim)[ch];
+    }
+#pragma unroll
+    for (int i = 0; i < 32 / kPer; ++i)
+      *reinterpret_cast<uint4 *>(dst + sw128_offset(row0 + kPer * i + lane / kLanes, 16u * (ch & 7))) = v[i];
+  };
+  if (warp < 8 && x0 < x1) load_queries(static_cast<int>(x0 / p.nkt));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
-  const int64_t tot = static_cast<int64_t>(p.pv.H_kv) * p.npairs * p.nkt;
-  const int64_t x0 = tot * c / G, x1 = tot * (c + 1) / G;
   auto fail = [&]() {
     raise_flag(p.status, kFlagTimeout);
     *abort_s = 1;
@@ -316,26 +337,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (first) r = static_cast<int64_t>(at.item % p.npairs) * kRows + 128 * w + row;
       if (r - row >= p.rows) continue;
       if (first) {
-        // the warp's 32 query rows, into the K-major swizzled layout (every
-        // product of the piece before has been read out); a load covers whole rows
-        const int hk = at.item / p.npairs;
-        const int64_t r0 = r - row + 32 * (warp & 3);
-        constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a load
-        uint4 v[32 / kPer];
-#pragma unroll
-        for (int i = 0; i < 32 / kPer; ++i) {
-          const int64_t rr = r0 + kPer * i + lane / kLanes;
-          const int t = static_cast<int>(rr) / p.group;
-          const int64_t src = static_cast<int64_t>(t) * p.pv.H + static_cast<int64_t>(hk) * p.group + (rr - static_cast<int64_t>(t) * p.group);
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (rr < p.rows) v[i] = reinterpret_cast<const uint4 *>(p.q + src * kDim)[lane % kLanes];
-        }
-#pragma unroll
-        for (int i = 0; i < 32 / kPer; ++i) {
-          const int ch = lane % kLanes;
-          *reinterpret_cast<uint4 *>(qt + (ch >> 3) * L::kBlock +
-                                     sw128_offset(32 * (warp & 3) + kPer * i + lane / kLanes, 16u * (ch & 7))) = v[i];
-        }
+        // (every product of the piece before has been read out)
+        if (n > 0) load_queries(at.item);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[w]);
@@ -467,39 +470,30 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 template <int kDim, int kSplit>
 __global__ void __launch_bounds__(256)
 merge_rows_kernel(const PrefixParams p, const ListParams own, int cols, int grid_shared) {
-  __shared__ float acc_s[8][kDim + 1];
-  pdl_wait();
+  __shared__ float acc_s[8][kDim + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *own.counter = 0;  // for the next call
-  const int64_t rows = static_cast<int64_t>(p.pv.T) * p.pv.H;
-  const int64_t id = min(static_cast<int64_t>(blockIdx.x) * (8 / kSplit) + warp / kSplit, rows - 1);
-  const bool in = static_cast<int64_t>(blockIdx.x) * (8 / kSplit) + warp / kSplit < rows;
-  const int t = static_cast<int>(id / p.pv.H), h = static_cast<int>(id % p.pv.H);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * (8 / kSplit) + warp / kSplit;
+  bool ok = id < static_cast<int64_t>(p.pv.T) * p.pv.H;
+  const int t = ok ? static_cast<int>(id / p.pv.H) : 0, h = ok ? static_cast<int>(id - static_cast<int64_t>(t) * p.pv.H) : 0;
   int b, pos;
-  const bool ok = load_paged_token(p.pv, t, nullptr, false, b, pos) && pos >= p.pages * p.pv.P;
-  const int hk = h / p.group, g = h % p.group;
+  ok = ok && load_paged_token(p.pv, t, nullptr, false, b, pos) && pos >= p.pages * p.pv.P;
+  const int hk = h / p.group, g = h - hk * p.group;
   const int64_t r = static_cast<int64_t>(t) * p.group + g;
   const int64_t tot = static_cast<int64_t>(p.pv.H_kv) * p.npairs * p.nkt;
   const int64_t item = static_cast<int64_t>(hk) * p.npairs + r / kRows;
   const int a0 = cta_of(item * p.nkt, tot, grid_shared), a1 = cta_of((item + 1) * p.nkt - 1, tot, grid_shared);
   const int64_t u = (static_cast<int64_t>(t) * p.pv.H_kv + hk) * own.gb + g / 64;
-  const int2 rng = ok ? own.info[u] : make_int2(0, -1);
-  const int na = a1 - a0 + 1, total = ok ? na + rng.y - rng.x + 1 : 0;
-  auto locate = [&](int k, const float2 *&ml, const float *&o) {
-    if (k < na) {
-      const int64_t at = (item + a0 + k) * kRows + r % kRows;
-      ml = p.ml + at;
-      o = p.part + at * kDim;
-    } else {
-      const int64_t at = (u + rng.x + (k - na)) * cols + g % 64;
-      ml = own.ml + at;
-      o = own.part + at * kDim;
-    }
-  };
-  float out[kDim / 32];
-  if (!merge_parts<kDim, kSplit>(total, warp % kSplit, lane, locate, acc_s, out) || !ok || !in) return;
-#pragma unroll
-  for (int e = 0; e < kDim / 32; ++e) own.out[id * kDim + kDim / 32 * lane + e] = __float2bfloat16_rn(out[e]);
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *own.counter = 0;  // for the next call
+  Merge<kDim> m;
+  if (ok) {
+    const int2 rng = own.info[u];
+    m.add(warp % kSplit, kSplit, a1 - a0 + 1, lane, p.ml, p.part,
+          [&](int k) { return (item + a0 + k) * kRows + r % kRows; });
+    m.add(warp % kSplit, kSplit, rng.y - rng.x + 1, lane, own.ml, own.part,
+          [&](int k) { return (u + rng.x + k) * cols + g % 64; });
+  }
+  if (m.template join<kSplit>(acc_s, lane) && ok) m.store(own.out + id * kDim, lane);
 }
 
 size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -580,13 +574,18 @@ cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int share
   // The page list of the sequences' own pages streams from HBM while the shared
   // part keeps the tensor cores busy: it gets SMs of its own, by the two parts'
   // tile counts (the own pages taken as half the table's) at about 1.7 us a tile
-  // of 256 rows and 0.9 us a list tile (2.2 with many heads); what it has left is shared out as the
+  // of 256 rows and 1.3 us a list tile (2.2 with many heads); what it has left is shared out as the
   // shared part's CTAs leave.
   const int sms = std::min(sm_count(), kMaxCtas);
   const double shared_us = 1.7 * static_cast<double>(s.items) * s.nkt;
-  const double own_us = (list_cols(pa) == 16 ? 0.9 : 2.2) * 0.5 * static_cast<double>(pa.T) * pa.H_kv * ((pa.H / pa.H_kv + 63) / 64) *
+  const double own_us = (list_cols(pa) == 16 ? 1.3 : 2.2) * 0.5 * static_cast<double>(pa.T) * pa.H_kv * ((pa.H / pa.H_kv + 63) / 64) *
                         ((pa.max_pages - shared_pages + s.spt - 1) / s.spt);
-  const int most = std::max(sms / 2, static_cast<int>(sms * shared_us / (shared_us + own_us) + 0.5));
+  int most = std::max(sms / 2, static_cast<int>(sms * shared_us / (shared_us + own_us) + 0.5));
+  // a CTA whose range crosses into another item pays about four tiles for the
+  // change (O out, queries in): with at least one CTA per item, whole CTAs per
+  // item (128 x 64 heads: 134 us with 142 CTAs for 32 items, 129 with 128)
+  if (s.items <= most)
+    most = static_cast<int>(std::min<int64_t>(sms / s.items, (most + s.items / 2) / s.items) * s.items);
   const int grid = static_cast<int>(std::min<int64_t>(most, s.items * s.nkt));
   cudaError_t e = pa.D == 128 ? launch_shared<128>(pa, p, grid, stream) : launch_shared<64>(pa, p, grid, stream);
   if (e != cudaSuccess) return e;

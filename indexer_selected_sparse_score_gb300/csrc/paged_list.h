@@ -6,68 +6,92 @@
 
 namespace sa {
 
-constexpr int kMaxParts = 2048;  // most parts of a claimed list
+constexpr int kMaxParts = 1024;  // most parts of a claimed list
 // Word of the workspace header that counts claimed parts: 0 between calls (the
 // merge that ends a call resets it).
 constexpr int kCounterWord = 16;
 
-// Weighted mean of `total` parts (locate(k) gives part k's (reference, sum) and
-// output row): out[e] = value kDim / 32 lane + e of the row.  kSplit warps take
-// every kSplit-th part (`mine` first) and the first of them returns true with
-// the result; with kSplit > 1 every thread of the block calls this.
-template <int kDim, int kSplit, typename Locate>
-__device__ __forceinline__ bool merge_parts(int total, int mine, int lane, const Locate &locate, float (*acc_s)[kDim + 1],
-                                            float (&out)[kDim / 32]) {
-  constexpr int V = kDim / 32;
-  const float2 *ml;
-  const float *o;
-  float M = -INFINITY;
-  for (int k = lane; k < total; k += 32) {
-    locate(k, ml, o);
-    M = fmaxf(M, ml->x);
+// Running merge of parts (reference, sum, output row): a warp per row, lane l
+// holding values V l .. V l + V - 1 of it.  Eight parts' loads go out together.
+template <int kDim>
+struct Merge {
+  static constexpr int V = kDim / 32;
+  float M = -INFINITY, l = 0.f, acc[V] = {};
+
+  __device__ __forceinline__ void scale_to(float m) {
+    const float f = M == -INFINITY ? 0.f : exp2f(M - m);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= f;
+    M = m;
   }
+  // Parts first, first + step, .. below total; at(k) is part k's row number in
+  // ml and part.
+  template <typename At>
+  __device__ __forceinline__ void add(int first, int step, int total, int lane, const float2 *ml, const float *part,
+                                      const At &at) {
+    for (int k0 = first; k0 < total; k0 += 8 * step) {
+      float2 s[8];
+      float x[8][V];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  float acc[V] = {}, l = 0.f;
-  for (int k0 = 0; k0 < total; k0 += 32 * kSplit) {
-    float a = 0.f, la = 0.f;  // this lane's part: weight, weighted sum
-    const float *row = nullptr;
-    const int k = k0 + mine + kSplit * lane;
-    if (k < total) {
-      locate(k, ml, row);
-      const float2 v = *ml;
-      a = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
-      la = a * v.y;
-    }
-    const int n = min(32, (total - k0 - mine + kSplit - 1) / kSplit);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float w = __shfl_sync(0xffffffffu, a, i);
-      l += __shfl_sync(0xffffffffu, la, i);
-      const float *src =
-          reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), i));
+      for (int i = 0; i < 8; ++i) {
+        const int64_t row = at(min(k0 + i * step, total - 1));
+        s[i] = ml[row];
+        if constexpr (V == 4)
+          *reinterpret_cast<float4 *>(x[i]) = *reinterpret_cast<const float4 *>(part + row * kDim + V * lane);
+        else
+          *reinterpret_cast<float2 *>(x[i]) = *reinterpret_cast<const float2 *>(part + row * kDim + V * lane);
+      }
+      float m = M;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, src[V * lane + e], acc[e]);
-    }
-  }
-  if constexpr (kSplit > 1) {
-    const int warp = threadIdx.x >> 5;
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, s[i].x);
+      if (m == -INFINITY) continue;
+      scale_to(m);
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc_s[warp][V * lane + e] = acc[e];
-    if (lane == 0) acc_s[warp][kDim] = l;
-    __syncthreads();
-    if (mine != 0) return false;
-    for (int w = 1; w < kSplit; ++w) {
+      for (int i = 0; i < 8; ++i) {
+        const float w = k0 + i * step < total && s[i].x != -INFINITY ? exp2f(s[i].x - m) : 0.f;
+        l = fmaf(w, s[i].y, l);
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += acc_s[warp + w][V * lane + e];
-      l += acc_s[warp + w][kDim];
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(w, w > 0.f ? x[i][e] : 0.f, acc[e]);
+      }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  // Joins the kSplit warps that hold a row (warps kSplit r .. of the block); the
+  // first of them returns true.  Every thread of the block calls it.
+  template <int kSplit>
+  __device__ __forceinline__ bool join(float (*s)[kDim + 2], int lane) {
+    if constexpr (kSplit == 1) {
+      return true;
+    } else {
+      const int warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int e = 0; e < V; ++e) out[e] = acc[e] * inv;
-  return true;
-}
+      for (int e = 0; e < V; ++e) s[warp][V * lane + e] = acc[e];
+      if (lane == 0) {
+        s[warp][kDim] = M;
+        s[warp][kDim + 1] = l;
+      }
+      __syncthreads();
+      if (warp % kSplit) return false;
+      float m = M;
+      for (int w = 1; w < kSplit; ++w) m = fmaxf(m, s[warp + w][kDim]);
+      if (m == -INFINITY) return true;
+      scale_to(m);
+      for (int w = 1; w < kSplit; ++w) {
+        const float f = s[warp + w][kDim] == -INFINITY ? 0.f : exp2f(s[warp + w][kDim] - m);
+        l = fmaf(f, s[warp + w][kDim + 1], l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(f, s[warp + w][V * lane + e], acc[e]);
+      }
+      return true;
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16 *row, int lane) const {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < V; e += 2)
+      *reinterpret_cast<__nv_bfloat162 *>(row + V * lane + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+  }
+};
 
 struct ListParams {
   PagedView pv;
