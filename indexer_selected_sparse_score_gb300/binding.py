@@ -155,8 +155,15 @@ def _p(x) -> Optional[int]:
     return x.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream (3 us of a
+# call that launches in 3); absent from some torch builds.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _s(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -303,9 +310,10 @@ def _token_stride(name: str, x) -> int:
     raw pointer); the heads of a token have to be dense."""
     if not isinstance(x, torch.Tensor):
         return 0
-    if x.dim() != 3 or x.stride(2) != 1 or (x.size(1) > 1 and x.stride(1) != x.size(2)):
+    stride, shape = x.stride(), x.shape
+    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise SAError(SA_ERR_INVALID_ARG, f"{name} must be [T, heads, D] with dense heads")
-    return x.stride(0) if x.size(0) > 1 else 0
+    return stride[0] if shape[0] > 1 else 0
 
 
 def sa_paged_append(pa: PagedArgs, k, v, ws, q=None, q_out=None, rope: Optional[RopeArgs] = None,

@@ -94,15 +94,19 @@ index_key_kernel(const uint16_t *__restrict__ kproj, int n, const int32_t *__res
 
 }  // namespace
 
-double rope_frequency(const sa_rope_args &rope, int i) {
+RopeRamp rope_ramp(const sa_rope_args &rope) {
+  if (rope.original_seq_len <= 0) return RopeRamp{0.0, 0.0};
+  auto corrected = [&](double turns) {
+    return rope.dim * std::log(rope.original_seq_len / (turns * 2.0 * kPi)) / (2.0 * std::log(rope.base));
+  };
+  return RopeRamp{std::max(std::floor(corrected(rope.beta_fast)), 0.0),
+                  std::min(std::ceil(corrected(rope.beta_slow)), static_cast<double>(rope.dim - 1))};
+}
+
+double rope_frequency(const sa_rope_args &rope, const RopeRamp &r, int i) {
   double f = 1.0 / std::pow(rope.base, static_cast<double>(2 * i) / rope.dim);
   if (rope.original_seq_len > 0) {
-    auto corrected = [&](double turns) {
-      return rope.dim * std::log(rope.original_seq_len / (turns * 2.0 * kPi)) / (2.0 * std::log(rope.base));
-    };
-    const double low = std::max(std::floor(corrected(rope.beta_fast)), 0.0);
-    const double high = std::min(std::ceil(corrected(rope.beta_slow)), static_cast<double>(rope.dim - 1));
-    const double ramp = std::min(std::max((i - low) / std::max(high - low, 1e-3), 0.0), 1.0);
+    const double ramp = std::min(std::max((i - r.low) / std::max(r.high - r.low, 1e-3), 0.0), 1.0);
     f = f / rope.factor * ramp + f * (1.0 - ramp);
   }
   return f;
@@ -115,7 +119,8 @@ cudaError_t launch_index_key_publish(const void *kproj, int n, const int32_t *se
   if (n == 0) return cudaSuccess;
   const int64_t kseq_rows = k_seq_stride ? k_seq_stride / kKeyDim : N_rows;
   RopeFreqs fr{};
-  for (int i = 0; i < rope.dim / 2; ++i) fr.f[i] = rope_frequency(rope, i);
+  const RopeRamp ramp = rope_ramp(rope);
+  for (int i = 0; i < rope.dim / 2; ++i) fr.f[i] = rope_frequency(rope, ramp, i);
   return launch_ex(false, index_key_kernel, dim3((n + kKeyWarps - 1) / kKeyWarps), dim3(32 * kKeyWarps), 0, stream, 1,
                    static_cast<const uint16_t *>(kproj), n, seq, grp, r, weight, eps, rope.dim, fr, k_I, k_scale, B,
                    N_rows, kseq_rows, status);

@@ -111,7 +111,11 @@ cudaError_t launch_sparse_mqa_umma(const sa_index_args &ia, const sa_attn_args &
 // dimension of beta_fast keep it, those above that of beta_slow are divided by
 // factor, and a linear ramp fades between (the corrected dimension: the one
 // whose wavelength completes `turns` rotations over the training context).
-double rope_frequency(const sa_rope_args &rope, int i);
+struct RopeRamp {
+  double low, high;  // pairs between which YaRN's ramp runs
+};
+RopeRamp rope_ramp(const sa_rope_args &rope);
+double rope_frequency(const sa_rope_args &rope, const RopeRamp &ramp, int i);
 
 // Paged cache (sa_paged_args).  `status` is the workspace's status word.
 cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t k_stride, const void *v,

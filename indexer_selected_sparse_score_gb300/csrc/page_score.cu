@@ -65,6 +65,8 @@ constexpr int kThreads = 256;
 constexpr int kHeads = 8;       // KV heads of a CTA
 constexpr int kPass = 16;       // 16-page tiles of one pass over the shared memory
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // D += A B, 16 x 8 x 16, bf16 inputs.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -77,14 +79,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 
 // The 16-page tiles that the tokens see form one list, cut evenly over the CTAs
 // of x (four to an SM, all at once: tokens differ in length, and a second wave
-// would start its chain of dependent loads when the first has ended); z takes 8
-// KV heads.  A warp's item is a tile of one head: A rows are the pages, B
+// would start its chain of dependent loads when the first has ended; `flat`:
+// few tiles, one to a CTA); z takes 8 KV heads.  A warp's item is a tile of one head: A rows are the pages, B
 // columns 0-2 the query's pieces.  The order of the dims within a product is
 // free, so lane 4 g + i holds 16-byte chunks i, i + 4, .. of rows g and g + 8
 // as they lie in memory, two k-steps a chunk.
 template <int kDim>
 __global__ void __launch_bounds__(kThreads, 4)
-score_token_kernel(const ScoreParams p) {
+score_token_kernel(const ScoreParams p, int flat) {
   constexpr int kChunks = kDim / 8, kLoads = kChunks / 4;  // of a row; a lane's loads of it
   __shared__ __align__(16) uint16_t qs[kHeads][3][kDim];
   __shared__ float tile[kHeads][16 * kPass];
@@ -104,20 +106,34 @@ score_token_kernel(const ScoreParams p) {
   const int per = (p.pv.T + kThreads - 1) / kThreads;
   const int ta = min(tid * per, p.pv.T), tb = min(ta + per, p.pv.T);
   long long own = 0, total;
+  long long x0, x1;
   int b;
-  for (int t = ta; t < tb; ++t) own += (seen(t, c == 0 && blockIdx.z == 0, b) + 15) >> 4;
-  long long before = block_prefix(own, warp_s, total);
-  const int cta = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1ll)));
-  const long long x0 = total * min(c, cta) / cta, x1 = total * min(c + 1, cta) / cta;
-  if (before <= x0 && x0 < before + own) {
-    for (int t = ta; t < tb; ++t) {
-      const int n = (seen(t, false, b) + 15) >> 4;
-      if (x0 < before + n) {
-        start_t = t;
-        start_off = before;
-        break;
+  if (flat > 0) {
+    // few tiles: CTA c takes tile c % flat of token c / flat, and no scan
+    const int t = c / flat, a = c % flat;
+    const int n = (seen(t, a == 0 && blockIdx.z == 0, b) + 15) >> 4;
+    x0 = a;
+    x1 = min(a + 1, n);
+    if (tid == 0) {
+      start_t = t;
+      start_off = 0;
+    }
+  } else {
+    for (int t = ta; t < tb; ++t) own += (seen(t, c == 0 && blockIdx.z == 0, b) + 15) >> 4;
+    long long before = block_prefix(own, warp_s, total);
+    const int cta = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1ll)));
+    x0 = total * min(c, cta) / cta;
+    x1 = total * min(c + 1, cta) / cta;
+    if (before <= x0 && x0 < before + own) {
+      for (int t = ta; t < tb; ++t) {
+        const int n = (seen(t, false, b) + 15) >> 4;
+        if (x0 < before + n) {
+          start_t = t;
+          start_off = before;
+          break;
+        }
+        before += n;
       }
-      before += n;
     }
   }
   // columns past the pages a token sees
@@ -163,6 +179,15 @@ score_token_kernel(const ScoreParams p) {
     }
     summed = t;
     __syncthreads();
+    if (e == n && base + e < x1 && t + 1 < p.pv.T) {
+      // the next token's queries and page table are on their way meanwhile
+      const int line = tid * 64;  // 128-byte lines of its heads' queries
+      if (line < nh * G * kDim)
+        prefetch_l2(p.q + (static_cast<int64_t>(t + 1) * p.pv.H + static_cast<int64_t>(h0) * G) * kDim + line);
+      const int nb = p.pv.q_seq[t + 1];
+      if (nb >= 0 && nb < p.pv.B && tid < 8 && 32 * tid < p.pv.max_pages)
+        prefetch_l2(p.pv.page_table + nb * p.pv.table_stride + 32 * tid);
+    }
     const int items = (e - a) * nh;
     constexpr int kAtOnce = 2;  // items whose rows a warp has in flight
     for (int it0 = warp * kAtOnce; it0 < items; it0 += kThreads / 32 * kAtOnce) {
@@ -480,8 +505,9 @@ cudaError_t launch_page_scores(const sa_paged_args &pa, const void *q, const voi
   const int groups = (pa.H_kv + kHeads - 1) / kHeads;
   const int64_t most = static_cast<int64_t>(pa.T) * ((pa.max_pages + 15) / 16);
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, std::max(4 * sm_count() / groups, 1))), 1, groups);
-  return pa.D == 128 ? launch_ex(false, score_token_kernel<128>, grid, dim3(kThreads), 0, stream, 1, p)
-                     : launch_ex(false, score_token_kernel<64>, grid, dim3(kThreads), 0, stream, 1, p);
+  const int flat = most == grid.x ? (pa.max_pages + 15) / 16 : 0;
+  return pa.D == 128 ? launch_ex(false, score_token_kernel<128>, grid, dim3(kThreads), 0, stream, 1, p, flat)
+                     : launch_ex(false, score_token_kernel<64>, grid, dim3(kThreads), 0, stream, 1, p, flat);
 }
 
 }  // namespace sa

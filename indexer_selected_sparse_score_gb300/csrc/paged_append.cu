@@ -192,7 +192,7 @@ page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int pe
     const int64_t tile = static_cast<int64_t>(pages[i]) * pv.H_kv + h;
     const uint4 *src = reinterpret_cast<const uint4 *>(K + tile * pv.P * kDim) + lane;
     float s[8] = {};
-#pragma unroll 8
+#pragma unroll 16
     for (int r = 0; r < pv.P; r += kRows) {
       const uint4 x = src[r * kLanes];
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -239,8 +239,9 @@ cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t 
   p.halves = halves ? 1 : 0;
   p.status = status;
   Turns turns{};
+  const RopeRamp ramp = p.dim > 0 ? rope_ramp(*rope) : RopeRamp{0.0, 0.0};
   for (int i = 0; i < p.dim / 2; ++i) {
-    const double f = rope_frequency(*rope, i) / (2.0 * 3.14159265358979323846);
+    const double f = rope_frequency(*rope, ramp, i) / (2.0 * 3.14159265358979323846);
     turns.f[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
   }
   cudaError_t e = launch_ex(false, paged_append_kernel, dim3(pa.T), dim3(kThreads), 0, stream, 1, p, turns);

@@ -156,6 +156,14 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     return;
   }
   pdl_trigger();
+  if (p.counter) {
+    // a CTA that starts when every part has been claimed leaves at once
+    const bool late = tid == 0 && *static_cast<volatile uint32_t *>(p.counter) >= static_cast<uint32_t>(p.parts);
+    if (__syncthreads_or(late)) {
+      pdl_wait();
+      return;
+    }
+  }
   if (tid == 0) {
     for (int i = 0; i < kSl; ++i) {
       mbar_init(&full[i], 1);
@@ -316,13 +324,18 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const int e = static_cast<int>(min(static_cast<long long>(cnt), x_end - base));
         const bool starts = a == 0, ends = e == cnt;
         int b = 0, pos = 0;
+        const int hk = sub / p.gb, nlist = p.whole ? 0 : p.K;
+        // (the list's entries do not wait for the token's position)
+        auto entry = [&](int i) -> int {
+          return i < nlist ? p.idx[(static_cast<int64_t>(t) * p.pv.H_kv + hk) * p.K + i] : 0;
+        };
+        int entry_ahead = entry(a * spt + lane);
         const bool tok = load_paged_token(p.pv, t, p.status, lane == 0 && sub == 0 && starts && !p.whole, b, pos);
         if (tok) {
-          const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64;
+          const int h0 = hk * p.group + (sub % p.gb) * 64;
           const int last = pos >> p.pv.logP;
           const int own = pos + 1 - last * p.pv.P;  // positions of the token's own page that it sees
           const int f = p.whole ? p.first_page : max(last + 1 - p.local, 0);
-          const int nlist = p.whole ? 0 : p.K;
           const int r1 = min(e * spt, nlist + last + 1 - f);
           int r = a * spt, qh = 0, qe = 0;  // raw entries, queue head and end
           // the part of tile y is floor(((y + 1) G - 1) / tot)
@@ -334,11 +347,9 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           if (p.keep && starts && lane == 0) p.info[u] = make_int2(c, c_last);
           // page entry i of the list (page id, bit 30 set for the token's own
           // page, whose later positions are masked), -1 when it names no page
-          auto resolve = [&](int i) -> int {
+          auto resolve = [&](int i, int j) -> int {
             if (i >= r1) return -1;
-            int j;
             if (i < nlist) {
-              j = p.idx[(static_cast<int64_t>(t) * p.pv.H_kv + hk) * p.K + i];
               if (j < 0 || j >= f) {
                 if (j < -1 || j > last) raise_flag(p.status, kFlagBadIndex);
                 return -1;
@@ -350,12 +361,12 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             return page < 0 ? -1 : page | (j == last ? 1 << 30 : 0);
           };
           bool first = true, more = true;
-          int ahead = resolve(r + lane);  // the next batch, resolved while earlier tiles are copied
+          int ahead = resolve(r + lane, entry_ahead);  // the next batch, resolved while earlier tiles are copied
           while (more) {
             while (qe - qh <= spt && r < r1) {  // enough for this tile and to know whether another follows
               const int rest = qe - qh, ent = ahead;
               r += 32;
-              ahead = resolve(r + lane);
+              ahead = resolve(r + lane, entry(r + lane));
               const int keep = lane < rest ? queue[qh + lane] : 0;
               const uint32_t m = __ballot_sync(0xffffffffu, ent >= 0);
               __syncwarp();
@@ -836,8 +847,11 @@ cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams 
   w += round_up(slots * list_cols(pa) * sizeof(float2));
   p.info = p.cut = reinterpret_cast<int2 *>(w);
   int grid = std::min(sm_count() * (list_cols(pa) == 16 ? 2 : 1), list_ctas(pa));
-  if (!p.whole) {
-    const int spt = kTile / pa.P;
+  const int spt = kTile / pa.P;
+  if (p.whole) {
+    const int64_t tiles = (pa.max_pages - p.first_page + spt - 1) / spt;  // of a unit, at most
+    grid = static_cast<int>(std::min<int64_t>(grid, std::max<int64_t>(1, static_cast<int64_t>(units) * tiles)));
+  } else {
     const int64_t entries = static_cast<int64_t>(p.K) + std::min(p.local, pa.max_pages);
     p.tpu = static_cast<int>(std::max<int64_t>(1, (entries + spt - 1) / spt));
     grid = static_cast<int>(std::min<int64_t>(grid, static_cast<int64_t>(units) * p.tpu));
