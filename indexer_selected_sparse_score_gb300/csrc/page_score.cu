@@ -65,8 +65,6 @@ constexpr int kThreads = 256;
 constexpr int kHeads = 8;       // KV heads of a CTA
 constexpr int kPass = 16;       // 16-page tiles of one pass over the shared memory
 
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // D += A B, 16 x 8 x 16, bf16 inputs.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -77,117 +75,70 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The 16-page tiles that the tokens see form one list, cut evenly over the CTAs
-// of x (four to an SM, all at once: tokens differ in length, and a second wave
-// would start its chain of dependent loads when the first has ended; `flat`:
-// few tiles, one to a CTA); z takes 8 KV heads.  A warp's item is a tile of one head: A rows are the pages, B
-// columns 0-2 the query's pieces.  The order of the dims within a product is
-// free, so lane 4 g + i holds 16-byte chunks i, i + 4, .. of rows g and g + 8
-// as they lie in memory, two k-steps a chunk.
+// CTA (t S + s, z): the s-th of S shares of the 16-page tiles that token t sees,
+// for KV heads 8 z .. 8 z + 7.  (Sharing the tiles of all tokens out evenly cost
+// more than the uneven tokens do: a scan of the positions first, and a second
+// chain of dependent loads wherever a CTA crossed into another token.)  A warp's
+// item is a tile of one head: A rows are the pages, B columns 0-2 the query's
+// pieces.  The order of the dims within a product is free, so lane 4 g + i holds
+// 16-byte chunks i, i + 4, .. of rows g and g + 8 as they lie in memory, two
+// k-steps a chunk.
 template <int kDim>
-__global__ void __launch_bounds__(kThreads, 4)
-score_token_kernel(const ScoreParams p, int flat) {
+__global__ void __launch_bounds__(kThreads, 3)
+score_token_kernel(const ScoreParams p, int S) {
   constexpr int kChunks = kDim / 8, kLoads = kChunks / 4;  // of a row; a lane's loads of it
   __shared__ __align__(16) uint16_t qs[kHeads][3][kDim];
   __shared__ float tile[kHeads][16 * kPass];
   __shared__ int page_s[16 * kPass];
-  __shared__ long long warp_s[kThreads / 32], start_off;
-  __shared__ int start_t;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t = blockIdx.x / S, share = blockIdx.x - t * S;
   const int h0 = blockIdx.z * kHeads, nh = min(kHeads, p.pv.H_kv - h0), G = p.pv.H / p.pv.H_kv;
-  // complete pages a token sees (-1 for a token to skip)
-  auto seen = [&](int t, bool report, int &b) -> int {
-    int pos;
-    const bool ok = load_paged_token(p.pv, t, p.status, report, b, pos);
-    if (report && p.row_seq)
-      for (int h = 0; h < p.pv.H_kv; ++h) write_row_token(p, static_cast<int64_t>(t) * p.pv.H_kv + h, ok, b, pos);
-    return ok ? (pos + 1) >> p.pv.logP : -1;
-  };
-  const int per = (p.pv.T + kThreads - 1) / kThreads;
-  const int ta = min(tid * per, p.pv.T), tb = min(ta + per, p.pv.T);
-  long long own = 0, total;
-  long long x0, x1;
-  int b;
-  if (flat > 0) {
-    // few tiles: CTA c takes tile c % flat of token c / flat, and no scan
-    const int t = c / flat, a = c % flat;
-    const int n = (seen(t, a == 0 && blockIdx.z == 0, b) + 15) >> 4;
-    x0 = a;
-    x1 = min(a + 1, n);
-    if (tid == 0) {
-      start_t = t;
-      start_off = 0;
-    }
-  } else {
-    for (int t = ta; t < tb; ++t) own += (seen(t, c == 0 && blockIdx.z == 0, b) + 15) >> 4;
-    long long before = block_prefix(own, warp_s, total);
-    const int cta = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1ll)));
-    x0 = total * min(c, cta) / cta;
-    x1 = total * min(c + 1, cta) / cta;
-    if (before <= x0 && x0 < before + own) {
-      for (int t = ta; t < tb; ++t) {
-        const int n = (seen(t, false, b) + 15) >> 4;
-        if (x0 < before + n) {
-          start_t = t;
-          start_off = before;
-          break;
-        }
-        before += n;
+  // the queries' loads do not wait for the token's position
+  if (tid < nh * kChunks) {
+    float q[8];
+    const int h = tid / kChunks, ch = tid % kChunks;
+    sum_queries<kDim>(p, t, h0 + h, G, ch, q);
+#pragma unroll
+    for (int piece = 0; piece < 3; ++piece) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = pack_bf16x2(q[2 * i], q[2 * i + 1]);
+        q[2 * i] -= __uint_as_float(w[i] << 16);
+        q[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
       }
+      *reinterpret_cast<uint4 *>(&qs[h][piece][8 * ch]) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  // columns past the pages a token sees
-  for (int t = c; t < p.pv.T; t += gridDim.x) {
-    const int vis = seen(t, false, b);
-    if (vis < 0) continue;
+  int b, pos;
+  const bool ok = load_paged_token(p.pv, t, p.status, tid == 0 && share == 0 && blockIdx.z == 0, b, pos);
+  if (p.row_seq && share == 0 && tid < nh)
+    write_row_token(p, static_cast<int64_t>(t) * p.pv.H_kv + h0 + tid, ok, b, pos);
+  if (!ok) return;
+  const int vis = (pos + 1) >> p.pv.logP, n = (vis + 15) >> 4;
+  const int last = static_cast<int>(static_cast<int64_t>(n) * (share + 1) / S);
+  int a = static_cast<int>(static_cast<int64_t>(n) * share / S);
+  auto page_at = [&](int first) -> int {  // of this thread's page of the pass from tile `first`
+    const int j = 16 * first + tid;
+    return j < min(16 * min(first + kPass, last), vis) ? load_page(p.pv, b, j, p.status, blockIdx.z == 0) : -1;
+  };
+  int page = page_at(a);
+  // the share of the columns past the pages the token sees
+  {
+    const int past = p.pv.max_pages - vis;
+    const int c0 = vis + static_cast<int>(static_cast<int64_t>(past) * share / S);
+    const int c1 = vis + static_cast<int>(static_cast<int64_t>(past) * (share + 1) / S);
     for (int h = warp; h < nh; h += kThreads / 32) {
       float *row = p.scores + (static_cast<int64_t>(t) * p.pv.H_kv + h0 + h) * p.ld;
-      for (int j = vis + lane; j < p.pv.max_pages; j += 32) row[j] = -INFINITY;
+      for (int j = c0 + lane; j < c1; j += 32) row[j] = -INFINITY;
     }
   }
-  __syncthreads();
   const int g = lane >> 2, ti = lane & 3;
-  long long x = x0, base = start_off;
-  int t = start_t, summed = -1;
-  while (x < x1) {
-    const int vis = seen(t, false, b);
-    const int n = (vis + 15) >> 4;
-    if (n <= 0) {
-      ++t;
-      continue;
-    }
-    // tiles [a, e) of token t
-    const int a = static_cast<int>(x - base);
-    const int e = static_cast<int>(min(min(static_cast<long long>(n), x1 - base), static_cast<long long>(a) + kPass));
-    const int j0 = 16 * a, nj = min(16 * e, vis) - j0;
-    if (tid < nj) page_s[tid] = load_page(p.pv, b, j0 + tid, p.status, blockIdx.z == 0);
-    if (summed != t && tid < nh * kChunks) {
-      float s[8];
-      const int h = tid / kChunks, ch = tid % kChunks;
-      sum_queries<kDim>(p, t, h0 + h, G, ch, s);
-#pragma unroll
-      for (int piece = 0; piece < 3; ++piece) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
-          s[2 * i] -= __uint_as_float(w[i] << 16);
-          s[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-        *reinterpret_cast<uint4 *>(&qs[h][piece][8 * ch]) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    summed = t;
+  for (; a < last; a += kPass) {
+    const int e = min(a + kPass, last), j0 = 16 * a, nj = min(16 * e, vis) - j0;
+    page_s[tid] = page;
     __syncthreads();
-    if (e == n && base + e < x1 && t + 1 < p.pv.T) {
-      // the next token's queries and page table are on their way meanwhile
-      const int line = tid * 64;  // 128-byte lines of its heads' queries
-      if (line < nh * G * kDim)
-        prefetch_l2(p.q + (static_cast<int64_t>(t + 1) * p.pv.H + static_cast<int64_t>(h0) * G) * kDim + line);
-      const int nb = p.pv.q_seq[t + 1];
-      if (nb >= 0 && nb < p.pv.B && tid < 8 && 32 * tid < p.pv.max_pages)
-        prefetch_l2(p.pv.page_table + nb * p.pv.table_stride + 32 * tid);
-    }
+    page = page_at(e);  // the next pass's, meanwhile
     const int items = (e - a) * nh;
     constexpr int kAtOnce = 2;  // items whose rows a warp has in flight
     for (int it0 = warp * kAtOnce; it0 < items; it0 += kThreads / 32 * kAtOnce) {
@@ -199,10 +150,10 @@ score_token_kernel(const ScoreParams p, int flat) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int j = 16 * jt + g + 8 * r;
-          const int page = it < items && j < nj ? page_s[j] : -1;
-          bad[m][r] = page < 0;
+          const int id = it < items ? page_s[j] : -1;  // -1 past the pages as well
+          bad[m][r] = id < 0;
           const uint4 *src = reinterpret_cast<const uint4 *>(
-              p.k_mean + (static_cast<int64_t>(max(page, 0)) * p.pv.H_kv + h0 + h) * kDim);
+              p.k_mean + (static_cast<int64_t>(max(id, 0)) * p.pv.H_kv + h0 + h) * kDim);
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) v[m][r][i] = bad[m][r] ? make_uint4(0, 0, 0, 0) : src[ti + 4 * i];
         }
@@ -231,12 +182,7 @@ score_token_kernel(const ScoreParams p, int flat) {
       float *row = p.scores + (static_cast<int64_t>(t) * p.pv.H_kv + h0 + h) * p.ld + j0;
       for (int j = lane; j < nj; j += 32) row[j] = tile[h][j];
     }
-    __syncthreads();  // the next pass writes tile and page_s
-    x = base + e;
-    if (e == n) {
-      base += n;
-      ++t;
-    }
+    __syncthreads();  // the next pass writes tile
   }
 }
 
@@ -503,11 +449,13 @@ cudaError_t launch_page_scores(const sa_paged_args &pa, const void *q, const voi
   if (pa.T >= 16 * static_cast<int64_t>(pa.B))
     return pa.D == 128 ? launch_tile<128>(pa, p, stream) : launch_tile<64>(pa, p, stream);
   const int groups = (pa.H_kv + kHeads - 1) / kHeads;
-  const int64_t most = static_cast<int64_t>(pa.T) * ((pa.max_pages + 15) / 16);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, std::max(4 * sm_count() / groups, 1))), 1, groups);
-  const int flat = most == grid.x ? (pa.max_pages + 15) / 16 : 0;
-  return pa.D == 128 ? launch_ex(false, score_token_kernel<128>, grid, dim3(kThreads), 0, stream, 1, p, flat)
-                     : launch_ex(false, score_token_kernel<64>, grid, dim3(kThreads), 0, stream, 1, p, flat);
+  // shares of a token: three CTAs per SM over all (as many as run at once), no
+  // more than it has tiles
+  const int64_t target = std::max<int64_t>(1, 3LL * sm_count() / (static_cast<int64_t>(pa.T) * groups));
+  const int S = static_cast<int>(std::min<int64_t>(target, (pa.max_pages + 15) / 16));
+  const dim3 grid(static_cast<unsigned>(pa.T) * S, 1, groups);
+  return pa.D == 128 ? launch_ex(false, score_token_kernel<128>, grid, dim3(kThreads), 0, stream, 1, p, S)
+                     : launch_ex(false, score_token_kernel<64>, grid, dim3(kThreads), 0, stream, 1, p, S);
 }
 
 }  // namespace sa
