@@ -189,7 +189,7 @@ score_token_kernel(const ScoreParams p, int S) {
 // ------------------------------------------------------ 128 tokens at a time
 
 constexpr int kTile = 128;  // tokens, and pages, of a product
-constexpr int kTileThreads = 512;
+constexpr int kTileThreads = 512;  // and one warp that issues the products
 constexpr int kPieces = 3;  // bf16 pieces of a summed query
 
 template <int kDim>
@@ -212,7 +212,7 @@ struct ScoreSmem {
 // block's product running and the one after being gathered while the current
 // one's scores are written.
 template <int kDim>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(kTileThreads + 32, 1)
 score_tile_kernel(const ScoreParams p) {
   using L = ScoreSmem<kDim>;
   constexpr int kChunks = kDim / 8;
@@ -248,6 +248,7 @@ score_tile_kernel(const ScoreParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
+  const bool worker = warp < kTileThreads / 32;    // not the issuer, which only joins the barriers
   const int row = 32 * (warp & 3) + lane;          // this thread's token
   const int2 mine = tok_s[row];
   const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -259,7 +260,7 @@ score_tile_kernel(const ScoreParams p) {
   // the summed queries, split into bf16 pieces (round to nearest: each piece
   // takes at least 8 bits of what is left), while the first mean keys come in
   auto sum_all = [&]() {
-    for (int i = tid; i < kTile * kChunks; i += kTileThreads) {
+    for (int i = worker ? tid : kTile * kChunks; i < kTile * kChunks; i += kTileThreads) {
       const int r = i / kChunks, ch = i % kChunks;
       float a[8] = {};
       if (r < nt) sum_queries<kDim>(p, t0 + r, h, G, ch, a);
@@ -309,9 +310,16 @@ score_tile_kernel(const ScoreParams p) {
     // when written
     // Row r of the block is copied by threads 4 r .. 4 r + 3, 16 bytes at a
     // time into the swizzle (gathered TMA loads take 70 ns each to issue).
+    // The page ids are looked up a block ahead.
+    auto look_up = [&](int i) -> int {
+      const int j = i * kTile + (tid >> 2);
+      return worker && j < seen ? load_page(p.pv, b, j, p.status, h == 0) : -1;
+    };
+    int page_ahead = look_up(0);
     auto gather = [&](int i) {
-      const int bf = (n + i) & 1, r = tid >> 2, j = i * kTile + r;
-      const int page = j < seen ? load_page(p.pv, b, j, p.status, h == 0) : -1;
+      if (!worker) return;
+      const int bf = (n + i) & 1, r = tid >> 2, page = page_ahead;
+      page_ahead = look_up(i + 1);
       if ((tid & 3) == 0) page_s[bf * kTile + r] = page;
       const uint16_t *src = p.k_mean + (static_cast<int64_t>(max(page, 0)) * p.pv.H_kv + h) * kDim;
 #pragma unroll
@@ -351,7 +359,7 @@ score_tile_kernel(const ScoreParams p) {
     }
     if (used > 0) {
       landed();
-      if (warp == 0) multiply(0);
+      if (!worker) multiply(0);
       if (used > 1) gather(1);
     }
     for (int i = 0; i < nblk; ++i) {
@@ -359,6 +367,13 @@ score_tile_kernel(const ScoreParams p) {
       const bool live = i < used;
       float v[32];
       const int c0 = 32 * (warp >> 2), j0 = i * kTile + c0;
+      if (!worker) {
+        if (live) {
+          landed();
+          if (i + 1 < used) multiply(i + 1);
+        }
+        continue;
+      }
       if (live) {
         if (!mbar_wait_warp(&ready[bf], (u >> 1) & 1) && lane == 0) raise_flag(p.status, kFlagTimeout);
         tc_fence_after();
@@ -375,7 +390,6 @@ score_tile_kernel(const ScoreParams p) {
             v[e] = j0 + e < mine.y && ((exist >> e) & 1u) ? v[e] : -INFINITY;
         }
         landed();  // block i + 1 is in; buffer bf (keys, page ids, accumulator) is free
-        if (warp == 0 && i + 1 < used) multiply(i + 1);
         if (i + 2 < used) gather(i + 2);
       } else {
 #pragma unroll
@@ -427,7 +441,7 @@ cudaError_t launch_tile(const sa_paged_args &pa, const ScoreParams &p, cudaStrea
   static bool attr_done[64] = {};
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_ex(false, kern, dim3((pa.T + kTile - 1) / kTile, pa.H_kv), dim3(kTileThreads), smem, stream, 1, p);
+  return launch_ex(false, kern, dim3((pa.T + kTile - 1) / kTile, pa.H_kv), dim3(kTileThreads + 32), smem, stream, 1, p);
 }
 
 }  // namespace

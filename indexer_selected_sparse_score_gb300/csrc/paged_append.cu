@@ -166,7 +166,7 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
 
 // Mean of the key rows of every page whose last position is among the tokens.
 // CTA x: tokens x * per .. + per - 1 (at most kMeanThreads); a warp takes a
-// (page, KV head).  It runs after the append has written every row, so a page
+// (page, KV head), or all of them share one.  It runs after the append has written every row, so a page
 // may fill from tokens in any order; which pages those are is found before the
 // wait.
 template <int kDim>
@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kMeanThreads)
 page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int per) {
   constexpr int kLanes = kDim / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a load
   __shared__ int pages[kMeanThreads], n_s;
+  __shared__ float part[kMeanThreads / 32][kDim];
   if (threadIdx.x == 0) n_s = 0;
   __syncthreads();
   const int own = blockIdx.x * per + threadIdx.x;
@@ -187,13 +188,17 @@ page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int pe
   __syncthreads();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes;
-  for (int it = warp; it < n_s * pv.H_kv; it += kMeanThreads / 32) {
+  constexpr int kWarps = kMeanThreads / 32;
+  const int items = n_s * pv.H_kv;
+  // with few (page, head) pairs the block's warps share each of them
+  const bool share = items < kWarps;
+  for (int it = share ? 0 : warp; it < items; it += share ? 1 : kWarps) {
     const int i = it / pv.H_kv, h = it - i * pv.H_kv;
     const int64_t tile = static_cast<int64_t>(pages[i]) * pv.H_kv + h;
     const uint4 *src = reinterpret_cast<const uint4 *>(K + tile * pv.P * kDim) + lane;
     float s[8] = {};
 #pragma unroll 16
-    for (int r = 0; r < pv.P; r += kRows) {
+    for (int r = share ? warp * kRows : 0; r < pv.P; r += share ? kWarps * kRows : kRows) {
       const uint4 x = src[r * kLanes];
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -206,7 +211,20 @@ page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int pe
     for (int e = 0; e < 8; ++e)
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) s[e] += __shfl_xor_sync(0xffffffffu, s[e], o);
-    if (lane < kLanes) {
+    if (share) {
+      if (lane < kLanes) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[warp][8 * c + e] = s[e];
+      }
+      __syncthreads();
+      if (warp == 0 && lane < kLanes) {
+        for (int w = 1; w < kWarps; ++w)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] += part[w][8 * c + e];
+      }
+      __syncthreads();
+    }
+    if (lane < kLanes && (!share || warp == 0)) {
       const float f = 1.f / static_cast<float>(pv.P);  // exact: P is a power of two
       *reinterpret_cast<uint4 *>(k_mean + tile * kDim + 8 * c) =
           make_uint4(pack_bf16(s[0] * f, s[1] * f), pack_bf16(s[2] * f, s[3] * f), pack_bf16(s[4] * f, s[5] * f),
