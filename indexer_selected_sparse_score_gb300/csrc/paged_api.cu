@@ -80,13 +80,13 @@ sa_status check_shared(const sa_paged_args *pa, int32_t shared_pages) {
 }
 
 // Workspace of the fused call: scores, indices and the top-k's token arrays
-// (one row per token and KV head), then the attention's scratch.
+// (one row per token and KV head; none for K = 0), then the attention's scratch.
 struct FusedLayout {
   size_t scores, idx, row_seq, row_pos, attn, total;
 };
 FusedLayout fused_layout(const sa_paged_args &pa, int K, int local) {
   FusedLayout L{};
-  const size_t rows = static_cast<size_t>(pa.T) * pa.H_kv;
+  const size_t rows = K > 0 ? static_cast<size_t>(pa.T) * pa.H_kv : 0;
   size_t off = 256;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -115,8 +115,7 @@ extern "C" {
 size_t sa_paged_workspace_size(const sa_paged_args *pa, int32_t K, int32_t local, int32_t shared_pages) {
   if (check_paged(pa, false) != SA_OK || check_lists(K, local) != SA_OK || check_shared(pa, shared_pages) != SA_OK)
     return 0;
-  const size_t block = K > 0 ? fused_layout(*pa, K, local).total : 256 + round_up(sa::block_attn_scratch(*pa, 0, local));
-  return std::max(block, 256 + round_up(sa::prefix_attn_scratch(*pa, shared_pages)));
+  return std::max(fused_layout(*pa, K, local).total, 256 + round_up(sa::prefix_attn_scratch(*pa, shared_pages)));
 }
 
 sa_status sa_paged_append(const sa_paged_args *pa, const void *k, int64_t k_stride, const void *v, int64_t v_stride,

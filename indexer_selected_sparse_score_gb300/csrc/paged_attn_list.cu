@@ -157,8 +157,9 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   }
   pdl_trigger();
   if (p.counter) {
-    // a CTA that starts when every part has been claimed leaves at once
-    const bool late = tid == 0 && *static_cast<volatile uint32_t *>(p.counter) >= static_cast<uint32_t>(p.parts);
+    // a CTA that starts when every part has been claimed leaves at once (not
+    // CTA 0, which reports the tokens it skips)
+    const bool late = tid == 0 && blockIdx.x > 0 && *static_cast<volatile uint32_t *>(p.counter) >= static_cast<uint32_t>(p.parts);
     if (__syncthreads_or(late)) {
       pdl_wait();
       return;

@@ -588,3 +588,174 @@ def test_a_long_cache_passes_32_bit_offsets():
     for t in range(2):
         page = int(table[t, int(c.pos[t]) // P])
         assert torch.equal(K[page, :, int(c.pos[t]) % P], kv[0, t])
+
+
+# ------------------------------------------------- masks, scales, large lists ---
+
+@pytest.mark.parametrize("Hkv,G,T_per,B", [(9, 2, 1, 5), (17, 1, 1, 3), (3, 4, 40, 2), (1, 8, 15, 2)])
+def test_scores_with_nan_means_of_unseen_pages(Hkv, G, T_per, B):
+    P, D = 16, 128
+    lens = [T_per + 16 * 20 + 7 * b for b in range(B)]
+    c = Case(30, lens, D, P, Hkv, G)
+    c.tokens([b for b in range(B) for _ in range(T_per)], [p for n in lens for p in range(n - T_per, n)]).upload()
+    mean = (torch.randn(c.total, Hkv, D, generator=c.g) / 4).bfloat16()
+    seen = torch.zeros(c.total, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        seen[c.table[b, :n // P].long()] = True
+    mean[~seen] = float("nan")
+    mean = mean.to(DEV)
+    scores = torch.empty(c.T, Hkv, c.max_pages, device=DEV)
+    ws = sb.new_paged_workspace(c.pa)
+    sb.sa_page_scores(c.pa, c.d["q"], mean, scores, ws)
+    status_ok(ws)
+    check_scores(c, mean, scores)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.07, 0.3])
+@pytest.mark.parametrize("shared", [0, 3])
+def test_attention_at_other_scales(scale, shared):
+    P = 32
+    c = Case(31, [shared * P + 77, shared * P + 300], 128, P, 1, 16, shared=shared)
+    c.scale = scale
+    c.tokens([0, 1], [n - 1 for n in c.lens]).upload()
+    out, out2 = c.out(), c.out()
+    idx = make_idx(c, 4, 1, seed=2)
+    ws = sb.new_paged_workspace(c.pa, 4, 1, shared)
+    sb.sa_prefix_attn(c.pa, c.d["q"], shared, out, ws)
+    sb.sa_block_attn(c.pa, c.d["q"], idx.to(DEV), 4, 1, out2, ws)
+    status_ok(ws)
+    c.check(out, lambda t, h: list(range(int(c.pos[t]) + 1)))
+    c.check(out2, lambda t, h: ref.block_keys(int(c.pos[t]), P, idx[t, h].tolist(), 1, c.max_pages))
+
+
+@pytest.mark.parametrize("D,P,G,K", [(128, 16, 8, 700), (64, 16, 64, 700), (128, 128, 40, 90)])
+def test_block_attention_over_long_lists(D, P, G, K):
+    n = 100 * P if P == 128 else 800 * P
+    c = Case(32, [n - 5], D, P, 1, G)
+    c.tokens([0, 0], [n - 6, n // 2]).upload()
+    idx = make_idx(c, K, 2, seed=5, tricks=False)
+    idx[0, 0] = torch.arange(K, dtype=torch.int32) + (3 if P != 128 else 1)
+    out = c.out()
+    ws = sb.new_paged_workspace(c.pa, K, 2)
+    sb.sa_block_attn(c.pa, c.d["q"], idx.to(DEV), K, 2, out, ws)
+    status_ok(ws)
+    c.check(out, lambda t, h: ref.block_keys(int(c.pos[t]), P, idx[t, h].tolist(), 2, c.max_pages))
+
+
+def test_block_attention_rows_without_any_key_are_zero():
+    c = Case(33, [100, 100], 128, 16, 2, 8)
+    c.tokens([0, 1], [99, 50]).upload()
+    idx = torch.full((2, 2, 5), -1, dtype=torch.int32)
+    idx[1, 1, 2] = 1
+    out = c.out()
+    ws = sb.new_paged_workspace(c.pa, 5, 0)
+    sb.sa_block_attn(c.pa, c.d["q"], idx.to(DEV), 5, 0, out, ws)
+    status_ok(ws)
+    assert bool((out[0] == 0).all()) and bool((out[1, :8] == 0).all()) and bool((out[1, 8:] != 0).any())
+    c.check(out, lambda t, h: ref.block_keys(int(c.pos[t]), 16, idx[t, h].tolist(), 0, c.max_pages))
+
+
+@pytest.mark.parametrize("G,shared", [(8, 0), (8, 2), (64, 2), (128, 1)])
+def test_prefix_attention_with_uneven_long_tails(G, shared):
+    P, D = 64, 128
+    tails = [1, 2900, 3, 64, 1500, 1, 700, 130, 5, 2048]
+    c = Case(34, [shared * P + n for n in tails], D, P, 2 if G <= 64 else 1, G, shared=shared)
+    c.tokens(range(len(tails)), [n - 1 for n in c.lens]).upload()
+    out = c.out()
+    ws = sb.new_paged_workspace(c.pa, shared_pages=shared)
+    for _ in range(3):  # the claims start from zero at every call
+        out.fill_(7.0)
+        sb.sa_prefix_attn(c.pa, c.d["q"], shared, out, ws)
+    status_ok(ws)
+    c.check(out, lambda t, h: list(range(int(c.pos[t]) + 1)))
+
+
+def test_prefix_attention_when_every_token_lies_inside_the_shared_pages():
+    c = Case(35, [200, 200], 128, 32, 1, 8, shared=7)
+    c.tokens([0, 1], [100, 199]).upload()
+    out = c.out()
+    ws = sb.new_paged_workspace(c.pa, shared_pages=7)
+    sb.sa_prefix_attn(c.pa, c.d["q"], 7, out, ws)
+    assert sb.sa_check_device_status(ws) == sb.SA_ERR_DEVICE_DATA
+    assert bool((out == 7.0).all())
+
+
+def test_prefix_attention_with_a_bad_shared_page():
+    P, shared = 16, 11
+    c = Case(36, [shared * P + 9, shared * P + 40], 128, P, 1, 16, shared=shared)
+    c.tokens([0, 1], [n - 1 for n in c.lens]).upload()
+    for bad in ([4], list(range(8)), list(range(shared))):
+        table = c.d["table"].clone()
+        table[0, bad] = c.total + 5
+        pa = sb.paged_args(c.d["seq"], c.d["pos"], table, c.H, 1, 128, P, c.total, c.d["K"], c.d["V"], c.scale)
+        out = c.out()
+        ws = sb.new_paged_workspace(pa, shared_pages=shared)
+        sb.sa_prefix_attn(pa, c.d["q"], shared, out, ws)
+        assert sb.sa_check_device_status(ws) == sb.SA_ERR_DEVICE_DATA
+        c.check(out, lambda t, h: [p for p in range(int(c.pos[t]) + 1) if p // P not in bad])
+
+
+def test_prefix_attention_raises_its_reference_along_the_keys():
+    # keys grow along the sequence, so that every tile passes the one before by
+    # far more than the lazy margin
+    P, shared, D = 64, 8, 128
+    c = Case(37, [shared * P + 500, shared * P + 200], D, P, 1, 64, shared=shared)
+    for b, n in enumerate(c.lens):
+        for j in range((n + P - 1) // P):
+            page = int(c.table[b, j])
+            if b == 0 or j >= shared:
+                c.K[page] = (c.K[page].float() * (1 + 3.0 * j)).bfloat16()
+    c.tokens([0, 1], [n - 1 for n in c.lens]).upload()
+    out, out2 = c.out(), c.out()
+    idx = make_idx(c, 9, 1, seed=1, tricks=False)
+    ws = sb.new_paged_workspace(c.pa, 9, 1, shared)
+    sb.sa_prefix_attn(c.pa, c.d["q"], shared, out, ws)
+    sb.sa_block_attn(c.pa, c.d["q"], idx.to(DEV), 9, 1, out2, ws)
+    status_ok(ws)
+    c.check(out, lambda t, h: list(range(int(c.pos[t]) + 1)))
+    c.check(out2, lambda t, h: ref.block_keys(int(c.pos[t]), P, idx[t, h].tolist(), 1, c.max_pages))
+
+
+@pytest.mark.parametrize("new,Hkv,G,K,local", [(150, 2, 8, 5, 1), (1, 3, 5, 7, 2), (64, 1, 64, 0, 2)])
+def test_fused_block_attention(new, Hkv, G, K, local):
+    D, P = 128, 32
+    lens = [900 + new, 31 + new, 400 + new]
+    c = Case(38, lens, D, P, Hkv, G)
+    c.tokens([b for b in range(3) for _ in range(new)], [p for n in lens for p in range(n - new, n)]).upload()
+    mean = (torch.randn(c.total, Hkv, D, generator=c.g) / 5).bfloat16().to(DEV)
+    ws = sb.new_paged_workspace(c.pa, K, local)
+    idx = torch.full((c.T, Hkv, max(K, 1)), 77, dtype=torch.int32, device=DEV)
+    out, out2, out3 = c.out(), c.out(), c.out()
+    sb.sa_fused_block_attn(c.pa, c.d["q"], mean, K, local, idx if K else None, out, ws)
+    sb.sa_fused_block_attn(c.pa, c.d["q"], mean, K, local, None, out2, ws)
+    sb.sa_block_attn(c.pa, c.d["q"], idx if K else None, K, local, out3, ws)
+    status_ok(ws)
+    assert torch.equal(out, out2) and torch.equal(out, out3)
+    if K == 0:
+        return
+    # the picks are the exact top-k of the scores this call's scorer gives
+    scores = torch.empty(c.T, Hkv, c.max_pages, device=DEV)
+    sb.sa_page_scores(c.pa, c.d["q"], mean, scores, ws)
+    s = scores.cpu()
+    for t in range(c.T):
+        f = max(int(c.pos[t]) // P + 1 - local, 0)
+        for h in range(Hkv):
+            order = sorted(range(f), key=lambda j: (-float(s[t, h, j]), j))[:K]
+            assert idx[t, h].tolist() == sorted(order) + [-1] * (K - len(order)), (t, h)
+
+
+def test_calls_run_on_the_stream_they_are_given():
+    # the calls run on the stream they are given, whichever is current
+    c = Case(39, [300], 128, 64, 1, 8).tokens([0], [299]).upload()
+    ws = sb.new_paged_workspace(c.pa)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a, b = c.out(), c.out()
+    torch.cuda.synchronize()
+    sb.sa_prefix_attn(c.pa, c.d["q"], 0, a, ws, stream=side)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        sb.sa_prefix_attn(c.pa, c.d["q"], 0, b, ws)
+    side.synchronize()
+    assert torch.equal(a, b)
+    c.check(a, lambda t, h: list(range(300)))
