@@ -395,19 +395,18 @@ typedef struct {
  * (256), sa_block_attn and sa_fused_block_attn with these K and local,
  * sa_prefix_attn with these shared_pages (pass 0 for what is not used).
  * Returns 0 when the arguments are invalid.  Initialise the workspace with
- * sa_workspace_init; graphs that may run at once need one each. */
+ * sa_workspace_init, and again after a call that returned SA_ERR_CUDA; graphs
+ * that may run at once need one each. */
 SA_API size_t sa_paged_workspace_size(const sa_paged_args *pa, int32_t K, int32_t local, int32_t shared_pages);
 
 /* Appends new keys and values to the pages, rotary embedding applied on the
- * way ("DeepSeek-V4.1-Flash-NVFP4 inference/model.py", Attention._window_kv:
- * apply_rotary_emb, then the cache write).  For token t at position p of
+ * way.  For token t at position p of
  * sequence b, page i = page_table[b, p / P], slot s = p % P, every KV head h:
  *   K[i, h, s] = bf16( R(p) k[t, h] ),   V[i, h, s] = v[t, h]
  * with R(p) the rotation of the last rope->dim values at position p (rope NULL
  * or dim 0: none; dim a multiple of 16, at most D).  rope_halves 0 pairs
- * adjacent values (2i, 2i + 1), nonzero pairs value i with value i + dim / 2
- * ("DeepSeek-V3.2-Exp inference/model.py", apply_rotary_emb with interleaved
- * false).  With q ([T, H, D]) the rotated queries go to q_out ([T, H, D]
+ * adjacent values (2i, 2i + 1), nonzero pairs value i with value i + dim / 2.
+ * With q ([T, H, D]) the rotated queries go to q_out ([T, H, D]
  * dense; q_out == q is allowed when q is dense).  k, v and q rows of
  * consecutive tokens are *_stride elements apart (0: dense; else a multiple of
  * 8 of at least the row), heads dense, e.g. slices of one projection's output.
@@ -415,8 +414,8 @@ SA_API size_t sa_paged_workspace_size(const sa_paged_args *pa, int32_t K, int32_
  * With k_mean ([n_pages, H_kv, D] bf16), every page whose last position is
  * among the tokens gets the mean of its P key rows as stored (summed in fp32,
  * rounded once): the keys sa_page_scores reads.  The positions of one call are
- * distinct within a sequence, in any order; a position given twice leaves
- * either token's values.  Angles are taken as exact multiples of the frequency
+ * distinct within a sequence, in any order; of a position given twice every
+ * value is one token's or the other's.  Angles are taken as exact multiples of the frequency
  * modulo a turn (64-bit fixed point), so far positions lose nothing. */
 SA_API sa_status sa_paged_append(const sa_paged_args *pa, const void *k, int64_t k_stride, const void *v,
                                  int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
@@ -429,7 +428,8 @@ SA_API sa_status sa_paged_append(const sa_paged_args *pa, const void *k, int64_t
  * and -inf for n_vis(t) <= j < max_pages (and for a page id out of range).
  * q: [T, H, D] bf16 dense, rotated; k_mean as sa_paged_append keeps it;
  * scores: [T, H_kv, ld] fp32, columns 0 .. max_pages - 1 of every row written,
- * ld >= max_pages.  The queries' sum and the products are held in fp32.  Rows
+ * ld >= max_pages.  The queries' sum and the products are held in fp32 (of a
+ * sum that is infinite the score is NaN).  Rows
  * of T * H_kv scores are what sa_topk selects from (r = P, one row per token
  * and KV head); sa_fused_block_attn does so.  K and V of pa are not read and
  * may be NULL. */
@@ -446,7 +446,7 @@ SA_API sa_status sa_page_scores(const sa_paged_args *pa, const void *q, const vo
  * concatenated, as in sa_sparse_attn).
  *   out[t, h'] = sum_j softmax(scale q[t, h'] . K_j) V_j,  0 for a row without keys.
  * q, out: [T, H, D] bf16 dense; idx: [T, H_kv, K] int32 (NULL when K is 0);
- * K >= 0, local >= 0.  The logits, the softmax statistics and the output sums
+ * 0 <= K <= 2^30, local >= 0.  The logits, the softmax statistics and the output sums
  * are fp32; the weights enter their product as bf16. */
 SA_API sa_status sa_block_attn(const sa_paged_args *pa, const void *q, const int32_t *idx, int32_t K, int32_t local,
                                void *out, void *ws, size_t ws_bytes, sa_stream_t stream);

@@ -313,7 +313,17 @@ def _token_stride(name: str, x) -> int:
     stride, shape = x.stride(), x.shape
     if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise SAError(SA_ERR_INVALID_ARG, f"{name} must be [T, heads, D] with dense heads")
+    if shape[0] > 1 and stride[0] < shape[1] * shape[2]:  # an expanded tensor; the library takes 0 as dense
+        raise SAError(SA_ERR_INVALID_ARG, f"{name}'s tokens overlap")
     return stride[0] if shape[0] > 1 else 0
+
+
+def _dense(name: str, x, itemsize: int):
+    """Pointer of a tensor that the library takes as dense rows of ``itemsize``-byte
+    values (a raw pointer or None as it is)."""
+    if isinstance(x, torch.Tensor) and not (x.element_size() == itemsize and x.is_contiguous()):
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} must be contiguous, of {itemsize}-byte values (got {x.dtype})")
+    return _p(x)
 
 
 def sa_paged_append(pa: PagedArgs, k, v, ws, q=None, q_out=None, rope: Optional[RopeArgs] = None,
@@ -322,37 +332,47 @@ def sa_paged_append(pa: PagedArgs, k, v, ws, q=None, q_out=None, rope: Optional[
     ``q`` is rotated into ``q_out`` alongside, and ``k_mean`` gets the mean key of
     every page that fills.  k, v and q may be slices of a fused projection
     (their token strides are passed on)."""
+    for name, x in (("k", k), ("v", v), ("q", q)):
+        if isinstance(x, torch.Tensor) and x.element_size() != 2:
+            raise SAError(SA_ERR_INVALID_ARG, f"{name} must be bf16 (got {x.dtype})")
     p, n = _ws(ws)
     _check(load().sa_paged_append(ctypes.byref(pa), _p(k), _token_stride("k", k), _p(v), _token_stride("v", v), _p(q),
-                                  _token_stride("q", q), _p(q_out), ctypes.byref(rope) if rope is not None else None,
-                                  int(halves), _p(k_mean), p, n, _s(stream)))
+                                  _token_stride("q", q), _dense("q_out", q_out, 2),
+                                  ctypes.byref(rope) if rope is not None else None, int(halves),
+                                  _dense("k_mean", k_mean, 2), p, n, _s(stream)))
 
 
 def sa_page_scores(pa: PagedArgs, q, k_mean, scores, ws, stream=None, ld=None) -> None:
     """Score of every complete page for every token and KV head ([T, H_kv, ld] fp32)."""
     if ld is None:
         ld = scores.stride(-2) if isinstance(scores, torch.Tensor) and scores.dim() == 3 else pa.max_pages
+    if isinstance(scores, torch.Tensor) and (scores.element_size() != 4 or (scores.dim() == 3 and (
+            scores.stride(2) != 1 or (scores.shape[0] > 1 and scores.stride(0) != scores.shape[1] * ld)))):
+        raise SAError(SA_ERR_INVALID_ARG, "scores must be [T, H_kv, ld] fp32 with evenly spaced rows")
     p, n = _ws(ws)
-    _check(load().sa_page_scores(ctypes.byref(pa), _p(q), _p(k_mean), _p(scores), int(ld), p, n, _s(stream)))
+    _check(load().sa_page_scores(ctypes.byref(pa), _dense("q", q, 2), _dense("k_mean", k_mean, 2), _p(scores), int(ld), p,
+                               n, _s(stream)))
 
 
 def sa_block_attn(pa: PagedArgs, q, idx, K: int, local: int, out, ws, stream=None) -> None:
     """Attention over the pages of ``idx`` ([T, H_kv, K] int32) and the ``local`` newest pages."""
     p, n = _ws(ws)
-    _check(load().sa_block_attn(ctypes.byref(pa), _p(q), _p(idx), K, local, _p(out), p, n, _s(stream)))
+    _check(load().sa_block_attn(ctypes.byref(pa), _dense("q", q, 2), _dense("idx", idx, 4), K, local,
+                              _dense("out", out, 2), p, n, _s(stream)))
 
 
 def sa_fused_block_attn(pa: PagedArgs, q, k_mean, K: int, local: int, idx_out, out, ws, stream=None) -> None:
     """Page scores, exact top-k and attention over the picks and the local pages."""
     p, n = _ws(ws)
-    _check(load().sa_fused_block_attn(ctypes.byref(pa), _p(q), _p(k_mean), K, local, _p(idx_out), _p(out), p, n,
-                                      _s(stream)))
+    _check(load().sa_fused_block_attn(ctypes.byref(pa), _dense("q", q, 2), _dense("k_mean", k_mean, 2), K, local,
+                                    _dense("idx_out", idx_out, 4), _dense("out", out, 2), p, n, _s(stream)))
 
 
 def sa_prefix_attn(pa: PagedArgs, q, shared_pages: int, out, ws, stream=None) -> None:
     """Attention over whole sequences whose first ``shared_pages`` pages are the same."""
     p, n = _ws(ws)
-    _check(load().sa_prefix_attn(ctypes.byref(pa), _p(q), shared_pages, _p(out), p, n, _s(stream)))
+    _check(load().sa_prefix_attn(ctypes.byref(pa), _dense("q", q, 2), shared_pages, _dense("out", out, 2), p, n,
+                               _s(stream)))
 
 
 def sa_check_device_status(ws, stream=None) -> int:
@@ -442,8 +462,13 @@ def paged_args(q_seq, q_pos, page_table, H: int, H_kv: int, D: int, P: int, n_pa
     if page_table.dim() != 2 or page_table.stride(1) != 1:
         raise SAError(SA_ERR_INVALID_ARG, "page_table must be [B, max_pages] with dense rows")
     B, max_pages = page_table.shape
-    return PagedArgs(B, q_seq.numel(), H, H_kv, D, P, n_pages, max_pages, _p(q_seq), _p(q_pos), _p(page_table),
-                     page_table.stride(0) if B > 1 else 0, _p(K), _p(V), float(scale))
+    if B > 1 and page_table.stride(0) < max_pages:  # an expanded table; the library takes 0 as dense
+        raise SAError(SA_ERR_INVALID_ARG, "page_table's rows overlap")
+    if q_pos.numel() != q_seq.numel() or page_table.element_size() != 4:
+        raise SAError(SA_ERR_INVALID_ARG, "need q_seq and q_pos of one length, and page_table of int32")
+    return PagedArgs(B, q_seq.numel(), H, H_kv, D, P, n_pages, max_pages, _dense("q_seq", q_seq, 4),
+                     _dense("q_pos", q_pos, 4), _p(page_table), page_table.stride(0) if B > 1 else 0,
+                     _dense("K", K, 2), _dense("V", V, 2), float(scale))
 
 
 def new_paged_workspace(pa: PagedArgs, K: int = 0, local: int = 0, shared_pages: int = 0, device="cuda",

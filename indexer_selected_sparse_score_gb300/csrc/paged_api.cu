@@ -70,6 +70,7 @@ sa_status check_stride(const char *name, int64_t stride, int64_t row) {
 
 sa_status check_lists(int32_t K, int32_t local) {
   if (K < 0 || local < 0) return set_error(SA_ERR_INVALID_ARG, "need K >= 0 and local >= 0 (got %d, %d)", K, local);
+  if (K > 1 << 30) return set_error(SA_ERR_UNSUPPORTED, "K = %d above 2^30", K);
   return SA_OK;
 }
 

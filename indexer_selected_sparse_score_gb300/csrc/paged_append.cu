@@ -1,7 +1,5 @@
 // New keys and values into the pages of a paged cache, rotary embedding on the
-// way ("DeepSeek-V4.1-Flash-NVFP4 inference/model.py", Attention._window_kv:
-// apply_rotary_emb of the new kv, then the cache write), the queries rotated
-// alongside, and the mean key of every page that fills.
+// way, the queries rotated alongside, and the mean key of every page that fills.
 //
 // Rotation: pair i turns by p f_i.  The frequency is held as a 64-bit fraction
 // of a turn, F = f / (2 pi) 2^64, so p F modulo 2^64 is the angle modulo a turn
@@ -15,6 +13,15 @@
 // token: every thread issues its rows' loads, then a part of the block finds
 // the token's page and tables the rotations in shared memory, and 32-byte units
 // (two 16-byte chunks, the two halves of their pairs) leave through registers.
+// The means are a second kernel that starts in the first one's tail: a page may
+// fill from tokens of any CTA, and its rows are still in L2.
+//
+// Measured, 64 query and 8 KV heads of 128, means included: 64 tokens of a
+// decode step 11 us (two launches and a chain of dependent loads); a ragged
+// prefill of 10,907 tokens 99 us, 4.5 TB/s of the 449 MB it must move (the
+// first kernel about 5.4 TB/s, the means 10-14 us).  4096 tokens of 64 + 1
+// heads: 37 us, 3.8 TB/s.  A persistent grid that overlapped the next token's
+// loads with this one's stores measured 120 us against 95 on the prefill.
 #include <algorithm>
 #include <cmath>
 
@@ -166,9 +173,9 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
 
 // Mean of the key rows of every page whose last position is among the tokens.
 // CTA x: tokens x * per .. + per - 1 (at most kMeanThreads); a warp takes a
-// (page, KV head), or all of them share one.  It runs after the append has written every row, so a page
-// may fill from tokens in any order; which pages those are is found before the
-// wait.
+// (page, KV head), or all of them share one.  Sums are fp32, rounded to bf16
+// once.  It runs after the append has written every row, so a page may fill
+// from tokens in any order; which pages those are is found before the wait.
 template <int kDim>
 __global__ void __launch_bounds__(kMeanThreads)
 page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int per) {

@@ -12,9 +12,10 @@
 //   O += P V    M = 128 rows, N = D, K = 128 keys, V read MN-major as it landed
 // A CTA holds two row tiles (A, B: 256 rows) against the same K and V tiles,
 // each with its own softmax warpgroup and its own issuing warp; the issuers take
-// turns, so one tile's products run while the other's weights are computed.  A row's logits are taken
-// relative to a reference set by the piece's first tile; only when a vote of the
-// warp finds one that passes it by 2^8 is it raised and O rescaled.  Weights are rounded to bf16 for the product,
+// turns, so one tile's products run while the other's weights are computed.  A
+// row's logits are taken relative to a reference set by the piece's first tile;
+// only when a vote of the warp finds one that passes it by 2^8 is it raised and O
+// rescaled.  Weights are rounded to bf16 for the product (2^-8 of each at most);
 // logits, statistics and O are fp32.
 //
 // Work: (KV head, 256 rows) items x key tiles form one list cut evenly over one
@@ -22,6 +23,13 @@
 // The positions past the shared pages, each sequence's own, are a page-list
 // call (paged_attn_list.cu) that starts as SMs fall free, and a last kernel
 // merges a row's pieces of both.
+//
+// Measured, heads of 128: 128 tokens of 64 heads over one KV head behind 32 K
+// shared keys 125 us, 1.1 PFLOP/s over the whole call (the shared product runs
+// at about 1.5 on the 128 SMs it gets; the own pages' list and the merge, 5 us,
+// are the rest).  64 tokens of 64 over 8 heads, 32 K shared and up to 1500 own
+// keys: 90 us, 4.0 TB/s of the 360 MB it must read beside 0.8 PFLOP/s.  4 tokens
+// of 16 over 2 heads, 4160 shared keys: 16 us, three launches.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -574,8 +582,8 @@ cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int share
   // The page list of the sequences' own pages streams from HBM while the shared
   // part keeps the tensor cores busy: it gets SMs of its own, by the two parts'
   // tile counts (the own pages taken as half the table's) at about 1.7 us a tile
-  // of 256 rows and 1.3 us a list tile (2.2 with many heads); what it has left is shared out as the
-  // shared part's CTAs leave.
+  // of 256 rows and 1.3 us a list tile (2.2 with many heads); what it has left is
+  // shared out as the shared part's CTAs leave.
   const int sms = std::min(sm_count(), kMaxCtas);
   const double shared_us = 1.7 * static_cast<double>(s.items) * s.nkt;
   const double own_us = (list_cols(pa) == 16 ? 1.3 : 2.2) * 0.5 * static_cast<double>(pa.T) * pa.H_kv * ((pa.H / pa.H_kv + 63) / 64) *

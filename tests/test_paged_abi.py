@@ -176,3 +176,48 @@ def test_strides_of_python_tensors():
         binding._token_stride("k", torch.zeros(2, 4, 128).transpose(0, 1))
     with pytest.raises(binding.SAError):
         binding.paged_args(x, x, torch.zeros(5, 2, dtype=torch.int32).T, 16, 2, 128, 64, 10, x, x, 1.0)
+
+
+def test_tensors_the_library_would_misread_are_refused(lib):
+    import torch
+    B, T, H, Hkv, D, P, n = 3, 4, 16, 2, 128, 64, 10
+    i32, bf = dict(dtype=torch.int32), dict(dtype=torch.bfloat16)
+    seq, pos, table = torch.zeros(T, **i32), torch.zeros(T, **i32), torch.zeros(B, 5, **i32)
+    cache = torch.zeros(n, Hkv, P, D, **bf)
+
+    def args(**kw):
+        a = dict(q_seq=seq, q_pos=pos, page_table=table, K=cache, V=cache)
+        a.update(kw)
+        return binding.paged_args(a["q_seq"], a["q_pos"], a["page_table"], H, Hkv, D, P, n, a["K"], a["V"], 1.0)
+
+    pa = args()
+    for kw in (dict(q_seq=seq.long()), dict(q_pos=pos.long()), dict(q_pos=torch.zeros(2 * T, **i32)[::2]),
+               dict(q_pos=pos[1:]), dict(page_table=table.long()), dict(page_table=table[:1].expand(B, 5)),
+               dict(K=cache.float()), dict(V=torch.zeros(n, 2, Hkv, P, D, **bf)[:, 0])):
+        with pytest.raises(binding.SAError):
+            args(**kw)
+    # tokens that share one row, as a broadcast leaves them
+    k, q, ws = torch.zeros(T, Hkv, D, **bf), torch.zeros(T, H, D, **bf), torch.zeros(1 << 16, dtype=torch.uint8)
+    for x in (k[:1].expand(T, Hkv, D), k.float()):
+        with pytest.raises(binding.SAError):
+            binding.sa_paged_append(pa, x, k, ws)
+    bad_q = torch.zeros(T, 2 * H, D, **bf)[:, :H]
+    mean, scores, idx = torch.zeros(n, Hkv, D, **bf), torch.zeros(T, Hkv, 8), torch.zeros(T, Hkv, 4, **i32)
+    for call in (lambda: binding.sa_paged_append(pa, k, k, ws, q=q, q_out=bad_q),
+                 lambda: binding.sa_page_scores(pa, bad_q, mean, scores, ws),
+                 lambda: binding.sa_page_scores(pa, q, mean.float(), scores, ws),
+                 lambda: binding.sa_page_scores(pa, q, mean, scores.double(), ws),
+                 lambda: binding.sa_page_scores(pa, q, mean, torch.zeros(T, 2 * Hkv, 8)[:, :Hkv], ws),
+                 lambda: binding.sa_block_attn(pa, bad_q, idx, 4, 1, q, ws),
+                 lambda: binding.sa_block_attn(pa, q, idx.long(), 4, 1, q, ws),
+                 lambda: binding.sa_block_attn(pa, q, idx, 4, 1, bad_q, ws),
+                 lambda: binding.sa_fused_block_attn(pa, q, mean, 4, 1, idx.long(), q, ws),
+                 lambda: binding.sa_prefix_attn(pa, q, 1, q.float(), ws)):
+        with pytest.raises(binding.SAError):
+            call()
+
+
+def test_lists_past_2_30_entries_are_refused(lib):
+    assert _block(lib, _pa(), K=(1 << 30) + 1) == UNS
+    assert _fused(lib, _pa(), K=(1 << 30) + 1) == UNS
+    assert lib.sa_paged_workspace_size(_ref(_pa()), (1 << 30) + 1, 1, 0) == 0
