@@ -676,10 +676,13 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         // share of the row)
         if (!mbar_wait_warp(&full[s], phase_of(place_v(n))) && lane == 0) fail();
         if (!present) {
-          constexpr int kChunks = kDim / 8 * NH / N;  // 16-byte chunks of this thread's share of the row
+          // the row in 16-byte chunks, shared by the threads that hold its key, each
+          // lane in an order of its own (rows are 128 bytes apart: the same chunk
+          // of all of them lies in the same banks)
+          constexpr int kChunks = kDim / 8 * NH / N;
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
-            const int ch = (hb ? kChunks : 0) + i;
+            const int ch = ((hb ? kChunks : 0) + i) ^ (key & 7);
             *reinterpret_cast<uint4 *>(ring + s * L::kKv + (ch >> 3) * L::kBlock + key * 128 + 16 * (ch & 7)) =
                 make_uint4(0, 0, 0, 0);
           }
