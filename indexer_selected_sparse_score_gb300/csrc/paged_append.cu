@@ -31,8 +31,8 @@
 namespace sa {
 namespace {
 
-constexpr int kThreads = 320;     // append: two units a thread at 64 + 2 x 8 heads of dim 128
-constexpr int kMeanThreads = 256;
+constexpr int kThreads = 320;     // append, at most: two units a thread at 64 + 2 x 8 heads of dim 128
+constexpr int kMeanThreads = 256, kMeanHeads = 2;
 constexpr int kMaxPairs = 64;
 
 struct Turns {
@@ -107,13 +107,14 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
   bool ok = false;
   int page = -1, slot = 0;
   bool tabled = false;
-  for (int base = 0; base < units; base += kUnits * kThreads) {
+  const int threads = blockDim.x;
+  for (int base = 0; base < units; base += kUnits * threads) {
     // the rows' loads need no more than t: they go out before the token's
     // position and page are known
     uint4 x[kUnits], y[kUnits];
 #pragma unroll
     for (int e = 0; e < kUnits; ++e) {
-      const int u = base + e * kThreads + threadIdx.x;
+      const int u = base + e * threads + threadIdx.x;
       if (u >= units) continue;
       int c0, c1;
       chunks(u, c0, c1);
@@ -143,7 +144,7 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
     if (!ok) return;  // the whole CTA alike
 #pragma unroll
     for (int e = 0; e < kUnits; ++e) {
-      const int u = base + e * kThreads + threadIdx.x;
+      const int u = base + e * threads + threadIdx.x;
       if (u >= units) continue;
       int c0, c1;
       chunks(u, c0, c1);
@@ -171,17 +172,36 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
   }
 }
 
+// Adds kLoads loads of 32 chunks each, all in flight at once.
+template <int kLoads>
+__device__ __forceinline__ void add_rows(const uint4 *src, float (&s)[8]) {
+  uint4 x[kLoads];
+#pragma unroll
+  for (int e = 0; e < kLoads; ++e) x[e] = src[e * 32];
+#pragma unroll
+  for (int e = 0; e < kLoads; ++e) {
+    const uint32_t u[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s[2 * k] += lo_f(u[k]);
+      s[2 * k + 1] += hi_f(u[k]);
+    }
+  }
+}
+
 // Mean of the key rows of every page whose last position is among the tokens.
-// CTA x: tokens x * per .. + per - 1 (at most kMeanThreads); a warp takes a
-// (page, KV head), or all of them share one.  Sums are fp32, rounded to bf16
-// once.  It runs after the append has written every row, so a page may fill
-// from tokens in any order; which pages those are is found before the wait.
+// CTA (x, y): tokens x * per .. + per - 1 (at most kMeanThreads), KV heads
+// y * kMeanHeads .. + kMeanHeads - 1.  Its (page, head) pairs share its warps,
+// one to eight of them each.  Sums are fp32, rounded to bf16 once.  It runs
+// after the append has written every row, so a page may fill from tokens in any
+// order; which pages those are is found before the wait.
 template <int kDim>
 __global__ void __launch_bounds__(kMeanThreads)
 page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int per) {
   constexpr int kLanes = kDim / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a load
+  constexpr int kWarps = kMeanThreads / 32;
   __shared__ int pages[kMeanThreads], n_s;
-  __shared__ float part[kMeanThreads / 32][kDim];
+  __shared__ float part[kWarps][kDim];
   if (threadIdx.x == 0) n_s = 0;
   __syncthreads();
   const int own = blockIdx.x * per + threadIdx.x;
@@ -195,43 +215,48 @@ page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int pe
   __syncthreads();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes;
-  constexpr int kWarps = kMeanThreads / 32;
-  const int items = n_s * pv.H_kv;
-  // with few (page, head) pairs the block's warps share each of them
-  const bool share = items < kWarps;
-  for (int it = share ? 0 : warp; it < items; it += share ? 1 : kWarps) {
-    const int i = it / pv.H_kv, h = it - i * pv.H_kv;
-    const int64_t tile = static_cast<int64_t>(pages[i]) * pv.H_kv + h;
-    const uint4 *src = reinterpret_cast<const uint4 *>(K + tile * pv.P * kDim) + lane;
+  const int h0 = blockIdx.y * kMeanHeads, heads = min(kMeanHeads, pv.H_kv - h0);
+  const int items = n_s * heads, loads = pv.P / kRows;  // loads of a page (both powers of two)
+  // warps of an item: a power of two; with more than one every item is in the
+  // first round
+  int share = 1;
+  while (2 * share * items <= kWarps && 2 * share <= loads) share *= 2;
+  const int each = loads / share;  // of a warp
+  if (items == 0) return;
+  const int w = warp % share;  // this warp's part of the rows
+  for (int it0 = 0; it0 < items; it0 += kWarps / share) {
+    const int it = it0 + warp / share;
     float s[8] = {};
-#pragma unroll 16
-    for (int r = share ? warp * kRows : 0; r < pv.P; r += share ? kWarps * kRows : kRows) {
-      const uint4 x = src[r * kLanes];
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[2 * e] += lo_f(w[e]);
-        s[2 * e + 1] += hi_f(w[e]);
+    int64_t tile = 0;
+    if (it < items) {
+      const int i = it / heads;
+      tile = static_cast<int64_t>(pages[i]) * pv.H_kv + h0 + it - i * heads;
+      const uint4 *src = reinterpret_cast<const uint4 *>(K + tile * pv.P * kDim) + lane;
+      if (each >= 16) {
+        for (int r = 0; r < each; r += 16) add_rows<16>(src + (w * each + r) * 32, s);
+      } else if (each >= 4) {
+        for (int r = 0; r < each; r += 4) add_rows<4>(src + (w * each + r) * 32, s);
+      } else {
+        for (int r = 0; r < each; ++r) add_rows<1>(src + (w * each + r) * 32, s);
       }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) s[e] += __shfl_xor_sync(0xffffffffu, s[e], o);
-    if (share) {
+    if (share > 1) {
       if (lane < kLanes) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) part[warp][8 * c + e] = s[e];
       }
       __syncthreads();
-      if (warp == 0 && lane < kLanes) {
-        for (int w = 1; w < kWarps; ++w)
+      if (w == 0 && lane < kLanes) {
+        for (int k = 1; k < share; ++k)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] += part[w][8 * c + e];
+          for (int e = 0; e < 8; ++e) s[e] += part[warp + k][8 * c + e];
       }
-      __syncthreads();
     }
-    if (lane < kLanes && (!share || warp == 0)) {
+    if (lane < kLanes && w == 0 && it < items) {
       const float f = 1.f / static_cast<float>(pv.P);  // exact: P is a power of two
       *reinterpret_cast<uint4 *>(k_mean + tile * kDim + 8 * c) =
           make_uint4(pack_bf16(s[0] * f, s[1] * f), pack_bf16(s[2] * f, s[3] * f), pack_bf16(s[4] * f, s[5] * f),
@@ -269,12 +294,14 @@ cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t 
     const double f = rope_frequency(*rope, ramp, i) / (2.0 * 3.14159265358979323846);
     turns.f[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
   }
-  cudaError_t e = launch_ex(false, paged_append_kernel, dim3(pa.T), dim3(kThreads), 0, stream, 1, p, turns);
+  const int units = (p.q_heads + 2 * pa.H_kv) * (pa.D / 16);
+  const int threads = std::min(std::max((units / 2 + 31) & ~31, kMaxPairs), kThreads);
+  cudaError_t e = launch_ex(false, paged_append_kernel, dim3(pa.T), dim3(threads), 0, stream, 1, p, turns);
   if (e != cudaSuccess || !k_mean) return e;
   // one CTA per token while they are few, two CTAs per SM for more (most
-  // tokens end no page)
+  // tokens end no page), for every pair of heads
   const int per = std::min(std::max(1, pa.T / (2 * sm_count())), kMeanThreads);
-  const dim3 grid((pa.T + per - 1) / per);
+  const dim3 grid((pa.T + per - 1) / per, (pa.H_kv + kMeanHeads - 1) / kMeanHeads);
   return pa.D == 128 ? launch_ex(true, page_mean_kernel<128>, grid, dim3(kMeanThreads), 0, stream, 1, p.pv,
                                  static_cast<const uint16_t *>(pa.K), static_cast<uint16_t *>(k_mean), per)
                      : launch_ex(true, page_mean_kernel<64>, grid, dim3(kMeanThreads), 0, stream, 1, p.pv,
