@@ -600,7 +600,10 @@ cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int share
   e = launch_page_list(pa, q, own, out, scratch, status, true, stream);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(pa.T) * pa.H;
-  const bool many = grid >= 8 * s.items;  // pieces of a row's shared part
+  // eight warps to a row when it has many pieces of the shared part and the
+  // rows are one wave of blocks (64 tokens of 64 heads in 9 pieces: 38 us with
+  // eight, 28 with one; 4 tokens of 16 heads in 20 to 30: 18 and 21)
+  const bool many = grid >= 8 * s.items && rows <= 4 * sm_count();
   const dim3 blocks(static_cast<unsigned>(many ? rows : (rows + 7) / 8));
   const int cols = list_cols(pa);
   if (pa.D == 128)
