@@ -307,11 +307,17 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       }
     };
     int c = blockIdx.x;  // the part being worked on
+    // parts may be claimed, one ahead: CTAs start when the kernel before leaves
+    // their SM
+    int claim = 0;
+    if (p.counter && lane == 0) claim = static_cast<int>(atomicAdd(p.counter, 1u));
+    int b = 0, pos = 0, at = -1;  // sequence and position of token `at`
+    bool tok = false;
     while (ok) {
       if (p.counter) {
-        // parts are claimed: CTAs start when the kernel before leaves their SM
-        if (lane == 0) c = static_cast<int>(atomicAdd(p.counter, 1u));
-        c = __shfl_sync(0xffffffffu, c, 0);
+        c = __shfl_sync(0xffffffffu, claim, 0);
+        if (c >= G) break;
+        if (lane == 0) claim = static_cast<int>(atomicAdd(p.counter, 1u));
       }
       const long long x_begin = tot * min(c, G) / G, x_end = tot * min(c + 1, G) / G;
       int cut_unit = -1, cut_last = 0;
@@ -333,23 +339,23 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const int a = static_cast<int>(x - base);
         const int e = static_cast<int>(min(static_cast<long long>(cnt), x_end - base));
         const bool starts = a == 0, ends = e == cnt;
-        int b = 0, pos = 0;
-        const int hk = sub / p.gb, nlist = p.whole ? 0 : p.K;
+        const int hk = p.gb == 1 ? sub : sub / p.gb, nlist = p.whole ? 0 : p.K;
         // (the list's entries do not wait for the token's position)
         auto entry = [&](int i) -> int {
           return i < nlist ? p.idx[(static_cast<int64_t>(t) * p.pv.H_kv + hk) * p.K + i] : 0;
         };
         int entry_ahead = entry(a * spt + lane);
-        const bool tok = load_paged_token(p.pv, t, p.status, lane == 0 && sub == 0 && starts && !p.whole, b, pos);
+        if (t != at) tok = load_paged_token(p.pv, t, p.status, lane == 0 && sub == 0 && starts && !p.whole, b, pos);
+        at = t;
         if (tok) {
-          const int h0 = hk * p.group + (sub % p.gb) * 64;
+          const int h0 = hk * p.group + (sub - hk * p.gb) * 64;
           const int last = pos >> p.pv.logP;
           const int own = pos + 1 - last * p.pv.P;  // positions of the token's own page that it sees
           const int f = p.whole ? p.first_page : max(last + 1 - p.local, 0);
           const int r1 = min(e * spt, nlist + last + 1 - f);
           int r = a * spt, qh = 0, qe = 0;  // raw entries, queue head and end
           // the part of tile y is floor(((y + 1) G - 1) / tot)
-          const int c_last = static_cast<int>(((base + cnt) * G - 1) / tot);
+          const int c_last = ends ? c : static_cast<int>(((base + cnt) * G - 1) / tot);
           if (starts && !ends) {
             cut_unit = u;
             cut_last = c_last;
@@ -376,7 +382,8 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             while (qe - qh <= spt && r < r1) {  // enough for this tile and to know whether another follows
               const int rest = qe - qh, ent = ahead;
               r += 32;
-              ahead = resolve(r + lane, entry(r + lane));
+              ahead = -1;
+              if (r < r1) ahead = resolve(r + lane, entry(r + lane));
               const int keep = lane < rest ? queue[qh + lane] : 0;
               const uint32_t m = __ballot_sync(0xffffffffu, ent >= 0);
               __syncwarp();
@@ -408,8 +415,10 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             // been issued.
             bool mine = true;
             if ((kSl & 1) != 0 && n >= 3) {
-              const long long since = clock64();
-              while (mine && issued_s[1] < n - 2) mine = clock64() - since < kWaitBudgetCycles && !*abort_s;
+              if (issued_s[1] < n - 2) {
+                const long long since = clock64();
+                while (mine && issued_s[1] < n - 2) mine = clock64() - since < kWaitBudgetCycles && !*abort_s;
+              }
               mine = __all_sync(0xffffffffu, mine);
             }
             if (!mine || !mbar_wait_warp(&empty[s], phase_of(m) ^ 1) || *abort_s) {
@@ -468,7 +477,6 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         if (lane == 0) p.cut[c] = make_int2(cut_unit, cut_last);
         break;
       }
-      if (c >= G) break;
     }
     if (lane == 0) {
       if (ok) {
