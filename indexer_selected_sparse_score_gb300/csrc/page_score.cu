@@ -50,14 +50,25 @@ __device__ __forceinline__ void add_bf16x8(float (&a)[8], uint4 x) {
   }
 }
 
-// Sum of the G queries of (token t, KV head h) over 8 dims from chunk c.
-template <int kDim>
-__device__ __forceinline__ void sum_queries(const ScoreParams &p, int64_t t, int h, int G, int c, float (&a)[8]) {
+// Sum of queries first, first + step, .. below G of (token t, KV head h) over 8
+// dims from chunk c, kLoads in flight at a time (a loop left to the compiler
+// takes what is left of its unrolling, all of a small group, one by one).
+template <int kDim, int kLoads>
+__device__ __forceinline__ void sum_queries(const ScoreParams &p, int64_t t, int h, int G, int c, int first, int step,
+                                            float (&a)[8]) {
   const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (t * p.pv.H + static_cast<int64_t>(h) * G) * kDim) + c;
 #pragma unroll
   for (int i = 0; i < 8; ++i) a[i] = 0.f;
-#pragma unroll 16
-  for (int g = 0; g < G; ++g) add_bf16x8(a, src[g * (kDim / 8)]);
+  for (int g = first; g < G; g += kLoads * step) {
+    uint4 x[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (g + i * step < G) x[i] = src[(g + i * step) * (kDim / 8)];
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) add_bf16x8(a, x[i]);
+  }
 }
 
 __device__ __forceinline__ void write_row_token(const ScoreParams &p, int64_t row, bool ok, int b, int pos) {
@@ -70,6 +81,7 @@ __device__ __forceinline__ void write_row_token(const ScoreParams &p, int64_t ro
 
 constexpr int kThreads = 256;
 constexpr int kHeads = 8;       // KV heads of a CTA
+constexpr int kSumLoads = 8;    // queries a thread has in flight
 constexpr int kPass = 16;       // 16-page tiles of one pass over the shared memory
 
 // D += A B, 16 x 8 x 16, bf16 inputs.
@@ -95,16 +107,33 @@ __global__ void __launch_bounds__(kThreads, 3)
 score_token_kernel(const ScoreParams p, int S) {
   constexpr int kChunks = kDim / 8, kLoads = kChunks / 4;  // of a row; a lane's loads of it
   __shared__ __align__(16) uint16_t qs[kHeads][3][kDim];
-  __shared__ float tile[kHeads][16 * kPass];
+  __shared__ __align__(16) float tile[kHeads][16 * kPass];
   __shared__ int page_s[16 * kPass];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t = blockIdx.x / S, share = blockIdx.x - t * S;
   const int h0 = blockIdx.z * kHeads, nh = min(kHeads, p.pv.H_kv - h0), G = p.pv.H / p.pv.H_kv;
-  // the queries' loads do not wait for the token's position
-  if (tid < nh * kChunks) {
-    float q[8];
-    const int h = tid / kChunks, ch = tid % kChunks;
-    sum_queries<kDim>(p, t, h0 + h, G, ch, q);
+  // The queries' loads do not wait for the token's position.  A thread sums a
+  // chunk over every parts-th query; `tile` joins the parts.
+  const int sums = nh * kChunks;
+  int parts = 1;
+  while (parts * 2 * sums <= kThreads && parts * 2 * kSumLoads <= G) parts *= 2;
+  const int part = tid / sums, h = (tid - part * sums) / kChunks, ch = tid % kChunks;
+  float q[8];
+  if (part < parts) sum_queries<kDim, kSumLoads>(p, t, h0 + h, G, ch, part, parts, q);
+  if (parts > 1) {
+    float4 *joint = reinterpret_cast<float4 *>(&tile[0][0]);  // [parts][sums][2]
+    if (part > 0 && part < parts) {
+      joint[2 * tid] = make_float4(q[0], q[1], q[2], q[3]);
+      joint[2 * tid + 1] = make_float4(q[4], q[5], q[6], q[7]);
+    }
+    __syncthreads();
+    for (int i = 1; part == 0 && i < parts; ++i) {
+      const float4 u = joint[2 * (tid + i * sums)], w = joint[2 * (tid + i * sums) + 1];
+      q[0] += u.x, q[1] += u.y, q[2] += u.z, q[3] += u.w;
+      q[4] += w.x, q[5] += w.y, q[6] += w.z, q[7] += w.w;
+    }
+  }
+  if (part == 0) {
 #pragma unroll
     for (int piece = 0; piece < 3; ++piece) {
       uint32_t w[4];
@@ -259,7 +288,6 @@ score_tile_kernel(const ScoreParams p) {
   const int row = 32 * (warp & 3) + lane;          // this thread's token
   const int2 mine = tok_s[row];
   const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-  float *out = p.scores + (static_cast<int64_t>(t0 + row) * p.pv.H_kv + h) * p.ld;
   float4 *stage = reinterpret_cast<float4 *>(smem + L::stage + warp * 2048);
   const bool vec = (p.ld & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scores) & 15) == 0;
   const int nblk = (p.pv.max_pages + kTile - 1) / kTile;
@@ -270,7 +298,7 @@ score_tile_kernel(const ScoreParams p) {
     for (int i = worker ? tid : kTile * kChunks; i < kTile * kChunks; i += kTileThreads) {
       const int r = i / kChunks, ch = i % kChunks;
       float a[8] = {};
-      if (r < nt) sum_queries<kDim>(p, t0 + r, h, G, ch, a);
+      if (r < nt) sum_queries<kDim, 16>(p, t0 + r, h, G, ch, 0, 1, a);
       const uint32_t off = (ch >> 3) * L::kBlock + sw128_offset(r, 16u * (ch & 7));
 #pragma unroll
       for (int piece = 0; piece < kPieces; ++piece) {
@@ -404,30 +432,37 @@ score_tile_kernel(const ScoreParams p) {
       }
       // 32 rows x 32 columns of the warp, transposed through shared memory 16
       // columns at a time so that a store covers 64 contiguous bytes of each of
-      // eight rows
-      if (vec && j0 + 32 <= p.pv.max_pages) {
+      // eight rows, or, where rows are not 16-byte aligned or end, of each of two
+      const bool whole = vec && j0 + 32 <= p.pv.max_pages;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          __syncwarp();
+      for (int half = 0; half < 2; ++half) {
+        __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            stage[4 * lane + (e ^ ((lane >> 1) & 3))] =
-                make_float4(v[16 * half + 4 * e], v[16 * half + 4 * e + 1], v[16 * half + 4 * e + 2], v[16 * half + 4 * e + 3]);
-          __syncwarp();
+        for (int e = 0; e < 4; ++e)
+          stage[4 * lane + (e ^ ((lane >> 1) & 3))] =
+              make_float4(v[16 * half + 4 * e], v[16 * half + 4 * e + 1], v[16 * half + 4 * e + 2], v[16 * half + 4 * e + 3]);
+        __syncwarp();
+        const int j = j0 + 16 * half;
+        if (whole) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = 8 * e + (lane >> 2), ch = lane & 3;
             const float4 x = stage[4 * r + (ch ^ ((r >> 1) & 3))];
             const int row_r = 32 * (warp & 3) + r;
             if (tok_s[row_r].x == b)
-              *reinterpret_cast<float4 *>(p.scores + (static_cast<int64_t>(t0 + row_r) * p.pv.H_kv + h) * p.ld + j0 +
-                                          16 * half + 4 * ch) = x;
+              *reinterpret_cast<float4 *>(p.scores + (static_cast<int64_t>(t0 + row_r) * p.pv.H_kv + h) * p.ld + j + 4 * ch) = x;
+          }
+        } else if (j < p.pv.max_pages) {
+          const int col = lane & 15;
+#pragma unroll 4
+          for (int e = 0; e < 16; ++e) {
+            const int r = 2 * e + (lane >> 4);
+            const float x = reinterpret_cast<const float *>(stage + 4 * r + ((col >> 2) ^ ((r >> 1) & 3)))[col & 3];
+            const int row_r = 32 * (warp & 3) + r;
+            if (tok_s[row_r].x == b && j + col < p.pv.max_pages)
+              p.scores[(static_cast<int64_t>(t0 + row_r) * p.pv.H_kv + h) * p.ld + j + col] = x;
           }
         }
-      } else if (mine.x == b) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (j0 + e < p.pv.max_pages) out[j0 + e] = v[e];
       }
       __syncwarp();
     }
@@ -466,10 +501,22 @@ cudaError_t launch_page_scores(const sa_paged_args &pa, const void *q, const voi
                       row_seq,
                       row_pos,
                       status};
-  // a product pays once a tile of 128 tokens holds few sequences
-  if (pa.T >= 16 * static_cast<int64_t>(pa.B))
-    return pa.D == 128 ? launch_tile<128>(pa, p, stream) : launch_tile<64>(pa, p, stream);
+  // The kernel whose time is the lower by the measured costs (us): of the token
+  // kernel a CTA per token and 8 heads and an item per 16 pages and head; of the
+  // tile kernel, per wave of CTAs, a start, the queries' sum and the blocks of 128
+  // pages, once for every sequence among a tile's tokens.  Measured (tile, token):
+  // 4096 tokens, 4 KV heads, 512 pages 35 and 195; 1300 tokens, 8 heads, 1121
+  // pages 62 and 239; 2048, 2 heads, 147 pages 17 and 27; 1300, 1 head of 64
+  // queries, 1121 pages 63 and 51; 600, 4 heads, 44 pages 17 and 12; 475 tokens
+  // of two sequences, 14 pages 31 and 10.
   const int groups = (pa.H_kv + kHeads - 1) / kHeads;
+  const double T = pa.T, items = T * pa.H_kv * ((pa.max_pages + 15) / 16);
+  const double token_us = 5.5 + 0.0065 * T * groups + 0.33e-3 * items;
+  const int64_t tiles = (static_cast<int64_t>(pa.T) + kTile - 1) / kTile * pa.H_kv;
+  const double blocks = (pa.max_pages + kTile - 1) / kTile * (1.0 + (pa.B - 1.0) * kTile / T);
+  const double tile_us = static_cast<double>((tiles + sm_count() - 1) / sm_count()) * (10.0 + 0.5 * (pa.H / pa.H_kv) + 5.0 * blocks);
+  if (tile_us < token_us)
+    return pa.D == 128 ? launch_tile<128>(pa, p, stream) : launch_tile<64>(pa, p, stream);
   // shares of a token: three CTAs per SM over all (as many as run at once), no
   // more than it has tiles
   const int64_t target = std::max<int64_t>(1, 3LL * sm_count() / (static_cast<int64_t>(pa.T) * groups));
