@@ -288,6 +288,8 @@ score_tile_kernel(const ScoreParams p) {
   const int row = 32 * (warp & 3) + lane;          // this thread's token
   const int2 mine = tok_s[row];
   const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  const int64_t row_step = static_cast<int64_t>(p.pv.H_kv) * p.ld;  // scores of a token
+  float *rows = p.scores + (t0 + 32 * (warp & 3)) * row_step + h * p.ld;
   float4 *stage = reinterpret_cast<float4 *>(smem + L::stage + warp * 2048);
   const bool vec = (p.ld & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scores) & 15) == 0;
   const int nblk = (p.pv.max_pages + kTile - 1) / kTile;
@@ -397,6 +399,7 @@ score_tile_kernel(const ScoreParams p) {
       if (!worker) multiply(0);
       if (used > 1) gather(1);
     }
+    const uint32_t ours = __ballot_sync(0xffffffffu, mine.x == b);  // rows of the warp's tokens
     for (int i = 0; i < nblk; ++i) {
       const int u = n + i, bf = u & 1;
       const bool live = i < used;
@@ -415,14 +418,17 @@ score_tile_kernel(const ScoreParams p) {
         tmem_load(tmem + lanes + kTile * bf + c0, reinterpret_cast<uint32_t(&)[32]>(v));
         tmem_ld_wait();
         tc_fence_before();
-        const bool all = j0 + 32 <= mine.y;
         const int pg = page_s[bf * kTile + c0 + lane];
-        const uint32_t exist = __ballot_sync(0xffffffffu, pg >= 0);
+        // columns that exist and that this row's token sees
+        const int sees = mine.y - j0;
+        const uint32_t cols = __ballot_sync(0xffffffffu, pg >= 0) &
+                              (sees >= 32 ? 0xffffffffu : sees > 0 ? (1u << sees) - 1 : 0u);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v[e] *= p.scale;
-          if (!all || exist != 0xffffffffu)
-            v[e] = j0 + e < mine.y && ((exist >> e) & 1u) ? v[e] : -INFINITY;
+        for (int e = 0; e < 32; ++e) v[e] *= p.scale;
+        if (cols != 0xffffffffu) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((cols >> e) & 1u)) v[e] = -INFINITY;
         }
         landed();  // block i + 1 is in; buffer bf (keys, page ids, accumulator) is free
         if (i + 2 < used) gather(i + 2);
@@ -444,23 +450,22 @@ score_tile_kernel(const ScoreParams p) {
         __syncwarp();
         const int j = j0 + 16 * half;
         if (whole) {
+          float *dst = rows + (lane >> 2) * row_step + j + 4 * (lane & 3);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = 8 * e + (lane >> 2), ch = lane & 3;
-            const float4 x = stage[4 * r + (ch ^ ((r >> 1) & 3))];
-            const int row_r = 32 * (warp & 3) + r;
-            if (tok_s[row_r].x == b)
-              *reinterpret_cast<float4 *>(p.scores + (static_cast<int64_t>(t0 + row_r) * p.pv.H_kv + h) * p.ld + j + 4 * ch) = x;
+          for (int e = 0; e < 4; ++e, dst += 8 * row_step) {
+            const int r = 8 * e + (lane >> 2);
+            const float4 x = stage[4 * r + ((lane & 3) ^ ((r >> 1) & 3))];
+            if ((ours >> r) & 1u) *reinterpret_cast<float4 *>(dst) = x;
           }
-        } else if (j < p.pv.max_pages) {
+        } else {
           const int col = lane & 15;
+          float *dst = rows + (lane >> 4) * row_step + j + col;
+          const uint32_t write = j + col < p.pv.max_pages ? ours >> (lane >> 4) : 0u;
 #pragma unroll 4
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 16; ++e, dst += 2 * row_step) {
             const int r = 2 * e + (lane >> 4);
             const float x = reinterpret_cast<const float *>(stage + 4 * r + ((col >> 2) ^ ((r >> 1) & 3)))[col & 3];
-            const int row_r = 32 * (warp & 3) + r;
-            if (tok_s[row_r].x == b && j + col < p.pv.max_pages)
-              p.scores[(static_cast<int64_t>(t0 + row_r) * p.pv.H_kv + h) * p.ld + j + col] = x;
+            if ((write >> (2 * e)) & 1u) *dst = x;
           }
         }
       }
@@ -506,15 +511,15 @@ cudaError_t launch_page_scores(const sa_paged_args &pa, const void *q, const voi
   // tile kernel, per wave of CTAs, a start, the queries' sum and the blocks of 128
   // pages, once for every sequence among a tile's tokens.  Measured (tile, token):
   // 4096 tokens, 4 KV heads, 512 pages 35 and 195; 1300 tokens, 8 heads, 1121
-  // pages 62 and 239; 2048, 2 heads, 147 pages 17 and 27; 1300, 1 head of 64
-  // queries, 1121 pages 63 and 51; 600, 4 heads, 44 pages 17 and 12; 475 tokens
-  // of two sequences, 14 pages 31 and 10.
+  // pages 48 and 239; 300, 8 heads, 958 pages 31 and 49; 2048, 2 heads, 147 pages
+  // 14 and 25; 1300, 1 head of 64 queries, 1121 pages 61 and 50; 600, 4 heads, 44
+  // pages 14 and 12; 475 tokens of two sequences, 14 pages 27 and 8.
   const int groups = (pa.H_kv + kHeads - 1) / kHeads;
   const double T = pa.T, items = T * pa.H_kv * ((pa.max_pages + 15) / 16);
   const double token_us = 5.5 + 0.0065 * T * groups + 0.33e-3 * items;
   const int64_t tiles = (static_cast<int64_t>(pa.T) + kTile - 1) / kTile * pa.H_kv;
   const double blocks = (pa.max_pages + kTile - 1) / kTile * (1.0 + (pa.B - 1.0) * kTile / T);
-  const double tile_us = static_cast<double>((tiles + sm_count() - 1) / sm_count()) * (10.0 + 0.5 * (pa.H / pa.H_kv) + 5.0 * blocks);
+  const double tile_us = static_cast<double>((tiles + sm_count() - 1) / sm_count()) * (9.0 + 0.5 * (pa.H / pa.H_kv) + 3.0 * blocks);
   if (tile_us < token_us)
     return pa.D == 128 ? launch_tile<128>(pa, p, stream) : launch_tile<64>(pa, p, stream);
   // shares of a token: three CTAs per SM over all (as many as run at once), no
