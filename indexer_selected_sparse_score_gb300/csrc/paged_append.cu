@@ -213,7 +213,6 @@ page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int pe
     }
   }
   __syncthreads();
-  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes;
   const int h0 = blockIdx.y * kMeanHeads, heads = min(kMeanHeads, pv.H_kv - h0);
   const int items = n_s * heads, loads = pv.P / kRows;  // loads of a page (both powers of two)
@@ -222,8 +221,9 @@ page_mean_kernel(const PagedView pv, const uint16_t *K, uint16_t *k_mean, int pe
   int share = 1;
   while (2 * share * items <= kWarps && 2 * share <= loads) share *= 2;
   const int each = loads / share;  // of a warp
+  const int w = warp % share;      // this warp's part of the rows
+  pdl_wait();
   if (items == 0) return;
-  const int w = warp % share;  // this warp's part of the rows
   for (int it0 = 0; it0 < items; it0 += kWarps / share) {
     const int it = it0 + warp / share;
     float s[8] = {};
@@ -295,7 +295,11 @@ cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t 
     turns.f[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
   }
   const int units = (p.q_heads + 2 * pa.H_kv) * (pa.D / 16);
-  const int threads = std::min(std::max((units / 2 + 31) & ~31, kMaxPairs), kThreads);
+  // two units a thread when the tokens fill the SMs (7465 of 40 rows of 128: 46
+  // us with one, 40 with two), one when they do not (147 of 28 rows of 64: 6.9 us
+  // with two, 6.2 with one)
+  const int per_thread = pa.T > 4 * sm_count() ? 2 : 1;
+  const int threads = std::min(std::max((units / per_thread + 31) & ~31, kMaxPairs), kThreads);
   cudaError_t e = launch_ex(false, paged_append_kernel, dim3(pa.T), dim3(threads), 0, stream, 1, p, turns);
   if (e != cudaSuccess || !k_mean) return e;
   // one CTA per token while they are few, two CTAs per SM for more (most
