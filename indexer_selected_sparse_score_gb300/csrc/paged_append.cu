@@ -295,11 +295,11 @@ cudaError_t launch_paged_append(const sa_paged_args &pa, const void *k, int64_t 
     turns.f[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
   }
   const int units = (p.q_heads + 2 * pa.H_kv) * (pa.D / 16);
-  // two units a thread when the tokens fill the SMs (7465 of 40 rows of 128: 46
-  // us with one, 40 with two), one when they do not (147 of 28 rows of 64: 6.9 us
-  // with two, 6.2 with one)
-  const int per_thread = pa.T > 4 * sm_count() ? 2 : 1;
-  const int threads = std::min(std::max((units / per_thread + 31) & ~31, kMaxPairs), kThreads);
+  // when the tokens fill the SMs, blocks of two units a thread (7465 tokens of 40
+  // rows of 128: 46 us with blocks of kThreads, 40 so); a few tokens are served by
+  // the larger block sooner (8 of 32 rows of 64: 5.4 us, 6.2 with 128 threads)
+  const int threads =
+      pa.T > 4 * sm_count() ? std::min(std::max((units / 2 + 31) & ~31, kMaxPairs), kThreads) : kThreads;
   cudaError_t e = launch_ex(false, paged_append_kernel, dim3(pa.T), dim3(threads), 0, stream, 1, p, turns);
   if (e != cudaSuccess || !k_mean) return e;
   // one CTA per token while they are few, two CTAs per SM for more (most
