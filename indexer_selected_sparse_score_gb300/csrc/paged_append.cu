@@ -83,20 +83,20 @@ __device__ __forceinline__ void rotate_halves(uint4 &x, uint4 &y, const float2 *
   y = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 4)
 paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
   __shared__ float2 cs[kMaxPairs];
   pdl_trigger();
   const int t = blockIdx.x;
-  const int upr = p.D >> 4;                 // 32-byte units per row
+  const int log_upr = p.D == 128 ? 3 : 2;   // of the 32-byte units per row
   const int kept = (p.D - p.dim) >> 4;      // units before the rotated span
   const int span = p.dim >> 3;              // chunks of the rotated span
   const int first = (p.D >> 3) - span;      // first rotated chunk
-  const int units = (p.q_heads + 2 * p.pv.H_kv) * upr;
+  const int units = (p.q_heads + 2 * p.pv.H_kv) << log_upr;
   // chunks of unit u within its row: two neighbours, or the two halves of
   // eight pairs
   auto chunks = [&](int u, int &c0, int &c1) {
-    const int i = u % upr, j = i - kept;
+    const int i = u & ((1 << log_upr) - 1), j = i - kept;
     const bool half = p.halves && j >= 0;
     c0 = half ? first + j : 2 * i;
     c1 = half ? c0 + (span >> 1) : 2 * i + 1;
@@ -118,7 +118,7 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
       if (u >= units) continue;
       int c0, c1;
       chunks(u, c0, c1);
-      const int row = u / upr, h = row - p.q_heads;
+      const int row = u >> log_upr, h = row - p.q_heads;
       const uint16_t *src = h < 0           ? p.q + t * p.q_stride + static_cast<int64_t>(row) * p.D
                             : h < p.pv.H_kv ? p.k + t * p.k_stride + static_cast<int64_t>(h) * p.D
                                             : p.v + t * p.v_stride + static_cast<int64_t>(h - p.pv.H_kv) * p.D;
@@ -148,7 +148,7 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
       if (u >= units) continue;
       int c0, c1;
       chunks(u, c0, c1);
-      const int row = u / upr, h = row - p.q_heads;
+      const int row = u >> log_upr, h = row - p.q_heads;
       uint16_t *dst;
       if (h < 0) {
         dst = p.q_out + (static_cast<int64_t>(t) * p.pv.H + row) * p.D;
