@@ -17,11 +17,11 @@
 // fill from tokens of any CTA, and its rows are still in L2.
 //
 // Measured, 64 query and 8 KV heads of 128, means included: 64 tokens of a
-// decode step 11 us (two launches and a chain of dependent loads); a ragged
-// prefill of 10,907 tokens 99 us, 4.5 TB/s of the 449 MB it must move (the
-// first kernel about 5.4 TB/s, the means 10-14 us).  4096 tokens of 64 + 1
-// heads: 37 us, 3.8 TB/s.  A persistent grid that overlapped the next token's
-// loads with this one's stores measured 120 us against 95 on the prefill.
+// decode step 8 to 12 us (two launches and a chain of dependent loads); a ragged
+// prefill of 10,907 tokens 90 us, 5.0 TB/s of the 449 MB it must move (the first
+// kernel about 5.7 TB/s, the means 11 us).  4096 tokens of 64 + 1 heads: 35 us,
+// 4.0 TB/s.  A persistent grid that overlapped the next token's loads with this
+// one's stores measured 120 us against 95 on the prefill.
 #include <algorithm>
 #include <cmath>
 
@@ -102,7 +102,8 @@ paged_append_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
     c1 = half ? c0 + (span >> 1) : 2 * i + 1;
   };
   // units a thread has in flight (3 of 256 threads and 1 of 640 measured 2 and
-  // 12 % slower on a prefill)
+  // 12 % slower on a prefill; five blocks of 320 per SM instead of four spill
+  // registers: 91 us against 90, three leave too little in flight: 100)
   constexpr int kUnits = 2;
   bool ok = false;
   int page = -1, slot = 0;

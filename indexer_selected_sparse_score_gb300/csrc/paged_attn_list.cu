@@ -38,11 +38,14 @@
 //
 // Measured, heads of 128: 64 tokens of 64 heads over one KV head, 34 pages of 64
 // each: 29 us, 2.5 TB/s of the 72 MB it must read (about 3 us to the first tile,
-// 2.2 us a tile of 64 KB per SM against 1.5 at HBM's rate, and 5 us of merge
-// with its launch).  966 tokens of 32 over 4 heads, 13 pages of 128 each: 225
-// us; the lists differ from token to token, so 3.3 GB pass from L2 to the SMs at
-// 14.6 TB/s (about 50 bytes a clock and SM), which bounds it.  One token of 16
-// over 2 heads, 34 pages of 64: 12 us, two launches and their chains of loads.
+// 7 tiles of 64 KB on each SM, 1.5 us each at HBM's rate, and 5 us of merge with
+// its launch).  966 tokens of 32 over 4 heads, 13 pages of 128 each: 206 us; the
+// lists differ from token to token, so 3.4 GB pass from L2 to the SMs at 16 TB/s
+// (about 60 bytes a clock and SM), which bounds it.  One token of 16 over 2
+// heads, 34 pages of 64: 12 us, two launches and their chains of loads.  Units
+// of a tile or two cost about 2 us each and CTA, half of it the walk of the
+// list, half the chain of a tile: 306 tokens of 64 over 8 heads at the start of
+// a sequence 51 us.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
