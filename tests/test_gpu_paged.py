@@ -759,3 +759,83 @@ def test_calls_run_on_the_stream_they_are_given():
     side.synchronize()
     assert torch.equal(a, b)
     c.check(a, lambda t, h: list(range(300)))
+
+
+# ------------------------------------------------------- many tokens at once ---
+
+@pytest.mark.parametrize("D,P,Hkv,G,lens,new,order,ld", [
+    (128, 16, 8, 2, [5001], 700, "rising", 0),
+    (64, 16, 4, 4, [4001, 2500], 600, "rising", 0),
+    (128, 64, 8, 1, [16384], 1300, "rising", 0),          # whole blocks of pages, rows 16-byte aligned
+    (128, 32, 8, 16, [9000], 513, "rising", 288),
+    (128, 16, 8, 3, [3007, 1200, 2999], 300, "mixed", 0),
+    (64, 16, 8, 1, [3000, 16, 700], 400, "falling", 191),
+])
+def test_scores_of_large_chunks(D, P, Hkv, G, lens, new, order, ld):
+    r = np.random.RandomState(5)
+    c = Case(40, lens, D, P, Hkv, G)
+    at = [(b, p) for b, n in enumerate(lens) for p in range(max(n - new, 0), n)]
+    if order == "mixed":
+        at = [at[i] for i in r.permutation(len(at))]
+    elif order == "falling":
+        at = at[::-1]
+    bad = [17, len(at) // 2, len(at) - 1] if order == "mixed" else []
+    seq, pos = [b for b, _ in at], [p for _, p in at]
+    for t in bad:
+        seq[t] = len(lens) if t == 17 else -3
+    c.tokens(seq, pos)
+    mean = (torch.randn(c.total, Hkv, D, generator=c.g) / 8).bfloat16()
+    seen = torch.zeros(c.total, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        seen[c.table[b, :n // P].long()] = True
+    mean[~seen] = float("nan")
+    lost = order == "falling"
+    if lost:  # a page whose id is out of range scores -inf
+        c.table[0, 5] = c.total
+    c.upload()
+    width = ld or c.max_pages
+    scores = torch.full((c.T, Hkv, width), 9.0, device=DEV)
+    ws = sb.new_paged_workspace(c.pa)
+    sb.sa_page_scores(c.pa, c.d["q"], mean.to(DEV), scores, ws)
+    assert sb.sa_check_device_status(ws) == (sb.SA_ERR_DEVICE_DATA if bad or lost else sb.SA_OK)
+    got = scores.cpu().double()
+    q = c.q.double().view(c.T, Hkv, G, D)
+    assert bool((got[..., c.max_pages:] == 9.0).all()) and bool((got[bad] == 9.0).all())
+    for b, n in enumerate(lens):
+        tok = [t for t in range(c.T) if seq[t] == b]
+        k = torch.zeros(Hkv, c.max_pages, D, dtype=torch.float64)
+        ids = c.table[b, :n // P].long().clamp(max=c.total - 1)
+        k[:, :n // P] = mean[ids].double().nan_to_num().transpose(0, 1)
+        s = torch.einsum("thd,hjd->thj", q[tok].sum(2), k) * c.scale
+        # as check_scores: G sums and D products in fp32
+        bound = torch.einsum("thd,hjd->thj", q[tok].abs().sum(2), k.abs()) * c.scale * (G + D + 4) * 2.0 ** -23
+        vis = (torch.tensor([pos[t] for t in tok]) + 1) // P
+        live = (torch.arange(c.max_pages)[None] < vis[:, None])[:, None].expand(-1, Hkv, -1).clone()
+        if lost and b == 0:
+            live[..., 5] = False
+        row = got[tok][..., :c.max_pages]
+        assert bool((row[~live] == -float("inf")).all())
+        assert bool(((row - s).abs() <= bound)[live].all())
+
+
+@pytest.mark.parametrize("D,P,Hkv,G,dim,halves", [(128, 64, 8, 3, 128, True), (64, 16, 3, 1, 32, False),
+                                                  (128, 128, 1, 64, 64, False), (64, 128, 5, 1, 64, True)])
+def test_append_of_many_tokens(D, P, Hkv, G, dim, halves):
+    lens = [5 * P + 3, 2000, 17, 901]
+    c = Case(41, lens, D, P, Hkv, G)
+    seq, pos = [b for b, n in enumerate(lens) for _ in range(n)], [p for n in lens for p in range(n)]
+    order = np.random.RandomState(2).permutation(len(seq))
+    c.tokens([seq[i] for i in order], [pos[i] for i in order]).upload()
+    rope = sb.RopeArgs(dim, 10000.0, 1.0, 0, 32.0, 1.0)
+    k, v = (torch.randn(c.T, Hkv, D, generator=c.g).bfloat16().to(DEV) for _ in range(2))
+    mean, q_out = torch.full((c.total, Hkv, D), 5.0, dtype=torch.bfloat16, device=DEV), c.out()
+    ws = run_append(c, k, v, q=c.d["q"], q_out=q_out, rope=rope, halves=halves, k_mean=mean)
+    status_ok(ws)
+    check_append(c, k.cpu(), v.cpu(), c.q, ref.rope_freqs(dim, 10000.0), halves, q_out, c.K, c.V)
+    K, got = c.d["K"].cpu().double(), mean.cpu().double()
+    full = torch.zeros(c.total, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        full[c.table[b, :n // P].long()] = True
+    assert bool((got[~full] == 5.0).all())
+    m, e = K[full].mean(dim=2), 2.0 ** -24 * K[full].abs().sum(dim=2)  # fp32 sum of P rows
+    assert bool(((got[full] - m).abs() <= 2.0 ** -8 * (m.abs() + e) + e).all())
