@@ -61,6 +61,7 @@ namespace {
 using namespace umma;
 
 constexpr int kTile = 128;      // keys per tile
+constexpr int kFewBlocks = 640; // of a merge (four per SM are resident)
 constexpr int kQueue = 40;      // page entries the loader holds: under a tile's and one batch of 32
 // The reference a weight is taken against lies kHead above the maximum that
 // set it (log2 units), and is raised once a logit passes that maximum by kLazy:
@@ -755,9 +756,9 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   if (p.keep) pdl_wait();
   tc_fence_before();
   __syncthreads();
-  if (tid < kSl) {
-    // every copy lands before the CTA exits: the last one issued into slot tid
-    // (long done unless a wait gave up)
+  if (*abort_s && tid < kSl) {
+    // A wait gave up, so a copy may be on its way (else its product has waited
+    // for each): the last one issued into slot tid lands before the CTA exits.
     auto issued = [&](int m) {
       return m == 0 ? issued_s[0] > 0 : (m & 1) ? (m + 1) / 2 < issued_s[0] : (m - 2) / 2 < issued_s[1];
     };
@@ -772,18 +773,37 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   }
 }
 
-// Merges the parts of the unit that CTA c's range cuts: o = sum 2^(m_i - M) o_i
+// Merges the parts of the unit that starts in CTA c's range and ends past it: o = sum 2^(m_i - M) o_i
 // / sum 2^(m_i - M) l_i.  kSplit warps per head, each every kSplit-th part (8
 // when a unit has many parts: the chain of loads is then what the merge costs).
 template <int N, int kDim, int kSplit>
 __global__ void __launch_bounds__(256)
 merge_cut_kernel(const ListParams p) {
   __shared__ float acc_s[8][kDim + 2];
-  pdl_wait();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int2 cut = p.cut[c];
+  const int upt = p.pv.H_kv * p.gb;
+  __shared__ int2 cut_s;
+  const bool known = !p.whole && gridDim.x * gridDim.y <= kFewBlocks;
+  if (known) {
+    // Which unit CTA c cut can be worked out while the kernel before runs: it
+    // saves a load after the wait (one token over 34 pages 12.9 to 12.3 us, over
+    // 20 pages of 16 12.4 to 11.6).  With many blocks the divisions take more of
+    // that kernel's issue slots than the load costs (64 tokens 29.1 to 30.9):
+    // those read what it wrote.
+    if (threadIdx.x == 0) {
+      const long long tot = static_cast<long long>(p.pv.T) * upt * p.tpu, G = min(static_cast<long long>(p.parts), tot);
+      const long long x0 = tot * c / G, x1 = tot * (c + 1) / G, u = (x1 - 1) / p.tpu, end = (u + 1) * p.tpu;
+      int b, pos;
+      const bool is = u * p.tpu >= x0 && end > x1 &&
+                      load_paged_token(p.pv, static_cast<int>(u / upt), nullptr, false, b, pos);
+      cut_s = is ? make_int2(static_cast<int>(u), static_cast<int>((end * G - 1) / tot)) : make_int2(-1, 0);
+    }
+    __syncthreads();
+  }
+  pdl_wait();
+  const int2 cut = known ? cut_s : p.cut[c];
   if (cut.x < 0) return;
-  const int upt = p.pv.H_kv * p.gb, t = cut.x / upt, sub = cut.x % upt;
+  const int t = cut.x / upt, sub = cut.x % upt;
   const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64, heads = min(64, (hk + 1) * p.group - h0);
   const int i = blockIdx.y * (8 / kSplit) + warp / kSplit;
   if (i >= heads) return;  // (kSplit 8: the whole block)
