@@ -156,12 +156,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const int64_t x0 = tot * c / G, x1 = tot * (c + 1) / G;
   // A softmax warp's 32 query rows of an item, into the K-major swizzled layout;
   // a load covers whole rows.
-  auto load_queries = [&](int item) {
-    constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a load
-    const int hk = item / p.npairs, row0 = 32 * (warp & 3), ch = lane % kLanes;
-    const int64_t r0 = static_cast<int64_t>(item - hk * p.npairs) * kRows + 128 * (warp >> 2) + row0;
-    uint8_t *dst = qs + (warp >> 2) * L::kKv + (ch >> 3) * L::kBlock;
-    uint4 v[32 / kPer];
+  constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a load
+  auto fetch_queries = [&](int item, uint4 (&v)[32 / kPer]) {
+    const int hk = item / p.npairs, ch = lane % kLanes;
+    const int64_t r0 = static_cast<int64_t>(item - hk * p.npairs) * kRows + 128 * (warp >> 2) + 32 * (warp & 3);
 #pragma unroll
     for (int i = 0; i < 32 / kPer; ++i) {
       const int64_t rr = r0 + kPer * i + lane / kLanes;
@@ -170,15 +168,23 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       v[i] = make_uint4(0, 0, 0, 0);
       if (rr < p.rows) v[i] = reinterpret_cast<const uint4 *>(p.q + src * kDim)[ch];
     }
+  };
+  auto put_queries = [&](const uint4 (&v)[32 / kPer]) {
+    const int ch = lane % kLanes;
+    uint8_t *dst = qs + (warp >> 2) * L::kKv + (ch >> 3) * L::kBlock;
 #pragma unroll
     for (int i = 0; i < 32 / kPer; ++i)
-      *reinterpret_cast<uint4 *>(dst + sw128_offset(row0 + kPer * i + lane / kLanes, 16u * (ch & 7))) = v[i];
+      *reinterpret_cast<uint4 *>(dst + sw128_offset(32 * (warp & 3) + kPer * i + lane / kLanes, 16u * (ch & 7))) = v[i];
   };
-  if (warp < 8 && x0 < x1) load_queries(static_cast<int>(x0 / p.nkt));
+  // the first item's are on their way while the block sets up and the loader
+  // finds its pages
+  uint4 first_q[32 / kPer];
+  if (warp < 8 && x0 < x1) fetch_queries(static_cast<int>(x0 / p.nkt), first_q);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
+  if (warp < 8 && x0 < x1) put_queries(first_q);
   auto fail = [&]() {
     raise_flag(p.status, kFlagTimeout);
     *abort_s = 1;
@@ -346,7 +352,11 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (r - row >= p.rows) continue;
       if (first) {
         // (every product of the piece before has been read out)
-        if (n > 0) load_queries(at.item);
+        if (n > 0) {
+          uint4 v[32 / kPer];
+          fetch_queries(at.item, v);
+          put_queries(v);
+        }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[w]);
@@ -600,17 +610,25 @@ cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int share
   e = launch_page_list(pa, q, own, out, scratch, status, true, stream);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(pa.T) * pa.H;
-  // eight warps to a row when it has many pieces of the shared part and the
-  // rows are one wave of blocks (64 tokens of 64 heads in 9 pieces: 38 us with
-  // eight, 28 with one; 4 tokens of 16 heads in 20 to 30: 18 and 21)
-  const bool many = grid >= 8 * s.items && rows <= 4 * sm_count();
-  const dim3 blocks(static_cast<unsigned>(many ? rows : (rows + 7) / 8));
+  // eight or four warps to a row when it has pieces of the shared part for each
+  // of them and the rows are one wave of blocks (85 tokens of 16 heads in 17
+  // pieces: 43.7 us with one, 42.2 with four; 4 of 16 in 33: 20.2 with one, 16.7
+  // with eight; 61 of 48 in 9: 26.1 with one, 38 with eight)
+  const int64_t pieces = (grid + s.items - 1) / s.items;
+  auto pays = [&](int split) { return pieces >= 2 * split && rows * split <= 40ll * sm_count(); };
+  const int split = pays(8) ? 8 : pays(4) ? 4 : 1;
   const int cols = list_cols(pa);
+  auto merge = [&](auto kernel) {
+    const dim3 blocks(static_cast<unsigned>((rows * split + 7) / 8));
+    return launch_ex(true, kernel, blocks, dim3(256), 0, stream, 1, p, own, cols, grid);
+  };
   if (pa.D == 128)
-    return many ? launch_ex(true, merge_rows_kernel<128, 8>, blocks, dim3(256), 0, stream, 1, p, own, cols, grid)
-                : launch_ex(true, merge_rows_kernel<128, 1>, blocks, dim3(256), 0, stream, 1, p, own, cols, grid);
-  return many ? launch_ex(true, merge_rows_kernel<64, 8>, blocks, dim3(256), 0, stream, 1, p, own, cols, grid)
-              : launch_ex(true, merge_rows_kernel<64, 1>, blocks, dim3(256), 0, stream, 1, p, own, cols, grid);
+    return split == 8   ? merge(merge_rows_kernel<128, 8>)
+           : split == 4 ? merge(merge_rows_kernel<128, 4>)
+                        : merge(merge_rows_kernel<128, 1>);
+  return split == 8   ? merge(merge_rows_kernel<64, 8>)
+         : split == 4 ? merge(merge_rows_kernel<64, 4>)
+                      : merge(merge_rows_kernel<64, 1>);
 }
 
 }  // namespace sa
