@@ -173,10 +173,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     // a CTA that starts when every part has been claimed leaves at once (not
     // CTA 0, which reports the tokens it skips)
     const bool late = tid == 0 && blockIdx.x > 0 && *static_cast<volatile uint32_t *>(p.counter) >= static_cast<uint32_t>(p.parts);
-    if (__syncthreads_or(late)) {
-      pdl_wait();
-      return;
-    }
+    if (__syncthreads_or(late)) return;
   }
   if (tid == 0) {
     for (int i = 0; i < kSl; ++i) {
@@ -310,6 +307,15 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         t += 32;
       }
     };
+    // First tile of part c.  Claimed parts shrink towards the end, from twice the
+    // mean to one tile, so that CTAs that start late share what is left.
+    auto part_begin = [&](int c) -> long long {
+      if (!p.counter) return tot * c / G;
+      // c (2 G - c) / G^2 in steps of 2^-11, and a tile for every part
+      static_assert(kMaxParts <= 1024, "32 bits");
+      const uint32_t w = (static_cast<uint32_t>(c * (2 * G - c)) << 11) / static_cast<uint32_t>(G * G);
+      return c + ((tot - G) * w >> 11);
+    };
     int c = blockIdx.x;  // the part being worked on
     // parts may be claimed: CTAs start when the kernel before leaves their SM; one
     // ahead while there are more left than CTAs
@@ -325,7 +331,7 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         held = G - c > static_cast<int>(gridDim.x);
         if (lane == 0 && held) claim = static_cast<int>(atomicAdd(p.counter, 1u));
       }
-      const long long x_begin = tot * min(c, G) / G, x_end = tot * min(c + 1, G) / G;
+      const long long x_begin = part_begin(min(c, G)), x_end = part_begin(min(c + 1, G));
       int cut_unit = -1, cut_last = 0;
       long long x = x_begin;
       if (x < x_end) {
@@ -360,13 +366,14 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           const int f = p.whole ? p.first_page : max(last + 1 - p.local, 0);
           const int r1 = min(e * spt, nlist + last + 1 - f);
           int r = a * spt, qh = 0, qe = 0;  // raw entries, queue head and end
-          // the part of tile y is floor(((y + 1) G - 1) / tot)
-          const int c_last = ends ? c : static_cast<int>(((base + cnt) * G - 1) / tot);
-          if (starts && !ends) {
+          if (p.keep) {
+            if (lane == 0 && starts) p.info[u].x = c;
+            if (lane == 0 && ends) p.info[u].y = c;
+          } else if (starts && !ends) {
+            // the part of tile y is floor(((y + 1) G - 1) / tot)
             cut_unit = u;
-            cut_last = c_last;
+            cut_last = static_cast<int>(((base + cnt) * G - 1) / tot);
           }
-          if (p.keep && starts && lane == 0) p.info[u] = make_int2(c, c_last);
           // page entry i of the list (page id, bit 30 set for the token's own
           // page, whose later positions are masked), -1 when it names no page
           auto resolve = [&](int i, int j) -> int {
@@ -751,9 +758,10 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       }
     }
   }
-  // parts of a whole-sequence call are merged by a kernel that also needs the
-  // one before this: completing after it makes the chain transitive
-  if (p.keep) pdl_wait();
+  // The merge of kept parts also needs the kernel before this one: a CTA that
+  // completes after it makes the chain transitive (one, so that the others leave
+  // their SMs to the merge).
+  if (p.keep && blockIdx.x == 0) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (*abort_s && tid < kSl) {
