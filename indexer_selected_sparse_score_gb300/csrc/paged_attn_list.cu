@@ -317,19 +317,14 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       return c + ((tot - G) * w >> 11);
     };
     int c = blockIdx.x;  // the part being worked on
-    // parts may be claimed: CTAs start when the kernel before leaves their SM; one
-    // ahead while there are more left than CTAs
-    int claim = 0;
-    bool held = false;
     int b = 0, pos = 0, at = -1;  // sequence and position of token `at`
     bool tok = false;
     while (ok) {
       if (p.counter) {
-        if (lane == 0 && !held) claim = static_cast<int>(atomicAdd(p.counter, 1u));
-        c = __shfl_sync(0xffffffffu, claim, 0);
+        // parts are claimed: CTAs start when the kernel before leaves their SM
+        if (lane == 0) c = static_cast<int>(atomicAdd(p.counter, 1u));
+        c = __shfl_sync(0xffffffffu, c, 0);
         if (c >= G) break;
-        held = G - c > static_cast<int>(gridDim.x);
-        if (lane == 0 && held) claim = static_cast<int>(atomicAdd(p.counter, 1u));
       }
       const long long x_begin = part_begin(min(c, G)), x_end = part_begin(min(c + 1, G));
       int cut_unit = -1, cut_last = 0;

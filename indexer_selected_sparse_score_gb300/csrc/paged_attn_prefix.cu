@@ -591,12 +591,12 @@ cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int share
   p.status = status;
   // The page list of the sequences' own pages streams from HBM while the shared
   // part keeps the tensor cores busy: it gets SMs of its own, by the two parts'
-  // costs: about 1.7 us a tile of 256 rows, and 1 us a unit and 0.75 a list tile
+  // costs: about 1.4 us a tile of 256 rows, and 1 us a unit and 0.75 a list tile
   // (with many heads 1.5 and 1.5), the own pages taken as half the table's.  What
   // it has left is shared out as the shared part's CTAs leave.
   const int sms = std::min(sm_count(), kMaxCtas);
   const bool few = list_cols(pa) == 16;
-  const double shared_us = 1.7 * static_cast<double>(s.items) * s.nkt;
+  const double shared_us = 1.4 * static_cast<double>(s.items) * s.nkt;
   const double unit_us = (few ? 1.0 : 1.5) + (few ? 0.75 : 1.5) * 0.5 * ((pa.max_pages - shared_pages + s.spt - 1) / s.spt);
   const double own_us = unit_us * static_cast<double>(pa.T) * pa.H_kv * ((pa.H / pa.H_kv + 63) / 64);
   int most = std::max(sms / 2, static_cast<int>(sms * shared_us / (shared_us + own_us) + 0.5));
