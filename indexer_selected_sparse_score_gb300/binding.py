@@ -305,25 +305,27 @@ def sa_paged_workspace_size(pa: PagedArgs, K: int = 0, local: int = 0, shared_pa
     return int(load().sa_paged_workspace_size(ctypes.byref(pa), K, local, shared_pages))
 
 
-def _token_stride(name: str, x) -> int:
-    """Elements between consecutive tokens of [T, heads, D] rows (0: dense, or a
-    raw pointer); the heads of a token have to be dense."""
-    if not isinstance(x, torch.Tensor):
-        return 0
-    stride, shape = x.stride(), x.shape
-    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
-        raise SAError(SA_ERR_INVALID_ARG, f"{name} must be [T, heads, D] with dense heads")
-    if shape[0] > 1 and stride[0] < shape[1] * shape[2]:  # an expanded tensor; the library takes 0 as dense
+def _token_rows(name: str, x, heads: int, dim: int, T: int):
+    """Pointer of [T, heads, dim] bf16 rows and the elements between consecutive
+    tokens (0: dense, or a raw pointer); the heads of a token have to be dense."""
+    if x is None or type(x) is int:
+        return x, 0
+    stride = x.stride()
+    if x.element_size() != 2 or len(stride) != 3 or stride[2] != 1 or (stride[1] != dim and heads > 1):
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} must be [T, heads, D] bf16 with dense heads")
+    if T > 1 and stride[0] < heads * dim:  # an expanded tensor; the library takes 0 as dense
         raise SAError(SA_ERR_INVALID_ARG, f"{name}'s tokens overlap")
-    return stride[0] if shape[0] > 1 else 0
+    return x.data_ptr(), stride[0] if T > 1 else 0
 
 
 def _dense(name: str, x, itemsize: int):
     """Pointer of a tensor that the library takes as dense rows of ``itemsize``-byte
     values (a raw pointer or None as it is)."""
-    if isinstance(x, torch.Tensor) and not (x.element_size() == itemsize and x.is_contiguous()):
+    if x is None or type(x) is int:
+        return x
+    if x.element_size() != itemsize or not x.is_contiguous():
         raise SAError(SA_ERR_INVALID_ARG, f"{name} must be contiguous, of {itemsize}-byte values (got {x.dtype})")
-    return _p(x)
+    return x.data_ptr()
 
 
 def sa_paged_append(pa: PagedArgs, k, v, ws, q=None, q_out=None, rope: Optional[RopeArgs] = None,
@@ -332,12 +334,12 @@ def sa_paged_append(pa: PagedArgs, k, v, ws, q=None, q_out=None, rope: Optional[
     ``q`` is rotated into ``q_out`` alongside, and ``k_mean`` gets the mean key of
     every page that fills.  k, v and q may be slices of a fused projection
     (their token strides are passed on)."""
-    for name, x in (("k", k), ("v", v), ("q", q)):
-        if isinstance(x, torch.Tensor) and x.element_size() != 2:
-            raise SAError(SA_ERR_INVALID_ARG, f"{name} must be bf16 (got {x.dtype})")
+    T, D = pa.T, pa.D
+    kp, ks = _token_rows("k", k, pa.H_kv, D, T)
+    vp, vs = _token_rows("v", v, pa.H_kv, D, T)
+    qp, qs = _token_rows("q", q, pa.H, D, T)
     p, n = _ws(ws)
-    _check(load().sa_paged_append(ctypes.byref(pa), _p(k), _token_stride("k", k), _p(v), _token_stride("v", v), _p(q),
-                                  _token_stride("q", q), _dense("q_out", q_out, 2),
+    _check(load().sa_paged_append(ctypes.byref(pa), kp, ks, vp, vs, qp, qs, _dense("q_out", q_out, 2),
                                   ctypes.byref(rope) if rope is not None else None, int(halves),
                                   _dense("k_mean", k_mean, 2), p, n, _s(stream)))
 

@@ -167,13 +167,15 @@ def test_workspace_grows_with_what_it_holds(lib):
 
 def test_strides_of_python_tensors():
     import torch
-    x = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
-    assert binding._token_stride("k", x) == 256
-    assert binding._token_stride("k", torch.zeros(4, 6, 128)[:, 1:3]) == 768
-    with pytest.raises(binding.SAError):
-        binding._token_stride("k", torch.zeros(4, 2, 256)[..., ::2])
-    with pytest.raises(binding.SAError):
-        binding._token_stride("k", torch.zeros(2, 4, 128).transpose(0, 1))
+    bf = dict(dtype=torch.bfloat16)
+    x = torch.zeros(4, 2, 128, **bf)
+    assert binding._token_rows("k", x, 2, 128, 4) == (x.data_ptr(), 256)
+    y = torch.zeros(4, 6, 128, **bf)[:, 1:3]
+    assert binding._token_rows("k", y, 2, 128, 4) == (y.data_ptr(), 768)
+    assert binding._token_rows("k", None, 2, 128, 4) == (None, 0) and binding._token_rows("k", 256, 2, 128, 4) == (256, 0)
+    for bad in (torch.zeros(4, 2, 256, **bf)[..., ::2], torch.zeros(2, 4, 128, **bf).transpose(0, 1), x.view(4, 256)):
+        with pytest.raises(binding.SAError):
+            binding._token_rows("k", bad, 2, 128, 4)
     with pytest.raises(binding.SAError):
         binding.paged_args(x, x, torch.zeros(5, 2, dtype=torch.int32).T, 16, 2, 128, 64, 10, x, x, 1.0)
 
