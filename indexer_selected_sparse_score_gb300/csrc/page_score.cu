@@ -447,7 +447,8 @@ score_tile_kernel(const ScoreParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           stage[4 * lane + (e ^ ((lane >> 1) & 3))] =
-              make_float4(v[16 * half + 4 * e], v[16 * half + 4 * e + 1], v[16 * half + 4 * e + 2], v[16 * half + 4 * e + 3]);
+              make_float4(v[16 * half + 4 * e], v[16 * half + 4 * e + 1], v[16 * half + 4 * e + 2],
+                          v[16 * half + 4 * e + 3]);
         __syncwarp();
         const int j = j0 + 16 * half;
         if (whole) {
@@ -520,7 +521,8 @@ cudaError_t launch_page_scores(const sa_paged_args &pa, const void *q, const voi
   const double token_us = 5.5 + 0.0065 * T * groups + 0.33e-3 * items;
   const int64_t tiles = (static_cast<int64_t>(pa.T) + kTile - 1) / kTile * pa.H_kv;
   const double blocks = (pa.max_pages + kTile - 1) / kTile * (1.0 + (pa.B - 1.0) * kTile / T);
-  const double tile_us = static_cast<double>((tiles + sm_count() - 1) / sm_count()) * (9.0 + 0.5 * (pa.H / pa.H_kv) + 3.0 * blocks);
+  const double tile_us = static_cast<double>((tiles + sm_count() - 1) / sm_count()) *
+                         (9.0 + 0.5 * (pa.H / pa.H_kv) + 3.0 * blocks);
   if (tile_us < token_us)
     return pa.D == 128 ? launch_tile<128>(pa, p, stream) : launch_tile<64>(pa, p, stream);
   // shares of a token: three CTAs per SM over all (as many as run at once), no

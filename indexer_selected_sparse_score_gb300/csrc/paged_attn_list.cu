@@ -23,13 +23,14 @@
 // parts: one for each CTA, one CTA per SM, two with up to 16 heads (a decode
 // step reads each page once, so HBM is the bound and every SM must stream to the
 // end); beside the product with the shared pages, whose CTAs leave their SMs at
-// different times, four per SM that CTAs claim.  A unit that falls into several
-// CTAs leaves its parts (m_ref, sum, O) in scratch for a merge kernel.  (A
-// cluster per unit that merges over distributed shared memory instead: 33.5 us
-// against 31.0 for 64 tokens of 64 heads over 2112 keys, and 16.5 against 14.2
-// for a single token.)  Entries that name no page are dropped before tiles are
-// formed; positions past the token's own are masked, and the V rows they hold
-// are zeroed in shared memory, since 0 x NaN would reach the sum.
+// different times, four per SM that CTAs claim, shrinking towards the end.  A
+// unit that falls into several CTAs leaves its parts (m_ref, sum, O) in scratch
+// for a merge kernel.  (A cluster per unit that merges over distributed shared
+// memory instead: 33.5 us against 31.0 for 64 tokens of 64 heads over 2112 keys,
+// and 16.5 against 14.2 for a single token.)  Entries that name no page are
+// dropped before tiles are formed; positions past the token's own are masked,
+// and the V rows they hold are zeroed in shared memory, since 0 x NaN would
+// reach the sum.
 //
 // Warps: 0-3 or 0-7 softmax and output; the next two issue S^T and O^T; then one
 // resolves the lists, copies K and publishes one record per tile; the last
@@ -39,7 +40,7 @@
 // Measured, heads of 128: 64 tokens of 64 heads over one KV head, 34 pages of 64
 // each: 29 us, 2.5 TB/s of the 72 MB it must read (about 3 us to the first tile,
 // 7 tiles of 64 KB on each SM, 1.5 us each at HBM's rate, and 5 us of merge with
-// its launch).  966 tokens of 32 over 4 heads, 13 pages of 128 each: 206 us; the
+// its launch).  966 tokens of 32 over 4 heads, 13 pages of 128 each: 205 us; the
 // lists differ from token to token, so 3.4 GB pass from L2 to the SMs at 16 TB/s
 // (about 60 bytes a clock and SM), which bounds it.  One token of 16 over 2
 // heads, 34 pages of 64: 12 us, two launches and their chains of loads.  Units
@@ -172,7 +173,8 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   if (p.counter) {
     // a CTA that starts when every part has been claimed leaves at once (not
     // CTA 0, which reports the tokens it skips)
-    const bool late = tid == 0 && blockIdx.x > 0 && *static_cast<volatile uint32_t *>(p.counter) >= static_cast<uint32_t>(p.parts);
+    const bool late = tid == 0 && blockIdx.x > 0 &&
+                      *static_cast<volatile uint32_t *>(p.counter) >= static_cast<uint32_t>(p.parts);
     if (__syncthreads_or(late)) return;
   }
   if (tid == 0) {
