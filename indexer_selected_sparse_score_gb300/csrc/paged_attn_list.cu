@@ -20,7 +20,7 @@
 // output that is itself rounded to bf16); logits, sums and O are fp32.
 //
 // Work: the tiles of all units (128 keys each) form one list, cut evenly into
-// parts: one for each CTA, one CTA per SM, two with up to 16 heads (a decode
+// parts, at the units' ends where that costs a CTA little: one for each CTA, one CTA per SM, two with up to 16 heads (a decode
 // step reads each page once, so HBM is the bound and every SM must stream to the
 // end); beside the product with the shared pages, whose CTAs leave their SMs at
 // different times, four per SM that CTAs claim, shrinking towards the end.  A
@@ -38,8 +38,8 @@
 // drains its copies and products and returns.
 //
 // Measured, heads of 128: 64 tokens of 64 heads over one KV head, 34 pages of 64
-// each: 29 us, 2.5 TB/s of the 72 MB it must read (about 3 us to the first tile,
-// 7 tiles of 64 KB on each SM, 1.5 us each at HBM's rate, and 5 us of merge with
+// each: 28 us, 2.6 TB/s of the 72 MB it must read (about 3 us to the first tile,
+// 8.5 tiles of 64 KB on each SM, 1.2 us each at HBM's rate, and 5 us of merge with
 // its launch).  966 tokens of 32 over 4 heads, 13 pages of 128 each: 205 us; the
 // lists differ from token to token, so 3.4 GB pass from L2 to the SMs at 16 TB/s
 // (about 60 bytes a clock and SM), which bounds it.  One token of 16 over 2
@@ -62,6 +62,11 @@ namespace {
 using namespace umma;
 
 constexpr int kTile = 128;      // keys per tile
+// Tiles that a CTA saves by not crossing into another unit (64 tokens of 64 heads,
+// 17 tiles each: 30.3 us cut evenly over 152 CTAs, 28.0 over two for each unit),
+// and that a call saves without a merge (26 units of two tiles: 13.9 us in halves,
+// 12.4 whole).
+constexpr int kCross = 2, kMerge = 2;
 constexpr int kFewBlocks = 640; // of a merge (four per SM are resident)
 constexpr int kQueue = 40;      // page entries the loader holds: under a tile's and one batch of 32
 // The reference a weight is taken against lies kHead above the maximum that
@@ -835,6 +840,7 @@ cudaError_t launch_list(const sa_paged_args &pa, const void *q, ListParams &p, i
   e = launch_ex(pdl, kern, dim3(grid), dim3(L::kThreads), smem, stream, 1, qmap, kmap, vmap, p);
   if (e != cudaSuccess || p.keep) return e;
   const int64_t units = static_cast<int64_t>(pa.T) * pa.H_kv * p.gb;
+  if (!p.whole && units == grid) return cudaSuccess;  // every unit was one CTA's
   return units * 8 <= grid
              ? launch_ex(true, merge_cut_kernel<N, kDim, 8>, dim3(grid, N), dim3(256), 0, stream, 1, p)
              : launch_ex(true, merge_cut_kernel<N, kDim, 1>, dim3(grid, N / 8), dim3(256), 0, stream, 1, p);
@@ -905,7 +911,13 @@ cudaError_t launch_page_list(const sa_paged_args &pa, const void *q, ListParams 
   } else {
     const int64_t entries = static_cast<int64_t>(p.K) + std::min(p.local, pa.max_pages);
     p.tpu = static_cast<int>(std::max<int64_t>(1, (entries + spt - 1) / spt));
-    grid = static_cast<int>(std::min<int64_t>(grid, static_cast<int64_t>(units) * p.tpu));
+    const int64_t n = static_cast<int64_t>(units), even = (n * p.tpu + grid - 1) / grid;  // tiles of a CTA
+    int64_t k = std::min<int64_t>(grid / n, p.tpu);  // whole CTAs of each unit
+    if (k > 0 && p.tpu <= even + kMerge)
+      k = 1;
+    else if (k > 0 && (p.tpu + k - 1) / k > even + kCross)
+      k = 0;
+    grid = static_cast<int>(k > 0 ? n * k : std::min<int64_t>(grid, n * p.tpu));
   }
   p.parts = p.keep ? std::min(4 * sm_count(), kMaxParts) : grid;
   p.counter = p.keep ? status + kCounterWord : nullptr;
