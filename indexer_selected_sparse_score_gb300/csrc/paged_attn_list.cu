@@ -20,17 +20,17 @@
 // output that is itself rounded to bf16); logits, sums and O are fp32.
 //
 // Work: the tiles of all units (128 keys each) form one list, cut evenly into
-// parts, at the units' ends where that costs a CTA little: one for each CTA, one CTA per SM, two with up to 16 heads (a decode
-// step reads each page once, so HBM is the bound and every SM must stream to the
-// end); beside the product with the shared pages, whose CTAs leave their SMs at
-// different times, four per SM that CTAs claim, shrinking towards the end.  A
-// unit that falls into several CTAs leaves its parts (m_ref, sum, O) in scratch
-// for a merge kernel.  (A cluster per unit that merges over distributed shared
-// memory instead: 33.5 us against 31.0 for 64 tokens of 64 heads over 2112 keys,
-// and 16.5 against 14.2 for a single token.)  Entries that name no page are
-// dropped before tiles are formed; positions past the token's own are masked,
-// and the V rows they hold are zeroed in shared memory, since 0 x NaN would
-// reach the sum.
+// parts, at the units' ends where that costs a CTA little: one part for each CTA,
+// one CTA per SM, two with up to 16 heads (a decode step reads each page once, so
+// HBM is the bound and every SM must stream to the end); beside the product with
+// the shared pages, whose CTAs leave their SMs at different times, four per SM
+// that CTAs claim, shrinking towards the end.  A unit that falls into several
+// CTAs leaves its parts (m_ref, sum, O) in scratch for a merge kernel.  (A
+// cluster per unit that merges over distributed shared memory instead: 33.5 us
+// against 31.0 for 64 tokens of 64 heads over 2112 keys, and 16.5 against 14.2
+// for a single token.)  Entries that name no page are dropped before tiles are
+// formed; positions past the token's own are masked, and the V rows they hold
+// are zeroed in shared memory, since 0 x NaN would reach the sum.
 //
 // Warps: 0-3 or 0-7 softmax and output; the next two issue S^T and O^T; then one
 // resolves the lists, copies K and publishes one record per tile; the last
