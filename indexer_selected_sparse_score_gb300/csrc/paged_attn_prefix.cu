@@ -157,34 +157,31 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // A softmax warp's 32 query rows of an item, into the K-major swizzled layout;
   // a load covers whole rows.
   constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a load
-  auto fetch_queries = [&](int item, uint4 (&v)[32 / kPer]) {
+  auto load_queries = [&](int item) {
+    uint4 v[32 / kPer];
     const int hk = item / p.npairs, ch = lane % kLanes;
-    const int64_t r0 = static_cast<int64_t>(item - hk * p.npairs) * kRows + 128 * (warp >> 2) + 32 * (warp & 3);
+    // row r is head r % group of token r / group
+    int r = (item - hk * p.npairs) * kRows + 128 * (warp >> 2) + 32 * (warp & 3) + lane / kLanes;
+    int t = r / p.group, g = r - t * p.group;
 #pragma unroll
-    for (int i = 0; i < 32 / kPer; ++i) {
-      const int64_t rr = r0 + kPer * i + lane / kLanes;
-      const int t = static_cast<int>(rr) / p.group;
-      const int64_t src = static_cast<int64_t>(t) * p.pv.H + hk * p.group + (rr - static_cast<int64_t>(t) * p.group);
+    for (int i = 0; i < 32 / kPer; ++i, r += kPer, g += kPer) {
+      while (g >= p.group) {
+        g -= p.group;
+        ++t;
+      }
+      const int64_t src = static_cast<int64_t>(t) * p.pv.H + hk * p.group + g;
       v[i] = make_uint4(0, 0, 0, 0);
-      if (rr < p.rows) v[i] = reinterpret_cast<const uint4 *>(p.q + src * kDim)[ch];
+      if (r < p.rows) v[i] = reinterpret_cast<const uint4 *>(p.q + src * kDim)[ch];
     }
-  };
-  auto put_queries = [&](const uint4 (&v)[32 / kPer]) {
-    const int ch = lane % kLanes;
     uint8_t *dst = qs + (warp >> 2) * L::kKv + (ch >> 3) * L::kBlock;
 #pragma unroll
     for (int i = 0; i < 32 / kPer; ++i)
       *reinterpret_cast<uint4 *>(dst + sw128_offset(32 * (warp & 3) + kPer * i + lane / kLanes, 16u * (ch & 7))) = v[i];
   };
-  // the first item's are on their way while the block sets up and the loader
-  // finds its pages
-  uint4 first_q[32 / kPer];
-  if (warp < 8 && x0 < x1) fetch_queries(static_cast<int>(x0 / p.nkt), first_q);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
-  if (warp < 8 && x0 < x1) put_queries(first_q);
   auto fail = [&]() {
     raise_flag(p.status, kFlagTimeout);
     *abort_s = 1;
@@ -352,11 +349,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (r - row >= p.rows) continue;
       if (first) {
         // (every product of the piece before has been read out)
-        if (n > 0) {
-          uint4 v[32 / kPer];
-          fetch_queries(at.item, v);
-          put_queries(v);
-        }
+        load_queries(at.item);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[w]);
