@@ -182,6 +182,9 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                       *static_cast<volatile uint32_t *>(p.counter) >= static_cast<uint32_t>(p.parts);
     if (__syncthreads_or(late)) return;
   }
+  // parts are claimed by the loader of K, the first while the block sets up
+  int claim = 0;
+  if (p.counter && warp == kWarpK && lane == 0) claim = static_cast<int>(atomicAdd(p.counter, 1u));
   if (tid == 0) {
     for (int i = 0; i < kSl; ++i) {
       mbar_init(&full[i], 1);
@@ -326,11 +329,10 @@ page_list_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     int c = blockIdx.x;  // the part being worked on
     int b = 0, pos = 0, at = -1;  // sequence and position of token `at`
     bool tok = false;
-    while (ok) {
+    for (bool again = false; ok; again = true) {
       if (p.counter) {
-        // parts are claimed: CTAs start when the kernel before leaves their SM
-        if (lane == 0) c = static_cast<int>(atomicAdd(p.counter, 1u));
-        c = __shfl_sync(0xffffffffu, c, 0);
+        if (again && lane == 0) claim = static_cast<int>(atomicAdd(p.counter, 1u));
+        c = __shfl_sync(0xffffffffu, claim, 0);
         if (c >= G) break;
       }
       const long long x_begin = part_begin(min(c, G)), x_end = part_begin(min(c + 1, G));
