@@ -38,9 +38,9 @@
 // drains its copies and products and returns.
 //
 // Measured, heads of 128: 64 tokens of 64 heads over one KV head, 34 pages of 64
-// each: 28 us, 2.6 TB/s of the 72 MB it must read (about 3 us to the first tile,
+// each: 27 us, 2.7 TB/s of the 72 MB it must read (about 3 us to the first tile,
 // 8.5 tiles of 64 KB on each SM, 1.2 us each at HBM's rate, and 5 us of merge with
-// its launch).  966 tokens of 32 over 4 heads, 13 pages of 128 each: 205 us; the
+// its launch).  966 tokens of 32 over 4 heads, 13 pages of 128 each: 203 us; the
 // lists differ from token to token, so 3.4 GB pass from L2 to the SMs at 16 TB/s
 // (about 60 bytes a clock and SM), which bounds it.  One token of 16 over 2
 // heads, 34 pages of 64: 12 us, two launches and their chains of loads.  Units

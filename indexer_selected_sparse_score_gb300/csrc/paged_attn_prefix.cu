@@ -25,11 +25,11 @@
 // merges a row's pieces of both.
 //
 // Measured, heads of 128: 128 tokens of 64 heads over one KV head behind 32 K
-// shared keys 121 us, 1.15 PFLOP/s over the whole call (the shared product runs
+// shared keys 120 us, 1.16 PFLOP/s over the whole call (the shared product runs
 // at about 1.5 on the 128 SMs it gets; the own pages' list and the merge, 5 us,
 // are the rest).  64 tokens of 64 over 8 heads, 32 K shared and up to 1500 own
-// keys: 89 us, 4.1 TB/s of the 360 MB it must read beside 0.8 PFLOP/s.  4 tokens
-// of 16 over 2 heads, 4160 shared keys: 15 us, three launches.
+// keys: 87 us, 4.1 TB/s of the 360 MB it must read beside 0.8 PFLOP/s.  4 tokens
+// of 16 over 2 heads, 4160 shared keys: 14 us, three launches.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
