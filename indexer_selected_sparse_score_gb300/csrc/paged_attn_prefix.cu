@@ -369,7 +369,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int e = 0; e < 128; ++e)
           if (!((mask >> (e >> 4)) & 1u)) v[e] = cs > 0.f ? -INFINITY : INFINITY;  // cs v = -inf
       }
+      // A sum of 0: the piece has met no key of the row yet.  Its logits are then
+      // taken against 0, so that none is lost to a placeholder.
       if (first) ref = 0.f;
+      const bool fresh = l == 0.f;
       float2 *v2 = reinterpret_cast<float2 *>(v);
       float top = -INFINITY;
       {
@@ -382,18 +385,17 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
       }
-      if (__any_sync(0xffffffffu, first || top > kLazy - kHead)) {
-        // the piece's first tile, or a logit passes its row's reference by the
-        // lazy margin: raise it; the sum and O (which holds the products up to
-        // the tile before) shrink in step.  (Finite even when the tile has no
-        // key: the next tile then raises it.)
-        const float up = first ? fmaxf(top + kHead, -1e30f) : fmaxf(top + kHead, 0.f);
+      if (__any_sync(0xffffffffu, fresh || top > kLazy - kHead)) {
+        // the row's first keys, or a logit passes its reference by the lazy
+        // margin: set or raise it; the sum and O (which holds the products up to
+        // the tile before) shrink in step.  A tile without a key leaves it at 0.
+        const float up = top == -INFINITY ? 0.f : fresh ? top + kHead : fmaxf(top + kHead, 0.f);
         const float2 nup2 = make_float2(-up, -up);
         ref += up;
 #pragma unroll
         for (int e = 0; e < 64; ++e) v2[e] = add2(v2[e], nup2);
         if (!first) {
-          const float fac = exp2f(-up);
+          const float fac = exp2f(fminf(-up, 0.f));  // (above 1 for a sum of 0 only)
           l *= fac;
 #pragma unroll 1
           for (int i = 0; i < kDim / 16; ++i) {
@@ -436,7 +438,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         ++pieces;
         tc_fence_after();
         const int64_t to_row = static_cast<int64_t>(at.item + c) * kRows + 128 * w + row;
-        if (r < p.rows) p.ml[to_row] = make_float2(ref, l);
+        if (r < p.rows) p.ml[to_row] = make_float2(l == 0.f ? -INFINITY : ref, l);
         // O of the warp's rows, 32 columns at a time through this warp's part of
         // the query tile (its products are done), so that a store covers 128
         // contiguous bytes of each of four rows

@@ -839,3 +839,33 @@ def test_append_of_many_tokens(D, P, Hkv, G, dim, halves):
     assert bool((got[~full] == 5.0).all())
     m, e = K[full].mean(dim=2), 2.0 ** -24 * K[full].abs().sum(dim=2)  # fp32 sum of P rows
     assert bool(((got[full] - m).abs() <= 2.0 ** -8 * (m.abs() + e) + e).all())
+
+
+# ------------------------------------------------------------ shared pieces ---
+
+@pytest.mark.parametrize("D,P,G,T", [(128, 128, 64, 32), (64, 128, 128, 16), (128, 64, 16, 96)])
+@pytest.mark.parametrize("lost", ["first", "first two tiles", "odd tiles", "even tiles", "most"])
+def test_prefix_attention_with_shared_tiles_lost(D, P, G, T, lost):
+    # several tiles of 128 shared keys to a CTA, some without a page: where a
+    # piece begins with one, the tiles after it count as ever.  Logits several
+    # units apart, so that a tile's weights are far from equal.
+    tiles, spt = 96, 128 // P
+    shared = tiles * spt
+    bad_tiles = dict(zip(("first", "first two tiles", "odd tiles", "even tiles", "most"),
+                         ([0], [0, 1], range(1, tiles, 2), range(0, tiles, 2), range(0, tiles - 5))))[lost]
+    c = Case(50, [shared * P + 9, shared * P + 200, shared * P + 128], D, P, 1, G, shared=shared)
+    c.tokens([t % 3 for t in range(T)], [c.lens[t % 3] - 1 - t // 3 % 9 for t in range(T)])
+    c.q *= 5
+    c.upload()
+    table = c.d["table"].clone()
+    bad = torch.tensor([j * spt + i for j in bad_tiles for i in range(spt)])
+    table[0, bad.to(DEV)] = -1
+    pa = sb.paged_args(c.d["seq"], c.d["pos"], table, c.H, 1, D, P, c.total, c.d["K"], c.d["V"], c.scale)
+    out = c.out()
+    ws = sb.new_paged_workspace(pa, shared_pages=shared)
+    sb.sa_prefix_attn(pa, c.d["q"], shared, out, ws)
+    assert sb.sa_check_device_status(ws) == sb.SA_ERR_DEVICE_DATA
+    keep = torch.ones(shared, dtype=torch.bool)
+    keep[bad] = False
+    pos = torch.arange(shared * P)[keep.repeat_interleave(P)]
+    c.check(out, lambda t, h: torch.cat([pos, torch.arange(shared * P, int(c.pos[t]) + 1)]), tokens=range(0, T, 5))
