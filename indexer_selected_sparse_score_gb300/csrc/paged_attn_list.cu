@@ -53,6 +53,7 @@
 
 #include "internal.h"
 #include "paged.cuh"
+#include "paged_bounds.h"
 #include "paged_list.h"
 #include "paged_umma.cuh"
 
@@ -102,11 +103,7 @@ struct ListSmem {
   // of 32 in the 64-byte swizzle.
   static constexpr int kPBufs = N <= 32 ? 2 : 1;
   static constexpr uint32_t kPRow = N == 16 ? 64 : 128;
-  // Tile records.  Record n + kSlots / 2 + 5 is written once S(n + 5) is done,
-  // for which the weights of tile n + 2 were written and so, with two P^T
-  // buffers at most, O(n) issued: every reader (V's loader among them) is past
-  // record n.
-  static constexpr int kRecs = kSlots / 2 + 5;
+  static constexpr int kRecs = list_records(kSlots);       // tile records
   static constexpr uint32_t kBlock = kTile * 128;          // one 64-dim block of a tile
   static constexpr uint32_t kKv = kBlock * (kDim / 64);
   static constexpr size_t ring = 0;
