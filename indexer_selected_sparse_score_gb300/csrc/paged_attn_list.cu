@@ -811,7 +811,7 @@ merge_cut_kernel(const ListParams p) {
   }
   pdl_wait();
   const int2 cut = known ? cut_s : p.cut[c];
-  if (cut.x < 0) return;
+  if (!cut_ok(cut.x, cut.y, static_cast<int64_t>(p.pv.T) * upt, c, p.parts)) return;  // (-1: none)
   const int t = cut.x / upt, sub = cut.x % upt;
   const int hk = sub / p.gb, h0 = hk * p.group + (sub % p.gb) * 64, heads = min(64, (hk + 1) * p.group - h0);
   const int i = blockIdx.y * (8 / kSplit) + warp / kSplit;

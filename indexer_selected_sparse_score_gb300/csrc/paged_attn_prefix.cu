@@ -36,6 +36,7 @@
 
 #include "internal.h"
 #include "paged.cuh"
+#include "paged_bounds.h"
 #include "paged_list.h"
 #include "paged_umma.cuh"
 
@@ -503,8 +504,9 @@ merge_rows_kernel(const PrefixParams p, const ListParams own, int cols, int grid
     const int2 rng = own.info[u];
     m.add(warp % kSplit, kSplit, a1 - a0 + 1, lane, p.ml, p.part,
           [&](int k) { return (item + a0 + k) * kRows + r % kRows; });
-    m.add(warp % kSplit, kSplit, rng.y - rng.x + 1, lane, own.ml, own.part,
-          [&](int k) { return (u + rng.x + k) * cols + g % 64; });
+    if (part_range_ok(rng.x, rng.y, own.parts))  // (else a wait gave up, and was flagged)
+      m.add(warp % kSplit, kSplit, rng.y - rng.x + 1, lane, own.ml, own.part,
+            [&](int k) { return (u + rng.x + k) * cols + g % 64; });
   }
   if (m.template join<kSplit>(acc_s, lane) && ok) m.store(own.out + id * kDim, lane);
 }

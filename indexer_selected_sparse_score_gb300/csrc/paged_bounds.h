@@ -1,6 +1,14 @@
 // Sizes and range checks of the page-list kernel that host code can compile.
 #pragma once
 
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define SA_BOUNDS_FN __host__ __device__ inline
+#else
+#define SA_BOUNDS_FN inline
+#endif
+
 namespace sa {
 
 // Tile records that the loader of the page-list kernel keeps, for a ring of
@@ -11,5 +19,14 @@ namespace sa {
 // n - slots / 2 - 5.  The end record waits for no slot, so it has only what the
 // record before it had: one more.
 constexpr int list_records(int slots) { return slots / 2 + 6; }
+
+// What a merge reads from scratch is taken only where it can be a range of this
+// call: after a wait that gave up (the status word says so) it may be anything.
+// The parts first .. last of a unit, of `parts` in all.
+SA_BOUNDS_FN bool part_range_ok(int first, int last, int parts) { return first >= 0 && first <= last && last < parts; }
+// A unit of `units` that CTA c cut, its last part in CTA `last` of `ctas`.
+SA_BOUNDS_FN bool cut_ok(int64_t unit, int last, int64_t units, int c, int ctas) {
+  return unit >= 0 && unit < units && part_range_ok(c, last, ctas);
+}
 
 }  // namespace sa

@@ -72,3 +72,31 @@ def test_every_reader_is_past_a_record_that_is_overwritten(bounds, slots, pbufs)
 
 def test_a_ring_of_one_record_less_is_told_apart():
     assert unread_records(6, 2, 8) and unread_records(12, 2, 11)
+
+
+def test_ranges_a_merge_may_follow(bounds):
+    # own parts are read at slots unit + first .. unit + last of units + 1024, in
+    # last - first + 1 rounds: anything else that scratch may hold is refused
+    good = [(0, 0, 1), (0, 607, 608), (600, 607, 608), (5, 5, 1024)]
+    bad = [(-1, 0, 608), (0, -1, 608), (3, 2, 608), (0, 608, 608), (608, 608, 608), ("INT_MIN", "INT_MAX", 608),
+           ("INT_MAX", "INT_MAX", 608), (0, "INT_MAX", 608), ("INT_MIN", 0, 608), (0x3F800000, 0x40000000, 608)]
+    assert bounds(*[f"part_range_ok({a}, {b}, {n})" for a, b, n in good]) == [1] * len(good)
+    assert bounds(*[f"part_range_ok({a}, {b}, {n})" for a, b, n in bad]) == [0] * len(bad)
+
+
+def test_cuts_a_merge_may_follow(bounds):
+    good = [(0, 4, 10, 3, 152), (9, 3, 10, 3, 152), (9, 151, 10, 3, 152), ((1 << 30) - 1, 1, 1 << 30, 0, 256)]
+    bad = [(-1, 0, 10, 0, 152), (10, 4, 10, 3, 152), (0, 2, 10, 3, 152), (0, 152, 10, 3, 152), ("INT_MIN", 5, 10, 3, 152),
+           ("INT_MAX", 5, 10, 3, 152), (0, "INT_MAX", 10, 3, 152), (0, "INT_MIN", 10, 3, 152)]
+    assert bounds(*["cut_ok({}, {}, {}, {}, {})".format(*x) for x in good]) == [1] * len(good)
+    assert bounds(*["cut_ok({}, {}, {}, {}, {})".format(*x) for x in bad]) == [0] * len(bad)
+
+
+def test_the_merges_check_what_they_read():
+    # the ranges that come from scratch pass through the checks above
+    prefix = open(build.CSRC + "/paged_attn_prefix.cu").read()
+    lists = open(build.CSRC + "/paged_attn_list.cu").read()
+    read = prefix.index("own.info[u]")
+    assert read < prefix.index("part_range_ok(rng.x, rng.y, own.parts)", read) < prefix.index("own.ml, own.part", read)
+    read = lists.index(": p.cut[c];")
+    assert read < lists.index("cut_ok(cut.x, cut.y", read) < lists.index("m.add(", read)
