@@ -11,8 +11,16 @@ constexpr int kMaxParts = 1024;  // most parts of a claimed list
 // merge that ends a call resets it).
 constexpr int kCounterWord = 16;
 
+// The larger of the two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Running merge of parts (reference, sum, output row): a warp per row, lane l
 // holding values V l .. V l + V - 1 of it.  Eight parts' loads go out together.
+// A part whose reference or sum is NaN makes the row NaN, as in a unit of one part.
 template <int kDim>
 struct Merge {
   static constexpr int V = kDim / 32;
@@ -44,7 +52,7 @@ struct Merge {
       }
       float m = M;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, s[i].x);
+      for (int i = 0; i < 8; ++i) m = max_nan(m, s[i].x);
       if (m == -INFINITY) continue;
       scale_to(m);
 #pragma unroll
@@ -73,7 +81,7 @@ struct Merge {
       __syncthreads();
       if (warp % kSplit) return false;
       float m = M;
-      for (int w = 1; w < kSplit; ++w) m = fmaxf(m, s[warp + w][kDim]);
+      for (int w = 1; w < kSplit; ++w) m = max_nan(m, s[warp + w][kDim]);
       if (m == -INFINITY) return true;
       scale_to(m);
       for (int w = 1; w < kSplit; ++w) {
@@ -86,7 +94,7 @@ struct Merge {
     }
   }
   __device__ __forceinline__ void store(__nv_bfloat16 *row, int lane) const {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int e = 0; e < V; e += 2)
       *reinterpret_cast<__nv_bfloat162 *>(row + V * lane + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);

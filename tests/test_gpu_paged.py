@@ -869,3 +869,46 @@ def test_prefix_attention_with_shared_tiles_lost(D, P, G, T, lost):
     keep[bad] = False
     pos = torch.arange(shared * P)[keep.repeat_interleave(P)]
     c.check(out, lambda t, h: torch.cat([pos, torch.arange(shared * P, int(c.pos[t]) + 1)]), tokens=range(0, T, 5))
+
+
+# --------------------------------------------------------------------- NaN ---
+
+@pytest.mark.parametrize("T,D,P,Hkv,G,K,shared", [
+    (1, 128, 64, 2, 8, 32, 0), (1, 64, 16, 1, 16, 200, 300), (1, 128, 128, 1, 64, 9, 40),   # units cut over CTAs
+    (3, 128, 64, 1, 40, 60, 70), (40, 128, 32, 2, 16, 6, 9), (150, 64, 64, 1, 64, 3, 5),
+    (333, 128, 64, 1, 8, 1, 1),                                                             # units of one CTA each
+])
+def test_nan_stays_in_the_rows_it_belongs_to(T, D, P, Hkv, G, K, shared):
+    # a head of NaN in the first query, and a NaN key of KV head 0 that only the
+    # last token (alone in its sequence) sees: NaN there however the work is cut,
+    # and nowhere else
+    n = max((K + 3) * P, (shared + 2) * P) + T + 7
+    c = Case(51, [n, n], D, P, Hkv, G, shared=shared)
+    c.tokens([0] * (T - 1) + [1], [n - 1 - t for t in range(T)])
+    c.q[0, G // 2] = float("nan")
+    last = int(c.pos[T - 1])
+    c.K[int(c.table[1, last // P]), 0, last % P] = float("nan")
+    c.upload()
+    idx = torch.full((T, Hkv, max(K, 1)), -1, dtype=torch.int32)
+    for t in range(T):
+        idx[t, :, :K] = torch.arange(K, dtype=torch.int32)
+    out, out2, out3 = c.out(), c.out(), c.out()
+    ws = sb.new_paged_workspace(c.pa, K, 2, shared)
+    sb.sa_block_attn(c.pa, c.d["q"], idx.to(DEV), K, 2, out, ws)
+    sb.sa_prefix_attn(c.pa, c.d["q"], shared, out2, ws)
+    sb.sa_prefix_attn(c.pa, c.d["q"], 0, out3, sb.new_paged_workspace(c.pa))
+    status_ok(ws)
+    want = torch.zeros(T, c.H, D, dtype=torch.bool)
+    want[0, G // 2] = True
+    want[T - 1, :G] = True
+    for o in (out, out2, out3):
+        assert torch.equal(torch.isnan(o.cpu()), want)
+    c.q[0, G // 2] = 0  # (the oracle's bound is one for a group's heads; this head is not compared below)
+    for o, keys in ((out, lambda t: ref.block_keys(int(c.pos[t]), P, range(K), 2, c.max_pages)),
+                    (out2, lambda t: list(range(int(c.pos[t]) + 1))), (out3, lambda t: list(range(int(c.pos[t]) + 1)))):
+        for t in range(0, T, 29):
+            for h in range(Hkv):
+                r, bound = c.rows(t, h, keys(t))
+                err = (o[t, h * G:(h + 1) * G].cpu().double() - r).abs()
+                rows = ~want[t, h * G:(h + 1) * G, 0]
+                assert bool((err <= bound)[rows].all()), (t, h)
