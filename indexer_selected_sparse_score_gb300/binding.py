@@ -75,6 +75,8 @@ class PagedArgs(ctypes.Structure):
     ]
 
 
+_BF16, _INT32 = torch.bfloat16, torch.int32
+
 EXPORTED = ("sa_workspace_size", "sa_workspace_init", "sa_indexer_scores", "sa_topk",
             "sa_candidate_blocks", "sa_candidate_words", "sa_topk_candidates", "sa_rotate_quant",
             "sa_compress_prefill", "sa_compress_decode", "sa_index_key_publish",
@@ -305,27 +307,55 @@ def sa_paged_workspace_size(pa: PagedArgs, K: int = 0, local: int = 0, shared_pa
     return int(load().sa_paged_workspace_size(ctypes.byref(pa), K, local, shared_pages))
 
 
-def _token_rows(name: str, x, heads: int, dim: int, T: int):
+def _token_rows(name: str, x, heads: int, dim: int, T: int, device: Optional[int] = None):
     """Pointer of [T, heads, dim] bf16 rows and the elements between consecutive
     tokens (0: dense, or a raw pointer); the heads of a token have to be dense."""
     if x is None or type(x) is int:
         return x, 0
-    stride = x.stride()
-    if x.element_size() != 2 or len(stride) != 3 or stride[2] != 1 or (stride[1] != dim and heads > 1):
+    stride, shape = x.stride(), x.shape
+    if (x.dtype is _BF16 and shape == (T, heads, dim) and T > 1 and stride[2] == 1 and stride[1] == dim and
+            stride[0] >= heads * dim and (device is None or x.get_device() == device)):
+        return x.data_ptr(), stride[0]
+    if x.dtype is not _BF16 or len(stride) != 3 or stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise SAError(SA_ERR_INVALID_ARG, f"{name} must be [T, heads, D] bf16 with dense heads")
+    if shape[0] < T or shape[1] < heads or shape[2] != dim:
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} is {list(shape)}: need {[T, heads, dim]}")
     if T > 1 and stride[0] < heads * dim:  # an expanded tensor; the library takes 0 as dense
         raise SAError(SA_ERR_INVALID_ARG, f"{name}'s tokens overlap")
+    if device is not None and x.get_device() != device:
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} is on another device than the workspace")
     return x.data_ptr(), stride[0] if T > 1 else 0
 
 
-def _dense(name: str, x, itemsize: int):
-    """Pointer of a tensor that the library takes as dense rows of ``itemsize``-byte
-    values (a raw pointer or None as it is)."""
+def _dense(name: str, x, dtype, rows: int, row: int, device: Optional[int] = None):
+    """Pointer of a tensor that the library takes as ``rows`` dense rows of ``row``
+    values (a raw pointer or None as it is); further rows may follow."""
     if x is None or type(x) is int:
         return x
-    if x.element_size() != itemsize or not x.is_contiguous():
-        raise SAError(SA_ERR_INVALID_ARG, f"{name} must be contiguous, of {itemsize}-byte values (got {x.dtype})")
+    if x.dtype is not dtype or not x.is_contiguous():
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} must be contiguous, of {dtype} (got {x.dtype})")
+    n = x.numel()
+    if n != rows * row and rows * row > 0 and (n < rows * row or (x.dim() > 1 and n != x.shape[0] * row)):
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} is {list(x.shape)}: need {rows} rows of {row} values")
+    if device is not None and x.get_device() != device:
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} is on another device than the workspace")
     return x.data_ptr()
+
+
+def _paged_ws(pa: PagedArgs, ws, stream):
+    """Workspace pointer and bytes, the device that the tensors of a paged call
+    have to be on (the workspace's, which is the current one), and the stream."""
+    if ws is None:
+        return None, 0, None, stream
+    device = ws.get_device()
+    if getattr(pa, "device", device) != device:
+        raise SAError(SA_ERR_INVALID_ARG, "the cache is on another device than the workspace")
+    if device >= 0:
+        if torch._C._cuda_getDevice() != device:
+            raise SAError(SA_ERR_INVALID_ARG, "the workspace is on another device than the current one")
+        if stream is None and _raw_stream is not None:
+            stream = _raw_stream(device)
+    return ws.data_ptr(), ws.nbytes, device, stream
 
 
 def sa_paged_append(pa: PagedArgs, k, v, ws, q=None, q_out=None, rope: Optional[RopeArgs] = None,
@@ -334,47 +364,79 @@ def sa_paged_append(pa: PagedArgs, k, v, ws, q=None, q_out=None, rope: Optional[
     ``q`` is rotated into ``q_out`` alongside, and ``k_mean`` gets the mean key of
     every page that fills.  k, v and q may be slices of a fused projection
     (their token strides are passed on)."""
-    T, D = pa.T, pa.D
-    kp, ks = _token_rows("k", k, pa.H_kv, D, T)
-    vp, vs = _token_rows("v", v, pa.H_kv, D, T)
-    qp, qs = _token_rows("q", q, pa.H, D, T)
-    p, n = _ws(ws)
-    _check(load().sa_paged_append(ctypes.byref(pa), kp, ks, vp, vs, qp, qs, _dense("q_out", q_out, 2),
+    T, D, n_kv = pa.T, pa.D, pa.H_kv
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    kp, ks = _token_rows("k", k, n_kv, D, T, dev)
+    vp, vs = _token_rows("v", v, n_kv, D, T, dev)
+    qp, qs = _token_rows("q", q, pa.H, D, T, dev)
+    _check(load().sa_paged_append(ctypes.byref(pa), kp, ks, vp, vs, qp, qs,
+                                  _dense("q_out", q_out, _BF16, T, pa.H * D, dev),
                                   ctypes.byref(rope) if rope is not None else None, int(halves),
-                                  _dense("k_mean", k_mean, 2), p, n, _s(stream)))
+                                  _dense("k_mean", k_mean, _BF16, pa.n_pages, n_kv * D, dev), p, n, _s(stream)))
 
 
 def sa_page_scores(pa: PagedArgs, q, k_mean, scores, ws, stream=None, ld=None) -> None:
     """Score of every complete page for every token and KV head ([T, H_kv, ld] fp32)."""
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    sp = scores
+    if isinstance(scores, torch.Tensor):
+        sp, ld = _score_rows(pa, scores, ld, dev)
+    elif ld is None:
+        ld = pa.max_pages
+    _check(load().sa_page_scores(ctypes.byref(pa), _dense("q", q, _BF16, pa.T, pa.H * pa.D, dev),
+                                 _dense("k_mean", k_mean, _BF16, pa.n_pages, pa.H_kv * pa.D, dev), sp, int(ld), p, n,
+                                 _s(stream)))
+
+
+def _score_rows(pa: PagedArgs, x, ld, device):
+    """Pointer and row stride of a score tensor: [T, H_kv, columns] or [T * H_kv,
+    columns] with evenly spaced rows, or one dimension of rows ``ld`` (max_pages)
+    apart."""
+    rows, dims, shape, stride = pa.T * pa.H_kv, x.dim(), x.shape, x.stride()
+    if x.dtype is not torch.float32 or (dims > 0 and stride[-1] != 1 and shape[-1] > 1):
+        raise SAError(SA_ERR_INVALID_ARG, "scores must be fp32 with dense rows")
     if ld is None:
-        ld = scores.stride(-2) if isinstance(scores, torch.Tensor) and scores.dim() == 3 else pa.max_pages
-    if isinstance(scores, torch.Tensor) and (scores.element_size() != 4 or (scores.dim() == 3 and (
-            scores.stride(2) != 1 or (scores.shape[0] > 1 and scores.stride(0) != scores.shape[1] * ld)))):
-        raise SAError(SA_ERR_INVALID_ARG, "scores must be [T, H_kv, ld] fp32 with evenly spaced rows")
-    p, n = _ws(ws)
-    _check(load().sa_page_scores(ctypes.byref(pa), _dense("q", q, 2), _dense("k_mean", k_mean, 2), _p(scores), int(ld), p,
-                               n, _s(stream)))
+        ld = pa.max_pages if rows <= 1 or dims not in (2, 3) else stride[0] if shape[1] == 1 or dims == 2 else stride[1]
+    if dims == 3:
+        ok = shape[0] >= pa.T and shape[1] == pa.H_kv and (shape[0] <= 1 or stride[0] == shape[1] * ld) and (
+            shape[1] <= 1 or stride[1] == ld)
+    elif dims == 2:
+        ok = shape[0] >= rows and (shape[0] <= 1 or stride[0] == ld)
+    else:
+        ok = dims == 1 and (rows == 0 or shape[0] >= (rows - 1) * ld + pa.max_pages)
+    if rows > 0 and not (ok and (dims == 1 or shape[-1] >= pa.max_pages)):
+        raise SAError(SA_ERR_INVALID_ARG, f"scores are {list(shape)} of strides {list(stride)}: need [T, H_kv, ld] with "
+                                          f"evenly spaced rows of at least {pa.max_pages}")
+    if device is not None and x.get_device() != device:
+        raise SAError(SA_ERR_INVALID_ARG, "scores are on another device than the workspace")
+    return x.data_ptr(), ld
 
 
 def sa_block_attn(pa: PagedArgs, q, idx, K: int, local: int, out, ws, stream=None) -> None:
     """Attention over the pages of ``idx`` ([T, H_kv, K] int32) and the ``local`` newest pages."""
-    p, n = _ws(ws)
-    _check(load().sa_block_attn(ctypes.byref(pa), _dense("q", q, 2), _dense("idx", idx, 4), K, local,
-                              _dense("out", out, 2), p, n, _s(stream)))
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    row = pa.H * pa.D
+    _check(load().sa_block_attn(ctypes.byref(pa), _dense("q", q, _BF16, pa.T, row, dev),
+                              _dense("idx", idx, _INT32, pa.T, pa.H_kv * K, dev), K, local,
+                              _dense("out", out, _BF16, pa.T, row, dev), p, n, _s(stream)))
 
 
 def sa_fused_block_attn(pa: PagedArgs, q, k_mean, K: int, local: int, idx_out, out, ws, stream=None) -> None:
     """Page scores, exact top-k and attention over the picks and the local pages."""
-    p, n = _ws(ws)
-    _check(load().sa_fused_block_attn(ctypes.byref(pa), _dense("q", q, 2), _dense("k_mean", k_mean, 2), K, local,
-                                    _dense("idx_out", idx_out, 4), _dense("out", out, 2), p, n, _s(stream)))
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    row = pa.H * pa.D
+    _check(load().sa_fused_block_attn(ctypes.byref(pa), _dense("q", q, _BF16, pa.T, row, dev),
+                                    _dense("k_mean", k_mean, _BF16, pa.n_pages, pa.H_kv * pa.D, dev), K, local,
+                                    _dense("idx_out", idx_out, _INT32, pa.T, pa.H_kv * K, dev),
+                                    _dense("out", out, _BF16, pa.T, row, dev), p, n, _s(stream)))
 
 
 def sa_prefix_attn(pa: PagedArgs, q, shared_pages: int, out, ws, stream=None) -> None:
     """Attention over whole sequences whose first ``shared_pages`` pages are the same."""
-    p, n = _ws(ws)
-    _check(load().sa_prefix_attn(ctypes.byref(pa), _dense("q", q, 2), shared_pages, _dense("out", out, 2), p, n,
-                               _s(stream)))
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    row = pa.H * pa.D
+    _check(load().sa_prefix_attn(ctypes.byref(pa), _dense("q", q, _BF16, pa.T, row, dev), shared_pages,
+                               _dense("out", out, _BF16, pa.T, row, dev), p, n, _s(stream)))
 
 
 def sa_check_device_status(ws, stream=None) -> int:
@@ -466,11 +528,22 @@ def paged_args(q_seq, q_pos, page_table, H: int, H_kv: int, D: int, P: int, n_pa
     B, max_pages = page_table.shape
     if B > 1 and page_table.stride(0) < max_pages:  # an expanded table; the library takes 0 as dense
         raise SAError(SA_ERR_INVALID_ARG, "page_table's rows overlap")
-    if q_pos.numel() != q_seq.numel() or page_table.element_size() != 4:
+    T = q_seq.numel()
+    if q_pos.numel() != T or page_table.dtype is not torch.int32:
         raise SAError(SA_ERR_INVALID_ARG, "need q_seq and q_pos of one length, and page_table of int32")
-    return PagedArgs(B, q_seq.numel(), H, H_kv, D, P, n_pages, max_pages, _dense("q_seq", q_seq, 4),
-                     _dense("q_pos", q_pos, 4), _p(page_table), page_table.stride(0) if B > 1 else 0,
-                     _dense("K", K, 2), _dense("V", V, 2), float(scale))
+    for name, x in (("K", K), ("V", V)):  # (with one KV head [n, P, 1, D] lies in memory as [n, 1, P, D] does)
+        if (type(x) is torch.Tensor and x.shape != (n_pages, H_kv, P, D) and x.dim() == 4 and H_kv > 1 and
+                x.shape[1:] != (H_kv, P, D)):
+            raise SAError(SA_ERR_INVALID_ARG, f"{name} is {list(x.shape)}: need {[n_pages, H_kv, P, D]}")
+    dev = q_seq.get_device()
+    if page_table.get_device() != dev:
+        raise SAError(SA_ERR_INVALID_ARG, "page_table is on another device than q_seq")
+    pa = PagedArgs(B, T, H, H_kv, D, P, n_pages, max_pages, _dense("q_seq", q_seq, _INT32, T, 1, dev),
+                   _dense("q_pos", q_pos, _INT32, T, 1, dev), _p(page_table), page_table.stride(0) if B > 1 else 0,
+                   _dense("K", K, _BF16, n_pages, H_kv * P * D, dev),
+                   _dense("V", V, _BF16, n_pages, H_kv * P * D, dev), float(scale))
+    pa.device = dev
+    return pa
 
 
 def new_paged_workspace(pa: PagedArgs, K: int = 0, local: int = 0, shared_pages: int = 0, device="cuda",

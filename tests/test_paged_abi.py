@@ -223,3 +223,94 @@ def test_lists_past_2_30_entries_are_refused(lib):
     assert _block(lib, _pa(), K=(1 << 30) + 1) == UNS
     assert _fused(lib, _pa(), K=(1 << 30) + 1) == UNS
     assert lib.sa_paged_workspace_size(_ref(_pa()), (1 << 30) + 1, 1, 0) == 0
+
+
+class _Elsewhere:
+    """A tensor that says it lies on another device."""
+
+    def __init__(self, x):
+        self._x = x
+
+    def __getattr__(self, name):
+        return getattr(self._x, name)
+
+    def get_device(self):
+        return self._x.get_device() + 1
+
+
+def test_types_and_sizes_the_library_would_misread_are_refused(lib):
+    # a tensor of the right width but another type, or smaller than the call
+    # reads or writes, never reaches the library
+    import torch
+    B, T, H, Hkv, D, P, n, K = 3, 4, 16, 2, 128, 64, 10, 4
+    i32, bf, f16 = dict(dtype=torch.int32), dict(dtype=torch.bfloat16), dict(dtype=torch.float16)
+    seq, table = torch.zeros(T, **i32), torch.zeros(B, 5, **i32)
+    cache = torch.zeros(n, Hkv, P, D, **bf)
+
+    def args(**kw):
+        a = dict(q_seq=seq, q_pos=seq, page_table=table, K=cache, V=cache)
+        a.update(kw)
+        return binding.paged_args(a["q_seq"], a["q_pos"], a["page_table"], H, Hkv, D, P, n, a["K"], a["V"], 1.0)
+
+    for kw in (dict(q_seq=seq.float()), dict(q_pos=seq.float()), dict(page_table=table.float()), dict(K=cache.half()),
+               dict(V=cache.half()), dict(K=cache[:-1]), dict(V=cache[:, :1].contiguous()),
+               dict(K=torch.zeros(n, P, Hkv, D, **bf)), dict(V=cache.view(-1)[:-8]), dict(K=_Elsewhere(cache)),
+               dict(page_table=_Elsewhere(table))):
+        with pytest.raises(binding.SAError):
+            args(**kw)
+    pa = args()
+    k, q, ws = torch.zeros(T, Hkv, D, **bf), torch.zeros(T, H, D, **bf), torch.zeros(1 << 16, dtype=torch.uint8)
+    mean, scores, idx = torch.zeros(n, Hkv, D, **bf), torch.zeros(T, Hkv, 8), torch.zeros(T, Hkv, K, **i32)
+    wide = torch.zeros(T, Hkv, K + 1, **i32)
+    bad_q = (q.half(), q[:-1], q[:, :-1].contiguous(), torch.zeros(T, H, 64, **bf), _Elsewhere(q))
+    calls = []
+    for x in (k.half(), k[:-1], k[:, :1], torch.zeros(T, Hkv, 64, **bf), _Elsewhere(k)):
+        calls += [lambda x=x: binding.sa_paged_append(pa, x, k, ws), lambda x=x: binding.sa_paged_append(pa, k, x, ws)]
+    for x in bad_q:
+        calls += [lambda x=x: binding.sa_paged_append(pa, k, k, ws, q=x, q_out=q),
+                  lambda x=x: binding.sa_paged_append(pa, k, k, ws, q=q, q_out=x),
+                  lambda x=x: binding.sa_page_scores(pa, x, mean, scores, ws),
+                  lambda x=x: binding.sa_block_attn(pa, x, idx, K, 1, q, ws),
+                  lambda x=x: binding.sa_block_attn(pa, q, idx, K, 1, x, ws),
+                  lambda x=x: binding.sa_fused_block_attn(pa, x, mean, K, 1, idx, q, ws),
+                  lambda x=x: binding.sa_fused_block_attn(pa, q, mean, K, 1, idx, x, ws),
+                  lambda x=x: binding.sa_prefix_attn(pa, x, 1, q, ws),
+                  lambda x=x: binding.sa_prefix_attn(pa, q, 1, x, ws)]
+    for x in (mean.half(), mean[:-1], mean[:, :1].contiguous(), _Elsewhere(mean)):
+        calls += [lambda x=x: binding.sa_paged_append(pa, k, k, ws, k_mean=x),
+                  lambda x=x: binding.sa_page_scores(pa, q, x, scores, ws),
+                  lambda x=x: binding.sa_fused_block_attn(pa, q, x, K, 1, idx, q, ws)]
+    for x in (idx.float(), idx[:-1], wide, idx[:, :, :-1].contiguous(), _Elsewhere(idx)):
+        calls += [lambda x=x: binding.sa_block_attn(pa, q, x, K, 1, q, ws),
+                  lambda x=x: binding.sa_fused_block_attn(pa, q, mean, K, 1, x, q, ws)]
+    for x in (scores.int(), scores[:-1], scores[:, :1].contiguous(), scores[..., :4], scores.view(T * Hkv, 8)[:-1],
+              scores.view(T * Hkv, 8)[:, :4], scores.view(-1)[:T * Hkv * 5 - 1], torch.zeros(T, Hkv, 8, 2)[..., 0],
+              scores.view(T * Hkv // 2, 16), scores.view(1, T * Hkv, 8)):
+        calls.append(lambda x=x: binding.sa_page_scores(pa, q, mean, x, ws))
+    calls.append(lambda: binding.sa_page_scores(pa, q, mean, scores, ws, ld=9))
+    calls.append(lambda: binding.sa_prefix_attn(pa, q, 1, q, _Elsewhere(ws)))
+    for i, call in enumerate(calls):
+        with pytest.raises(binding.SAError) as e:
+            call()
+        assert e.value.status == INV, i
+
+
+def test_layouts_the_library_reads_right_are_taken():
+    import torch
+    bf = dict(dtype=torch.bfloat16)
+    q = torch.zeros(6, 16, 128, **bf)
+    for x in (q, q.view(6, 16 * 128), q.view(-1), q.view(2, 3, 16, 128), q.view(96, 128)):
+        assert binding._dense("q", x, torch.bfloat16, 6, 16 * 128) == q.data_ptr()
+    for x in (q, q.view(6, 16 * 128), q.view(-1)):  # more tokens than the call's
+        assert binding._dense("q", x, torch.bfloat16, 4, 16 * 128) == q.data_ptr()
+    assert binding._dense("q", q, torch.bfloat16, 0, 16 * 128) == q.data_ptr()
+    assert binding._dense("q", None, torch.bfloat16, 4, 8) is None and binding._dense("q", 256, torch.bfloat16, 4, 8) == 256
+    assert binding._token_rows("k", q, 8, 128, 5) == (q.data_ptr(), 16 * 128)
+    pa = _pa(T=6, H=16, H_kv=2, max_pages=5)
+    s = torch.zeros(6, 2, 8)
+    for x, ld in ((s, 8), (s[..., :5], 8), (s.view(12, 8), 8), (s.view(12, 8)[:, :5], 8), (s.view(-1), 5),
+                  (torch.zeros(7, 2, 5), 5)):
+        assert binding._score_rows(pa, x, None, None) == (x.data_ptr(), ld)
+    one = _pa(T=6, H=16, H_kv=1, max_pages=5)
+    assert binding._score_rows(one, s[:, 1:], None, None) == (s[:, 1:].data_ptr(), 16)
+    assert binding._score_rows(pa, s.view(-1), 8, None) == (s.data_ptr(), 8)
