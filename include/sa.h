@@ -428,8 +428,9 @@ SA_API sa_status sa_paged_append(const sa_paged_args *pa, const void *k, int64_t
  * and -inf for n_vis(t) <= j < max_pages (and for a page id out of range).
  * q: [T, H, D] bf16 dense, rotated; k_mean as sa_paged_append keeps it;
  * scores: [T, H_kv, ld] fp32, columns 0 .. max_pages - 1 of every row written,
- * ld >= max_pages.  The queries' sum and the products are held in fp32 (of a
- * sum that is infinite the score is NaN).  Rows
+ * ld >= max_pages.  The queries' sum and the products are held in fp32 (a
+ * sum past bf16's range counts as infinite; infinite sums and means give the
+ * infinity or NaN that the formula gives).  Rows
  * of T * H_kv scores are what sa_topk selects from (r = P, one row per token
  * and KV head); sa_fused_block_attn does so.  K and V of pa are not read and
  * may be NULL. */

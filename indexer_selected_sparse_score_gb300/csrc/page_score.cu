@@ -4,7 +4,9 @@
 //
 // The score is an fp32 number, so the summed query enters the tensor cores as
 // three bf16 pieces (q = hi + mid + lo to 2^-24 of it) against the bf16 means:
-// products exact, sums fp32.  Two kernels.  With few tokens per sequence (a
+// products exact, sums fp32.  Of an infinite sum or mean the lower pieces make
+// NaN (0 x inf, inf - inf); there the upper pieces' product alone is the score.
+// Two kernels.  With few tokens per sequence (a
 // decode step) every mean key is met by one token: a stream of 2 D-byte rows
 // bound by HBM; there a warp-level product takes 16 pages' rows straight from
 // registers against the three pieces as columns (on the CUDA cores the unpacking
@@ -78,6 +80,24 @@ __device__ __forceinline__ void write_row_token(const ScoreParams &p, int64_t ro
   p.row_pos[row] = max(f * p.pv.P - 1, 0);
 }
 
+// Product of a summed query's upper piece with a mean key; the query's 16-byte
+// chunk c lies at q, or at its place in row `row` of a 128-byte-swizzled tile of
+// 64-dim blocks.
+template <int kDim, uint32_t kBlock = 0>
+__device__ float upper_product(const void *q, int row, const uint16_t *k) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < kDim / 8; ++c) {
+    const uint32_t off = kBlock ? (c >> 3) * kBlock + sw128_offset(row, 16u * (c & 7)) : 16u * c;
+    float x[8] = {}, y[8] = {};
+    add_bf16x8(x, *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(q) + off));
+    add_bf16x8(y, reinterpret_cast<const uint4 *>(k)[c]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+  }
+  return sum;
+}
+
 // ------------------------------------------------------- one token at a time
 
 constexpr int kThreads = 256;
@@ -109,10 +129,11 @@ score_token_kernel(const ScoreParams p, int S) {
   constexpr int kChunks = kDim / 8, kLoads = kChunks / 4;  // of a row; a lane's loads of it
   __shared__ __align__(16) uint16_t qs[kHeads][3][kDim];
   __shared__ __align__(16) float tile[kHeads][16 * kPass];
-  __shared__ int page_s[16 * kPass];
+  __shared__ int page_s[16 * kPass], odd_s;  // odd_s: a score is NaN
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t = blockIdx.x / S, share = blockIdx.x - t * S;
   const int h0 = blockIdx.z * kHeads, nh = min(kHeads, p.pv.H_kv - h0), G = p.pv.H / p.pv.H_kv;
+  if (tid == 0) odd_s = 0;
   // The queries' loads do not wait for the token's position.  A thread sums a
   // chunk over every parts-th query; `tile` joins the parts.
   const int sums = nh * kChunks;
@@ -154,7 +175,8 @@ score_token_kernel(const ScoreParams p, int S) {
   if (!ok) return;
   const int vis = (pos + 1) >> p.pv.logP, n = (vis + 15) >> 4;
   const int last = static_cast<int>(static_cast<int64_t>(n) * (share + 1) / S);
-  int a = static_cast<int>(static_cast<int64_t>(n) * share / S);
+  const int begin = static_cast<int>(static_cast<int64_t>(n) * share / S);
+  int a = begin;
   auto page_at = [&](int first) -> int {  // of this thread's page of the pass from tile `first`
     const int j = 16 * first + tid;
     return j < min(16 * min(first + kPass, last), vis) ? load_page(p.pv, b, j, p.status, blockIdx.z == 0) : -1;
@@ -201,8 +223,10 @@ score_token_kernel(const ScoreParams p, int S) {
       // columns 0 and 1 sit in lane 4 g, column 2 in lane 4 g + 1
       const float e0 = __shfl_down_sync(0xffffffffu, d[0], 1), e1 = __shfl_down_sync(0xffffffffu, d[2], 1);
       if (ti == 0) {
-        tile[h][16 * jt + g] = bad[0] ? -INFINITY : (d[0] + (d[1] + e0)) * p.scale;
-        tile[h][16 * jt + g + 8] = bad[1] ? -INFINITY : (d[2] + (d[3] + e1)) * p.scale;
+        const float s0 = (d[0] + (d[1] + e0)) * p.scale, s1 = (d[2] + (d[3] + e1)) * p.scale;
+        tile[h][16 * jt + g] = bad[0] ? -INFINITY : s0;
+        tile[h][16 * jt + g + 8] = bad[1] ? -INFINITY : s1;
+        if (s0 != s0 || s1 != s1) odd_s = 1;
       }
     }
     __syncthreads();
@@ -211,6 +235,19 @@ score_token_kernel(const ScoreParams p, int S) {
       for (int j = lane; j < nj; j += 32) row[j] = tile[h][j];
     }
     __syncthreads();  // the next pass writes tile
+  }
+  if (!odd_s) return;
+  // NaN among the scores: an infinity in a sum or mean, perhaps, whose score is
+  // the upper piece's product
+  for (int h = warp; h < nh; h += kThreads / 32) {
+    float *row = p.scores + (static_cast<int64_t>(t) * p.pv.H_kv + h0 + h) * p.ld;
+    // (the columns of the passes above, by the same threads)
+    for (int j = 16 * begin + lane; j < min(16 * last, vis); j += 32) {
+      if (row[j] == row[j]) continue;
+      const int id = load_page(p.pv, b, j, nullptr, false);
+      const uint16_t *k = p.k_mean + (static_cast<int64_t>(max(id, 0)) * p.pv.H_kv + h0 + h) * kDim;
+      row[j] = p.scale * upper_product<kDim>(qs[h][0], 0, k);
+    }
   }
 }
 
@@ -234,6 +271,11 @@ struct ScoreSmem {
   static constexpr size_t total = misc + 32;
   static_assert(total + 1024 <= 232448, "shared memory budget");
 };
+
+template <int kDim>
+__device__ __noinline__ float upper_product_of_tile(const uint8_t *qs, int row, const uint16_t *k) {
+  return upper_product<kDim, ScoreSmem<kDim>::kBlock>(qs, row, k);
+}
 
 // CTA (x, h): tokens 128 x .. 128 x + 127, KV head h, every page.  Per
 // sequence among the tokens: blocks of 128 pages, two in flight, the next
@@ -421,6 +463,20 @@ score_tile_kernel(const ScoreParams p) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!((cols >> e) & 1u)) v[e] = -INFINITY;
+        }
+        // NaN: an infinity among the sums or means, perhaps (the three pieces'
+        // products share the accumulator)
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) odd |= v[e] != v[e];
+        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int id = __shfl_sync(0xffffffffu, pg, e);
+            if (v[e] != v[e])  // (a masked column is -inf here: the page exists)
+              v[e] = p.scale * upper_product_of_tile<kDim>(
+                                   qs, row, p.k_mean + (static_cast<int64_t>(id) * p.pv.H_kv + h) * kDim);
+          }
         }
         landed();  // block i + 1 is in; buffer bf (keys, page ids, accumulator) is free
         if (i + 2 < used) gather(i + 2);

@@ -912,3 +912,46 @@ def test_nan_stays_in_the_rows_it_belongs_to(T, D, P, Hkv, G, K, shared):
                 err = (o[t, h * G:(h + 1) * G].cpu().double() - r).abs()
                 rows = ~want[t, h * G:(h + 1) * G, 0]
                 assert bool((err <= bound)[rows].all()), (t, h)
+
+
+# --------------------------------------------------------------- infinities ---
+
+@pytest.mark.parametrize("D,P,Hkv,G,lens,new", [
+    (128, 64, 8, 1, [16384], 1300), (64, 16, 4, 4, [4001, 2500], 600), (128, 16, 8, 2, [5001], 700),  # chunks
+    (128, 64, 8, 8, [4000, 700, 64, 2222], 1), (64, 16, 2, 3, [777, 300], 2), (128, 32, 1, 64, [3000], 1),
+])
+def test_scores_of_infinite_means_and_sums(D, P, Hkv, G, lens, new):
+    c = Case(52, lens, D, P, Hkv, G)
+    at = [(b, p) for b, n in enumerate(lens) for p in range(max(n - new, 0), n)]
+    c.tokens([b for b, _ in at], [p for _, p in at])
+    mean = (torch.randn(c.total, Hkv, D, generator=c.g) / 8).bfloat16()
+    r = np.random.RandomState(7)
+    for b, n in enumerate(lens):
+        for j in range(0, n // P, 3):  # one infinite value of a mean, and two (the score may be NaN)
+            mean[int(c.table[b, j]), r.randint(Hkv), r.randint(D)] = float("inf") * (1 if j % 2 else -1)
+            if j % 4 == 0:
+                mean[int(c.table[b, j]), r.randint(Hkv), r.randint(D)] = float("inf")
+    # the last token's queries of the last KV head: one value infinite
+    c.q[-1, -1, 5] = float("-inf")
+    mean[:, :, 5] = mean[:, :, 5] + 0.01
+    c.upload()
+    scores = torch.full((c.T, Hkv, c.max_pages), 9.0, device=DEV)
+    ws = sb.new_paged_workspace(c.pa)
+    sb.sa_page_scores(c.pa, c.d["q"], mean.to(DEV), scores, ws)
+    status_ok(ws)
+    got, q, kinds = scores.cpu().double(), c.q.double().view(c.T, Hkv, G, D), [0, 0, 0]
+    for b, n in enumerate(lens):
+        tok = [t for t in range(c.T) if int(c.seq[t]) == b]
+        k = mean[c.table[b, :n // P].long()].double().transpose(0, 1)
+        s = torch.einsum("thd,hjd->thj", q[tok].sum(2), k) * c.scale
+        # as check_scores: G sums and D products in fp32
+        bound = torch.einsum("thd,hjd->thj", q[tok].abs().sum(2), k.abs()) * c.scale * (G + D + 4) * 2.0 ** -23
+        live = (torch.arange(n // P)[None] < ((c.pos[tok] + 1) // P)[:, None])[:, None].expand(-1, Hkv, -1)
+        row = got[tok][..., :n // P]
+        nan, inf = torch.isnan(s), torch.isinf(s)
+        assert torch.equal(torch.isnan(row)[live], nan[live])
+        assert torch.equal(row[live & inf], s[live & inf])
+        fine = live & ~nan & ~inf
+        assert bool(((row - s).abs() <= bound)[fine].all())
+        kinds = [x + int(y[live].sum()) for x, y in zip(kinds, (nan, inf, fine))]
+    assert kinds[1] > 0 and (kinds[2] > 0 or c.T * Hkv == 1)
