@@ -532,7 +532,7 @@ def paged_args(q_seq, q_pos, page_table, H: int, H_kv: int, D: int, P: int, n_pa
     if q_pos.numel() != T or page_table.dtype is not torch.int32:
         raise SAError(SA_ERR_INVALID_ARG, "need q_seq and q_pos of one length, and page_table of int32")
     for name, x in (("K", K), ("V", V)):  # (with one KV head [n, P, 1, D] lies in memory as [n, 1, P, D] does)
-        if (type(x) is torch.Tensor and x.shape != (n_pages, H_kv, P, D) and x.dim() == 4 and H_kv > 1 and
+        if (x is not None and type(x) is not int and x.shape != (n_pages, H_kv, P, D) and x.dim() == 4 and H_kv > 1 and
                 x.shape[1:] != (H_kv, P, D)):
             raise SAError(SA_ERR_INVALID_ARG, f"{name} is {list(x.shape)}: need {[n_pages, H_kv, P, D]}")
     dev = q_seq.get_device()
