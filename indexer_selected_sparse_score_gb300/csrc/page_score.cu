@@ -16,12 +16,12 @@
 // the scores.
 //
 // Measured, heads of 128, pages of 64: 64 tokens (64 over 8 heads) at 32 K to
-// 64 K positions 24 us, 4.2 TB/s of the 104 MB it must move (5.7 TB/s once
+// 64 K positions 23.8 us, 4.4 TB/s of the 104 MB it must move (5.7 TB/s once
 // started: two chains of loads pass before the first mean keys arrive); a
-// 4096-token chunk (64 over 4 heads) at 28 K positions 34 us, 3.0 TB/s (the
+// 4096-token chunk (64 over 4 heads) at 28 K positions 33 us, 3.1 TB/s (the
 // queries' 67 MB on the 128 SMs that have a tile, then the scores, little of the
-// two overlapping); 4 tokens (16 over 2 heads) at 4 K positions 6 us, one launch
-// and its chain of loads.
+// two overlapping); 4 tokens (16 over 2 heads) at 4 K positions 6.4 to 7.3 us
+// called from Python, one launch and its chain of loads.
 #include <algorithm>
 
 #include "internal.h"

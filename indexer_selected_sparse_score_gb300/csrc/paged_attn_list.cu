@@ -38,11 +38,13 @@
 // drains its copies and products and returns.
 //
 // Measured, heads of 128: 64 tokens of 64 heads over one KV head, 34 pages of 64
-// each: 27 us, 2.7 TB/s of the 72 MB it must read (about 3 us to the first tile,
-// 8.5 tiles of 64 KB on each SM, 1.2 us each at HBM's rate, and 5 us of merge with
-// its launch).  966 tokens of 32 over 4 heads, 13 pages of 128 each: 203 us; the
-// lists differ from token to token, so 3.4 GB pass from L2 to the SMs at 16 TB/s
-// (about 60 bytes a clock and SM), which bounds it.  One token of 16 over 2
+// each: 27 us, 2.7 TB/s of the 72 MB it must read, by two CTAs to a unit, so on
+// 128 of the SMs (about 3 us to the first tile, 8.5 tiles of 64 KB, 1.25 us each at
+// HBM's rate, and 5 us of merge with its launch: 19 us; the rest are waits that no
+// measurement has placed).  966 tokens of 32 over 4 heads, 13
+// pages of 128 each: 205 us; a page is copied once for every token that lists it,
+// so 3.4 GB pass from L2 to the SMs at 16 TB/s (about 60 bytes a clock and SM),
+// which bounds work cut by tokens as it is here (cut by pages it would move less).  One token of 16 over 2
 // heads, 34 pages of 64: 12 us, two launches and their chains of loads.  Units
 // of a tile or two cost about 2 us each and CTA, half of it the walk of the
 // list, half the chain of a tile: 306 tokens of 64 over 8 heads at the start of

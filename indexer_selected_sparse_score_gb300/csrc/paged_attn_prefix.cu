@@ -25,10 +25,10 @@
 // merges a row's pieces of both.
 //
 // Measured, heads of 128: 128 tokens of 64 heads over one KV head behind 32 K
-// shared keys 120 us, 1.16 PFLOP/s over the whole call (the shared product runs
+// shared keys 116 us, 1.20 PFLOP/s over the whole call (the shared product runs
 // at about 1.5 on the 128 SMs it gets; the own pages' list and the merge, 5 us,
 // are the rest).  64 tokens of 64 over 8 heads, 32 K shared and up to 1500 own
-// keys: 87 us, 4.1 TB/s of the 360 MB it must read beside 0.8 PFLOP/s.  4 tokens
+// keys: 86 us, 4.2 TB/s of the 360 MB it must read beside 0.8 PFLOP/s.  4 tokens
 // of 16 over 2 heads, 4160 shared keys: 14 us, three launches.
 #include <cudaTypedefs.h>
 
@@ -590,7 +590,11 @@ cudaError_t launch_prefix_attn(const sa_paged_args &pa, const void *q, int share
   // part keeps the tensor cores busy: it gets SMs of its own, by the two parts'
   // costs: about 1.4 us a tile of 256 rows, and 1 us a unit and 0.75 a list tile
   // (with many heads 1.5 and 1.5), the own pages taken as half the table's.  What
-  // it has left is shared out as the shared part's CTAs leave.
+  // it has left is shared out as the shared part's CTAs leave.  (The host does not
+  // know the sequences' lengths, so a table much wider than they are takes SMs from
+  // the shared product: 128 tokens of 64 heads behind 256 pages of 128 with 4 own
+  // pages 120 us, in a table of twice the width 210; 64 of 64 over 8 behind 512
+  // pages of 64 with 11 own pages 89 and 108.)
   const int sms = std::min(sm_count(), kMaxCtas);
   const bool few = list_cols(pa) == 16;
   const double shared_us = 1.4 * static_cast<double>(s.items) * s.nkt;
