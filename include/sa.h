@@ -127,7 +127,8 @@ typedef struct {
  * the arguments are invalid. */
 SA_API size_t sa_workspace_size(const sa_index_args *ia, const sa_attn_args *aa, int32_t K);
 
-/* Zero-fills the workspace header (the sticky device status word).  Call it
+/* Zero-fills the workspace's first 4096 bytes (all of it when it is smaller),
+ * which hold the sticky device status word and the calls' counters.  Call it
  * once on a new workspace.  Enqueued on `stream`. */
 SA_API sa_status sa_workspace_init(void *ws, size_t ws_bytes, sa_stream_t stream);
 
@@ -471,6 +472,102 @@ SA_API sa_status sa_fused_block_attn(const sa_paged_args *pa, const void *q, con
  * cache.  q, out and precision as for sa_block_attn. */
 SA_API sa_status sa_prefix_attn(const sa_paged_args *pa, const void *q, int32_t shared_pages, void *out, void *ws,
                                 size_t ws_bytes, sa_stream_t stream);
+
+/* ------------------------------------------------------- a small paged cache
+ *
+ * The paged cache held in 4 bits: a row of D values is D / 2 bytes of e2m1 codes
+ * (value 2i in the low half of byte i; codes 0 .. 7 are 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6, bit 3 the sign) and D / 16 bytes of e4m3 scales, one for 16 values
+ * ("DeepSeek-V4.1-Flash-NVFP4 inference/model.py", fp4_act_quant of the
+ * compressed KV: e2m1 blocks of 16 with e4m3 scales):
+ *   value = gain * e4m3(scale) * e2m1(code)
+ * p.K, p.V: [n_pages, H_kv, P, D / 2] bytes; K_scale, V_scale: [n_pages, H_kv, P,
+ * D / 16] bytes; everything else as in sa_paged_args, whose rules on skipped
+ * tokens and pages hold for the calls below.  A position of a page is a slot
+ * here: q_pos[t] is token t's slot, and a token attends the slots 0 .. q_pos[t].
+ * The position that a key is rotated at may be another (rope_pos below), so that
+ * a sequence whose slots have been freed goes on where its slots end. */
+typedef struct {
+  sa_paged_args p;
+  void *K_scale, *V_scale; /* 16-byte aligned */
+  float k_gain, v_gain;    /* factors of all keys and all values: powers of two in [2^-60, 2^60] */
+} sa_paged4_args;
+
+/* What is kept of every slot for an eviction: weight[b, h, j], the attention
+ * weight that slot j of sequence b and KV head h has gathered, and born[b, h, j],
+ * the position of the token in it.  [B, H_kv, ld], ld >= max_pages * P. */
+
+/* Bytes of workspace of the calls below for these shapes (0 when the arguments
+ * are invalid).  As for sa_paged_workspace_size, initialise it with
+ * sa_workspace_init, again after a call that returned SA_ERR_CUDA or a status of
+ * SA_ERR_TIMEOUT; calls and graphs that may run at once need one each. */
+SA_API size_t sa_paged4_workspace_size(const sa_paged4_args *pa);
+
+/* Appends new keys and values.  For token t in slot q_pos[t], every KV head:
+ *   y = bf16( R(r) k[t, h] ), z = y / k_gain;  and z = v[t, h] / v_gain
+ * with R as in sa_paged_append (rope->dim a multiple of 32) at r = rope_pos[t]
+ * ([T] int32, any value; NULL for q_pos[t]); then for every 16 values
+ *   scale = e4m3( max(max |z| / 6, 2^-9) ), codes = e2m1( z / scale ),
+ * both to the nearest, ties to even, saturating at 448 and 6, the quotients
+ * exact.  A NaN among the 16 makes the scale NaN (and so all of them).  q, q_out,
+ * the strides and a slot given twice as for sa_paged_append.  With weight and
+ * born ([B, H_kv, ld], both or neither) the slot's record begins for every KV
+ * head: weight 0, born r. */
+SA_API sa_status sa_paged4_append(const sa_paged4_args *pa, const void *k, int64_t k_stride, const void *v,
+                                  int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                  const sa_rope_args *rope, int32_t rope_halves, const int32_t *rope_pos, float *weight,
+                                  int32_t *born, int64_t ld, void *ws, size_t ws_bytes, sa_stream_t stream);
+
+/* The rows of given slots as bf16: k_out[t, h], v_out[t, h] ([T, H_kv, D] dense;
+ * either may be NULL) of slot q_pos[t] of sequence q_seq[t] -- to hand a sequence
+ * to a cache of another format, or to see what the cache holds.  A skipped token
+ * leaves its rows as they were.  Values are exact (six significant bits). */
+SA_API sa_status sa_paged4_read(const sa_paged4_args *pa, void *k_out, void *v_out, void *ws, size_t ws_bytes,
+                                sa_stream_t stream);
+
+/* Attention over whole sequences:
+ *   out[t, h'] = sum_j softmax(scale q[t, h'] . K_j) V_j,  0 <= j <= q_pos[t]
+ *   lse[t, h'] = log sum_j exp(scale q[t, h'] . K_j)
+ * out: [T, H, D] bf16 dense; lse: [T, H] fp32 or NULL.  A row without keys (all
+ * of its pages out of range) has out 0 and lse -inf.  Serves one token per
+ * sequence, a few drafted ones and chunks of prompts; a sequence's tokens share
+ * its keys where they follow one another in the call.  Keys and values enter
+ * their products exactly, as fp16; queries as fp16 scaled by a power of two per
+ * row (exact but for values 2^-29 of the row's largest); the weights are rounded
+ * to fp16 (2^-11 of each at most); logits, statistics and sums are fp32. */
+SA_API sa_status sa_paged4_attn(const sa_paged4_args *pa, const void *q, void *out, float *lse, void *ws,
+                                size_t ws_bytes, sa_stream_t stream);
+
+/* Attention weights into the slots' records: for every sequence b of the call,
+ * KV head h and slot j
+ *   weight[b, h, j] += sum over b's tokens t with j <= q_pos[t] and the heads h' of h of
+ *                      exp(scale q[t, h'] . K_j - lse[t, h'])
+ * lse: [T, H] fp32, as sa_paged4_attn leaves it (a row whose lse is -inf adds
+ * nothing).  Values of V are not read.  Sums are fp32, in one order if the tokens
+ * of each sequence follow one another in the call; a sequence that comes in
+ * several places adds them in any order. */
+SA_API sa_status sa_paged4_weights(const sa_paged4_args *pa, const void *q, const float *lse, float *weight, int64_t ld,
+                                   void *ws, size_t ws_bytes, sa_stream_t stream);
+
+/* Frees slots by what they have gathered.  Sequence b holds length[b] slots, its
+ * newest token has position newest[b].  For every KV head by itself: the slots
+ * with born > newest[b] - recent stay, and of the others those of the largest
+ * weight, min(budget, length[b]) slots in all (ties to the lower slot; if more
+ * than budget are recent, the lowest of those; NaN counts as the largest).  The
+ * slots that stay and lie before the new end keep their place; the i-th freed
+ * slot before it takes the row of the i-th staying slot behind it, in the pages
+ * of K, V and their scales.  weight_out and born_out get the records of the new
+ * order, slots 0 .. min(budget, length[b]) - 1 (others are left as they were);
+ * they may not overlap weight and born.  length_out[b] = min(budget, length[b]).
+ * The pages of a sequence that loses slots belong to it alone.  length, newest,
+ * length_out: [B] int32 (length_out may not be length).  q_seq, q_pos and T of
+ * pa are not read.  A length outside [0, max_pages * P] is flagged, and taken as
+ * 0; a row whose page is out of range does not move.  budget >= 1, 0 <= recent <=
+ * budget. */
+SA_API sa_status sa_paged4_evict(const sa_paged4_args *pa, const int32_t *length, const int32_t *newest, int32_t budget,
+                                 int32_t recent, const float *weight, const int32_t *born, float *weight_out,
+                                 int32_t *born_out, int64_t ld, int32_t *length_out, void *ws, size_t ws_bytes,
+                                 sa_stream_t stream);
 
 /* Synchronises `stream`, then reads and clears the workspace's sticky device
  * status: SA_OK, SA_ERR_DEVICE_DATA (out-of-range device data was skipped)

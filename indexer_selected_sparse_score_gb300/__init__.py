@@ -10,13 +10,16 @@ from .binding import (  # noqa: F401
     AttnArgs,
     DeviceProblem,
     IndexArgs,
+    Paged4Args,
     PagedArgs,
     RopeArgs,
     SAError,
     SA_BF16,
     SA_FP8_E4M3,
+    new_paged4_workspace,
     new_paged_workspace,
     new_workspace,
+    paged4_args,
     paged_args,
     sa_block_attn,
     sa_check_device_status,
@@ -24,6 +27,12 @@ from .binding import (  # noqa: F401
     sa_fused_decode,
     sa_indexer_scores,
     sa_page_scores,
+    sa_paged4_append,
+    sa_paged4_attn,
+    sa_paged4_evict,
+    sa_paged4_read,
+    sa_paged4_weights,
+    sa_paged4_workspace_size,
     sa_paged_append,
     sa_paged_workspace_size,
     sa_prefix_attn,

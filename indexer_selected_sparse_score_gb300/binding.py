@@ -75,7 +75,14 @@ class PagedArgs(ctypes.Structure):
     ]
 
 
-_BF16, _INT32 = torch.bfloat16, torch.int32
+class Paged4Args(ctypes.Structure):
+    _fields_ = [
+        ("p", PagedArgs), ("K_scale", ctypes.c_void_p), ("V_scale", ctypes.c_void_p),
+        ("k_gain", ctypes.c_float), ("v_gain", ctypes.c_float),
+    ]
+
+
+_BF16, _INT32, _FP32, _UINT8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
 EXPORTED = ("sa_workspace_size", "sa_workspace_init", "sa_indexer_scores", "sa_topk",
             "sa_candidate_blocks", "sa_candidate_words", "sa_topk_candidates", "sa_rotate_quant",
@@ -84,7 +91,8 @@ EXPORTED = ("sa_workspace_size", "sa_workspace_init", "sa_indexer_scores", "sa_t
             "sa_fused_decode_launch_count", "sa_check_device_status", "sa_status_string",
             "sa_last_error_detail", "sa_fused_decode_noalloc", "sa_noalloc_scratch_bytes", "sa_set_wait_budget",
             "sa_paged_workspace_size", "sa_paged_append", "sa_page_scores", "sa_block_attn", "sa_fused_block_attn",
-            "sa_prefix_attn")
+            "sa_prefix_attn", "sa_paged4_workspace_size", "sa_paged4_append", "sa_paged4_read", "sa_paged4_attn",
+            "sa_paged4_weights", "sa_paged4_evict")
 
 _LIB = None
 
@@ -132,6 +140,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.sa_block_attn.argtypes = [PA, vp, vp, i32, i32, vp, vp, sz, vp]
     lib.sa_fused_block_attn.argtypes = [PA, vp, vp, i32, i32, vp, vp, vp, sz, vp]
     lib.sa_prefix_attn.argtypes = [PA, vp, i32, vp, vp, sz, vp]
+    P4 = ctypes.POINTER(Paged4Args)
+    lib.sa_paged4_workspace_size.argtypes = [P4]
+    lib.sa_paged4_workspace_size.restype = sz
+    lib.sa_paged4_append.argtypes = [P4, vp, i64, vp, i64, vp, i64, vp, ctypes.POINTER(RopeArgs), i32, vp, vp, vp, i64,
+                                     vp, sz, vp]
+    lib.sa_paged4_read.argtypes = [P4, vp, vp, vp, sz, vp]
+    lib.sa_paged4_attn.argtypes = [P4, vp, vp, vp, vp, sz, vp]
+    lib.sa_paged4_weights.argtypes = [P4, vp, vp, vp, i64, vp, sz, vp]
+    lib.sa_paged4_evict.argtypes = [P4, vp, vp, i32, i32, vp, vp, vp, vp, i64, vp, vp, sz, vp]
     lib.sa_check_device_status.argtypes = [vp, vp]
     lib.sa_set_wait_budget.argtypes = [i64]
     lib.sa_set_wait_budget.restype = i32
@@ -142,7 +159,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                  "sa_topk_candidates", "sa_rotate_quant", "sa_compress_prefill", "sa_compress_decode",
                  "sa_index_key_publish", "sa_sparse_attn",
                  "sa_fused_decode", "sa_fused_decode_staged", "sa_check_device_status", "sa_paged_append",
-                 "sa_page_scores", "sa_block_attn", "sa_fused_block_attn", "sa_prefix_attn"):
+                 "sa_page_scores", "sa_block_attn", "sa_fused_block_attn", "sa_prefix_attn", "sa_paged4_append",
+                 "sa_paged4_read", "sa_paged4_attn", "sa_paged4_weights", "sa_paged4_evict"):
         getattr(lib, name).restype = i32
     if path == LIB:
         _LIB = lib
@@ -439,6 +457,84 @@ def sa_prefix_attn(pa: PagedArgs, q, shared_pages: int, out, ws, stream=None) ->
                                _dense("out", out, _BF16, pa.T, row, dev), p, n, _s(stream)))
 
 
+def sa_paged4_workspace_size(pa: Paged4Args) -> int:
+    return int(load().sa_paged4_workspace_size(ctypes.byref(pa)))
+
+
+def _records(pa: Paged4Args, name: str, x, dtype, device: Optional[int] = None):
+    """Pointer and row stride of the slots' records ([B, H_kv, ld], dense; a raw
+    pointer is taken as rows of max_pages * P)."""
+    if x is None or type(x) is int:
+        return x, pa.p.max_pages * pa.p.P
+    if x.dim() != 3 or x.shape[0] != pa.p.B or x.shape[1] != pa.p.H_kv:
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} is {list(x.shape)}: need {[pa.p.B, pa.p.H_kv]} rows")
+    ld = x.shape[2]
+    return _dense(name, x, dtype, pa.p.B * pa.p.H_kv, ld, device), ld
+
+
+def sa_paged4_append(pa: Paged4Args, k, v, ws, q=None, q_out=None, rope: Optional[RopeArgs] = None,
+                     halves: bool = False, rope_pos=None, weight=None, born=None, stream=None) -> None:
+    """New keys and values into a 4-bit cache: rotated (at ``rope_pos``, the slot's
+    number unless given) and quantised; ``q`` is rotated into ``q_out`` alongside,
+    and ``weight`` and ``born`` ([B, H_kv, ld]) get the slots' fresh records."""
+    a = pa.p
+    T, D, n_kv = a.T, a.D, a.H_kv
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    kp, ks = _token_rows("k", k, n_kv, D, T, dev)
+    vp, vs = _token_rows("v", v, n_kv, D, T, dev)
+    qp, qs = _token_rows("q", q, a.H, D, T, dev)
+    wp, ld = _records(pa, "weight", weight, _FP32, dev)
+    bp, bld = _records(pa, "born", born, _INT32, dev)
+    if ld != bld and weight is not None and born is not None:
+        raise SAError(SA_ERR_INVALID_ARG, "weight and born differ in their rows")
+    _check(load().sa_paged4_append(ctypes.byref(pa), kp, ks, vp, vs, qp, qs,
+                                   _dense("q_out", q_out, _BF16, T, a.H * D, dev),
+                                   ctypes.byref(rope) if rope is not None else None, int(halves),
+                                   _dense("rope_pos", rope_pos, _INT32, T, 1, dev), wp, bp, ld, p, n, _s(stream)))
+
+
+def sa_paged4_read(pa: Paged4Args, k_out, v_out, ws, stream=None) -> None:
+    """The rows of the tokens' slots as bf16 ([T, H_kv, D]; either may be None)."""
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    row = pa.p.H_kv * pa.p.D
+    _check(load().sa_paged4_read(ctypes.byref(pa), _dense("k_out", k_out, _BF16, pa.p.T, row, dev),
+                                 _dense("v_out", v_out, _BF16, pa.p.T, row, dev), p, n, _s(stream)))
+
+
+def sa_paged4_attn(pa: Paged4Args, q, out, ws, lse=None, stream=None) -> None:
+    """Attention over whole sequences of a 4-bit cache; ``lse`` ([T, H] fp32) gets
+    the logarithm of every row's sum of exponentials."""
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    T, row = pa.p.T, pa.p.H * pa.p.D
+    _check(load().sa_paged4_attn(ctypes.byref(pa), _dense("q", q, _BF16, T, row, dev),
+                                 _dense("out", out, _BF16, T, row, dev), _dense("lse", lse, _FP32, T, pa.p.H, dev), p, n,
+                                 _s(stream)))
+
+
+def sa_paged4_weights(pa: Paged4Args, q, lse, weight, ws, stream=None) -> None:
+    """Adds the tokens' attention weights to the slots' records ([B, H_kv, ld] fp32)."""
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    wp, ld = _records(pa, "weight", weight, _FP32, dev)
+    _check(load().sa_paged4_weights(ctypes.byref(pa), _dense("q", q, _BF16, pa.p.T, pa.p.H * pa.p.D, dev),
+                                    _dense("lse", lse, _FP32, pa.p.T, pa.p.H, dev), wp, ld, p, n, _s(stream)))
+
+
+def sa_paged4_evict(pa: Paged4Args, length, newest, budget: int, recent: int, weight, born, weight_out, born_out,
+                    length_out, ws, stream=None) -> None:
+    """Cuts every sequence to ``budget`` slots per KV head: the ``recent`` newest
+    stay and the heaviest of the others; freed slots take rows from behind."""
+    p, n, dev, stream = _paged_ws(pa, ws, stream)
+    recs = [_records(pa, name, x, dt, dev) for name, x, dt in (
+        ("weight", weight, _FP32), ("born", born, _INT32), ("weight_out", weight_out, _FP32),
+        ("born_out", born_out, _INT32))]
+    if len({ld for _, ld in recs}) != 1:
+        raise SAError(SA_ERR_INVALID_ARG, "the records differ in their rows")
+    lens = [_dense(name, x, _INT32, pa.p.B, 1, dev) for name, x in (
+        ("length", length), ("newest", newest), ("length_out", length_out))]
+    _check(load().sa_paged4_evict(ctypes.byref(pa), lens[0], lens[1], budget, recent, recs[0][0], recs[1][0], recs[2][0],
+                                  recs[3][0], recs[0][1], lens[2], p, n, _s(stream)))
+
+
 def sa_check_device_status(ws, stream=None) -> int:
     """Synchronise, read and clear the sticky device status; returns the sa status."""
     return int(load().sa_check_device_status(_p(ws), _s(stream)))
@@ -549,6 +645,35 @@ def paged_args(q_seq, q_pos, page_table, H: int, H_kv: int, D: int, P: int, n_pa
 def new_paged_workspace(pa: PagedArgs, K: int = 0, local: int = 0, shared_pages: int = 0, device="cuda",
                         stream=None) -> torch.Tensor:
     n = sa_paged_workspace_size(pa, K, local, shared_pages)
+    if n == 0:
+        raise SAError(SA_ERR_INVALID_ARG, "workspace size query rejected the arguments")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    sa_workspace_init(ws, stream)
+    return ws
+
+
+def paged4_args(q_seq, q_pos, page_table, H: int, H_kv: int, D: int, P: int, n_pages: int, K, V, K_scale, V_scale,
+                scale: float, k_gain: float = 1.0, v_gain: float = 1.0) -> Paged4Args:
+    """Argument struct of the 4-bit paged calls (the caller keeps the tensors
+    alive): K and V [n_pages, H_kv, P, D / 2], K_scale and V_scale [n_pages, H_kv, P,
+    D / 16], all uint8 (scales may be float8_e4m3fn); the rest as for ``paged_args``."""
+    base = paged_args(q_seq, q_pos, page_table, H, H_kv, D, P, n_pages, None, None, scale)
+    ptrs = []
+    for name, x, per in (("K", K, 2), ("V", V, 2), ("K_scale", K_scale, 16), ("V_scale", V_scale, 16)):
+        if x is not None and type(x) is not int:
+            if tuple(x.shape) != (n_pages, H_kv, P, D // per):
+                raise SAError(SA_ERR_INVALID_ARG, f"{name} is {list(x.shape)}: need {[n_pages, H_kv, P, D // per]}")
+            if per == 16 and x.dtype is torch.float8_e4m3fn:
+                x = x.view(_UINT8)
+        ptrs.append(_dense(name, x, _UINT8, n_pages, H_kv * P * (D // per), base.device))
+    base.K, base.V = ptrs[0], ptrs[1]
+    pa = Paged4Args(base, ptrs[2], ptrs[3], float(k_gain), float(v_gain))
+    pa.device = base.device
+    return pa
+
+
+def new_paged4_workspace(pa: Paged4Args, device="cuda", stream=None) -> torch.Tensor:
+    n = sa_paged4_workspace_size(pa)
     if n == 0:
         raise SAError(SA_ERR_INVALID_ARG, "workspace size query rejected the arguments")
     ws = torch.empty(n, dtype=torch.uint8, device=device)

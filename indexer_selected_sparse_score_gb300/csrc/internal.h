@@ -139,6 +139,32 @@ bool encode_rows(CUtensorMap *m, const void *base, uint64_t rows, int dim, uint3
 size_t block_attn_scratch(const sa_paged_args &pa, int K, int local);
 size_t prefix_attn_scratch(const sa_paged_args &pa, int shared_pages);
 
+// Argument checks of the paged calls: the shapes (and the cache's pointers), and
+// the rows and rotation of an append whose rotated span comes in units of
+// dim_unit values.
+sa_status check_paged(const sa_paged_args *pa, bool need_cache);
+sa_status check_append(const sa_paged_args *pa, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                       const void *q, int64_t q_stride, const void *q_out, const sa_rope_args *rope, int dim_unit);
+
+// Paged cache held in 4 bits (sa_paged4_args).
+cudaError_t launch_paged4_append(const sa_paged4_args &pa, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                 const sa_rope_args *rope, bool halves, const int32_t *rope_pos, float *weight,
+                                 int32_t *born, int64_t ld, uint32_t *status, cudaStream_t stream);
+cudaError_t launch_paged4_read(const sa_paged4_args &pa, void *k_out, void *v_out, uint32_t *status,
+                               cudaStream_t stream);
+constexpr int kAttn4Counters = 512;  // words of the workspace header, 0 between calls
+cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, float *lse, void *scratch,
+                         uint32_t *counters, uint32_t *status, cudaStream_t stream);
+size_t attn4_scratch(const sa_paged4_args &pa);
+cudaError_t launch_weights4(const sa_paged4_args &pa, const void *q, const float *lse, float *weight, int64_t ld,
+                            void *scratch, uint32_t *status, cudaStream_t stream);
+size_t weights4_scratch(const sa_paged4_args &pa);
+cudaError_t launch_evict4(const sa_paged4_args &pa, const int32_t *length, const int32_t *newest, int budget, int recent,
+                          const float *weight, const int32_t *born, float *weight_out, int32_t *born_out, int64_t ld,
+                          int32_t *length_out, void *scratch, uint32_t *status, cudaStream_t stream);
+size_t evict4_scratch(const sa_paged4_args &pa);
+
 // Kernel launches of one fused call (index score, top-k, attention, combine).
 int fused_launch_count(const sa_index_args &ia, const sa_attn_args &aa, int K,
                        const SplitPlan &plan);

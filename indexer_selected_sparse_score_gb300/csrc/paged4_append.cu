@@ -1,0 +1,311 @@
+// The writer and the reader of a paged cache held in 4 bits.
+//
+// append: rows in, rotated (as paged_append.cu does, see the note on angles
+// there), rounded to bf16, and quantised: s = e4m3(max(amax / 6, 2^-9)) of every
+// 16 values, codes = e2m1(z / s).  The gain is a power of two, so z = y / gain has
+// bf16's eight significant bits and s four: z / s either is a midpoint between
+// two codes or lies 2^-9 of it away (z 2^k and m s are integers below 2^8).  So
+// the quotient is taken as z times the rounded 1 / s, rounded to 14 significant
+// bits (which restores a midpoint and moves no other value across one), and
+// the hardware's conversion rounds it as the exact quotient.
+//
+// Traffic per token: 4 D bytes of every key and value row pair in, 9/8 D out, 4 D
+// of every query head; bound by HBM for a prefill, by its chain of loads for a
+// decode step.  One CTA per token, its rows' loads issued before its page is
+// known; a thread holds two chunks of eight values, the two halves of a block of
+// 16, or (halves) of two blocks that it shares with its neighbour.
+//
+// read: a thread per 16 values.
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "paged4.cuh"
+#include "paged_list.h"
+
+namespace sa {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kMaxPairs = 64;
+
+struct Turns {
+  uint64_t f[kMaxPairs];  // turns per position, times 2^64
+};
+
+struct AppendParams {
+  Paged4View c;
+  const uint16_t *k, *v, *q;
+  int64_t k_stride, v_stride, q_stride;
+  uint16_t *q_out;
+  const int32_t *rope_pos;
+  float *weight;
+  int32_t *born;
+  int64_t ld;
+  float k_inv, v_inv;  // 1 / gain
+  int q_heads;         // H, or 0 without queries
+  int D, dim, halves;
+  uint32_t *status;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Four adjacent pairs of one chunk.
+__device__ __forceinline__ void rotate_adjacent(uint32_t (&w)[4], const float2 *cs) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 c = cs[i];
+    const float a = lo_f(w[i]), b = hi_f(w[i]);
+    w[i] = pack_bf16(a * c.x - b * c.y, a * c.y + b * c.x);
+  }
+}
+
+// Eight pairs (u[e], w[e]) of two chunks half the rotated span apart.
+__device__ __forceinline__ void rotate_halves(uint32_t (&u)[4], uint32_t (&w)[4], const float2 *cs) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
+    const float a0 = lo_f(u[i]), a1 = hi_f(u[i]), b0 = lo_f(w[i]), b1 = hi_f(w[i]);
+    u[i] = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
+    w[i] = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
+  }
+}
+
+// Largest magnitude of a chunk of eight, NaN if one is.
+__device__ __forceinline__ float chunk_top(const uint32_t (&w)[4], float inv) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_nan(max_nan(m, fabsf(lo_f(w[i]) * inv)), fabsf(hi_f(w[i]) * inv));
+  return m;
+}
+
+// Scale byte of a block whose largest magnitude is `top`.
+__device__ __forceinline__ uint32_t scale_byte(float top) {
+  if (top != top) return 0x7Fu;
+  const float s = fminf(fmaxf(__fdiv_rn(top, 6.f), 0x1p-9f), 448.f);
+  return __nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Codes of a chunk of eight values over a scale (byte).
+__device__ __forceinline__ uint32_t chunk_codes(const uint32_t (&w)[4], float inv, uint32_t scale) {
+  if (scale == 0x7Fu) return 0u;
+  const float r = __frcp_rn(e4m3_bits_to_float(static_cast<uint8_t>(scale)));
+  auto quotient = [&](float y) {
+    // 14 significant bits, to the nearest (infinities stay)
+    return __uint_as_float((__float_as_uint(y * inv * r) + 0x200u) & ~0x3FFu);
+  };
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t two;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tmov.b32 %0, {b, 0, 0, 0};\n\t}"
+        : "=r"(two)
+        : "f"(quotient(hi_f(w[i]))), "f"(quotient(lo_f(w[i]))));
+    out |= two << (8 * i);
+  }
+  return out;
+}
+
+__global__ void __launch_bounds__(kThreads, 4)
+append4_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
+  __shared__ float2 cs[kMaxPairs];
+  const PagedView &pv = p.c.v;
+  const int t = blockIdx.x, threads = blockDim.x;
+  const int log_upr = p.D == 128 ? 3 : 2;  // of the units (two chunks of eight values) of a row
+  const int kept = (p.D - p.dim) >> 4;     // units before the rotated span
+  const int span = p.dim >> 3;             // chunks of the rotated span
+  const int first = (p.D >> 3) - span;     // first rotated chunk
+  const int units = (p.q_heads + 2 * pv.H_kv) << log_upr;
+  // chunks of unit u within its row: two neighbours, or the two halves of eight
+  // pairs; a row's last units hold its rotated span (values are rotated in
+  // halves whether or not they are a value row's, so that rows are alike)
+  auto chunks = [&](int u, int &c0, int &c1) {
+    const int i = u & ((1 << log_upr) - 1), j = i - kept;
+    const bool half = p.halves && j >= 0;
+    c0 = half ? first + j : 2 * i;
+    c1 = half ? c0 + (span >> 1) : 2 * i + 1;
+    return half;
+  };
+  constexpr int kUnits = 2;
+  bool ok = false, tabled = false;
+  int page = -1, slot = 0;
+  for (int base = 0; base < units; base += kUnits * threads) {
+    uint32_t x[kUnits][4], y[kUnits][4];
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e) {
+      const int u = base + e * threads + threadIdx.x;
+      if (u >= units) continue;
+      int c0, c1;
+      chunks(u, c0, c1);
+      const int row = u >> log_upr, h = row - p.q_heads;
+      const uint16_t *src = h < 0        ? p.q + t * p.q_stride + static_cast<int64_t>(row) * p.D
+                            : h < pv.H_kv ? p.k + t * p.k_stride + static_cast<int64_t>(h) * p.D
+                                          : p.v + t * p.v_stride + static_cast<int64_t>(h - pv.H_kv) * p.D;
+      *reinterpret_cast<uint4 *>(x[e]) = *reinterpret_cast<const uint4 *>(src + 8 * c0);
+      *reinterpret_cast<uint4 *>(y[e]) = *reinterpret_cast<const uint4 *>(src + 8 * c1);
+    }
+    if (!tabled) {
+      const int turn = p.rope_pos ? p.rope_pos[t] : pv.q_pos[t];
+      int b, pos;
+      ok = load_paged_token(pv, t, p.status, threadIdx.x == 0, b, pos);
+      if (ok) {
+        page = load_page(pv, b, pos >> pv.logP, p.status, threadIdx.x == 0);
+        slot = pos & (pv.P - 1);
+        if (threadIdx.x < p.dim / 2) {
+          const uint64_t ph = static_cast<uint64_t>(static_cast<int64_t>(turn)) * turns.f[threadIdx.x] + (uint64_t{1} << 31);
+          float sn, c;
+          sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &sn, &c);
+          cs[threadIdx.x] = make_float2(c, sn);
+        }
+        if (p.weight) {
+          for (int h = threadIdx.x; h < pv.H_kv; h += threads) {
+            const int64_t at = (static_cast<int64_t>(b) * pv.H_kv + h) * p.ld + pos;
+            p.weight[at] = 0.f;
+            p.born[at] = turn;
+          }
+        }
+      }
+      __syncthreads();
+      tabled = true;
+    }
+    if (!ok) return;  // the whole CTA alike
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e) {
+      const int u = base + e * threads + threadIdx.x;
+      const bool mine = u < units;
+      if (!__any_sync(0xffffffffu, mine)) continue;
+      int c0, c1;
+      const bool half = chunks(u, c0, c1);
+      const int row = u >> log_upr, h = row - p.q_heads;
+      if (mine && h < pv.H_kv && c0 >= first) {
+        if (half) {
+          rotate_halves(x[e], y[e], cs + 8 * (c0 - first));
+        } else {
+          rotate_adjacent(x[e], cs + 4 * (c0 - first));
+          rotate_adjacent(y[e], cs + 4 * (c1 - first));
+        }
+      }
+      if (mine && h < 0) {
+        uint16_t *dst = p.q_out + (static_cast<int64_t>(t) * pv.H + row) * p.D;
+        *reinterpret_cast<uint4 *>(dst + 8 * c0) = *reinterpret_cast<uint4 *>(x[e]);
+        *reinterpret_cast<uint4 *>(dst + 8 * c1) = *reinterpret_cast<uint4 *>(y[e]);
+      }
+      const bool held = mine && h >= 0 && page >= 0;
+      if (!__any_sync(0xffffffffu, held)) continue;
+      const bool key = h < pv.H_kv;
+      const float inv = key ? p.k_inv : p.v_inv;
+      float tx = held ? chunk_top(x[e], inv) : 0.f, ty = held ? chunk_top(y[e], inv) : 0.f;
+      const float ox = __shfl_xor_sync(0xffffffffu, tx, 1), oy = __shfl_xor_sync(0xffffffffu, ty, 1);
+      if (!held) continue;
+      if (half) {  // the neighbour holds the blocks' other chunks
+        tx = max_nan(tx, ox);
+        ty = max_nan(ty, oy);
+      } else {
+        tx = ty = max_nan(tx, ty);
+      }
+      const uint32_t sx = scale_byte(tx), sy = half ? scale_byte(ty) : sx;
+      const uint32_t wx = chunk_codes(x[e], inv, sx), wy = chunk_codes(y[e], inv, sy);
+      const int64_t at = (static_cast<int64_t>(page) * pv.H_kv + (key ? h : h - pv.H_kv)) * pv.P + slot;
+      uint8_t *codes = (key ? p.c.K : p.c.V) + at * (p.D / 2), *scales = (key ? p.c.Ks : p.c.Vs) + at * (p.D / 16);
+      if (half) {
+        *reinterpret_cast<uint32_t *>(codes + 4 * c0) = wx;
+        *reinterpret_cast<uint32_t *>(codes + 4 * c1) = wy;
+        if (!(c0 & 1)) scales[c0 >> 1] = static_cast<uint8_t>(sx);
+        if (!(c1 & 1)) scales[c1 >> 1] = static_cast<uint8_t>(sy);
+      } else {
+        *reinterpret_cast<uint2 *>(codes + 4 * c0) = make_uint2(wx, wy);
+        scales[c0 >> 1] = static_cast<uint8_t>(sx);
+      }
+    }
+  }
+}
+
+// CTA (x): tokens; a thread per block of 16 values.
+__global__ void __launch_bounds__(256)
+read4_kernel(const Paged4View c, int D, float k_gain, float v_gain, uint16_t *k_out, uint16_t *v_out, int kinds,
+             uint32_t *status) {
+  const PagedView &pv = c.v;
+  const int t = blockIdx.x;
+  int b, pos;
+  if (!load_paged_token(pv, t, status, threadIdx.x == 0, b, pos)) return;
+  const int page = load_page(pv, b, pos >> pv.logP, status, threadIdx.x == 0);
+  if (page < 0) return;
+  const int log_b = D == 128 ? 3 : 2;
+  for (int u = threadIdx.x; u < (kinds * pv.H_kv) << log_b; u += blockDim.x) {
+    const int row = u >> log_b, blk = u & ((1 << log_b) - 1);
+    const bool key = k_out && row < pv.H_kv;
+    const int h = row < pv.H_kv ? row : row - pv.H_kv;
+    const int64_t at = (static_cast<int64_t>(page) * pv.H_kv + h) * pv.P + (pos & (pv.P - 1));
+    const uint2 w = *reinterpret_cast<const uint2 *>((key ? c.K : c.V) + at * (D / 2) + 8 * blk);
+    const float s = (key ? k_gain : v_gain) * e4m3_bits_to_float((key ? c.Ks : c.Vs)[at * (D / 16) + blk]);
+    __half2 d[8];
+    e2m1x8_to_half2(w.x, *reinterpret_cast<__half2(*)[4]>(d));
+    e2m1x8_to_half2(w.y, *reinterpret_cast<__half2(*)[4]>(d + 4));
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = __half22float2(d[i]);
+      o[i] = pack_bf16(f.x * s, f.y * s);
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>((key ? k_out : v_out) + (static_cast<int64_t>(t) * pv.H_kv + h) * D + 16 * blk);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged4_append(const sa_paged4_args &pa, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                 const sa_rope_args *rope, bool halves, const int32_t *rope_pos, float *weight,
+                                 int32_t *born, int64_t ld, uint32_t *status, cudaStream_t stream) {
+  if (pa.p.T == 0) return cudaSuccess;
+  AppendParams p;
+  p.c = paged4_view(pa);
+  p.k = static_cast<const uint16_t *>(k);
+  p.v = static_cast<const uint16_t *>(v);
+  p.q = static_cast<const uint16_t *>(q);
+  const int64_t kv_row = static_cast<int64_t>(pa.p.H_kv) * pa.p.D;
+  p.k_stride = k_stride ? k_stride : kv_row;
+  p.v_stride = v_stride ? v_stride : kv_row;
+  p.q_stride = q_stride ? q_stride : static_cast<int64_t>(pa.p.H) * pa.p.D;
+  p.q_out = static_cast<uint16_t *>(q_out);
+  p.rope_pos = rope_pos;
+  p.weight = weight;
+  p.born = born;
+  p.ld = ld;
+  p.k_inv = 1.f / pa.k_gain;
+  p.v_inv = 1.f / pa.v_gain;
+  p.q_heads = q ? pa.p.H : 0;
+  p.D = pa.p.D;
+  p.dim = rope ? rope->dim : 0;
+  p.halves = halves ? 1 : 0;
+  p.status = status;
+  Turns turns{};
+  const RopeRamp ramp = p.dim > 0 ? rope_ramp(*rope) : RopeRamp{0.0, 0.0};
+  for (int i = 0; i < p.dim / 2; ++i) {
+    const double f = rope_frequency(*rope, ramp, i) / (2.0 * 3.14159265358979323846);
+    turns.f[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
+  }
+  const int units = (p.q_heads + 2 * pa.p.H_kv) * (pa.p.D / 16);
+  const int threads =
+      pa.p.T > 4 * sm_count() ? std::min(std::max((units / 2 + 31) & ~31, kMaxPairs), kThreads) : kThreads;
+  return launch_ex(false, append4_kernel, dim3(pa.p.T), dim3(threads), 0, stream, 1, p, turns);
+}
+
+cudaError_t launch_paged4_read(const sa_paged4_args &pa, void *k_out, void *v_out, uint32_t *status,
+                               cudaStream_t stream) {
+  const int kinds = (k_out ? 1 : 0) + (v_out ? 1 : 0);
+  if (pa.p.T == 0 || kinds == 0) return cudaSuccess;
+  const int units = kinds * pa.p.H_kv * (pa.p.D / 16);
+  return launch_ex(false, read4_kernel, dim3(pa.p.T), dim3(std::min((units + 31) & ~31, 256)), 0, stream, 1,
+                   paged4_view(pa), pa.p.D, pa.k_gain, pa.v_gain, static_cast<uint16_t *>(k_out),
+                   static_cast<uint16_t *>(v_out), kinds, status);
+}
+
+}  // namespace sa

@@ -17,6 +17,10 @@ sa_status cuda_fail(cudaError_t e, const char *what) {
   return set_error(SA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+}  // namespace
+
+namespace sa {
+
 sa_status check_paged(const sa_paged_args *pa, bool need_cache) {
   if (!pa) return set_error(SA_ERR_INVALID_ARG, "paged args pointer is NULL");
   if (pa->B < 1 || pa->T < 0 || pa->H < 1 || pa->H_kv < 1 || pa->H % pa->H_kv || pa->n_pages < 1 || pa->max_pages < 1)
@@ -50,6 +54,47 @@ sa_status check_paged(const sa_paged_args *pa, bool need_cache) {
   return SA_OK;
 }
 
+namespace {
+
+sa_status check_stride(const char *name, int64_t stride, int64_t row) {
+  if (stride != 0 && (stride < row || stride % 8))
+    return set_error(SA_ERR_INVALID_ARG, "%s_stride %lld: need 0 or a multiple of 8 of at least %lld", name,
+                     static_cast<long long>(stride), static_cast<long long>(row));
+  return SA_OK;
+}
+
+}  // namespace
+
+sa_status check_append(const sa_paged_args *pa, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                       const void *q, int64_t q_stride, const void *q_out, const sa_rope_args *rope, int dim_unit) {
+  const int64_t kv_row = static_cast<int64_t>(pa->H_kv) * pa->D, q_row = static_cast<int64_t>(pa->H) * pa->D;
+  if (sa_status s = check_stride("k", k_stride, kv_row)) return s;
+  if (sa_status s = check_stride("v", v_stride, kv_row)) return s;
+  if (sa_status s = check_stride("q", q_stride, q_row)) return s;
+  if (pa->T > 0 && (!k || !v)) return set_error(SA_ERR_INVALID_ARG, "k and v must be device pointers");
+  if ((q == nullptr) != (q_out == nullptr)) return set_error(SA_ERR_INVALID_ARG, "q and q_out go together");
+  if (q && q == q_out && q_stride != 0 && q_stride != q_row)
+    return set_error(SA_ERR_INVALID_ARG, "q_out may be q only when q is dense");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16))
+    return set_error(SA_ERR_INVALID_ARG, "k, v, q and q_out must be 16-byte aligned");
+  if (rope) {
+    if (rope->dim < 0 || rope->dim > pa->D || rope->dim % dim_unit)
+      return set_error(SA_ERR_INVALID_ARG, "rope dim %d: need a multiple of %d in [0, %d]", rope->dim, dim_unit, pa->D);
+    if (rope->dim > 0 &&
+        (!std::isfinite(rope->base) || rope->base <= 1.0 || !std::isfinite(rope->factor) || rope->factor <= 0.0 ||
+         (rope->original_seq_len > 0 && !(std::isfinite(rope->beta_fast) && rope->beta_fast > 0.0 &&
+                                          std::isfinite(rope->beta_slow) && rope->beta_slow > 0.0))))
+      return set_error(SA_ERR_INVALID_ARG, "rope base > 1, factor > 0 and, with YaRN, beta_fast and beta_slow > 0");
+  }
+  return SA_OK;
+}
+
+}  // namespace sa
+
+namespace {
+
+using sa::check_paged;
+
 sa_status check_scale(const sa_paged_args *pa) {
   return std::isfinite(pa->scale) ? SA_OK : set_error(SA_ERR_INVALID_ARG, "scale is not finite");
 }
@@ -58,13 +103,6 @@ sa_status check_ws(void *ws, size_t ws_bytes, size_t need) {
   if (!ws) return set_error(SA_ERR_WORKSPACE, "workspace pointer is NULL");
   if (!aligned(ws, 16)) return set_error(SA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   if (ws_bytes < need) return set_error(SA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
-  return SA_OK;
-}
-
-sa_status check_stride(const char *name, int64_t stride, int64_t row) {
-  if (stride != 0 && (stride < row || stride % 8))
-    return set_error(SA_ERR_INVALID_ARG, "%s_stride %lld: need 0 or a multiple of 8 of at least %lld", name,
-                     static_cast<long long>(stride), static_cast<long long>(row));
   return SA_OK;
 }
 
@@ -123,25 +161,8 @@ sa_status sa_paged_append(const sa_paged_args *pa, const void *k, int64_t k_stri
                           const void *q, int64_t q_stride, void *q_out, const sa_rope_args *rope, int32_t rope_halves,
                           void *k_mean, void *ws, size_t ws_bytes, sa_stream_t stream) {
   if (sa_status s = check_paged(pa, true)) return s;
-  const int64_t kv_row = static_cast<int64_t>(pa->H_kv) * pa->D, q_row = static_cast<int64_t>(pa->H) * pa->D;
-  if (sa_status s = check_stride("k", k_stride, kv_row)) return s;
-  if (sa_status s = check_stride("v", v_stride, kv_row)) return s;
-  if (sa_status s = check_stride("q", q_stride, q_row)) return s;
-  if (pa->T > 0 && (!k || !v)) return set_error(SA_ERR_INVALID_ARG, "k and v must be device pointers");
-  if ((q == nullptr) != (q_out == nullptr)) return set_error(SA_ERR_INVALID_ARG, "q and q_out go together");
-  if (q && q == q_out && q_stride != 0 && q_stride != q_row)
-    return set_error(SA_ERR_INVALID_ARG, "q_out may be q only when q is dense");
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(k_mean, 16))
-    return set_error(SA_ERR_INVALID_ARG, "k, v, q, q_out and k_mean must be 16-byte aligned");
-  if (rope) {
-    if (rope->dim < 0 || rope->dim > pa->D || rope->dim % 16)
-      return set_error(SA_ERR_INVALID_ARG, "rope dim %d: need a multiple of 16 in [0, %d]", rope->dim, pa->D);
-    if (rope->dim > 0 &&
-        (!std::isfinite(rope->base) || rope->base <= 1.0 || !std::isfinite(rope->factor) || rope->factor <= 0.0 ||
-         (rope->original_seq_len > 0 && !(std::isfinite(rope->beta_fast) && rope->beta_fast > 0.0 &&
-                                          std::isfinite(rope->beta_slow) && rope->beta_slow > 0.0))))
-      return set_error(SA_ERR_INVALID_ARG, "rope base > 1, factor > 0 and, with YaRN, beta_fast and beta_slow > 0");
-  }
+  if (sa_status s = sa::check_append(pa, k, k_stride, v, v_stride, q, q_stride, q_out, rope, 16)) return s;
+  if (!aligned(k_mean, 16)) return set_error(SA_ERR_INVALID_ARG, "k_mean must be 16-byte aligned");
   if (sa_status s = check_ws(ws, ws_bytes, 256)) return s;
   cudaError_t e = sa::launch_paged_append(*pa, k, k_stride, v, v_stride, q, q_stride, q_out, rope, rope_halves != 0,
                                           k_mean, at<uint32_t>(ws, 0), cu(stream));

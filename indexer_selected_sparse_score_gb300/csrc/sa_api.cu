@@ -218,7 +218,7 @@ size_t sa_workspace_size(const sa_index_args *ia, const sa_attn_args *aa, int32_
 
 sa_status sa_workspace_init(void *ws, size_t ws_bytes, sa_stream_t stream) {
   if (sa_status s = check_ws(ws, ws_bytes, 256)) return s;
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = cudaMemsetAsync(ws, 0, std::min<size_t>(ws_bytes, 4096), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, "cudaMemsetAsync");
 }
 
