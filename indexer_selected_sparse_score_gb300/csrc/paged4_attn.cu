@@ -29,54 +29,49 @@
 // copies; a page's rows of one KV head are contiguous).  A unit that is cut leaves
 // parts in scratch; the CTA that adds the last of them (a counter) merges them in
 // order.
+#include <cfloat>
+#include <climits>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged4_mma.cuh"
 #include "paged4_units.cuh"
-#include "umma.cuh"
+#include "paged_umma.cuh"
 
 namespace sa {
 namespace {
 
 using namespace umma;
 
-constexpr int kTile = 128;               // slots per tile, 16 per warp
-constexpr int kWarps = 8;                // and a copy warp
-constexpr int kThreads = 32 * kWarps + 32;
-constexpr int kCtasPerSm = 2;
-constexpr int kLeast = 2;                // tiles of a CTA, at least
 
-// What the copy warp tells of a tile.
-struct TileInfo {
-  int t0, n, h0, g;      // unit: first token, tokens, first query head, heads of a token
-  int base;              // first slot
-  int low, last;         // lowest and highest slot of the unit's valid tokens
-  uint32_t have;         // bit w: slots 16 w .. of the tile are in a page
-  int first, end;        // first, last tile of this CTA's part of the unit
-  int c0, c1;            // CTAs that share the unit
-  int pos[16];           // slots of the tokens, -1 for one to be skipped
-};
+constexpr int kTile = 128;               // slots per tile: the grain of the work's division
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCtasPerSm = 2;            // 16 warps of 128 registers
+constexpr int kGroup = 32;               // slots of a warp's step
+constexpr int kStages = 3;               // groups that a warp has in its ring
+#ifndef SA4_LEAST
+#define SA4_LEAST 2
+#endif
+constexpr int kLeast = SA4_LEAST;                // tiles of a CTA, at least
 
 template <int kDim, int NT>
 struct AttnSmem {
-  static constexpr int kStages = kDim == 128 ? 3 : 6;
-  static constexpr uint32_t kCodes = kTile * kDim / 2, kScales = kTile * kDim / 16;
-  static constexpr uint32_t kQ = 8 * NT * kDim * 2;  // queries as they come
-  static constexpr uint32_t kStage = 2 * (kCodes + kScales) + kQ;
-  static constexpr size_t red = static_cast<size_t>(kStages) * kStage;      // [warp][D / 4][32] fp32
-  static constexpr size_t qf = red + kWarps * (kDim / 4) * 32 * 4;  // [NT][D / 32][32] 16 B: fragments
-  static constexpr size_t info = qf + kQ;
-  static constexpr size_t cols = info + kStages * sizeof(TileInfo);         // factor, limit of a column
-  static constexpr size_t stat = cols + 16 * 8;                             // [warp][16] reference, sum
-  static constexpr size_t poison = stat + kWarps * 16 * 8;                  // [8] lowest slot with a NaN block
-  static constexpr size_t bars = poison + 32;
-  static constexpr size_t scan = bars + (2 * kStages + 1) * 8;
+  static constexpr uint32_t kCodes = kGroup * kDim / 2, kScales = kGroup * kDim / 16;  // of a group
+  static constexpr uint32_t kStage = 2 * (kCodes + kScales);
+  static constexpr uint32_t kRing = kStages * kStage;  // of a warp; at a part's end it holds its O, [D / 4][32] fp32
+  static constexpr size_t qf = static_cast<size_t>(kWarps) * kRing;               // [NT][D / 32][32] 16 B: fragments
+  static constexpr size_t cols = qf + 8 * NT * kDim * 2;                         // factor, limit of a column
+  static constexpr size_t poison = cols + 16 * 8;                                // [8] lowest slot with a NaN block
+  static constexpr uint32_t stat = kDim / 4 * 32 * 4;  // within a warp's ring at a part's end: [16] reference, sum
+  static constexpr size_t scan = poison + 32;
   static constexpr size_t start = scan + 32 * 8;
   static constexpr size_t flag = start + sizeof(UnitStart);
   static constexpr size_t total = flag + 16;
-  static_assert(sizeof(TileInfo) % 8 == 0 && sizeof(UnitStart) % 8 == 0 && kQ % 16 == 0, "alignment");
-  static_assert(total <= 113 * 1024, "two CTAs per SM");
+  static_assert(sizeof(UnitStart) % 8 == 0 && kRing >= stat + 16 * 8, "layout");
+  static_assert((total + 1024) * kCtasPerSm <= 228 * 1024, "shared memory of an SM");
 };
 
 struct Attn4Params {
@@ -110,351 +105,282 @@ __device__ __forceinline__ void store_columns(const float (&o)[4], const float (
   }
 }
 
-// Joins the parts of a unit shared by CTAs c0 .. c1, in their order.
-template <int kDim, int NT>
-__device__ __forceinline__ void merge_parts(const float *part, const float2 *ml, int c0, int c1, int nt, int mt, int lane,
-                                            float (&o)[4], float (&m)[2], float (&sum)[2]) {
-  constexpr int kBatch = 8;  // parts whose loads go out together
-  for (int k0 = c0; k0 <= c1; k0 += kBatch) {
-    float x[kBatch][4];
-    float4 s[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int k = min(k0 + i, c1);
-      const int64_t slot = 2 * static_cast<int64_t>(k) + (k == c0);
-      s[i] = __ldcg(reinterpret_cast<const float4 *>(ml + slot * 16 + 8 * nt + 2 * (lane & 3)));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[i][e] = __ldcg(part + ((slot * NT + nt) * (kDim / 4) + 4 * mt + e) * 32 + lane);
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float top = m[e];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, e ? s[i].z : s[i].x);
-      if (top == -INFINITY) continue;
-      const float f = m[e] == top ? 1.f : exp2f(m[e] - top);
-      m[e] = top;
-      sum[e] *= f;
-      o[e] *= f;
-      o[2 + e] *= f;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (k0 + i > c1) continue;
-        const float r = e ? s[i].z : s[i].x;
-        const float w = r == top ? 1.f : exp2f(r - top);
-        sum[e] = fmaf(w, e ? s[i].w : s[i].y, sum[e]);
-        o[e] = fmaf(w, x[i][e], o[e]);
-        o[2 + e] = fmaf(w, x[i][2 + e], o[2 + e]);
-      }
-    }
-  }
-}
-
-template <int kDim, int NT>
+template <int kDim, int NT, bool kSmall>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 attn4_kernel(const Attn4Params p) {
   using L = AttnSmem<kDim, NT>;
-  constexpr int kStages = L::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bars), *empty = full + kStages, *meet = empty + kStages;
-  TileInfo *infos = reinterpret_cast<TileInfo *>(smem + L::info);
   UnitStart *start = reinterpret_cast<UnitStart *>(smem + L::start);
-  volatile int *flags = reinterpret_cast<volatile int *>(smem + L::flag);  // [0] abort, [1] last of a unit's parts
+  volatile int *last_s = reinterpret_cast<volatile int *>(smem + L::flag);  // whether this CTA merges a unit's parts
   const PagedView &pv = p.c.v;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
-    }
-    mbar_init(meet, kWarps);
-    flags[0] = 0;
-    fence_barrier_init();
-  }
   long long x0, x1;
   int ctas;
   const int heads = pv.H_kv * p.gb;
   find_units(pv, p.nt, heads, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
   __syncthreads();
+  if (x0 >= x1) return;
+  const long long total = start->total;
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ copy warp
-    int issued = 0;
-    bool ok = true;
-    if (x0 < x1) {
-      const long long total = start->total;
-      int block = start->block, hv = start->head, kt = start->tile;
-      int skip_to = start->t0;  // units of the block before this token are not of this CTA
-      long long x = x0;
-      while (x < x1 && ok && static_cast<int64_t>(block) * p.nt < pv.T) {
-        // the units of one block: lane l holds token block * nt + l
-        const int t = block * p.nt + lane;
-        const bool in = lane < p.nt && t < pv.T;
-        const int b = in ? pv.q_seq[t] : -1, pos = in ? pv.q_pos[t] : -1;
-        const bool valid = in && b >= 0 && b < pv.B && pos >= 0 && (pos >> pv.logP) < pv.max_pages;
-        const int b_prev = __shfl_up_sync(0xffffffffu, b, 1);
-        uint32_t starts = __ballot_sync(0xffffffffu, in && (lane == 0 || b != b_prev));
-        const int count = __popc(__ballot_sync(0xffffffffu, in));
-        while (starts && x < x1 && ok) {
-          const int l0 = __ffs(starts) - 1;
-          starts &= starts - 1;
-          const int l1 = starts ? __ffs(starts) - 1 : count;
-          const int t0 = block * p.nt + l0;
-          if (t0 < skip_to) continue;
-          const bool member = lane >= l0 && lane < l1 && valid;
-          const int last = static_cast<int>(__reduce_max_sync(0xffffffffu, member ? pos : -1));
-          const int low = static_cast<int>(__reduce_min_sync(0xffffffffu, member ? pos : 0x7FFFFFFF));
-          const int cost = (last + kTile) / kTile;
-          if (cost == 0) continue;
-          const int seq = __shfl_sync(0xffffffffu, b, l0);
-          const int mypos = __shfl_sync(0xffffffffu, valid ? pos : -1, min(l0 + lane, 31));
-          for (; hv < heads && x < x1 && ok; ++hv) {
-            const int hk = hv / p.gb, g0 = 16 * (hv - hk * p.gb), ng = min(16, p.group - g0), h0 = hk * p.group + g0;
-            const long long u0 = x - kt, u1 = u0 + cost;
-            const int c0 = u0 < x0 ? cta_of_tile(u0, total, ctas) : blockIdx.x;
-            const int c1 = u1 > x1 ? cta_of_tile(u1 - 1, total, ctas) : blockIdx.x;
-            bool fresh = true;
-            for (; kt < cost && x < x1; ++kt, ++x) {
-              const int s = issued % kStages;
-              // lane 4 q + kind copies page q's part: codes and scales of K and V
-              const int base = kt * kTile, q = lane >> 2, kind = lane & 3;
-              const int from = base + (q << pv.logP);
-              const int rows = min(pv.P, ((min(last - from, kTile) + 16) & ~15));  // this page's, by sixteens
-              int page = -1;
-              if (q < (kTile >> pv.logP) && from <= last)
-                page = load_page(pv, seq, from >> pv.logP, p.status, kind == 0);
-              uint32_t have = 0;
-              const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0 && kind == 0);
-#pragma unroll
-              for (int w = 0; w < kWarps; ++w) have |= ((pages >> (4 * ((16 * w) >> pv.logP))) & 1u) << w;
-              const uint32_t row_bytes = kind < 2 ? kDim / 2 : kDim / 16;
-              const uint32_t bytes = page >= 0 ? rows * row_bytes : 0u;
-              const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
-              if (!mbar_wait_warp(&empty[s], ((issued / kStages) & 1) ^ 1) || flags[0]) {
-                ok = false;
-                break;
-              }
-              uint8_t *stage = smem + s * L::kStage;
-              TileInfo *in_s = &infos[s];
-              const uint32_t q_bytes = fresh ? static_cast<uint32_t>(l1 - l0) * ng * kDim * 2 : 0u;
-              if (lane < 16) in_s->pos[lane] = l0 + lane < l1 ? mypos : -1;
-              if (lane == 0) {
-                in_s->t0 = t0;
-                in_s->n = l1 - l0;
-                in_s->h0 = h0;
-                in_s->g = ng;
-                in_s->base = base;
-                in_s->low = low;
-                in_s->last = last;
-                in_s->have = have;
-                in_s->first = fresh;
-                in_s->end = kt + 1 == cost || x + 1 == x1;
-                in_s->c0 = c0;
-                in_s->c1 = c1;
-              }
-              __syncwarp();
-              if (lane == 0) mbar_expect_tx(&full[s], sum + q_bytes);
-              __syncwarp();
-              ++issued;
-              if (bytes) {
-                const int64_t at = (static_cast<int64_t>(page) * pv.H_kv + hk) * pv.P * row_bytes;
-                const uint8_t *src = (kind == 0 ? p.c.K : kind == 1 ? p.c.V : kind == 2 ? p.c.Ks : p.c.Vs) + at;
-                uint8_t *dst = stage + (kind == 0   ? 0
-                                        : kind == 1 ? L::kCodes
-                                        : kind == 2 ? 2 * L::kCodes
-                                                    : 2 * L::kCodes + L::kScales) + (q << pv.logP) * row_bytes;
-                bulk_load(dst, src, bytes, &full[s]);
-              }
-              if (fresh && lane < l1 - l0)
-                bulk_load(stage + 2 * (L::kCodes + L::kScales) + lane * ng * kDim * 2,
-                          p.q + (static_cast<int64_t>(t0 + lane) * pv.H + h0) * kDim, ng * kDim * 2,
-                          &full[s]);
-              fresh = false;
-            }
-            if (kt < cost) break;  // the range ends inside the unit
-            kt = 0;
-          }
-          if (hv == heads) hv = 0;
-        }
-        ++block;
-      }
-    }
-    if (lane == 0) {
-      if (!ok) {
-        raise_flag(p.status, kFlagTimeout);
-        flags[0] = 1;
-      }
-      // every copy lands before the CTA exits
-      for (int m = max(0, issued - kStages); m < issued; ++m) mbar_wait(&full[m % kStages], (m / kStages) & 1);
-    }
-    __syncwarp();
-    return;
-  }
-
-  // --------------------------------------------------------- product warps
   const int g = lane >> 2, tq = lane & 3;
   uint4 *qf = reinterpret_cast<uint4 *>(smem + L::qf);
   float2 *cols = reinterpret_cast<float2 *>(smem + L::cols);  // factor of the logits, limit (as an int)
-  float2 *stat = reinterpret_cast<float2 *>(smem + L::stat);
   int *poison = reinterpret_cast<int *>(smem + L::poison);
-  float *red = reinterpret_cast<float *>(smem + L::red);
-  int met = 0;
-  bool ok = true;
-  // the product warps meet (a bounded wait: a warp that gave up must not hold the others)
-  auto sync = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(meet);
-    ok = mbar_wait_warp(meet, (met++) & 1) && ok;
-  };
+  uint8_t *ring = smem + warp * L::kRing;
+  const uint32_t ring_s = smem_u32(ring);
+  constexpr int kMt = kDim / 16, kEach = (kMt + kWarps - 1) / kWarps;  // pairs of O's rows, of a warp
   Columns<kDim, NT> a;
-  long long left = x1 - x0;
-  for (int n = 0; left > 0; ++n, --left) {
-    const int s = n % kStages;
-    if (!mbar_wait_warp(&full[s], (n / kStages) & 1)) {
-      ok = false;
-      break;
-    }
-    const uint8_t *stage = smem + s * L::kStage;
-    const TileInfo &ti = infos[s];
-    if (ti.first) {
-      // queries as fp16 fragments, a column per warp
-      if (tid < 8) poison[tid] = 0x7FFFFFFF;
+
+  // Every warp walks the CTA's units by itself: lane l holds token l of a block.
+  int block = start->block, hv = start->head, kt0 = start->tile;
+  const int skip_to = start->t0;  // units of the first block before this token are not of this CTA
+  long long x = x0;
+  int t_seq = -1, t_pos = -1, n_seq = -1, n_pos = -1;
+  auto load_block = [&](int i, int &seq, int &pos) {
+    const int64_t t = static_cast<int64_t>(i) * p.nt + lane;
+    const bool in = lane < p.nt && t < pv.T;
+    seq = in ? pv.q_seq[t] : INT_MIN;
+    pos = in ? pv.q_pos[t] : -1;
+  };
+  load_block(block, n_seq, n_pos);
+  for (; x < x1 && static_cast<int64_t>(block) * p.nt < pv.T; ++block) {
+    t_seq = n_seq;
+    t_pos = n_pos;
+    load_block(block + 1, n_seq, n_pos);
+    const bool in = t_seq != INT_MIN;
+    const bool valid = in && t_seq >= 0 && t_seq < pv.B && t_pos >= 0 && (t_pos >> pv.logP) < pv.max_pages;
+    const int prev = __shfl_up_sync(0xffffffffu, t_seq, 1);
+    uint32_t starts = __ballot_sync(0xffffffffu, in && (lane == 0 || t_seq != prev));
+    const int count = __popc(__ballot_sync(0xffffffffu, in));
+    while (starts && x < x1) {
+      const int l0 = __ffs(starts) - 1;
+      starts &= starts - 1;
+      const int l1 = starts ? __ffs(starts) - 1 : count;
+      const int t0 = block * p.nt + l0;
+      if (t0 < skip_to) continue;
+      const bool member = lane >= l0 && lane < l1 && valid;
+      const int last = __reduce_max_sync(0xffffffffu, member ? t_pos : -1);
+      const int low = __reduce_min_sync(0xffffffffu, member ? t_pos : INT_MAX);
+      const int cost = (last + kTile) / kTile;
+      if (cost == 0) continue;
+      const int seq = __shfl_sync(0xffffffffu, t_seq, l0);
+      for (; hv < heads && x < x1; ++hv, kt0 = 0) {
+        const int hk = hv / p.gb, g0 = 16 * (hv - hk * p.gb), ng = min(16, p.group - g0), h0 = hk * p.group + g0;
+        const int ncols = (l1 - l0) * ng;
+        const long long u0 = x - kt0, u1 = u0 + cost;
+        const int c0 = u0 < x0 ? cta_of_tile(u0, total, ctas) : blockIdx.x;
+        const int c1 = u1 > x1 ? cta_of_tile(u1 - 1, total, ctas) : blockIdx.x;
+        const int kt1 = static_cast<int>(min(static_cast<long long>(cost), kt0 + (x1 - x)));
+        x += kt1 - kt0;
+        // ------------------------------- this CTA's part of a unit: tiles kt0 .. kt1 - 1
+        // groups of 32 slots: warp w takes first + w, + 8, ..; lane l holds the page of
+        // the l-th of each 32 (pages of 16: of the halves of each 16 groups)
+        constexpr int kPer = kTile / kGroup;       // groups of a tile
+        constexpr int kIds = kSmall ? 16 : 32;     // groups whose pages the lanes hold
+        const int n_groups = min(kt1 * kPer, last / kGroup + 1) - kt0 * kPer - warp;
+        const int mine = n_groups > 0 ? (n_groups + kWarps - 1) / kWarps : 0;
+        const int first = kt0 * kPer + warp;
+        auto load_ids = [&](int i) {
+          const int j = i + (kSmall ? lane >> 1 : lane);
+          const int slot = kGroup * (first + kWarps * j) + (kSmall ? 16 * (lane & 1) : 0);
+          if (j >= mine || slot > last) return -1;
+          return load_page(pv, seq, slot >> pv.logP, p.status, true);
+        };
+        int ids = load_ids(0), ids_next = -1;
+        uint32_t held = __ballot_sync(0xffffffffu, ids >= 0), held_now = held;  // which of them are pages
+        auto copy = [&](int i) {
+          if (i < mine) {
+            const uint32_t st = ring_s + (i % kStages) * L::kStage;
+            const int slot = kGroup * (first + kWarps * i);
+            constexpr int kS = kDim / 16;     // 16-byte chunks of the scales of 16 rows
+            // rows of a page from `in` on, into the ring from row `at` on; where there is
+            // no page nothing is read
+            auto rows = [&](int id, int in, uint32_t at, auto n_tag) {
+              constexpr int n = decltype(n_tag)::value;
+              const uint32_t bytes = id >= 0 ? 16u : 0u;
+              const int64_t row = (static_cast<int64_t>(max(id, 0) * pv.H_kv + hk) << pv.logP) + in;
+              const uint8_t *k = p.c.K + row * (kDim / 2) + 16 * lane, *v = p.c.V + row * (kDim / 2) + 16 * lane;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        stage_column<kDim>(reinterpret_cast<const uint16_t *>(stage + 2 * (L::kCodes + L::kScales)), 8 * nt + warp,
-                           ti.n * ti.g, lane, qf, [&](int col, float inv) {
-                             cols[col] = make_float2(p.qk_scale * inv,
-                                                     __int_as_float(col < ti.n * ti.g ? ti.pos[col / ti.g] : -1));
-                           });
-      sync();
-      if (!ok) break;
-      a.begin(qf, cols, lane);
-    }
-    const int base = ti.base + 16 * warp;
-    if (((ti.have >> warp) & 1u) && base <= ti.last) {
-      const uint8_t *k = stage + 16 * warp * (kDim / 2), *v = k + L::kCodes;
-      const uint8_t *ks = stage + 2 * L::kCodes + 16 * warp * (kDim / 16), *vs = ks + L::kScales;
-      const bool edge = base + 15 > ti.low;
-      a.step(k, ks, v, vs, base, edge, ti.low, ti.last, qf, poison, lane);
-    }
-    if (!ti.end) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
-      continue;
-    }
-    // ------------------------------------------ the part of a unit is done
-    const int t0 = ti.t0, ng = ti.g, ncols = ti.n * ng, h0 = ti.h0, c0 = ti.c0, c1 = ti.c1;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
-    a.sum_up();
-    if (g == 0) {
+              for (int e = 0; e < n * kDim / 2; e += 512) {
+                cp_async16_or_zero(st + at * (kDim / 2) + e + 16 * lane, k + e, bytes);
+                cp_async16_or_zero(st + L::kCodes + at * (kDim / 2) + e + 16 * lane, v + e, bytes);
+              }
+              constexpr int kC = n / 16 * kS;  // chunks of scales, of K and of V
+              const int c = lane % kC;
+              if (2 * kC == 32 || lane < 2 * kC)
+                cp_async16_or_zero(st + 2 * L::kCodes + (lane < kC ? 0 : L::kScales) + at * (kDim / 16) + 16 * c,
+                                   (lane < kC ? p.c.Ks : p.c.Vs) + row * (kDim / 16) + 16 * c, bytes);
+            };
+            if constexpr (kSmall) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+              for (int h = 0; h < 2; ++h)
+                rows(__shfl_sync(0xffffffffu, ids, (2 * i + h) & 31), 0, 16 * h, std::integral_constant<int, 16>());
+            } else {
+              rows(__shfl_sync(0xffffffffu, ids, i & 31), slot & (pv.P - 1), 0, std::integral_constant<int, 32>());
+            }
+          }
+          cp_async_commit();
+        };
 #pragma unroll
-        for (int e = 0; e < 2; ++e) stat[warp * 16 + 8 * nt + 2 * tq + e] = make_float2(a.ref[nt][e], a.l[nt][e]);
-    }
-    sync();
-    if (!ok) break;
-    const int d = kDim / 8 * g + 2 * warp;  // of the O values that this thread finishes: d, d + 1 of two columns
-    const int bad = warp < kDim / 16 ? poison[d >> 4] : 0;
-    const bool cut = c0 != c1;
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
-    constexpr int kMt = kDim / 16;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      // the column's reference over the warps, its sum, and this warp's factor
-      float m[2], sum[2], fac[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int col = 8 * nt + 2 * tq + e;
-        m[e] = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) m[e] = fmaxf(m[e], stat[w * 16 + col].x);
-        sum[e] = 0.f;
-        const float mm = m[e] == -INFINITY ? 0.f : m[e];
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 x = stat[w * 16 + col];
-          sum[e] += x.y * (x.x == -INFINITY ? 0.f : exp2f(x.x - mm));
+        for (int i = 0; i < kStages - 1; ++i) copy(i);
+        if (tid < 8) poison[tid] = INT_MAX;
+        // queries as fp16 fragments, a column per warp
+#pragma unroll 1
+        for (int col = warp; col < 8 * NT; col += kWarps) {
+          const int i = min(col / ng, l1 - l0 - 1);
+          const int pos = __shfl_sync(0xffffffffu, valid ? t_pos : -1, l0 + i);
+          stage_column<kDim>(p.q + (static_cast<int64_t>(t0 + i) * pv.H + h0 + col - i * ng) * kDim, col, col < ncols, lane,
+                             qf, [&](float inv) {
+                               cols[col] = make_float2(p.qk_scale * inv, __int_as_float(col < ncols ? pos : -1));
+                             });
         }
-        fac[e] = a.ref[nt][e] == -INFINITY ? 0.f : exp2f(a.ref[nt][e] - mm);
-      }
-      float *mine = red + warp * (kDim / 4) * 32 + lane;
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mine[(4 * mt + e) * 32] = a.o[nt][mt][e] * fac[e & 1];
-      sync();
-      if (!ok) break;
-      if (warp < kMt) {
-        float o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[e] = 0.f;
-          for (int w = 0; w < kWarps; ++w) o[e] += red[(w * (kDim / 4) + 4 * warp + e) * 32 + lane];
+        __syncthreads();
+        a.begin(cols, lane);
+#pragma unroll 1
+        for (int i = 0; i < mine; ++i) {
+          const int ahead = i + kStages - 1;
+          if (ahead % kIds == 0) {
+            ids = ids_next;
+            held = __ballot_sync(0xffffffffu, ids >= 0);
+          }
+          if (i % kIds == 0) held_now = held;  // (ahead is among the same)
+          cp_async_wait<kStages - 2>();
+          __syncwarp();
+          copy(ahead);
+          if (ahead % kIds == 4) ids_next = load_ids(ahead - 4 + kIds);
+          const int base = kGroup * (first + kWarps * i);
+          const uint32_t halves = kSmall ? (held_now >> (2 * (i % kIds))) & 3u : ((held_now >> (i % kIds)) & 1u) * 3u;
+          if (halves) {
+            const uint8_t *st = ring + (i % kStages) * L::kStage;
+            a.step(st, st + 2 * L::kCodes, st + L::kCodes, st + 2 * L::kCodes + L::kScales, base,
+                   base + kGroup - 1 > low || halves != 3u, halves, low, last, qf, poison, lane);
+          }
         }
-        // a NaN block of V that the column's token attends
+        cp_async_wait<0>();
+        a.sum_up();
+        const bool cut = c0 != c1;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
+        // The warps' sums and O joined: into scratch (to_part) or the output.
+        auto join = [&](bool to_part) {
+          if (g == 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (a.lim[nt][e & 1] >= bad) o[e] = NAN;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) reinterpret_cast<float2 *>(ring + L::stat)[8 * nt + 2 * tq + e] = make_float2(a.ref[nt][e], a.l[nt][e]);
+          }
+          __syncthreads();
+          int bad[kEach];
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) bad[i] = poison[(kDim / 8 * g + 2 * ((warp + i * kWarps) % kMt)) >> 4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            // the columns' references over the warps, their sums, this warp's factors
+            float m[2] = {-FLT_MAX, -FLT_MAX}, sum[2] = {}, fac[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              auto stat = [&](int w) {
+                return reinterpret_cast<const float2 *>(smem + w * L::kRing + L::stat)[8 * nt + 2 * tq + e];
+              };
+              for (int w = 0; w < kWarps; ++w) m[e] = fmaxf(m[e], stat(w).x);
+              for (int w = 0; w < kWarps; ++w) sum[e] += stat(w).y * exp2_fast(stat(w).x - m[e]);
+              fac[e] = exp2_fast(a.ref[nt][e] - m[e]);
+            }
+            float *mine_s = reinterpret_cast<float *>(ring) + lane;
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mine_s[(4 * mt + e) * 32] = a.o[nt][mt][e] * fac[e & 1];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+              const int mt = warp + i * kWarps, d = kDim / 8 * g + 2 * mt;
+              if (mt >= kMt) break;
+              float o[4] = {};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) o[e] += reinterpret_cast<const float *>(smem + w * L::kRing)[(4 * mt + e) * 32 + lane];
+                // a NaN block of V that the column's token attends
+                if (a.lim[nt][e & 1] >= bad[i]) o[e] = NAN;
+              }
+              if (to_part) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) __stcg(p.part + ((slot * NT + nt) * (kDim / 4) + 4 * mt + e) * 32 + lane, o[e]);
+                if (mt == 0 && g == 0)
+                  __stcg(reinterpret_cast<float4 *>(p.ml + slot * 16 + 8 * nt + 2 * tq), make_float4(m[0], sum[0], m[1], sum[1]));
+              } else {
+                store_columns<kDim>(o, m, sum, 8 * nt + 2 * tq, ncols, a.lim[nt], p, t0, h0, ng, d, mt == 0 && g == 0);
+              }
+            }
+            if (NT > 1) __syncthreads();
+          }
+        };
+        join(cut);
         if (cut) {
+          __threadfence();
+          __syncthreads();
+          if (tid == 0) {
+            const uint32_t before = atomicAdd(&p.counters[c0], 1u);
+            *last_s = before == static_cast<uint32_t>(c1 - c0);
+            if (*last_s) p.counters[c0] = 0;  // for the next call
+            __threadfence();
+          }
+          __syncthreads();
+          if (*last_s) {
+            // the last one here: every warp takes every seventh part
+            a.begin(cols, lane);
+            for (int k = c0 + warp; k <= c1; k += kWarps) {
+              const int64_t from = 2 * static_cast<int64_t>(k) + (k == c0);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p.part[((slot * NT + nt) * (kDim / 4) + 4 * warp + e) * 32 + lane] = o[e];
-          if (warp == 0 && g == 0)
+              for (int nt = 0; nt < NT; ++nt) {
+                float x[kMt][4];
+                const float4 s = __ldcg(reinterpret_cast<const float4 *>(p.ml + from * 16 + 8 * nt + 2 * tq));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) p.ml[slot * 16 + 8 * nt + 2 * tq + e] = make_float2(m[e], sum[e]);
-        } else {
-          store_columns<kDim>(o, m, sum, 8 * nt + 2 * tq, ncols, a.lim[nt], p, t0, h0, ng, d, warp == 0 && g == 0);
+                for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) x[mt][e] = __ldcg(p.part + ((from * NT + nt) * (kDim / 4) + 4 * mt + e) * 32 + lane);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float r = e ? s.z : s.x, m = fmaxf(a.ref[nt][e], r);
+                  const float f0 = exp2_fast(a.ref[nt][e] - m), f1 = exp2_fast(r - m);
+                  a.ref[nt][e] = m;
+                  a.l[nt][e] = a.l[nt][e] * f0 + (e ? s.w : s.y) * f1;
+#pragma unroll
+                  for (int mt = 0; mt < kMt; ++mt) {
+                    a.o[nt][mt][e] = a.o[nt][mt][e] * f0 + x[mt][e] * f1;
+                    a.o[nt][mt][e + 2] = a.o[nt][mt][e + 2] * f0 + x[mt][e + 2] * f1;
+                  }
+                }
+              }
+            }
+            join(false);
+          }
         }
+        __syncthreads();  // (the next part's copies land where O was)
       }
-      if (NT > 1) sync();
-      if (!ok) break;
+      if (hv == heads) hv = 0;
     }
-    if (!ok) break;
-    if (cut) {
-      __threadfence();
-      sync();
-      if (!ok) break;
-      if (tid == 0) {
-        const uint32_t before = atomicAdd(&p.counters[c0], 1u);
-        flags[1] = before == static_cast<uint32_t>(c1 - c0);
-        if (flags[1]) p.counters[c0] = 0;  // for the next call
-        __threadfence();
-      }
-      sync();
-      if (!ok) break;
-      if (flags[1] && warp < kMt) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float o[4] = {}, m[2] = {-INFINITY, -INFINITY}, sum[2] = {};
-          merge_parts<kDim, NT>(p.part, p.ml, c0, c1, nt, warp, lane, o, m, sum);
-          store_columns<kDim>(o, m, sum, 8 * nt + 2 * tq, ncols, a.lim[nt], p, t0, h0, ng, d, warp == 0 && g == 0);
-        }
-      }
-    }
-    // (the next part's first write to what is read here comes after its first meeting)
-  }
-  if (!ok && lane == 0) {
-    raise_flag(p.status, kFlagTimeout);
-    flags[0] = 1;
   }
 }
 
 int grid_of() { return std::min(kCtasPerSm * sm_count(), kAttn4Counters); }
 
-template <int kDim, int NT>
+template <int kDim, int NT, bool kSmall>
 cudaError_t launch(const Attn4Params &p, cudaStream_t stream) {
-  auto kern = attn4_kernel<kDim, NT>;
+  auto kern = attn4_kernel<kDim, NT, kSmall>;
   static bool done[64] = {};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), AttnSmem<kDim, NT>::total, done);
   if (e != cudaSuccess) return e;
   return launch_ex(false, kern, dim3(grid_of()), dim3(kThreads), AttnSmem<kDim, NT>::total, stream, 1, p);
 }
 
+size_t most_parts() { return 2 * static_cast<size_t>(grid_of()); }
 size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
 size_t attn4_scratch(const sa_paged4_args &pa) {
-  return round_up(2 * sizeof(float) * grid_of() * 16 * pa.p.D) + round_up(2 * sizeof(float2) * grid_of() * 16);
+  return round_up(sizeof(float) * most_parts() * 16 * pa.p.D) + round_up(sizeof(float2) * most_parts() * 16);
 }
 
 cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, float *lse, void *scratch,
@@ -466,7 +392,7 @@ cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, flo
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
   p.part = static_cast<float *>(scratch);
-  p.ml = reinterpret_cast<float2 *>(static_cast<char *>(scratch) + round_up(2 * sizeof(float) * grid_of() * 16 * pa.p.D));
+  p.ml = reinterpret_cast<float2 *>(static_cast<char *>(scratch) + round_up(sizeof(float) * most_parts() * 16 * pa.p.D));
   p.counters = counters;
   p.group = pa.p.H / pa.p.H_kv;
   p.qk_scale = pa.p.scale * pa.k_gain * kLog2e;
@@ -475,8 +401,15 @@ cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, flo
   // tokens of a block: one as long as the call can be a token per sequence
   p.gb = (p.group + 15) / 16;
   p.nt = pa.p.T <= pa.p.B ? 1 : std::max(1, 16 / p.group);
-  if (p.nt * p.group <= 8) return pa.p.D == 128 ? launch<128, 1>(p, stream) : launch<64, 1>(p, stream);
-  return pa.p.D == 128 ? launch<128, 2>(p, stream) : launch<64, 2>(p, stream);
+  auto of_pages = [&](auto dim, auto nt) {
+    constexpr int kDim = decltype(dim)::value, NT = decltype(nt)::value;
+    return pa.p.P == 16 ? launch<kDim, NT, true>(p, stream) : launch<kDim, NT, false>(p, stream);
+  };
+  auto of_columns = [&](auto dim) {
+    return p.nt * p.group <= 8 ? of_pages(dim, std::integral_constant<int, 1>())
+                               : of_pages(dim, std::integral_constant<int, 2>());
+  };
+  return pa.p.D == 128 ? of_columns(std::integral_constant<int, 128>()) : of_columns(std::integral_constant<int, 64>());
 }
 
 }  // namespace sa

@@ -67,6 +67,19 @@ __device__ __forceinline__ void cp_async16_plain(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
+// The same to a 32-bit shared address, of `bytes` (16, or 0: zeros, and nothing is read).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// The copies this thread issued since its last commit form a group; cp_async_wait
+// returns once at most N of its groups are incomplete.
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // MN-major 128-byte-swizzled operand: rows = K (8-row atoms 1024 B apart), 64 M
 // or N values per row, blocks of 64 of them `lbo` bytes apart.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
