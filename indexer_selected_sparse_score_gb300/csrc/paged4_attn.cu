@@ -47,18 +47,20 @@ using namespace umma;
 
 
 constexpr int kTile = 128;               // slots per tile: the grain of the work's division
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 2;            // 16 warps of 128 registers
+// Warps of a CTA: with two CTAs per SM, 128 registers each for 8 of them and 168 for 6
+// (O of 16 columns of 128 alone is 64)
+template <int kDim, int NT>
+constexpr int warps_of() {
+  return kDim == 128 && NT == 2 ? 6 : 8;
+}
+constexpr int kCtasPerSm = 2;
 constexpr int kGroup = 32;               // slots of a warp's step
 constexpr int kStages = 3;               // groups that a warp has in its ring
-#ifndef SA4_LEAST
-#define SA4_LEAST 2
-#endif
-constexpr int kLeast = SA4_LEAST;                // tiles of a CTA, at least
+constexpr int kLeast = 2;                // tiles of a CTA, at least
 
 template <int kDim, int NT>
 struct AttnSmem {
+  static constexpr int kWarps = warps_of<kDim, NT>();
   static constexpr uint32_t kCodes = kGroup * kDim / 2, kScales = kGroup * kDim / 16;  // of a group
   static constexpr uint32_t kStage = 2 * (kCodes + kScales);
   static constexpr uint32_t kRing = kStages * kStage;  // of a warp; at a part's end it holds its O, [D / 4][32] fp32
@@ -106,9 +108,10 @@ __device__ __forceinline__ void store_columns(const float (&o)[4], const float (
 }
 
 template <int kDim, int NT, bool kSmall>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(32 * warps_of<kDim, NT>(), kCtasPerSm)
 attn4_kernel(const Attn4Params p) {
   using L = AttnSmem<kDim, NT>;
+  constexpr int kWarps = L::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   UnitStart *start = reinterpret_cast<UnitStart *>(smem + L::start);
   volatile int *last_s = reinterpret_cast<volatile int *>(smem + L::flag);  // whether this CTA merges a unit's parts
@@ -371,7 +374,7 @@ cudaError_t launch(const Attn4Params &p, cudaStream_t stream) {
   static bool done[64] = {};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), AttnSmem<kDim, NT>::total, done);
   if (e != cudaSuccess) return e;
-  return launch_ex(false, kern, dim3(grid_of()), dim3(kThreads), AttnSmem<kDim, NT>::total, stream, 1, p);
+  return launch_ex(false, kern, dim3(grid_of()), dim3(32 * warps_of<kDim, NT>()), AttnSmem<kDim, NT>::total, stream, 1, p);
 }
 
 size_t most_parts() { return 2 * static_cast<size_t>(grid_of()); }
