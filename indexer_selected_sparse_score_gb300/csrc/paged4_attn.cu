@@ -84,7 +84,7 @@ struct Attn4Params {
   float *part;         // [2 grid][NT][D / 4][32]
   float2 *ml;          // [2 grid][16]: reference (log2 units), sum
   uint32_t *counters;  // [grid], 0 between calls
-  int group, gb, nt;   // query heads of a KV head, their parts, tokens of a block
+  int group, nt;       // query heads of a KV head, tokens of a block (group * nt <= 16)
   float qk_scale, v_gain;
   uint32_t *status;
 };
@@ -119,8 +119,7 @@ attn4_kernel(const Attn4Params p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long long x0, x1;
   int ctas;
-  const int heads = pv.H_kv * p.gb;
-  find_units(pv, p.nt, heads, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
+  find_units(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
   __syncthreads();
   if (x0 >= x1) return;
   const long long total = start->total;
@@ -135,14 +134,14 @@ attn4_kernel(const Attn4Params p) {
   Columns<kDim, NT> a;
 
   // Every warp walks the CTA's units by itself: lane l holds token l of a block.
-  int block = start->block, hv = start->head, kt0 = start->tile;
+  int block = start->block, hk = start->head, kt0 = start->tile;
   const int skip_to = start->t0;  // units of the first block before this token are not of this CTA
   long long x = x0;
   int t_seq = -1, t_pos = -1, n_seq = -1, n_pos = -1;
   auto load_block = [&](int i, int &seq, int &pos) {
     const int64_t t = static_cast<int64_t>(i) * p.nt + lane;
     const bool in = lane < p.nt && t < pv.T;
-    seq = in ? pv.q_seq[t] : INT_MIN;
+    seq = in ? pv.q_seq[t] : -1;
     pos = in ? pv.q_pos[t] : -1;
   };
   load_block(block, n_seq, n_pos);
@@ -150,11 +149,11 @@ attn4_kernel(const Attn4Params p) {
     t_seq = n_seq;
     t_pos = n_pos;
     load_block(block + 1, n_seq, n_pos);
-    const bool in = t_seq != INT_MIN;
+    const int count = static_cast<int>(min(static_cast<int64_t>(p.nt), pv.T - static_cast<int64_t>(block) * p.nt));
+    const bool in = lane < count;
     const bool valid = in && t_seq >= 0 && t_seq < pv.B && t_pos >= 0 && (t_pos >> pv.logP) < pv.max_pages;
     const int prev = __shfl_up_sync(0xffffffffu, t_seq, 1);
     uint32_t starts = __ballot_sync(0xffffffffu, in && (lane == 0 || t_seq != prev));
-    const int count = __popc(__ballot_sync(0xffffffffu, in));
     while (starts && x < x1) {
       const int l0 = __ffs(starts) - 1;
       starts &= starts - 1;
@@ -167,8 +166,8 @@ attn4_kernel(const Attn4Params p) {
       const int cost = (last + kTile) / kTile;
       if (cost == 0) continue;
       const int seq = __shfl_sync(0xffffffffu, t_seq, l0);
-      for (; hv < heads && x < x1; ++hv, kt0 = 0) {
-        const int hk = hv / p.gb, g0 = 16 * (hv - hk * p.gb), ng = min(16, p.group - g0), h0 = hk * p.group + g0;
+      for (; hk < pv.H_kv && x < x1; ++hk, kt0 = 0) {
+        const int ng = p.group, h0 = hk * ng;
         const int ncols = (l1 - l0) * ng;
         const long long u0 = x - kt0, u1 = u0 + cost;
         const int c0 = u0 < x0 ? cta_of_tile(u0, total, ctas) : blockIdx.x;
@@ -361,7 +360,7 @@ attn4_kernel(const Attn4Params p) {
         }
         __syncthreads();  // (the next part's copies land where O was)
       }
-      if (hv == heads) hv = 0;
+      if (hk == pv.H_kv) hk = 0;
     }
   }
 }
@@ -380,15 +379,26 @@ cudaError_t launch(const Attn4Params &p, cudaStream_t stream) {
 size_t most_parts() { return 2 * static_cast<size_t>(grid_of()); }
 size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// Query columns that a call's units have in common keys: heads of a KV head times the
+// tokens that a sequence has on average (one, where every sequence can have its own).
+int columns_of(const sa_paged4_args &pa) {
+  const int64_t each = (pa.p.T + static_cast<int64_t>(pa.p.B) - 1) / pa.p.B;
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(each, 1) * (pa.p.H / pa.p.H_kv), 1 << 20));
+}
+
 }  // namespace
 
 size_t attn4_scratch(const sa_paged4_args &pa) {
+  if (columns_of(pa) > 16) return attn4_umma_scratch(pa);
   return round_up(sizeof(float) * most_parts() * 16 * pa.p.D) + round_up(sizeof(float2) * most_parts() * 16);
 }
 
 cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, float *lse, void *scratch,
                          uint32_t *counters, uint32_t *status, cudaStream_t stream) {
   if (pa.p.T == 0) return cudaSuccess;
+  const int columns = columns_of(pa);
+  if (columns > 16)
+    return launch_attn4_umma(pa, q, out, lse, columns > 128 ? 256 : 128, scratch, counters, status, stream);
   Attn4Params p;
   p.c = paged4_view(pa);
   p.q = static_cast<const uint16_t *>(q);
@@ -402,8 +412,7 @@ cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, flo
   p.v_gain = pa.v_gain;
   p.status = status;
   // tokens of a block: one as long as the call can be a token per sequence
-  p.gb = (p.group + 15) / 16;
-  p.nt = pa.p.T <= pa.p.B ? 1 : std::max(1, 16 / p.group);
+  p.nt = pa.p.T <= pa.p.B ? 1 : 16 / p.group;
   auto of_pages = [&](auto dim, auto nt) {
     constexpr int kDim = decltype(dim)::value, NT = decltype(nt)::value;
     return pa.p.P == 16 ? launch<kDim, NT, true>(p, stream) : launch<kDim, NT, false>(p, stream);

@@ -1,0 +1,807 @@
+// Attention of many query columns (tokens x heads of a KV head, up to 256) over a
+// cache held in 4 bits, on the 5th-generation tensor cores.
+//
+//   S = Q K^T   M = 128 rows, N = 128 keys, K = D; a softmax thread owns a row
+//   P           fp16, written over S in tensor memory (the A operand of P V)
+//   O += P V    M = 128 rows, N = D, K = 128 keys, V read MN-major
+// Four warps turn codes into fp16 tiles in the 128-byte swizzle: they copy the codes
+// of the next tiles asynchronously (a warp the rows that it converts, so copies need
+// no barrier), multiply by the blocks' scales and store.  A tile costs them about
+// 350 issue slots a scheduler, the products 512 clocks each for 128 rows: the
+// conversion hides behind the products of 256 rows and nearly behind those of 128.
+//
+// Two streams of products take turns on the tensor cores, each with a softmax
+// warpgroup and an issuing warp:
+//   two row tiles (units of up to 256 rows: chunks of a prompt): both meet every key
+//   tile, so a tile is converted once for 256 rows;
+//   one row tile (up to 128: a few tokens or one, of many heads): both hold the same
+//   rows, and key tiles go to them in turn; their sums and O are joined at the end.
+// A row's logits are taken relative to a reference that is raised (and O rescaled)
+// when one passes it by 2^14; weights are then at most 2^14, normal in fp16 down to
+// 2^-28 of the largest.
+//
+// Work: paged4_units.cuh, units cut evenly over one CTA per SM; what has to be
+// joined goes to scratch, and the CTA that adds a unit's last part (a counter)
+// merges its rows in order.
+#include <cfloat>
+#include <climits>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "paged4_mma.cuh"
+#include "paged4_units.cuh"
+#include "paged_list.h"
+#include "paged_umma.cuh"
+
+namespace sa {
+namespace {
+
+using namespace umma;
+
+constexpr int kTile = 128;
+constexpr int kThreads = 512;
+constexpr int kWarpMma = 12;   // and 13: the issuers (14 and 15 only join the block barriers)
+constexpr int kWarpCopy = 8;   // .. 11
+constexpr int kLeast = 2;      // tiles of a CTA, at least
+constexpr int kInfos = 8;
+// Registers per thread: 512 threads start with 128 each; the softmax warpgroups
+// raise their limit, the others lower theirs: 2 * 176 + 104 + 56 = 4 * 128.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 176, kCopyRegs = 104, kOtherRegs = 56;
+static_assert(2 * kSoftmaxRegs + kCopyRegs + kOtherRegs <= 4 * kLaunchRegs, "register split exceeds the launch allocation");
+
+struct TileInfo {
+  int t0, n, hk;     // unit: first token, tokens, KV head
+  int base;          // first slot
+  int low, last;     // lowest and highest slot of the unit's valid tokens
+  uint32_t have;     // bit j: slots 16 j .. of the tile are in a page
+  int first, end;    // first, last tile of this CTA's part of the unit
+  int c0, c1;        // CTAs that share the unit
+  int tiles;         // of the part
+  int part;          // parts of this CTA before
+  int pad;
+};
+
+template <int kDim, bool kTwo>
+struct UmmaSmem {
+  static constexpr int kRowTiles = kTwo ? 2 : 1;
+  static constexpr int kSlots = (kDim == 128 ? (kTwo ? 3 : 4) : 6);  // fp16 tiles: K(0), V(0), K(1), ..
+  static constexpr int kStages = kDim == 128 ? 3 : 4;                // tiles of codes
+  static constexpr uint32_t kBlock = kTile * 128;
+  static constexpr uint32_t kKv = kBlock * (kDim / 64);
+  static constexpr uint32_t kCodes = 32 * kDim / 2, kScales = 32 * kDim / 16;  // of a warp's rows
+  static constexpr uint32_t kStage = 2 * (kCodes + kScales);
+  static constexpr size_t q = 0;                                     // [row tile][D / 64][128 rows][128 B]
+  static constexpr size_t kv = q + kRowTiles * kKv;
+  static constexpr size_t codes = kv + kSlots * kKv;                 // [warp][stage]
+  static constexpr size_t info = codes + 4 * kStages * kStage;
+  static constexpr size_t factor = info + kInfos * sizeof(TileInfo); // [row tile][128] of the logits
+  static constexpr size_t poison = factor + kRowTiles * 512;         // [kInfos][4 warps][8]
+  static constexpr size_t bars = poison + kInfos * 4 * 8 * 4;
+  static constexpr int kBars = 2 * kSlots + 2 * kInfos + 2 + 2 + 4 + 2 + 2 + 2 + 1;
+  static constexpr size_t scan = bars + kBars * 8;
+  static constexpr size_t start = scan + 32 * 8;
+  static constexpr size_t misc = start + sizeof(UnitStart);
+  static constexpr size_t total = misc + 16;
+  static_assert(total + 1024 <= 232448, "shared memory budget");
+  static_assert(sizeof(TileInfo) % 8 == 0 && bars % 8 == 0 && start % 8 == 0, "alignment");
+};
+
+struct UmmaParams {
+  Paged4View c;
+  const uint16_t *q;
+  __nv_bfloat16 *out;
+  float *lse;
+  float *part;         // [slot][stream][128][D]
+  float2 *ml;          // [slot][stream][128]: reference (log2 units, -inf: nothing), sum
+  uint32_t *counters;  // [grid], 0 between calls
+  int group, nt;
+  float qk_scale, v_gain;
+  uint32_t *status;
+};
+
+__device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int kDim, bool kTwo>
+__global__ void __launch_bounds__(kThreads, 1)
+umma4_kernel(const UmmaParams p) {
+  using L = UmmaSmem<kDim, kTwo>;
+  constexpr int kSlots = L::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *qs = smem + L::q, *kvs = smem + L::kv;
+  TileInfo *infos = reinterpret_cast<TileInfo *>(smem + L::info);
+  float *factor = reinterpret_cast<float *>(smem + L::factor);
+  int *poison = reinterpret_cast<int *>(smem + L::poison);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
+  uint64_t *full = bars, *empty = full + kSlots, *ifull = empty + kSlots, *iempty = ifull + kInfos;
+  uint64_t *qfull = iempty + kInfos, *sfull = qfull + 2;
+  uint64_t *pfull = sfull + 2, *ofull = pfull + 4, *turn = ofull + 2, *done = turn + 2, *meet = done + 2;  // pfull: [stream][half]
+  UnitStart *start = reinterpret_cast<UnitStart *>(smem + L::start);
+  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
+  volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 4);
+  volatile int *last_s = reinterpret_cast<volatile int *>(smem + L::misc + 8);
+  const PagedView &pv = p.c.v;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&full[i], 4);
+      mbar_init(&empty[i], kTwo ? 2 : 1);
+    }
+    for (int i = 0; i < kInfos; ++i) {
+      mbar_init(&ifull[i], 1);
+      mbar_init(&iempty[i], 10);  // two issuers, eight softmax warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 4);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[2 * i], 4);
+      mbar_init(&pfull[2 * i + 1], 4);
+      mbar_init(&ofull[i], 1);
+      mbar_init(&turn[i], 1);
+      mbar_init(&done[i], 1);
+    }
+    mbar_init(meet, 8);
+    *abort_s = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(tmem_base_s, 512);
+    tmem_relinquish();
+  }
+  long long x0, x1;
+  int ctas;
+  find_units(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_s;
+  const long long total = start->total;
+  const long long tiles = x1 - x0;
+  auto fail = [&]() {
+    raise_flag(p.status, kFlagTimeout);
+    *abort_s = 1;
+  };
+
+  if (warp >= kWarpMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < kWarpMma + 2) {
+      // ---------------------------------------------- issuer of one stream
+      const int w = warp - kWarpMma;
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = idesc_f16(128, kTile);
+      constexpr uint32_t idesc_o = idesc_f16(128, kDim) | (1u << 16);  // V is MN-major
+      const uint32_t ts = tmem + 128 * w, to = tmem + 256 + 128 * w;
+      const uint64_t dq = desc_sw128_kmajor(smem_u32(qs + (kTwo ? w : 0) * L::kKv));
+      bool ok = true, two = false, live = true;
+      int qn = 0, ln = 0, turns = 0, in_part = 0;
+      auto take_turn = [&]() -> bool {
+        if (!two) return true;
+        const int k = turns++;
+        return w == 0 ? k == 0 || mbar_wait_warp(&turn[1], (k - 1) & 1) : mbar_wait_warp(&turn[0], k & 1);
+      };
+      auto wait_full = [&](int m) { return mbar_wait_warp(&full[m % kSlots], (m / kSlots) & 1); };
+      auto issue_s = [&](int m) {
+        if (leader) {
+          const uint64_t db = desc_sw128_kmajor(smem_u32(kvs + (m % kSlots) * L::kKv));
+#pragma unroll
+          for (int kk = 0; kk < kDim / 16; ++kk) {
+            const uint64_t o = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+            mma_f16(ts, dq + o, db + o, idesc_s, kk > 0);
+          }
+          mma_commit(&sfull[w]);
+          mma_commit(&empty[m % kSlots]);
+        }
+      };
+      auto issue_o = [&](int m, int half, bool fresh) {
+        if (leader) {
+          const uint64_t dv = desc_mn(smem_u32(kvs + (m % kSlots) * L::kKv), L::kBlock);
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            mma_f16_tmem_a(to, ts + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, !(fresh && kk == 0));
+        }
+      };
+      for (int n = 0; n < tiles; ++n) {
+        if (!mbar_wait_warp(&ifull[n % kInfos], (n / kInfos) & 1)) {
+          ok = false;
+          break;
+        }
+        const int mk = 2 * n, mv = mk + 1;
+        const bool part_first = infos[n % kInfos].first, part_end = infos[n % kInfos].end;
+        const int rows = infos[n % kInfos].n * p.group, count = infos[n % kInfos].tiles;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&iempty[n % kInfos]);
+        if constexpr (kTwo) {
+          if (part_first) {
+            two = rows > 128;
+            live = w == 0 || two;
+          }
+          if (!live) {  // only frees the ring
+            ok = wait_full(mk);
+            if (ok && leader) mbar_arrive(&empty[mk % kSlots]);
+            ok = ok && wait_full(mv);
+            if (!ok) break;
+            if (leader) mbar_arrive(&empty[mv % kSlots]);
+            __syncwarp();
+            continue;
+          }
+          if (part_first) {
+            ok = wait_full(mk) && mbar_wait_warp(&qfull[w], (qn++) & 1) && take_turn();
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(mk);
+            if (leader && two) mbar_arrive(&turn[w]);
+            __syncwarp();
+          }
+          ok = wait_full(mv) && (part_end || wait_full(mv + 1)) && mbar_wait_warp(&pfull[2 * w], ln & 1) && take_turn();
+          if (!ok || *abort_s) break;
+          tc_fence_after();
+          issue_o(mv, 0, part_first);
+          ok = mbar_wait_warp(&pfull[2 * w + 1], ln & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_o(mv, 1, false);
+          if (leader) {
+            if (part_end) mma_commit(&ofull[w]);
+            mma_commit(&empty[mv % kSlots]);
+          }
+          if (!part_end) issue_s(mv + 1);
+          if (leader && two) mbar_arrive(&turn[w]);
+          __syncwarp();
+          ++ln;
+        } else {
+          // tiles of a part go to the streams in turn
+          if (part_first) in_part = 0;
+          const int j = in_part++;
+          if ((j & 1) != w) continue;
+          ok = wait_full(mk) && (j >= 2 || mbar_wait_warp(&qfull[w], (qn++) & 1));
+          if (!ok || *abort_s) break;
+          tc_fence_after();
+          issue_s(mk);
+          __syncwarp();
+          ok = wait_full(mv) && mbar_wait_warp(&pfull[2 * w], ln & 1);
+          if (!ok || *abort_s) break;
+          tc_fence_after();
+          issue_o(mv, 0, j < 2);
+          ok = mbar_wait_warp(&pfull[2 * w + 1], ln & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_o(mv, 1, false);
+          if (leader) {
+            if (j + 2 >= count) mma_commit(&ofull[w]);
+            mma_commit(&empty[mv % kSlots]);
+          }
+          __syncwarp();
+          ++ln;
+        }
+      }
+      if (!ok && lane == 0) fail();
+      if (leader && tiles > 0) {
+        mma_commit(&done[w]);
+        if (!mbar_wait(&done[w], 0)) raise_flag(p.status, kFlagTimeout);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kWarpCopy) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+    // ------------------------- codes in, fp16 tiles out: rows 32 cw .. 32 cw + 31
+    const int cw = warp - kWarpCopy;
+    uint8_t *codes = smem + L::codes + cw * L::kStages * L::kStage;
+    const uint32_t codes_s = smem_u32(codes);
+    bool ok = true;
+    int block = start->block, hv = start->head, kt0 = start->tile;
+    long long x = x0;
+    int n = 0, part = 0;
+    // first token of the block that is not yet in a unit (before `start` they are other CTAs')
+    int i0 = x0 < x1 ? static_cast<int>(start->t0 - static_cast<int64_t>(block) * p.nt) : 0;
+    while (ok && x < x1 && static_cast<int64_t>(block) * p.nt < pv.T) {
+      const int in_block = static_cast<int>(min(static_cast<int64_t>(p.nt), pv.T - static_cast<int64_t>(block) * p.nt));
+      while (ok && x < x1 && i0 < in_block) {
+        // the unit that begins at token i0
+        const int t0 = block * p.nt + i0;
+        const int seq = pv.q_seq[t0];
+        int last = -1, low = INT_MAX, len = 0;
+        for (bool more = true; more;) {
+          const int l = i0 + len + lane;
+          const bool in = l < in_block;
+          const int b = in ? pv.q_seq[block * p.nt + l] : 0, pos = in ? pv.q_pos[block * p.nt + l] : -1;
+          const uint32_t other = __ballot_sync(0xffffffffu, !in || b != seq);
+          const int take = other ? __ffs(other) - 1 : 32;
+          const bool valid = lane < take && b >= 0 && b < pv.B && pos >= 0 && (pos >> pv.logP) < pv.max_pages;
+          last = max(last, __reduce_max_sync(0xffffffffu, valid ? pos : -1));
+          low = min(low, __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX));
+          len += take;
+          more = take == 32;
+        }
+        i0 += len;
+        const int cost = (last + kTile) / kTile;
+        if (cost == 0) continue;
+        for (; ok && hv < pv.H_kv && x < x1; ++hv, kt0 = 0) {
+          const long long u0 = x - kt0, u1 = u0 + cost;
+          const int c0 = u0 < x0 ? cta_of_tile(u0, total, ctas) : blockIdx.x;
+          const int c1 = u1 > x1 ? cta_of_tile(u1 - 1, total, ctas) : blockIdx.x;
+          const int kt1 = static_cast<int>(min(static_cast<long long>(cost), kt0 + (x1 - x))), count = kt1 - kt0;
+          x += count;
+          int *bad = poison + ((part % kInfos) * 4 + cw) * 8;
+          // lane l: the page of the l-th 16 slots of this warp's rows: two of each tile
+          auto load_ids = [&](int i) {
+            const int slot = kTile * (kt0 + i + (lane >> 1)) + 32 * cw + 16 * (lane & 1);
+            if (i + (lane >> 1) >= count || slot > last) return -1;
+            return load_page(pv, seq, slot >> pv.logP, p.status, true);
+          };
+          // (and of the first warp, lane j: the page of 16 slots j of the next tile, for
+          // the tile's description)
+          auto load_all = [&](int i) {
+            const int slot = kTile * (kt0 + i) + 16 * lane;
+            if (cw != 0 || lane >= 8 || i >= count || slot > last) return -1;
+            return load_page(pv, seq, slot >> pv.logP, nullptr, false);
+          };
+          int ids = load_ids(0), ids_next = -1, all = load_all(0);
+          auto copy = [&](int i) {
+            if (i < count) {
+              const int id0 = __shfl_sync(0xffffffffu, ids, (2 * i) & 31), id1 = __shfl_sync(0xffffffffu, ids, (2 * i + 1) & 31);
+              const uint32_t st = codes_s + (i % L::kStages) * L::kStage;
+              const int slot = kTile * (kt0 + i) + 32 * cw;
+              auto row_of = [&](int half) {
+                const int id = half ? id1 : id0;
+                return (static_cast<int64_t>(max(id, 0) * pv.H_kv + hv) << pv.logP) + ((slot + 16 * half) & (pv.P - 1)) -
+                       16 * half;
+              };
+              const int64_t row0 = row_of(0), row1 = row_of(1);
+              constexpr int kC = kDim / 32;  // 16-byte chunks of a row's codes
+              constexpr int kR = 32 / kC;    // rows of a load
+              const int r = lane / kC, ch = lane % kC;
+#pragma unroll
+              for (int e = 0; e < 32; e += kR) {
+                const int64_t row = (e < 16 ? row0 : row1) + e + r;
+                const uint32_t bytes = (e < 16 ? id0 : id1) >= 0 ? 16u : 0u;
+                // chunks of a row swapped so that eight rows' reads meet no bank twice
+                const int sw = kDim == 128 ? ch ^ ((e + r) >> 1 & 3) : ch ^ ((e + r) >> 2 & 1);
+                const uint32_t to = st + (e + r) * (kDim / 2) + 16 * sw;
+                cp_async16_or_zero(to, p.c.K + row * (kDim / 2) + 16 * ch, bytes);
+                cp_async16_or_zero(to + L::kCodes, p.c.V + row * (kDim / 2) + 16 * ch, bytes);
+              }
+              constexpr int kSc = 2 * kDim / 16;  // chunks of the scales of 32 rows
+              if (lane < 2 * kSc) {
+                const int c = lane % kSc, half = c >= kSc / 2;
+                cp_async16_or_zero(st + 2 * L::kCodes + 16 * lane,
+                                   (lane < kSc ? p.c.Ks : p.c.Vs) + (half ? row1 : row0) * (kDim / 16) + 16 * c,
+                                   (half ? id1 : id0) >= 0 ? 16u : 0u);
+              }
+            }
+            cp_async_commit();
+          };
+#pragma unroll
+          for (int i = 0; i < L::kStages - 1; ++i) copy(i);
+          if (lane < 8) bad[lane] = INT_MAX;
+          __syncwarp();
+          for (int i = 0; i < count && ok; ++i, ++n) {
+            const int ahead = i + L::kStages - 1;
+            if ((ahead & 15) == 0) ids = ids_next;
+            cp_async_wait<L::kStages - 2>();
+            __syncwarp();
+            copy(ahead);  // (into the stage that the tile before was read from)
+            if ((ahead & 15) == 4) ids_next = load_ids(ahead - 4 + 16);
+            if (cw == 0) {
+              const uint32_t have = __ballot_sync(0xffffffffu, all >= 0);
+              all = load_all(i + 1);
+              if (!mbar_wait_warp(&iempty[n % kInfos], ((n / kInfos) & 1) ^ 1) || *abort_s) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) {
+                infos[n % kInfos] = TileInfo{t0, len, hv, kTile * (kt0 + i), low, last, have, i == 0, i + 1 == count,
+                                             c0, c1, count, part, 0};
+                mbar_arrive(&ifull[n % kInfos]);
+              }
+            }
+            const uint8_t *st = codes + (i % L::kStages) * L::kStage;
+            const int slot = kTile * (kt0 + i) + 32 * cw + lane;
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+              const int m = 2 * n + kv;
+              // this lane's row: its scales, zero past the unit's last slot
+              uint32_t sc[kDim / 64];
+              const uint8_t *ss = st + 2 * L::kCodes + kv * L::kScales + lane * (kDim / 16);
+              if constexpr (kDim == 128)
+                *reinterpret_cast<uint2 *>(sc) = *reinterpret_cast<const uint2 *>(ss);
+              else
+                sc[0] = *reinterpret_cast<const uint32_t *>(ss);
+              if (slot > last) {
+#pragma unroll
+                for (int e = 0; e < kDim / 64; ++e) sc[e] = 0;
+              } else if (kv == 1 && slot > low) {
+#pragma unroll
+                for (int e = 0; e < kDim / 16; ++e)
+                  if (e4m3_is_nan((sc[e >> 2] >> (8 * (e & 3))) & 0xFFu)) {
+                    sc[e >> 2] &= ~(0xFFu << (8 * (e & 3)));
+                    atomicMin(&bad[e], slot);
+                  }
+              }
+              const uint4 *cd = reinterpret_cast<const uint4 *>(st + kv * L::kCodes + lane * (kDim / 2));
+              const int sw = kDim == 128 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+              uint4 c[kDim / 32];
+#pragma unroll
+              for (int e = 0; e < kDim / 32; ++e) c[e] = cd[e ^ sw];
+              if (!mbar_wait_warp(&empty[m % kSlots], ((m / kSlots) & 1) ^ 1) || *abort_s) {
+                ok = false;
+                break;
+              }
+              uint8_t *dst = kvs + (m % kSlots) * L::kKv;
+              const int row = 32 * cw + lane;
+#pragma unroll
+              for (int e = 0; e < kDim / 32; ++e) {
+                const __half2 two = e4m3x2_to_half2(sc[e >> 1] >> (16 * (e & 1)));
+                const uint32_t words[4] = {c[e].x, c[e].y, c[e].z, c[e].w};
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) {
+                  const __half2 s2 = i4 < 2 ? __low2half2(two) : __high2half2(two);
+                  __half2 d[4];
+                  e2m1x8_to_half2(words[i4], d);
+                  *reinterpret_cast<uint4 *>(dst + (e >> 1) * L::kBlock + sw128_offset(row, 64 * (e & 1) + 16 * i4)) =
+                      make_uint4(as_u32(__hmul2(d[0], s2)), as_u32(__hmul2(d[1], s2)), as_u32(__hmul2(d[2], s2)),
+                                 as_u32(__hmul2(d[3], s2)));
+                }
+              }
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&full[m % kSlots]);
+            }
+          }
+          ++part;
+          cp_async_wait<0>();
+          __syncwarp();
+        }
+        if (hv == pv.H_kv) hv = 0;
+      }
+      ++block;
+      i0 = 0;
+    }
+    cp_async_wait<0>();
+    if (!ok && lane == 0) fail();
+  } else {
+    // ------------------------------------------------- softmax of one stream
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
+    uint8_t *qt = qs + (kTwo ? w : 0) * L::kKv;
+    float *fac = factor + (kTwo ? w : 0) * 128;
+    float ref = 0.f, l = 0.f, cs = 0.f;
+    int ln = 0, pieces = 0, in_part = 0, met = 0, lim = -1, r = 0;
+    bool ok = true, live = true, idle = false;
+    auto sync = [&]() {  // of the softmax warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet);
+      ok = mbar_wait_warp(meet, (met++) & 1) && ok;
+    };
+    int qn = 0;
+    for (int n = 0; n < tiles; ++n) {
+      ok = mbar_wait_warp(&ifull[n % kInfos], (n / kInfos) & 1);
+      if (!ok || *abort_s) break;
+      const TileInfo ti = infos[n % kInfos];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[n % kInfos]);
+      const int rows = ti.n * p.group;
+      bool mine = true;  // this stream has the tile
+      if (ti.first) {
+        in_part = 0;
+        l = 0.f;
+        ref = 0.f;
+        live = kTwo ? w == 0 || rows > 128 : w == 0 || ti.tiles > 1;
+        r = (kTwo ? 128 * w : 0) + row;
+        if (live) {
+          // the row's token and limit
+          const int i = r / p.group;
+          lim = -1;
+          if (r < rows) {
+            const int pos = pv.q_pos[ti.t0 + i];
+            if (pos >= 0 && (pos >> pv.logP) < pv.max_pages) lim = pos;
+          }
+          if (kTwo || w == 0) {
+            // the warp's 32 query rows as fp16, each scaled by a power of two, into the
+            // K-major swizzled layout; a load covers whole rows
+            constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;
+            const int ch = lane % kLanes;
+            const int rw = (kTwo ? 128 * w : 0) + 32 * (warp & 3);
+            uint8_t *dst = qt + (ch >> 3) * L::kBlock;
+#pragma unroll 4
+            for (int e = 0; e < 32; e += kPer) {
+              const int rr = rw + e + lane / kLanes, tt = rr / p.group;
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (rr < rows)
+                v = reinterpret_cast<const uint4 *>(
+                    p.q + (static_cast<int64_t>(ti.t0 + tt) * pv.H + ti.hk * p.group + rr - tt * p.group) * kDim)[ch];
+              uint32_t u[4] = {v.x, v.y, v.z, v.w};
+              float top = 0.f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+#pragma unroll
+              for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const float f = to_half_factor(top);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                u[j] = as_u32(__floats2half2_rn(__uint_as_float(u[j] << 16) * f, __uint_as_float(u[j] & 0xFFFF0000u) * f));
+              *reinterpret_cast<uint4 *>(dst + sw128_offset(rr - (kTwo ? 128 * w : 0), 16u * (ch & 7))) =
+                  make_uint4(u[0], u[1], u[2], u[3]);
+              if (ch == 0) fac[rr - (kTwo ? 128 * w : 0)] = p.qk_scale / f;
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&qfull[w]);
+              if (!kTwo && ti.tiles > 1) mbar_arrive(&qfull[1]);
+            }
+          }
+          if (!kTwo && w == 1) {
+            // (the other stream's warps stage the rows that both hold)
+            ok = mbar_wait_warp(&qfull[1], (qn++) & 1);
+            if (!ok) break;
+          }
+          cs = fac[row];
+          idle = !__any_sync(0xffffffffu, lim >= 0);
+        }
+      }
+      if constexpr (!kTwo) mine = (in_part & 1) == w;
+      ++in_part;
+      const bool part_end = ti.end;
+      if (live && mine) {
+        const bool first = kTwo ? ti.first : in_part <= 2;
+        const bool mine_end = kTwo ? part_end : in_part + 2 > ti.tiles;
+        ok = mbar_wait_warp(&sfull[w], ln & 1);
+        if (!ok || *abort_s) break;
+        tc_fence_after();
+        if (idle) {  // (its rows' weights and O may be anything)
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&pfull[2 * w]);
+            mbar_arrive(&pfull[2 * w + 1]);
+          }
+        } else {
+        float v[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_load(ts + 32 * i, reinterpret_cast<uint32_t(&)[32]>(v[32 * i]));
+        tmem_ld_wait();
+        const bool masked = ti.have != 0xFFu || ti.base + kTile - 1 > ti.low;
+        const bool fresh = l == 0.f && lim >= 0;
+        float2 *v2 = reinterpret_cast<float2 *>(v);
+        const float2 cs2 = make_float2(cs, cs), nref2 = make_float2(-ref, -ref);
+#pragma unroll
+        for (int e = 0; e < 64; ++e) v2[e] = fma2(v2[e], cs2, nref2);
+        if (masked) {
+          const int d = lim - ti.base;  // the row's last slot in the tile
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (e > d || !((ti.have >> (e >> 4)) & 1u)) v[e] = -INFINITY;
+        }
+        float top;
+        {
+          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 64; ++e) t4[e & 3] = max3(t4[e & 3], v2[e].x, v2[e].y);
+          top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+        }
+        if (__any_sync(0xffffffffu, fresh || top > kRefTop)) {
+          // the row's first keys, or a logit passes its reference: set or raise it; the
+          // sum and O (which holds the products up to the tile before) shrink in step
+          const float up = top == -INFINITY ? 0.f : fresh || top > kRefTop ? top - kRefHead : 0.f;
+          const float2 nup2 = make_float2(-up, -up);
+          ref += up;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) v2[e] = add2(v2[e], nup2);
+          if (!first) {
+            const float f = exp2f(fminf(-up, 0.f));
+            l *= f;
+#pragma unroll 1
+            for (int i = 0; i < kDim / 16; ++i) {
+              uint32_t o[16];
+              tmem_load(to + 16 * i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_store(to + 16 * i, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float2 y = v2[32 * half + e];
+            const float2 w2 = make_float2(exp2_hw(y.x), exp2_hw(y.y));
+            sum[e & 1] = add2(sum[e & 1], w2);
+            pk[e] = as_u32(__floats2half2_rn(w2.x, w2.y));
+          }
+          tmem_store(ts + 32 * half, pk);
+          tmem_store(ts + 32 * half + 16, pk + 16);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[2 * w + half]);
+        }
+        const float2 sum2 = add2(sum[0], sum[1]);
+        l += sum2.x + sum2.y;
+        }
+        ++ln;
+        if (mine_end) {
+          ok = mbar_wait_warp(&ofull[w], pieces & 1);
+          if (!ok) break;
+          ++pieces;
+          tc_fence_after();
+        }
+      }
+      if (!part_end) continue;
+      // ------------------------------------------------- the part is done
+      const bool cut = ti.c0 != ti.c1, joined = cut || !kTwo;
+      const int64_t slot = 3 * static_cast<int64_t>(blockIdx.x) +
+                           (!cut ? 2 : ti.c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
+      const int64_t at = (slot * 2 + w) * 128 + row;
+      const int *bad = poison + (ti.part % kInfos) * 32;
+      auto poisoned = [&](int blk) {
+        return lim >= min(min(bad[blk], bad[8 + blk]), min(bad[16 + blk], bad[24 + blk]));
+      };
+      const bool stored = live && r < rows && lim >= 0;
+      if (joined) __stcg(p.ml + at, live ? make_float2(l == 0.f ? -INFINITY : ref, l) : make_float2(-INFINITY, 0.f));
+      if (live) {
+        const float inv = l != 0.f ? p.v_gain / l : 0.f;
+        const int i = r / p.group;
+        const int64_t out_row = static_cast<int64_t>(ti.t0 + i) * pv.H + ti.hk * p.group + r - i * p.group;
+#pragma unroll 1
+        for (int blk = 0; blk < kDim / 16; ++blk) {
+          uint32_t o[16];
+          tmem_load(to + 16 * blk, o);
+          tmem_ld_wait();
+          if (stored) {
+            if (poisoned(blk)) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = 0x7FFFFFFFu;
+            }
+            if (joined) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                __stcg(reinterpret_cast<float4 *>(p.part + at * kDim + 16 * blk + e),
+                       make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                   __uint_as_float(o[e + 3])));
+            } else {
+              uint32_t b[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                b[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+              uint4 *dst = reinterpret_cast<uint4 *>(p.out + out_row * kDim + 16 * blk);
+              dst[0] = make_uint4(b[0], b[1], b[2], b[3]);
+              dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
+            }
+          }
+        }
+        if (!joined && stored && p.lse)
+          p.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
+        tc_fence_before();
+      }
+      if (!joined) continue;
+      __threadfence();
+      sync();
+      if (!ok) break;
+      bool merge = true;
+      if (cut) {
+        if (tid == 0) {
+          const uint32_t before = atomicAdd(&p.counters[ti.c0], 1u);
+          *last_s = before == static_cast<uint32_t>(ti.c1 - ti.c0);
+          if (*last_s) p.counters[ti.c0] = 0;  // for the next call
+          __threadfence();
+        }
+        sync();
+        if (!ok) break;
+        merge = *last_s;
+      }
+      if (merge) {
+        // rows warp, + 8, ..: the unit's parts and their streams in order
+        constexpr int V = kDim / 32;
+        const int subs = kTwo ? 1 : 2, count = (ti.c1 - ti.c0 + 1) * subs;
+        for (int rr = warp; rr < rows; rr += 8) {
+          const int i = rr / p.group, pos = pv.q_pos[ti.t0 + i];
+          if (pos < 0 || (pos >> pv.logP) >= pv.max_pages) continue;
+          float M = -INFINITY, sum = 0.f, acc[V] = {};
+          for (int k0 = 0; k0 < count; k0 += 4) {
+            float2 s[4];
+            float y[4][V];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = min(k0 + e, count - 1), c = ti.c0 + k / subs;
+              const int64_t sl = 3 * static_cast<int64_t>(c) + (!cut ? 2 : c == ti.c0 ? 1 : 0);
+              const int64_t a = (sl * 2 + (kTwo ? rr >> 7 : k % subs)) * 128 + (rr & 127);
+              s[e] = __ldcg(p.ml + a);
+              if constexpr (V == 4)
+                *reinterpret_cast<float4 *>(y[e]) = __ldcg(reinterpret_cast<const float4 *>(p.part + a * kDim + V * lane));
+              else
+                *reinterpret_cast<float2 *>(y[e]) = __ldcg(reinterpret_cast<const float2 *>(p.part + a * kDim + V * lane));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (k0 + e >= count || s[e].x == -INFINITY) continue;  // (nothing, and what lies there may be anything)
+              const float m = max_nan(M, s[e].x);
+              const float f0 = M == m ? 1.f : exp2f(M - m), f1 = s[e].x == m ? 1.f : exp2f(s[e].x - m);
+              M = m;
+              sum = sum * f0 + s[e].y * f1;
+#pragma unroll
+              for (int j = 0; j < V; ++j) acc[j] = acc[j] * f0 + y[e][j] * f1;
+            }
+          }
+          const int64_t out_row = static_cast<int64_t>(ti.t0 + i) * pv.H + ti.hk * p.group + rr - i * p.group;
+          const float inv = sum != 0.f ? p.v_gain / sum : 0.f;
+#pragma unroll
+          for (int j = 0; j < V; j += 2)
+            *reinterpret_cast<__nv_bfloat162 *>(p.out + out_row * kDim + V * lane + j) =
+                __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
+          if (lane == 0 && p.lse) p.lse[out_row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+        }
+      }
+      sync();  // (the next part writes its own rows where a merge may still read)
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) fail();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+int grid_of() { return std::min(sm_count(), kAttn4Counters); }
+
+template <int kDim, bool kTwo>
+cudaError_t launch(const UmmaParams &p, cudaStream_t stream) {
+  auto kern = umma4_kernel<kDim, kTwo>;
+  // the register split assumes kLaunchRegs registers per thread at launch; anything
+  // else could leave a raise waiting forever
+  static int regs = -1;
+  if (regs < 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void *>(kern));
+    if (e != cudaSuccess) return e;
+    regs = fa.numRegs;
+  }
+  if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  const size_t smem = UmmaSmem<kDim, kTwo>::total + 1024;
+  static bool done[64] = {};
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, done);
+  if (e != cudaSuccess) return e;
+  return launch_ex(false, kern, dim3(grid_of()), dim3(kThreads), smem, stream, 1, p);
+}
+
+}  // namespace
+
+size_t attn4_umma_scratch(const sa_paged4_args &pa) {
+  const size_t rows = static_cast<size_t>(grid_of()) * 3 * 2 * 128;
+  return round_up(rows * pa.p.D * sizeof(float)) + round_up(rows * sizeof(float2));
+}
+
+cudaError_t launch_attn4_umma(const sa_paged4_args &pa, const void *q, void *out, float *lse, int rows, void *scratch,
+                              uint32_t *counters, uint32_t *status, cudaStream_t stream) {
+  UmmaParams p;
+  p.c = paged4_view(pa);
+  p.q = static_cast<const uint16_t *>(q);
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  p.part = static_cast<float *>(scratch);
+  p.ml = reinterpret_cast<float2 *>(static_cast<char *>(scratch) +
+                                    round_up(static_cast<size_t>(grid_of()) * 3 * 2 * 128 * pa.p.D * sizeof(float)));
+  p.counters = counters;
+  p.group = pa.p.H / pa.p.H_kv;
+  p.nt = std::max(1, rows / p.group);
+  p.qk_scale = pa.p.scale * pa.k_gain * kLog2e;
+  p.v_gain = pa.v_gain;
+  p.status = status;
+  if (rows > 128) return pa.p.D == 128 ? launch<128, true>(p, stream) : launch<64, true>(p, stream);
+  return pa.p.D == 128 ? launch<128, false>(p, stream) : launch<64, false>(p, stream);
+}
+
+}  // namespace sa
