@@ -40,15 +40,16 @@ namespace {
 using namespace umma;
 
 constexpr int kTile = 128;
-constexpr int kThreads = 512;
-constexpr int kWarpMma = 12;   // and 13: the issuers (14 and 15 only join the block barriers)
-constexpr int kWarpCopy = 8;   // .. 11
+constexpr int kThreads = 640;
+constexpr int kWarpConv = 8;   // .. 11 convert keys, 12 .. 15 values (rows 32 i .. 32 i + 31 of a tile each)
+constexpr int kWarpMma = 16;   // and 17: the issuers
+constexpr int kWarpInfo = 18;  // describes the tiles (19 only joins the block barriers)
 constexpr int kLeast = 2;      // tiles of a CTA, at least
-constexpr int kInfos = 8;
-// Registers per thread: 512 threads start with 128 each; the softmax warpgroups
-// raise their limit, the others lower theirs: 2 * 176 + 104 + 56 = 4 * 128.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 176, kCopyRegs = 104, kOtherRegs = 56;
-static_assert(2 * kSoftmaxRegs + kCopyRegs + kOtherRegs <= 4 * kLaunchRegs, "register split exceeds the launch allocation");
+constexpr int kInfos = 8, kParts = 4;
+// Registers per thread: 640 threads start with 96 each; the softmax warpgroups raise
+// their limit, the last one lowers its own: 2 * 120 + 2 * 96 + 48 = 5 * 96.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 120, kOtherRegs = 48;
+static_assert(2 * kSoftmaxRegs + 2 * kLaunchRegs + kOtherRegs <= 5 * kLaunchRegs, "register split exceeds the launch allocation");
 
 struct TileInfo {
   int t0, n, hk;     // unit: first token, tokens, KV head
@@ -65,20 +66,21 @@ struct TileInfo {
 template <int kDim, bool kTwo>
 struct UmmaSmem {
   static constexpr int kRowTiles = kTwo ? 2 : 1;
-  static constexpr int kSlots = (kDim == 128 ? (kTwo ? 3 : 4) : 6);  // fp16 tiles: K(0), V(0), K(1), ..
-  static constexpr int kStages = kDim == 128 ? 3 : 4;                // tiles of codes
+  static constexpr int kSlots = kDim == 128 ? 4 : 6;                  // fp16 tiles: K(0), V(0), K(1), ..
+  static constexpr int kStages = kDim == 128 ? (kTwo ? 1 : 3) : 4;    // tiles of codes
   static constexpr uint32_t kBlock = kTile * 128;
   static constexpr uint32_t kKv = kBlock * (kDim / 64);
   static constexpr uint32_t kCodes = 32 * kDim / 2, kScales = 32 * kDim / 16;  // of a warp's rows
-  static constexpr uint32_t kStage = 2 * (kCodes + kScales);
-  static constexpr size_t q = 0;                                     // [row tile][D / 64][128 rows][128 B]
+  static constexpr uint32_t kStage = kCodes + kScales;
+  static constexpr size_t q = 0;                                      // [row tile][D / 64][128 rows][128 B]
   static constexpr size_t kv = q + kRowTiles * kKv;
-  static constexpr size_t codes = kv + kSlots * kKv;                 // [warp][stage]
-  static constexpr size_t info = codes + 4 * kStages * kStage;
-  static constexpr size_t factor = info + kInfos * sizeof(TileInfo); // [row tile][128] of the logits
-  static constexpr size_t poison = factor + kRowTiles * 512;         // [kInfos][4 warps][8]
+  static constexpr size_t codes = kv + kSlots * kKv;                  // [converting warp][stage]
+  static constexpr size_t info = codes + 8 * kStages * kStage;
+  static constexpr size_t parts = info + kInfos * sizeof(TileInfo);   // [kParts] tiles, rows of a part
+  static constexpr size_t factor = parts + kParts * 8;  // [row tile][128] of the logits
+  static constexpr size_t poison = factor + kRowTiles * 512;          // [kInfos][4 warps][8]
   static constexpr size_t bars = poison + kInfos * 4 * 8 * 4;
-  static constexpr int kBars = 2 * kSlots + 2 * kInfos + 2 + 2 + 4 + 2 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kSlots + 2 * kInfos + 2 * kParts + 2 + 2 + 4 + 2 + 2 + 2 + 2 + 1;
   static constexpr size_t scan = bars + kBars * 8;
   static constexpr size_t start = scan + 32 * 8;
   static constexpr size_t misc = start + sizeof(UnitStart);
@@ -104,6 +106,12 @@ __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// mbar_wait_warp with a first look that costs a vote: most phases are complete by
+// the time they are asked for.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) || mbar_wait_warp(bar, parity);
+}
+
 template <int kDim, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
 umma4_kernel(const UmmaParams p) {
@@ -113,12 +121,14 @@ umma4_kernel(const UmmaParams p) {
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *qs = smem + L::q, *kvs = smem + L::kv;
   TileInfo *infos = reinterpret_cast<TileInfo *>(smem + L::info);
+  int2 *parts = reinterpret_cast<int2 *>(smem + L::parts);
   float *factor = reinterpret_cast<float *>(smem + L::factor);
   int *poison = reinterpret_cast<int *>(smem + L::poison);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
-  uint64_t *full = bars, *empty = full + kSlots, *ifull = empty + kSlots, *iempty = ifull + kInfos;
-  uint64_t *qfull = iempty + kInfos, *sfull = qfull + 2;
-  uint64_t *pfull = sfull + 2, *ofull = pfull + 4, *turn = ofull + 2, *done = turn + 2, *meet = done + 2;  // pfull: [stream][half]
+  uint64_t *full = bars, *empty = full + kSlots;
+  uint64_t *ifull = empty + kSlots, *iempty = ifull + kInfos, *gfull = iempty + kInfos, *gempty = gfull + kParts;
+  uint64_t *qfull = gempty + kParts, *sfull = qfull + 2;
+  uint64_t *pfull = sfull + 2, *opv = pfull + 4, *ofull = opv + 2, *turn = ofull + 2, *done = turn + 2, *meet = done + 2;
   UnitStart *start = reinterpret_cast<UnitStart *>(smem + L::start);
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 4);
@@ -132,13 +142,18 @@ umma4_kernel(const UmmaParams p) {
     }
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&ifull[i], 1);
-      mbar_init(&iempty[i], 10);  // two issuers, eight softmax warps
+      mbar_init(&iempty[i], 8);  // softmax warps
+    }
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&gfull[i], 1);
+      mbar_init(&gempty[i], 2);  // issuers
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[2 * i], 4);
       mbar_init(&pfull[2 * i + 1], 4);
+      mbar_init(&opv[i], 1);
       mbar_init(&ofull[i], 1);
       mbar_init(&turn[i], 1);
       mbar_init(&done[i], 1);
@@ -165,140 +180,16 @@ umma4_kernel(const UmmaParams p) {
     *abort_s = 1;
   };
 
-  if (warp >= kWarpMma) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < kWarpMma + 2) {
-      // ---------------------------------------------- issuer of one stream
-      const int w = warp - kWarpMma;
-      const bool leader = elect_one();
-      constexpr uint32_t idesc_s = idesc_f16(128, kTile);
-      constexpr uint32_t idesc_o = idesc_f16(128, kDim) | (1u << 16);  // V is MN-major
-      const uint32_t ts = tmem + 128 * w, to = tmem + 256 + 128 * w;
-      const uint64_t dq = desc_sw128_kmajor(smem_u32(qs + (kTwo ? w : 0) * L::kKv));
-      bool ok = true, two = false, live = true;
-      int qn = 0, ln = 0, turns = 0, in_part = 0;
-      auto take_turn = [&]() -> bool {
-        if (!two) return true;
-        const int k = turns++;
-        return w == 0 ? k == 0 || mbar_wait_warp(&turn[1], (k - 1) & 1) : mbar_wait_warp(&turn[0], k & 1);
-      };
-      auto wait_full = [&](int m) { return mbar_wait_warp(&full[m % kSlots], (m / kSlots) & 1); };
-      auto issue_s = [&](int m) {
-        if (leader) {
-          const uint64_t db = desc_sw128_kmajor(smem_u32(kvs + (m % kSlots) * L::kKv));
-#pragma unroll
-          for (int kk = 0; kk < kDim / 16; ++kk) {
-            const uint64_t o = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
-            mma_f16(ts, dq + o, db + o, idesc_s, kk > 0);
-          }
-          mma_commit(&sfull[w]);
-          mma_commit(&empty[m % kSlots]);
-        }
-      };
-      auto issue_o = [&](int m, int half, bool fresh) {
-        if (leader) {
-          const uint64_t dv = desc_mn(smem_u32(kvs + (m % kSlots) * L::kKv), L::kBlock);
-#pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            mma_f16_tmem_a(to, ts + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, !(fresh && kk == 0));
-        }
-      };
-      for (int n = 0; n < tiles; ++n) {
-        if (!mbar_wait_warp(&ifull[n % kInfos], (n / kInfos) & 1)) {
-          ok = false;
-          break;
-        }
-        const int mk = 2 * n, mv = mk + 1;
-        const bool part_first = infos[n % kInfos].first, part_end = infos[n % kInfos].end;
-        const int rows = infos[n % kInfos].n * p.group, count = infos[n % kInfos].tiles;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&iempty[n % kInfos]);
-        if constexpr (kTwo) {
-          if (part_first) {
-            two = rows > 128;
-            live = w == 0 || two;
-          }
-          if (!live) {  // only frees the ring
-            ok = wait_full(mk);
-            if (ok && leader) mbar_arrive(&empty[mk % kSlots]);
-            ok = ok && wait_full(mv);
-            if (!ok) break;
-            if (leader) mbar_arrive(&empty[mv % kSlots]);
-            __syncwarp();
-            continue;
-          }
-          if (part_first) {
-            ok = wait_full(mk) && mbar_wait_warp(&qfull[w], (qn++) & 1) && take_turn();
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(mk);
-            if (leader && two) mbar_arrive(&turn[w]);
-            __syncwarp();
-          }
-          ok = wait_full(mv) && (part_end || wait_full(mv + 1)) && mbar_wait_warp(&pfull[2 * w], ln & 1) && take_turn();
-          if (!ok || *abort_s) break;
-          tc_fence_after();
-          issue_o(mv, 0, part_first);
-          ok = mbar_wait_warp(&pfull[2 * w + 1], ln & 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_o(mv, 1, false);
-          if (leader) {
-            if (part_end) mma_commit(&ofull[w]);
-            mma_commit(&empty[mv % kSlots]);
-          }
-          if (!part_end) issue_s(mv + 1);
-          if (leader && two) mbar_arrive(&turn[w]);
-          __syncwarp();
-          ++ln;
-        } else {
-          // tiles of a part go to the streams in turn
-          if (part_first) in_part = 0;
-          const int j = in_part++;
-          if ((j & 1) != w) continue;
-          ok = wait_full(mk) && (j >= 2 || mbar_wait_warp(&qfull[w], (qn++) & 1));
-          if (!ok || *abort_s) break;
-          tc_fence_after();
-          issue_s(mk);
-          __syncwarp();
-          ok = wait_full(mv) && mbar_wait_warp(&pfull[2 * w], ln & 1);
-          if (!ok || *abort_s) break;
-          tc_fence_after();
-          issue_o(mv, 0, j < 2);
-          ok = mbar_wait_warp(&pfull[2 * w + 1], ln & 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_o(mv, 1, false);
-          if (leader) {
-            if (j + 2 >= count) mma_commit(&ofull[w]);
-            mma_commit(&empty[mv % kSlots]);
-          }
-          __syncwarp();
-          ++ln;
-        }
-      }
-      if (!ok && lane == 0) fail();
-      if (leader && tiles > 0) {
-        mma_commit(&done[w]);
-        if (!mbar_wait(&done[w], 0)) raise_flag(p.status, kFlagTimeout);
-      }
-      __syncwarp();
-    }
-  } else if (warp >= kWarpCopy) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-    // ------------------------- codes in, fp16 tiles out: rows 32 cw .. 32 cw + 31
-    const int cw = warp - kWarpCopy;
-    uint8_t *codes = smem + L::codes + cw * L::kStages * L::kStage;
-    const uint32_t codes_s = smem_u32(codes);
-    bool ok = true;
+  // Calls use(seq, t0, len, low, last, hv, kt0, count, c0, c1) for the parts of units
+  // that this CTA has, in order; stops when it returns false.  (A whole warp.)
+  auto walk = [&](const auto &use) {
     int block = start->block, hv = start->head, kt0 = start->tile;
     long long x = x0;
-    int n = 0, part = 0;
     // first token of the block that is not yet in a unit (before `start` they are other CTAs')
     int i0 = x0 < x1 ? static_cast<int>(start->t0 - static_cast<int64_t>(block) * p.nt) : 0;
-    while (ok && x < x1 && static_cast<int64_t>(block) * p.nt < pv.T) {
+    while (x < x1 && static_cast<int64_t>(block) * p.nt < pv.T) {
       const int in_block = static_cast<int>(min(static_cast<int64_t>(p.nt), pv.T - static_cast<int64_t>(block) * p.nt));
-      while (ok && x < x1 && i0 < in_block) {
+      while (x < x1 && i0 < in_block) {
         // the unit that begins at token i0
         const int t0 = block * p.nt + i0;
         const int seq = pv.q_seq[t0];
@@ -318,147 +209,286 @@ umma4_kernel(const UmmaParams p) {
         i0 += len;
         const int cost = (last + kTile) / kTile;
         if (cost == 0) continue;
-        for (; ok && hv < pv.H_kv && x < x1; ++hv, kt0 = 0) {
+        for (; hv < pv.H_kv && x < x1; ++hv, kt0 = 0) {
           const long long u0 = x - kt0, u1 = u0 + cost;
           const int c0 = u0 < x0 ? cta_of_tile(u0, total, ctas) : blockIdx.x;
           const int c1 = u1 > x1 ? cta_of_tile(u1 - 1, total, ctas) : blockIdx.x;
-          const int kt1 = static_cast<int>(min(static_cast<long long>(cost), kt0 + (x1 - x))), count = kt1 - kt0;
+          const int count = static_cast<int>(min(static_cast<long long>(cost - kt0), x1 - x));
           x += count;
-          int *bad = poison + ((part % kInfos) * 4 + cw) * 8;
-          // lane l: the page of the l-th 16 slots of this warp's rows: two of each tile
-          auto load_ids = [&](int i) {
-            const int slot = kTile * (kt0 + i + (lane >> 1)) + 32 * cw + 16 * (lane & 1);
-            if (i + (lane >> 1) >= count || slot > last) return -1;
-            return load_page(pv, seq, slot >> pv.logP, p.status, true);
-          };
-          // (and of the first warp, lane j: the page of 16 slots j of the next tile, for
-          // the tile's description)
-          auto load_all = [&](int i) {
-            const int slot = kTile * (kt0 + i) + 16 * lane;
-            if (cw != 0 || lane >= 8 || i >= count || slot > last) return -1;
-            return load_page(pv, seq, slot >> pv.logP, nullptr, false);
-          };
-          int ids = load_ids(0), ids_next = -1, all = load_all(0);
-          auto copy = [&](int i) {
-            if (i < count) {
-              const int id0 = __shfl_sync(0xffffffffu, ids, (2 * i) & 31), id1 = __shfl_sync(0xffffffffu, ids, (2 * i + 1) & 31);
-              const uint32_t st = codes_s + (i % L::kStages) * L::kStage;
-              const int slot = kTile * (kt0 + i) + 32 * cw;
-              auto row_of = [&](int half) {
-                const int id = half ? id1 : id0;
-                return (static_cast<int64_t>(max(id, 0) * pv.H_kv + hv) << pv.logP) + ((slot + 16 * half) & (pv.P - 1)) -
-                       16 * half;
-              };
-              const int64_t row0 = row_of(0), row1 = row_of(1);
-              constexpr int kC = kDim / 32;  // 16-byte chunks of a row's codes
-              constexpr int kR = 32 / kC;    // rows of a load
-              const int r = lane / kC, ch = lane % kC;
-#pragma unroll
-              for (int e = 0; e < 32; e += kR) {
-                const int64_t row = (e < 16 ? row0 : row1) + e + r;
-                const uint32_t bytes = (e < 16 ? id0 : id1) >= 0 ? 16u : 0u;
-                // chunks of a row swapped so that eight rows' reads meet no bank twice
-                const int sw = kDim == 128 ? ch ^ ((e + r) >> 1 & 3) : ch ^ ((e + r) >> 2 & 1);
-                const uint32_t to = st + (e + r) * (kDim / 2) + 16 * sw;
-                cp_async16_or_zero(to, p.c.K + row * (kDim / 2) + 16 * ch, bytes);
-                cp_async16_or_zero(to + L::kCodes, p.c.V + row * (kDim / 2) + 16 * ch, bytes);
-              }
-              constexpr int kSc = 2 * kDim / 16;  // chunks of the scales of 32 rows
-              if (lane < 2 * kSc) {
-                const int c = lane % kSc, half = c >= kSc / 2;
-                cp_async16_or_zero(st + 2 * L::kCodes + 16 * lane,
-                                   (lane < kSc ? p.c.Ks : p.c.Vs) + (half ? row1 : row0) * (kDim / 16) + 16 * c,
-                                   (half ? id1 : id0) >= 0 ? 16u : 0u);
-              }
-            }
-            cp_async_commit();
-          };
-#pragma unroll
-          for (int i = 0; i < L::kStages - 1; ++i) copy(i);
-          if (lane < 8) bad[lane] = INT_MAX;
-          __syncwarp();
-          for (int i = 0; i < count && ok; ++i, ++n) {
-            const int ahead = i + L::kStages - 1;
-            if ((ahead & 15) == 0) ids = ids_next;
-            cp_async_wait<L::kStages - 2>();
-            __syncwarp();
-            copy(ahead);  // (into the stage that the tile before was read from)
-            if ((ahead & 15) == 4) ids_next = load_ids(ahead - 4 + 16);
-            if (cw == 0) {
-              const uint32_t have = __ballot_sync(0xffffffffu, all >= 0);
-              all = load_all(i + 1);
-              if (!mbar_wait_warp(&iempty[n % kInfos], ((n / kInfos) & 1) ^ 1) || *abort_s) {
-                ok = false;
-                break;
-              }
-              if (lane == 0) {
-                infos[n % kInfos] = TileInfo{t0, len, hv, kTile * (kt0 + i), low, last, have, i == 0, i + 1 == count,
-                                             c0, c1, count, part, 0};
-                mbar_arrive(&ifull[n % kInfos]);
-              }
-            }
-            const uint8_t *st = codes + (i % L::kStages) * L::kStage;
-            const int slot = kTile * (kt0 + i) + 32 * cw + lane;
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-              const int m = 2 * n + kv;
-              // this lane's row: its scales, zero past the unit's last slot
-              uint32_t sc[kDim / 64];
-              const uint8_t *ss = st + 2 * L::kCodes + kv * L::kScales + lane * (kDim / 16);
-              if constexpr (kDim == 128)
-                *reinterpret_cast<uint2 *>(sc) = *reinterpret_cast<const uint2 *>(ss);
-              else
-                sc[0] = *reinterpret_cast<const uint32_t *>(ss);
-              if (slot > last) {
-#pragma unroll
-                for (int e = 0; e < kDim / 64; ++e) sc[e] = 0;
-              } else if (kv == 1 && slot > low) {
-#pragma unroll
-                for (int e = 0; e < kDim / 16; ++e)
-                  if (e4m3_is_nan((sc[e >> 2] >> (8 * (e & 3))) & 0xFFu)) {
-                    sc[e >> 2] &= ~(0xFFu << (8 * (e & 3)));
-                    atomicMin(&bad[e], slot);
-                  }
-              }
-              const uint4 *cd = reinterpret_cast<const uint4 *>(st + kv * L::kCodes + lane * (kDim / 2));
-              const int sw = kDim == 128 ? (lane >> 1) & 3 : (lane >> 2) & 1;
-              uint4 c[kDim / 32];
-#pragma unroll
-              for (int e = 0; e < kDim / 32; ++e) c[e] = cd[e ^ sw];
-              if (!mbar_wait_warp(&empty[m % kSlots], ((m / kSlots) & 1) ^ 1) || *abort_s) {
-                ok = false;
-                break;
-              }
-              uint8_t *dst = kvs + (m % kSlots) * L::kKv;
-              const int row = 32 * cw + lane;
-#pragma unroll
-              for (int e = 0; e < kDim / 32; ++e) {
-                const __half2 two = e4m3x2_to_half2(sc[e >> 1] >> (16 * (e & 1)));
-                const uint32_t words[4] = {c[e].x, c[e].y, c[e].z, c[e].w};
-#pragma unroll
-                for (int i4 = 0; i4 < 4; ++i4) {
-                  const __half2 s2 = i4 < 2 ? __low2half2(two) : __high2half2(two);
-                  __half2 d[4];
-                  e2m1x8_to_half2(words[i4], d);
-                  *reinterpret_cast<uint4 *>(dst + (e >> 1) * L::kBlock + sw128_offset(row, 64 * (e & 1) + 16 * i4)) =
-                      make_uint4(as_u32(__hmul2(d[0], s2)), as_u32(__hmul2(d[1], s2)), as_u32(__hmul2(d[2], s2)),
-                                 as_u32(__hmul2(d[3], s2)));
-                }
-              }
-              fence_proxy_async();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&full[m % kSlots]);
-            }
-          }
-          ++part;
-          cp_async_wait<0>();
-          __syncwarp();
+          if (!use(seq, t0, len, low, last, hv, kt0, count, c0, c1)) return;
         }
         if (hv == pv.H_kv) hv = 0;
       }
       ++block;
       i0 = 0;
     }
+  };
+
+  if (warp >= kWarpMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < kWarpMma + 2) {
+      // ---------------------------------------------- issuer of one stream
+      const int w = warp - kWarpMma;
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = idesc_f16(128, kTile);
+      constexpr uint32_t idesc_o = idesc_f16(128, kDim) | (1u << 16);  // V is MN-major
+      const uint32_t ts = tmem + 128 * w, to = tmem + 256 + 128 * w;
+      const uint64_t dq = desc_sw128_kmajor(smem_u32(qs + (kTwo ? w : 0) * L::kKv));
+      const uint32_t kv0 = smem_u32(kvs);
+      bool ok = true, two = false;
+      int qn = 0, ln = 0, turns = 0;
+      // Two row tiles: the issuers take turns, O_A(n), S_A(n + 1), then O_B(n), S_B(n + 1),
+      // so that the softmax of one runs while the products of the other do.
+      auto take_turn = [&]() -> bool {
+        if (!two) return true;
+        const int k = turns++;
+        return w == 0 ? k == 0 || wait_warp(&turn[1], (k - 1) & 1) : wait_warp(&turn[0], k & 1);
+      };
+      auto wait_full = [&](int m) { return wait_warp(&full[m % kSlots], (m / kSlots) & 1); };
+      // (the address once for the warp, so that the descriptors are uniform values)
+      auto slot_of = [&](int m) { return __reduce_or_sync(0xffffffffu, kv0 + (m % kSlots) * L::kKv); };
+      auto issue_s = [&](int m) {
+        const uint32_t at = slot_of(m);
+        if (leader) {
+          const uint64_t db = desc_sw128_kmajor(at);
+#pragma unroll
+          for (int kk = 0; kk < kDim / 16; ++kk) {
+            const uint64_t o = ((kk >> 2) * L::kBlock + (kk & 3) * 32) >> 4;
+            mma_f16(ts, dq + o, db + o, idesc_s, kk > 0);
+          }
+          mma_commit(&sfull[w]);
+          mma_commit(&empty[m % kSlots]);
+        }
+        __syncwarp();
+      };
+      auto issue_o = [&](int m, int half, bool fresh, bool end) {
+        const uint32_t at = slot_of(m);
+        if (leader) {
+          const uint64_t dv = desc_mn(at, L::kBlock);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_tmem_a(to, ts + 32 * half + 8 * kk, dv + (((4 * half + kk) * 2048) >> 4), idesc_o, !(fresh && kk == 0));
+          if (!half) mma_commit(&opv[w]);
+          if (half && end) mma_commit(&ofull[w]);
+          if (half) mma_commit(&empty[m % kSlots]);
+        }
+        __syncwarp();
+      };
+      int n = 0;
+      for (int part = 0; n < tiles && ok; ++part) {
+        ok = wait_warp(&gfull[part % kParts], (part / kParts) & 1) && !*abort_s;
+        if (!ok) break;
+        const int count = parts[part % kParts].x, rows = parts[part % kParts].y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&gempty[part % kParts]);
+        if constexpr (kTwo) {
+          two = rows > 128;
+          if (w == 1 && !two) {  // only frees the ring
+            for (int m = 2 * n; m < 2 * (n + count) && ok; ++m) {
+              ok = wait_full(m);
+              if (ok && leader) mbar_arrive(&empty[m % kSlots]);
+              __syncwarp();
+            }
+            n += count;
+            continue;
+          }
+          ok = wait_full(2 * n) && wait_warp(&qfull[w], (qn++) & 1) && take_turn();
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(2 * n);
+          if (leader && two) mbar_arrive(&turn[w]);
+        } else {
+          if (w < count) ok = wait_warp(&qfull[w], (qn++) & 1);
+        }
+        // own tiles of the part: every one, or every second
+        constexpr int kStep = kTwo ? 1 : 2;
+        for (int j = kTwo ? 0 : w; j < count; j += kStep) {
+          const int mk = 2 * (n + j), mv = mk + 1;
+          const bool end = j + kStep >= count;
+          if constexpr (kTwo) {
+            ok = wait_full(mv) && (end || wait_full(mk + 2)) && wait_warp(&pfull[2 * w], ln & 1) &&
+                 wait_warp(&pfull[2 * w + 1], ln & 1) && take_turn();
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(mv, 0, j == 0, end);
+            issue_o(mv, 1, false, end);
+            if (!end) issue_s(mk + 2);
+            if (leader && two) mbar_arrive(&turn[w]);
+          } else {
+            ok = ok && wait_full(mk);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(mk);
+            ok = wait_full(mv) && wait_warp(&pfull[2 * w], ln & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(mv, 0, j == w, end);
+            ok = wait_warp(&pfull[2 * w + 1], ln & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(mv, 1, false, end);
+          }
+          ++ln;
+        }
+        n += count;
+      }
+      if (!ok && lane == 0) fail();
+      if (leader && tiles > 0) {
+        mma_commit(&done[w]);
+        if (!mbar_wait(&done[w], 0)) raise_flag(p.status, kFlagTimeout);
+      }
+      __syncwarp();
+    }
+    if (warp == kWarpInfo) {
+      // ------------------------------------------------ descriptions of tiles
+      int n = 0, part = 0;
+      bool ok = true;
+      walk([&](int seq, int t0, int len, int low, int last, int hv, int kt0, int count, int c0, int c1) {
+        // lane j: the page of 16 slots j of a tile, loaded a tile ahead
+        auto entry = [&](int i) {
+          const int slot = kTile * (kt0 + i) + 16 * lane;
+          return i < count && lane < 8 && slot <= last ? load_page(pv, seq, slot >> pv.logP, p.status, true) : -1;
+        };
+        ok = wait_warp(&gempty[part % kParts], ((part / kParts) & 1) ^ 1) && !*abort_s;
+        if (!ok) return false;
+        if (lane == 0) {
+          parts[part % kParts] = make_int2(count, len * p.group);
+          mbar_arrive(&gfull[part % kParts]);
+        }
+        int next = entry(0);
+        for (int i = 0; i < count; ++i, ++n) {
+          const uint32_t have = __ballot_sync(0xffffffffu, next >= 0);
+          next = entry(i + 1);
+          ok = wait_warp(&iempty[n % kInfos], ((n / kInfos) & 1) ^ 1) && !*abort_s;
+          if (!ok) return false;
+          if (lane == 0) {
+            infos[n % kInfos] =
+                TileInfo{t0, len, hv, kTile * (kt0 + i), low, last, have, i == 0, i + 1 == count, c0, c1, count, part, 0};
+            mbar_arrive(&ifull[n % kInfos]);
+          }
+        }
+        ++part;
+        return true;
+      });
+      if (!ok && lane == 0) fail();
+    }
+  } else if (warp >= kWarpConv) {
+    // ---------------------------- codes to fp16 tiles: 32 rows of keys or of values
+    const int kv = (warp - kWarpConv) >> 2, cw = warp & 3;
+    uint8_t *ring = smem + L::codes + (warp - kWarpConv) * L::kStages * L::kStage;
+    const uint32_t ring_s = smem_u32(ring);
+    const uint8_t *codes = kv ? p.c.V : p.c.K, *scales = kv ? p.c.Vs : p.c.Ks;
+    constexpr int kItems = kDim / 32, kRows = 32 / kItems;
+    // Copies: chunk ch (16 bytes) of row kRows e + of a warp's 32, the chunks of a row
+    // swapped by bits of the row so that the reads below meet no bank twice
+    const int ch = lane % (kDim / 32), cr = lane / (kDim / 32);
+    // Item e of a lane: the 32 values from 32 seg on of row kRows e + of (eight lanes in
+    // a row store two neighbouring 64-byte pieces of four rows)
+    const int seg = kDim == 128 ? (lane & 1) + 2 * (lane >> 4) : lane & 1;
+    const int of = kDim == 128 ? (lane >> 1) & 7 : lane >> 1;
+    auto swapped = [](int row, int c) { return kDim == 128 ? c ^ ((row & 2) ? 2 : 0) : c; };
+    bool ok = true;
+    int n = 0, part = 0;
+    walk([&](int seq, int t0, int len, int low, int last, int hv, int kt0, int count, int c0, int c1) {
+      // lane l: the page of the l-th 16 slots of this warp's rows, two of each tile
+      auto load_ids = [&](int i) {
+        const int slot = kTile * (kt0 + i + (lane >> 1)) + 32 * cw + 16 * (lane & 1);
+        if (i + (lane >> 1) >= count || slot > last) return -1;
+        return load_page(pv, seq, slot >> pv.logP, nullptr, false);
+      };
+      int ids = load_ids(0), ids_next = -1;
+      auto copy = [&](int i) {
+        if (i < count) {
+          const int id0 = __shfl_sync(0xffffffffu, ids, (2 * i) & 31), id1 = __shfl_sync(0xffffffffu, ids, (2 * i + 1) & 31);
+          const uint32_t st = ring_s + (i % L::kStages) * L::kStage;
+          const int slot = kTile * (kt0 + i) + 32 * cw;
+          // (where there is no page, zeros)
+          const int64_t row0 = (static_cast<int64_t>(max(id0, 0) * pv.H_kv + hv) << pv.logP) + (slot & (pv.P - 1));
+          const int64_t row1 = (static_cast<int64_t>(max(id1, 0) * pv.H_kv + hv) << pv.logP) + ((slot + 16) & (pv.P - 1));
+          const uint32_t b0 = id0 >= 0 ? 16u : 0u, b1 = id1 >= 0 ? 16u : 0u;
+          const uint8_t *s0 = codes + row0 * (kDim / 2) + 16 * lane, *s1 = codes + row1 * (kDim / 2) + 16 * lane;
+          const uint32_t to = st + cr * (kDim / 2) + 16 * swapped(cr, ch);
+#pragma unroll
+          for (int e = 0; e < kItems / 2; ++e) {
+            cp_async16_or_zero(to + 512 * e, s0 + 512 * e, b0);
+            cp_async16_or_zero(to + 8 * kDim + 512 * e, s1 + 512 * e, b1);
+          }
+          constexpr int kSc = kDim / 16;  // chunks of the scales of 16 rows
+          if (lane < 2 * kSc)
+            cp_async16_or_zero(st + L::kCodes + 16 * lane,
+                               scales + (lane < kSc ? row0 : row1) * (kDim / 16) + 16 * (lane % kSc), lane < kSc ? b0 : b1);
+        }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < L::kStages; ++i) copy(i);
+      int *bad = poison + ((part % kInfos) * 4 + cw) * 8;
+      if (kv == 1 && lane < 8) bad[lane] = INT_MAX;
+      __syncwarp();
+      for (int i = 0; i < count; ++i, ++n) {
+        const int ahead = i + L::kStages;
+        if ((ahead & 15) == 0) ids = ids_next;
+        cp_async_wait<L::kStages - 1>();
+        __syncwarp();
+        const uint8_t *st = ring + (i % L::kStages) * L::kStage;
+        const int base = kTile * (kt0 + i) + 32 * cw;
+        uint4 c[kItems];
+        uint32_t sc[kItems];
+#pragma unroll
+        for (int e = 0; e < kItems; ++e) {
+          const int row = of + kRows * e;
+          c[e] = *reinterpret_cast<const uint4 *>(st + row * (kDim / 2) + 16 * swapped(row, seg));
+          sc[e] = reinterpret_cast<const uint16_t *>(st + L::kCodes + row * (kDim / 16))[seg];
+        }
+        __syncwarp();
+        copy(ahead);  // (into the stage just read)
+        if ((ahead & 15) == 5) ids_next = load_ids(ahead - 5 + 16);
+        if (base + 31 > (kv ? low : last)) {
+          // rows past the last slot become zeros; a NaN block of values that not every row
+          // of queries attends is left out and noted
+#pragma unroll
+          for (int e = 0; e < kItems; ++e) {
+            const int slot = base + of + kRows * e;
+            if (slot > last) {
+              sc[e] = 0;
+            } else if (kv == 1 && slot > low) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                if (e4m3_is_nan((sc[e] >> (8 * b)) & 0xFFu)) {
+                  sc[e] &= 0xFFu << (8 * (1 - b));
+                  atomicMin(&bad[2 * seg + b], slot);
+                }
+            }
+          }
+        }
+        const int m = 2 * n + kv;
+        ok = wait_warp(&empty[m % kSlots], ((m / kSlots) & 1) ^ 1) && !*abort_s;
+        if (!ok) return false;
+        uint8_t *dst = kvs + (m % kSlots) * L::kKv + (seg >> 1) * L::kBlock;
+#pragma unroll
+        for (int e = 0; e < kItems; ++e) {
+          const int row = 32 * cw + of + kRows * e;
+          const __half2 two = e4m3x2_to_half2(sc[e]);
+          const uint32_t words[4] = {c[e].x, c[e].y, c[e].z, c[e].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __half2 s2 = j < 2 ? __low2half2(two) : __high2half2(two);
+            __half2 d[4];
+            e2m1x8_to_half2(words[j], d);
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 64 * (seg & 1) + 16 * j)) =
+                make_uint4(as_u32(__hmul2(d[0], s2)), as_u32(__hmul2(d[1], s2)), as_u32(__hmul2(d[2], s2)),
+                           as_u32(__hmul2(d[3], s2)));
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[m % kSlots]);
+      }
+      ++part;
+      cp_async_wait<0>();
+      __syncwarp();
+      return true;
+    });
     cp_async_wait<0>();
     if (!ok && lane == 0) fail();
   } else {
@@ -470,7 +500,7 @@ umma4_kernel(const UmmaParams p) {
     uint8_t *qt = qs + (kTwo ? w : 0) * L::kKv;
     float *fac = factor + (kTwo ? w : 0) * 128;
     float ref = 0.f, l = 0.f, cs = 0.f;
-    int ln = 0, pieces = 0, in_part = 0, met = 0, lim = -1, r = 0;
+    int ln = 0, pieces = 0, in_part = 0, met = 0, lim = -1, r = 0, reps = 1;
     bool ok = true, live = true, idle = false;
     auto sync = [&]() {  // of the softmax warps
       __syncwarp();
@@ -478,20 +508,26 @@ umma4_kernel(const UmmaParams p) {
       ok = mbar_wait_warp(meet, (met++) & 1) && ok;
     };
     int qn = 0;
+    TileInfo ti;
     for (int n = 0; n < tiles; ++n) {
-      ok = mbar_wait_warp(&ifull[n % kInfos], (n / kInfos) & 1);
+      ok = wait_warp(&ifull[n % kInfos], (n / kInfos) & 1);
       if (!ok || *abort_s) break;
-      const TileInfo ti = infos[n % kInfos];
+      const TileInfo &info = infos[n % kInfos];
+      const int base = info.base, part_first = info.first, part_end = info.end;
+      const uint32_t tile_have = info.have;
+      if (part_first) ti = info;  // (what is the same for all tiles of a part)
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[n % kInfos]);
       const int rows = ti.n * p.group;
       bool mine = true;  // this stream has the tile
-      if (ti.first) {
+      if (part_first) {
         in_part = 0;
         l = 0.f;
         ref = 0.f;
         live = kTwo ? w == 0 || rows > 128 : w == 0 || ti.tiles > 1;
-        r = (kTwo ? 128 * w : 0) + row;
+        // (up to 64 rows lie in the tile twice, each copy with half of the keys)
+        reps = !kTwo && rows <= 64 ? 2 : 1;
+        r = kTwo ? 128 * w + row : row & (128 / reps - 1);
         if (live) {
           // the row's token and limit
           const int i = r / p.group;
@@ -505,29 +541,37 @@ umma4_kernel(const UmmaParams p) {
             // K-major swizzled layout; a load covers whole rows
             constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;
             const int ch = lane % kLanes;
-            const int rw = (kTwo ? 128 * w : 0) + 32 * (warp & 3);
             uint8_t *dst = qt + (ch >> 3) * L::kBlock;
-#pragma unroll 4
-            for (int e = 0; e < 32; e += kPer) {
-              const int rr = rw + e + lane / kLanes, tt = rr / p.group;
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (rr < rows)
-                v = reinterpret_cast<const uint4 *>(
-                    p.q + (static_cast<int64_t>(ti.t0 + tt) * pv.H + ti.hk * p.group + rr - tt * p.group) * kDim)[ch];
-              uint32_t u[4] = {v.x, v.y, v.z, v.w};
-              float top = 0.f;
+            constexpr int kBatch = 8;  // loads that go out together
+#pragma unroll 1
+            for (int e0 = 0; e0 < 32; e0 += kBatch * kPer) {
+              uint4 v[kBatch];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+              for (int e = 0; e < kBatch; ++e) {
+                const int to_row = 32 * (warp & 3) + e0 + e * kPer + lane / kLanes;
+                const int rr = kTwo ? 128 * w + to_row : to_row & (128 / reps - 1), tt = rr / p.group;
+                v[e] = make_uint4(0, 0, 0, 0);
+                if (rr < rows)
+                  v[e] = reinterpret_cast<const uint4 *>(
+                      p.q + (static_cast<int64_t>(ti.t0 + tt) * pv.H + ti.hk * p.group + rr - tt * p.group) * kDim)[ch];
+              }
 #pragma unroll
-              for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const float f = to_half_factor(top);
+              for (int e = 0; e < kBatch; ++e) {
+                const int to_row = 32 * (warp & 3) + e0 + e * kPer + lane / kLanes;
+                uint32_t u[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+                float top = 0.f;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                u[j] = as_u32(__floats2half2_rn(__uint_as_float(u[j] << 16) * f, __uint_as_float(u[j] & 0xFFFF0000u) * f));
-              *reinterpret_cast<uint4 *>(dst + sw128_offset(rr - (kTwo ? 128 * w : 0), 16u * (ch & 7))) =
-                  make_uint4(u[0], u[1], u[2], u[3]);
-              if (ch == 0) fac[rr - (kTwo ? 128 * w : 0)] = p.qk_scale / f;
+                for (int j = 0; j < 4; ++j)
+                  top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+#pragma unroll
+                for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float f = to_half_factor(top);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  u[j] = as_u32(__floats2half2_rn(__uint_as_float(u[j] << 16) * f, __uint_as_float(u[j] & 0xFFFF0000u) * f));
+                *reinterpret_cast<uint4 *>(dst + sw128_offset(to_row, 16u * (ch & 7))) = make_uint4(u[0], u[1], u[2], u[3]);
+                if (ch == 0) fac[to_row] = p.qk_scale / f;
+              }
             }
             fence_proxy_async();
             __syncwarp();
@@ -547,87 +591,131 @@ umma4_kernel(const UmmaParams p) {
       }
       if constexpr (!kTwo) mine = (in_part & 1) == w;
       ++in_part;
-      const bool part_end = ti.end;
       if (live && mine) {
-        const bool first = kTwo ? ti.first : in_part <= 2;
+        const bool first = kTwo ? part_first : in_part <= 2;
         const bool mine_end = kTwo ? part_end : in_part + 2 > ti.tiles;
-        ok = mbar_wait_warp(&sfull[w], ln & 1);
-        if (!ok || *abort_s) break;
-        tc_fence_after();
-        if (idle) {  // (its rows' weights and O may be anything)
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&pfull[2 * w]);
-            mbar_arrive(&pfull[2 * w + 1]);
-          }
-        } else {
-        float v[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_load(ts + 32 * i, reinterpret_cast<uint32_t(&)[32]>(v[32 * i]));
-        tmem_ld_wait();
-        const bool masked = ti.have != 0xFFu || ti.base + kTile - 1 > ti.low;
-        const bool fresh = l == 0.f && lim >= 0;
-        float2 *v2 = reinterpret_cast<float2 *>(v);
-        const float2 cs2 = make_float2(cs, cs), nref2 = make_float2(-ref, -ref);
-#pragma unroll
-        for (int e = 0; e < 64; ++e) v2[e] = fma2(v2[e], cs2, nref2);
-        if (masked) {
-          const int d = lim - ti.base;  // the row's last slot in the tile
-#pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e > d || !((ti.have >> (e >> 4)) & 1u)) v[e] = -INFINITY;
-        }
-        float top;
-        {
-          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 64; ++e) t4[e & 3] = max3(t4[e & 3], v2[e].x, v2[e].y);
-          top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
-        }
-        if (__any_sync(0xffffffffu, fresh || top > kRefTop)) {
-          // the row's first keys, or a logit passes its reference: set or raise it; the
-          // sum and O (which holds the products up to the tile before) shrink in step
-          const float up = top == -INFINITY ? 0.f : fresh || top > kRefTop ? top - kRefHead : 0.f;
-          const float2 nup2 = make_float2(-up, -up);
-          ref += up;
-#pragma unroll
-          for (int e = 0; e < 64; ++e) v2[e] = add2(v2[e], nup2);
-          if (!first) {
-            const float f = exp2f(fminf(-up, 0.f));
-            l *= f;
-#pragma unroll 1
-            for (int i = 0; i < kDim / 16; ++i) {
-              uint32_t o[16];
-              tmem_load(to + 16 * i, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_store(to + 16 * i, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+        const bool masked = tile_have != 0xFFu || base + kTile - 1 > ti.low;
         for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 y = v2[32 * half + e];
-            const float2 w2 = make_float2(exp2_hw(y.x), exp2_hw(y.y));
-            sum[e & 1] = add2(sum[e & 1], w2);
-            pk[e] = as_u32(__floats2half2_rn(w2.x, w2.y));
+          if (half == 0) {
+            ok = wait_warp(&sfull[w], ln & 1);
+            if (!ok || *abort_s) break;
+            tc_fence_after();
           }
-          tmem_store(ts + 32 * half, pk);
-          tmem_store(ts + 32 * half + 16, pk + 16);
-          tmem_wait_st();
-          tc_fence_before();
+          const uint32_t th = ts + 64 * half, tp = ts + 32 * half;  // logits, weights
+          if (idle) {  // (its rows' weights and O may be anything)
+          } else if (reps == 2 && half != (warp >> 1 & 1)) {
+            // the other copy of the rows has these keys
+            const uint32_t zero[16] = {};
+            tmem_store(tp, zero);
+            tmem_store(tp + 16, zero);
+            if (half) {
+              tmem_wait_st();
+              tc_fence_before();
+            }
+          } else {
+            // the half's logits relative to the reference, in v
+            float v[64];
+            float2 *v2 = reinterpret_cast<float2 *>(v);
+            auto logits = [&]() {
+              tmem_load(th, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+              tmem_load(th + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+              tmem_ld_wait();
+              const float2 cs2 = make_float2(cs, cs), nref2 = make_float2(-ref, -ref);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v2[e] = fma2(v2[e], cs2, nref2);
+              if (masked) {
+                const int d = lim - base - 64 * half;  // the row's last slot in the half
+                const uint32_t have = tile_have >> (4 * half);
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                  if (e > d || !((have >> (e >> 4)) & 1u)) v[e] = -INFINITY;
+              }
+            };
+            uint32_t pk[32];
+            float sum;
+            auto weights = [&]() {
+              float2 t[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float2 w2 = make_float2(exp2_hw(v2[e].x), exp2_hw(v2[e].y));
+                t[e & 1] = add2(t[e & 1], w2);
+                pk[e] = as_u32(__floats2half2_rn(w2.x, w2.y));
+              }
+              t[0] = add2(t[0], t[1]);
+              sum = t[0].x + t[0].y;
+            };
+            logits();
+            const bool fresh = l == 0.f && lim >= 0;
+            // The weights are taken as they come; only where their sum tells that one may
+            // be past 2^9 (all are below 2^15 otherwise), or the row has met no key yet, the
+            // reference is looked at.
+            bool again = __any_sync(0xffffffffu, fresh);
+            if (!again) {
+              weights();
+              again = __any_sync(0xffffffffu, sum > 32768.f);
+              if (again) logits();
+            }
+            if (again) {
+              float top;
+              {
+                float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 32; ++e) t4[e & 3] = max3(t4[e & 3], v2[e].x, v2[e].y);
+                top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+              }
+              // the row's first keys, or a logit 2^8 above its reference: set or raise it;
+              // the sum and O shrink in step, and the first half's weights, or O once their
+              // product has been added.  By a power of two, which rounds nothing.
+              const float up = top == -INFINITY ? 0.f : fresh || top > 8.f ? rintf(top - kRefHead) : 0.f;
+              const float2 nup2 = make_float2(-up, -up);
+              ref += up;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v2[e] = add2(v2[e], nup2);
+              if (!(first && half == 0)) {
+                if (!kTwo && half && reps == 1) {
+                  ok = wait_warp(&opv[w], ln & 1);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                const float f = exp2f(fminf(-up, 0.f));
+                l *= f;
+                if (kTwo && half) {
+                  const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    uint32_t o[16];
+                    tmem_load(ts + 16 * i, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = as_u32(__hmul2(*reinterpret_cast<__half2 *>(&o[e]), f2));
+                    tmem_store(ts + 16 * i, o);
+                  }
+                }
+#pragma unroll 1
+                for (int i = 0; i < kDim / 16; ++i) {
+                  uint32_t o[16];
+                  tmem_load(to + 16 * i, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_store(to + 16 * i, o);
+                }
+                tmem_wait_st();
+              }
+              weights();
+            }
+            tmem_store(tp, pk);
+            tmem_store(tp + 16, pk + 16);
+            tmem_wait_st();
+            tc_fence_before();
+            l += sum;
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&pfull[2 * w + half]);
+          // (copies of rows hand over both halves together)
+          if (lane == 0 && (reps == 1 || half)) mbar_arrive(&pfull[2 * w + half]);
+          if (lane == 0 && reps == 2 && half) mbar_arrive(&pfull[2 * w]);
         }
-        const float2 sum2 = add2(sum[0], sum[1]);
-        l += sum2.x + sum2.y;
-        }
+        if (!ok || *abort_s) break;
         ++ln;
         if (mine_end) {
           ok = mbar_wait_warp(&ofull[w], pieces & 1);
@@ -700,45 +788,63 @@ umma4_kernel(const UmmaParams p) {
         merge = *last_s;
       }
       if (merge) {
-        // rows warp, + 8, ..: the unit's parts and their streams in order
-        constexpr int V = kDim / 32;
-        const int subs = kTwo ? 1 : 2, count = (ti.c1 - ti.c0 + 1) * subs;
-        for (int rr = warp; rr < rows; rr += 8) {
-          const int i = rr / p.group, pos = pv.q_pos[ti.t0 + i];
-          if (pos < 0 || (pos >> pv.logP) >= pv.max_pages) continue;
-          float M = -INFINITY, sum = 0.f, acc[V] = {};
-          for (int k0 = 0; k0 < count; k0 += 4) {
-            float2 s[4];
-            float y[4][V];
+        // Four rows of a warp at a time (warp, + 8, + 16, + 24), the unit's parts and their
+        // streams in order, two of them in flight.
+        constexpr int V = kDim / 32, kR = 4;
+        const int subs = kTwo ? 1 : 2 * reps, count = (ti.c1 - ti.c0 + 1) * subs;
+        for (int r0 = warp; r0 < rows; r0 += 8 * kR) {
+          float M[kR], sum[kR], acc[kR][V] = {};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+          for (int j = 0; j < kR; ++j) {
+            M[j] = -INFINITY;
+            sum[j] = 0.f;
+          }
+          for (int k0 = 0; k0 < count; k0 += 2) {
+            float2 s[2][kR];
+            float y[2][kR][V];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
               const int k = min(k0 + e, count - 1), c = ti.c0 + k / subs;
               const int64_t sl = 3 * static_cast<int64_t>(c) + (!cut ? 2 : c == ti.c0 ? 1 : 0);
-              const int64_t a = (sl * 2 + (kTwo ? rr >> 7 : k % subs)) * 128 + (rr & 127);
-              s[e] = __ldcg(p.ml + a);
-              if constexpr (V == 4)
-                *reinterpret_cast<float4 *>(y[e]) = __ldcg(reinterpret_cast<const float4 *>(p.part + a * kDim + V * lane));
-              else
-                *reinterpret_cast<float2 *>(y[e]) = __ldcg(reinterpret_cast<const float2 *>(p.part + a * kDim + V * lane));
+#pragma unroll
+              for (int j = 0; j < kR; ++j) {
+                const int rr = min(r0 + 8 * j, rows - 1);
+                const int64_t a = (sl * 2 + (kTwo ? rr >> 7 : k & 1)) * 128 + (kTwo ? rr & 127 : rr + 64 * (k % subs >> 1));
+                s[e][j] = __ldcg(p.ml + a);
+                if constexpr (V == 4)
+                  *reinterpret_cast<float4 *>(y[e][j]) = __ldcg(reinterpret_cast<const float4 *>(p.part + a * kDim + V * lane));
+                else
+                  *reinterpret_cast<float2 *>(y[e][j]) = __ldcg(reinterpret_cast<const float2 *>(p.part + a * kDim + V * lane));
+              }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (k0 + e >= count || s[e].x == -INFINITY) continue;  // (nothing, and what lies there may be anything)
-              const float m = max_nan(M, s[e].x);
-              const float f0 = M == m ? 1.f : exp2f(M - m), f1 = s[e].x == m ? 1.f : exp2f(s[e].x - m);
-              M = m;
-              sum = sum * f0 + s[e].y * f1;
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-              for (int j = 0; j < V; ++j) acc[j] = acc[j] * f0 + y[e][j] * f1;
-            }
+              for (int j = 0; j < kR; ++j) {
+                const float x = s[e][j].x;
+                if (k0 + e >= count || x == -INFINITY) continue;  // (nothing, and what lies there may be anything)
+                const float m = max_nan(M[j], x);
+                const float f0 = M[j] == m ? 1.f : exp2f(M[j] - m), f1 = x == m ? 1.f : exp2f(x - m);
+                M[j] = m;
+                sum[j] = sum[j] * f0 + s[e][j].y * f1;
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[j][i] = acc[j][i] * f0 + y[e][j][i] * f1;
+              }
           }
-          const int64_t out_row = static_cast<int64_t>(ti.t0 + i) * pv.H + ti.hk * p.group + rr - i * p.group;
-          const float inv = sum != 0.f ? p.v_gain / sum : 0.f;
 #pragma unroll
-          for (int j = 0; j < V; j += 2)
-            *reinterpret_cast<__nv_bfloat162 *>(p.out + out_row * kDim + V * lane + j) =
-                __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
-          if (lane == 0 && p.lse) p.lse[out_row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+          for (int j = 0; j < kR; ++j) {
+            const int rr = r0 + 8 * j, i = rr / p.group;
+            if (rr >= rows) continue;
+            const int pos = pv.q_pos[ti.t0 + i];
+            if (pos < 0 || (pos >> pv.logP) >= pv.max_pages) continue;
+            const int64_t out_row = static_cast<int64_t>(ti.t0 + i) * pv.H + ti.hk * p.group + rr - i * p.group;
+            const float inv = sum[j] != 0.f ? p.v_gain / sum[j] : 0.f;
+#pragma unroll
+            for (int e = 0; e < V; e += 2)
+              *reinterpret_cast<__nv_bfloat162 *>(p.out + out_row * kDim + V * lane + e) =
+                  __floats2bfloat162_rn(acc[j][e] * inv, acc[j][e + 1] * inv);
+            if (lane == 0 && p.lse) p.lse[out_row] = sum[j] == 0.f ? -INFINITY : (M[j] + log2f(sum[j])) * 0.69314718055994531f;
+          }
         }
       }
       sync();  // (the next part writes its own rows where a merge may still read)

@@ -11,39 +11,55 @@
 
 namespace sa {
 
-// Highest slot of a unit's tokens that are valid, -1 if none is.
-struct UnitSpan {
-  int t0, n, b, last;
-};
-
-// Calls use(span) for the units of token block i; flags its tokens that have to be
-// skipped (status may be NULL).
-template <typename Use>
-__device__ __forceinline__ void units_of_block(const PagedView &v, int nt, int i, uint32_t *status, const Use &use) {
-  const int t1 = min(v.T, (i + 1) * nt);
-  UnitSpan u{0, 0, -1, -1};
-  for (int t = i * nt; t < t1; ++t) {
-    const int b = v.q_seq[t], pos = v.q_pos[t];
-    if (u.n == 0 || b != u.b) {
-      if (u.n > 0) use(u);
-      u = UnitSpan{t, 0, b, -1};
-    }
-    ++u.n;
-    if (b < 0 || b >= v.B)
-      raise_flag(status, kFlagBadSeq);
-    else if (pos < 0 || (pos >> v.logP) >= v.max_pages)
-      raise_flag(status, kFlagBadPos);
-    else
-      u.last = max(u.last, pos);
-  }
-  if (u.n > 0) use(u);
-}
-
 // Where a CTA's range of tiles begins.
 struct UnitStart {
   int block, t0, head, tile;
   long long total;  // tiles of the call
 };
+
+// One warp: calls use(first token, last slot) for the units that begin among tokens
+// t0 .. t1 - 1 (t0 begins one), in order, until it returns false; the slot is -1 for
+// a unit without a valid token.  Tokens that have to be skipped are flagged (status
+// may be NULL).
+template <typename Use>
+__device__ __forceinline__ void units_of_tokens(const PagedView &v, int nt, int t0, int t1, uint32_t *status,
+                                                const Use &use) {
+  const int lane = threadIdx.x & 31;
+  int open = -1, last = -1, prev = 0;  // the unit under way, its last slot; the token before
+  for (int base = t0; base < v.T && (base < t1 || open >= 0); base += 32) {
+    const int t = base + lane;
+    const bool in = t < v.T;
+    const int b = in ? v.q_seq[t] : 0, pos = in ? v.q_pos[t] : -1;
+    int slot = -1;
+    if (in) {
+      const bool bad_seq = b < 0 || b >= v.B, bad_pos = pos < 0 || (pos >> v.logP) >= v.max_pages;
+      if (!bad_seq && !bad_pos)
+        slot = pos;
+      else if (t < t1)
+        raise_flag(status, bad_seq ? kFlagBadSeq : kFlagBadPos);
+    }
+    int before = __shfl_up_sync(0xffffffffu, b, 1);
+    if (lane == 0) before = prev;
+    prev = __shfl_sync(0xffffffffu, b, 31);
+    uint32_t starts = __ballot_sync(0xffffffffu, in && (t == t0 || t % nt == 0 || b != before));
+    // tokens before the first start belong to the unit under way
+    for (int l = 0; l < 32;) {
+      const bool begins = (starts >> l) & 1u;
+      if (begins) {
+        if (open >= 0 && !use(open, last)) return;
+        open = -1;
+        if (base + l >= t1) return;
+        open = base + l;
+        last = -1;
+        starts &= ~(1u << l);
+      }
+      const int end = starts ? __ffs(starts) - 1 : 32;  // (a start at l itself has been taken)
+      last = max(last, __reduce_max_sync(0xffffffffu, lane >= l && lane < end ? slot : -1));
+      l = end;
+    }
+  }
+  if (open >= 0) use(open, last);
+}
 
 // Every thread of the CTA calls it.  CTA c of g takes the tiles total * c / g ..
 // total * (c + 1) / g - 1 with g = min(grid, total / least) (at least one); x0 and
@@ -51,33 +67,69 @@ struct UnitStart {
 // 32 long longs of shared memory.
 __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads, int tile, int least, long long *warp_s,
                                            UnitStart *out, uint32_t *status, long long &x0, long long &x1, int &ctas) {
-  const int blocks = (v.T + nt - 1) / nt, threads = blockDim.x;
-  const int per = (blocks + threads - 1) / threads;
-  const int i0 = min(static_cast<int>(threadIdx.x) * per, blocks), i1 = min(i0 + per, blocks);
+  // warp w takes the units that begin in its stretch of blocks (of whole 32s of tokens,
+  // where a block is one)
+  const int warps = (blockDim.x + 31) >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grain = nt == 1 ? 32 : nt;
+  const int grains = (v.T + grain - 1) / grain, per = (grains + warps - 1) / warps;
+  const int t0 = static_cast<int>(min(static_cast<int64_t>(v.T), static_cast<int64_t>(warp) * per * grain));
+  const int t1 = static_cast<int>(min(static_cast<int64_t>(v.T), (static_cast<int64_t>(warp) + 1) * per * grain));
+  uint32_t *report = blockIdx.x == 0 ? status : nullptr;
   long long sum = 0;
-  for (int i = i0; i < i1; ++i)
-    units_of_block(v, nt, i, blockIdx.x == 0 ? status : nullptr, [&](const UnitSpan &u) { sum += (u.last + tile) / tile; });
+  if (nt == 1) {
+    for (int t = t0 + lane; t < t1; t += 32) {
+      int b, pos;
+      if (load_paged_token(v, t, report, report != nullptr, b, pos)) sum += (pos + tile) / tile;
+    }
+  } else if (t0 < t1) {
+    units_of_tokens(v, nt, t0, t1, report, [&](int, int last) {
+      if (lane == 0) sum += (last + tile) / tile;
+      return true;
+    });
+  }
   sum *= heads;
   long long total;
-  const long long before = block_prefix(sum, warp_s, total);
+  long long before = block_prefix(sum, warp_s, total);
   const long long most = total / least;
   ctas = static_cast<int>(max(1ll, min(static_cast<long long>(gridDim.x), most)));
   const int c = blockIdx.x;
   x0 = c < ctas ? total * c / ctas : total;
   x1 = c < ctas ? total * (c + 1) / ctas : total;
+  // (the warp's first tile and its number of tiles)
+  before = __shfl_sync(0xffffffffu, before, 0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (x0 < x1 && x0 >= before && x0 < before + sum) {
     long long at = before;
-    bool found = false;
-    for (int i = i0; i < i1 && !found; ++i)
-      units_of_block(v, nt, i, nullptr, [&](const UnitSpan &u) {
-        const int cost = (u.last + tile) / tile;
-        if (!found && x0 < at + static_cast<long long>(cost) * heads) {
-          const int rest = static_cast<int>(x0 - at);
-          *out = UnitStart{i, u.t0, rest / cost, rest % cost, total};
-          found = true;
+    auto take = [&](int t, int last) {
+      const int cost = (last + tile) / tile;
+      if (x0 < at + static_cast<long long>(cost) * heads) {
+        const int rest = static_cast<int>(x0 - at);
+        if (lane == 0) *out = UnitStart{t / nt, t, rest / cost, rest % cost, total};
+        return false;
+      }
+      at += static_cast<long long>(cost) * heads;
+      return true;
+    };
+    if (nt == 1) {
+      // 32 tokens at a time: skip those whose tiles end before x0
+      for (int base = t0; base < t1; base += 32) {
+        const int t = base + lane;
+        int b, pos, last = -1;
+        if (t < t1 && load_paged_token(v, t, nullptr, false, b, pos)) last = pos;
+        long long cost = static_cast<long long>((last + tile) / tile) * heads;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+        if (x0 >= at + cost) {
+          at += cost;
+          continue;
         }
-        at += static_cast<long long>(cost) * heads;
-      });
+        for (int l = 0; l < 32; ++l)
+          if (!take(base + l, __shfl_sync(0xffffffffu, last, l))) return;
+      }
+    } else {
+      units_of_tokens(v, nt, t0, t1, nullptr, take);
+    }
   }
 }
 
