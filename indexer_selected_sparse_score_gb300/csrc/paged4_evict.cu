@@ -24,8 +24,6 @@
 namespace sa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeysInSmem = 49152;
 
@@ -39,7 +37,6 @@ struct EvictParams {
   int32_t *length_out;
   int64_t ld;
   int budget, recent, D, share;
-  int cap;        // keys that fit in shared memory
   int list;       // entries of a CTA's lists
   int2 *lists;    // [CTA][list]: (freed slot, staying slot)
   uint32_t *status;
@@ -47,6 +44,7 @@ struct EvictParams {
 
 // Every thread of the CTA calls it: the sum of v over the warps before this one
 // (v alike in a warp), and over all.
+template <int kWarps>
 __device__ __forceinline__ int warp_prefix(int v, int *s, int &total) {
   const int warp = threadIdx.x >> 5;
   __syncthreads();
@@ -62,9 +60,11 @@ __device__ __forceinline__ int warp_prefix(int v, int *s, int &total) {
   return before;
 }
 
-template <bool kCached>
-__global__ void __launch_bounds__(kThreads)
+// kThreads: 256 for short rows, four CTAs to an SM; 1024 for long ones.
+template <bool kCached, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 evict4_kernel(const EvictParams p) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ uint32_t keys_s[];
   __shared__ int hist[kBins];
   __shared__ int scan[kWarps];
@@ -117,9 +117,15 @@ evict4_kernel(const EvictParams p) {
       }
       if ((x & mask) == prefix) {
         const uint32_t d = (x >> shift) & ((1u << bits) - 1);
-        // (the recent slots are alike: one addition a warp for those of its first lane's digit)
-        const uint32_t peers = __match_any_sync(__activemask(), d);
-        if (lane == __ffs(peers) - 1) atomicAdd(&hist[d], __popc(peers));
+        // (many may be alike, the recent slots are: one addition for those of the first
+        // lane's digit)
+        const uint32_t active = __activemask();
+        const int lead = __ffs(active) - 1;
+        const uint32_t same = __ballot_sync(active, d == __shfl_sync(active, d, lead));
+        if (lane == lead)
+          atomicAdd(&hist[d], __popc(same));
+        else if (!((same >> lane) & 1u))
+          atomicAdd(&hist[d], 1);
       }
     }
     __syncthreads();
@@ -138,7 +144,7 @@ evict4_kernel(const EvictParams p) {
       if (lane >= o) up += v;
     }
     int total;
-    int above = warp_prefix(__shfl_sync(0xffffffffu, up, 31), scan, total) + up - sum;
+    int above = warp_prefix<kWarps>(__shfl_sync(0xffffffffu, up, 31), scan, total) + up - sum;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       if (above < need && above + own[e] >= need) pick = make_int2(kBins - 1 - (tid * kPer + e), above);
@@ -156,7 +162,7 @@ evict4_kernel(const EvictParams p) {
   int ties = 0, total;
   for (int j = j0 + lane; j - lane < j1; j += 32)
     ties += __popc(__ballot_sync(0xffffffffu, j < j1 && key(j) == prefix));
-  const int ties_before = warp_prefix(ties, scan, total);
+  const int ties_before = warp_prefix<kWarps>(ties, scan, total);
   // walk(use): use(j, kept, in) for 32 slots at a time, with the ballots of it
   auto walk = [&](const auto &use) {
     int seen = ties_before;
@@ -176,7 +182,7 @@ evict4_kernel(const EvictParams p) {
     movers += __popc(__ballot_sync(0xffffffffu, kept && j >= keep));
   });
   int moves;
-  int hole = warp_prefix(holes, scan, moves), mover = warp_prefix(movers, scan, total);
+  int hole = warp_prefix<kWarps>(holes, scan, moves), mover = warp_prefix<kWarps>(movers, scan, total);
   int2 *list = p.lists + static_cast<int64_t>(blockIdx.x) * p.list;
   walk([&](int j, bool kept, bool in) {
     const bool is_hole = in && !kept && j < keep, is_mover = kept && j >= keep;
@@ -203,7 +209,7 @@ evict4_kernel(const EvictParams p) {
   // 16 lanes a row: codes of K and V (D / 2 bytes each) and scales
   const int sub = lane & 15, mine = (moves - part + p.share - 1) / p.share;
   const int chunks = p.D / 32;  // 16-byte chunks of a row's codes
-  constexpr int kRows = 4;      // rows a group of lanes has in flight
+  constexpr int kRows = 2;      // rows a group of lanes has in flight
   const int groups = 2 * kWarps;
   for (int i0 = 2 * warp + (lane >> 4); i0 < mine; i0 += kRows * groups) {
     uint4 x[kRows];
@@ -270,6 +276,14 @@ int share_of(const sa_paged4_args &pa) {
   const int64_t rows = static_cast<int64_t>(pa.p.B) * pa.p.H_kv;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, sm_count() / rows)));
 }
+template <int kThreads>
+cudaError_t launch_cached(const EvictParams &p, dim3 grid, int most, cudaStream_t stream) {
+  auto kern = evict4_kernel<true, kThreads>;
+  static bool done[64] = {};
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), kKeysInSmem * 4, done);
+  if (e != cudaSuccess) return e;
+  return launch_ex(false, kern, grid, dim3(kThreads), static_cast<size_t>(most) * 4, stream, 1, p);
+}
 int list_of(const sa_paged4_args &pa) { return (pa.p.max_pages * pa.p.P / 2) / share_of(pa) + 1; }
 
 }  // namespace
@@ -299,13 +313,9 @@ cudaError_t launch_evict4(const sa_paged4_args &pa, const int32_t *length, const
   p.lists = static_cast<int2 *>(scratch);
   p.status = status;
   const int most = pa.p.max_pages * pa.p.P;
-  p.cap = std::min(most, kKeysInSmem);
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(pa.p.B) * pa.p.H_kv * p.share));
-  if (most > kKeysInSmem) return launch_ex(false, evict4_kernel<false>, grid, dim3(kThreads), 0, stream, 1, p);
-  static bool done[64] = {};
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(evict4_kernel<true>), kKeysInSmem * 4, done);
-  if (e != cudaSuccess) return e;
-  return launch_ex(false, evict4_kernel<true>, grid, dim3(kThreads), static_cast<size_t>(most) * 4, stream, 1, p);
+  if (most > kKeysInSmem) return launch_ex(false, evict4_kernel<false, 1024>, grid, dim3(1024), 0, stream, 1, p);
+  return most > 8192 ? launch_cached<1024>(p, grid, most, stream) : launch_cached<256>(p, grid, most, stream);
 }
 
 }  // namespace sa

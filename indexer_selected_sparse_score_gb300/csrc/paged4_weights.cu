@@ -1,29 +1,33 @@
 // The attention weight that every slot of a 4-bit cache gathers in a call: the sum
 // over the call's tokens and the heads of a KV head of exp(logit - lse).
 //
-// Keys stay, queries pass: a tile of 128 slots belongs to one CTA, which takes
-// every token of the sequence's run of tokens against it, so a slot's sum has one
-// owner and one order.  A warp holds 16 keys as fp16 operands in registers
-// (layout as in paged4_attn.cu) and takes eight columns (token, head) at a time:
+// Keys stay, queries pass: 32 slots belong to one warp, which takes every token of
+// the sequence's run of tokens against them, so a slot's sum has one owner and one
+// order, and warps need nothing of each other.  A warp turns the codes of its slots
+// into fp16 operands in registers (layout as in paged4_attn.cu) and takes eight
+// columns (token, head) at a time:
 //   S^T = K Q^T, M = 16 keys, N = 8 columns, K = D;  w = 2^(S cs - lse log2 e)
-// A decode step is bound by HBM (72 bytes of codes a slot and KV head at D = 128,
-// and its record read and written); a chunk by the products.
+// Its codes come through a ring of its own by asynchronous copies.  A decode step is
+// bound by HBM (72 bytes of codes a slot and KV head at D = 128, and its record read
+// and written); a chunk by the products.
 #include <algorithm>
 
 #include "internal.h"
 #include "paged4_mma.cuh"
 #include "paged4_units.cuh"
-#include "umma.cuh"
+#include "paged_umma.cuh"
 
 namespace sa {
 namespace {
 
 using namespace umma;
 
-constexpr int kTile = 128;
+constexpr int kTile = 32;                // slots of a warp's step
 constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps + 32;
-constexpr int kRunsInSmem = 1024;  // tokens whose runs a CTA works out by itself
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCtasPerSm = 2;            // 16 warps of 128 registers (three CTAs spill: 55 us against 49)
+constexpr int kStages = 4;               // tiles that a warp has in its ring
+constexpr int kRunsInSmem = 256;         // tokens whose runs a CTA works out by itself
 
 struct WeightsParams {
   Paged4View c;
@@ -38,26 +42,16 @@ struct WeightsParams {
   uint32_t *status;
 };
 
-struct TileInfo {
-  int t0, n, hk, b, base, last;
-  uint32_t have;
-  int first;
-};
-
 template <int kDim>
 struct WeightsSmem {
-  static constexpr int kStages = kDim == 128 ? 6 : 8;
   static constexpr uint32_t kCodes = kTile * kDim / 2, kScales = kTile * kDim / 16;
   static constexpr uint32_t kStage = kCodes + kScales;
-  static constexpr size_t info = static_cast<size_t>(kStages) * kStage;
-  static constexpr size_t bars = info + kStages * sizeof(TileInfo);
-  static constexpr size_t scan = bars + 2 * kStages * 8;
+  static constexpr size_t scan = static_cast<size_t>(kWarps) * kStages * kStage;
   static constexpr size_t off = scan + 32 * 8;
   static constexpr size_t t0 = off + (kRunsInSmem + 1) * 8;
   static constexpr size_t last = t0 + (kRunsInSmem + 2) * 4;
-  static constexpr size_t flag = last + kRunsInSmem * 4;
-  static constexpr size_t total = flag + 16;
-  static_assert(sizeof(TileInfo) % 8 == 0 && t0 % 8 == 0, "alignment");
+  static constexpr size_t total = last + kRunsInSmem * 4;
+  static_assert(t0 % 8 == 0 && (total + 1024) * kCtasPerSm <= 228 * 1024, "layout");
 };
 
 __global__ void __launch_bounds__(1024) plan_kernel(const PagedView v, const Runs r, int *n_runs, uint32_t *status) {
@@ -67,24 +61,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PagedView v, const Run
 }
 
 template <int kDim>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
 weights4_kernel(const WeightsParams p) {
   using L = WeightsSmem<kDim>;
-  constexpr int kStages = L::kStages, kFr = kDim / 32;
+  constexpr int kFr = kDim / 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bars), *empty = full + kStages;
-  TileInfo *infos = reinterpret_cast<TileInfo *>(smem + L::info);
-  volatile int *flags = reinterpret_cast<volatile int *>(smem + L::flag);
   const PagedView &pv = p.c.v;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
-    }
-    flags[0] = 0;
-    fence_barrier_init();
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Runs r = p.runs;
   int runs;
   if (pv.T <= kRunsInSmem) {
@@ -93,119 +76,58 @@ weights4_kernel(const WeightsParams p) {
     runs = plan_runs(pv, kTile, reinterpret_cast<long long *>(smem + L::scan), r, blockIdx.x == 0 ? p.status : nullptr);
   } else {
     runs = *p.n_runs;
-    __syncthreads();
   }
   const long long total = r.off[runs];
-  const long long x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
+  // warp w of all takes the tiles total * w / warps ..: a CTA's are far apart, so that
+  // the warps of an SM do not end together
+  const int workers = gridDim.x * kWarps, me = warp * gridDim.x + blockIdx.x;
+  long long x = total * me / workers;
+  const long long x1 = total * (me + 1) / workers;
+  if (x >= x1) return;
 
-  if (warp == kWarps) {
-    int issued = 0;
-    bool ok = true;
-    if (x0 < x1) {
-      int run = run_of_tile(r.off, runs, x0);
-      long long x = x0;
-      for (; x < x1 && ok; ++run) {
-        const int last = r.last[run], cost = (last + kTile) / kTile;
-        if (cost == 0) continue;
-        const int t0 = r.t0[run], n = r.t0[run + 1] - t0, seq = pv.q_seq[t0];
-        int rest = static_cast<int>(x - r.off[run]);
-        int hk = rest / cost, kt = rest - hk * cost;
-        bool fresh = true;
-        for (; hk < pv.H_kv && x < x1; ++x) {
-          const int s = issued % kStages;
-          // lane 2 q + kind copies page q's part: codes, scales
-          const int base = kt * kTile, q = lane >> 1, kind = lane & 1, from = base + (q << pv.logP);
-          const int rows = min(pv.P, ((min(last - from, kTile) + 16) & ~15));
-          int page = -1;
-          if (q < (kTile >> pv.logP) && from <= last) page = load_page(pv, seq, from >> pv.logP, p.status, kind == 0);
-          const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0 && kind == 0);
-          uint32_t have = 0;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) have |= ((pages >> (2 * ((16 * w) >> pv.logP))) & 1u) << w;
-          const uint32_t row_bytes = kind ? kDim / 16 : kDim / 2;
-          const uint32_t bytes = page >= 0 ? rows * row_bytes : 0u;
-          const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
-          if (!mbar_wait_warp(&empty[s], ((issued / kStages) & 1) ^ 1) || flags[0]) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            infos[s] = TileInfo{t0, n, hk, seq, base, last, have, fresh};
-            mbar_expect_tx(&full[s], sum);
-          }
-          __syncwarp();
-          ++issued;
-          if (bytes) {
-            const int64_t at = (static_cast<int64_t>(page) * pv.H_kv + hk) * pv.P * row_bytes;
-            bulk_load(smem + s * L::kStage + (kind ? L::kCodes : 0) + (q << pv.logP) * row_bytes,
-                      (kind ? p.c.Ks : p.c.K) + at, bytes, &full[s]);
-          }
-          fresh = false;
-          if (++kt == cost) {
-            kt = 0;
-            ++hk;
-            fresh = true;
-          }
-        }
-      }
-    }
-    if (lane == 0) {
-      if (!ok) {
-        raise_flag(p.status, kFlagTimeout);
-        flags[0] = 1;
-      }
-      for (int m = max(0, issued - kStages); m < issued; ++m) mbar_wait(&full[m % kStages], (m / kStages) & 1);
-    }
-    __syncwarp();
-    return;
-  }
-
-  // --------------------------------------------------------- product warps
   const int g = lane >> 2, tq = lane & 3;
-  long long left = x1 - x0;
-  uint4 qr[kFr] = {};
-  float cs[2] = {}, ls[2] = {};
-  int lim[2] = {-1, -1};
+  uint8_t *ring = smem + warp * kStages * L::kStage;
+  const uint32_t ring_s = smem_u32(ring);
+  uint4 qr[kFr];
+  float cs[2], ls[2];
+  int lim[2];
   // Columns 8 c .. 8 c + 7 of a unit: fragments of the column g, and the factor,
   // logarithm and limit of columns 2 t and 2 t + 1.
   auto load_columns = [&](int t0, int ncols, int hk, int c) {
     const int col = 8 * c + g;
-    float x[kDim / 4], top = 0.f;
     const bool in = col < ncols;
     const int i = in ? col / p.group : 0, h = in ? hk * p.group + col - i * p.group : 0;
     const uint4 *src =
         reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(t0 + i) * pv.H + h) * kDim + kDim / 4 * tq);
-#pragma unroll
-    for (int j = 0; j < kFr; ++j) {
-      const uint4 w = in ? src[j] : make_uint4(0, 0, 0, 0);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[8 * j + 2 * e] = __uint_as_float(u[e] << 16);
-        x[8 * j + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-      }
+    float l = 0.f, top = 0.f;
+    int pos = -1;
+    if (in) {
+      l = p.lse[static_cast<int64_t>(t0 + i) * pv.H + h] * kLog2e;
+      pos = pv.q_pos[t0 + i];
     }
 #pragma unroll
-    for (int e = 0; e < kDim / 4; ++e) top = fmaxf(top, fabsf(x[e]));
+    for (int j = 0; j < kFr; ++j) qr[j] = in ? src[j] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < kFr; ++j) {
+      const uint32_t u[4] = {qr[j].x, qr[j].y, qr[j].z, qr[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xFFFF0000u))));
+    }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const float f = to_half_factor(top), own = p.qk_scale / f;
 #pragma unroll
     for (int j = 0; j < kFr; ++j) {
-      uint32_t u[4];
+      uint32_t u[4] = {qr[j].x, qr[j].y, qr[j].z, qr[j].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = as_u32(__floats2half2_rn(x[8 * j + 2 * e] * f, x[8 * j + 2 * e + 1] * f));
+      for (int e = 0; e < 4; ++e)
+        u[e] = as_u32(__floats2half2_rn(__uint_as_float(u[e] << 16) * f, __uint_as_float(u[e] & 0xFFFF0000u) * f));
       qr[j] = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    // (column g's factor and row are in the lanes of group g)
-    float l = 0.f;
-    int pos = -1;
-    if (in) {
-      const int t = t0 + i;
-      l = p.lse[static_cast<int64_t>(t) * pv.H + h] * kLog2e;
-      const int at = pv.q_pos[t];
-      if (l != -INFINITY && at >= 0 && (at >> pv.logP) < pv.max_pages) pos = at;
-    }
+    // (column g's factor and row are in the lanes of group g; a row whose lse is -inf
+    // adds nothing)
+    if (pos < 0 || (pos >> pv.logP) >= pv.max_pages || l == -INFINITY) pos = -1;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int from = 4 * (2 * tq + e);
@@ -214,62 +136,104 @@ weights4_kernel(const WeightsParams p) {
       lim[e] = __shfl_sync(0xffffffffu, pos, from);
     }
   };
-  bool ok = true;
-  for (int n = 0; left > 0; ++n, --left) {
-    const int s = n % kStages;
-    if (!mbar_wait_warp(&full[s], (n / kStages) & 1)) {
-      ok = false;
-      break;
-    }
-    const TileInfo ti = infos[s];
-    const int ncols = ti.n * p.group, groups = (ncols + 7) / 8;
-    if (ti.first && groups == 1) load_columns(ti.t0, ncols, ti.hk, 0);
-    const int base = ti.base + 16 * warp;
-    const bool live = ((ti.have >> warp) & 1u) && base <= ti.last;
-    __half2 a[2][kFr][4];
-    if (live) {
-      const uint8_t *k = smem + s * L::kStage + 16 * warp * (kDim / 2);
-      KeyRows<kDim> rows;
-      rows.load(k, smem + s * L::kStage + L::kCodes + 16 * warp * (kDim / 16), g, tq);
+  for (int run = run_of_tile(r.off, runs, x); x < x1; ++run) {
+    const int last = r.last[run], cost = (last + kTile) / kTile;
+    if (cost == 0) continue;
+    const int t0 = r.t0[run], n = r.t0[run + 1] - t0, seq = pv.q_seq[t0];
+    const int ncols = n * p.group, groups = (ncols + 7) / 8;
+    const int rest = static_cast<int>(x - r.off[run]);
+    int hk = rest / cost, kt0 = rest - hk * cost;
+    for (; hk < pv.H_kv && x < x1; ++hk, kt0 = 0) {
+      const int count = static_cast<int>(min(static_cast<long long>(cost - kt0), x1 - x));
+      x += count;
+      // lane l: the page of the l-th 16 slots from here on, two of each tile
+      auto load_ids = [&](int i) {
+        const int slot = kTile * (kt0 + i + (lane >> 1)) + 16 * (lane & 1);
+        if (i + (lane >> 1) >= count || slot > last) return -1;
+        return load_page(pv, seq, slot >> pv.logP, p.status, true);
+      };
+      int ids = load_ids(0), ids_next = -1;
+      uint32_t held = __ballot_sync(0xffffffffu, ids >= 0), held_now = held;
+      auto copy = [&](int i) {
+        if (i < count) {
+          const int id0 = __shfl_sync(0xffffffffu, ids, (2 * i) & 31), id1 = __shfl_sync(0xffffffffu, ids, (2 * i + 1) & 31);
+          const uint32_t st = ring_s + (i % kStages) * L::kStage;
+          const int slot = kTile * (kt0 + i);
+          const int64_t row0 = (static_cast<int64_t>(max(id0, 0) * pv.H_kv + hk) << pv.logP) + (slot & (pv.P - 1));
+          const int64_t row1 = (static_cast<int64_t>(max(id1, 0) * pv.H_kv + hk) << pv.logP) + ((slot + 16) & (pv.P - 1));
+          const uint32_t b0 = id0 >= 0 ? 16u : 0u, b1 = id1 >= 0 ? 16u : 0u;
+          const uint8_t *s0 = p.c.K + row0 * (kDim / 2) + 16 * lane, *s1 = p.c.K + row1 * (kDim / 2) + 16 * lane;
 #pragma unroll
-      for (int i = 0; i < kFr; ++i) {
-        rows.values(0, i, a[0][i]);
-        rows.values(1, i, a[1][i]);
+          for (int e = 0; e < kDim / 64; ++e) {
+            cp_async16_or_zero(st + 16 * lane + 512 * e, s0 + 512 * e, b0);
+            cp_async16_or_zero(st + 16 * lane + 8 * kDim + 512 * e, s1 + 512 * e, b1);
+          }
+          constexpr int kSc = kDim / 16;  // chunks of the scales of 16 rows
+          if (lane < 2 * kSc)
+            cp_async16_or_zero(st + L::kCodes + 16 * lane,
+                               p.c.Ks + (lane < kSc ? row0 : row1) * (kDim / 16) + 16 * (lane % kSc), lane < kSc ? b0 : b1);
+        }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) copy(i);
+      if (groups == 1) load_columns(t0, ncols, hk, 0);
+      float *weight = p.weight + (static_cast<int64_t>(seq) * pv.H_kv + hk) * p.ld;
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        const int ahead = i + kStages - 1;
+        if ((ahead & 15) == 0) {
+          ids = ids_next;
+          held = __ballot_sync(0xffffffffu, ids >= 0);
+        }
+        if ((i & 15) == 0) held_now = held;  // (ahead is among the same)
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        copy(ahead);
+        if ((ahead & 15) == 4) ids_next = load_ids(ahead - 4 + 16);
+        const int base = kTile * (kt0 + i);
+        const uint32_t halves = (held_now >> (2 * (i & 15))) & 3u;
+        if (!halves) continue;
+        const uint8_t *st = ring + (i % kStages) * L::kStage;
+        KeyRows<kDim> rows[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rows[h].load(st + h * (8 * kDim), st + L::kCodes + h * kDim, g, tq);
+        float sum[4] = {};  // of rows g, g + 8, g + 16, g + 24
+        for (int c = 0; c < groups; ++c) {
+          if (groups > 1) load_columns(t0, ncols, hk, c);
+          float acc[2][4] = {};
+#pragma unroll
+          for (int j = 0; j < kFr; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              __half2 a[4], b[4];
+              rows[h].values(0, j, a);
+              rows[h].values(1, j, b);
+              mma_16816(acc[h], as_u32(a[0]), as_u32(b[0]), as_u32(a[1]), as_u32(b[1]), qr[j].x, qr[j].y);
+              mma_16816(acc[h], as_u32(a[2]), as_u32(b[2]), as_u32(a[3]), as_u32(b[3]), qr[j].z, qr[j].w);
+            }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float w = exp2_fast(fmaf(acc[h][e], cs[e & 1], -ls[e & 1]));
+              if (base + 16 * h + g + 4 * (e & 2) <= lim[e & 1]) sum[2 * h + (e >> 1)] += w;
+            }
+        }
+        // over the columns; lane (g, t) gets row g + 8 t
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+        }
+        const float own = tq == 0 ? sum[0] : tq == 1 ? sum[1] : tq == 2 ? sum[2] : sum[3];
+        const int slot = base + g + 8 * tq;
+        // one addition a slot and run (a sequence in several runs adds in any order)
+        if (slot <= last && ((halves >> (tq >> 1)) & 1u)) atomicAdd(weight + slot, own);
       }
+      cp_async_wait<0>();
+      __syncwarp();
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
-    if (!live) continue;
-    float sum[2] = {};
-    for (int c = 0; c < groups; ++c) {
-      if (groups > 1) load_columns(ti.t0, ncols, ti.hk, c);
-      float acc[2][4] = {};
-#pragma unroll
-      for (int i = 0; i < kFr; ++i) {
-        mma_16816(acc[0], as_u32(a[0][i][0]), as_u32(a[1][i][0]), as_u32(a[0][i][1]), as_u32(a[1][i][1]), qr[i].x, qr[i].y);
-        mma_16816(acc[1], as_u32(a[0][i][2]), as_u32(a[1][i][2]), as_u32(a[0][i][3]), as_u32(a[1][i][3]), qr[i].z, qr[i].w);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float w = exp2_fast(fmaf(acc[0][e] + acc[1][e], cs[e & 1], -ls[e & 1]));
-        if (base + g + 4 * (e & 2) <= lim[e & 1]) sum[e >> 1] += w;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-      sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-    }
-    // one addition a slot and run (a sequence in several runs adds in any order)
-    if (tq < 2) {
-      const int slot = base + g + 8 * tq;
-      if (slot <= ti.last)
-        atomicAdd(p.weight + (static_cast<int64_t>(ti.b) * pv.H_kv + ti.hk) * p.ld + slot, tq ? sum[1] : sum[0]);
-    }
-  }
-  if (!ok && lane == 0) {
-    raise_flag(p.status, kFlagTimeout);
-    flags[0] = 1;
   }
 }
 
@@ -281,7 +245,7 @@ cudaError_t launch(const WeightsParams &p, cudaStream_t stream) {
   static bool done[64] = {};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), WeightsSmem<kDim>::total, done);
   if (e != cudaSuccess) return e;
-  return launch_ex(false, kern, dim3(2 * sm_count()), dim3(kThreads), WeightsSmem<kDim>::total, stream, 1, p);
+  return launch_ex(false, kern, dim3(kCtasPerSm * sm_count()), dim3(kThreads), WeightsSmem<kDim>::total, stream, 1, p);
 }
 
 }  // namespace
