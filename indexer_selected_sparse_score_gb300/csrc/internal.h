@@ -164,6 +164,13 @@ size_t attn4_umma_scratch(const sa_paged4_args &pa);
 cudaError_t launch_weights4(const sa_paged4_args &pa, const void *q, const float *lse, float *weight, int64_t ld,
                             void *scratch, uint32_t *status, cudaStream_t stream);
 size_t weights4_scratch(const sa_paged4_args &pa);
+// On the 5th-generation tensor cores.
+cudaError_t launch_weights4_umma(const sa_paged4_args &pa, const void *q, const float *lse, float *weight, int64_t ld,
+                                 void *scratch, uint32_t *status, cudaStream_t stream);
+size_t weights4_umma_scratch(const sa_paged4_args &pa);
+// Query columns that a call's units have in common keys: heads of a KV head times the
+// tokens that a sequence has on average (one, where every sequence can have its own).
+int columns_of(const sa_paged4_args &pa);
 cudaError_t launch_evict4(const sa_paged4_args &pa, const int32_t *length, const int32_t *newest, int budget, int recent,
                           const float *weight, const int32_t *born, float *weight_out, int32_t *born_out, int64_t ld,
                           int32_t *length_out, void *scratch, uint32_t *status, cudaStream_t stream);

@@ -379,14 +379,12 @@ cudaError_t launch(const Attn4Params &p, cudaStream_t stream) {
 size_t most_parts() { return 2 * static_cast<size_t>(grid_of()); }
 size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Query columns that a call's units have in common keys: heads of a KV head times the
-// tokens that a sequence has on average (one, where every sequence can have its own).
+}  // namespace
+
 int columns_of(const sa_paged4_args &pa) {
   const int64_t each = (pa.p.T + static_cast<int64_t>(pa.p.B) - 1) / pa.p.B;
   return static_cast<int>(std::min<int64_t>(std::max<int64_t>(each, 1) * (pa.p.H / pa.p.H_kv), 1 << 20));
 }
-
-}  // namespace
 
 size_t attn4_scratch(const sa_paged4_args &pa) {
   if (columns_of(pa) > 16) return attn4_umma_scratch(pa);

@@ -27,6 +27,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;            // 16 warps of 128 registers (three CTAs spill: 55 us against 49)
 constexpr int kStages = 4;               // tiles that a warp has in its ring
+constexpr int kMostColumns = 32;          // of a unit, on average; more: paged4_weights_umma.cu
 constexpr int kRunsInSmem = 256;         // tokens whose runs a CTA works out by itself
 
 struct WeightsParams {
@@ -251,12 +252,14 @@ cudaError_t launch(const WeightsParams &p, cudaStream_t stream) {
 }  // namespace
 
 size_t weights4_scratch(const sa_paged4_args &pa) {
+  if (columns_of(pa) > kMostColumns) return weights4_umma_scratch(pa);
   return round_up((static_cast<size_t>(pa.p.T) + 2) * 8) + 2 * round_up((static_cast<size_t>(pa.p.T) + 2) * 4) + 256;
 }
 
 cudaError_t launch_weights4(const sa_paged4_args &pa, const void *q, const float *lse, float *weight, int64_t ld,
                             void *scratch, uint32_t *status, cudaStream_t stream) {
   if (pa.p.T == 0) return cudaSuccess;
+  if (columns_of(pa) > kMostColumns) return launch_weights4_umma(pa, q, lse, weight, ld, scratch, status, stream);
   WeightsParams p;
   p.c = paged4_view(pa);
   p.q = static_cast<const uint16_t *>(q);
