@@ -10,7 +10,7 @@
 //
 // An item is (run, KV head, 128 slots): its keys are converted once, and the tiles of
 // the run's tokens pass them; an item is one CTA's, so a slot's sum has one owner and
-// one order.  Tiles' logits go to four buffers of tensor memory that two warpgroups
+// one order.  Tiles' logits go to four buffers of tensor memory that four warpgroups
 // empty in turn; bound by the exponentials (32 a clock and SM: 512 clocks a tile)
 // beside the products (512 clocks).
 #include <climits>
@@ -28,12 +28,14 @@ namespace {
 using namespace umma;
 
 constexpr int kTile = 128;
-constexpr int kThreads = 512;
-constexpr int kWarpConv = 8;    // .. 11
-constexpr int kWarpMma = 12;
-constexpr int kWarpCopy = 13;
-constexpr int kWarpInfo = 14;   // (15 only joins the block barriers)
+constexpr int kGroups = 4;         // warpgroups that sum (with two 139 us for a chunk that takes 99, three 101)
+constexpr int kWarpConv = 4 * kGroups;    // and the next three
+constexpr int kWarpMma = kWarpConv + 4;
+constexpr int kWarpCopy = kWarpMma + 1;
+constexpr int kWarpInfo = kWarpMma + 2;   // (the last one only joins the block barriers)
+constexpr int kThreads = 32 * (kWarpMma + 4);
 constexpr int kInfos = 4, kBufs = 4;
+constexpr int kConsts = 8;      // tiles whose factors and limits are held (longer than their queries)
 
 // A tile of columns as the first kernel leaves it.
 template <int kDim>
@@ -44,6 +46,7 @@ struct ColumnTile {
   static constexpr uint32_t limit = factor + 64 * 16;        // [128]: the column's last slot, -1: it adds nothing
   static constexpr uint32_t low = limit + 128 * 4;           // lowest limit of the tile's columns; highest
   static constexpr uint32_t total = low + 64;
+  static constexpr uint32_t consts = total - factor;
 };
 
 struct ItemInfo {
@@ -59,13 +62,14 @@ struct WSmem {
   using Q = ColumnTile<kDim>;
   static constexpr int kSlots = 3;                          // tiles of columns
   static constexpr uint32_t kKeys = Q::kBlock * (kDim / 64);
-  static constexpr uint32_t kQ = (Q::total + 1023) & ~1023u;
+  static constexpr uint32_t kQ = Q::factor;
   static constexpr size_t keys = 0;                         // [2]
   static constexpr size_t q = keys + 2 * kKeys;
-  static constexpr size_t info = q + kSlots * kQ;
-  static constexpr size_t sums = info + kInfos * sizeof(ItemInfo);  // [128] of the second warpgroup
-  static constexpr size_t bars = sums + 512;
-  static constexpr int kBars = 2 * 2 + 2 * kSlots + 2 * kBufs + 2 * kInfos + 2 + 1;
+  static constexpr size_t consts = q + kSlots * kQ;         // [kConsts]
+  static constexpr size_t info = consts + kConsts * Q::consts;
+  static constexpr size_t sums = info + kInfos * sizeof(ItemInfo);  // [128] of each further warpgroup
+  static constexpr size_t bars = sums + (kGroups - 1) * 512;
+  static constexpr int kBars = 2 * 2 + 2 * kSlots + 2 * kConsts + 2 * kBufs + 2 * kInfos + 2 + 1;
   static constexpr size_t misc = bars + kBars * 8;
   static constexpr size_t total = misc + 16;
   static_assert(total + 1024 <= 232448 && sizeof(ItemInfo) % 16 == 0, "shared memory budget");
@@ -164,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
   ItemInfo *infos = reinterpret_cast<ItemInfo *>(smem + L::info);
   float *sums = reinterpret_cast<float *>(smem + L::sums);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
-  uint64_t *kfull = bars, *kempty = kfull + 2, *qfull = kempty + 2, *qempty = qfull + L::kSlots, *sfull = qempty + L::kSlots;
+  uint64_t *kfull = bars, *kempty = kfull + 2, *qfull = kempty + 2, *qempty = qfull + L::kSlots, *cfull = qempty + L::kSlots;
+  uint64_t *cempty = cfull + kConsts, *sfull = cempty + kConsts;
   uint64_t *sempty = sfull + kBufs, *ifull = sempty + kBufs, *iempty = ifull + kInfos, *meet = iempty + kInfos, *done = meet + 2;
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 4);
@@ -174,11 +179,15 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kfull[i], 4);
       mbar_init(&kempty[i], 1);
-      mbar_init(&meet[i], 4);  // [0]: the second warpgroup's sums are there; [1]: they have been read
+      mbar_init(&meet[i], i == 0 ? 4 * (kGroups - 1) : 4);  // [0]: the further warpgroups' sums are there; [1]: they have been read
     }
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(&qfull[i], 1);
-      mbar_init(&qempty[i], 5);  // the issuer's products and four softmax warps
+      mbar_init(&qempty[i], 1);
+    }
+    for (int i = 0; i < kConsts; ++i) {
+      mbar_init(&cfull[i], 1);
+      mbar_init(&cempty[i], 4);
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&sfull[i], 1);
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
     }
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&ifull[i], 1);
-      mbar_init(&iempty[i], 14);  // softmax, converting, issuing and copying warps
+      mbar_init(&iempty[i], 4 * kGroups + 6);  // softmax, converting, issuing and copying warps
     }
     mbar_init(done, 1);
     *abort_s = 0;
@@ -262,12 +271,16 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
       if (!item_of(n, it)) break;
       for (int b = it.b0; b <= it.b1; ++b, ++m) {
         const int s = m % L::kSlots;
-        ok = wait_warp(&qempty[s], ((m / L::kSlots) & 1) ^ 1) && !*abort_s;
+        const int cslot = m % kConsts;
+        ok = wait_warp(&qempty[s], ((m / L::kSlots) & 1) ^ 1) && wait_warp(&cempty[cslot], ((m / kConsts) & 1) ^ 1) &&
+             !*abort_s;
         if (!ok) break;
         if (leader) {
-          mbar_expect_tx(&qfull[s], Q::total);
-          bulk_load(smem + L::q + s * L::kQ, p.tiles + (static_cast<size_t>(it.hk) * p.blocks + b) * Q::total, Q::total,
-                    &qfull[s]);
+          const uint8_t *src = p.tiles + (static_cast<size_t>(it.hk) * p.blocks + b) * Q::total;
+          mbar_expect_tx(&qfull[s], L::kQ);
+          bulk_load(smem + L::q + s * L::kQ, src, L::kQ, &qfull[s]);
+          mbar_expect_tx(&cfull[cslot], Q::consts);
+          bulk_load(smem + L::consts + cslot * Q::consts, src + Q::factor, Q::consts, &cfull[cslot]);
         }
         __syncwarp();
       }
@@ -276,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
       if (!ok) fail();
       // every copy lands before the CTA exits
       for (int k = max(0, m - L::kSlots); k < m; ++k) mbar_wait(&qfull[k % L::kSlots], (k / L::kSlots) & 1);
+      for (int k = max(0, m - kConsts); k < m; ++k) mbar_wait(&cfull[k % kConsts], (k / kConsts) & 1);
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
@@ -369,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
       ++live;
     }
     if (!ok && lane == 0) fail();
-  } else if (warp < 8) {
-    // -------------------------------- sums: a warpgroup takes every second tile
+  } else if (warp < kWarpConv) {
+    // ------------------------------- sums: a warpgroup takes every kGroups-th tile
     const int w = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     int m = 0, met = 0;
@@ -382,12 +396,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
       const bool held = slot <= it.last && ((it.have >> (row >> 4)) & 1u);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int b = it.b0; b <= it.b1; ++b, ++m) {
-        if ((m & 1) != w) continue;
-        const int s = m % L::kSlots, buf = m % kBufs;
-        ok = wait_warp(&sfull[buf], (m / kBufs) & 1) && wait_warp(&qfull[s], (m / L::kSlots) & 1) && !*abort_s;
+        if (m % kGroups != w) continue;
+        const int cslot = m % kConsts, buf = m % kBufs;
+        ok = wait_warp(&sfull[buf], (m / kBufs) & 1) && wait_warp(&cfull[cslot], (m / kConsts) & 1) && !*abort_s;
         if (!ok) break;
         tc_fence_after();
-        const uint8_t *tile = smem + L::q + s * L::kQ;
+        const uint8_t *tile = smem + L::consts + cslot * Q::consts - Q::factor;
         // columns of this run, and whether all of them see all of the keys
         const int tb = b * p.nt, te = min(tb + p.nt, pv.T);
         const bool all = tb >= it.t0 && te <= it.t1 &&
@@ -395,12 +409,15 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
         const int c0 = (it.t0 - tb) * p.group, c1 = (min(it.t1, te) - tb) * p.group;
         const float4 *fc = reinterpret_cast<const float4 *>(tile + Q::factor);
         const int *limit = reinterpret_cast<const int *>(tile + Q::limit);
-#pragma unroll 1
+        // 32 columns at a time, the next ones on their way
+        float v[2][32];
+        const uint32_t at = tmem + lanes + 128 * buf;
+        tmem_load(at, reinterpret_cast<uint32_t(&)[32]>(v[0][0]));
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float v[32];
-          tmem_load(tmem + lanes + 128 * buf + 32 * i, reinterpret_cast<uint32_t(&)[32]>(v[0]));
           tmem_ld_wait();
-          float2 *v2 = reinterpret_cast<float2 *>(v);
+          if (i < 3) tmem_load(at + 32 * (i + 1), reinterpret_cast<uint32_t(&)[32]>(v[(i + 1) & 1][0]));
+          float2 *v2 = reinterpret_cast<float2 *>(v[i & 1]);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float4 f = fc[16 * i + e];
@@ -413,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const int c = 32 * i + e;
-              if (c >= c0 && c < c1 && slot <= limit[c]) sum[0].x += exp2_hw(v[e]);
+              if (c >= c0 && c < c1 && slot <= limit[c]) sum[0].x += exp2_hw(v[i & 1][e]);
             }
           }
         }
@@ -421,24 +438,26 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sempty[buf]);
-          mbar_arrive(&qempty[s]);
+          mbar_arrive(&cempty[cslot]);
         }
       }
       if (!ok) break;
-      // the two warpgroups' sums, the first's first
+      // the warpgroups' sums, the first's first
       sum[0] = add2(sum[0], sum[1]);
       const float own = sum[0].x + sum[0].y;
-      if (w == 1) {
+      if (w > 0) {
         ok = wait_warp(&meet[1], (met & 1) ^ 1);  // (those of the item before have been read)
         if (!ok) break;
-        sums[row] = own;
+        sums[128 * (w - 1) + row] = own;
         __syncwarp();
         if (lane == 0) mbar_arrive(&meet[0]);
         ++met;
       } else {
         ok = wait_warp(&meet[0], met & 1);
         if (!ok) break;
-        const float both = own + sums[row];
+        float both = own;
+#pragma unroll
+        for (int i = 0; i < kGroups - 1; ++i) both += sums[128 * i + row];
         __syncwarp();
         if (lane == 0) mbar_arrive(&meet[1]);
         ++met;
