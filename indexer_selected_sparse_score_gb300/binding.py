@@ -461,15 +461,19 @@ def sa_paged4_workspace_size(pa: Paged4Args) -> int:
     return int(load().sa_paged4_workspace_size(ctypes.byref(pa)))
 
 
-def _records(pa: Paged4Args, name: str, x, dtype, device: Optional[int] = None):
+def _records(a: PagedArgs, name: str, x, dtype, device: Optional[int] = None):
     """Pointer and row stride of the slots' records ([B, H_kv, ld], dense; a raw
     pointer is taken as rows of max_pages * P)."""
     if x is None or type(x) is int:
-        return x, pa.p.max_pages * pa.p.P
-    if x.dim() != 3 or x.shape[0] != pa.p.B or x.shape[1] != pa.p.H_kv:
-        raise SAError(SA_ERR_INVALID_ARG, f"{name} is {list(x.shape)}: need {[pa.p.B, pa.p.H_kv]} rows")
-    ld = x.shape[2]
-    return _dense(name, x, dtype, pa.p.B * pa.p.H_kv, ld, device), ld
+        return x, a.max_pages * a.P
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != a.B or shape[1] != a.H_kv:
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} is {list(shape)}: need {[a.B, a.H_kv]} rows")
+    if x.dtype is not dtype or not x.is_contiguous():
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} must be contiguous, of {dtype} (got {x.dtype})")
+    if device is not None and x.get_device() != device:
+        raise SAError(SA_ERR_INVALID_ARG, f"{name} is on another device than the workspace")
+    return x.data_ptr(), shape[2]
 
 
 def sa_paged4_append(pa: Paged4Args, k, v, ws, q=None, q_out=None, rope: Optional[RopeArgs] = None,
@@ -483,8 +487,8 @@ def sa_paged4_append(pa: Paged4Args, k, v, ws, q=None, q_out=None, rope: Optiona
     kp, ks = _token_rows("k", k, n_kv, D, T, dev)
     vp, vs = _token_rows("v", v, n_kv, D, T, dev)
     qp, qs = _token_rows("q", q, a.H, D, T, dev)
-    wp, ld = _records(pa, "weight", weight, _FP32, dev)
-    bp, bld = _records(pa, "born", born, _INT32, dev)
+    wp, ld = _records(a, "weight", weight, _FP32, dev)
+    bp, bld = _records(a, "born", born, _INT32, dev)
     if ld != bld and weight is not None and born is not None:
         raise SAError(SA_ERR_INVALID_ARG, "weight and born differ in their rows")
     _check(load().sa_paged4_append(ctypes.byref(pa), kp, ks, vp, vs, qp, qs,
@@ -496,27 +500,32 @@ def sa_paged4_append(pa: Paged4Args, k, v, ws, q=None, q_out=None, rope: Optiona
 def sa_paged4_read(pa: Paged4Args, k_out, v_out, ws, stream=None) -> None:
     """The rows of the tokens' slots as bf16 ([T, H_kv, D]; either may be None)."""
     p, n, dev, stream = _paged_ws(pa, ws, stream)
-    row = pa.p.H_kv * pa.p.D
-    _check(load().sa_paged4_read(ctypes.byref(pa), _dense("k_out", k_out, _BF16, pa.p.T, row, dev),
-                                 _dense("v_out", v_out, _BF16, pa.p.T, row, dev), p, n, _s(stream)))
+    a = pa.p
+    T, row = a.T, a.H_kv * a.D
+    _check(load().sa_paged4_read(ctypes.byref(pa), _dense("k_out", k_out, _BF16, T, row, dev),
+                                 _dense("v_out", v_out, _BF16, T, row, dev), p, n, _s(stream)))
 
 
 def sa_paged4_attn(pa: Paged4Args, q, out, ws, lse=None, stream=None) -> None:
     """Attention over whole sequences of a 4-bit cache; ``lse`` ([T, H] fp32) gets
     the logarithm of every row's sum of exponentials."""
     p, n, dev, stream = _paged_ws(pa, ws, stream)
-    T, row = pa.p.T, pa.p.H * pa.p.D
+    a = pa.p
+    T, H = a.T, a.H
+    row = H * a.D
     _check(load().sa_paged4_attn(ctypes.byref(pa), _dense("q", q, _BF16, T, row, dev),
-                                 _dense("out", out, _BF16, T, row, dev), _dense("lse", lse, _FP32, T, pa.p.H, dev), p, n,
+                                 _dense("out", out, _BF16, T, row, dev), _dense("lse", lse, _FP32, T, H, dev), p, n,
                                  _s(stream)))
 
 
 def sa_paged4_weights(pa: Paged4Args, q, lse, weight, ws, stream=None) -> None:
     """Adds the tokens' attention weights to the slots' records ([B, H_kv, ld] fp32)."""
     p, n, dev, stream = _paged_ws(pa, ws, stream)
-    wp, ld = _records(pa, "weight", weight, _FP32, dev)
-    _check(load().sa_paged4_weights(ctypes.byref(pa), _dense("q", q, _BF16, pa.p.T, pa.p.H * pa.p.D, dev),
-                                    _dense("lse", lse, _FP32, pa.p.T, pa.p.H, dev), wp, ld, p, n, _s(stream)))
+    a = pa.p
+    T, H = a.T, a.H
+    wp, ld = _records(a, "weight", weight, _FP32, dev)
+    _check(load().sa_paged4_weights(ctypes.byref(pa), _dense("q", q, _BF16, T, H * a.D, dev),
+                                    _dense("lse", lse, _FP32, T, H, dev), wp, ld, p, n, _s(stream)))
 
 
 def sa_paged4_evict(pa: Paged4Args, length, newest, budget: int, recent: int, weight, born, weight_out, born_out,
@@ -524,15 +533,17 @@ def sa_paged4_evict(pa: Paged4Args, length, newest, budget: int, recent: int, we
     """Cuts every sequence to ``budget`` slots per KV head: the ``recent`` newest
     stay and the heaviest of the others; freed slots take rows from behind."""
     p, n, dev, stream = _paged_ws(pa, ws, stream)
-    recs = [_records(pa, name, x, dt, dev) for name, x, dt in (
-        ("weight", weight, _FP32), ("born", born, _INT32), ("weight_out", weight_out, _FP32),
-        ("born_out", born_out, _INT32))]
-    if len({ld for _, ld in recs}) != 1:
+    a = pa.p
+    B = a.B
+    wp, ld = _records(a, "weight", weight, _FP32, dev)
+    bp, ld1 = _records(a, "born", born, _INT32, dev)
+    wo, ld2 = _records(a, "weight_out", weight_out, _FP32, dev)
+    bo, ld3 = _records(a, "born_out", born_out, _INT32, dev)
+    if not ld == ld1 == ld2 == ld3:
         raise SAError(SA_ERR_INVALID_ARG, "the records differ in their rows")
-    lens = [_dense(name, x, _INT32, pa.p.B, 1, dev) for name, x in (
-        ("length", length), ("newest", newest), ("length_out", length_out))]
-    _check(load().sa_paged4_evict(ctypes.byref(pa), lens[0], lens[1], budget, recent, recs[0][0], recs[1][0], recs[2][0],
-                                  recs[3][0], recs[0][1], lens[2], p, n, _s(stream)))
+    _check(load().sa_paged4_evict(ctypes.byref(pa), _dense("length", length, _INT32, B, 1, dev),
+                                  _dense("newest", newest, _INT32, B, 1, dev), budget, recent, wp, bp, wo, bo, ld,
+                                  _dense("length_out", length_out, _INT32, B, 1, dev), p, n, _s(stream)))
 
 
 def sa_check_device_status(ws, stream=None) -> int:

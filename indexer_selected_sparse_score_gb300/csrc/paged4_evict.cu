@@ -69,6 +69,7 @@ evict4_kernel(const EvictParams p) {
   __shared__ int hist[kBins];
   __shared__ int scan[kWarps];
   __shared__ int2 pick;  // digit, keys above it
+  __shared__ int found;  // keys of it
   const PagedView &pv = p.c.v;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = blockIdx.x % p.share;
@@ -93,28 +94,37 @@ evict4_kernel(const EvictParams p) {
     return;
   }
   const int64_t oldest = static_cast<int64_t>(p.newest[b]) - p.recent;  // recent: born after it
-  auto key_of = [&](int j) -> uint32_t {
-    if (born[j] > oldest) return 0xFFFFFFFFu;
-    const float w = weight[j];
-    return w != w ? 0xFFFFFFFEu : ordered_key(w);
+  auto make_key = [&](int b_, float w) -> uint32_t {
+    return b_ > oldest ? 0xFFFFFFFFu : w != w ? 0xFFFFFFFEu : ordered_key(w);
   };
-  auto key = [&](int j) -> uint32_t { return kCached ? keys_s[j] : key_of(j); };
+  auto key = [&](int j) -> uint32_t { return kCached ? keys_s[j] : make_key(born[j], weight[j]); };
+  if (kCached) {
+    constexpr int kBatch = 8;  // loads that go out together
+    for (int j0 = tid; j0 < n; j0 += kBatch * kThreads) {
+      int bb[kBatch];
+      float ww[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int j = min(j0 + e * kThreads, n - 1);
+        bb[e] = born[j];
+        ww[e] = weight[j];
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+        if (j0 + e * kThreads < n) keys_s[j0 + e * kThreads] = make_key(bb[e], ww[e]);
+    }
+  }
   // ------------------------------------------------------------ selection
   uint32_t prefix = 0, mask = 0;
   int need = keep;  // of the keys that match the digits so far
+  int equal = 0;    // keys that are the budget-th largest's
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     __syncthreads();
     for (int j = tid; j < n; j += kThreads) {
-      uint32_t x;
-      if (kCached && pass == 0) {
-        x = key_of(j);
-        keys_s[j] = x;
-      } else {
-        x = key(j);
-      }
+      const uint32_t x = key(j);
       if ((x & mask) == prefix) {
         const uint32_t d = (x >> shift) & ((1u << bits) - 1);
         // (many may be alike, the recent slots are: one addition for those of the first
@@ -147,44 +157,58 @@ evict4_kernel(const EvictParams p) {
     int above = warp_prefix<kWarps>(__shfl_sync(0xffffffffu, up, 31), scan, total) + up - sum;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      if (above < need && above + own[e] >= need) pick = make_int2(kBins - 1 - (tid * kPer + e), above);
+      if (above < need && above + own[e] >= need) {
+        pick = make_int2(kBins - 1 - (tid * kPer + e), above);
+        found = own[e];
+      }
       above += own[e];
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(pick.x) << shift;
     mask |= ((1u << bits) - 1) << shift;
     need -= pick.y;
+    equal = found;
   }
   // Kept: keys above `prefix`, and the lowest `need` slots of that key.  Each warp
   // takes a stretch of slots.
   const int each = ((n + kWarps - 1) / kWarps + 31) & ~31;
   const int j0 = min(warp * each, n), j1 = min(j0 + each, n);
-  int ties = 0, total;
-  for (int j = j0 + lane; j - lane < j1; j += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, j < j1 && key(j) == prefix));
-  const int ties_before = warp_prefix<kWarps>(ties, scan, total);
-  // walk(use): use(j, kept, in) for 32 slots at a time, with the ballots of it
+  const bool all_equal = equal == need;  // (no ties to break)
+  int ties_before = 0, total;
+  if (!all_equal) {
+    int ties = 0;
+    for (int j = j0 + lane; j - lane < j1; j += 32)
+      ties += __popc(__ballot_sync(0xffffffffu, j < j1 && key(j) == prefix));
+    ties_before = warp_prefix<kWarps>(ties, scan, total);
+  }
+  // walk(use): use(j, kept, in) for 32 slots at a time
   auto walk = [&](const auto &use) {
     int seen = ties_before;
     for (int jb = j0; jb < j1; jb += 32) {
       const int j = jb + lane;
       const uint32_t x = j < j1 ? key(j) : 0u;
-      const bool tie = j < j1 && x == prefix;
-      const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-      const bool kept = j < j1 && (x > prefix || (tie && seen + __popc(tied & ((1u << lane) - 1)) < need));
-      seen += __popc(tied);
+      bool kept = j < j1 && (all_equal ? x >= prefix : x > prefix);
+      if (!all_equal) {
+        const bool tie = j < j1 && x == prefix;
+        const uint32_t tied = __ballot_sync(0xffffffffu, tie);
+        kept |= tie && seen + __popc(tied & ((1u << lane) - 1)) < need;
+        seen += __popc(tied);
+      }
       use(j, kept, j < j1);
     }
   };
   int holes = 0, movers = 0;
   walk([&](int j, bool kept, bool in) {
-    holes += __popc(__ballot_sync(0xffffffffu, in && !kept && j < keep));
-    movers += __popc(__ballot_sync(0xffffffffu, kept && j >= keep));
+    holes += in && !kept && j < keep;
+    movers += kept && j >= keep;
+    if (kCached && in) keys_s[j] = kept;  // from here on (a slot is read by its lane alone)
   });
+  holes = __reduce_add_sync(0xffffffffu, holes);
+  movers = __reduce_add_sync(0xffffffffu, movers);
   int moves;
   int hole = warp_prefix<kWarps>(holes, scan, moves), mover = warp_prefix<kWarps>(movers, scan, total);
   int2 *list = p.lists + static_cast<int64_t>(blockIdx.x) * p.list;
-  walk([&](int j, bool kept, bool in) {
+  auto note = [&](int j, bool kept, bool in) {
     const bool is_hole = in && !kept && j < keep, is_mover = kept && j >= keep;
     const uint32_t bh = __ballot_sync(0xffffffffu, is_hole), bm = __ballot_sync(0xffffffffu, is_mover);
     const uint32_t below = (1u << lane) - 1;
@@ -198,12 +222,43 @@ evict4_kernel(const EvictParams p) {
     }
     hole += __popc(bh);
     mover += __popc(bm);
-    // slots that stay in place
-    if (kept && j < keep && (j >> 5) % p.share == part) {
-      weight_out[j] = weight[j];
-      born_out[j] = born[j];
+  };
+  if (kCached) {
+    for (int jb = j0; jb < j1; jb += 32) {
+      const int j = jb + lane;
+      note(j, j < j1 && keys_s[j], j < j1);
     }
-  });
+    __syncthreads();
+    // the records of slots that stay in place: this CTA's share
+    constexpr int kBatch = 4;
+    const int stride = p.share * kThreads;
+    for (int a0 = part * kThreads + tid; a0 < keep; a0 += kBatch * stride) {
+      float ww[kBatch];
+      int bb[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int j = min(a0 + e * stride, keep - 1);
+        ww[e] = weight[j];
+        bb[e] = born[j];
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int j = a0 + e * stride;
+        if (j < keep && keys_s[j]) {
+          weight_out[j] = ww[e];
+          born_out[j] = bb[e];
+        }
+      }
+    }
+  } else {
+    walk([&](int j, bool kept, bool in) {
+      note(j, kept, in);
+      if (kept && j < keep && (j >> 5) % p.share == part) {
+        weight_out[j] = weight[j];
+        born_out[j] = born[j];
+      }
+    });
+  }
   __syncthreads();
   // ---------------------------------------------------------------- moves
   // 16 lanes a row: codes of K and V (D / 2 bytes each) and scales
