@@ -14,21 +14,28 @@
 //                 g's values of keys 2t, 2t + 1, 2t + 8, 2t + 9; code pairs of two keys
 //                 are joined before the conversion (four operations for eight pairs)
 //   P^T           two 8 x 8 transposes in registers (movmatrix)
-// A warp owns 16 of a tile's 128 keys with sums and O of its own, so nothing is
-// exchanged until the CTA's part of a unit ends.  (The 5th-generation tensor cores
-// would need the fp16 operands in shared memory, four times the codes' bytes there
-// and back, for products that fill an eighth of their rows; the warp-level
-// product's rate, measured 1018 multiply-adds a clock and SM, serves 8 columns at
-// three times HBM's pace and 16 at one and a half.  More columns: paged4_umma.cu.)
+// A warp takes every 8th (or 6th) group of 32 keys, with a ring of copies, sums and O
+// of its own, so that nothing is exchanged until the CTA's part of a unit ends.  (The
+// 5th-generation tensor cores would need the fp16 operands in shared memory, four
+// times the codes' bytes there and back, for products that fill an eighth of their
+// rows; the warp-level product's rate, measured 1018 multiply-adds a clock and SM,
+// serves 8 columns at three times HBM's pace and 16 at one and a half.  More columns:
+// paged4_umma.cu.)
+//
+// What bounds it is issue: about 310 instructions for 16 keys and 8 columns (counters:
+// the ALU pipe, which the conversion shares with the masks and selects, is the fullest).
+// 64 sequences of 2 .. 16 K slots, 64 heads over 8 of 128: 163 us, 5.5 TB/s; 32 sequences of 4 tokens (16 columns, O of 64 registers): 75 us.
+// Measured against: a copy warp with barriers for all (219 us: a wait that is already
+// over still costs a warp 150 to 200 clocks), 7 or 5 warps for 16 columns (79, 84 us).
 //
 // A column's logits are taken relative to a reference that is raised (and O
 // rescaled) only when one passes it by 2^14; weights are then at most 2^14 and
 // enter the product as fp16, normal down to 2^-28 of the largest.
 //
-// Work: paged4_units.cuh.  A copy warp keeps a ring of tiles in flight (bulk
-// copies; a page's rows of one KV head are contiguous).  A unit that is cut leaves
-// parts in scratch; the CTA that adds the last of them (a counter) merges them in
-// order.
+// Work: paged4_units.cuh.  A warp's copies are 16 bytes a lane, three groups in flight;
+// a page's rows of one KV head are contiguous, and a page that is not there reads as
+// zeros.  A unit that is cut leaves parts in scratch; the CTA that adds the last of
+// them (a counter) merges them in order.
 #include <cfloat>
 #include <climits>
 
@@ -329,7 +336,7 @@ attn4_kernel(const Attn4Params p) {
           }
           __syncthreads();
           if (*last_s) {
-            // the last one here: every warp takes every seventh part
+            // the last one here: a warp takes every 8th (6th) part
             a.begin(cols, lane);
             for (int k = c0 + warp; k <= c1; k += kWarps) {
               const int64_t from = 2 * static_cast<int64_t>(k) + (k == c0);
