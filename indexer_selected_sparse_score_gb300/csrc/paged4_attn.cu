@@ -64,6 +64,9 @@ constexpr int kCtasPerSm = 2;
 constexpr int kGroup = 32;               // slots of a warp's step
 constexpr int kStages = 3;               // groups that a warp has in its ring
 constexpr int kLeast = 2;                // tiles of a CTA, at least
+constexpr int kFan = 16;                 // parts that a CTA merges; a unit of more is merged in two steps
+constexpr int kMostCtas = 400;           // counters: one a CTA, then one per kFan CTAs
+static_assert(kMostCtas + kMostCtas / kFan <= kAttn4Counters, "counters");
 
 template <int kDim, int NT>
 struct AttnSmem {
@@ -90,7 +93,7 @@ struct Attn4Params {
   float *lse;
   float *part;         // [2 grid][NT][D / 4][32]
   float2 *ml;          // [2 grid][16]: reference (log2 units), sum
-  uint32_t *counters;  // [grid], 0 between calls
+  uint32_t *counters;  // [kAttn4Counters], 0 between calls
   int group, nt;       // query heads of a KV head, tokens of a block (group * nt <= 16)
   float qk_scale, v_gain;
   uint32_t *status;
@@ -137,6 +140,7 @@ attn4_kernel(const Attn4Params p) {
   int *poison = reinterpret_cast<int *>(smem + L::poison);
   uint8_t *ring = smem + warp * L::kRing;
   const uint32_t ring_s = smem_u32(ring);
+  constexpr int kCols = (8 * NT + kWarps - 1) / kWarps;                   // columns that a warp stages
   constexpr int kMt = kDim / 16, kEach = (kMt + kWarps - 1) / kWarps;  // pairs of O's rows, of a warp
   Columns<kDim, NT> a;
 
@@ -189,6 +193,12 @@ attn4_kernel(const Attn4Params p) {
         const int n_groups = min(kt1 * kPer, last / kGroup + 1) - kt0 * kPer - warp;
         const int mine = n_groups > 0 ? (n_groups + kWarps - 1) / kWarps : 0;
         const int first = kt0 * kPer + warp;
+        uint32_t qw[kCols][kDim / 64];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          const int col = warp + j * kWarps, i = min(col, ncols - 1) / ng;
+          load_column<kDim>(p.q + (static_cast<int64_t>(t0 + i) * pv.H + h0 + col - i * ng) * kDim, col < ncols, lane, qw[j]);
+        }
         auto load_ids = [&](int i) {
           const int j = i + (kSmall ? lane >> 1 : lane);
           const int slot = kGroup * (first + kWarps * j) + (kSmall ? 16 * (lane & 1) : 0);
@@ -234,14 +244,13 @@ attn4_kernel(const Attn4Params p) {
         for (int i = 0; i < kStages - 1; ++i) copy(i);
         if (tid < 8) poison[tid] = INT_MAX;
         // queries as fp16 fragments, a column per warp
-#pragma unroll 1
-        for (int col = warp; col < 8 * NT; col += kWarps) {
-          const int i = min(col / ng, l1 - l0 - 1);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          const int col = warp + j * kWarps, i = min(col / ng, l1 - l0 - 1);
           const int pos = __shfl_sync(0xffffffffu, valid ? t_pos : -1, l0 + i);
-          stage_column<kDim>(p.q + (static_cast<int64_t>(t0 + i) * pv.H + h0 + col - i * ng) * kDim, col, col < ncols, lane,
-                             qf, [&](float inv) {
-                               cols[col] = make_float2(p.qk_scale * inv, __int_as_float(col < ncols ? pos : -1));
-                             });
+          if (col >= 8 * NT) continue;
+          const float inv = stage_column<kDim>(qw[j], col, lane, qf);
+          if (lane == 0) cols[col] = make_float2(p.qk_scale * inv, __int_as_float(col < ncols ? pos : -1));
         }
         __syncthreads();
         a.begin(cols, lane);
@@ -268,7 +277,7 @@ attn4_kernel(const Attn4Params p) {
         cp_async_wait<0>();
         a.sum_up();
         const bool cut = c0 != c1;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
+        int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
         // The warps' sums and O joined: into scratch (to_part) or the output.
         auto join = [&](bool to_part) {
           if (g == 0) {
@@ -326,43 +335,63 @@ attn4_kernel(const Attn4Params p) {
         };
         join(cut);
         if (cut) {
-          __threadfence();
-          __syncthreads();
-          if (tid == 0) {
-            const uint32_t before = atomicAdd(&p.counters[c0], 1u);
-            *last_s = before == static_cast<uint32_t>(c1 - c0);
-            if (*last_s) p.counters[c0] = 0;  // for the next call
-            __threadfence();
-          }
-          __syncthreads();
-          if (*last_s) {
-            // the last one here: a warp takes every 8th (6th) part
-            a.begin(cols, lane);
-            for (int k = c0 + warp; k <= c1; k += kWarps) {
-              const int64_t from = 2 * static_cast<int64_t>(k) + (k == c0);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float x[kMt][4];
-                const float4 s = __ldcg(reinterpret_cast<const float4 *>(p.ml + from * 16 + 8 * nt + 2 * tq));
-#pragma unroll
-                for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) x[mt][e] = __ldcg(p.part + ((from * NT + nt) * (kDim / 4) + 4 * mt + e) * 32 + lane);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float r = e ? s.z : s.x, m = fmaxf(a.ref[nt][e], r);
-                  const float f0 = exp2_fast(a.ref[nt][e] - m), f1 = exp2_fast(r - m);
-                  a.ref[nt][e] = m;
-                  a.l[nt][e] = a.l[nt][e] * f0 + (e ? s.w : s.y) * f1;
-#pragma unroll
-                  for (int mt = 0; mt < kMt; ++mt) {
-                    a.o[nt][mt][e] = a.o[nt][mt][e] * f0 + x[mt][e] * f1;
-                    a.o[nt][mt][e + 2] = a.o[nt][mt][e + 2] * f0 + x[mt][e + 2] * f1;
+          // The last CTA to add a part merges them.  Of more than kFan, it merges its group's
+          // into the first one's place, and the last group to be done merges the groups' (a
+          // CTA reads 4 KB of 8 columns a part at 30 bytes a clock: one token over 304 CTAs
+          // 19.1 us by one CTA a unit).
+          const int me = static_cast<int>(blockIdx.x);
+          bool groups = c1 - c0 >= kFan;
+          int lo = groups ? c0 + (me - c0) / kFan * kFan : c0, hi = groups ? min(lo + kFan - 1, c1) : c1;
+          int span = 1, counter = lo;
+          for (;;) {
+            if (groups && lo == hi) {
+              // (a group of one has its part in place; its counter is the next unit's)
+            } else {
+              __threadfence();
+              __syncthreads();
+              if (tid == 0) {
+                const uint32_t before = atomicAdd(&p.counters[counter], 1u);
+                *last_s = before == static_cast<uint32_t>((hi - lo) / span);
+                if (*last_s) p.counters[counter] = 0;  // for the next call
+                __threadfence();
+              }
+              __syncthreads();
+              if (!*last_s) break;
+              // every warp takes a part in turn
+              a.begin(cols, lane);
+              for (int k = lo + warp * span; k <= hi; k += kWarps * span) {
+                const int64_t from = 2 * static_cast<int64_t>(k) + (k == c0);
+  #pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float x[kMt][4];
+                  const float4 s = __ldcg(reinterpret_cast<const float4 *>(p.ml + from * 16 + 8 * nt + 2 * tq));
+  #pragma unroll
+                  for (int mt = 0; mt < kMt; ++mt)
+  #pragma unroll
+                    for (int e = 0; e < 4; ++e) x[mt][e] = __ldcg(p.part + ((from * NT + nt) * (kDim / 4) + 4 * mt + e) * 32 + lane);
+  #pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const float r = e ? s.z : s.x, m = fmaxf(a.ref[nt][e], r);
+                    const float f0 = exp2_fast(a.ref[nt][e] - m), f1 = exp2_fast(r - m);
+                    a.ref[nt][e] = m;
+                    a.l[nt][e] = a.l[nt][e] * f0 + (e ? s.w : s.y) * f1;
+  #pragma unroll
+                    for (int mt = 0; mt < kMt; ++mt) {
+                      a.o[nt][mt][e] = a.o[nt][mt][e] * f0 + x[mt][e] * f1;
+                      a.o[nt][mt][e + 2] = a.o[nt][mt][e + 2] * f0 + x[mt][e + 2] * f1;
+                    }
                   }
                 }
               }
+              slot = 2 * static_cast<int64_t>(lo) + (lo == c0);
+              join(groups);
+              if (!groups) break;
             }
-            join(false);
+            groups = false;
+            lo = c0;
+            hi = c0 + (c1 - c0) / kFan * kFan;
+            span = kFan;
+            counter = kMostCtas + c0 / kFan;
           }
         }
         __syncthreads();  // (the next part's copies land where O was)
@@ -372,7 +401,7 @@ attn4_kernel(const Attn4Params p) {
   }
 }
 
-int grid_of() { return std::min(kCtasPerSm * sm_count(), kAttn4Counters); }
+int grid_of() { return std::min(kCtasPerSm * sm_count(), kMostCtas); }
 
 template <int kDim, int NT, bool kSmall>
 cudaError_t launch(const Attn4Params &p, cudaStream_t stream) {

@@ -34,21 +34,26 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return y;
 }
 
-// One warp brings column `col` of the queries (kDim bf16 at src; zeros unless in) into
-// fragments of the K Q^T product as fp16, scaled by a power of two; done(1 / factor)
-// in one lane.  Fragment (nt, i) of lane (g, t): 16 bytes, the values
-// kDim / 4 t + 8 i .. + 7 of column 8 nt + g.
-template <int kDim, typename Done>
-__device__ __forceinline__ void stage_column(const uint16_t *src, int col, bool in, int lane, uint4 *qf,
-                                             const Done &done) {
-  constexpr int V = kDim / 32;
-  uint32_t w[V / 2] = {};
+// One warp brings a column of the queries into fragments of the K Q^T product as fp16,
+// scaled by a power of two.  load_column: a lane's part of kDim bf16 at src (zeros
+// unless in).
+template <int kDim>
+__device__ __forceinline__ void load_column(const uint16_t *src, bool in, int lane, uint32_t (&w)[kDim / 64]) {
+#pragma unroll
+  for (int i = 0; i < kDim / 64; ++i) w[i] = 0;
   if (in) {
-    if constexpr (V == 4)
+    if constexpr (kDim == 128)
       *reinterpret_cast<uint2 *>(w) = reinterpret_cast<const uint2 *>(src)[lane];
     else
       w[0] = reinterpret_cast<const uint32_t *>(src)[lane];
   }
+}
+
+// stage_column: as column `col`; returns 1 / factor.  Fragment (nt, i) of lane (g, t):
+// 16 bytes, the values kDim / 4 t + 8 i .. + 7 of column 8 nt + g.
+template <int kDim>
+__device__ __forceinline__ float stage_column(uint32_t (&w)[kDim / 64], int col, int lane, uint4 *qf) {
+  constexpr int V = kDim / 32;
   float x[V], top = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -67,7 +72,7 @@ __device__ __forceinline__ void stage_column(const uint16_t *src, int col, bool 
     *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
   else
     *reinterpret_cast<uint32_t *>(dst) = w[0];
-  if (lane == 0) done(1.f / f);
+  return 1.f / f;
 }
 
 // Key rows g and g + 8 of 16 (codes at k, scales at ks): words of codes and, per
