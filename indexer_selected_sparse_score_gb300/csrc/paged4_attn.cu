@@ -129,10 +129,11 @@ attn4_kernel(const Attn4Params p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long long x0, x1;
   int ctas;
-  find_units(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
+  find_units<true>(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
   __syncthreads();
   if (x0 >= x1) return;
   const long long total = start->total;
+  const int round = start->round;
 
   const int g = lane >> 2, tq = lane & 3;
   uint4 *qf = reinterpret_cast<uint4 *>(smem + L::qf);
@@ -176,15 +177,16 @@ attn4_kernel(const Attn4Params p) {
       const int low = __reduce_min_sync(0xffffffffu, member ? t_pos : INT_MAX);
       const int cost = (last + kTile) / kTile;
       if (cost == 0) continue;
+      const int counted = (cost + round - 1) / round * round;
       const int seq = __shfl_sync(0xffffffffu, t_seq, l0);
       for (; hk < pv.H_kv && x < x1; ++hk, kt0 = 0) {
         const int ng = p.group, h0 = hk * ng;
         const int ncols = (l1 - l0) * ng;
-        const long long u0 = x - kt0, u1 = u0 + cost;
+        const long long u0 = x - kt0, u1 = u0 + counted;
         const int c0 = u0 < x0 ? cta_of_tile(u0, total, ctas) : blockIdx.x;
         const int c1 = u1 > x1 ? cta_of_tile(u1 - 1, total, ctas) : blockIdx.x;
-        const int kt1 = static_cast<int>(min(static_cast<long long>(cost), kt0 + (x1 - x)));
-        x += kt1 - kt0;
+        const int end = static_cast<int>(min(static_cast<long long>(counted), kt0 + (x1 - x))), kt1 = min(cost, end);
+        x += end - kt0;
         // ------------------------------- this CTA's part of a unit: tiles kt0 .. kt1 - 1
         // groups of 32 slots: warp w takes first + w, + 8, ..; lane l holds the page of
         // the l-th of each 32 (pages of 16: of the halves of each 16 groups)

@@ -11,10 +11,17 @@
 
 namespace sa {
 
+// a / b of non-negative values, mostly below 2^32.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Where a CTA's range of tiles begins.
 struct UnitStart {
   int block, t0, head, tile;
   long long total;  // tiles of the call
+  int round, pad;   // units count as multiples of it
 };
 
 // One warp: calls use(first token, last slot) for the units that begin among tokens
@@ -65,6 +72,14 @@ __device__ __forceinline__ void units_of_tokens(const PagedView &v, int nt, int 
 // total * (c + 1) / g - 1 with g = min(grid, total / least) (at least one); x0 and
 // x1 get them, `ctas` g, and out (shared memory) the first one's place.  warp_s:
 // 32 long longs of shared memory.
+//
+// kWhole: where there are no more units than CTAs (and at most 64 tokens), no CTA has to
+// have parts of two: every unit is cut into pieces of one length (out->round; units then
+// count as multiples of it), if one that is at most 7 tiles above the even share gives no
+// more pieces than CTAs.  (A second part costs a CTA about 4 us, a tile of 128 rows of 144
+// bytes 0.8 us when all stream: 16 tokens of 32 over 8 heads of 64 at 0.1 .. 3 K slots
+// 19.9 us by even shares.)  Each warp finds its CTA's place by itself then.
+template <bool kWhole = false>
 __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads, int tile, int least, long long *warp_s,
                                            UnitStart *out, uint32_t *status, long long &x0, long long &x1, int &ctas) {
   // warp w takes the units that begin in its stretch of blocks (of whole 32s of tokens,
@@ -75,6 +90,55 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
   const int t0 = static_cast<int>(min(static_cast<int64_t>(v.T), static_cast<int64_t>(warp) * per * grain));
   const int t1 = static_cast<int>(min(static_cast<int64_t>(v.T), (static_cast<int64_t>(warp) + 1) * per * grain));
   uint32_t *report = blockIdx.x == 0 ? status : nullptr;
+  if (kWhole && nt == 1 && v.T <= 64 && static_cast<int64_t>(v.T) * heads <= gridDim.x) {
+    int cost[2];  // of tokens lane and 32 + lane
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = 32 * e + lane;
+      int b, pos;
+      cost[e] = t < v.T && load_paged_token(v, t, report, report != nullptr && warp == 0, b, pos) ? (pos + tile) / tile : 0;
+    }
+    const int all = __reduce_add_sync(0xffffffffu, cost[0] + cost[1]);
+    long long total = static_cast<long long>(all) * heads;
+    const int most = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, total / least)));
+    const int shortest = max(least, static_cast<int>(divide(total + gridDim.x - 1, gridDim.x)));
+    // the shortest of 8 lengths that is long enough (a longer one gives no more pieces)
+    auto pieces = [&](int n) {
+      return __reduce_add_sync(0xffffffffu, (cost[0] + n - 1) / n + (cost[1] + n - 1) / n) * heads;
+    };
+    int round = 1;
+    ctas = most;
+    if (all > 0 && pieces(shortest + 7) <= static_cast<int>(gridDim.x)) {
+      round = shortest;
+#pragma unroll
+      for (int step = 4; step > 0; step >>= 1)
+        if (pieces(round + step - 1) > static_cast<int>(gridDim.x)) round += step;
+      ctas = pieces(round);
+      total = static_cast<long long>(ctas) * round;
+    }
+    const int c = blockIdx.x;
+    x0 = c < ctas ? divide(total * c, ctas) : total;
+    x1 = c < ctas ? divide(total * (c + 1), ctas) : total;
+    long long before = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int counted = (cost[e] + round - 1) / round * round;
+      long long upto = static_cast<long long>(counted) * heads;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      upto += before;
+      const long long from = upto - static_cast<long long>(counted) * heads;
+      if (warp == 0 && x0 < x1 && x0 >= from && x0 < upto) {
+        const int rest = static_cast<int>(x0 - from), t = 32 * e + lane;
+        *out = UnitStart{t, t, rest / counted, rest % counted, total, round, 0};
+      }
+      before = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return;
+  }
   long long sum = 0;
   if (nt == 1) {
     for (int t = t0 + lane; t < t1; t += 32) {
@@ -93,8 +157,8 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
   const long long most = total / least;
   ctas = static_cast<int>(max(1ll, min(static_cast<long long>(gridDim.x), most)));
   const int c = blockIdx.x;
-  x0 = c < ctas ? total * c / ctas : total;
-  x1 = c < ctas ? total * (c + 1) / ctas : total;
+  x0 = c < ctas ? divide(total * c, ctas) : total;
+  x1 = c < ctas ? divide(total * (c + 1), ctas) : total;
   // (the warp's first tile and its number of tiles)
   before = __shfl_sync(0xffffffffu, before, 0);
 #pragma unroll
@@ -105,7 +169,7 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
       const int cost = (last + tile) / tile;
       if (x0 < at + static_cast<long long>(cost) * heads) {
         const int rest = static_cast<int>(x0 - at);
-        if (lane == 0) *out = UnitStart{t / nt, t, rest / cost, rest % cost, total};
+        if (lane == 0) *out = UnitStart{t / nt, t, rest / cost, rest % cost, total, 1, 0};
         return false;
       }
       at += static_cast<long long>(cost) * heads;
@@ -209,7 +273,7 @@ __device__ __forceinline__ int run_of_tile(const long long *off, int runs, long 
 
 // The CTA of `ctas` whose range holds tile y of `total`.
 __device__ __forceinline__ int cta_of_tile(long long y, long long total, int ctas) {
-  return static_cast<int>(((y + 1) * ctas - 1) / total);
+  return static_cast<int>(divide((y + 1) * ctas - 1, total));
 }
 
 }  // namespace sa
