@@ -349,13 +349,11 @@ attn4_kernel(const Attn4Params p) {
             if (groups && lo == hi) {
               // (a group of one has its part in place; its counter is the next unit's)
             } else {
-              __threadfence();
               __syncthreads();
               if (tid == 0) {
-                const uint32_t before = atomicAdd(&p.counters[counter], 1u);
-                *last_s = before == static_cast<uint32_t>((hi - lo) / span);
-                if (*last_s) p.counters[counter] = 0;  // for the next call
-                __threadfence();
+                const bool last_one = count_part(p.counters + counter) == static_cast<uint32_t>((hi - lo) / span);
+                if (last_one) p.counters[counter] = 0;  // for the next call
+                *last_s = last_one;
               }
               __syncthreads();
               if (!*last_s) break;

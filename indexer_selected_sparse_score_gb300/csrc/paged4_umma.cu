@@ -780,16 +780,14 @@ umma4_kernel(const UmmaParams p) {
         tc_fence_before();
       }
       if (!joined) continue;
-      __threadfence();
       sync();
       if (!ok) break;
       bool merge = true;
       if (cut) {
         if (tid == 0) {
-          const uint32_t before = atomicAdd(&p.counters[ti.c0], 1u);
-          *last_s = before == static_cast<uint32_t>(ti.c1 - ti.c0);
-          if (*last_s) p.counters[ti.c0] = 0;  // for the next call
-          __threadfence();
+          const bool last_one = count_part(p.counters + ti.c0) == static_cast<uint32_t>(ti.c1 - ti.c0);
+          if (last_one) p.counters[ti.c0] = 0;  // for the next call
+          *last_s = last_one;
         }
         sync();
         if (!ok) break;

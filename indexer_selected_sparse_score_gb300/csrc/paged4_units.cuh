@@ -17,6 +17,15 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return a / b;
 }
 
+// One thread, after a barrier of the threads that have written: counts a part as added.
+// What they wrote before is seen by whoever's call returns a larger number (and by
+// those that it meets at a barrier afterwards).
+__device__ __forceinline__ uint32_t count_part(uint32_t *counter) {
+  uint32_t before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  return before;
+}
+
 // Where a CTA's range of tiles begins.
 struct UnitStart {
   int block, t0, head, tile;
