@@ -568,6 +568,32 @@ def test_evict_long(n, budget):
     _check_evict(c, [n], [n - 1], budget, 128, w, born)
 
 
+@pytest.mark.parametrize("B,Hkv,P", [(40, 4, 64), (10, 4, 128), (5, 4, 32), (19, 8, 16), (1, 1, 64)])
+def test_evict_few_and_many_rows(B, Hkv, P):
+    """Rows of one CTA of either size, and of two, four and eight."""
+    lens = [1100 + 37 * i % 1500 for i in range(B)]
+    r = np.random.RandomState(43)
+    for ties in (False, True):
+        c = Case(43, lens, 64, P, Hkv, 1).tokens([], [])
+        c.q = torch.zeros(0, c.H, 64, dtype=torch.bfloat16)
+        c.upload()
+        w, born = _records(c, r, lens, ties)
+        _check_evict(c, lens, [n - 1 for n in lens], 1000, 100, w, born)
+
+
+@pytest.mark.parametrize("n", [33, 5000, 33000])
+def test_evict_from_a_wide_table(n):
+    """A table whose rows could be longer than what eight CTAs hold."""
+    c = Case(44, [n], 64, P=128, Hkv=1, G=1)
+    c.table = np.concatenate([c.table, np.full((1, 3200), -1, np.int32)], axis=1)
+    c.max_pages = c.table.shape[1]
+    c.tokens([], [])
+    c.q = torch.zeros(0, c.H, c.D, dtype=torch.bfloat16)
+    c.upload()
+    w, born = _records(c, np.random.RandomState(44), [n], ties=True)
+    _check_evict(c, [n], [n - 1], max(n // 3, 1), n // 10, w, born)
+
+
 def test_evict_special_weights_and_lengths():
     lens = [200, 200, 200, 200, 200]
     c = Case(42, lens, P=32, Hkv=2, G=1)
