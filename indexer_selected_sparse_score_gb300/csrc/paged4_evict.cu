@@ -15,8 +15,10 @@
 //
 // A row is one CTA's, or where rows are few, a cluster's: each of its CTAs holds the
 // keys of a stretch of slots and the histograms and counts are added up over
-// distributed shared memory (2 prompts of 4 heads and 16 .. 33 K slots: 26.6 us; 16 CTAs
-// that each hold all of a row's keys 40.9).  64 sequences of 8 heads and 2112 slots: 22.4 us.
+// distributed shared memory (2 prompts of 4 heads and 16 .. 33 K slots: 20.5 us; 16 CTAs
+// that each hold all of a row's keys 40.9; a barrier of a cluster costs 2500 clocks, and one
+// fewer by lists that stay apart, with one before the end, is no gain: 22.5).  64 sequences
+// of 8 heads and 2112 slots: 20.5 us, a row's chain of loads, three digits, counts and moves.
 #include <algorithm>
 
 #include "internal.h"
@@ -49,16 +51,32 @@ struct EvictParams {
   uint32_t *status;
 };
 
-// The value at the same place of shared memory in the cluster's CTA `rank`.
-__device__ __forceinline__ uint32_t remote_smem(const void *p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(umma::smem_u32(p)), "r"(rank));
-  return a;
+constexpr int kMostShare = 8;
+
+// The values at p's place in the shared memory of the cluster's `share` CTAs, zeros past
+// them; the loads go out together.
+template <bool kCluster>
+__device__ __forceinline__ void load_ranks(const int2 *p, int share, int2 (&v)[kMostShare]) {
+  v[0] = kCluster ? make_int2(0, 0) : *p;
+#pragma unroll
+  for (int r = kCluster ? 0 : 1; r < kMostShare; ++r) {
+    v[r] = make_int2(0, 0);
+    if (kCluster && r < share) {
+      uint32_t a;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(umma::smem_u32(p)), "r"(r));
+      asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v[r].x), "=r"(v[r].y) : "r"(a) : "memory");
+    }
+  }
 }
-__device__ __forceinline__ int2 remote_int2(const int2 *p, uint32_t rank) {
-  int2 v;
-  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(remote_smem(p, rank)) : "memory");
-  return v;
+
+// Sum of x over the lanes up to this one.
+__device__ __forceinline__ int scan_warp(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += up;
+  }
+  return x;
 }
 
 // kThreads: 256 where rows are many, four CTAs to an SM; kCluster: share CTAs a row;
@@ -69,8 +87,9 @@ evict4_kernel(const EvictParams p) {
   constexpr int kWarps = kThreads / 32, kHists = kCluster ? 3 : 1;
   extern __shared__ __align__(16) uint32_t keys_s[];
   __shared__ __align__(16) int hist[kHists][kBins];
+  __shared__ __align__(16) int sums[kHists][kBins / 32];
   __shared__ long long scan[32];
-  __shared__ int2 exchange[2];
+  __shared__ int2 ties_s, count_s, ranks_s[2];  // (of a cluster)
   __shared__ int2 pick;  // digit, keys above it
   __shared__ int found;  // keys of it
   const PagedView &pv = p.c.v;
@@ -153,29 +172,45 @@ evict4_kernel(const EvictParams p) {
         if ((x & mask) == prefix) count(now, (x >> shift) & ((1u << bits) - 1));
       }
     }
-    kCluster ? cluster_sync() : __syncthreads();
-    // the digit that holds the need-th largest: sums from the top, kPer bins a thread
+    __syncthreads();
+    // the digit that holds the need-th largest: sums of 32 bins each, then one warp looks
+    // for the 32 bins that hold it, and for the bin
     constexpr int kPer = kBins / kThreads;
-    int own[kPer] = {}, sum = 0;  // (ascending bins)
-    const int2 *mine = reinterpret_cast<const int2 *>(now + kBins - (tid + 1) * kPer);
-    for (int r = 0; r < share; ++r)
+    int sum = 0;
 #pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) {
-        const int2 v = kCluster ? remote_int2(mine + e, r) : mine[e];
-        own[2 * e] += v.x;
-        own[2 * e + 1] += v.y;
+    for (int e = 0; e < kPer / 2; ++e) {
+      const int2 v = reinterpret_cast<const int2 *>(now + tid * kPer)[e];
+      sum += v.x + v.y;
+    }
+#pragma unroll
+    for (int o = 16 / kPer; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    int *coarse = sums[kCluster ? pass : 0];
+    if (tid % (32 / kPer) == 0) coarse[tid * kPer / 32] = sum;
+    kCluster ? cluster_sync() : __syncthreads();
+    if (warp == 0) {
+      // lane l: sums 62 - 2 l, + 1, so that a scan over lanes goes down from the top
+      int2 v[kMostShare];
+      load_ranks<kCluster>(reinterpret_cast<const int2 *>(coarse) + 31 - lane, share, v);
+      int2 x = v[0];
+#pragma unroll
+      for (int i = 1; i < kMostShare; ++i) x = make_int2(x.x + v[i].x, x.y + v[i].y);
+      int upto = scan_warp(x.x + x.y, lane);
+      int above = upto - x.x - x.y;  // keys of larger digits
+      const uint32_t at = __ballot_sync(0xffffffffu, above < need && upto >= need);
+      const int l = __ffs(at) - 1;  // (there is one: need is at least 1 and at most the keys)
+      const bool low = above + x.y < need;
+      const int group = __shfl_sync(0xffffffffu, 2 * (31 - lane) + (low ? 0 : 1), l);
+      above = __shfl_sync(0xffffffffu, low ? above + x.y : above, l);
+      // lane l: bin 31 - l of the 32
+      load_ranks<kCluster>(reinterpret_cast<const int2 *>(now + 32 * group) + (31 - lane) / 2, share, v);
+      int own = 0;
+#pragma unroll
+      for (int i = 0; i < kMostShare; ++i) own += lane & 1 ? v[i].x : v[i].y;
+      upto = above + scan_warp(own, lane);
+      if (upto - own < need && upto >= need) {
+        pick = make_int2(32 * group + 31 - lane, upto - own);
+        found = own;
       }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) sum += own[e];
-    long long total;
-    int above = static_cast<int>(block_prefix(sum, scan, total));
-#pragma unroll
-    for (int e = kPer - 1; e >= 0; --e) {
-      if (above < need && above + own[e] >= need) {
-        pick = make_int2(kBins - (tid + 1) * kPer + e, above);
-        found = own[e];
-      }
-      above += own[e];
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(pick.x) << shift;
@@ -188,20 +223,27 @@ evict4_kernel(const EvictParams p) {
     }
   }
   // The sums of v over the cluster's CTAs before this one, and over all.
-  auto over_ranks = [&](int which, int2 v, int2 &all) {
+  auto over_ranks = [&](int2 &v_s, int2 v, int2 &all) {
     all = v;
-    int2 before = make_int2(0, 0);
-    if (kCluster) {
-      if (tid == 0) exchange[which] = v;
-      cluster_sync();
-      all = make_int2(0, 0);
-      for (int r = 0; r < share; ++r) {
-        const int2 x = remote_int2(exchange + which, r);
-        if (r < rank) before = make_int2(before.x + x.x, before.y + x.y);
-        all = make_int2(all.x + x.x, all.y + x.y);
+    if (!kCluster) return make_int2(0, 0);
+    if (tid == 0) v_s = v;
+    cluster_sync();
+    if (warp == 0) {
+      int2 x[kMostShare], before = make_int2(0, 0), sum = before;
+      load_ranks<true>(&v_s, share, x);
+#pragma unroll
+      for (int r = 0; r < kMostShare; ++r) {
+        if (r < rank) before = make_int2(before.x + x[r].x, before.y + x[r].y);
+        sum = make_int2(sum.x + x[r].x, sum.y + x[r].y);
+      }
+      if (lane == 0) {
+        ranks_s[0] = before;
+        ranks_s[1] = sum;
       }
     }
-    return before;
+    __syncthreads();
+    all = ranks_s[1];
+    return ranks_s[0];
   };
   // Kept: keys above `prefix`, and the lowest `need` slots of that key.  Each warp
   // takes a stretch of words.
@@ -222,7 +264,7 @@ evict4_kernel(const EvictParams p) {
     long long total;
     int seen = static_cast<int>(block_prefix(lane == 0 ? ties : 0, scan, total));
     int2 all;
-    seen = __shfl_sync(0xffffffffu, seen, 0) + over_ranks(0, make_int2(static_cast<int>(total), 0), all).x;
+    seen = __shfl_sync(0xffffffffu, seen, 0) + over_ranks(ties_s, make_int2(static_cast<int>(total), 0), all).x;
     for (int w = w0; w < w1; ++w) {
       const int j = s0 + 32 * w + lane;
       const uint32_t x = j < s1 ? key(j) : 0u;
@@ -253,12 +295,12 @@ evict4_kernel(const EvictParams p) {
   own = block_prefix(own, scan, total);
   int2 all;
   const int2 before =
-      over_ranks(1, make_int2(static_cast<int>(total & 0xffffffff), static_cast<int>(total >> 32)), all);
+      over_ranks(count_s, make_int2(static_cast<int>(total & 0xffffffff), static_cast<int>(total >> 32)), all);
   int hole = before.x + static_cast<int>(own & 0xffffffff), mover = before.y + static_cast<int>(own >> 32);
-  const int moves = all.y;
+  const int moves = all.y;  // (as many slots are freed)
   // (one CTA's lists lie over its keys, at most half of its slots each)
-  int *holes_at = kCached && !kCluster ? reinterpret_cast<int *>(keys_s) : p.lists + 2 * row * p.list;
-  int *movers_at = holes_at + (kCached && !kCluster ? each / 2 : p.list);
+  int *holes_at = kCluster ? p.lists + 2 * row * p.list : reinterpret_cast<int *>(keys_s);
+  int *movers_at = holes_at + (kCluster ? p.list : each / 2);
   for (int w = a; w < z; ++w) {
     for (uint32_t m = freed(w); m; m &= m - 1) holes_at[hole++] = s0 + 32 * w + __ffs(m) - 1;
     for (uint32_t m = moving(w); m; m &= m - 1) movers_at[mover++] = s0 + 32 * w + __ffs(m) - 1;
@@ -288,66 +330,62 @@ evict4_kernel(const EvictParams p) {
   }
   kCluster ? cluster_sync() : __syncthreads();
   // ---------------------------------------------------------------- moves
-  // 16 lanes a row: codes of K and V (D / 2 bytes each) and scales
+  // 16 lanes a row, each a piece: 16 bytes of K's or V's codes, the scales of K or V, the
+  // weight, the birth; rows whose page is out of range move their record alone
   const int sub = lane & 15, mine = (moves - rank + share - 1) / share;
-  const int chunks = p.D / 32;  // 16-byte chunks of a row's codes
-  constexpr int kRows = 2;      // rows a group of lanes has in flight
+  const int chunks = p.D / 32, what = sub - 2 * chunks;  // (of a row's codes)
+  const uint8_t *from = nullptr;
+  uint8_t *to = nullptr;
+  int unit = 0, bytes = 0;  // between slots, of the piece
+  const bool record = what >= 2 && what < 4;
+  if (what < 0) {
+    from = to = (sub < chunks ? p.c.K : p.c.V) + 16 * (sub % chunks);
+    unit = p.D / 2;
+    bytes = 16;
+  } else if (what < 2) {
+    from = to = what ? p.c.Vs : p.c.Ks;
+    unit = bytes = p.D / 16;
+  } else if (record) {
+    from = what == 2 ? reinterpret_cast<const uint8_t *>(weight) : reinterpret_cast<const uint8_t *>(born);
+    to = what == 2 ? reinterpret_cast<uint8_t *>(weight_out) : reinterpret_cast<uint8_t *>(born_out);
+    unit = bytes = 4;
+  }
+  constexpr int kRows = 4;      // rows a group of lanes has in flight
   const int groups = 2 * kWarps;
   for (int i0 = 2 * warp + (lane >> 4); i0 < mine; i0 += kRows * groups) {
-    uint4 x[kRows];
-    int to[kRows];
-    int64_t dst[kRows];
     int2 mv[kRows];  // freed slot, staying slot
-    int64_t src[kRows];
+    int64_t src[kRows], dst[kRows];
+    uint4 x[kRows];
 #pragma unroll
     for (int e = 0; e < kRows; ++e) {
-      const int i = i0 + e * groups;
-      mv[e] = i < mine ? make_int2(holes_at[rank + i * share], movers_at[rank + i * share]) : make_int2(-1, -1);
+      const int i = rank + min(i0 + e * groups, mine - 1) * share;
+      mv[e] = make_int2(holes_at[i], movers_at[i]);
     }
 #pragma unroll
     for (int e = 0; e < kRows; ++e) {
-      to[e] = -1;
-      if (mv[e].x < 0) continue;
       const int pd = load_page(pv, b, mv[e].x >> pv.logP, p.status, sub == 0);
       const int ps = load_page(pv, b, mv[e].y >> pv.logP, p.status, sub == 0);
-      if (pd < 0 || ps < 0) continue;
-      to[e] = 1;
-      dst[e] = (static_cast<int64_t>(pd) * pv.H_kv + h) * pv.P + (mv[e].x & (pv.P - 1));
-      src[e] = (static_cast<int64_t>(ps) * pv.H_kv + h) * pv.P + (mv[e].y & (pv.P - 1));
+      const bool held = pd >= 0 && ps >= 0;
+      dst[e] = record ? mv[e].x : held ? (static_cast<int64_t>(pd) * pv.H_kv + h) * pv.P + (mv[e].x & (pv.P - 1)) : -1;
+      src[e] = record ? mv[e].y : held ? (static_cast<int64_t>(ps) * pv.H_kv + h) * pv.P + (mv[e].y & (pv.P - 1)) : -1;
+      if (bytes == 0 || i0 + e * groups >= mine) dst[e] = -1;
     }
-    // lane sub: chunk sub of K's codes, of V's, then the scales and the records
-    const int what = sub < chunks ? 0 : sub < 2 * chunks ? 1 : sub - 2 * chunks + 2;
-    const int ch = sub % chunks;
 #pragma unroll
     for (int e = 0; e < kRows; ++e) {
-      if (mv[e].x < 0) continue;
-      if (what < 2) {
-        if (to[e] > 0) x[e] = *reinterpret_cast<const uint4 *>((what ? p.c.V : p.c.K) + src[e] * (p.D / 2) + 16 * ch);
-      } else if (what < 4) {
-        const uint8_t *s = (what == 3 ? p.c.Vs : p.c.Ks) + (to[e] > 0 ? src[e] : 0) * (p.D / 16);
-        if (to[e] > 0) {
-          x[e].x = *reinterpret_cast<const uint32_t *>(s);
-          if (p.D == 128) x[e].y = *reinterpret_cast<const uint32_t *>(s + 4);
-        }
-      } else if (what == 4) {
-        x[e].x = __float_as_uint(weight[mv[e].y]);
-        x[e].y = static_cast<uint32_t>(born[mv[e].y]);
+      const uint8_t *at = from + src[e] * unit;
+      if (dst[e] >= 0) {
+        if (bytes == 16) x[e] = *reinterpret_cast<const uint4 *>(at);
+        if (bytes == 8) *reinterpret_cast<uint2 *>(&x[e]) = *reinterpret_cast<const uint2 *>(at);
+        if (bytes == 4) x[e].x = *reinterpret_cast<const uint32_t *>(at);
       }
     }
 #pragma unroll
     for (int e = 0; e < kRows; ++e) {
-      if (mv[e].x < 0) continue;
-      if (what < 2) {
-        if (to[e] > 0) *reinterpret_cast<uint4 *>((what ? p.c.V : p.c.K) + dst[e] * (p.D / 2) + 16 * ch) = x[e];
-      } else if (what < 4) {
-        uint8_t *s = (what == 3 ? p.c.Vs : p.c.Ks) + (to[e] > 0 ? dst[e] : 0) * (p.D / 16);
-        if (to[e] > 0) {
-          *reinterpret_cast<uint32_t *>(s) = x[e].x;
-          if (p.D == 128) *reinterpret_cast<uint32_t *>(s + 4) = x[e].y;
-        }
-      } else if (what == 4) {
-        weight_out[mv[e].x] = __uint_as_float(x[e].x);
-        born_out[mv[e].x] = static_cast<int32_t>(x[e].y);
+      uint8_t *at = to + dst[e] * unit;
+      if (dst[e] >= 0) {
+        if (bytes == 16) *reinterpret_cast<uint4 *>(at) = x[e];
+        if (bytes == 8) *reinterpret_cast<uint2 *>(at) = make_uint2(x[e].x, x[e].y);
+        if (bytes == 4) *reinterpret_cast<uint32_t *>(at) = x[e].x;
       }
     }
   }
@@ -358,15 +396,15 @@ evict4_kernel(const EvictParams p) {
 int share_of(const sa_paged4_args &pa) {
   const int64_t rows = static_cast<int64_t>(pa.p.B) * pa.p.H_kv, most = static_cast<int64_t>(pa.p.max_pages) * pa.p.P;
   int share = 1;
-  while (share < 8 && ((rows * share * 2 <= sm_count() && most > 1024 * share) || most > static_cast<int64_t>(kKeysInSmem) * share))
+  while (share < kMostShare && ((rows * share * 2 <= sm_count() && most > 1024 * share) || most > static_cast<int64_t>(kKeysInSmem) * share))
     share *= 2;
   return share;
 }
-int list_of(const sa_paged4_args &pa) { return pa.p.max_pages * pa.p.P / 2 + 1; }
 int slice_of(const sa_paged4_args &pa) {
   const int unit = 32 * share_of(pa);
   return (pa.p.max_pages * pa.p.P + unit - 1) / unit * 32;
 }
+int list_of(const sa_paged4_args &pa) { return pa.p.max_pages * pa.p.P / 2 + 1; }
 int words_of(const sa_paged4_args &pa) { return slice_of(pa) > kKeysInSmem ? share_of(pa) * slice_of(pa) / 32 : 0; }
 
 template <bool kCached, int kThreads, bool kCluster>
@@ -383,7 +421,7 @@ cudaError_t launch(const EvictParams &p, int64_t rows, int slice, cudaStream_t s
 
 size_t evict4_scratch(const sa_paged4_args &pa) {
   const size_t rows = static_cast<size_t>(pa.p.B) * pa.p.H_kv;
-  return rows * (share_of(pa) > 1 ? 2 * list_of(pa) * sizeof(int) + words_of(pa) * sizeof(uint32_t) : 0);
+  return rows * (share_of(pa) > 1 ? 2 * static_cast<size_t>(list_of(pa)) * sizeof(int) + words_of(pa) * sizeof(uint32_t) : 0);
 }
 
 cudaError_t launch_evict4(const sa_paged4_args &pa, const int32_t *length, const int32_t *newest, int budget, int recent,
