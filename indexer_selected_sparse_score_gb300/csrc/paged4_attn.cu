@@ -24,7 +24,9 @@
 //
 // What bounds it is issue: about 310 instructions for 16 keys and 8 columns (counters:
 // the ALU pipe, which the conversion shares with the masks and selects, is the fullest).
-// 64 sequences of 2 .. 16 K slots, 64 heads over 8 of 128: 163 us, 5.5 TB/s; 32 sequences of 4 tokens (16 columns, O of 64 registers): 75 us.
+// 64 sequences of 8 .. 16 K slots, 64 heads over 8 of 128: 163 us, 5.4 TB/s; 32 sequences
+// of 4 tokens at 2 .. 8 K (16 columns, O of 64 registers, three warps a scheduler): 72 us;
+// one token of 16 over 2 heads at 40 K slots: 16 us, a chain of loads, joins and merges.
 // Measured against: a copy warp with barriers for all (219 us: a wait that is already
 // over still costs a warp 150 to 200 clocks), 7 or 5 warps for 16 columns (79, 84 us).
 //
@@ -35,7 +37,7 @@
 // Work: paged4_units.cuh.  A warp's copies are 16 bytes a lane, three groups in flight;
 // a page's rows of one KV head are contiguous, and a page that is not there reads as
 // zeros.  A unit that is cut leaves parts in scratch; the CTA that adds the last of
-// them (a counter) merges them in order.
+// them (a counter) merges them in order, in two steps where they are many.
 #include <cfloat>
 #include <climits>
 
@@ -51,7 +53,6 @@ namespace sa {
 namespace {
 
 using namespace umma;
-
 
 constexpr int kTile = 128;               // slots per tile: the grain of the work's division
 // Warps of a CTA: with two CTAs per SM, 128 registers each for 8 of them and 168 for 6

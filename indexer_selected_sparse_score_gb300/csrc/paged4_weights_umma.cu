@@ -11,8 +11,10 @@
 // An item is (run, KV head, 128 slots): its keys are converted once, and the tiles of
 // the run's tokens pass them; an item is one CTA's, so a slot's sum has one owner and
 // one order.  Tiles' logits go to four buffers of tensor memory that four warpgroups
-// empty in turn; bound by the exponentials (32 a clock and SM: 512 clocks a tile)
-// beside the products (512 clocks).
+// empty in turn.  The exponentials (32 a clock and SM) and the products take 512 clocks a
+// tile each; measured 1130, which are the issuing warp's (waits 300, issue 640) and, with
+// a second one, the query tiles' on their way from L2: 1024 prompt tokens of 32 over 4
+// heads at 8 K slots 99 us, 10 of them the first kernel's.
 #include <climits>
 
 #include <algorithm>

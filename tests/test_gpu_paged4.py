@@ -247,6 +247,19 @@ def test_same_results_again_and_from_a_graph():
         c.check_attn(out, lse)
 
 
+def test_nothing_to_attend():
+    """Calls whose every token is skipped leave everything as it was."""
+    lens = [100, 200]
+    for G, T in ((8, 2), (8, 100), (48, 2), (48, 100)):
+        c = Case(13, lens, G=G).tokens([-2 ** 31, 2, 0, 1] * (T // 2), [5, 5, 2 ** 31 - 1, -2 ** 31] * (T // 2)).upload()
+        out, lse = c.attn(expect=sb.SA_ERR_DEVICE_DATA)
+        assert (out == 7).all() and (lse == 7).all()
+        weight = torch.full((c.B, c.Hkv, c.max_pages * c.P), 3.0, device=DEV)
+        sb.sa_paged4_weights(c.pa, c.d["q"], lse, weight, c.ws)
+        assert sb.sa_check_device_status(c.ws) == sb.SA_ERR_DEVICE_DATA
+        assert (weight == 3).all()
+
+
 # ----------------------------------------------------------------- append ---
 
 def _state(c, ld=None):
@@ -681,3 +694,160 @@ def test_a_loop_that_decodes_within_a_budget():
         call(range(B), slots, position)
         slots, position = [s + 1 for s in slots], [p + 1 for p in position]
     assert slots == [97, 97, 44]
+
+
+class Step:
+    """A decode step over a full cache: append, attention, slot weights, eviction."""
+
+    def __init__(self, seed, G, lens):
+        self.c = c = Case(seed, [n + 1 for n in lens], G=G, Hkv=2).tokens(range(len(lens)), lens).upload()
+        r = np.random.RandomState(seed)
+        dev = lambda x: torch.from_numpy(x).to(DEV)  # noqa: E731
+        self.x = torch.from_numpy(r.standard_normal((c.T, c.H + 2 * c.Hkv, c.D))).bfloat16().to(DEV)
+        ld = c.max_pages * c.P
+        self.turn = dev(np.array(lens, np.int32) + 1000)
+        self.weight = dev(np.exp(r.standard_normal((c.B, c.Hkv, ld))).astype(np.float32))
+        self.born = dev(np.tile(np.arange(ld, dtype=np.int32) + 1000, (c.B, c.Hkv, 1)))
+        self.length = dev(np.array(lens, np.int32) + 1)
+        self.rope = sb.RopeArgs(64, 10000.0, 1.0, 0, 32.0, 1.0)
+        self.state = dict(K=c.d["K"], Ks=c.d["Ks"], V=c.d["V"], Vs=c.d["Vs"], weight=self.weight, born=self.born)
+        self.out = dict(q=torch.zeros(c.T, c.H, c.D, dtype=torch.bfloat16, device=DEV),
+                        out=torch.zeros(c.T, c.H, c.D, dtype=torch.bfloat16, device=DEV),
+                        lse=torch.zeros(c.T, c.H, device=DEV), wo=torch.zeros_like(self.weight),
+                        bo=torch.zeros_like(self.born), lo=torch.zeros_like(self.length))
+        self.before = {k: v.clone() for k, v in self.state.items()}
+
+    def run(self):
+        c, o = self.c, self.out
+        x, H, Hkv = self.x, c.H, c.Hkv
+        sb.sa_paged4_append(c.pa, x[:, H:H + Hkv], x[:, H + Hkv:], c.ws, q=x[:, :H], q_out=o["q"], rope=self.rope,
+                            halves=True, rope_pos=self.turn, weight=self.weight, born=self.born)
+        sb.sa_paged4_attn(c.pa, o["q"], o["out"], c.ws, lse=o["lse"])
+        sb.sa_paged4_weights(c.pa, o["q"], o["lse"], self.weight, c.ws)
+        sb.sa_paged4_evict(c.pa, self.length, self.turn, 200, 40, self.weight, self.born, o["wo"], o["bo"], o["lo"], c.ws)
+
+    def reset(self):
+        for k, v in self.state.items():
+            v.copy_(self.before[k])
+        for v in self.out.values():
+            v.zero_()
+
+    def result(self):
+        torch.cuda.synchronize()
+        return {k: v.clone() for k, v in list(self.state.items()) + list(self.out.items())}
+
+
+def _same(a, b):
+    for k in a:
+        assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("G", [8, 48])
+def test_a_step_from_a_graph_and_on_another_stream(G):
+    s = Step(60, G, [300, 17, 1000, 250])
+    s.run()
+    want = s.result()
+    assert s.out["lo"].tolist() == [200, 18, 200, 200]
+    s.reset()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        s.run()
+    _same(s.result(), want)
+    s.reset()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.run()
+    for _ in range(3):
+        s.reset()
+        g.replay()
+        _same(s.result(), want)
+    assert sb.sa_check_device_status(s.c.ws) == sb.SA_OK
+
+
+@pytest.mark.parametrize("G", [8, 48])
+def test_steps_at_once(G):
+    """Two steps with caches and workspaces of their own, on two streams at once, eagerly and
+    from graphs."""
+    steps = [Step(61, G, [3000, 17, 1000, 250]), Step(62, G, [64, 5000, 900])]
+    want = []
+    for s in steps:
+        s.run()
+        want.append(s.result())
+    streams = [torch.cuda.Stream() for _ in steps]
+    graphs = []
+    for s in steps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.run()
+        graphs.append(g)
+    for use_graphs in (False, True):
+        for _ in range(5):
+            for s in steps:
+                s.reset()
+            torch.cuda.synchronize()
+            for s, g, stream in zip(steps, graphs, streams):
+                with torch.cuda.stream(stream):
+                    g.replay() if use_graphs else s.run()
+            for s, w in zip(steps, want):
+                _same(s.result(), w)
+
+
+@pytest.mark.parametrize("G", [4, 40])
+def test_rows_past_four_gigabytes(G):
+    """Pages whose bytes lie past 32 bits of offset: written, read, attended, weighed, moved."""
+    n_pages, Hkv, P, D, lens = 140000, 8, 64, 128, [130, 70]
+    H, B = Hkv * G, len(lens)
+    r = np.random.RandomState(70)
+    cache = [torch.empty(n_pages, Hkv, P, w, dtype=torch.uint8, device=DEV) for w in (D // 2, D // 2, D // 16, D // 16)]
+    table = torch.tensor([[n_pages - 1, 139000, 138321], [0, 132000, -1]], dtype=torch.int32, device=DEV)
+    rows = torch.from_numpy(r.standard_normal((sum(lens), 2 * Hkv, D))).bfloat16().to(DEV)
+    seq = torch.from_numpy(np.repeat(np.arange(B), lens).astype(np.int32)).to(DEV)
+    pos = torch.from_numpy(np.concatenate([np.arange(n) for n in lens]).astype(np.int32)).to(DEV)
+    args = lambda s, p: sb.paged4_args(s, p, table, H, Hkv, D, P, n_pages, *cache, D ** -0.5)  # noqa: E731
+    pa = args(seq, pos)
+    ws = sb.new_paged4_workspace(pa)
+    weight, born = torch.zeros(B, Hkv, 3 * P, device=DEV), torch.zeros(B, Hkv, 3 * P, dtype=torch.int32, device=DEV)
+    sb.sa_paged4_append(pa, rows[:, :Hkv], rows[:, Hkv:], ws, weight=weight, born=born)
+
+    def read():
+        k, v = (torch.zeros(sum(lens), Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        sb.sa_paged4_read(pa, k, v, ws)
+        return k, v
+    k, v = read()
+    # (a code is half a step of up to 1 of 6 scales away, a scale 2^-4 of itself)
+    amax = rows.float().unflatten(-1, (-1, 16)).abs().amax(-1, keepdim=True).expand(-1, -1, -1, 16).flatten(-2)
+    assert ((torch.cat([k, v], 1).float() - rows.float()).abs() <= amax * (1 / 6 + 2 ** -3)).all()
+    last_seq, last_pos = torch.arange(B, dtype=torch.int32, device=DEV), torch.tensor(lens, dtype=torch.int32, device=DEV) - 1
+    last = args(last_seq, last_pos)
+    q = torch.from_numpy(r.standard_normal((B, H, D))).bfloat16().to(DEV)
+    out, lse = torch.zeros_like(q), torch.zeros(B, H, device=DEV)
+    last_ws = sb.new_paged4_workspace(last)
+    sb.sa_paged4_attn(last, q, out, last_ws, lse=lse)
+    sb.sa_paged4_weights(last, q, lse, weight, last_ws)
+    at = np.cumsum([0] + lens)
+    for b in range(B):
+        for h in range(Hkv):
+            kk, vv = (x[at[b]:at[b + 1], h].double().cpu() for x in (k, v))
+            o, l, s, eps, mag = r4.attention(q[b, h * G:(h + 1) * G].double().cpu(), kk, vv, torch.ones(lens[b], dtype=torch.bool),
+                                             D ** -0.5)
+            sl = slice(h * G, (h + 1) * G)
+            assert ((out[b, sl].double().cpu() - o).abs() <= r4.out_bound(o, mag, eps, lens[b], float(vv.abs().max()))).all()
+            assert ((lse[b, sl].double().cpu() - l).abs() <= r4.lse_bound(l, eps, lens[b])).all()
+            w = torch.softmax(s, -1).sum(0)
+            # weights: logits and lse off by eps and the bound above, sums of G terms
+            off = 2 * eps + float(r4.lse_bound(l, eps, lens[b]).max()) + 2.0 ** -20 + G * 2.0 ** -23
+            assert ((weight[b, h, :lens[b]].double().cpu() - w).abs() <= w * off * 1.01).all()
+    wo, bo = torch.zeros_like(weight), torch.zeros_like(born)
+    left = torch.zeros(B, dtype=torch.int32, device=DEV)
+    sb.sa_paged4_evict(pa, torch.tensor(lens, dtype=torch.int32, device=DEV), torch.tensor(lens, dtype=torch.int32, device=DEV) - 1,
+                       60, 10, weight, born, wo, bo, left, ws)
+    assert left.tolist() == [60, 60]
+    k2, v2 = read()
+    for b in range(B):
+        for h in range(Hkv):
+            src = r4.evict(lens[b], lens[b] - 1, 60, 10, weight[b, h].cpu().numpy(), born[b, h].cpu().numpy())
+            src = torch.tensor(src, device=DEV)
+            assert torch.equal(k2[at[b]:at[b] + 60, h], k[at[b] + src, h]) and torch.equal(v2[at[b]:at[b] + 60, h], v[at[b] + src, h])
+            assert torch.equal(wo[b, h, :60], weight[b, h, src])
+    assert sb.sa_check_device_status(ws) == sb.SA_OK and sb.sa_check_device_status(last_ws) == sb.SA_OK
