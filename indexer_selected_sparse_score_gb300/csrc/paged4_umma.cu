@@ -54,6 +54,9 @@ constexpr int kWarpMma = 16;   // and 17: the issuers
 constexpr int kWarpInfo = 18;  // describes the tiles (19 only joins the block barriers)
 constexpr int kLeast = 2;      // tiles of a CTA, at least
 constexpr int kInfos = 8, kParts = 4;
+constexpr int kFan = 4;            // parts that are merged at once; more in two steps, of the root of their number
+constexpr int kMostCtas = 256;     // counters: two a CTA
+static_assert(2 * kMostCtas <= kAttn4Counters, "counters");
 // Registers per thread: 640 threads start with 96 each; the softmax warpgroups raise
 // their limit, the last one lowers its own: 2 * 120 + 2 * 96 + 48 = 5 * 96.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 120, kOtherRegs = 48;
@@ -104,7 +107,7 @@ struct UmmaParams {
   float *lse;
   float *part;         // [slot][stream][128][D]
   float2 *ml;          // [slot][stream][128]: reference (log2 units, -inf: nothing), sum
-  uint32_t *counters;  // [grid], 0 between calls
+  uint32_t *counters;  // [kAttn4Counters], 0 between calls
   int group, nt;
   float qk_scale, v_gain;
   uint32_t *status;
@@ -782,22 +785,13 @@ umma4_kernel(const UmmaParams p) {
       if (!joined) continue;
       sync();
       if (!ok) break;
-      bool merge = true;
-      if (cut) {
-        if (tid == 0) {
-          const bool last_one = count_part(p.counters + ti.c0) == static_cast<uint32_t>(ti.c1 - ti.c0);
-          if (last_one) p.counters[ti.c0] = 0;  // for the next call
-          *last_s = last_one;
-        }
-        sync();
-        if (!ok) break;
-        merge = *last_s;
-      }
-      if (merge) {
-        // Four rows of a warp at a time (warp, + 8, + 16, + 24), the unit's parts and their
-        // streams in order, two of them in flight.
+      // The parts of CTAs lo, lo + span, .. hi (subs pieces each) joined in order, into the
+      // output or into the first one's place (groups).  Four rows of a warp at a time (warp,
+      // + 8, + 16, + 24), two pieces of each in flight.
+      auto merge = [&](int lo, int hi, int span, int subs, bool groups) {
         constexpr int V = kDim / 32, kR = 4;
-        const int subs = kTwo ? 1 : 2 * reps, count = (ti.c1 - ti.c0 + 1) * subs;
+        const int count = ((hi - lo) / span + 1) * subs;
+        auto slot_of_cta = [&](int c) { return 3 * static_cast<int64_t>(c) + (!cut ? 2 : c == ti.c0 ? 1 : 0); };
         for (int r0 = warp; r0 < rows; r0 += 8 * kR) {
           float M[kR], sum[kR], acc[kR][V] = {};
 #pragma unroll
@@ -810,12 +804,12 @@ umma4_kernel(const UmmaParams p) {
             float y[2][kR][V];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int k = min(k0 + e, count - 1), c = ti.c0 + k / subs;
-              const int64_t sl = 3 * static_cast<int64_t>(c) + (!cut ? 2 : c == ti.c0 ? 1 : 0);
+              const int k = min(k0 + e, count - 1), i = k / subs, sub = k - i * subs;
+              const int64_t sl = slot_of_cta(lo + i * span);
 #pragma unroll
               for (int j = 0; j < kR; ++j) {
                 const int rr = min(r0 + 8 * j, rows - 1);
-                const int64_t a = (sl * 2 + (kTwo ? rr >> 7 : k & 1)) * 128 + (kTwo ? rr & 127 : rr + 64 * (k % subs >> 1));
+                const int64_t a = (sl * 2 + (rr >> 7) + (sub & 1)) * 128 + (rr & 127) + 64 * (sub >> 1);
                 s[e][j] = __ldcg(p.ml + a);
                 if constexpr (V == 4)
                   *reinterpret_cast<float4 *>(y[e][j]) = __ldcg(reinterpret_cast<const float4 *>(p.part + a * kDim + V * lane));
@@ -841,6 +835,14 @@ umma4_kernel(const UmmaParams p) {
           for (int j = 0; j < kR; ++j) {
             const int rr = r0 + 8 * j, i = rr / p.group;
             if (rr >= rows) continue;
+            if (groups) {
+              const int64_t a = (slot_of_cta(lo) * 2 + (rr >> 7)) * 128 + (rr & 127);
+              if (lane == 0) __stcg(p.ml + a, make_float2(M[j], sum[j]));
+#pragma unroll
+              for (int e = 0; e < V; e += 2)
+                __stcg(reinterpret_cast<float2 *>(p.part + a * kDim + V * lane + e), make_float2(acc[j][e], acc[j][e + 1]));
+              continue;
+            }
             const int pos = pv.q_pos[ti.t0 + i];
             if (pos < 0 || (pos >> pv.logP) >= pv.max_pages) continue;
             const int64_t out_row = static_cast<int64_t>(ti.t0 + i) * pv.H + ti.hk * p.group + rr - i * p.group;
@@ -852,6 +854,46 @@ umma4_kernel(const UmmaParams p) {
             if (lane == 0 && p.lse) p.lse[out_row] = sum[j] == 0.f ? -INFINITY : (M[j] + log2f(sum[j])) * 0.69314718055994531f;
           }
         }
+      };
+      const int pieces = kTwo ? 1 : 2 * reps;
+      if (!cut) {
+        merge(blockIdx.x, blockIdx.x, 1, pieces, false);
+      } else {
+        // the last CTA to add a part merges them; of many, its group's, and the last group to
+        // be done the groups' (one CTA reads 50 bytes a clock)
+        const int me = static_cast<int>(blockIdx.x), parts_n = ti.c1 - ti.c0 + 1;
+        const int fan = max(kFan, static_cast<int>(ceilf(sqrtf(static_cast<float>(parts_n)))));
+        bool groups = parts_n > fan;
+        int lo = groups ? ti.c0 + (me - ti.c0) / fan * fan : ti.c0, hi = groups ? min(lo + fan - 1, ti.c1) : ti.c1;
+        int span = 1, subs = pieces;
+        uint32_t *counter = p.counters + lo;
+        for (;;) {
+          // (the counter of a group of one is the next unit's)
+          const int others = (hi - lo) / span;
+          bool last_one = others == 0;
+          if (!last_one) {
+            if (tid == 0) {
+              last_one = count_part(counter) == static_cast<uint32_t>(others);
+              if (last_one) *counter = 0;  // for the next call
+              *last_s = last_one;
+            }
+            sync();
+            if (!ok) break;
+            last_one = *last_s;
+          }
+          if (!last_one) break;
+          merge(lo, hi, span, subs, groups);
+          if (!groups) break;
+          sync();
+          if (!ok) break;
+          groups = false;
+          lo = ti.c0;
+          hi = ti.c0 + (parts_n - 1) / fan * fan;
+          span = fan;
+          subs = 1;
+          counter = p.counters + kMostCtas + ti.c0;
+        }
+        if (!ok) break;
       }
       sync();  // (the next part writes its own rows where a merge may still read)
       if (!ok) break;
@@ -867,7 +909,7 @@ umma4_kernel(const UmmaParams p) {
 }
 
 size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-int grid_of() { return std::min(sm_count(), kAttn4Counters); }
+int grid_of() { return std::min(sm_count(), kMostCtas); }
 
 template <int kDim, bool kTwo>
 cudaError_t launch(const UmmaParams &p, cudaStream_t stream) {
