@@ -159,7 +159,7 @@ cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, flo
 size_t attn4_scratch(const sa_paged4_args &pa);
 // On the 5th-generation tensor cores, units of up to `rows` (128 or 256) query rows.
 cudaError_t launch_attn4_umma(const sa_paged4_args &pa, const void *q, void *out, float *lse, int rows, void *scratch,
-                              uint32_t *counters, uint32_t *status, cudaStream_t stream);
+                              uint32_t *status, cudaStream_t stream);
 size_t attn4_umma_scratch(const sa_paged4_args &pa);
 cudaError_t launch_weights4(const sa_paged4_args &pa, const void *q, const float *lse, float *weight, int64_t ld,
                             void *scratch, uint32_t *status, cudaStream_t stream);

@@ -433,7 +433,7 @@ cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, flo
   if (pa.p.T == 0) return cudaSuccess;
   const int columns = columns_of(pa);
   if (columns > 16)
-    return launch_attn4_umma(pa, q, out, lse, columns > 128 ? 256 : 128, scratch, counters, status, stream);
+    return launch_attn4_umma(pa, q, out, lse, columns > 128 ? 256 : 128, scratch, status, stream);
   Attn4Params p;
   p.c = paged4_view(pa);
   p.q = static_cast<const uint16_t *>(q);

@@ -28,9 +28,9 @@
 // product.  1554 prompt tokens of 32 over 4 heads at 4 .. 8 K slots: 244 us, 0.82
 // PFLOP/s; 64 tokens of 64 heads over one KV head at 16 .. 65 K: 250 us.
 //
-// Work: paged4_units.cuh, units cut evenly over one CTA per SM; what has to be
-// joined goes to scratch, and the CTA that adds a unit's last part (a counter)
-// merges its rows in order.
+// Work: paged4_units.cuh, units cut evenly over one CTA per SM, or few of them into pieces
+// of one length; what has to be joined goes to scratch, and a second kernel joins the
+// units that were cut, in order.
 #include <cfloat>
 #include <climits>
 
@@ -54,9 +54,6 @@ constexpr int kWarpMma = 16;   // and 17: the issuers
 constexpr int kWarpInfo = 18;  // describes the tiles (19 only joins the block barriers)
 constexpr int kLeast = 2;      // tiles of a CTA, at least
 constexpr int kInfos = 8, kParts = 4;
-constexpr int kFan = 4;            // parts that are merged at once; more in two steps, of the root of their number
-constexpr int kMostCtas = 256;     // counters: two a CTA
-static_assert(2 * kMostCtas <= kAttn4Counters, "counters");
 // Registers per thread: 640 threads start with 96 each; the softmax warpgroups raise
 // their limit, the last one lowers its own: 2 * 120 + 2 * 96 + 48 = 5 * 96.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 120, kOtherRegs = 48;
@@ -107,7 +104,7 @@ struct UmmaParams {
   float *lse;
   float *part;         // [slot][stream][128][D]
   float2 *ml;          // [slot][stream][128]: reference (log2 units, -inf: nothing), sum
-  uint32_t *counters;  // [kAttn4Counters], 0 between calls
+  int4 *cuts;          // [grid] unit whose first part is the CTA's: first token, rows, KV head, last CTA; rows 0: none
   int group, nt;
   float qk_scale, v_gain;
   uint32_t *status;
@@ -121,6 +118,76 @@ __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N) {
 // the time they are asked for.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) || mbar_wait_warp(bar, parity);
+}
+
+// One warp: row rr of a unit, its pieces (the parts of CTAs c0 .. c1, of two streams, each
+// with two copies of up to 64 rows) joined in order, into the output.
+template <int kDim, bool kTwo>
+__device__ __forceinline__ void join_row(const UmmaParams &p, int rr, int rows, int t0, int hk, int c0, int c1, int lane) {
+  constexpr int V = kDim / 32;
+  const PagedView &pv = p.c.v;
+  const int i = rr / p.group, pos = pv.q_pos[t0 + i];
+  if (pos < 0 || (pos >> pv.logP) >= pv.max_pages) return;
+  const int log_subs = kTwo ? 0 : rows <= 64 ? 2 : 1, count = (c1 - c0 + 1) << log_subs;
+  auto piece = [&](int k) {  // its index among the rows of scratch
+    const int c = c0 + (k >> log_subs), sub = k & ((1 << log_subs) - 1);
+    return ((3 * c + (c0 == c1 ? 2 : c == c0 ? 1 : 0)) * 2 + (rr >> 7) + (sub & 1)) * 128 + (rr & 127) + 64 * (sub >> 1);
+  };
+  float M = -INFINITY;
+  for (int k = lane; k < count; k += 32) M = max_nan(M, __ldcg(&p.ml[piece(k)].x));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float sum = 0.f, acc[V] = {};
+  for (int k0 = 0; k0 < count; k0 += 32) {
+    // lane l: the factor of piece k0 + l, below 0 where it has nothing (what lies there may be anything)
+    float f = -1.f;
+    if (k0 + lane < count) {
+      const float2 v = __ldcg(p.ml + piece(k0 + lane));
+      if (v.x != -INFINITY) {
+        f = v.x == M ? 1.f : exp2_hw(v.x - M);
+        sum += v.y * f;
+      }
+    }
+    constexpr int kBatch = 8;  // loads that go out together
+    for (int k1 = k0; k1 < min(count, k0 + 32); k1 += kBatch) {
+      float y[kBatch][V], fk[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        fk[e] = __shfl_sync(0xffffffffu, f, (k1 + e) & 31);
+        const float *src = p.part + static_cast<int64_t>(piece(min(k1 + e, count - 1))) * kDim + V * lane;
+        if constexpr (V == 4)
+          *reinterpret_cast<float4 *>(y[e]) = __ldcg(reinterpret_cast<const float4 *>(src));
+        else
+          *reinterpret_cast<float2 *>(y[e]) = __ldcg(reinterpret_cast<const float2 *>(src));
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        if (k1 + e >= count || fk[e] < 0.f) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = fmaf(y[e][j], fk[e], acc[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int64_t out_row = static_cast<int64_t>(t0 + i) * pv.H + hk * p.group + rr - i * p.group;
+  const float inv = sum != 0.f ? p.v_gain / sum : 0.f;
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    *reinterpret_cast<__nv_bfloat162 *>(p.out + out_row * kDim + V * lane + e) =
+        __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[out_row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+}
+
+// Joins the units that were cut: CTA (x: eight rows, y: CTA of the first part), a warp a row.
+// (Many SMs at once: by the CTA that added the last part, 11 tokens of 32 over 2 heads at 8 K
+// slots took 128 us, in two steps 75.)
+template <int kDim, bool kTwo>
+__global__ void __launch_bounds__(256) join4_kernel(const UmmaParams p) {
+  pdl_wait();
+  const int4 u = p.cuts[blockIdx.y];
+  const int rr = 8 * blockIdx.x + (threadIdx.x >> 5);
+  if (rr < u.y) join_row<kDim, kTwo>(p, rr, u.y, u.x, u.z, blockIdx.y, u.w, threadIdx.x & 31);
 }
 
 template <int kDim, bool kTwo>
@@ -143,10 +210,11 @@ umma4_kernel(const UmmaParams p) {
   UnitStart *start = reinterpret_cast<UnitStart *>(smem + L::start);
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + L::misc);
   volatile int *abort_s = reinterpret_cast<volatile int *>(smem + L::misc + 4);
-  volatile int *last_s = reinterpret_cast<volatile int *>(smem + L::misc + 8);
   const PagedView &pv = p.c.v;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
   if (tid == 0) {
+    p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 4);
       mbar_init(&empty[i], kTwo ? 2 : 1);
@@ -179,13 +247,14 @@ umma4_kernel(const UmmaParams p) {
   }
   long long x0, x1;
   int ctas;
-  find_units(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
+  find_units<true>(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
   const long long total = start->total;
-  const long long tiles = x1 - x0;
+  const int round = start->round;
+  const long long tiles = x0 < x1 && round > 1 ? start->tiles : x1 - x0;
   auto fail = [&]() {
     raise_flag(p.status, kFlagTimeout);
     *abort_s = 1;
@@ -221,11 +290,12 @@ umma4_kernel(const UmmaParams p) {
         const int cost = (last + kTile) / kTile;
         if (cost == 0) continue;
         for (; hv < pv.H_kv && x < x1; ++hv, kt0 = 0) {
-          const long long u0 = x - kt0, u1 = u0 + cost;
+          const int counted = (cost + round - 1) / round * round;
+          const long long u0 = x - kt0, u1 = u0 + counted;
           const int c0 = u0 < x0 ? cta_of_tile(u0, total, ctas) : blockIdx.x;
           const int c1 = u1 > x1 ? cta_of_tile(u1 - 1, total, ctas) : blockIdx.x;
-          const int count = static_cast<int>(min(static_cast<long long>(cost - kt0), x1 - x));
-          x += count;
+          const int taken = static_cast<int>(min(static_cast<long long>(counted - kt0), x1 - x)), count = min(taken, cost - kt0);
+          x += taken;
           if (!use(seq, t0, len, low, last, hv, kt0, count, c0, c1)) return;
         }
         if (hv == pv.H_kv) hv = 0;
@@ -783,119 +853,17 @@ umma4_kernel(const UmmaParams p) {
         tc_fence_before();
       }
       if (!joined) continue;
+      if (cut) {  // (joined by the next kernel)
+        if (!kTwo) sync();  // (the streams share the queries)
+        if (!ok) break;
+        if (ti.c0 == static_cast<int>(blockIdx.x) && tid == 0)
+          p.cuts[blockIdx.x] = make_int4(ti.t0, rows, ti.hk, ti.c1);
+        continue;
+      }
       sync();
       if (!ok) break;
-      // The parts of CTAs lo, lo + span, .. hi (subs pieces each) joined in order, into the
-      // output or into the first one's place (groups).  Four rows of a warp at a time (warp,
-      // + 8, + 16, + 24), two pieces of each in flight.
-      auto merge = [&](int lo, int hi, int span, int subs, bool groups) {
-        constexpr int V = kDim / 32, kR = 4;
-        const int count = ((hi - lo) / span + 1) * subs;
-        auto slot_of_cta = [&](int c) { return 3 * static_cast<int64_t>(c) + (!cut ? 2 : c == ti.c0 ? 1 : 0); };
-        for (int r0 = warp; r0 < rows; r0 += 8 * kR) {
-          float M[kR], sum[kR], acc[kR][V] = {};
-#pragma unroll
-          for (int j = 0; j < kR; ++j) {
-            M[j] = -INFINITY;
-            sum[j] = 0.f;
-          }
-          for (int k0 = 0; k0 < count; k0 += 2) {
-            float2 s[2][kR];
-            float y[2][kR][V];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int k = min(k0 + e, count - 1), i = k / subs, sub = k - i * subs;
-              const int64_t sl = slot_of_cta(lo + i * span);
-#pragma unroll
-              for (int j = 0; j < kR; ++j) {
-                const int rr = min(r0 + 8 * j, rows - 1);
-                const int64_t a = (sl * 2 + (rr >> 7) + (sub & 1)) * 128 + (rr & 127) + 64 * (sub >> 1);
-                s[e][j] = __ldcg(p.ml + a);
-                if constexpr (V == 4)
-                  *reinterpret_cast<float4 *>(y[e][j]) = __ldcg(reinterpret_cast<const float4 *>(p.part + a * kDim + V * lane));
-                else
-                  *reinterpret_cast<float2 *>(y[e][j]) = __ldcg(reinterpret_cast<const float2 *>(p.part + a * kDim + V * lane));
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int j = 0; j < kR; ++j) {
-                const float x = s[e][j].x;
-                if (k0 + e >= count || x == -INFINITY) continue;  // (nothing, and what lies there may be anything)
-                const float m = max_nan(M[j], x);
-                const float f0 = M[j] == m ? 1.f : exp2f(M[j] - m), f1 = x == m ? 1.f : exp2f(x - m);
-                M[j] = m;
-                sum[j] = sum[j] * f0 + s[e][j].y * f1;
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[j][i] = acc[j][i] * f0 + y[e][j][i] * f1;
-              }
-          }
-#pragma unroll
-          for (int j = 0; j < kR; ++j) {
-            const int rr = r0 + 8 * j, i = rr / p.group;
-            if (rr >= rows) continue;
-            if (groups) {
-              const int64_t a = (slot_of_cta(lo) * 2 + (rr >> 7)) * 128 + (rr & 127);
-              if (lane == 0) __stcg(p.ml + a, make_float2(M[j], sum[j]));
-#pragma unroll
-              for (int e = 0; e < V; e += 2)
-                __stcg(reinterpret_cast<float2 *>(p.part + a * kDim + V * lane + e), make_float2(acc[j][e], acc[j][e + 1]));
-              continue;
-            }
-            const int pos = pv.q_pos[ti.t0 + i];
-            if (pos < 0 || (pos >> pv.logP) >= pv.max_pages) continue;
-            const int64_t out_row = static_cast<int64_t>(ti.t0 + i) * pv.H + ti.hk * p.group + rr - i * p.group;
-            const float inv = sum[j] != 0.f ? p.v_gain / sum[j] : 0.f;
-#pragma unroll
-            for (int e = 0; e < V; e += 2)
-              *reinterpret_cast<__nv_bfloat162 *>(p.out + out_row * kDim + V * lane + e) =
-                  __floats2bfloat162_rn(acc[j][e] * inv, acc[j][e + 1] * inv);
-            if (lane == 0 && p.lse) p.lse[out_row] = sum[j] == 0.f ? -INFINITY : (M[j] + log2f(sum[j])) * 0.69314718055994531f;
-          }
-        }
-      };
-      const int pieces = kTwo ? 1 : 2 * reps;
-      if (!cut) {
-        merge(blockIdx.x, blockIdx.x, 1, pieces, false);
-      } else {
-        // the last CTA to add a part merges them; of many, its group's, and the last group to
-        // be done the groups' (one CTA reads 50 bytes a clock)
-        const int me = static_cast<int>(blockIdx.x), parts_n = ti.c1 - ti.c0 + 1;
-        const int fan = max(kFan, static_cast<int>(ceilf(sqrtf(static_cast<float>(parts_n)))));
-        bool groups = parts_n > fan;
-        int lo = groups ? ti.c0 + (me - ti.c0) / fan * fan : ti.c0, hi = groups ? min(lo + fan - 1, ti.c1) : ti.c1;
-        int span = 1, subs = pieces;
-        uint32_t *counter = p.counters + lo;
-        for (;;) {
-          // (the counter of a group of one is the next unit's)
-          const int others = (hi - lo) / span;
-          bool last_one = others == 0;
-          if (!last_one) {
-            if (tid == 0) {
-              last_one = count_part(counter) == static_cast<uint32_t>(others);
-              if (last_one) *counter = 0;  // for the next call
-              *last_s = last_one;
-            }
-            sync();
-            if (!ok) break;
-            last_one = *last_s;
-          }
-          if (!last_one) break;
-          merge(lo, hi, span, subs, groups);
-          if (!groups) break;
-          sync();
-          if (!ok) break;
-          groups = false;
-          lo = ti.c0;
-          hi = ti.c0 + (parts_n - 1) / fan * fan;
-          span = fan;
-          subs = 1;
-          counter = p.counters + kMostCtas + ti.c0;
-        }
-        if (!ok) break;
-      }
-      sync();  // (the next part writes its own rows where a merge may still read)
+      for (int rr = warp; rr < rows; rr += 8) join_row<kDim, kTwo>(p, rr, rows, ti.t0, ti.hk, blockIdx.x, blockIdx.x, lane);
+      sync();  // (the next part writes its own rows where these are read)
       if (!ok) break;
     }
     if (!ok && lane == 0) fail();
@@ -909,7 +877,7 @@ umma4_kernel(const UmmaParams p) {
 }
 
 size_t round_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-int grid_of() { return std::min(sm_count(), kMostCtas); }
+int grid_of() { return sm_count(); }
 
 template <int kDim, bool kTwo>
 cudaError_t launch(const UmmaParams &p, cudaStream_t stream) {
@@ -928,27 +896,31 @@ cudaError_t launch(const UmmaParams &p, cudaStream_t stream) {
   static bool done[64] = {};
   const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), smem, done);
   if (e != cudaSuccess) return e;
-  return launch_ex(false, kern, dim3(grid_of()), dim3(kThreads), smem, stream, 1, p);
+  const cudaError_t l = launch_ex(false, kern, dim3(grid_of()), dim3(kThreads), smem, stream, 1, p);
+  if (l != cudaSuccess) return l;
+  return launch_ex(true, join4_kernel<kDim, kTwo>, dim3(kTwo ? 32 : 16, grid_of()), dim3(256), 0, stream, 1, p);
 }
 
 }  // namespace
 
 size_t attn4_umma_scratch(const sa_paged4_args &pa) {
   const size_t rows = static_cast<size_t>(grid_of()) * 3 * 2 * 128;
-  return round_up(rows * pa.p.D * sizeof(float)) + round_up(rows * sizeof(float2));
+  return round_up(rows * pa.p.D * sizeof(float)) + round_up(rows * sizeof(float2)) + grid_of() * sizeof(int4);
 }
 
 cudaError_t launch_attn4_umma(const sa_paged4_args &pa, const void *q, void *out, float *lse, int rows, void *scratch,
-                              uint32_t *counters, uint32_t *status, cudaStream_t stream) {
+                              uint32_t *status, cudaStream_t stream) {
+  const size_t scratch_rows = static_cast<size_t>(grid_of()) * 3 * 2 * 128;
   UmmaParams p;
   p.c = paged4_view(pa);
   p.q = static_cast<const uint16_t *>(q);
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
-  p.part = static_cast<float *>(scratch);
-  p.ml = reinterpret_cast<float2 *>(static_cast<char *>(scratch) +
-                                    round_up(static_cast<size_t>(grid_of()) * 3 * 2 * 128 * pa.p.D * sizeof(float)));
-  p.counters = counters;
+  char *w = static_cast<char *>(scratch);
+  p.part = reinterpret_cast<float *>(w);
+  w += round_up(scratch_rows * pa.p.D * sizeof(float));
+  p.ml = reinterpret_cast<float2 *>(w);
+  p.cuts = reinterpret_cast<int4 *>(w + round_up(scratch_rows * sizeof(float2)));
   p.group = pa.p.H / pa.p.H_kv;
   p.nt = std::max(1, rows / p.group);
   p.qk_scale = pa.p.scale * pa.k_gain * kLog2e;

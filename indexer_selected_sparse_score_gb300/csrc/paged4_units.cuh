@@ -30,7 +30,8 @@ __device__ __forceinline__ uint32_t count_part(uint32_t *counter) {
 struct UnitStart {
   int block, t0, head, tile;
   long long total;  // tiles of the call
-  int round, pad;   // units count as multiples of it
+  int round;        // units count as multiples of it
+  int tiles;        // above 1: the tiles that there are of the CTA's
 };
 
 // One warp: calls use(first token, last slot) for the units that begin among tokens
@@ -142,7 +143,8 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
       const long long from = upto - static_cast<long long>(counted) * heads;
       if (warp == 0 && x0 < x1 && x0 >= from && x0 < upto) {
         const int rest = static_cast<int>(x0 - from), t = 32 * e + lane;
-        *out = UnitStart{t, t, rest / counted, rest % counted, total, round, 0};
+        *out = UnitStart{t, t, rest / counted, rest % counted, total, round,
+                         min(round, cost[e] - rest % counted)};
       }
       before = __shfl_sync(0xffffffffu, upto, 31);
     }
