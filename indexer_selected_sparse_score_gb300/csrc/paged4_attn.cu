@@ -130,7 +130,8 @@ attn4_kernel(const Attn4Params p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long long x0, x1;
   int ctas;
-  find_units<true>(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
+  find_units<true>(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas,
+                   reinterpret_cast<int *>(smem));
   __syncthreads();
   if (x0 >= x1) return;
   const long long total = start->total;

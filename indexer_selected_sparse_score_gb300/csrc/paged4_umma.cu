@@ -228,7 +228,7 @@ umma4_kernel(const UmmaParams p) {
       mbar_init(&gempty[i], 2);  // issuers
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&qfull[i], 4);
+      mbar_init(&qfull[i], kTwo ? 4 : 8);  // the warps that stage queries
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[2 * i], 4);
       mbar_init(&pfull[2 * i + 1], 4);
@@ -247,7 +247,8 @@ umma4_kernel(const UmmaParams p) {
   }
   long long x0, x1;
   int ctas;
-  find_units<true>(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas);
+  find_units<true>(pv, p.nt, pv.H_kv, kTile, kLeast, reinterpret_cast<long long *>(smem + L::scan), start, p.status, x0, x1, ctas,
+                   reinterpret_cast<int *>(kvs));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -609,7 +610,7 @@ umma4_kernel(const UmmaParams p) {
         // (up to 64 rows lie in the tile twice, each copy with half of the keys)
         reps = !kTwo && rows <= 64 ? 2 : 1;
         r = kTwo ? 128 * w + row : row & (128 / reps - 1);
-        if (live) {
+        if (!kTwo || live) {
           // the row's token and limit
           const int i = r / p.group;
           lim = -1;
@@ -617,19 +618,21 @@ umma4_kernel(const UmmaParams p) {
             const int pos = pv.q_pos[ti.t0 + i];
             if (pos >= 0 && (pos >> pv.logP) < pv.max_pages) lim = pos;
           }
-          if (kTwo || w == 0) {
-            // the warp's 32 query rows as fp16, each scaled by a power of two, into the
-            // K-major swizzled layout; a load covers whole rows
+          {
+            // the warp's 32 query rows (of one row tile: 16) as fp16, each scaled by a power of
+            // two, into the K-major swizzled layout; a load covers whole rows
             constexpr int kLanes = kDim / 8, kPer = 32 / kLanes;
             const int ch = lane % kLanes;
             uint8_t *dst = qt + (ch >> 3) * L::kBlock;
-            constexpr int kBatch = 8;  // loads that go out together
+            constexpr int kRows = kTwo ? 32 : 16;
+            constexpr int kBatch = kRows / kPer < 8 ? kRows / kPer : 8;  // loads that go out together
+            const int first_row = 32 * (warp & 3) + (kTwo ? 0 : 16 * w);
 #pragma unroll 1
-            for (int e0 = 0; e0 < 32; e0 += kBatch * kPer) {
+            for (int e0 = 0; e0 < kRows; e0 += kBatch * kPer) {
               uint4 v[kBatch];
 #pragma unroll
               for (int e = 0; e < kBatch; ++e) {
-                const int to_row = 32 * (warp & 3) + e0 + e * kPer + lane / kLanes;
+                const int to_row = first_row + e0 + e * kPer + lane / kLanes;
                 const int rr = kTwo ? 128 * w + to_row : to_row & (128 / reps - 1), tt = rr / p.group;
                 v[e] = make_uint4(0, 0, 0, 0);
                 if (rr < rows)
@@ -638,7 +641,7 @@ umma4_kernel(const UmmaParams p) {
               }
 #pragma unroll
               for (int e = 0; e < kBatch; ++e) {
-                const int to_row = 32 * (warp & 3) + e0 + e * kPer + lane / kLanes;
+                const int to_row = first_row + e0 + e * kPer + lane / kLanes;
                 uint32_t u[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
                 float top = 0.f;
 #pragma unroll
@@ -657,13 +660,13 @@ umma4_kernel(const UmmaParams p) {
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(&qfull[w]);
+              mbar_arrive(&qfull[kTwo ? w : 0]);
               if (!kTwo && ti.tiles > 1) mbar_arrive(&qfull[1]);
             }
           }
-          if (!kTwo && w == 1) {
-            // (the other stream's warps stage the rows that both hold)
-            ok = mbar_wait_warp(&qfull[1], (qn++) & 1);
+          if (!kTwo && live) {
+            // (the other stream's warps stage half of the rows that both hold)
+            ok = mbar_wait_warp(&qfull[w], (qn++) & 1);
             if (!ok) break;
           }
           cs = fac[row];

@@ -83,15 +83,17 @@ __device__ __forceinline__ void units_of_tokens(const PagedView &v, int nt, int 
 // x1 get them, `ctas` g, and out (shared memory) the first one's place.  warp_s:
 // 32 long longs of shared memory.
 //
-// kWhole: where there are no more units than CTAs (and at most 64 tokens), no CTA has to
-// have parts of two: every unit is cut into pieces of one length (out->round; units then
-// count as multiples of it), if one that is at most 7 tiles above the even share gives no
-// more pieces than CTAs.  (A second part costs a CTA about 4 us, a tile of 128 rows of 144
+// kWhole (unit_s: 128 ints of shared memory): where there are no more units (for all
+// heads) than CTAs, at most 64, among no more tokens than threads, no CTA has to have
+// parts of two: every unit is cut into pieces of one length (out->round; units then count
+// as multiples of it), if one that is at most 7 tiles above the even share gives no more
+// pieces than CTAs.  (A second part costs a CTA about 4 us, a tile of 128 rows of 144
 // bytes 0.8 us when all stream: 16 tokens of 32 over 8 heads of 64 at 0.1 .. 3 K slots
-// 19.9 us by even shares.)  Each warp finds its CTA's place by itself then.
+// 14.4 us, by even shares 19.9.)  Of up to 64 units each warp finds its CTA's place by itself.
 template <bool kWhole = false>
 __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads, int tile, int least, long long *warp_s,
-                                           UnitStart *out, uint32_t *status, long long &x0, long long &x1, int &ctas) {
+                                           UnitStart *out, uint32_t *status, long long &x0, long long &x1, int &ctas,
+                                           int *unit_s = nullptr) {
   // warp w takes the units that begin in its stretch of blocks (of whole 32s of tokens,
   // where a block is one)
   const int warps = (blockDim.x + 31) >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -100,14 +102,43 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
   const int t0 = static_cast<int>(min(static_cast<int64_t>(v.T), static_cast<int64_t>(warp) * per * grain));
   const int t1 = static_cast<int>(min(static_cast<int64_t>(v.T), (static_cast<int64_t>(warp) + 1) * per * grain));
   uint32_t *report = blockIdx.x == 0 ? status : nullptr;
-  if (kWhole && nt == 1 && v.T <= 64 && static_cast<int64_t>(v.T) * heads <= gridDim.x) {
-    int cost[2];  // of tokens lane and 32 + lane
+  int units = 65;
+  int cost[2] = {0, 0}, first[2] = {0, 0};  // of units lane and 32 + lane: tiles, first token
+  if (kWhole && nt == 1 && v.T <= 64) {
+    uint32_t *own = warp == 0 ? report : nullptr;
+    units = v.T;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int t = 32 * e + lane;
       int b, pos;
-      cost[e] = t < v.T && load_paged_token(v, t, report, report != nullptr && warp == 0, b, pos) ? (pos + tile) / tile : 0;
+      first[e] = t;
+      if (t < v.T && load_paged_token(v, t, own, own != nullptr, b, pos)) cost[e] = (pos + tile) / tile;
     }
+  } else if (kWhole && v.T <= static_cast<int>(blockDim.x)) {
+    // a thread per token; unit_s: first tokens, last slots
+    const int t = threadIdx.x;
+    int b = -1, pos = -1;
+    const bool in = t < v.T, valid = in && load_paged_token(v, t, report, report != nullptr, b, pos);
+    const bool begins = in && (t % nt == 0 || b != v.q_seq[t - 1]);
+    if (t < 64) unit_s[64 + t] = -1;
+    long long all;
+    const int u = static_cast<int>(block_prefix(begins ? 1 : 0, warp_s, all)) - (begins ? 0 : 1);
+    if (all <= 64) {
+      if (begins) unit_s[u] = t;
+      if (valid) atomicMax(&unit_s[64 + u], pos);
+    }
+    __syncthreads();
+    if (all <= 64) {
+      units = static_cast<int>(all);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (32 * e + lane < units) {
+          first[e] = unit_s[32 * e + lane];
+          cost[e] = (unit_s[64 + 32 * e + lane] + tile) / tile;
+        }
+    }
+  }
+  if (units <= 64) {
     const int all = __reduce_add_sync(0xffffffffu, cost[0] + cost[1]);
     long long total = static_cast<long long>(all) * heads;
     const int most = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, total / least)));
@@ -118,7 +149,7 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
     };
     int round = 1;
     ctas = most;
-    if (all > 0 && pieces(shortest + 7) <= static_cast<int>(gridDim.x)) {
+    if (all > 0 && static_cast<int64_t>(units) * heads <= gridDim.x && pieces(shortest + 7) <= static_cast<int>(gridDim.x)) {
       round = shortest;
 #pragma unroll
       for (int step = 4; step > 0; step >>= 1)
@@ -142,8 +173,8 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
       upto += before;
       const long long from = upto - static_cast<long long>(counted) * heads;
       if (warp == 0 && x0 < x1 && x0 >= from && x0 < upto) {
-        const int rest = static_cast<int>(x0 - from), t = 32 * e + lane;
-        *out = UnitStart{t, t, rest / counted, rest % counted, total, round,
+        const int rest = static_cast<int>(x0 - from), t = first[e];
+        *out = UnitStart{t / nt, t, rest / counted, rest % counted, total, round,
                          min(round, cost[e] - rest % counted)};
       }
       before = __shfl_sync(0xffffffffu, upto, 31);
