@@ -127,14 +127,30 @@ __device__ __forceinline__ void join_row(const UmmaParams &p, int rr, int rows, 
   constexpr int V = kDim / 32;
   const PagedView &pv = p.c.v;
   const int i = rr / p.group, pos = pv.q_pos[t0 + i];
-  if (pos < 0 || (pos >> pv.logP) >= pv.max_pages) return;
   const int log_subs = kTwo ? 0 : rows <= 64 ? 2 : 1, count = (c1 - c0 + 1) << log_subs;
   auto piece = [&](int k) {  // its index among the rows of scratch
     const int c = c0 + (k >> log_subs), sub = k & ((1 << log_subs) - 1);
     return ((3 * c + (c0 == c1 ? 2 : c == c0 ? 1 : 0)) * 2 + (rr >> 7) + (sub & 1)) * 128 + (rr & 127) + 64 * (sub >> 1);
   };
+  // loads that go out together: rows of two row tiles are many and have few pieces (8: 5 us
+  // more for a chunk; 4 of the others: 8 us more for 64 heads over one)
+  constexpr int kBatch = kTwo ? 4 : 8;
+  float y[kBatch][V];
+  auto load = [&](int k) {
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      if (k + e >= count) continue;
+      const float *src = p.part + static_cast<int64_t>(piece(k + e)) * kDim + V * lane;
+      if constexpr (V == 4)
+        *reinterpret_cast<float4 *>(y[e]) = __ldcg(reinterpret_cast<const float4 *>(src));
+      else
+        *reinterpret_cast<float2 *>(y[e]) = __ldcg(reinterpret_cast<const float2 *>(src));
+    }
+  };
+  load(0);  // (needs nothing of the references)
   float M = -INFINITY;
   for (int k = lane; k < count; k += 32) M = max_nan(M, __ldcg(&p.ml[piece(k)].x));
+  if (pos < 0 || (pos >> pv.logP) >= pv.max_pages) return;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
   float sum = 0.f, acc[V] = {};
@@ -148,23 +164,14 @@ __device__ __forceinline__ void join_row(const UmmaParams &p, int rr, int rows, 
         sum += v.y * f;
       }
     }
-    constexpr int kBatch = 8;  // loads that go out together
     for (int k1 = k0; k1 < min(count, k0 + 32); k1 += kBatch) {
-      float y[kBatch][V], fk[kBatch];
+      if (k1 > 0) load(k1);
 #pragma unroll
       for (int e = 0; e < kBatch; ++e) {
-        fk[e] = __shfl_sync(0xffffffffu, f, (k1 + e) & 31);
-        const float *src = p.part + static_cast<int64_t>(piece(min(k1 + e, count - 1))) * kDim + V * lane;
-        if constexpr (V == 4)
-          *reinterpret_cast<float4 *>(y[e]) = __ldcg(reinterpret_cast<const float4 *>(src));
-        else
-          *reinterpret_cast<float2 *>(y[e]) = __ldcg(reinterpret_cast<const float2 *>(src));
-      }
+        const float fk = __shfl_sync(0xffffffffu, f, (k1 + e) & 31);
+        if (k1 + e >= count || fk < 0.f) continue;
 #pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        if (k1 + e >= count || fk[e] < 0.f) continue;
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = fmaf(y[e][j], fk[e], acc[j]);
+        for (int j = 0; j < V; ++j) acc[j] = fmaf(y[e][j], fk, acc[j]);
       }
     }
   }
@@ -183,7 +190,7 @@ __device__ __forceinline__ void join_row(const UmmaParams &p, int rr, int rows, 
 // (Many SMs at once: by the CTA that added the last part, 11 tokens of 32 over 2 heads at 8 K
 // slots took 128 us, in two steps 75.)
 template <int kDim, bool kTwo>
-__global__ void __launch_bounds__(256) join4_kernel(const UmmaParams p) {
+__global__ void __launch_bounds__(256, kTwo ? 6 : 4) join4_kernel(const UmmaParams p) {
   pdl_wait();
   const int4 u = p.cuts[blockIdx.y];
   const int rr = 8 * blockIdx.x + (threadIdx.x >> 5);
