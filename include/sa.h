@@ -535,7 +535,9 @@ SA_API sa_status sa_paged4_read(const sa_paged4_args *pa, void *k_out, void *v_o
  * their products exactly, as fp16; queries as fp16 scaled by a power of two per
  * row (exact but for values 2^-29 of the row's largest); the weights are rounded
  * to fp16 (by 2^-11 of each or 2^-30 of the row's largest at most); logits,
- * statistics and sums are fp32. */
+ * statistics and sums are fp32.  How the work is cut up goes by the tokens that
+ * a sequence has on average, T / B (the host does not know where they lie): for
+ * a chunk of few sequences of a large table, pass those rows of it alone. */
 SA_API sa_status sa_paged4_attn(const sa_paged4_args *pa, const void *q, void *out, float *lse, void *ws,
                                 size_t ws_bytes, sa_stream_t stream);
 

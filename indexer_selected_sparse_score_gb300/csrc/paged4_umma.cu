@@ -19,14 +19,17 @@
 //   rows, and key tiles go to them in turn; their sums and O are joined at the end.
 //   Up to 64 rows lie in the tile twice, each copy with half of a tile's keys, so that
 //   every softmax thread has keys to take.
-// A row's logits are taken relative to a reference that is raised (and O rescaled)
-// when one passes it by 2^14; weights are then at most 2^14, normal in fp16 down to
-// 2^-28 of the largest.
+// A row's logits are taken relative to a reference, 2^6 below its first ones' largest.
+// Where the weights of 64 keys add up to more than 2^15, it is raised by a power of two
+// that brings the largest back to 2^6, and O is rescaled; so weights stay below fp16's
+// largest and are normal down to 2^-19 of the row's largest, or more.
 //
 // Bound by a stream's chain: a tile's logits, softmax (2900 clocks for 128 keys beside
 // the other stream's products: loads from tensor memory wait behind them), weights,
-// product.  1554 prompt tokens of 32 over 4 heads at 4 .. 8 K slots: 244 us, 0.82
-// PFLOP/s; 64 tokens of 64 heads over one KV head at 16 .. 65 K: 250 us.
+// product (about 5000 clocks, of which the tensor cores work 2048).  1270 prompt tokens of
+// 32 over 4 heads at 6 .. 12 K slots: 238 us, 0.84 PFLOP/s; 64 tokens of 64 heads over one
+// KV head at 32 .. 65 K: 225 us; a call of one short unit: 24 us, of which a part's queries,
+// chain and stores are 15.
 //
 // Work: paged4_units.cuh, units cut evenly over one CTA per SM, or few of them into pieces
 // of one length; what has to be joined goes to scratch, and a second kernel joins the

@@ -581,13 +581,18 @@ def test_evict_long(n, budget):
     _check_evict(c, [n], [n - 1], budget, 128, w, born)
 
 
-@pytest.mark.parametrize("B,Hkv,P", [(40, 4, 64), (10, 4, 128), (5, 4, 32), (19, 8, 16), (1, 1, 64)])
-def test_evict_few_and_many_rows(B, Hkv, P):
-    """Rows of one CTA of either size, and of two, four and eight."""
+@pytest.mark.parametrize("B,Hkv,P,wide", [(40, 4, 64, 0), (10, 4, 128, 0), (5, 4, 32, 0), (19, 8, 16, 0), (1, 1, 64, 0),
+                                          (10, 8, 128, 300), (10, 8, 128, 500), (20, 8, 128, 100), (2, 2, 16, 400)])
+def test_evict_few_and_many_rows(B, Hkv, P, wide):
+    """Rows of one CTA of either size, and of two, four and eight; tables wider than they
+    need to be."""
     lens = [1100 + 37 * i % 1500 for i in range(B)]
     r = np.random.RandomState(43)
     for ties in (False, True):
-        c = Case(43, lens, 64, P, Hkv, 1).tokens([], [])
+        c = Case(43, lens, 64, P, Hkv, 1)
+        c.table = np.concatenate([c.table, np.full((B, wide), -1, np.int32)], axis=1)
+        c.max_pages = c.table.shape[1]
+        c.tokens([], [])
         c.q = torch.zeros(0, c.H, 64, dtype=torch.bfloat16)
         c.upload()
         w, born = _records(c, r, lens, ties)
