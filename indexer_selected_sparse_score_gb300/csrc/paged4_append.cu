@@ -1,7 +1,9 @@
 // The writer and the reader of a paged cache held in 4 bits.
 //
-// append: rows in, rotated (as paged_append.cu does, see the note on angles
-// there), rounded to bf16, and quantised: s = e4m3(max(amax / 6, 2^-9)) of every
+// append: rows in, rotated, rounded to bf16, and quantised (the angles are 64-bit
+// fixed-point turns, exact to 2^-64 of a turn a position; a key whose rounding fp32 does
+// not settle is carried as two floats, since one that is rounded the other way, one in
+// 10^5 otherwise, may get another code or its block another scale): s = e4m3(max(amax / 6, 2^-9)) of every
 // 16 values, codes = e2m1(z / s).  The gain is a power of two, so z = y / gain has
 // bf16's eight significant bits and s four: z / s either is a midpoint between
 // two codes or lies 2^-9 of it away (z 2^k and m s are integers below 2^8).  So
@@ -11,8 +13,8 @@
 //
 // Traffic per token: 4 D bytes of every key and value row pair in, 9/8 D out, 4 D
 // of every query head; bound by HBM and issue for a prefill (10,907 tokens of 64 + 2 x 8
-// heads 76 us, 4.5 TB/s, 67% of the issue slots), by its chain of loads for a decode step
-// (64 tokens 4 us).  One CTA per token, its rows' loads issued before its page is
+// heads 86 us, 4.9 TB/s, 62% of the issue slots), by its chain of loads for a decode step
+// (64 tokens 5 us).  One CTA per token, its rows' loads issued before its page is
 // known; a thread holds two chunks of eight values, the two halves of a block of
 // 16, or (halves) of two blocks that it shares with its neighbour.
 //
@@ -32,6 +34,7 @@ constexpr int kMaxPairs = 64;
 
 struct Turns {
   uint64_t f[kMaxPairs];  // turns per position, times 2^64
+  float4 at[17];          // cosine and sine of k / 128 turns, each as two floats: c, s, the rest of c, of s
 };
 
 struct AppendParams {
@@ -56,24 +59,114 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Four adjacent pairs of one chunk.
-__device__ __forceinline__ void rotate_adjacent(uint32_t (&w)[4], const float2 *cs) {
+// h + l = a + b exactly.
+__device__ __forceinline__ void two_sum(float a, float b, float &h, float &l) {
+  h = __fadd_rn(a, b);
+  const float x = __fsub_rn(h, a);
+  l = __fadd_rn(__fsub_rn(a, __fsub_rn(h, x)), __fsub_rn(b, x));
+}
+
+// Cosine and sine of ph 2^-64 turns to about 2^-40, each as two floats.  The angle is k
+// / 128 turns from the table, after whole quarters, and a rest of at most pi / 128, whose
+// power series end after the fifth and the sixth power.
+__device__ __forceinline__ float4 cos_sin(uint64_t ph, const float4 *at) {
+  constexpr double kTurn = 6.283185307179586476925286766559 / 18446744073709551616.0;
+  constexpr float kHi = static_cast<float>(kTurn), kLo = static_cast<float>(kTurn - static_cast<double>(kHi));
+  const uint32_t quarter = static_cast<uint32_t>((ph + (uint64_t{1} << 61)) >> 62);
+  const int64_t rest = static_cast<int64_t>(ph - (static_cast<uint64_t>(quarter) << 62));
+  const int k = static_cast<int>((rest + (int64_t{1} << 56)) >> 57);  // -16 .. 16
+  const int64_t d = rest - (static_cast<int64_t>(k) << 57);
+  const float d_hi = __ll2float_rn(d), d_lo = __ll2float_rn(d - __float2ll_rn(d_hi));
+  const float a = d_hi * kHi, a_lo = fmaf(d_hi, kHi, -a) + fmaf(d_hi, kLo, d_lo * kHi);
+  const float z = a * a, z_lo = fmaf(a, a, -z) + 2.f * a * a_lo;
+  const float sn_lo = fmaf(a * z, fmaf(z, 1.f / 120.f, -1.f / 6.f), a_lo);                   // sine: a + sn_lo
+  const float m = -0.5f * z, m_lo = fmaf(z * z, fmaf(z, -1.f / 720.f, 1.f / 24.f), -0.5f * z_lo);  // cosine: 1 + m + m_lo
+  float4 t = at[abs(k)];
+  if (k < 0) {
+    t.y = -t.y;
+    t.w = -t.w;
+  }
+  // u + (u m + v sn) for (u, v) = (cosine, -sine) and (sine, cosine) of the table
+  auto turned = [&](float u, float u_lo, float v, float v_lo, float &h, float &l) {
+    const float p = u * m, p_lo = fmaf(u, m, -p), q = v * a, q_lo = fmaf(v, a, -q);
+    float x, x_lo, y, y_lo;
+    two_sum(p, q, x, x_lo);
+    two_sum(u, x, y, y_lo);
+    const float low = y_lo + (x_lo + (p_lo + q_lo + fmaf(u, m_lo, u_lo * m) + fmaf(v, sn_lo, v_lo * a) + u_lo));
+    two_sum(y, low, h, l);
+  };
+  float4 o;
+  turned(t.x, t.z, -t.y, -t.w, o.x, o.z);
+  turned(t.y, t.w, t.x, t.z, o.y, o.w);
+  if (quarter & 1) o = make_float4(-o.y, o.x, -o.w, o.z);
+  if (quarter & 2) o = make_float4(-o.x, -o.y, -o.z, -o.w);
+  return o;
+}
+
+// a c + b s (c, s as two floats) rounded once to fp32, but for 2^-40 of it: a rotated key
+// whose bf16 is another one than the 64-bit value's (by way of fp32, as every conversion
+// of one goes) may be given another code, or its block another scale.
+__device__ __forceinline__ float exact_sum(float a, float c, float c_lo, float b, float s, float s_lo) {
+  const float p = a * c, p_lo = fmaf(a, c, -p), q = b * s, q_lo = fmaf(b, s, -q);
+  float x, x_lo, y, y_lo;
+  two_sum(p, q, x, x_lo);
+  two_sum(x, x_lo + (p_lo + q_lo + fmaf(a, c_lo, b * s_lo)), y, y_lo);
+  return fabsf(y) <= 3.4028235e38f ? y : p + q;  // (infinities, NaN)
+}
+
+// What a key's rotation needs where fp32 does not settle its rounding.
+struct ExactTurn {
+  int64_t turn;
+  const Turns *turns;
+};
+
+// (rarely called, and long)
+__device__ __noinline__ float2 turn_exactly(float a, float b, uint64_t ph, const float4 *at) {
+  const float4 t = cos_sin(ph, at);
+  return make_float2(exact_sum(a, t.x, t.z, b, -t.y, -t.w), exact_sum(a, t.y, t.w, b, t.x, t.z));
+}
+
+// A pair (a, b) turned by c, s (fp32): y0, y1.  For keys (e): sine and cosine are off by
+// 2^-23 and a step's rounding at most, products and sum by 2^-24 of the pair each, together
+// by 5 2^-24 (|a| + |b|); a value that is that near a midpoint of bf16 (one in 3000 or so)
+// is taken exactly.  (10,907 tokens of 64 + 2 x 8 heads, appended and read: 109 us; 99 without
+// looking, 126 with every key taken exactly.)
+template <bool kKey>
+__device__ __forceinline__ void turn_pair(float a, float b, float2 cs, int pair, const ExactTurn &e, float &y0, float &y1) {
+  y0 = a * cs.x - b * cs.y;
+  y1 = a * cs.y + b * cs.x;
+  if (kKey) {
+    auto middle = [](float y) { return __uint_as_float((__float_as_uint(y) & 0xFFFF0000u) | 0x8000u); };
+    const float err = 0x1.4p-22f * (fabsf(a) + fabsf(b));
+    if (fabsf(y0 - middle(y0)) <= err || fabsf(y1 - middle(y1)) <= err) {
+      const float2 y = turn_exactly(a, b, static_cast<uint64_t>(e.turn) * e.turns->f[pair], e.turns->at);
+      y0 = y.x;
+      y1 = y.y;
+    }
+  }
+}
+
+// Four adjacent pairs of one chunk, from `pair` on.
+template <bool kKey>
+__device__ __forceinline__ void rotate_adjacent(uint32_t (&w)[4], const float2 *cs, int pair, const ExactTurn &e) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 c = cs[i];
-    const float a = lo_f(w[i]), b = hi_f(w[i]);
-    w[i] = pack_bf16(a * c.x - b * c.y, a * c.y + b * c.x);
+    float y0, y1;
+    turn_pair<kKey>(lo_f(w[i]), hi_f(w[i]), cs[pair + i], pair + i, e, y0, y1);
+    w[i] = pack_bf16(y0, y1);
   }
 }
 
 // Eight pairs (u[e], w[e]) of two chunks half the rotated span apart.
-__device__ __forceinline__ void rotate_halves(uint32_t (&u)[4], uint32_t (&w)[4], const float2 *cs) {
+template <bool kKey>
+__device__ __forceinline__ void rotate_halves(uint32_t (&u)[4], uint32_t (&w)[4], const float2 *cs, int pair, const ExactTurn &e) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
-    const float a0 = lo_f(u[i]), a1 = hi_f(u[i]), b0 = lo_f(w[i]), b1 = hi_f(w[i]);
-    u[i] = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-    w[i] = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
+    float x0, x1, y0, y1;
+    turn_pair<kKey>(lo_f(u[i]), lo_f(w[i]), cs[pair + 2 * i], pair + 2 * i, e, x0, y0);
+    turn_pair<kKey>(hi_f(u[i]), hi_f(w[i]), cs[pair + 2 * i + 1], pair + 2 * i + 1, e, x1, y1);
+    u[i] = pack_bf16(x0, x1);
+    w[i] = pack_bf16(y0, y1);
   }
 }
 
@@ -134,6 +227,7 @@ append4_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
   };
   constexpr int kUnits = 2;
   bool ok = false, tabled = false;
+  ExactTurn exact{0, &turns};
   int page = -1, slot = 0;
   for (int base = 0; base < units; base += kUnits * threads) {
     uint32_t x[kUnits][4], y[kUnits][4];
@@ -152,16 +246,21 @@ append4_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
     }
     if (!tabled) {
       const int turn = p.rope_pos ? p.rope_pos[t] : pv.q_pos[t];
+      exact.turn = turn;
       int b, pos;
       ok = load_paged_token(pv, t, p.status, threadIdx.x == 0, b, pos);
       if (ok) {
         page = load_page(pv, b, pos >> pv.logP, p.status, threadIdx.x == 0);
         slot = pos & (pv.P - 1);
         if (threadIdx.x < p.dim / 2) {
-          const uint64_t ph = static_cast<uint64_t>(static_cast<int64_t>(turn)) * turns.f[threadIdx.x] + (uint64_t{1} << 31);
+          // the turn's first 32 bits in fp32, and a step along the circle by what that rounds off
+          const uint64_t ph = static_cast<uint64_t>(exact.turn) * turns.f[threadIdx.x] + (uint64_t{1} << 31);
+          const int32_t part = static_cast<int32_t>(ph >> 32);
+          const float x = static_cast<float>(part);
+          const float step = static_cast<float>(part - static_cast<int64_t>(x)) * static_cast<float>(3.14159265358979323846 * 0x1p-31);
           float sn, c;
-          sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &sn, &c);
-          cs[threadIdx.x] = make_float2(c, sn);
+          sincospif(x * 0x1p-31f, &sn, &c);
+          cs[threadIdx.x] = make_float2(fmaf(-sn, step, c), fmaf(c, step, sn));
         }
         if (p.weight) {
           for (int h = threadIdx.x; h < pv.H_kv; h += threads) {
@@ -185,10 +284,16 @@ append4_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
       const int row = u >> log_upr, h = row - p.q_heads;
       if (mine && h < pv.H_kv && c0 >= first) {
         if (half) {
-          rotate_halves(x[e], y[e], cs + 8 * (c0 - first));
+          if (h >= 0)
+            rotate_halves<true>(x[e], y[e], cs, 8 * (c0 - first), exact);
+          else
+            rotate_halves<false>(x[e], y[e], cs, 8 * (c0 - first), exact);
+        } else if (h >= 0) {
+          rotate_adjacent<true>(x[e], cs, 4 * (c0 - first), exact);
+          rotate_adjacent<true>(y[e], cs, 4 * (c1 - first), exact);
         } else {
-          rotate_adjacent(x[e], cs + 4 * (c0 - first));
-          rotate_adjacent(y[e], cs + 4 * (c1 - first));
+          rotate_adjacent<false>(x[e], cs, 4 * (c0 - first), exact);
+          rotate_adjacent<false>(y[e], cs, 4 * (c1 - first), exact);
         }
       }
       if (mine && h < 0) {
@@ -287,7 +392,19 @@ cudaError_t launch_paged4_append(const sa_paged4_args &pa, const void *k, int64_
   p.dim = rope ? rope->dim : 0;
   p.halves = halves ? 1 : 0;
   p.status = status;
+  // (a table of the circle, the same for every call)
+  static const struct Circle {
+    float4 at[17];
+    Circle() {
+      for (int k = 0; k <= 16; ++k) {
+        const double c = std::cos(k * 3.14159265358979323846 / 64.0), s = std::sin(k * 3.14159265358979323846 / 64.0);
+        const float ch = static_cast<float>(c), sh = static_cast<float>(s);
+        at[k] = make_float4(ch, sh, static_cast<float>(c - ch), static_cast<float>(s - sh));
+      }
+    }
+  } circle;
   Turns turns{};
+  std::copy(circle.at, circle.at + 17, turns.at);
   const RopeRamp ramp = p.dim > 0 ? rope_ramp(*rope) : RopeRamp{0.0, 0.0};
   for (int i = 0; i < p.dim / 2; ++i) {
     const double f = rope_frequency(*rope, ramp, i) / (2.0 * 3.14159265358979323846);

@@ -353,6 +353,25 @@ def test_append(D, P, Hkv, G, dim, halves):
     _check_append(c, k, v, dim, halves, [100069, 0, 2000000000, 7, -3, 64])
 
 
+@pytest.mark.parametrize("D,dim,halves,far", [(128, 128, True, 0), (128, 64, False, 100000), (64, 64, True, 3)])
+def test_append_rounds_keys_as_64_bits_do(D, dim, halves, far):
+    """Every code and scale of many rotated keys.  A key is within 2^-40 of its pair's
+    magnitude (2^-9 of the rounding's step to bf16, by way of fp32, 2^-15 of fp32's), so of
+    a million one in 2^-31 2^20, or none, is expected to be rounded another way; the 64-bit
+    angle is exact to 2^-52 of 10^5."""
+    n, Hkv = 1000, 8
+    c = Case(24, [n], D, 64, Hkv, 1).tokens([0] * n, range(n)).upload()
+    k, v = (torch.from_numpy(c.r.standard_normal((n, Hkv, D))).bfloat16() for _ in range(2))
+    turn = np.arange(n) * 7 + far
+    _append(c, k.to(DEV), v.to(DEV), dim, halves, turn)
+    kr, _ = ref.rotate(k.double(), turn, ref.rope_freqs(dim, 10000.0), halves)
+    for got, x in zip((("K", "Ks"), ("V", "Vs")), (kr, v.double())):
+        codes, scales = r4.quantise(x.float().bfloat16().double().numpy())
+        page = c.table[0, np.arange(n) // 64]
+        assert np.array_equal(c.d[got[0]].cpu().numpy()[page, :, np.arange(n) % 64], codes)
+        assert np.array_equal(c.d[got[1]].cpu().numpy()[page, :, np.arange(n) % 64], scales)
+
+
 def test_append_a_ragged_prompt():
     lens = [333, 1, 500, 64]
     seq = np.repeat(range(4), lens).tolist()

@@ -147,7 +147,7 @@ def test_evict_arguments(lib):
                dict(wo=1 << 20), dict(bo=2 << 20), dict(wo=2 << 20), dict(bo=1 << 20), dict(bo=3 << 20),
                dict(wo=(1 << 20) + 16), dict(no=4096), dict(no=8196)):
         assert _evict(lib, pa, **kw) == INV, kw
-    assert _evict(lib, pa, ws=None) == WS and _evict(lib, pa, nb=4096) == WS
+    assert _evict(lib, pa, ws=None) == WS and _evict(lib, pa, nb=4095) == WS
     assert _evict(lib, _pa(B=1 << 20, H_kv=128, H=128, n_pages=1)) == UNS
 
 
