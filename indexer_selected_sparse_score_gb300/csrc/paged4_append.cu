@@ -411,6 +411,8 @@ cudaError_t launch_paged4_append(const sa_paged4_args &pa, const void *k, int64_
     turns.f[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
   }
   const int units = (p.q_heads + 2 * pa.p.H_kv) * (pa.p.D / 16);
+  // few tokens: as many threads as may be, so that a CTA's loads go out at once; many: no more than
+  // a thread has two units
   const int threads =
       pa.p.T > 4 * sm_count() ? std::min(std::max((units / 2 + 31) & ~31, kMaxPairs), kThreads) : kThreads;
   return launch_ex(false, append4_kernel, dim3(pa.p.T), dim3(threads), 0, stream, 1, p, turns);

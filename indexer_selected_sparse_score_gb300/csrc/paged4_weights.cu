@@ -28,7 +28,10 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;            // 16 warps of 128 registers (three CTAs spill: 55 us against 49)
 constexpr int kStages = 4;               // tiles that a warp has in its ring
-constexpr int kMostColumns = 32;         // of a unit, on average; more: paged4_weights_umma.cu
+// Columns of a unit, on average; more: paged4_weights_umma.cu (64 sequences of 8 .. 16 K slots
+// and one KV head, 32 columns: 65 us here, 131 there; 64 columns: 117 and 148; 1024 prompt
+// tokens, 8192 columns a KV head: 1302 and 99).
+constexpr int kMostColumns = 64;
 constexpr int kRunsInSmem = 256;         // tokens whose runs a CTA works out by itself
 
 struct WeightsParams {
