@@ -434,9 +434,9 @@ cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, flo
   if (pa.p.T == 0) return cudaSuccess;
   // Up to 16 columns (O of more is more than a warp's registers) here.  More on the 5th-
   // generation tensor cores (1270 prompt tokens of 32 over 4 heads, in groups of 16 columns
-  // 2414 us here, 239 there), up to 128 with one row tile (64 sequences of 64 heads over one KV head: 223 us, with two 345; 4
-  // tokens of 32 heads over one: 72 and 90), above with two (those prompts 201 us
-  // alone, with one 263).
+  // 2414 us here, 239 there): up to 128 with one row tile (64 sequences of 64 heads over one
+  // KV head 223 us, with two 345; 4 tokens of 32 heads over one 72 and 90), above with two
+  // (those prompts 201 us alone, with one 263).
   const int columns = columns_of(pa);
   if (columns > 16)
     return launch_attn4_umma(pa, q, out, lse, columns > 128 ? 256 : 128, scratch, status, stream);
