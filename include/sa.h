@@ -25,7 +25,9 @@
  * sa_workspace_size() bytes, which must be zero-filled once before its first
  * use (sa_workspace_init).  All work is enqueued on the caller's stream; no
  * call synchronises except sa_check_device_status.  Calls that share a
- * workspace must not run concurrently.
+ * workspace must not run concurrently; calls of any kind may use one in turn
+ * (the largest of their sizes serves all of them), since what has to stay
+ * between calls lies in its first 4096 bytes, and scratch behind them.
  *
  * Errors: arguments are checked on the host before anything is enqueued; a
  * bad argument returns an error and enqueues nothing.  sa_last_error_detail()
@@ -127,9 +129,9 @@ typedef struct {
  * the arguments are invalid. */
 SA_API size_t sa_workspace_size(const sa_index_args *ia, const sa_attn_args *aa, int32_t K);
 
-/* Zero-fills the workspace's first 4096 bytes (all of it when it is smaller),
- * which hold the sticky device status word and the calls' counters.  Call it
- * once on a new workspace.  Enqueued on `stream`. */
+/* Zero-fills the workspace's header, its first 4096 bytes (all of it when it is
+ * smaller), which holds the sticky device status word and counters that a call
+ * leaves at zero.  Call it once on a new workspace.  Enqueued on `stream`. */
 SA_API sa_status sa_workspace_init(void *ws, size_t ws_bytes, sa_stream_t stream);
 
 /* Index scores ("DeepSeek-V4.1-Flash-NVFP4 inference/model.py",
@@ -172,7 +174,7 @@ SA_API sa_status sa_topk(const float *scores, int64_t ld, const sa_index_args *i
  * unspecified picks); cand: [T, sa_candidate_words(N_c, block_size)] uint32,
  * written in full.  block_size >= 1, topk_blocks >= 0; nb > 32768 or
  * N_c > 2^30 returns SA_ERR_UNSUPPORTED.  The selection is exact on the fp32 values.  The
- * workspace needs only its 256-byte header (the status word). */
+ * workspace needs only 256 bytes (for the status word). */
 SA_API sa_status sa_candidate_blocks(const float *scores, int64_t ld, const sa_index_args *ia, int32_t block_size,
                                      int32_t topk_blocks, uint32_t *cand, void *ws, size_t ws_bytes,
                                      sa_stream_t stream);
@@ -209,7 +211,7 @@ SA_API sa_status sa_topk_candidates(const float *scores, int64_t ld, const sa_in
  * 1); a d outside [0, dst_rows) is skipped and flagged (sa_check_device_status
  * reports SA_ERR_DEVICE_DATA).  x 16-byte aligned; codes, scales and dst 4-byte
  * aligned; dim other than 128 returns SA_ERR_UNSUPPORTED.  The workspace needs
- * only its 256-byte header.  Feeding the codes and scales to sa_indexer_scores
+ * only 256 bytes.  Feeding the codes and scales to sa_indexer_scores
  * (fp8 queries with q_scale, fp8 keys with k_scale) gives the V3.2 index score. */
 SA_API sa_status sa_rotate_quant(const void *x, int32_t rows, int32_t dim, const int32_t *dst, int64_t dst_rows,
                                  uint8_t *codes, float *scales, void *ws, size_t ws_bytes, sa_stream_t stream);
@@ -240,7 +242,7 @@ SA_API sa_status sa_compress_prefill(const float *kv, const float *score, int32_
  * out[b] ([B, D] bf16); the other rows of out are left untouched.  A negative
  * pos[b] is skipped and flagged in the workspace status word
  * (sa_check_device_status reports SA_ERR_DEVICE_DATA); the workspace needs
- * only its 256-byte header.  Same limits on r, D, B and eps as
+ * only 256 bytes.  Same limits on r, D, B and eps as
  * sa_compress_prefill. */
 SA_API sa_status sa_compress_decode(const float *kv, const float *score, const int32_t *pos, int32_t B, int32_t D,
                                     int32_t r, float *kv_state, float *score_state, const float *weight, float eps,
@@ -279,8 +281,8 @@ typedef struct {
  * quotients are correctly rounded fp32.  D_I = 128, dim a multiple of 4 in
  * [0, 128]; k_seq_stride 0 (dense: N_rows * D_I) or a multiple of D_I of at
  * least N_rows * D_I; seq[i] outside [0, B) or grp[i] outside [0, N_rows) is
- * skipped and flagged (SA_ERR_DEVICE_DATA).  The workspace needs only its
- * 256-byte header. */
+ * skipped and flagged (SA_ERR_DEVICE_DATA).  The workspace needs only
+ * 256 bytes. */
 SA_API sa_status sa_index_key_publish(const void *kproj, int32_t n, int32_t D_I, const int32_t *seq,
                                       const int32_t *grp, int32_t r, const float *weight, float eps,
                                       const sa_rope_args *rope, uint8_t *k_I, float *k_scale, int32_t B,
@@ -343,8 +345,8 @@ SA_API size_t sa_noalloc_scratch_bytes(void);
  * holds that array until the process exits.  Nothing is allocated or freed:
  * no cudaMalloc, cudaFree or allocating library routine is called.
  *
- * - Size limit: a problem whose scratch (sa_workspace_size for the same
- *   arguments) exceeds SA_NOALLOC_SCRATCH_BYTES is rejected with
+ * - Size limit: a problem whose scratch (3840 bytes less than sa_workspace_size
+ *   for the same arguments) exceeds SA_NOALLOC_SCRATCH_BYTES is rejected with
  *   SA_ERR_UNSUPPORTED and enqueues nothing.
  * - Set-up: the first call in each CUDA context (a device's primary context,
  *   with that device current, in the usual case) looks up the array's device

@@ -18,7 +18,14 @@ struct SplitPlan {
 };
 SplitPlan plan_splits(int T, int W, int K);
 
-// Workspace carve-up (byte offsets, 256-byte aligned).
+// A workspace starts with a header: the sticky status word, and from kWsCounters on the 4-bit
+// attention's counters, which have to be 0 between calls.  Every call's scratch lies behind
+// the header, so that calls of all kinds may share a workspace in turn.
+constexpr size_t kWsHeader = 4096;
+constexpr size_t kWsCounters = 1024;
+constexpr size_t kNoAllocHeader = 256;  // of the library's own scratch, which no other call uses
+
+// Workspace carve-up (byte offsets, 256-byte aligned); scratch from `header` on.
 struct WsLayout {
   size_t status, scores, idx, score_scratch, attn_scratch, part_m, part_l, part_o, total;
 };
@@ -30,7 +37,7 @@ int sm_count();
 // Sets a kernel's dynamic shared-memory limit once per device (flag array of
 // 64 devices owned by the caller).
 cudaError_t set_smem_once(const void *func, size_t bytes, bool *done_per_device);
-WsLayout ws_layout(const sa_index_args &ia, const sa_attn_args *aa, int K);
+WsLayout ws_layout(const sa_index_args &ia, const sa_attn_args *aa, int K, size_t header = kWsHeader);
 
 // Index scores.  `scratch` (idx_score_scratch(ia) bytes, 256-byte aligned)
 // holds the tensor-core kernel's packed queries and folded head weights.
@@ -153,7 +160,7 @@ cudaError_t launch_paged4_append(const sa_paged4_args &pa, const void *k, int64_
                                  int32_t *born, int64_t ld, uint32_t *status, cudaStream_t stream);
 cudaError_t launch_paged4_read(const sa_paged4_args &pa, void *k_out, void *v_out, uint32_t *status,
                                cudaStream_t stream);
-constexpr int kAttn4Counters = 512;  // words of the workspace header, 0 between calls
+constexpr int kAttn4Counters = 512;  // words of the workspace header from kWsCounters on, 0 between calls
 cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, float *lse, void *scratch,
                          uint32_t *counters, uint32_t *status, cudaStream_t stream);
 size_t attn4_scratch(const sa_paged4_args &pa);
@@ -214,7 +221,7 @@ cudaError_t launch_ex(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block,
 sa_status set_error(sa_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 
 // The fused launch sequence on a caller-chosen scratch region (laid out by
-// ws_layout) with a caller-chosen status word (may be NULL).
+// ws_layout behind kNoAllocHeader bytes) with a caller-chosen status word (may be NULL).
 sa_status fused_with_scratch(const sa_index_args *ia, const sa_attn_args *aa, int K,
                              int32_t *idx_out, void *out, void *scratch, size_t scratch_bytes,
                              uint32_t *status, cudaStream_t stream);

@@ -9,9 +9,8 @@ namespace {
 
 using sa::set_error;
 
-constexpr size_t kHeader = 4096;     // status word, counters
-constexpr size_t kCounters = 1024;   // byte offset of the attention's counters
-static_assert(kCounters + 4 * sa::kAttn4Counters <= kHeader, "header");
+using sa::kWsHeader;
+static_assert(sa::kWsCounters + 4 * sa::kAttn4Counters <= kWsHeader, "header");
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -66,7 +65,7 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 }
 
 uint32_t *status_of(void *ws) { return static_cast<uint32_t *>(ws); }
-void *scratch_of(void *ws) { return static_cast<char *>(ws) + kHeader; }
+void *scratch_of(void *ws) { return static_cast<char *>(ws) + kWsHeader; }
 cudaStream_t cu(sa_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace
@@ -75,7 +74,7 @@ extern "C" {
 
 size_t sa_paged4_workspace_size(const sa_paged4_args *pa) {
   if (check_paged4(pa, false, false) != SA_OK) return 0;
-  return kHeader + std::max({sa::attn4_scratch(*pa), sa::weights4_scratch(*pa), sa::evict4_scratch(*pa)});
+  return kWsHeader + std::max({sa::attn4_scratch(*pa), sa::weights4_scratch(*pa), sa::evict4_scratch(*pa)});
 }
 
 sa_status sa_paged4_append(const sa_paged4_args *pa, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -114,9 +113,9 @@ sa_status sa_paged4_attn(const sa_paged4_args *pa, const void *q, void *out, flo
   if (pa->p.T > 0 && !out) return set_error(SA_ERR_INVALID_ARG, "out must be a device pointer");
   if (!aligned(out, 16) || !aligned(lse, 4))
     return set_error(SA_ERR_INVALID_ARG, "out must be 16-byte aligned, lse 4-byte aligned");
-  if (sa_status s = check_ws(ws, ws_bytes, kHeader + sa::attn4_scratch(*pa))) return s;
+  if (sa_status s = check_ws(ws, ws_bytes, kWsHeader + sa::attn4_scratch(*pa))) return s;
   cudaError_t e = sa::launch_attn4(*pa, q, out, lse, scratch_of(ws),
-                                   reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + kCounters), status_of(ws),
+                                   reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + sa::kWsCounters), status_of(ws),
                                    cu(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, "4-bit attention launch");
 }
@@ -128,7 +127,7 @@ sa_status sa_paged4_weights(const sa_paged4_args *pa, const void *q, const float
   if (pa->p.T > 0 && (!lse || !weight)) return set_error(SA_ERR_INVALID_ARG, "lse and weight must be device pointers");
   if (!aligned(lse, 4)) return set_error(SA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   if (sa_status s = check_records(pa, weight, nullptr, ld)) return s;
-  if (sa_status s = check_ws(ws, ws_bytes, kHeader + sa::weights4_scratch(*pa))) return s;
+  if (sa_status s = check_ws(ws, ws_bytes, kWsHeader + sa::weights4_scratch(*pa))) return s;
   cudaError_t e = sa::launch_weights4(*pa, q, lse, weight, ld, scratch_of(ws), status_of(ws), cu(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, "slot weights launch");
 }
@@ -156,7 +155,7 @@ sa_status sa_paged4_evict(const sa_paged4_args *pa, const int32_t *length, const
       overlap(weight_out, bytes, born_out, bytes) || overlap(length, lens, length_out, lens) ||
       overlap(newest, lens, length_out, lens))
     return set_error(SA_ERR_INVALID_ARG, "the records and lengths that are written may not overlap those that are read");
-  if (sa_status s = check_ws(ws, ws_bytes, kHeader + sa::evict4_scratch(a))) return s;
+  if (sa_status s = check_ws(ws, ws_bytes, kWsHeader + sa::evict4_scratch(a))) return s;
   cudaError_t e = sa::launch_evict4(a, length, newest, budget, recent, weight, born, weight_out, born_out, ld, length_out,
                                     scratch_of(ws), status_of(ws), cu(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, "eviction launch");

@@ -126,7 +126,7 @@ struct FusedLayout {
 FusedLayout fused_layout(const sa_paged_args &pa, int K, int local) {
   FusedLayout L{};
   const size_t rows = K > 0 ? static_cast<size_t>(pa.T) * pa.H_kv : 0;
-  size_t off = 256;
+  size_t off = sa::kWsHeader;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += round_up(bytes);
@@ -154,7 +154,7 @@ extern "C" {
 size_t sa_paged_workspace_size(const sa_paged_args *pa, int32_t K, int32_t local, int32_t shared_pages) {
   if (check_paged(pa, false) != SA_OK || check_lists(K, local) != SA_OK || check_shared(pa, shared_pages) != SA_OK)
     return 0;
-  return std::max(fused_layout(*pa, K, local).total, 256 + round_up(sa::prefix_attn_scratch(*pa, shared_pages)));
+  return std::max(fused_layout(*pa, K, local).total, sa::kWsHeader + round_up(sa::prefix_attn_scratch(*pa, shared_pages)));
 }
 
 sa_status sa_paged_append(const sa_paged_args *pa, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -206,9 +206,9 @@ sa_status sa_block_attn(const sa_paged_args *pa, const void *q, const int32_t *i
   if (sa_status s = check_out(pa, out)) return s;
   if (pa->T > 0 && K > 0 && !idx) return set_error(SA_ERR_INVALID_ARG, "idx must be a device pointer");
   if (!aligned(idx, 4)) return set_error(SA_ERR_INVALID_ARG, "idx must be 4-byte aligned");
-  if (sa_status s = check_ws(ws, ws_bytes, 256 + sa::block_attn_scratch(*pa, K, local))) return s;
+  if (sa_status s = check_ws(ws, ws_bytes, sa::kWsHeader + sa::block_attn_scratch(*pa, K, local))) return s;
   cudaError_t e =
-      sa::launch_block_attn(*pa, q, idx, K, local, out, at<void>(ws, 256), at<uint32_t>(ws, 0), cu(stream));
+      sa::launch_block_attn(*pa, q, idx, K, local, out, at<void>(ws, sa::kWsHeader), at<uint32_t>(ws, 0), cu(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, "block attention launch");
 }
 
@@ -252,9 +252,9 @@ sa_status sa_prefix_attn(const sa_paged_args *pa, const void *q, int32_t shared_
   if (sa_status s = check_shared(pa, shared_pages)) return s;
   if (sa_status s = check_queries(pa, q, nullptr, false)) return s;
   if (sa_status s = check_out(pa, out)) return s;
-  if (sa_status s = check_ws(ws, ws_bytes, 256 + sa::prefix_attn_scratch(*pa, shared_pages))) return s;
+  if (sa_status s = check_ws(ws, ws_bytes, sa::kWsHeader + sa::prefix_attn_scratch(*pa, shared_pages))) return s;
   cudaError_t e =
-      sa::launch_prefix_attn(*pa, q, shared_pages, out, at<void>(ws, 256), at<uint32_t>(ws, 0), cu(stream));
+      sa::launch_prefix_attn(*pa, q, shared_pages, out, at<void>(ws, sa::kWsHeader), at<uint32_t>(ws, 0), cu(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, "prefix attention launch");
 }
 

@@ -131,11 +131,11 @@ T *at(void *ws, size_t off) {
 
 namespace sa {
 
-WsLayout ws_layout(const sa_index_args &ia, const sa_attn_args *aa, int K) {
+WsLayout ws_layout(const sa_index_args &ia, const sa_attn_args *aa, int K, size_t header) {
   WsLayout L{};
   size_t off = 0;
   L.status = off;
-  off += 256;
+  off += header;
   L.scores = off;
   off += round_up(sizeof(float) * static_cast<size_t>(ia.T) * ia.N_c);
   L.idx = off;
@@ -188,7 +188,7 @@ sa_status fused_with_scratch(const sa_index_args *ia, const sa_attn_args *aa, in
   if (ia->T > 0 && !out) return fail(SA_ERR_INVALID_ARG, "out must be a device pointer");
   if (!aligned4(idx_out) || !aligned16(out))
     return fail(SA_ERR_INVALID_ARG, "idx_out must be 4-byte and out 16-byte aligned");
-  const WsLayout L = ws_layout(*ia, aa, K);
+  const WsLayout L = ws_layout(*ia, aa, K, kNoAllocHeader);
   if (sa_status s = check_ws(scratch, scratch_bytes, L.total)) return s;
   float *scores = at<float>(scratch, L.scores);
   int32_t *idx = idx_out ? idx_out : at<int32_t>(scratch, L.idx);
@@ -218,7 +218,7 @@ size_t sa_workspace_size(const sa_index_args *ia, const sa_attn_args *aa, int32_
 
 sa_status sa_workspace_init(void *ws, size_t ws_bytes, sa_stream_t stream) {
   if (sa_status s = check_ws(ws, ws_bytes, 256)) return s;
-  cudaError_t e = cudaMemsetAsync(ws, 0, std::min<size_t>(ws_bytes, 4096), reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = cudaMemsetAsync(ws, 0, std::min<size_t>(ws_bytes, sa::kWsHeader), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, "cudaMemsetAsync");
 }
 

@@ -86,8 +86,9 @@ extern "C" sa_status sa_fused_decode_noalloc(const sa_index_args *ia, const sa_a
   if (K < 0) return sa::set_error(SA_ERR_INVALID_ARG, "K must be >= 0");
   if ((reinterpret_cast<uintptr_t>(device_status) & 3u) != 0)
     return sa::set_error(SA_ERR_INVALID_ARG, "device_status must be 4-byte aligned");
-  const size_t need = sa_workspace_size(ia, aa, K);
-  if (need == 0) return sa::set_error(SA_ERR_INVALID_ARG, "arguments rejected (see the other entry points' checks)");
+  if (sa_workspace_size(ia, aa, K) == 0)
+    return sa::set_error(SA_ERR_INVALID_ARG, "arguments rejected (see the other entry points' checks)");
+  const size_t need = sa::ws_layout(*ia, aa, K, sa::kNoAllocHeader).total;
   if (need > kNoAllocScratchBytes)
     return sa::set_error(SA_ERR_UNSUPPORTED,
                          "problem needs %zu bytes of scratch; sa_fused_decode_noalloc has %zu "
