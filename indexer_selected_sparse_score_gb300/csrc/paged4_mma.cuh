@@ -272,7 +272,9 @@ struct Columns {
             if (x[h][nt][k] != -INFINITY) top = fmaxf(top, __fmul_rn(s[h][nt][k], cs[nt][e]));
 #pragma unroll
         for (int m = 4; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        const float r = ref[nt][e], nr = top > r + kRefTop ? top - kRefHead : r;
+        // (passed as step() sees it: r + kRefTop would be rounded, by more than fp16 has room for
+        // where a step of fp32 is 4 or more)
+        const float r = ref[nt][e], nr = __fadd_rn(top, -r) > kRefTop ? top - kRefHead : r;
         const float f = r == nr ? 1.f : exp2_fast(r - nr);
         ref[nt][e] = nr;
         l[nt][e] *= f;
