@@ -507,9 +507,10 @@ SA_API size_t sa_paged4_workspace_size(const sa_paged4_args *pa);
 
 /* Appends new keys and values.  For token t in slot q_pos[t], every KV head:
  *   y = bf16( R(r) k[t, h] ), z = y / k_gain;  and z = v[t, h] / v_gain
- * (R k to 2^-40, rounded to fp32 and then to bf16) with R as in sa_paged_append
- * (rope->dim a multiple of 32) at r = rope_pos[t] ([T] int32, any value; NULL for
- * q_pos[t]); then for every 16 values
+ * (R k to 2^-39 + |r| 2^-61 of the pair's magnitude, R being the rotation by r times
+ * the frequencies as doubles; rounded to fp32 and then to bf16) with R as in
+ * sa_paged_append (rope->dim a multiple of 32) at r = rope_pos[t] ([T] int32, any
+ * value; NULL for q_pos[t]); then for every 16 values
  *   scale = e4m3( max(max |z| / 6, 2^-9) ), codes = e2m1( z / scale ),
  * both to the nearest, ties to even, saturating at 448 and 6, the quotients
  * exact.  A NaN among the 16 makes the scale NaN (and so all of them).  q, q_out,

@@ -1,7 +1,7 @@
 // The writer and the reader of a paged cache held in 4 bits.
 //
 // append: rows in, rotated, rounded to bf16, and quantised (the angles are 64-bit
-// fixed-point turns, exact to 2^-64 of a turn a position; a key whose rounding fp32 does
+// fixed-point turns, 2^-64 of a turn off a position at most; a key whose rounding fp32 does
 // not settle is carried as two floats, since one that is rounded the other way, one in
 // 10^5 otherwise, may get another code or its block another scale): s = e4m3(max(amax / 6, 2^-9)) of every
 // 16 values, codes = e2m1(z / s).  The gain is a power of two, so z = y / gain has
@@ -25,6 +25,7 @@
 #include "internal.h"
 #include "paged4.cuh"
 #include "paged_list.h"
+#include "paged_turns.h"
 
 namespace sa {
 namespace {
@@ -66,7 +67,7 @@ __device__ __forceinline__ void two_sum(float a, float b, float &h, float &l) {
   l = __fadd_rn(__fsub_rn(a, __fsub_rn(h, x)), __fsub_rn(b, x));
 }
 
-// Cosine and sine of ph 2^-64 turns to about 2^-40, each as two floats.  The angle is k
+// Cosine and sine of ph 2^-64 turns to 2^-39 (2^-39.7 over 5 million angles), each as two floats.  The angle is k
 // / 128 turns from the table, after whole quarters, and a rest of at most pi / 128, whose
 // power series end after the fifth and the sixth power.
 __device__ __forceinline__ float4 cos_sin(uint64_t ph, const float4 *at) {
@@ -103,7 +104,7 @@ __device__ __forceinline__ float4 cos_sin(uint64_t ph, const float4 *at) {
   return o;
 }
 
-// a c + b s (c, s as two floats) rounded once to fp32, but for 2^-40 of it: a rotated key
+// a c + b s (c, s as two floats) rounded once to fp32, but for 2^-39 of |a| + |b|: a rotated key
 // whose bf16 is another one than the 64-bit value's (by way of fp32, as every conversion
 // of one goes) may be given another code, or its block another scale.
 __device__ __forceinline__ float exact_sum(float a, float c, float c_lo, float b, float s, float s_lo) {
@@ -406,10 +407,7 @@ cudaError_t launch_paged4_append(const sa_paged4_args &pa, const void *k, int64_
   Turns turns{};
   std::copy(circle.at, circle.at + 17, turns.at);
   const RopeRamp ramp = p.dim > 0 ? rope_ramp(*rope) : RopeRamp{0.0, 0.0};
-  for (int i = 0; i < p.dim / 2; ++i) {
-    const double f = rope_frequency(*rope, ramp, i) / (2.0 * 3.14159265358979323846);
-    turns.f[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
-  }
+  for (int i = 0; i < p.dim / 2; ++i) turns.f[i] = turns_of(rope_frequency(*rope, ramp, i));
   const int units = (p.q_heads + 2 * pa.p.H_kv) * (pa.p.D / 16);
   // few tokens: as many threads as may be, so that a CTA's loads go out at once; many: no more than
   // a thread has two units

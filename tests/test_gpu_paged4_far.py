@@ -1,9 +1,12 @@
-"""The 4-bit cache where numbers are far from ordinary ones: logits past 2^24."""
+"""The 4-bit cache where numbers are far from ordinary ones: logits past 2^24,
+rotations at far positions."""
 import numpy as np
 import pytest
 import torch
 
 import paged4_ref as r4
+import turns
+from indexer_selected_sparse_score_gb300 import binding as sb
 from test_gpu_paged4 import Case, step
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +46,66 @@ def test_logits_where_a_step_of_fp32_is_not_small(G):
     assert not bad.any(), [rows[i] for i in bad.nonzero()[:, 0]]
     want = np.log(2) * (first + more) + np.log(n // 2)
     assert ((lse - want).abs() <= 2.0 ** -20 * want).all()
+
+
+def _turned(a, b, ang):
+    return a * np.cos(ang) - b * np.sin(ang), a * np.sin(ang) + b * np.cos(ang)
+
+
+def _bf16(x):
+    return torch.from_numpy(np.asarray(x)).float().bfloat16().double().numpy()
+
+
+@pytest.mark.parametrize("far,halves", [(2 ** 31 - 1, True), (-2 ** 31, False), (-(2 ** 30) - 7, True)])
+def test_append_at_far_positions(far, halves):
+    """Keys whose code depends on the last bits of the angle: one value, rotated, lies so near
+    the middle of two bf16 neighbours to either side of a code's border that an angle from
+    a frequency over 2 pi as a double (2^-56.5 of a turn off a position for a frequency of
+    1, 2^-22.8 in radians at 2^31) gives another code.  Base 2^32 and 64 rotated values:
+    frequencies 2^-i, exact.  What the call promises, 2^-39 + |r| 2^-61, is below 2^-29.9;
+    values within 2^-29 of a rounding's border, by way of fp32 too, are left out."""
+    D, dim, each = 128, 64, 800000
+    pos = far - np.sign(far) * 977 * np.arange(48)
+    ang = turns.angles(pos, 2.0 ** -np.arange(dim // 2.0))
+    double = [int(p) * int(2.0 ** 64 / (2 * np.pi)) % (1 << 64) / 2.0 ** 64 * 2 * np.pi for p in pos]
+    r = np.random.RandomState(abs(far) % 1000 + halves)
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])  # for a scale of 1
+    rows = []
+    for i in range(len(pos)):
+        a, b = (_bf16(r.choice([-1, 1], each) * 2.0 ** r.uniform(-m, 2, each)) for m in (2, 12))
+        y, z, e = _turned(a, b, ang[i, 0])[0], _turned(a, b, double[i])[0], 2.0 ** -29 * (np.abs(a) + np.abs(b))
+        # (a border is a bf16 value, and a tie: of two neighbours, the codes differ where it is one)
+        lo, hi = np.sort(np.abs([_bf16(y), _bf16(z)]), axis=0)
+        rows += [(i, a[j], b[j]) for j in np.nonzero((lo < hi) & (hi < 5.5) & (_bf16(y - e) == _bf16(y + e)))[0]
+                 if np.isin(borders, [lo[j], hi[j]]).any()]
+    n = len(rows)
+    at = np.array([x[0] for x in rows])
+    # pair 0 is the one above; pair 7's first value becomes 6, so that the scale of both's block is 1
+    first, step_, second = D - dim, (1 if halves else 2), (dim // 2 if halves else 1)
+    k = torch.zeros(n, 1, D, dtype=torch.float64)
+    k[:, 0, first], k[:, 0, first + second] = torch.tensor([x[1:] for x in rows], dtype=torch.float64).T
+    k[:, 0, first + 7 * step_] = torch.from_numpy(6 * np.cos(ang[at, 7])).bfloat16()
+    k[:, 0, first + 7 * step_ + second] = torch.from_numpy(-6 * np.sin(ang[at, 7])).bfloat16()
+
+    def quantised(angle):
+        x = k.clone().numpy()
+        for i in (0, 7):
+            u = first + i * step_
+            x[:, 0, u], x[:, 0, u + second] = _turned(k[:, 0, u].numpy(), k[:, 0, u + second].numpy(), angle[:, i])
+        return r4.quantise(_bf16(x))
+    codes, scales = quantised(ang[at])
+    other, _ = quantised(np.where(np.arange(dim // 2) == 0, np.array(double)[at][:, None], ang[at]))
+    block = slice(first // 2, first // 2 + 8)
+    tells = (codes != other)[:, 0, block].any(axis=1)
+    assert (scales[:, 0, first // 16] == 0x38).all() and tells.any()
+    c = Case(9, [n], D, 64, 1, 1).tokens([0] * n, range(n)).upload()
+    rope = sb.RopeArgs(dim, 2.0 ** 32, 1.0, 0, 32.0, 1.0)
+    k = k.bfloat16().to(DEV)
+    sb.sa_paged4_append(c.pa, k, k, c.ws, rope=rope, halves=halves,
+                        rope_pos=torch.from_numpy(pos[at].astype(np.int32)).to(DEV))
+    assert sb.sa_check_device_status(c.ws) == sb.SA_OK
+    page, slot = c.table[0, np.arange(n) // 64], np.arange(n) % 64
+    assert np.array_equal(c.d["Ks"].cpu().numpy()[page, 0, slot][:, first // 16], scales[:, 0, first // 16])
+    # (value 0 is the one that was looked at; its pair's other value and pair 7's small one may lie at a border)
+    got = c.d["K"].cpu().numpy()[page, 0, slot][:, first // 2] & 15
+    assert np.array_equal(got, codes[:, 0, first // 2] & 15), (got != codes[:, 0, first // 2] & 15).sum()
