@@ -8,6 +8,7 @@
 #pragma once
 
 #include "paged4.cuh"
+#include "paged_bounds.h"
 
 namespace sa {
 
@@ -173,9 +174,9 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
       upto += before;
       const long long from = upto - static_cast<long long>(counted) * heads;
       if (warp == 0 && x0 < x1 && x0 >= from && x0 < upto) {
-        const int rest = static_cast<int>(x0 - from), t = first[e];
-        *out = UnitStart{t / nt, t, rest / counted, rest % counted, total, round,
-                         min(round, cost[e] - rest % counted)};
+        const TilePlace at = tile_place(x0 - from, counted);
+        const int t = first[e];
+        *out = UnitStart{t / nt, t, at.head, at.tile, total, round, min(round, cost[e] - at.tile)};
       }
       before = __shfl_sync(0xffffffffu, upto, 31);
     }
@@ -210,8 +211,8 @@ __device__ __forceinline__ void find_units(const PagedView &v, int nt, int heads
     auto take = [&](int t, int last) {
       const int cost = (last + tile) / tile;
       if (x0 < at + static_cast<long long>(cost) * heads) {
-        const int rest = static_cast<int>(x0 - at);
-        if (lane == 0) *out = UnitStart{t / nt, t, rest / cost, rest % cost, total, 1, 0};
+        const TilePlace place = tile_place(x0 - at, cost);
+        if (lane == 0) *out = UnitStart{t / nt, t, place.head, place.tile, total, 1, 0};
         return false;
       }
       at += static_cast<long long>(cost) * heads;

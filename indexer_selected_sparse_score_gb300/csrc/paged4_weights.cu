@@ -146,8 +146,8 @@ weights4_kernel(const WeightsParams p) {
     if (cost == 0) continue;
     const int t0 = r.t0[run], n = r.t0[run + 1] - t0, seq = pv.q_seq[t0];
     const int ncols = n * p.group, groups = (ncols + 7) / 8;
-    const int rest = static_cast<int>(x - r.off[run]);
-    int hk = rest / cost, kt0 = rest - hk * cost;
+    const TilePlace place = tile_place(x - r.off[run], cost);
+    int hk = place.head, kt0 = place.tile;
     for (; hk < pv.H_kv && x < x1; ++hk, kt0 = 0) {
       const int count = static_cast<int>(min(static_cast<long long>(cost - kt0), x1 - x));
       x += count;

@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_umma_kernel(const WParams
       const int run = run_of_tile(p.runs.off, runs, x);
       const int last = p.runs.last[run], cost = (last + kTile) / kTile;
       const int t0 = p.runs.t0[run], t1 = p.runs.t0[run + 1], seq = pv.q_seq[t0];
-      const int rest = static_cast<int>(x - p.runs.off[run]), hk = rest / cost, base = (rest - hk * cost) * kTile;
+      const TilePlace place = tile_place(x - p.runs.off[run], cost);
+      const int hk = place.head, base = place.tile * kTile;
       const int slot = base + 16 * lane;
       int id = -1;
       if (lane < 8 && slot <= last) id = load_page(pv, seq, slot >> pv.logP, p.status, true);

@@ -34,4 +34,18 @@ SA_BOUNDS_FN bool cut_ok(int64_t unit, int last, int64_t units, int c, int ctas)
   return unit >= 0 && unit < units && part_range_ok(c, last, ctas);
 }
 
+
+// The KV head and the tile of it that the rest-th tile of a unit is, of `cost` tiles a head
+// (a unit of 2^30 slots and hundreds of heads has more than 2^31 tiles).
+struct TilePlace {
+  int head, tile;
+};
+SA_BOUNDS_FN TilePlace tile_place(int64_t rest, int cost) {
+  if ((rest >> 32) == 0) {
+    const uint32_t r = static_cast<uint32_t>(rest), c = static_cast<uint32_t>(cost);
+    return TilePlace{static_cast<int>(r / c), static_cast<int>(r % c)};
+  }
+  return TilePlace{static_cast<int>(rest / cost), static_cast<int>(rest % cost)};
+}
+
 }  // namespace sa
