@@ -513,10 +513,12 @@ SA_API size_t sa_paged4_workspace_size(const sa_paged4_args *pa);
  * value; NULL for q_pos[t]); then for every 16 values
  *   scale = e4m3( max(max |z| / 6, 2^-9) ), codes = e2m1( z / scale ),
  * both to the nearest, ties to even, saturating at 448 and 6, the quotients
- * exact.  A NaN among the 16 makes the scale NaN (and so all of them).  q, q_out,
- * the strides and a slot given twice as for sa_paged_append.  With weight and
- * born ([B, H_kv, ld], both or neither) the slot's record begins for every KV
- * head: weight 0, born r. */
+ * exact.  A NaN among the 16 makes the scale NaN (and so all of them).  q, q_out
+ * and the strides as for sa_paged_append.  The slots of one call are distinct (two
+ * sequences that name one page have its slots in common): of one given twice,
+ * every code and every scale is one token's or the other's, so that a value may be
+ * neither's.  With weight and born ([B, H_kv, ld], both or neither) the slot's
+ * record begins for every KV head: weight 0, born r. */
 SA_API sa_status sa_paged4_append(const sa_paged4_args *pa, const void *k, int64_t k_stride, const void *v,
                                   int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
                                   const sa_rope_args *rope, int32_t rope_halves, const int32_t *rope_pos, float *weight,
@@ -533,15 +535,22 @@ SA_API sa_status sa_paged4_read(const sa_paged4_args *pa, void *k_out, void *v_o
  *   out[t, h'] = sum_j softmax(scale q[t, h'] . K_j) V_j,  0 <= j <= q_pos[t]
  *   lse[t, h'] = log sum_j exp(scale q[t, h'] . K_j)
  * out: [T, H, D] bf16 dense; lse: [T, H] fp32 or NULL.  A row without keys (all
- * of its pages out of range) has out 0 and lse -inf.  Serves one token per
- * sequence, a few drafted ones and chunks of prompts; a sequence's tokens share
- * its keys where they follow one another in the call.  Keys and values enter
- * their products exactly, as fp16; queries as fp16 scaled by a power of two per
- * row (exact but for values 2^-29 of the row's largest); the weights are rounded
- * to fp16 (by 2^-11 of each or 2^-30 of the row's largest at most); logits,
- * statistics and sums are fp32.  How the work is cut up goes by the tokens that
- * a sequence has on average, T / B (the host does not know where they lie): for
- * a chunk of few sequences of a large table, pass those rows of it alone. */
+ * of its pages out of range), or whose logits are all -inf, has out 0 and lse
+ * -inf.  Serves one token per sequence, a few drafted ones and chunks of prompts;
+ * a sequence's tokens share its keys where they follow one another in the call.
+ * Keys and values enter their products exactly, as fp16; queries as fp16 scaled by
+ * a power of two per row (exact but for values 2^-29 of the row's largest); the
+ * weights are rounded to fp16 (by 2^-11 of each or 2^-30 of the row's largest at
+ * most); logits, statistics and sums are fp32.
+ *
+ * How the work is cut up goes by the tokens that a sequence has on average, T / B
+ * (the host does not know where they lie), skipped tokens and sequences without
+ * any among them.  Results are the same but for roundings, times are not: with T
+ * <= B every token reads its sequence's slots by itself, and where T / B times the
+ * heads of a KV head is above 16, a token of few heads takes the place of a whole
+ * tile of rows.  So for a few sequences of a large table pass those rows of it
+ * alone, and make two calls of a batch that mixes a prompt's chunk with single
+ * tokens. */
 SA_API sa_status sa_paged4_attn(const sa_paged4_args *pa, const void *q, void *out, float *lse, void *ws,
                                 size_t ws_bytes, sa_stream_t stream);
 

@@ -1,5 +1,5 @@
 """The 4-bit cache where numbers are far from ordinary ones: logits past 2^24,
-rotations at far positions."""
+infinite queries, rotations at far positions; and slots that a call is given twice."""
 import numpy as np
 import pytest
 import torch
@@ -46,6 +46,30 @@ def test_logits_where_a_step_of_fp32_is_not_small(G):
     assert not bad.any(), [rows[i] for i in bad.nonzero()[:, 0]]
     want = np.log(2) * (first + more) + np.log(n // 2)
     assert ((lse - want).abs() <= 2.0 ** -20 * want).all()
+
+
+@pytest.mark.parametrize("G", [8, 16, 32])
+def test_infinite_queries(G):
+    """All logits -inf: a row of zeros, and nothing gathered; one of +inf: NaN; -inf beside
+    finite ones: those alone."""
+    lens = [150, 150, 150]
+    c = Case(12, lens, D=128, P=64, Hkv=1, G=G).tokens(*step(lens))
+    for b in range(3):
+        for j in range(150):
+            codes = c.K[0][c.table[b, j // 64], 0, j % 64]
+            codes[0] = (codes[0] & 0xF0) | (0 if b == 2 and j % 2 else 2)  # value 0 is positive, or zero in every other slot
+            c.K[1][c.table[b, j // 64], 0, j % 64, 0] = 0x38
+    c.q[0, :, 0], c.q[1, :, 0] = -torch.inf, torch.inf
+    c.q[2, :, 0] = -3e38                                     # (-inf times zero is NaN; this is not)
+    c.q[2, :, 1:] = c.q[2, :, 1:] * 1e30
+    c.upload()
+    out, lse = c.attn()
+    assert (out[0] == 0).all() and (lse[0] == -torch.inf).all()
+    assert out[1].isnan().all() and lse[1].isnan().all()
+    assert torch.isfinite(out[2]).all() and torch.isfinite(lse[2]).all()
+    w = torch.ones(3, 1, c.max_pages * 64, device=DEV)
+    sb.sa_paged4_weights(c.pa, c.d["q"], lse, w, c.ws)
+    assert (w[0] == 1).all() and w[1, 0, :150].isnan().all() and (w[1, 0, 150:] == 1).all()
 
 
 def _turned(a, b, ang):
@@ -109,3 +133,25 @@ def test_append_at_far_positions(far, halves):
     # (value 0 is the one that was looked at; its pair's other value and pair 7's small one may lie at a border)
     got = c.d["K"].cpu().numpy()[page, 0, slot][:, first // 2] & 15
     assert np.array_equal(got, codes[:, 0, first // 2] & 15), (got != codes[:, 0, first // 2] & 15).sum()
+
+
+def test_a_slot_given_twice():
+    """Codes (in units of eight) and scales are one token's or the other's, perhaps of both in
+    one row; nothing else is written."""
+    n, D, P = 300, 128, 64
+    c = Case(11, [n], D, P, 2, 1).tokens([0] * (2 * n), list(range(n)) * 2).upload()
+    k, v = (torch.from_numpy(c.r.standard_normal((2 * n, 2, D)) * 4.0 ** np.repeat([0, 1], n)[:, None, None]).bfloat16()
+            for _ in range(2))
+    before = [c.d[x].cpu().numpy().copy() for x in ("K", "Ks", "V", "Vs")]
+    sb.sa_paged4_append(c.pa, k.to(DEV), v.to(DEV), c.ws)
+    assert sb.sa_check_device_status(c.ws) == sb.SA_OK
+    page, slot = c.table[0, np.arange(n) // P], np.arange(n) % P
+    for i, (x, name) in enumerate(((k, "K"), (k, "Ks"), (v, "V"), (v, "Vs"))):
+        want = r4.quantise(x.double().numpy())[i % 2]
+        got = c.d[name].cpu().numpy()
+        rows = got[page, :, slot]
+        unit = (lambda y: y.reshape(n, 2, -1, 4)) if i % 2 == 0 else (lambda y: y[..., None])
+        one, other = (unit(rows) == unit(want[:n])).all(axis=-1), (unit(rows) == unit(want[n:])).all(axis=-1)
+        assert (one | other).all()
+        got[page, :, slot] = before[i][page, :, slot]
+        assert np.array_equal(got, before[i])
