@@ -541,6 +541,8 @@ def sa_paged4_evict(pa: Paged4Args, length, newest, budget: int, recent: int, we
     bo, ld3 = _records(a, "born_out", born_out, _INT32, dev)
     if not ld == ld1 == ld2 == ld3:
         raise SAError(SA_ERR_INVALID_ARG, "the records differ in their rows")
+    if not (0 < budget < 1 << 31 and 0 <= recent <= budget):  # (the library would see 32 bits of a larger one)
+        raise SAError(SA_ERR_INVALID_ARG, f"budget {budget}, recent {recent}: need 1 <= budget < 2^31, 0 <= recent <= budget")
     _check(load().sa_paged4_evict(ctypes.byref(pa), _dense("length", length, _INT32, B, 1, dev),
                                   _dense("newest", newest, _INT32, B, 1, dev), budget, recent, wp, bp, wo, bo, ld,
                                   _dense("length_out", length_out, _INT32, B, 1, dev), p, n, _s(stream)))
