@@ -432,11 +432,13 @@ size_t attn4_scratch(const sa_paged4_args &pa) {
 cudaError_t launch_attn4(const sa_paged4_args &pa, const void *q, void *out, float *lse, void *scratch,
                          uint32_t *counters, uint32_t *status, cudaStream_t stream) {
   if (pa.p.T == 0) return cudaSuccess;
-  // Up to 16 columns (O of more is more than a warp's registers) here.  More on the 5th-
-  // generation tensor cores (1270 prompt tokens of 32 over 4 heads, in groups of 16 columns
-  // 2414 us here, 239 there): up to 128 with one row tile (64 sequences of 64 heads over one
+  // Up to 16 columns here (O of more is more than a warp's registers hold), where 16 of them take
+  // half of the time that they take on the 5th-generation tensor cores (every call with a cold
+  // L2: 64 sequences of 128 over 8 heads at 8 .. 16 K slots 238 us here and 449 there, 32
+  // sequences of 4 drafted tokens of 32 over 8 heads 74 and 141, one token of 100 slots 14 and
+  // 33).  More columns there: up to 128 with one row tile (64 sequences of 64 heads over one
   // KV head 223 us, with two 345; 4 tokens of 32 heads over one 72 and 90), above with two
-  // (those prompts 201 us alone, with one 263).
+  // (1270 prompt tokens of 32 over 4 heads without their join 201 us, with one 263).
   const int columns = columns_of(pa);
   if (columns > 16)
     return launch_attn4_umma(pa, q, out, lse, columns > 128 ? 256 : 128, scratch, status, stream);

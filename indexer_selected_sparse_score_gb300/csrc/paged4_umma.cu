@@ -26,7 +26,7 @@
 //
 // Bound by a stream's chain: a tile's logits, softmax (2900 clocks for 128 keys beside
 // the other stream's products: loads from tensor memory wait behind them), weights,
-// product (about 5000 clocks, of which the tensor cores work 2048).  1270 prompt tokens of
+// product: about 5000 clocks, in which the tensor cores work 1024 for each of the streams.  1270 prompt tokens of
 // 32 over 4 heads at 6 .. 12 K slots: 238 us, 0.84 PFLOP/s; 64 tokens of 64 heads over one
 // KV head at 32 .. 65 K: 225 us; a call of one short unit: 24 us, of which a part's queries,
 // chain and stores are 15.

@@ -2,8 +2,8 @@
 //
 // Tokens are taken in blocks of `nt` consecutive ones; the tokens of a block that
 // follow one another in one sequence are a unit: they attend the same slots, up
-// to their own.  A unit costs, for every KV head (or part of its query heads), the tiles of `tile` slots up to
-// its last valid token; the tiles of all units, unit by unit, KV head by KV head,
+// to their own.  A unit costs, for every KV head, the tiles of `tile` slots up to its
+// last valid token; the tiles of all units, unit by unit, KV head by KV head,
 // form one list that the CTAs cut evenly.
 #pragma once
 

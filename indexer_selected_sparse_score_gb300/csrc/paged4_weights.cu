@@ -28,9 +28,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 2;            // 16 warps of 128 registers (three CTAs spill: 55 us against 49)
 constexpr int kStages = 4;               // tiles that a warp has in its ring
-// Columns of a unit, on average; more: paged4_weights_umma.cu (64 sequences of 8 .. 16 K slots
-// and one KV head, 32 columns: 65 us here, 131 there; 64 columns: 117 and 148; 1024 prompt
-// tokens, 8192 columns a KV head: 1302 and 99).
+// Columns of a unit, on average; more: paged4_weights_umma.cu.  64 sequences of 8 .. 16 K slots
+// and one KV head, every call with a cold L2: 16 columns 45 us here and 141 there, 32 74 and 148,
+// 64 129 and 162, 96 184 and 100, 128 240 and 102.  16 sequences of 512 .. 1024 slots: 32
+// columns 14 and 23 us, 64 18 and 23, 96 23 and 23, 128 27 and 25; one of 100 slots: 64 18 and 21, 96
+// 25 and 23, so the border does not move with the slots.
 constexpr int kMostColumns = 64;
 constexpr int kRunsInSmem = 256;         // tokens whose runs a CTA works out by itself
 
